@@ -452,6 +452,149 @@ tsd_status tsd_commit_path(const tsd_attn_desc* desc, int S, const void* ktree,
                            void* vcache, int32_t* prefix_len, int32_t* err,
                            tsd_stream_t stream);
 
+/* --------------------------------------------------------------------------
+ * The 8-bit KV cache: tsd_cache_write_q8, tsd_commit_path_q8,
+ * tsd_tree_verify_attn_q8
+ *
+ * The cache with half the bytes of bf16: e4m3 codes, and one exponent byte e
+ * for each block of TSD_Q8_BLOCK = 64 tokens of a head, K and V apart.
+ *   value = code * 2^(e - 127)
+ * The block of position pos is pos / 64 (blocks do not depend on the prefix
+ * length).  Writes give e in 10..246; 0 and 255 are not used.
+ *
+ * kq, vq      contiguous [B][Hkv][cap][dk | dv], or pages
+ *             [num_pages][Hkv][page_size][dk | dv]; one byte per element
+ *             (vq and vexp unused and may be NULL when V aliases K)
+ * kexp, vexp  contiguous [B][Hkv][ceil(cap / 64)], or pages
+ *             [num_pages][Hkv][page_size / 64]; one byte each
+ * page_table, max_pages, page_size, num_pages
+ *             page_size = 0 (the rest unused, page_table NULL) for the
+ *             contiguous cache; otherwise as for tsd_tree_verify_attn_paged:
+ *             page_size a multiple of 128, cap = max_pages * page_size.  A page
+ *             that is written may be in the table once only.
+ * desc        B, R, Hq, Hkv, dk, dv, cap, dtype, v_aliases_k, scale as for
+ *             tsd_tree_verify_attn, with its head dims; dtype is that of q,
+ *             the new rows and out (the cache is always 8-bit).
+ *
+ * tsd_cache_write_q8 appends rows, for example a prefill: for request b with
+ * P = prefix_len[b] and n = new_len[b] (0..T), rows knew[b][0..n-1],
+ * vnew[b][0..n-1] ([B][T][Hkv][dk | dv], dtype) go to positions P..P+n-1, then
+ * prefix_len[b] = P + n.  tsd_commit_path_q8 is tsd_commit_path into the 8-bit
+ * cache: scratch rows accept_rows[b][0..L] go to P..P+L.  For each block that
+ * gets a row, with a the largest finite magnitude of its new rows:
+ *   need = the smallest e with a <= 448 * 2^(e - 127), within 10..246
+ *   e'   = need if the block starts at or behind P, else max(e, need)
+ * a new value x becomes the e4m3 code nearest to x * 2^(127 - e') (ties to
+ * even; magnitudes past 448, infinities too, become 448; NaN stays NaN), and
+ * where e' > e the codes c of the block's earlier rows become the nearest to
+ * c * 2^(e - e').  All else in the cache is left as it is.  A request with
+ * P + n > cap, P < 0 or n outside 0..T is skipped and reported as
+ * TSD_DEV_ERR_CAPACITY, a path outside its limits as TSD_DEV_ERR_BAD_TREE, a
+ * page outside the pool as TSD_DEV_ERR_BAD_PAGE.  No workspace.
+ *
+ * tsd_tree_verify_attn_q8 is tsd_tree_verify_attn over the 8-bit cache: the
+ * prefix keys and values are the codes' values, the scratch rows ktree, vtree
+ * are in dtype.  Rows behind prefix_len are not used, whatever they hold; nor
+ * are scratch rows that no row sees.  A NaN or an infinity in a scratch row
+ * reaches the outputs of the rows that see it and no others.  fp32 inputs are
+ * computed in fp32.  ws: tsd_verify_q8_workspace_size(desc) bytes (0 is a valid size);
+ * calls that may overlap, captured ones among them, each need their own.
+ * -------------------------------------------------------------------------- */
+#define TSD_Q8_BLOCK 64
+
+tsd_status tsd_cache_write_q8(const tsd_attn_desc* desc, int T, const void* knew,
+                              const void* vnew, const int32_t* new_len, void* kq, void* vq,
+                              void* kexp, void* vexp, const int32_t* page_table, int max_pages,
+                              int page_size, int num_pages, int32_t* prefix_len, int32_t* err,
+                              tsd_stream_t stream);
+
+tsd_status tsd_commit_path_q8(const tsd_attn_desc* desc, int S, const void* ktree,
+                              const void* vtree, const int32_t* accept_rows,
+                              const int32_t* accept_len, void* kq, void* vq, void* kexp,
+                              void* vexp, const int32_t* page_table, int max_pages,
+                              int page_size, int num_pages, int32_t* prefix_len, int32_t* err,
+                              tsd_stream_t stream);
+
+size_t tsd_verify_q8_workspace_size(const tsd_attn_desc* desc);
+
+tsd_status tsd_tree_verify_attn_q8(const tsd_attn_desc* desc, const void* q, const void* kq,
+                                   const void* vq, const void* kexp, const void* vexp,
+                                   const int32_t* page_table, int max_pages, int page_size,
+                                   int num_pages, const int32_t* prefix_len, const void* ktree,
+                                   const void* vtree, const uint64_t* mask, void* out,
+                                   float* lse, void* ws, size_t ws_bytes, int32_t* err,
+                                   tsd_stream_t stream);
+
+/* --------------------------------------------------------------------------
+ * A cache held at a budget: tsd_cache_weights(_q8), tsd_cache_evict(_q8)
+ *
+ * Eviction by accumulated attention weight.  The caller keeps, beside the
+ * cache, for each cached row
+ *   acc  [B][Hkv][cap] fp32   the attention weight it has received
+ *   pos  [B][Hkv][cap] int32  its token's position in the request
+ * and seen [B][Hkv] int32, the tokens that the request has had so far (equal
+ * over its heads).  After a prefill of P tokens: acc as the caller likes (0,
+ * or a prompt's own weights), pos = 0..P-1, seen = P.
+ *
+ * tsd_cache_weights goes between the walk and the commit of a round (the
+ * prefix length is still that of before).  With r_0..r_L the accepted rows of
+ * request b, P = prefix_len[b] and h over the query heads of a KV head:
+ *   acc[p]     = decay * acc[p] + sum_{i,h} exp(scale q[r_i][h] . k[p] - lse[r_i][h]),  p < P
+ *   acc[P + j] = sum_{i >= j, h} exp(scale q[r_i][h] . ktree[r_j] - lse[r_i][h]),      j <= L
+ *   pos[P + j] = seen + j, then seen += L + 1
+ * q, ktree, lse as given to and left by the verify call ([B][R][Hq][dk],
+ * [B][R][Hkv][dk], [B][R][Hq]); 0 <= decay <= 1; accept_rows [B][S+1],
+ * accept_len [B].  The other entries are left as they are.  A request whose
+ * P + 1 + L passes cap, with a bad path or a bad page, is skipped and reported
+ * as by the commit.  No workspace.
+ *
+ * tsd_cache_evict cuts every request that holds more than `keep` rows to
+ * `keep`, in place.  Each head ranks its rows by (protected first, acc desc,
+ * index asc) and keeps the first `keep`; a row is protected if pos < sink or
+ * pos >= seen - recent (sink + recent <= keep).  The kept rows at or behind
+ * `keep` move, in index order, into the places below `keep` that the dropped
+ * rows leave, in index order, K, V, acc and pos together; then prefix_len[b] =
+ * keep.  Rows behind the new length are left as they were.  The cache is then
+ * no longer in token order, which attention does not depend on.  A NaN in acc
+ * ranks above infinity.  In an 8-bit cache the exponent of a block that gets a
+ * row becomes the largest that its rows had before the call, and codes are
+ * rescaled to it as by a write.  A request with prefix_len outside 0..cap or a
+ * bad page is skipped and reported (CAPACITY, BAD_PAGE).  A page may be in the
+ * table once only.  ws: tsd_cache_evict_workspace_size(desc) bytes.
+ *
+ * Page arguments and desc (dtype: that of q and of the cache; of q alone where
+ * the cache is 8-bit) as above; R, Hq, scale are not used by the eviction.
+ * -------------------------------------------------------------------------- */
+tsd_status tsd_cache_weights(const tsd_attn_desc* desc, int S, const void* q,
+                             const void* kcache, const int32_t* page_table, int max_pages,
+                             int page_size, int num_pages, const int32_t* prefix_len,
+                             const void* ktree, const int32_t* accept_rows,
+                             const int32_t* accept_len, const float* lse, float decay,
+                             float* acc, int32_t* pos, int32_t* seen, int32_t* err,
+                             tsd_stream_t stream);
+
+tsd_status tsd_cache_weights_q8(const tsd_attn_desc* desc, int S, const void* q,
+                                const void* kq, const void* kexp, const int32_t* page_table,
+                                int max_pages, int page_size, int num_pages,
+                                const int32_t* prefix_len, const void* ktree,
+                                const int32_t* accept_rows, const int32_t* accept_len,
+                                const float* lse, float decay, float* acc, int32_t* pos,
+                                int32_t* seen, int32_t* err, tsd_stream_t stream);
+
+size_t tsd_cache_evict_workspace_size(const tsd_attn_desc* desc);
+
+tsd_status tsd_cache_evict(const tsd_attn_desc* desc, int keep, int sink, int recent,
+                           float* acc, int32_t* pos, const int32_t* seen, void* kcache,
+                           void* vcache, const int32_t* page_table, int max_pages,
+                           int page_size, int num_pages, int32_t* prefix_len, void* ws,
+                           size_t ws_bytes, int32_t* err, tsd_stream_t stream);
+
+tsd_status tsd_cache_evict_q8(const tsd_attn_desc* desc, int keep, int sink, int recent,
+                              float* acc, int32_t* pos, const int32_t* seen, void* kq, void* vq,
+                              void* kexp, void* vexp, const int32_t* page_table, int max_pages,
+                              int page_size, int num_pages, int32_t* prefix_len, void* ws,
+                              size_t ws_bytes, int32_t* err, tsd_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

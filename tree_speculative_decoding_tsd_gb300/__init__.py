@@ -46,6 +46,7 @@ TSD_DEV_ERR_TIMEOUT = 0x03000000
 TSD_DEV_ERR_MASK = 0x7F000000
 TSD_F32 = 0
 TSD_BF16 = 1
+TSD_Q8_BLOCK = 64
 VERIFY_PATHS = {"auto": 0, "generic": 1, "mma": 2, "tc": 3}   # TSD_PATH_* of tsd.h
 
 # every symbol the header declares
@@ -55,7 +56,10 @@ EXPORTED = ("tsd_status_string", "tsd_version", "tsd_tree_build_workspace_size",
             "tsd_tree_verify_attn", "tsd_tree_verify_attn_paged", "tsd_commit_path_paged",
             "tsd_accept_walk_workspace_size", "tsd_accept_walk", "tsd_accept_walk_static",
             "tsd_commit_path", "tsd_accept_commit", "tsd_target_argmax", "tsd_walk_commit",
-            "tsd_set_verify_path", "tsd_set_wait_budget")
+            "tsd_set_verify_path", "tsd_set_wait_budget",
+            "tsd_cache_write_q8", "tsd_commit_path_q8", "tsd_verify_q8_workspace_size",
+            "tsd_tree_verify_attn_q8", "tsd_cache_weights", "tsd_cache_weights_q8",
+            "tsd_cache_evict_workspace_size", "tsd_cache_evict", "tsd_cache_evict_q8")
 
 
 class TsdError(RuntimeError):
@@ -117,6 +121,26 @@ def _load():
                                     ctypes.POINTER(tsd_attn_desc), P, P, P, P, P, I, I, I, P, P,
                                     Z, P, P]
     lib.tsd_walk_commit.restype = I
+    D, F = ctypes.POINTER(tsd_attn_desc), ctypes.c_float
+    paging = [P, I, I, I]
+    lib.tsd_cache_write_q8.argtypes = [D, I, P, P, P, P, P, P, P, *paging, P, P, P]
+    lib.tsd_cache_write_q8.restype = I
+    lib.tsd_commit_path_q8.argtypes = [D, I, P, P, P, P, P, P, P, P, *paging, P, P, P]
+    lib.tsd_commit_path_q8.restype = I
+    lib.tsd_verify_q8_workspace_size.argtypes = [D]
+    lib.tsd_verify_q8_workspace_size.restype = Z
+    lib.tsd_tree_verify_attn_q8.argtypes = [D, P, P, P, P, P, *paging, P, P, P, P, P, P, P, Z, P, P]
+    lib.tsd_tree_verify_attn_q8.restype = I
+    lib.tsd_cache_weights.argtypes = [D, I, P, P, *paging, P, P, P, P, P, F, P, P, P, P, P]
+    lib.tsd_cache_weights.restype = I
+    lib.tsd_cache_weights_q8.argtypes = [D, I, P, P, P, *paging, P, P, P, P, P, F, P, P, P, P, P]
+    lib.tsd_cache_weights_q8.restype = I
+    lib.tsd_cache_evict_workspace_size.argtypes = [D]
+    lib.tsd_cache_evict_workspace_size.restype = Z
+    lib.tsd_cache_evict.argtypes = [D, I, I, I, P, P, P, P, P, *paging, P, P, Z, P, P]
+    lib.tsd_cache_evict.restype = I
+    lib.tsd_cache_evict_q8.argtypes = [D, I, I, I, P, P, P, P, P, P, P, *paging, P, P, Z, P, P]
+    lib.tsd_cache_evict_q8.restype = I
     lib.tsd_set_verify_path.argtypes = [I]
     lib.tsd_set_verify_path.restype = I
     lib.tsd_set_wait_budget.argtypes = [ctypes.c_longlong]
@@ -468,3 +492,164 @@ def tsd_accept_commit(logits, S, token, parent, mask, is_leaf, tgt, accept_len, 
     _check("tsd_accept_commit", _L().tsd_accept_commit(
         *walk, ctypes.byref(d), pkt, pvt, pkc, pvc, *paging, ppl, _ptr(ws), _nbytes(ws),
         _err(err), _stream(stream)))
+
+
+# ------------------------------------- the 8-bit cache, and eviction --
+
+_CODES = (torch.uint8, torch.float8_e4m3fn)
+_EXPS = (torch.uint8,) + ((torch.float8_e8m0fnu,) if hasattr(torch, "float8_e8m0fnu") else ())
+
+
+def _here(*tensors):
+    """The calls launch on the current device: every tensor has to live there."""
+    cur = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.is_cuda and t.device.index != cur:
+            raise ValueError(f"tensor on {t.device}, but the current device is cuda:{cur}")
+
+
+def q8_blocks(cap) -> int:
+    """Exponent bytes per head of a contiguous 8-bit cache of ``cap`` positions."""
+    return -(-int(cap) // TSD_Q8_BLOCK)
+
+
+def _cache_shapes(d, kcache, page_table, page_size):
+    """(leading dims, rows) of a contiguous or paged cache, and its page arguments."""
+    if page_table is None:
+        if page_size:
+            raise ValueError("page_size without a page_table")
+        return (d.B, d.Hkv), d.cap, (None, 0, 0, 0)
+    npg, mp = kcache.shape[0], page_table.shape[1]
+    return (npg, d.Hkv), page_size, (_t(page_table, "page_table", _I32, (d.B, mp)), mp, page_size,
+                                     npg)
+
+
+def _q8_cache(d, kq, vq, kexp, vexp, page_table, page_size):
+    lead, rows, paging = _cache_shapes(d, kq, page_table, page_size)
+    nb = q8_blocks(rows)
+    alias = bool(d.v_aliases_k)
+    return (_t(kq, "kq", _CODES, (*lead, rows, d.dk)),
+            None if alias else _t(vq, "vq", _CODES, (*lead, rows, d.dv)),
+            _t(kexp, "kexp", _EXPS, (*lead, nb)),
+            None if alias else _t(vexp, "vexp", _EXPS, (*lead, nb)), paging)
+
+
+def tsd_cache_write_q8(desc, knew, vnew, new_len, kq, vq, kexp, vexp, prefix_len, err=None,
+                       stream=None, page_table=None, page_size=0):
+    """Append rows knew/vnew [B][T][Hkv][d], new_len[b] of them, to the 8-bit cache."""
+    d = desc
+    dt = _attn_dtype(d)
+    _here(knew, vnew, new_len, kq, vq, kexp, vexp, prefix_len, err, page_table)
+    T = knew.shape[1]
+    pk, pv, pke, pve, paging = _q8_cache(d, kq, vq, kexp, vexp, page_table, page_size)
+    _check("tsd_cache_write_q8", _L().tsd_cache_write_q8(
+        ctypes.byref(d), T, _t(knew, "knew", dt, (d.B, T, d.Hkv, d.dk)),
+        None if d.v_aliases_k else _t(vnew, "vnew", dt, (d.B, T, d.Hkv, d.dv)),
+        _t(new_len, "new_len", _I32, (d.B,)), pk, pv, pke, pve, *paging,
+        _t(prefix_len, "prefix_len", _I32, (d.B,)), _err(err), _stream(stream)))
+
+
+def tsd_commit_path_q8(desc, S, ktree, vtree, accept_rows, accept_len, kq, vq, kexp, vexp,
+                       prefix_len, err=None, stream=None, page_table=None, page_size=0):
+    """tsd_commit_path into the 8-bit cache."""
+    d = desc
+    _here(ktree, vtree, accept_rows, accept_len, kq, vq, kexp, vexp, prefix_len, err, page_table)
+    pkt, pvt, par, pal, ppl = _commit_common(d, S, ktree, vtree, accept_rows, accept_len,
+                                             prefix_len)
+    pk, pv, pke, pve, paging = _q8_cache(d, kq, vq, kexp, vexp, page_table, page_size)
+    _check("tsd_commit_path_q8", _L().tsd_commit_path_q8(
+        ctypes.byref(d), S, pkt, pvt, par, pal, pk, pv, pke, pve, *paging, ppl, _err(err),
+        _stream(stream)))
+
+
+def tsd_verify_q8_workspace_size(desc: tsd_attn_desc) -> int:
+    return _L().tsd_verify_q8_workspace_size(ctypes.byref(desc))
+
+
+def tsd_tree_verify_attn_q8(desc, q, kq, vq, kexp, vexp, prefix_len, ktree, vtree, mask, out, lse,
+                            ws, err=None, stream=None, page_table=None, page_size=0):
+    """tsd_tree_verify_attn over the 8-bit cache (contiguous, or pages with ``page_table``)."""
+    d = desc
+    _here(q, kq, vq, kexp, vexp, prefix_len, ktree, vtree, mask, out, lse, ws, err, page_table)
+    pq, pl, pkt, pvt, pm, po, pls = _verify_common(d, q, prefix_len, ktree, vtree, mask, out, lse)
+    pk, pv, pke, pve, paging = _q8_cache(d, kq, vq, kexp, vexp, page_table, page_size)
+    _check("tsd_tree_verify_attn_q8", _L().tsd_tree_verify_attn_q8(
+        ctypes.byref(d), pq, pk, pv, pke, pve, *paging, pl, pkt, pvt, pm, po, pls, _ptr(ws),
+        _nbytes(ws), _err(err), _stream(stream)))
+
+
+def _weight_args(d, S, prefix_len, ktree, accept_rows, accept_len, lse, decay, acc, pos, seen):
+    return (_t(prefix_len, "prefix_len", _I32, (d.B,)),
+            _t(ktree, "ktree", _attn_dtype(d), (d.B, d.R, d.Hkv, d.dk)),
+            _t(accept_rows, "accept_rows", _I32, (d.B, S + 1)),
+            _t(accept_len, "accept_len", _I32, (d.B,)), _t(lse, "lse", _F32, (d.B, d.R, d.Hq)),
+            float(decay), _t(acc, "acc", _F32, (d.B, d.Hkv, d.cap)),
+            _t(pos, "pos", _I32, (d.B, d.Hkv, d.cap)), _t(seen, "seen", _I32, (d.B, d.Hkv)))
+
+
+def tsd_cache_weights(desc, S, q, kcache, prefix_len, ktree, accept_rows, accept_len, lse, decay,
+                      acc, pos, seen, err=None, stream=None, page_table=None, page_size=0):
+    """Add the attention weight that the accepted rows gave each cached row to ``acc``."""
+    d = desc
+    dt = _attn_dtype(d)
+    _here(q, kcache, prefix_len, ktree, accept_rows, accept_len, lse, acc, pos, seen, err,
+          page_table)
+    args = _weight_args(d, S, prefix_len, ktree, accept_rows, accept_len, lse, decay, acc, pos,
+                        seen)
+    lead, rows, paging = _cache_shapes(d, kcache, page_table, page_size)
+    _check("tsd_cache_weights", _L().tsd_cache_weights(
+        ctypes.byref(d), S, _t(q, "q", dt, (d.B, d.R, d.Hq, d.dk)),
+        _t(kcache, "kcache", dt, (*lead, rows, d.dk)), *paging, *args, _err(err),
+        _stream(stream)))
+
+
+def tsd_cache_weights_q8(desc, S, q, kq, kexp, prefix_len, ktree, accept_rows, accept_len, lse,
+                         decay, acc, pos, seen, err=None, stream=None, page_table=None,
+                         page_size=0):
+    """tsd_cache_weights for the 8-bit cache."""
+    d = desc
+    _here(q, kq, kexp, prefix_len, ktree, accept_rows, accept_len, lse, acc, pos, seen, err,
+          page_table)
+    args = _weight_args(d, S, prefix_len, ktree, accept_rows, accept_len, lse, decay, acc, pos,
+                        seen)
+    lead, rows, paging = _cache_shapes(d, kq, page_table, page_size)
+    _check("tsd_cache_weights_q8", _L().tsd_cache_weights_q8(
+        ctypes.byref(d), S, _t(q, "q", _attn_dtype(d), (d.B, d.R, d.Hq, d.dk)),
+        _t(kq, "kq", _CODES, (*lead, rows, d.dk)), _t(kexp, "kexp", _EXPS, (*lead, q8_blocks(rows))),
+        *paging, *args, _err(err), _stream(stream)))
+
+
+def tsd_cache_evict_workspace_size(desc: tsd_attn_desc) -> int:
+    return _L().tsd_cache_evict_workspace_size(ctypes.byref(desc))
+
+
+def _evict_state(d, acc, pos, seen):
+    return (_t(acc, "acc", _F32, (d.B, d.Hkv, d.cap)), _t(pos, "pos", _I32, (d.B, d.Hkv, d.cap)),
+            _t(seen, "seen", _I32, (d.B, d.Hkv)))
+
+
+def tsd_cache_evict(desc, keep, sink, recent, acc, pos, seen, kcache, vcache, prefix_len, ws,
+                    err=None, stream=None, page_table=None, page_size=0):
+    """Cut every request of more than ``keep`` cached rows to the ``keep`` heaviest ones."""
+    d = desc
+    dt = _attn_dtype(d)
+    _here(acc, pos, seen, kcache, vcache, prefix_len, ws, err, page_table)
+    lead, rows, paging = _cache_shapes(d, kcache, page_table, page_size)
+    _check("tsd_cache_evict", _L().tsd_cache_evict(
+        ctypes.byref(d), keep, sink, recent, *_evict_state(d, acc, pos, seen),
+        _t(kcache, "kcache", dt, (*lead, rows, d.dk)),
+        None if d.v_aliases_k else _t(vcache, "vcache", dt, (*lead, rows, d.dv)), *paging,
+        _t(prefix_len, "prefix_len", _I32, (d.B,)), _ptr(ws), _nbytes(ws), _err(err),
+        _stream(stream)))
+
+
+def tsd_cache_evict_q8(desc, keep, sink, recent, acc, pos, seen, kq, vq, kexp, vexp, prefix_len,
+                       ws, err=None, stream=None, page_table=None, page_size=0):
+    """tsd_cache_evict for the 8-bit cache."""
+    d = desc
+    _here(acc, pos, seen, kq, vq, kexp, vexp, prefix_len, ws, err, page_table)
+    pk, pv, pke, pve, paging = _q8_cache(d, kq, vq, kexp, vexp, page_table, page_size)
+    _check("tsd_cache_evict_q8", _L().tsd_cache_evict_q8(
+        ctypes.byref(d), keep, sink, recent, *_evict_state(d, acc, pos, seen), pk, pv, pke, pve,
+        *paging, _t(prefix_len, "prefix_len", _I32, (d.B,)), _ptr(ws), _nbytes(ws), _err(err),
+        _stream(stream)))

@@ -1,0 +1,504 @@
+// tsd_cache_evict, tsd_cache_evict_q8: the cache of every head cut to `keep`
+// rows by the attention weight each cached token has received.
+//
+// For a request with more than `keep` rows, each KV head ranks its rows by
+// (protected first, weight desc, index asc) and keeps the first `keep`.  A row
+// is protected if its token is one of the first `sink` or the last `recent`
+// ones.  The kept rows that lie at or behind `keep` move, in order, into the
+// places (in order) of the dropped rows below it: no row that is read is also
+// written, no row that stays is touched, and in the steady state (a few new
+// rows a round) only as many rows move as arrived.  Attention does not depend
+// on the order of the cached rows; `pos` carries each row's token position.
+//
+// select_kernel, one CTA per (head, request): the keep-th largest 32-bit key by
+// four 8-bit histogram rounds.  The histograms are private to each lane (bin x
+// lane, so a warp's 32 counts never meet in a bank, and equal exponents, the
+// usual case for weights, do not serialise); then ties, holes and movers are
+// numbered by ballots and one scan over the warps.  A warp takes consecutive
+// rows and keeps their keys in registers (up to 32 per thread; longer caches
+// are read again by each round).  Bounded by latency: four rounds over 8 bytes
+// a row.
+//
+// move_kernel: 16-byte vectors, one row (K and V) per warp and step, four
+// steps in flight.  move_q8_kernel: one CTA per block of 64 places, because an
+// incoming row with a larger exponent raises the block's:
+//   e' = max of the exponents that the block's rows had before the call,
+// and every code c becomes e4m3(c * 2^(e - e')).  Both are bounded by memory:
+// each moved row is read and written once.
+#include <cuda_bf16.h>
+
+#include "tsd_host.h"
+#include "tsd_q8.cuh"
+
+namespace tsd {
+namespace {
+
+constexpr int kSelThreads = 1024, kSelWarps = 32;
+
+struct EvictArgs {
+  float* acc;
+  int32_t* pos;
+  const int32_t* seen;
+  char* k;
+  char* v;
+  uint8_t* kexp;
+  uint8_t* vexp;
+  int32_t* prefix_len;
+  int32_t* err;
+  CacheMap map;
+  int keep, sink, recent;
+  long krow, vrow;          // bytes per K and V row (vrow 0: latent)
+  // workspace, per (request, head)
+  int32_t* count;           // rows that move; -1: the request keeps all its rows
+  int32_t* holes;           // [list] places below keep that fall free, ascending
+  int32_t* movers;          // [list] kept rows at or behind keep, ascending
+  int32_t* starts;          // [nblk + 1] holes before block j (8-bit cache)
+  uint8_t* kexp_old;        // [nblk] exponents of before the call (8-bit cache)
+  uint8_t* vexp_old;
+  int list, nblk;
+};
+
+// Exclusive sum over the 32 warps of one value per warp; `total` gets the sum.
+__device__ __forceinline__ int warps_before(int v, int* sm, int warp, int lane, int& total) {
+  __syncthreads();
+  if (lane == 0) sm[warp] = v;
+  __syncthreads();
+  const int x = sm[lane];
+  total = __reduce_add_sync(kFull, x);
+  return __reduce_add_sync(kFull, lane < warp ? x : 0);
+}
+
+template <int ITEMS, bool kQ8>
+__global__ void __launch_bounds__(kSelThreads, 1)
+select_kernel(const __grid_constant__ EvictArgs a) {
+  __shared__ uint32_t hist[256 * 32];
+  __shared__ int sums[kSelWarps];
+  __shared__ uint32_t total_of[256];
+  __shared__ uint32_t s_prefix, s_need;
+  __shared__ int s_bad;
+  constexpr int kSpan = kSelThreads * ITEMS;
+  grid_dependency_sync();
+  const int h = blockIdx.x, b = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const long bh = (long)b * a.map.Hkv + h;
+  const int P = a.prefix_len[b];
+  if (tid == 0) s_bad = 0;
+  __syncthreads();
+  if (P < 0 || P > a.map.cap) {
+    if (tid == 0) s_bad = TSD_DEV_ERR_CAPACITY;
+  } else if (a.map.page_size && P > a.keep) {
+    for (int p = tid; p < (P + a.map.page_size - 1) / a.map.page_size; p += kSelThreads) {
+      const int pg = a.map.page_table[(long)b * a.map.max_pages + p];
+      if (pg < 0 || pg >= a.map.num_pages) s_bad = TSD_DEV_ERR_BAD_PAGE;
+    }
+  }
+  __syncthreads();
+  if (s_bad != 0 || P <= a.keep) {
+    if (tid == 0) {
+      a.count[bh] = -1;
+      if (s_bad != 0) report_error(a.err, s_bad, b);
+    }
+    return;
+  }
+  const float* acc = a.acc + bh * a.map.cap;
+  const int32_t* pos = a.pos + bh * a.map.cap;
+  const long recent0 = (long)a.seen[bh] - a.recent;
+  const int rounds = (P + kSpan - 1) / kSpan;
+
+  // keys of the rows base + 32 it + lane of one span (0 past the end)
+  uint32_t key[ITEMS];
+  auto load = [&](int r) {
+    const int base = r * kSpan + warp * 32 * ITEMS + lane;
+    constexpr int kBatch = ITEMS < 8 ? ITEMS : 8;     // loads in flight per thread and array
+#pragma unroll
+    for (int i0 = 0; i0 < ITEMS; i0 += kBatch) {
+      float w[kBatch];
+      int p[kBatch];
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) {
+        const int i = base + 32 * (i0 + j);
+        w[j] = i < P ? acc[i] : 0.f;
+        p[j] = i < P ? pos[i] : 0;
+      }
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) {
+        const bool safe = p[j] < a.sink || p[j] >= recent0;
+        // (order keys of rows are above 0: the smallest is that of -NaN)
+        key[i0 + j] = base + 32 * (i0 + j) >= P ? 0u
+                      : safe                    ? 0xffffffffu
+                                                : max(f32_order_key(w[j]), 1u);
+      }
+    }
+  };
+  load(0);
+
+  if constexpr (kQ8) {   // the exponents of before, which the moves read while others write
+    for (int j = tid; j * kQ8Block < P; j += kSelThreads) {
+      const long e = a.map.block(b, h, j * kQ8Block);
+      a.kexp_old[bh * a.nblk + j] = a.kexp[e];
+      if (a.vrow) a.vexp_old[bh * a.nblk + j] = a.vexp[e];
+    }
+  }
+
+  // ---- the keep-th largest key: prefix holds its digits found so far, need
+  // the rank of the key among those that share them
+  uint32_t prefix = 0, need = (uint32_t)a.keep;
+#pragma unroll 1
+  for (int shift = 24; shift >= 0; shift -= 8) {
+    for (int i = tid; i < 256 * 32; i += kSelThreads) hist[i] = 0;
+    __syncthreads();
+    for (int r = 0; r < rounds; ++r) {
+      if (rounds > 1) load(r);
+#pragma unroll
+      for (int it = 0; it < ITEMS; ++it) {
+        // (rows past the end have key 0 and are left out: a row's is at least 1)
+        const bool in = key[it] != 0 && (shift == 24 || (key[it] >> (shift + 8)) == prefix);
+        if (in) atomicAdd(&hist[((key[it] >> shift) & 255u) * 32 + lane], 1u);
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t s = __reduce_add_sync(kFull, hist[(warp * 8 + i) * 32 + lane]);
+      if (lane == 0) total_of[warp * 8 + i] = s;
+    }
+    __syncthreads();
+    if (warp == 0) {       // lane l takes the bins 255 - 8l .. 248 - 8l, from the largest digit down
+      uint32_t c[8], mine = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        c[i] = total_of[255 - (8 * lane + i)];
+        mine += c[i];
+      }
+      uint32_t incl = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t up = __shfl_up_sync(kFull, incl, o);
+        if (lane >= o) incl += up;
+      }
+      uint32_t before = incl - mine;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if (before < need && need <= before + c[i]) {
+          s_prefix = (prefix << 8) | (uint32_t)(255 - (8 * lane + i));
+          s_need = need - before;
+        }
+        before += c[i];
+      }
+    }
+    __syncthreads();
+    prefix = s_prefix;
+    need = s_need;
+  }
+  const uint32_t cut = prefix;   // the smallest kept key; `need` rows that equal it stay
+
+  // ---- number the ties, then the holes and the movers, in index order
+  int ties_before = 0, holes_before = 0, movers_before = 0;
+#pragma unroll 1
+  for (int r = 0; r < rounds; ++r) {
+    if (rounds > 1) load(r);
+    const int base = r * kSpan + warp * 32 * ITEMS;
+    int t = 0;
+#pragma unroll
+    for (int it = 0; it < ITEMS; ++it) t += __popc(__ballot_sync(kFull, key[it] == cut));
+    int total;
+    int tie = ties_before + warps_before(t, sums, warp, lane, total);
+    ties_before += total;
+    uint32_t mine = 0;           // bit it: this lane's row of group it stays
+    int nh = 0, nm = 0;
+#pragma unroll
+    for (int it = 0; it < ITEMS; ++it) {
+      const uint32_t eq = __ballot_sync(kFull, key[it] == cut);
+      const int rank = tie + __popc(eq & ((1u << lane) - 1u));
+      const bool k = key[it] > cut || (key[it] == cut && rank < (int)need);
+      const uint32_t kept = __ballot_sync(kFull, k);
+      mine |= (uint32_t)k << it;
+      tie += __popc(eq);
+      const int i0 = base + 32 * it;
+      const int below = min(max(a.keep - i0, 0), 32);          // positions of the 32 below keep
+      const uint32_t lo = below == 32 ? 0xffffffffu : (1u << below) - 1u;
+      nh += __popc(~kept & lo);
+      nm += __popc(kept & ~lo);
+    }
+    int hole = holes_before + warps_before(nh, sums, warp, lane, total);
+    holes_before += total;
+    int mover = movers_before + warps_before(nm, sums, warp, lane, total);
+    movers_before += total;
+#pragma unroll
+    for (int it = 0; it < ITEMS; ++it) {
+      const int i0 = base + 32 * it, i = i0 + lane;
+      const int below = min(max(a.keep - i0, 0), 32);
+      const uint32_t lo = below == 32 ? 0xffffffffu : (1u << below) - 1u;
+      const uint32_t kept = __ballot_sync(kFull, (mine >> it) & 1u);
+      const uint32_t hm = ~kept & lo, mm = kept & ~lo;
+      const uint32_t lt = (1u << lane) - 1u;
+      if (kQ8 && lane == 0 && i0 % kQ8Block == 0 && i0 / kQ8Block <= a.nblk)
+        a.starts[bh * (a.nblk + 1) + i0 / kQ8Block] = hole;
+      if ((hm >> lane) & 1u) a.holes[bh * a.list + hole + __popc(hm & lt)] = i;
+      if ((mm >> lane) & 1u) a.movers[bh * a.list + mover + __popc(mm & lt)] = i;
+      hole += __popc(hm);
+      mover += __popc(mm);
+    }
+  }
+  if (tid == 0) {
+    a.count[bh] = holes_before;
+    if (kQ8) {      // the entry behind the last block of places (a span may end below it)
+      const int j = (a.keep + kQ8Block - 1) / kQ8Block;
+      a.starts[bh * (a.nblk + 1) + j] = holes_before;
+    }
+  }
+}
+
+// The rest of a moved row, and the new length (by the first CTA of a request).
+__device__ __forceinline__ void move_meta(const EvictArgs& a, long bh, int from, int to) {
+  a.acc[bh * a.map.cap + to] = a.acc[bh * a.map.cap + from];
+  a.pos[bh * a.map.cap + to] = a.pos[bh * a.map.cap + from];
+}
+
+constexpr int kMoveThreads = 256, kMoveUnroll = 4;
+
+__global__ void __launch_bounds__(kMoveThreads) move_kernel(const __grid_constant__ EvictArgs a) {
+  grid_dependency_sync();
+  const int h = blockIdx.y, b = blockIdx.z, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const long bh = (long)b * a.map.Hkv + h;
+  const int n = a.count[bh];
+  if (n < 0) return;
+  if (blockIdx.x == 0 && h == 0 && threadIdx.x == 0) a.prefix_len[b] = a.keep;
+  const int kv = (int)(a.krow / 16), vv = (int)(a.vrow / 16);
+  const int step = gridDim.x * (kMoveThreads / 32);
+  for (int m0 = blockIdx.x * (kMoveThreads / 32) + warp; m0 < n; m0 += step * kMoveUnroll) {
+    long from[kMoveUnroll], to[kMoveUnroll];
+#pragma unroll
+    for (int u = 0; u < kMoveUnroll; ++u) {
+      const int m = m0 + u * step;
+      from[u] = -1;
+      if (m < n) {
+        const int f = a.movers[bh * a.list + m], t = a.holes[bh * a.list + m];
+        from[u] = a.map.row(b, h, f);
+        to[u] = a.map.row(b, h, t);
+        if (lane == 0) move_meta(a, bh, f, t);
+      }
+    }
+    for (int c = lane; c < kv + vv; c += 32) {
+      const bool is_k = c < kv;
+      char* const p = is_k ? a.k : a.v;
+      const long row = is_k ? a.krow : a.vrow;
+      const long off = (long)(is_k ? c : c - kv) * 16;
+      int4 x[kMoveUnroll];
+#pragma unroll
+      for (int u = 0; u < kMoveUnroll; ++u)
+        if (from[u] >= 0) x[u] = *(const int4*)(p + from[u] * row + off);
+#pragma unroll
+      for (int u = 0; u < kMoveUnroll; ++u)
+        if (from[u] >= 0) *(int4*)(p + to[u] * row + off) = x[u];
+    }
+  }
+}
+
+constexpr int kMoveQ8Threads = 128;
+
+__global__ void __launch_bounds__(kMoveQ8Threads)
+move_q8_kernel(const __grid_constant__ EvictArgs a) {
+  __shared__ long s_from[kQ8Block];
+  __shared__ int s_to[kQ8Block];       // place within the block
+  __shared__ uint8_t s_e[2][kQ8Block];
+  __shared__ uint8_t s_hole[kQ8Block];
+  __shared__ int s_max[2];
+  grid_dependency_sync();
+  const int h = blockIdx.y, b = blockIdx.z, tid = threadIdx.x;
+  const long bh = (long)b * a.map.Hkv + h;
+  if (a.count[bh] < 0) return;
+  if (blockIdx.x == 0 && h == 0 && tid == 0) a.prefix_len[b] = a.keep;
+  const int parts = a.vrow ? 2 : 1;
+  for (int j = blockIdx.x; j * kQ8Block < a.keep; j += gridDim.x) {
+    const int h0 = a.starts[bh * (a.nblk + 1) + j], n = a.starts[bh * (a.nblk + 1) + j + 1] - h0;
+    if (n == 0) continue;              // (the same for the whole CTA)
+    const int rows = min(kQ8Block, a.keep - j * kQ8Block);
+    __syncthreads();                   // the block before is done with the shared arrays
+    if (tid < 2) s_max[tid] = 0;
+    if (tid < kQ8Block) s_hole[tid] = 0;
+    __syncthreads();
+    if (tid < n) {
+      const int f = a.movers[bh * a.list + h0 + tid], t = a.holes[bh * a.list + h0 + tid];
+      s_from[tid] = a.map.row(b, h, f);
+      s_to[tid] = t - j * kQ8Block;
+      s_hole[t - j * kQ8Block] = 1;
+      const int ek = a.kexp_old[bh * a.nblk + f / kQ8Block];
+      const int ev = a.vrow ? a.vexp_old[bh * a.nblk + f / kQ8Block] : 0;
+      s_e[0][tid] = (uint8_t)ek;
+      s_e[1][tid] = (uint8_t)ev;
+      atomicMax(&s_max[0], ek);
+      atomicMax(&s_max[1], ev);
+      move_meta(a, bh, f, t);
+    }
+    __syncthreads();
+    const long row0 = a.map.row(b, h, j * kQ8Block);
+    for (int part = 0; part < parts; ++part) {
+      const long rb = part == 0 ? a.krow : a.vrow;
+      uint8_t* const base = (uint8_t*)(part == 0 ? a.k : a.v);
+      const int own = (part == 0 ? a.kexp_old : a.vexp_old)[bh * a.nblk + j];
+      const int e = n < rows ? max(s_max[part], own) : s_max[part];
+      const int vr = (int)(rb / 16);
+      for (int w = tid; w < n * vr; w += kMoveQ8Threads) {
+        const int i = w / vr, c = w - i * vr;
+        uint4 x = *(const uint4*)(base + s_from[i] * rb + c * 16);
+        if (s_e[part][i] != e) {
+          const float f = pow2i((int)s_e[part][i] - e);
+          x.x = q8_rescale4(x.x, f);
+          x.y = q8_rescale4(x.y, f);
+          x.z = q8_rescale4(x.z, f);
+          x.w = q8_rescale4(x.w, f);
+        }
+        *(uint4*)(base + (row0 + s_to[i]) * rb + c * 16) = x;
+      }
+      if (e != own) {
+        const float f = pow2i(own - e);
+        for (int w = tid; w < rows * vr; w += kMoveQ8Threads) {
+          const int r = w / vr;
+          if (s_hole[r]) continue;
+          uint4* const p = (uint4*)(base + row0 * rb + (long)w * 16);
+          uint4 x = *p;
+          x.x = q8_rescale4(x.x, f);
+          x.y = q8_rescale4(x.y, f);
+          x.z = q8_rescale4(x.z, f);
+          x.w = q8_rescale4(x.w, f);
+          *p = x;
+        }
+        if (tid == 0) (part == 0 ? a.kexp : a.vexp)[a.map.block(b, h, j * kQ8Block)] = (uint8_t)e;
+      }
+    }
+  }
+}
+
+struct EvictPlan {
+  size_t count, holes, movers, starts, kexp, vexp, bytes;
+  int list, nblk;
+};
+
+EvictPlan plan_evict(const tsd_attn_desc& d) {
+  EvictPlan p{};
+  const size_t heads = (size_t)d.B * d.Hkv;
+  // at most min(keep, P - keep) rows move
+  p.list = d.cap / 2 + 1;
+  p.nblk = (d.cap + kQ8Block - 1) / kQ8Block;
+  size_t at = 0;
+  auto take = [&](size_t n) {
+    const size_t o = at;
+    at = (at + n + 15) / 16 * 16;
+    return o;
+  };
+  p.count = take(heads * 4);
+  p.holes = take(heads * p.list * 4);
+  p.movers = take(heads * p.list * 4);
+  p.starts = take(heads * (p.nblk + 1) * 4);
+  p.kexp = take(heads * p.nblk);
+  p.vexp = take(heads * p.nblk);
+  p.bytes = at;
+  return p;
+}
+
+template <bool kQ8>
+void launch_select(const EvictArgs& a, int B, cudaStream_t st) {
+  const dim3 grid(a.map.Hkv, B);
+  // keys per thread: enough registers for the whole cache up to 32 Ki rows
+  if (a.map.cap <= 4 * kSelThreads)
+    launch(select_kernel<4, kQ8>, grid, dim3(kSelThreads), 0, st, a);
+  else if (a.map.cap <= 8 * kSelThreads)
+    launch(select_kernel<8, kQ8>, grid, dim3(kSelThreads), 0, st, a);
+  else if (a.map.cap <= 16 * kSelThreads)
+    launch(select_kernel<16, kQ8>, grid, dim3(kSelThreads), 0, st, a);
+  else
+    launch(select_kernel<32, kQ8>, grid, dim3(kSelThreads), 0, st, a);
+}
+
+tsd_status evict_impl(const tsd_attn_desc* d, int keep, int sink, int recent, float* acc,
+                      int32_t* pos, const int32_t* seen, void* k, void* v, void* kexp, void* vexp,
+                      bool q8, const int32_t* page_table, int max_pages, int page_size,
+                      int num_pages, int32_t* prefix_len, void* ws, size_t ws_bytes, int32_t* err,
+                      tsd_stream_t stream) {
+  if (!q8_desc_ok(d) || (((uintptr_t)err) & 3u) != 0) return TSD_ERR_INVALID_ARG;
+  const bool alias = d->v_aliases_k != 0;
+  if (keep < 1 || sink < 0 || recent < 0 || (long)sink + recent > keep) return TSD_ERR_INVALID_ARG;
+  if (!ok_ptr(acc) || !ok_ptr(pos) || !ok_ptr(seen) || !ok_ptr(k) || !ok_ptr(prefix_len))
+    return TSD_ERR_INVALID_ARG;
+  if (!alias && !ok_ptr(v)) return TSD_ERR_INVALID_ARG;
+  if (q8 && (!ok_ptr(kexp) || (!alias && !ok_ptr(vexp)))) return TSD_ERR_INVALID_ARG;
+  if (!paging_ok(d, page_table, max_pages, page_size, num_pages)) return TSD_ERR_INVALID_ARG;
+  const EvictPlan p = plan_evict(*d);
+  if (!ok_ptr(ws) || ws_bytes < p.bytes) return TSD_ERR_INVALID_ARG;
+  if (d->Hkv > 65535) return TSD_ERR_INVALID_ARG;
+
+  const int es = q8 ? 1 : d->dtype == TSD_F32 ? 4 : 2;
+  EvictArgs a{};
+  a.acc = acc;
+  a.pos = pos;
+  a.seen = seen;
+  a.k = (char*)k;
+  a.v = alias ? nullptr : (char*)v;
+  a.kexp = q8 ? (uint8_t*)kexp : nullptr;
+  a.vexp = q8 && !alias ? (uint8_t*)vexp : nullptr;
+  a.prefix_len = prefix_len;
+  a.err = err;
+  a.map = cache_map(d, page_table, max_pages, page_size, num_pages);
+  a.keep = keep;
+  a.sink = sink;
+  a.recent = recent;
+  a.krow = (long)d->dk * es;
+  a.vrow = alias ? 0 : (long)d->dv * es;
+  char* w = (char*)ws;
+  a.count = (int32_t*)(w + p.count);
+  a.holes = (int32_t*)(w + p.holes);
+  a.movers = (int32_t*)(w + p.movers);
+  a.starts = (int32_t*)(w + p.starts);
+  a.kexp_old = (uint8_t*)(w + p.kexp);
+  a.vexp_old = (uint8_t*)(w + p.vexp);
+  a.list = p.list;
+  a.nblk = p.nblk;
+  const cudaStream_t st = (cudaStream_t)stream;
+  if (keep >= d->cap) return TSD_OK;   // no request can hold more
+  const long heads = (long)d->B * d->Hkv;
+  // about eight CTAs per SM over all heads, no more than there can be work for
+  if (q8) {
+    launch_select<true>(a, d->B, st);
+    long x = ceil_div(152L * 8, heads);
+    const long most = ceil_div(keep, kQ8Block);
+    if (x > most) x = most;
+    launch(move_q8_kernel, dim3((unsigned)x, d->Hkv, d->B), dim3(kMoveQ8Threads), 0, st, a);
+  } else {
+    launch_select<false>(a, d->B, st);
+    long x = ceil_div(152L * 8, heads);
+    const long most = ceil_div(p.list, kMoveThreads / 32);
+    if (x > most) x = most;
+    launch(move_kernel, dim3((unsigned)x, d->Hkv, d->B), dim3(kMoveThreads), 0, st, a);
+  }
+  return cuda_status();
+}
+
+}  // namespace
+}  // namespace tsd
+
+using namespace tsd;
+
+extern "C" size_t tsd_cache_evict_workspace_size(const tsd_attn_desc* d) {
+  if (!q8_desc_ok(d)) return 0;
+  return plan_evict(*d).bytes;
+}
+
+extern "C" tsd_status tsd_cache_evict(const tsd_attn_desc* d, int keep, int sink, int recent,
+                                      float* acc, int32_t* pos, const int32_t* seen, void* kcache,
+                                      void* vcache, const int32_t* page_table, int max_pages,
+                                      int page_size, int num_pages, int32_t* prefix_len, void* ws,
+                                      size_t ws_bytes, int32_t* err, tsd_stream_t stream) {
+  return evict_impl(d, keep, sink, recent, acc, pos, seen, kcache, vcache, nullptr, nullptr, false,
+                    page_table, max_pages, page_size, num_pages, prefix_len, ws, ws_bytes, err,
+                    stream);
+}
+
+extern "C" tsd_status tsd_cache_evict_q8(const tsd_attn_desc* d, int keep, int sink, int recent,
+                                         float* acc, int32_t* pos, const int32_t* seen, void* kq,
+                                         void* vq, void* kexp, void* vexp,
+                                         const int32_t* page_table, int max_pages, int page_size,
+                                         int num_pages, int32_t* prefix_len, void* ws,
+                                         size_t ws_bytes, int32_t* err, tsd_stream_t stream) {
+  return evict_impl(d, keep, sink, recent, acc, pos, seen, kq, vq, kexp, vexp, true, page_table,
+                    max_pages, page_size, num_pages, prefix_len, ws, ws_bytes, err, stream);
+}

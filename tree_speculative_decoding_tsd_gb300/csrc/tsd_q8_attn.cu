@@ -1,0 +1,410 @@
+// tsd_tree_verify_attn_q8: branch-aware tree attention over an 8-bit prefix
+// cache (codes and block exponents of tsd_q8.cuh) plus the scratch pad's rows
+// in the element type of q.
+//
+// Source: "Adapting Tree-Structured Speculative Decoding to DeepSeek-V4"
+// (review), research gap item 1 and "How it works" steps 3 and 5, as for
+// tsd_tree_verify_attn.  With s = scale q . k, p = exp(s - m), m the running
+// maximum: out = sum p v / sum p, lse = m + log sum p, in one pass over the
+// keys; splits of the prefix are merged by q8_combine_kernel.
+//
+// Paths: tsd_q8_tc.cu (tcgen05, bf16 heads of 64 or 128 dims), and
+// q8_simt_kernel here: fp32 inputs, computed in fp32 on the CUDA cores.  Its
+// CTA takes up to RB packed rows, one KV head and one split; a warp takes four
+// keys at a time, its lanes split the dims in words of four codes, and the
+// four dot products share their shuffles.  Bound by the shuffles and the
+// multiply-adds (RB x 2 d per key), not by the cache's bytes.
+#include <cuda_bf16.h>
+#include <math.h>
+
+#include "tsd_host.h"
+#include "tsd_q8_attn.cuh"
+
+namespace tsd {
+namespace {
+
+constexpr int kSimtThreads = 128, kSimtWarps = 4, kSimtKeys = 4;
+
+__device__ __forceinline__ float warp_total(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
+  return v;
+}
+
+__device__ __forceinline__ void load4(const float* p, float (&x)[4]) {
+  const float4 v = __ldg((const float4*)p);
+  x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
+}
+__device__ __forceinline__ void load4(const __nv_bfloat16* p, float (&x)[4]) {
+  const uint2 v = __ldg((const uint2*)p);
+  x[0] = __uint_as_float(v.x << 16);
+  x[1] = __uint_as_float(v.x & 0xffff0000u);
+  x[2] = __uint_as_float(v.y << 16);
+  x[3] = __uint_as_float(v.y & 0xffff0000u);
+}
+__device__ __forceinline__ void store_out(float* p, float x) { *p = x; }
+__device__ __forceinline__ void store_out(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
+
+// DV <= DK; ALIAS: the value is the first DV entries of the key.
+template <typename T, int DK, int DV, int RB, bool ALIAS>
+__global__ void __launch_bounds__(kSimtThreads)
+q8_simt_kernel(const __grid_constant__ Q8AttnArgs a) {
+  constexpr int WK = (DK / 4 + 31) / 32, WV = (DV / 4 + 31) / 32;   // words of four per lane
+  __shared__ float sm_m[kSimtWarps][RB], sm_l[kSimtWarps][RB];
+  __shared__ float sm_o[kSimtWarps][RB][DV];
+  grid_dependency_sync();
+  const int sp = blockIdx.x, hk = blockIdx.y / a.nrg, rg = blockIdx.y % a.nrg, b = blockIdx.z;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int P = min(max(a.plen[b], 0), a.map.cap);
+  const int nsb = q8_splits(a, P);
+  if (sp >= nsb) return;
+  const int k0 = min(sp * a.split_len, P), k1 = min(P, k0 + a.split_len);
+
+  float qv[RB][WK][4], o[RB][WV][4], m[RB], l[RB];
+  uint64_t rmask[RB];
+  const int nrows = min(RB, a.M - rg * RB);
+#pragma unroll
+  for (int i = 0; i < RB; ++i) {
+    const bool valid = i < nrows;
+    const int p = valid ? rg * RB + i : 0;
+    const int r = p / a.g, h = hk * a.g + p % a.g;
+    const T* qp = (const T*)a.q + (((long)b * a.R + r) * a.Hq + h) * DK;
+#pragma unroll
+    for (int t = 0; t < WK; ++t) {
+      const int w = lane + 32 * t;
+      float x[4] = {0.f, 0.f, 0.f, 0.f};
+      if (valid && w < DK / 4) load4(qp + 4 * w, x);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) qv[i][t][j] = x[j];
+    }
+    rmask[i] = valid && r > 0 ? a.mask[(long)b * a.R + r] : 0ull;
+    m[i] = -INFINITY;
+    l[i] = 0.f;
+#pragma unroll
+    for (int t = 0; t < WV; ++t)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) o[i][t][j] = 0.f;
+  }
+
+  // four keys with their values (zero where there is none), their weights of
+  // the scores, and for the tree the rows they are (-1: none)
+  auto visit = [&](float (&k)[kSimtKeys][WK][4], float (&v)[kSimtKeys][WV][4],
+                   const bool (&live)[kSimtKeys], bool tree, int j0) {
+#pragma unroll
+    for (int i = 0; i < RB; ++i) {
+      if (i >= nrows) break;
+      float s[kSimtKeys];
+#pragma unroll
+      for (int u = 0; u < kSimtKeys; ++u) {
+        s[u] = 0.f;
+#pragma unroll
+        for (int t = 0; t < WK; ++t)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) s[u] = fmaf(qv[i][t][j], k[u][t][j], s[u]);
+      }
+#pragma unroll
+      for (int x = 16; x > 0; x >>= 1)
+#pragma unroll
+        for (int u = 0; u < kSimtKeys; ++u) s[u] += __shfl_xor_sync(kFull, s[u], x);
+      float mx = m[i];
+#pragma unroll
+      for (int u = 0; u < kSimtKeys; ++u) {
+        const int j = j0 + u;
+        const bool sees = live[u] && (!tree || j == 0 || ((rmask[i] >> (j - 1)) & 1ull));
+        s[u] = sees ? s[u] * a.qscale : -INFINITY;
+        mx = fmaxf(mx, s[u]);
+      }
+      if (mx == -INFINITY) {                               // nothing seen yet, or only NaN
+        bool any = false;
+#pragma unroll
+        for (int u = 0; u < kSimtKeys; ++u) any |= s[u] != s[u];
+        if (!any) continue;
+      }
+      const float al = m[i] == -INFINITY ? 0.f : exp2f(m[i] - mx);
+      m[i] = mx;
+      l[i] *= al;
+#pragma unroll
+      for (int t = 0; t < WV; ++t)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o[i][t][j] *= al;
+#pragma unroll
+      for (int u = 0; u < kSimtKeys; ++u) {
+        if (s[u] == -INFINITY) continue;                   // (its value may be anything)
+        const float p = exp2f(s[u] - mx);
+        l[i] += p;
+#pragma unroll
+        for (int t = 0; t < WV; ++t)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) o[i][t][j] = fmaf(p, v[u][t][j], o[i][t][j]);
+      }
+    }
+  };
+
+  for (int j = k0 + warp * kSimtKeys; j < k1; j += kSimtWarps * kSimtKeys) {
+    float k[kSimtKeys][WK][4], v[kSimtKeys][WV][4];
+    bool live[kSimtKeys];
+    uint32_t kw[kSimtKeys][WK], vw[kSimtKeys][WV];
+    float fk[kSimtKeys], fv[kSimtKeys];
+#pragma unroll
+    for (int u = 0; u < kSimtKeys; ++u) {
+      const long row = j + u < k1 ? a.map.row(b, hk, j + u) : -1;
+      live[u] = row >= 0;
+      if (j + u < k1 && row < 0 && lane == 0) report_error(a.err, TSD_DEV_ERR_BAD_PAGE, b);
+      const long blk = live[u] ? a.map.block(b, hk, j + u) : 0;
+      fk[u] = live[u] ? q8_scale(a.ke[blk]) : 0.f;
+      fv[u] = ALIAS || !live[u] ? fk[u] : q8_scale(a.ve[blk]);
+#pragma unroll
+      for (int t = 0; t < WK; ++t) {
+        const int w = lane + 32 * t;
+        kw[u][t] = live[u] && w < DK / 4 ? __ldg((const uint32_t*)(a.kc + row * DK) + w) : 0u;
+      }
+#pragma unroll
+      for (int t = 0; t < WV; ++t) {
+        const int w = lane + 32 * t;
+        vw[u][t] = ALIAS ? kw[u][t]
+                         : live[u] && w < DV / 4 ? __ldg((const uint32_t*)(a.vc + row * DV) + w) : 0u;
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kSimtKeys; ++u) {
+#pragma unroll
+      for (int t = 0; t < WK; ++t) {
+        q8_unpack4(kw[u][t], k[u][t]);
+#pragma unroll
+        for (int x = 0; x < 4; ++x) k[u][t][x] *= fk[u];
+      }
+#pragma unroll
+      for (int t = 0; t < WV; ++t) {
+        q8_unpack4(vw[u][t], v[u][t]);
+#pragma unroll
+        for (int x = 0; x < 4; ++x) v[u][t][x] *= fv[u];
+      }
+    }
+    visit(k, v, live, false, 0);
+  }
+  if (sp == nsb - 1) {
+    const T* kt = (const T*)a.kt + ((long)b * a.R * a.map.Hkv + hk) * DK;
+    const T* vt = ALIAS ? kt : (const T*)a.vt + ((long)b * a.R * a.map.Hkv + hk) * DV;
+    constexpr int VS = ALIAS ? DK : DV;
+    for (int j = warp * kSimtKeys; j < a.R; j += kSimtWarps * kSimtKeys) {
+      float k[kSimtKeys][WK][4], v[kSimtKeys][WV][4];
+      bool live[kSimtKeys];
+#pragma unroll
+      for (int u = 0; u < kSimtKeys; ++u) {
+        live[u] = j + u < a.R;
+#pragma unroll
+        for (int t = 0; t < WK; ++t) {
+          const int w = lane + 32 * t;
+          float x[4] = {0.f, 0.f, 0.f, 0.f};
+          if (live[u] && w < DK / 4) load4(kt + (long)(j + u) * a.map.Hkv * DK + 4 * w, x);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) k[u][t][c] = x[c];
+        }
+#pragma unroll
+        for (int t = 0; t < WV; ++t) {
+          const int w = lane + 32 * t;
+          float x[4] = {0.f, 0.f, 0.f, 0.f};
+          if (live[u] && w < DV / 4) load4(vt + (long)(j + u) * a.map.Hkv * VS + 4 * w, x);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) v[u][t][c] = x[c];
+        }
+      }
+      visit(k, v, live, true, j);
+    }
+  }
+
+  // merge the four warps' running states
+#pragma unroll
+  for (int i = 0; i < RB; ++i) {
+    if (lane == 0) { sm_m[warp][i] = m[i]; sm_l[warp][i] = l[i]; }
+#pragma unroll
+    for (int t = 0; t < WV; ++t)
+      if (lane + 32 * t < DV / 4)
+        *(float4*)&sm_o[warp][i][4 * (lane + 32 * t)] =
+            make_float4(o[i][t][0], o[i][t][1], o[i][t][2], o[i][t][3]);
+  }
+  __syncthreads();
+  for (int idx = threadIdx.x; idx < nrows * DV; idx += kSimtThreads) {
+    const int i = idx / DV, c = idx - i * DV;
+    float mx = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < kSimtWarps; ++w) mx = fmaxf(mx, sm_m[w][i]);
+    float lt = 0.f, ot = 0.f;
+#pragma unroll
+    for (int w = 0; w < kSimtWarps; ++w) {
+      const float wt = sm_m[w][i] == -INFINITY ? 0.f : exp2f(sm_m[w][i] - mx);
+      lt = fmaf(sm_l[w][i], wt, lt);
+      ot = fmaf(sm_o[w][i][c], wt, ot);
+    }
+    // (a split whose pages are all missing saw nothing: weight 0)
+    const float res = mx == -INFINITY && lt == 0.f ? 0.f : ot / lt;
+    const float lse2 = mx + log2f(lt);
+    const int p = rg * RB + i;
+    const int r = p / a.g, h = hk * a.g + p % a.g;
+    const long orow = ((long)b * a.R + r) * a.Hq + h;
+    if (nsb == 1) {
+      store_out((T*)a.out + orow * DV + c, res);
+      if (c == 0) a.lse[orow] = lse2 * 0.69314718055994531f;
+    } else {
+      const long prow = (((long)b * a.Hq + h) * a.R + r) * a.nsplit + sp;
+      ((float*)a.part_o)[prow * DV + c] = res;
+      if (c == 0) a.part_meta[prow] = make_float2(lse2, 1.f);
+    }
+  }
+}
+
+// Merge of the splits of one output row by one warp: with L_s the log2-sum-exp
+// and c_s the scale of split s, out = sum_s 2^(L_s - L) c_s O_s and
+// L = log2 sum_s 2^(L_s).  PT: element type of the partial outputs.
+template <typename T, int DV, typename PT>
+__global__ void __launch_bounds__(128) q8_combine_kernel(const __grid_constant__ Q8AttnArgs a) {
+  grid_dependency_sync();
+  constexpr int NV = DV / 32;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const long row = (long)blockIdx.x * 4 + warp;
+  if (row >= (long)a.B * a.R * a.Hq) return;
+  const int b = (int)(row / ((long)a.R * a.Hq)), r = (int)((row / a.Hq) % a.R), h = (int)(row % a.Hq);
+  const int P = min(max(a.plen[b], 0), a.map.cap);
+  const int n = q8_splits(a, P);
+  if (n == 1) return;                    // written by its only split
+  const long base = (((long)b * a.Hq + h) * a.R + r) * a.nsplit;
+  float mx = -INFINITY;
+  for (int s = lane; s < n; s += 32) mx = fmaxf(mx, a.part_meta[base + s].x);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, o));
+  float sum = 0.f;
+  for (int s = lane; s < n; s += 32) {
+    const float L = a.part_meta[base + s].x;
+    if (L != -INFINITY) sum += exp2f(L - mx);
+  }
+  sum = warp_total(sum);
+  float acc[NV];
+#pragma unroll
+  for (int t = 0; t < NV; ++t) acc[t] = 0.f;
+  const PT* parts = (const PT*)a.part_o + base * DV;
+  for (int s0 = 0; s0 < n; s0 += 32) {
+    float w = 0.f;
+    if (s0 + lane < n) {
+      const float2 meta = a.part_meta[base + s0 + lane];
+      // the weight first, then the scale: each alone may be far from 1
+      w = meta.x == -INFINITY ? 0.f : exp2f(meta.x - mx) / sum * meta.y;
+    }
+    const int m = min(32, n - s0);
+#pragma unroll 4
+    for (int s = 0; s < m; ++s) {
+      const float ws = __shfl_sync(kFull, w, s);
+#pragma unroll
+      for (int t = 0; t < NV; ++t)
+        acc[t] = fmaf(ws, (float)parts[(long)(s0 + s) * DV + lane + 32 * t], acc[t]);
+    }
+  }
+#pragma unroll
+  for (int t = 0; t < NV; ++t) store_out((T*)a.out + row * DV + lane + 32 * t, acc[t]);
+  if (lane == 0) a.lse[row] = (mx + log2f(sum)) * 0.69314718055994531f;
+}
+
+Q8Plan plan_q8(const tsd_attn_desc& d) {
+  Q8Plan p{};
+  const int M = d.R * (d.Hq / d.Hkv);
+  p.path = kQ8Simt;
+  p.part_bytes = 4;
+  p.rb = d.dk > 128 ? 2 : 4;
+  p.nrg = (int)ceil_div(M, p.rb);
+  // about four CTAs per SM over the whole batch, splits of at least 64 keys
+  long ns = ceil_div(152L * 4, (long)d.B * d.Hkv * p.nrg);
+  const long most = ceil_div(d.cap, 64);
+  if (ns > most) ns = most;
+  p.split_len = (int)ceil_div(d.cap, ns);
+  p.nsplit = (int)ceil_div(d.cap, p.split_len);
+  p.ws_bytes = p.nsplit > 1 ? (size_t)d.B * d.Hq * d.R * p.nsplit *
+                                  (d.dv * (size_t)p.part_bytes + sizeof(float2))
+                            : 0;
+  return p;
+}
+
+template <typename T, int DV, typename PT>
+void launch_combine(const Q8AttnArgs& a, const Q8Plan& p, cudaStream_t st) {
+  if (p.nsplit <= 1) return;
+  const long rows = (long)a.B * a.R * a.Hq;
+  launch_plain(q8_combine_kernel<T, DV, PT>, dim3((unsigned)ceil_div(rows, 4)), dim3(128), 0, st, a);
+}
+
+template <typename T, int DK, int DV, int RB, bool ALIAS>
+void launch_simt(const Q8AttnArgs& a, const Q8Plan& p, cudaStream_t st) {
+  launch(q8_simt_kernel<T, DK, DV, RB, ALIAS>, dim3(p.nsplit, a.map.Hkv * p.nrg, a.B),
+         dim3(kSimtThreads), 0, st, a);
+  launch_combine<T, DV, float>(a, p, st);
+}
+
+}  // namespace
+}  // namespace tsd
+
+using namespace tsd;
+
+extern "C" size_t tsd_verify_q8_workspace_size(const tsd_attn_desc* d) {
+  if (!q8_desc_ok(d, true)) return 0;
+  return plan_q8(*d).ws_bytes;
+}
+
+extern "C" tsd_status tsd_tree_verify_attn_q8(const tsd_attn_desc* d, const void* q,
+                                              const void* kq, const void* vq, const void* kexp,
+                                              const void* vexp, const int32_t* page_table,
+                                              int max_pages, int page_size, int num_pages,
+                                              const int32_t* prefix_len, const void* ktree,
+                                              const void* vtree, const uint64_t* mask, void* out,
+                                              float* lse, void* ws, size_t ws_bytes, int32_t* err,
+                                              tsd_stream_t stream) {
+  if (!q8_desc_ok(d, true) || (((uintptr_t)err) & 3u) != 0) return TSD_ERR_INVALID_ARG;
+  const bool alias = d->v_aliases_k != 0;
+  if (!ok_ptr(q) || !ok_ptr(kq) || !ok_ptr(kexp) || !ok_ptr(prefix_len) || !ok_ptr(ktree) ||
+      !ok_ptr(mask) || !ok_ptr(out) || !ok_ptr(lse))
+    return TSD_ERR_INVALID_ARG;
+  if (!alias && (!ok_ptr(vq) || !ok_ptr(vexp) || !ok_ptr(vtree))) return TSD_ERR_INVALID_ARG;
+  if (!paging_ok(d, page_table, max_pages, page_size, num_pages)) return TSD_ERR_INVALID_ARG;
+  const Q8Plan p = plan_q8(*d);
+  if ((long)d->Hkv * p.nrg > 65535 || p.nsplit > 65535) return TSD_ERR_INVALID_ARG;
+  if (ws_bytes < p.ws_bytes || (p.ws_bytes > 0 && !ok_ptr(ws))) return TSD_ERR_INVALID_ARG;
+  Q8AttnArgs a{};
+  a.q = q;
+  a.kc = (const uint8_t*)kq;
+  a.vc = alias ? nullptr : (const uint8_t*)vq;
+  a.ke = (const uint8_t*)kexp;
+  a.ve = alias ? nullptr : (const uint8_t*)vexp;
+  a.plen = prefix_len;
+  a.kt = ktree;
+  a.vt = alias ? nullptr : vtree;
+  a.mask = mask;
+  a.out = out;
+  a.lse = lse;
+  if (p.nsplit > 1) {
+    const size_t parts = (size_t)d->B * d->Hq * d->R * p.nsplit;
+    a.part_o = ws;
+    a.part_meta = (float2*)((char*)ws + parts * d->dv * p.part_bytes);
+  }
+  a.err = err;
+  a.map = cache_map(d, page_table, max_pages, page_size, num_pages);
+  a.B = d->B;
+  a.R = d->R;
+  a.Hq = d->Hq;
+  a.g = d->Hq / d->Hkv;
+  a.M = d->R * a.g;
+  a.nsplit = p.nsplit;
+  a.split_len = p.split_len;
+  a.nrg = p.nrg;
+  a.rb = p.rb;
+  a.tree_split = p.tree_split;
+  a.qscale = d->scale * 1.4426950408889634f;
+  const cudaStream_t st = (cudaStream_t)stream;
+  const bool f32 = d->dtype == TSD_F32;
+  if (alias) {
+    if (f32) launch_simt<float, 576, 512, 2, true>(a, p, st);
+    else launch_simt<__nv_bfloat16, 576, 512, 2, true>(a, p, st);
+  } else if (d->dk == 128) {
+    if (f32) launch_simt<float, 128, 128, 4, false>(a, p, st);
+    else launch_simt<__nv_bfloat16, 128, 128, 4, false>(a, p, st);
+  } else {
+    if (f32) launch_simt<float, 64, 64, 4, false>(a, p, st);
+    else launch_simt<__nv_bfloat16, 64, 64, 4, false>(a, p, st);
+  }
+  return cuda_status();
+}

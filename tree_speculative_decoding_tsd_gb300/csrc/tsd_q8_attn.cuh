@@ -1,0 +1,50 @@
+// Shared declarations of the attention paths over the 8-bit cache.
+#pragma once
+
+#include "tsd_q8.cuh"
+
+namespace tsd {
+
+struct Q8AttnArgs {
+  const void* q;
+  const uint8_t* kc;
+  const uint8_t* vc;          // null: the value is the first dv entries of the key
+  const uint8_t* ke;
+  const uint8_t* ve;
+  const int32_t* plen;
+  const void* kt;
+  const void* vt;
+  const uint64_t* mask;
+  void* out;
+  float* lse;
+  void* part_o;               // [B][Hq][R][nsplit][dv] normalised outputs of the splits, over scale
+  float2* part_meta;          // [B][Hq][R][nsplit] (log2-sum-exp, scale)
+  int32_t* err;
+  CacheMap map;
+  int B, R, Hq, g, M;
+  int nsplit, split_len, nrg, rb, tree_split;
+  float qscale;               // softmax scale * log2(e)
+};
+
+enum Q8Path { kQ8Simt = 0, kQ8Tc = 1, kQ8Latent = 2 };
+
+struct Q8Plan {
+  int path;
+  int rb, nrg;                // packed rows per CTA, row groups per KV head
+  int nsplit, split_len;
+  int tree_split;             // the tree rows are a split of their own, behind the prefix splits
+  int part_bytes;             // element size of a split's output: 4 (fp32) or 2 (fp16)
+  size_t ws_bytes;
+};
+
+// Splits that hold work for a request of prefix length P.
+__device__ __forceinline__ int q8_splits(const Q8AttnArgs& a, int P) {
+  const int npre = P > 0 ? (P + a.split_len - 1) / a.split_len : 0;
+  return a.tree_split ? npre + 1 : max(npre, 1);
+}
+
+bool launch_q8_tc(const tsd_attn_desc& d, const Q8AttnArgs& a, const Q8Plan& p, cudaStream_t st);
+bool launch_q8_latent(const tsd_attn_desc& d, const Q8AttnArgs& a, const Q8Plan& p,
+                      cudaStream_t st);
+
+}  // namespace tsd

@@ -1,0 +1,283 @@
+// tsd_cache_write_q8, tsd_commit_path_q8: rows appended to the 8-bit cache.
+//
+// For each request, n rows land at positions P..P+n-1 (P the prefix length):
+// rows 0..n-1 of a dense [B][T] array (a prefill), or the accepted rows of the
+// scratch pad (a commit; Source: "Adapting Tree-Structured Speculative Decoding
+// to DeepSeek-V4" (review), "Secret weapon" and "How it works" step 6: only the
+// accepted path's KV is written).  Per block of 64 tokens that holds a new row
+// and per head:
+//   a  = max |x| over the block's new rows (finite elements)
+//   e' = max(e, need(a)) if the block holds earlier rows, else need(a)
+//   new codes = e4m3(x * 2^(127 - e')), earlier codes c -> e4m3(c * 2^(e - e'))
+// Products with powers of two are exact in fp32, so each code is rounded once
+// (an earlier code only where it becomes subnormal).
+//
+// write_block: one CTA takes a (block, head, K or V): the new rows stay in
+// registers between the maximum and the conversion, so the source is read
+// once and the codes are written once; earlier rows are read only when the
+// exponent grows.  Bounded by memory: 2 (or 4) bytes read and 1 written per
+// element.
+#include <cuda_bf16.h>
+
+#include "tsd_host.h"
+#include "tsd_q8.cuh"
+
+namespace tsd {
+namespace {
+
+struct Q8WriteArgs {
+  const void* src[2];      // K, V rows: [B][rows][Hkv][d]
+  uint8_t* codes[2];
+  uint8_t* exps[2];
+  int32_t* prefix_len;
+  const int32_t* count;    // commit: accepted draft rows L (L + 1 rows move); write: rows n
+  const int32_t* path;     // commit: [B][S+1] source rows
+  int32_t* err;
+  CacheMap map;
+  int rows, S, parts;      // source rows per request; path length bound; 1 (latent) or 2
+};
+
+constexpr int kNoCode = 0x7fffffff;
+
+// Threads of a CTA, and 8-element vectors of a block per thread.
+template <int D> constexpr int kWriteThreads = D > 128 ? 512 : 256;
+template <int D> constexpr int kWriteVecs = kQ8Block * D / 8 / kWriteThreads<D>;
+
+// Rows that request b appends (0 for none), or minus the error code that makes
+// the request be skipped: every thread of the CTA gets the same answer.
+template <bool kCommit>
+__device__ __forceinline__ int write_rows(const Q8WriteArgs& a, int b, int P, int& shared_code) {
+  if (threadIdx.x == 0) shared_code = kNoCode;
+  __syncthreads();
+  const int c = a.count[b];
+  int code = 0;
+  const long n = kCommit ? (long)c + 1 : c;
+  if (kCommit && (c < 0 || c > a.S)) code = TSD_DEV_ERR_BAD_TREE;
+  else if (!kCommit && (c < 0 || c > a.rows)) code = TSD_DEV_ERR_CAPACITY;
+  else if (P < 0 || P + n > a.map.cap) code = TSD_DEV_ERR_CAPACITY;
+  else {
+    if (kCommit)
+      for (int i = threadIdx.x; i < n; i += blockDim.x) {
+        const int r = a.path[(long)b * (a.S + 1) + i];
+        if (r < 0 || r >= a.rows) code = TSD_DEV_ERR_BAD_TREE;
+      }
+    if (a.map.page_size && n > 0) {
+      const int p1 = (int)((P + n - 1) / a.map.page_size);
+      for (int p = P / a.map.page_size + threadIdx.x; p <= p1; p += blockDim.x) {
+        const int pg = a.map.page_table[(long)b * a.map.max_pages + p];
+        if ((pg < 0 || pg >= a.map.num_pages) && code == 0) code = TSD_DEV_ERR_BAD_PAGE;
+      }
+    }
+  }
+  if (code != 0) atomicMin(&shared_code, code);
+  __syncthreads();
+  code = shared_code;
+  return code != kNoCode ? -code : (int)n;
+}
+
+// Block `blk` (positions 64 blk ..) of head h of request b, part 0 (K) or 1 (V).
+template <typename T, int D, bool kCommit>
+__device__ __forceinline__ void write_block(const Q8WriteArgs& a, int b, int h, int part, int blk,
+                                            int P, int n, uint32_t* warp_max) {
+  constexpr int kThreads = kWriteThreads<D>, kVecs = kWriteVecs<D>, VR = D / 8;
+  const int tid = threadIdx.x;
+  const int first = blk * kQ8Block;
+  const int r0 = max(P - first, 0);                  // the block's earlier rows end here
+  const int r1 = min(P + n - first, kQ8Block);       // and its new ones here
+  float x[kVecs][8];
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < kVecs; ++i) {
+    const int r = (tid + i * kThreads) / VR, c = (tid + i * kThreads) % VR;
+    if (r >= r0 && r < r1) {
+      int t = first + r - P;
+      if (kCommit) t = a.path[(long)b * (a.S + 1) + t];
+      load8((const T*)a.src[part] + (((long)b * a.rows + t) * a.map.Hkv + h) * D + c * 8, x[i]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x[i][j] = 0.f;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kVecs; ++i)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const uint32_t u = __float_as_uint(x[i][j]) & 0x7fffffffu;
+      m = max(m, u < 0x7f800000u ? u : 0u);          // infinities and NaN do not count
+    }
+  m = __reduce_max_sync(kFull, m);
+  __syncthreads();                                   // (warp_max of the task before)
+  if ((tid & 31) == 0) warp_max[tid >> 5] = m;
+  __syncthreads();
+  m = 0;
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) m = max(m, warp_max[w]);
+  uint8_t* const ep = a.exps[part] + a.map.block(b, h, first);
+  const int e_old = r0 > 0 ? *ep : 0;
+  const int e = max(q8_need(__uint_as_float(m)), e_old);
+  const float inv = q8_scale(254 - min(e, kQ8ExpMax));  // 2^(127 - e)
+  uint8_t* const row0 = a.codes[part] + a.map.row(b, h, first) * D;
+#pragma unroll
+  for (int i = 0; i < kVecs; ++i) {
+    const int v = tid + i * kThreads, r = v / VR;
+    if (r >= r0 && r < r1) {
+      uint2 w;
+      w.x = q8_pack4(x[i][0] * inv, x[i][1] * inv, x[i][2] * inv, x[i][3] * inv);
+      w.y = q8_pack4(x[i][4] * inv, x[i][5] * inv, x[i][6] * inv, x[i][7] * inv);
+      *(uint2*)(row0 + (long)v * 8) = w;
+    }
+  }
+  if (r0 > 0 && e != e_old) {
+    const float f = pow2i(e_old - e);
+    for (int v = tid; v < r0 * (D / 16); v += kThreads) {
+      uint4 w = *(uint4*)(row0 + (long)v * 16);
+      w.x = q8_rescale4(w.x, f);
+      w.y = q8_rescale4(w.y, f);
+      w.z = q8_rescale4(w.z, f);
+      w.w = q8_rescale4(w.w, f);
+      *(uint4*)(row0 + (long)v * 16) = w;
+    }
+  }
+  // (every thread has read the exponent before the barrier that follows)
+  __syncthreads();
+  if (tid == 0 && (r0 == 0 || e != e_old)) *ep = (uint8_t)e;
+}
+
+// Prefill: grid (blocks, part x head, request).  prefix_len changes only in
+// write_advance_kernel, so every CTA reads the length of before.
+template <typename T, int D>
+__global__ void __launch_bounds__(kWriteThreads<D>)
+write_q8_kernel(const __grid_constant__ Q8WriteArgs a) {
+  __shared__ int code;
+  __shared__ uint32_t warp_max[32];
+  grid_dependency_sync();
+  const int b = blockIdx.z, P = a.prefix_len[b];
+  const int n = write_rows<false>(a, b, P, code);
+  if (n <= 0) return;
+  const int blk = P / kQ8Block + blockIdx.x;
+  if (blk * (long)kQ8Block >= (long)P + n) return;
+  write_block<T, D, false>(a, b, blockIdx.y / a.parts, blockIdx.y % a.parts, blk, P, n, warp_max);
+}
+
+__global__ void __launch_bounds__(128) write_advance_kernel(const __grid_constant__ Q8WriteArgs a) {
+  __shared__ int code;
+  grid_dependency_sync();
+  const int b = blockIdx.x, P = a.prefix_len[b];
+  const int n = write_rows<false>(a, b, P, code);
+  if (threadIdx.x != 0) return;
+  if (n < 0) report_error(a.err, -n, b);
+  else a.prefix_len[b] = P + n;
+}
+
+// Commit: at most 17 rows, so at most two blocks per head and part.  One
+// cluster of kCommitCtas CTAs per request shares the (block, head, part) tasks;
+// the cluster barrier lets rank 0 advance the prefix length after every CTA
+// has read it, which saves a second launch (about 2 us of a 4 us call).
+constexpr int kCommitCtas = 8;
+
+template <typename T, int D>
+__global__ void __cluster_dims__(kCommitCtas, 1, 1) __launch_bounds__(kWriteThreads<D>)
+commit_q8_kernel(const __grid_constant__ Q8WriteArgs a) {
+  __shared__ int code;
+  __shared__ uint32_t warp_max[32];
+  grid_dependency_sync();
+  const int b = blockIdx.y, P = a.prefix_len[b];
+  const int n = write_rows<true>(a, b, P, code);     // (its barrier: the whole CTA has read P)
+  asm volatile("barrier.cluster.arrive.aligned;\n" ::: "memory");
+  if (n > 0) {
+    const int blk0 = P / kQ8Block, nb = (P + n - 1) / kQ8Block - blk0 + 1;
+    const int tasks = nb * a.map.Hkv * a.parts;
+    for (int t = blockIdx.x; t < tasks; t += kCommitCtas) {
+      const int hp = t / nb;
+      write_block<T, D, true>(a, b, hp / a.parts, hp % a.parts, blk0 + t % nb, P, n, warp_max);
+    }
+  }
+  asm volatile("barrier.cluster.wait.aligned;\n" ::: "memory");
+  if (blockIdx.x == 0 && threadIdx.x == 0) {
+    if (n < 0) report_error(a.err, -n, b);
+    else a.prefix_len[b] = P + n;
+  }
+}
+
+template <typename T, int D>
+void launch_write(const Q8WriteArgs& a, int B, int nblk, bool commit, cudaStream_t st) {
+  if (commit) {
+    launch(commit_q8_kernel<T, D>, dim3(kCommitCtas, B), dim3(kWriteThreads<D>), 0, st, a);
+    return;
+  }
+  launch(write_q8_kernel<T, D>, dim3(nblk, a.map.Hkv * a.parts, B), dim3(kWriteThreads<D>), 0, st, a);
+  launch(write_advance_kernel, dim3(B), dim3(128), 0, st, a);
+}
+
+tsd_status write_impl(const tsd_attn_desc* d, int rows, int S, const void* k, const void* v,
+                      const int32_t* path, const int32_t* count, void* kq, void* vq, void* kexp,
+                      void* vexp, const int32_t* page_table, int max_pages, int page_size,
+                      int num_pages, int32_t* prefix_len, int32_t* err, bool commit,
+                      tsd_stream_t stream) {
+  if (!q8_desc_ok(d) || (((uintptr_t)err) & 3u) != 0) return TSD_ERR_INVALID_ARG;
+  const bool alias = d->v_aliases_k != 0;
+  if (rows < 1 || (commit && (S < 1 || S > 16 || !ok_ptr(path)))) return TSD_ERR_INVALID_ARG;
+  if (!ok_ptr(k) || !ok_ptr(count) || !ok_ptr(kq) || !ok_ptr(kexp) || !ok_ptr(prefix_len))
+    return TSD_ERR_INVALID_ARG;
+  if (!alias && (!ok_ptr(v) || !ok_ptr(vq) || !ok_ptr(vexp))) return TSD_ERR_INVALID_ARG;
+  if (!paging_ok(d, page_table, max_pages, page_size, num_pages)) return TSD_ERR_INVALID_ARG;
+  Q8WriteArgs a{};
+  a.src[0] = k;
+  a.src[1] = alias ? nullptr : v;
+  a.codes[0] = (uint8_t*)kq;
+  a.codes[1] = alias ? nullptr : (uint8_t*)vq;
+  a.exps[0] = (uint8_t*)kexp;
+  a.exps[1] = alias ? nullptr : (uint8_t*)vexp;
+  a.prefix_len = prefix_len;
+  a.count = count;
+  a.path = path;
+  a.err = err;
+  a.map = cache_map(d, page_table, max_pages, page_size, num_pages);
+  a.rows = rows;
+  a.S = S;
+  a.parts = alias ? 1 : 2;
+  // n rows from any position of a block span at most this many blocks, and no
+  // more than the cache has
+  const long span = ((long)(rows < d->cap ? rows : d->cap) + kQ8Block - 2) / kQ8Block + 1;
+  const cudaStream_t st = (cudaStream_t)stream;
+  const bool f32 = d->dtype == TSD_F32;
+  if ((long)d->Hkv * a.parts > 65535) return TSD_ERR_INVALID_ARG;
+  if (d->dk == 576) {
+    if (f32) launch_write<float, 576>(a, d->B, (int)span, commit, st);
+    else launch_write<__nv_bfloat16, 576>(a, d->B, (int)span, commit, st);
+  } else if (d->dk == 128) {
+    if (f32) launch_write<float, 128>(a, d->B, (int)span, commit, st);
+    else launch_write<__nv_bfloat16, 128>(a, d->B, (int)span, commit, st);
+  } else {
+    if (f32) launch_write<float, 64>(a, d->B, (int)span, commit, st);
+    else launch_write<__nv_bfloat16, 64>(a, d->B, (int)span, commit, st);
+  }
+  return cuda_status();
+}
+
+}  // namespace
+}  // namespace tsd
+
+using namespace tsd;
+
+extern "C" tsd_status tsd_cache_write_q8(const tsd_attn_desc* d, int T, const void* knew,
+                                         const void* vnew, const int32_t* new_len, void* kq,
+                                         void* vq, void* kexp, void* vexp,
+                                         const int32_t* page_table, int max_pages, int page_size,
+                                         int num_pages, int32_t* prefix_len, int32_t* err,
+                                         tsd_stream_t stream) {
+  return write_impl(d, T, 0, knew, vnew, nullptr, new_len, kq, vq, kexp, vexp, page_table,
+                    max_pages, page_size, num_pages, prefix_len, err, false, stream);
+}
+
+extern "C" tsd_status tsd_commit_path_q8(const tsd_attn_desc* d, int S, const void* ktree,
+                                         const void* vtree, const int32_t* accept_rows,
+                                         const int32_t* accept_len, void* kq, void* vq,
+                                         void* kexp, void* vexp, const int32_t* page_table,
+                                         int max_pages, int page_size, int num_pages,
+                                         int32_t* prefix_len, int32_t* err,
+                                         tsd_stream_t stream) {
+  if (d == nullptr) return TSD_ERR_INVALID_ARG;
+  return write_impl(d, d->R, S, ktree, vtree, accept_rows, accept_len, kq, vq, kexp, vexp,
+                    page_table, max_pages, page_size, num_pages, prefix_len, err, true, stream);
+}
