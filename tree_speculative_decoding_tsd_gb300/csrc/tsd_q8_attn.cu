@@ -306,16 +306,40 @@ __global__ void __launch_bounds__(128) q8_combine_kernel(const __grid_constant__
 Q8Plan plan_q8(const tsd_attn_desc& d) {
   Q8Plan p{};
   const int M = d.R * (d.Hq / d.Hkv);
-  p.path = kQ8Simt;
-  p.part_bytes = 4;
-  p.rb = d.dk > 128 ? 2 : 4;
-  p.nrg = (int)ceil_div(M, p.rb);
-  // about four CTAs per SM over the whole batch, splits of at least 64 keys
-  long ns = ceil_div(152L * 4, (long)d.B * d.Hkv * p.nrg);
-  const long most = ceil_div(d.cap, 64);
-  if (ns > most) ns = most;
-  p.split_len = (int)ceil_div(d.cap, ns);
-  p.nsplit = (int)ceil_div(d.cap, p.split_len);
+  if (d.dtype == TSD_BF16 && !d.v_aliases_k) {
+    // tcgen05: at most 112 packed rows per CTA (shared memory), in equal groups
+    p.path = kQ8Tc;
+    p.part_bytes = 2;
+    p.nrg = (int)ceil_div(M, 112);
+    p.rb = (int)ceil_div(ceil_div(M, p.nrg), 16) * 16;
+    // One CTA per SM.  The split count minimises the modelled time of requests
+    // that fill the cache: waves of CTAs times (tiles of a CTA + 4 for its
+    // set-up and epilogue).
+    const long units = (long)d.B * d.Hkv * p.nrg, tiles = ceil_div(d.cap, 128);
+    const long lo = ceil_div(tiles, 256), hi = lo > 64 ? lo : tiles < 64 ? tiles : 64;
+    long best = -1, best_per = tiles;
+    for (long n = lo; n <= hi; ++n) {
+      const long per = ceil_div(tiles, n);
+      const long cost = ceil_div(units * ceil_div(tiles, per), 152L) * (per + 4);
+      if (best < 0 || cost < best) { best = cost; best_per = per; }
+    }
+    p.split_len = (int)best_per * 128;
+    p.nsplit = (int)ceil_div(d.cap, p.split_len);
+    // short splits: the scratch rows are a split of their own, not a longer last one
+    p.tree_split = p.nsplit > 1 && best_per <= 8 ? 1 : 0;
+    p.nsplit += p.tree_split;
+  } else {
+    p.path = kQ8Simt;
+    p.part_bytes = 4;
+    p.rb = d.dk > 128 ? 2 : 4;
+    p.nrg = (int)ceil_div(M, p.rb);
+    // about four CTAs per SM over the whole batch, splits of at least 64 keys
+    long ns = ceil_div(152L * 4, (long)d.B * d.Hkv * p.nrg);
+    const long most = ceil_div(d.cap, 64);
+    if (ns > most) ns = most;
+    p.split_len = (int)ceil_div(d.cap, ns);
+    p.nsplit = (int)ceil_div(d.cap, p.split_len);
+  }
   p.ws_bytes = p.nsplit > 1 ? (size_t)d.B * d.Hq * d.R * p.nsplit *
                                   (d.dv * (size_t)p.part_bytes + sizeof(float2))
                             : 0;
@@ -396,15 +420,17 @@ extern "C" tsd_status tsd_tree_verify_attn_q8(const tsd_attn_desc* d, const void
   a.qscale = d->scale * 1.4426950408889634f;
   const cudaStream_t st = (cudaStream_t)stream;
   const bool f32 = d->dtype == TSD_F32;
-  if (alias) {
+  if (p.path == kQ8Tc) {
+    if (!launch_q8_tc(*d, a, p, st)) return TSD_ERR_UNSUPPORTED;
+    if (d->dv == 128) launch_combine<__nv_bfloat16, 128, __half>(a, p, st);
+    else launch_combine<__nv_bfloat16, 64, __half>(a, p, st);
+  } else if (alias) {
     if (f32) launch_simt<float, 576, 512, 2, true>(a, p, st);
     else launch_simt<__nv_bfloat16, 576, 512, 2, true>(a, p, st);
   } else if (d->dk == 128) {
-    if (f32) launch_simt<float, 128, 128, 4, false>(a, p, st);
-    else launch_simt<__nv_bfloat16, 128, 128, 4, false>(a, p, st);
+    launch_simt<float, 128, 128, 4, false>(a, p, st);
   } else {
-    if (f32) launch_simt<float, 64, 64, 4, false>(a, p, st);
-    else launch_simt<__nv_bfloat16, 64, 64, 4, false>(a, p, st);
+    launch_simt<float, 64, 64, 4, false>(a, p, st);
   }
   return cuda_status();
 }
