@@ -72,14 +72,17 @@ __device__ __forceinline__ uint32_t q8_pack2(float a, float b) {
 __device__ __forceinline__ uint32_t q8_pack4(float a, float b, float c, float d) {
   return q8_pack2(a, b) | (q8_pack2(c, d) << 16);
 }
-// Two codes (low 16 bits of w) as fp16, exactly.
-__device__ __forceinline__ uint32_t q8_half2(uint32_t w) {
-  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w & 0xffffu), __NV_E4M3);
-  return (uint32_t)h.x | ((uint32_t)h.y << 16);
+// Four codes as two pairs of fp16, exactly.
+__device__ __forceinline__ void q8_half4(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  asm("{\n .reg .b16 a, b;\n mov.b32 {a, b}, %2;\n cvt.rn.f16x2.e4m3x2 %0, a;\n"
+      " cvt.rn.f16x2.e4m3x2 %1, b;\n}\n"
+      : "=r"(lo), "=r"(hi)
+      : "r"(w));
 }
 // Four codes as fp32.
 __device__ __forceinline__ void q8_unpack4(uint32_t w, float (&v)[4]) {
-  const uint32_t a = q8_half2(w), b = q8_half2(w >> 16);
+  uint32_t a, b;
+  q8_half4(w, a, b);
   const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&a));
   const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&b));
   v[0] = x.x; v[1] = x.y; v[2] = y.x; v[3] = y.y;

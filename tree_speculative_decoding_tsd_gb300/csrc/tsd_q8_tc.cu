@@ -25,10 +25,10 @@
 // straight from global memory into registers, one tile ahead (32 KB per SM in
 // flight), behind L2 prefetches of the tiles after it.
 //
-// Roles (800 threads): warps 0-15 softmax and epilogue (as in tsd_verify_tc.cu:
-// warpgroup w/4 owns a quarter of the columns, warp w%4 the TMEM lanes
-// 32(w%4)..+31, i.e. 32 keys of a tile or 32 dims of O^T); warp 16 owns the
-// tensor memory and issues the products; warps 17-24 widen K and V tiles into
+// Roles: WG warpgroups of softmax and epilogue (as in tsd_verify_tc.cu:
+// warpgroup w/4 owns N / WG of the columns, warp w%4 the TMEM lanes
+// 32(w%4)..+31, i.e. 32 keys of a tile or 32 dims of O^T); one warp owns the
+// tensor memory and issues the products; WW warps widen K and V tiles into
 // two stages each, laid out as the products read them (rows of 64 elements,
 // 128-byte swizzle).  P^T has two buffers.  mbarriers order widening -> S^T ->
 // softmax -> O^T; every wait is bounded as in the bf16 path.
@@ -48,10 +48,6 @@ namespace tsd {
 namespace {
 
 constexpr int kKeys = 128;
-constexpr int kSoftWarps = 16, kWideWarps = 8;
-constexpr int kMmaWarp = kSoftWarps, kWideWarp0 = kSoftWarps + 1;
-constexpr int kThreads = (kSoftWarps + 1 + kWideWarps) * 32;
-constexpr int kWideThreads = kWideWarps * 32;
 constexpr uint32_t kHalf = kKeys * 128;         // [128 rows][64 fp16]: 16 KB
 constexpr uint32_t kTile = 2 * kHalf;           // a widened K or V tile
 constexpr float kOverflow = 8.0f;               // log2 headroom of the lazy maximum
@@ -59,26 +55,33 @@ constexpr int kHeadroom = 7;                    // P^T's offset: 2^8 * 2^7 < 655
 constexpr int kMaxTiles = 256;                  // prefix tiles of a split
 constexpr int kPrefetch = 3;                    // tiles that the L2 prefetch runs ahead
 
-template <int N>
+// N packed rows, WG softmax warpgroups, WW widening warps.
+template <int N, int WG, int WW>
 struct Q8Layout {
+  static constexpr int soft_warps = 4 * WG;
+  static constexpr int threads = (soft_warps + 1 + WW) * 32;
   static constexpr uint32_t pt_bytes = 256u * N;                 // 128 keys x N fp16
   static constexpr uint32_t off_k = 0;
   static constexpr uint32_t off_v = 2 * kTile;
   static constexpr uint32_t off_p = 4 * kTile;
   static constexpr uint32_t off_q = off_p + 2 * pt_bytes;        // 2 x [N][64] fp16
   static constexpr uint32_t off_misc = off_q + 256u * N;
-  static constexpr int NH = N / 4;                // columns per warpgroup
-  static constexpr int NO = N / 32;               // column octets per warpgroup
-  static constexpr bool HQ = (N / 16) & 1;        // plus one quad
+  static constexpr int NH = N / WG;               // columns per warpgroup
+  static constexpr int NO = NH / 8;               // column octets per warpgroup
+  static constexpr bool HQ = NH % 8 != 0;         // plus one quad
   static constexpr int NU = NO + (HQ ? 1 : 0);
-  static constexpr int U0 = NO / 2;               // units of the first half
+  // columns are taken in two halves where one would need too many registers
+  static constexpr int U0 = NH > 24 ? NU / 2 : 0; // units of the first half
+  static constexpr int V0 = 8 * U0, V1 = NH - V0;
+  static constexpr int VMAX = V0 > V1 ? V0 : V1;
+  static_assert(NH % 4 == 0, "columns per warpgroup");
   static constexpr uint32_t off_m = off_misc;                          // float[N] running max
   static constexpr uint32_t off_alpha = off_m + 4 * N;                 // float[N]
   static constexpr uint32_t off_negm = off_alpha + 4 * N;              // float[N] -m (0 if -inf)
   static constexpr uint32_t off_shift = off_negm + 4 * N;              // float[N]
   static constexpr uint32_t off_c2 = off_shift + 4 * N;                // float[N] column scales
-  static constexpr uint32_t off_red = off_c2 + 4 * N;                  // float[16][NH]
-  static constexpr uint32_t off_rmask = off_red + 4 * kSoftWarps * NH; // u64[N]
+  static constexpr uint32_t off_red = off_c2 + 4 * N;                  // float[4 WG][NH]
+  static constexpr uint32_t off_rmask = off_red + 4 * soft_warps * NH; // u64[N]
   static constexpr uint32_t off_ooff = off_rmask + 8 * N;              // i64[N]
   static constexpr uint32_t off_rows = off_ooff + 8 * N;               // i64[kMaxTiles]
   static constexpr uint32_t off_tree = off_rows + 8 * kMaxTiles;       // 4 x 32 bits [128]
@@ -90,7 +93,7 @@ struct Q8Layout {
   static constexpr uint32_t total = off_flags + 16;
   static_assert(total + 1024 <= 232448, "shared memory budget");
   __device__ static int col(int lc, int wg) {
-    return lc < 8 * NO ? 32 * (lc >> 3) + 8 * wg + (lc & 7) : 32 * NO + 4 * wg + (lc - 8 * NO);
+    return lc < 8 * NO ? 8 * (WG * (lc >> 3) + wg) + (lc & 7) : 8 * WG * NO + 4 * wg + (lc - 8 * NO);
   }
 };
 
@@ -134,13 +137,16 @@ __device__ __forceinline__ uint4 scale8(const uint4& w, float f) {
 // the scale and its inverse are normal numbers.
 __device__ __forceinline__ int row_exponent(uint32_t top) { return max((int)(top >> 23), 15); }
 
-template <int N, int D>
-__global__ void __launch_bounds__(kThreads, 1)
+template <int N, int D, int WG, int WW>
+__global__ void __launch_bounds__(Q8Layout<N, WG, WW>::threads, 1)
 q8_tc_kernel(const __grid_constant__ Q8AttnArgs a) {
-  using L = Q8Layout<N>;
-  constexpr int NH = L::NH, NO = L::NO, NU = L::NU, U0 = L::U0;
+  using L = Q8Layout<N, WG, WW>;
+  constexpr int kSoftWarps = L::soft_warps, kWideWarps = WW, kWideThreads = 32 * WW;
+  constexpr int kMmaWarp = kSoftWarps, kWideWarp0 = kSoftWarps + 1;
+  constexpr int NH = L::NH, NO = L::NO, NU = L::NU, U0 = L::U0, VMAX = L::VMAX;
   constexpr int CH = D / 16;                     // 16-code chunks of a row
-  constexpr int NT = kKeys * CH / kWideThreads;  // chunks of a tile per widening thread
+  constexpr int kChunks = kKeys * CH;
+  constexpr int NT = (kChunks + kWideThreads - 1) / kWideThreads;  // of a tile, per widening thread
   grid_dependency_sync();
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   const uint32_t raw = su32(smem_raw);
@@ -220,6 +226,7 @@ q8_tc_kernel(const __grid_constant__ Q8AttnArgs a) {
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
       r[i] = make_uint4(0u, 0u, 0u, 0u);
+      // (the last round may be short; a row past the tile is never valid)
       if (row >= 0 && chunk_row(i) < nvalid)
         r[i] = ld_stream(base + (row + chunk_row(i)) * D + chunk_col(i) * 16);
     }
@@ -370,14 +377,12 @@ q8_tc_kernel(const __grid_constant__ Q8AttnArgs a) {
     auto widen = [&](const uint4 (&r)[NT], uint32_t stage) {
 #pragma unroll
       for (int i = 0; i < NT; ++i) {
+        if (kChunks % kWideThreads != 0 && wt + kWideThreads * i >= kChunks) break;
         const int row = chunk_row(i), c = chunk_col(i);
         const uint32_t w[4] = {r[i].x, r[i].y, r[i].z, r[i].w};
         uint32_t h[8];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          h[2 * j] = q8_half2(w[j]);
-          h[2 * j + 1] = q8_half2(w[j] >> 16);
-        }
+        for (int j = 0; j < 4; ++j) q8_half4(w[j], h[2 * j], h[2 * j + 1]);
         uint8_t* dst = smem + stage + (c >> 2) * kHalf + row * 128;
         const int u = 2 * (c & 3);
         *(uint4*)(dst + (((u + 0) ^ (row & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
@@ -479,10 +484,10 @@ q8_tc_kernel(const __grid_constant__ Q8AttnArgs a) {
     const int wg = warp >> 2, q = warp & 3;
     const int key = q * 32 + lane;
     const uint32_t lane_off = (uint32_t)(q * 32) << 16;
+    const int c_oct = 8 * wg, c_quad = 8 * WG * NO + 4 * wg;
     const uint32_t pt_oct = (uint32_t)key * 16u + (uint32_t)wg * 2048u;
     const uint32_t pt_quad =
-        (uint32_t)key * 16u + (4u * NO + (uint32_t)(wg >> 1)) * 2048u + (uint32_t)(wg & 1) * 8u;
-    const int c_oct = 8 * wg, c_quad = 32 * NO + 4 * wg;
+        (uint32_t)key * 16u + (uint32_t)(c_quad >> 3) * 2048u + (uint32_t)(c_quad & 4) * 2u;
     float2 l2[NH / 2];
 #pragma unroll
     for (int i = 0; i < NH / 2; ++i) l2[i] = make_float2(0.f, 0.f);
@@ -511,7 +516,6 @@ q8_tc_kernel(const __grid_constant__ Q8AttnArgs a) {
       for (int h = 0; h < 2; ++h) {
         const int ua = h == 0 ? 0 : U0, ub = h == 0 ? U0 : NU;
         if (ua >= ub) continue;
-        constexpr int VMAX = 8 * (NO - NO / 2) + 4;
         const int lc0 = 8 * ua;
         const int ncol = (ub == NU && L::HQ) ? 8 * (ub - 1 - ua) + 4 : 8 * (ub - ua);
         // x = S^T * scale - m, and the largest x
@@ -520,7 +524,7 @@ q8_tc_kernel(const __grid_constant__ Q8AttnArgs a) {
 #pragma unroll
           for (int u = ua; u < ub; ++u) {
             float* x = v + 8 * (u - ua);
-            if (u < NO) tmem_ld8(srow + (uint32_t)(32 * u + c_oct), x);
+            if (u < NO) tmem_ld8(srow + (uint32_t)(8 * WG * u + c_oct), x);
             else tmem_ld4(srow + (uint32_t)c_quad, x[0], x[1], x[2], x[3]);
           }
           tmem_wait_ld();
@@ -529,7 +533,7 @@ q8_tc_kernel(const __grid_constant__ Q8AttnArgs a) {
         for (int u = ua; u < ub; ++u) {
           float* x = v + 8 * (u - ua);
           const int nq = u < NO ? 2 : 1;
-          const int c = u < NO ? 32 * u + c_oct : c_quad;
+          const int c = u < NO ? 8 * WG * u + c_oct : c_quad;
 #pragma unroll
           for (int j = 0; j < nq; ++j) {
             const float4 nm = *(const float4*)(negm + c + 4 * j);
@@ -610,7 +614,7 @@ q8_tc_kernel(const __grid_constant__ Q8AttnArgs a) {
           for (int u = ua; u < ub; ++u) {
             float* x = v + 8 * (u - ua);
             const int nq = u < NO ? 2 : 1;
-            const int c = u < NO ? 32 * u + c_oct : c_quad;
+            const int c = u < NO ? 8 * WG * u + c_oct : c_quad;
             const int li = u < NO ? 4 * u : 4 * NO;
 #pragma unroll
             for (int j = 0; j < nq; ++j) {
@@ -662,7 +666,7 @@ q8_tc_kernel(const __grid_constant__ Q8AttnArgs a) {
             w[i] = pack_half2(pv.x, pv.y);
           }
           if (!failed) {
-            if (u < NO) *(uint4*)(pt + pt_oct + 8192u * u) = make_uint4(w[0], w[1], w[2], w[3]);
+            if (u < NO) *(uint4*)(pt + pt_oct + 2048u * WG * u) = make_uint4(w[0], w[1], w[2], w[3]);
             else *(uint2*)(pt + pt_quad) = make_uint2(w[0], w[1]);
           }
         }
@@ -719,7 +723,7 @@ q8_tc_kernel(const __grid_constant__ Q8AttnArgs a) {
 #pragma unroll
       for (int u = 0; u < NU; ++u) {
         float o[8];
-        const int c = u < NO ? 32 * u + c_oct : c_quad;
+        const int c = u < NO ? 8 * WG * u + c_oct : c_quad;
         if (u < NO) tmem_ld8(tm_o + lane_off + (uint32_t)c, o);
         else tmem_ld4(tm_o + lane_off + (uint32_t)c, o[0], o[1], o[2], o[3]);
         tmem_wait_ld();
@@ -748,23 +752,25 @@ q8_tc_kernel(const __grid_constant__ Q8AttnArgs a) {
   }
 }
 
-template <int N, int D>
+template <int N, int D, int WG, int WW>
 void launch_n(const Q8AttnArgs& a, const Q8Plan& p, cudaStream_t st) {
-  const uint32_t smem = Q8Layout<N>::total + 1024;
-  cudaFuncSetAttribute(q8_tc_kernel<N, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  launch(q8_tc_kernel<N, D>, dim3(a.map.Hkv * p.nrg, p.nsplit, a.B), dim3(kThreads), smem, st, a);
+  using L = Q8Layout<N, WG, WW>;
+  const uint32_t smem = L::total + 1024;
+  const auto kern = q8_tc_kernel<N, D, WG, WW>;
+  cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  launch(kern, dim3(a.map.Hkv * p.nrg, p.nsplit, a.B), dim3(L::threads), smem, st, a);
 }
 
 template <int D>
 bool launch_d(const Q8AttnArgs& a, const Q8Plan& p, cudaStream_t st) {
   switch (p.rb) {
-    case 16: launch_n<16, D>(a, p, st); return true;
-    case 32: launch_n<32, D>(a, p, st); return true;
-    case 48: launch_n<48, D>(a, p, st); return true;
-    case 64: launch_n<64, D>(a, p, st); return true;
-    case 80: launch_n<80, D>(a, p, st); return true;
-    case 96: launch_n<96, D>(a, p, st); return true;
-    case 112: launch_n<112, D>(a, p, st); return true;
+    case 16: launch_n<16, D, 1, 8>(a, p, st); return true;
+    case 32: launch_n<32, D, 1, 8>(a, p, st); return true;
+    case 48: launch_n<48, D, 2, 8>(a, p, st); return true;
+    case 64: launch_n<64, D, 2, 8>(a, p, st); return true;
+    case 80: launch_n<80, D, 4, 7>(a, p, st); return true;
+    case 96: launch_n<96, D, 4, 7>(a, p, st); return true;
+    case 112: launch_n<112, D, 4, 7>(a, p, st); return true;
   }
   return false;
 }
