@@ -6,32 +6,37 @@
 //   O^T[dim][n] += V_tile^T . P^T   M = 128 dims, N = packed rows, K = 128 keys
 // with fp32 accumulators in tensor memory (S^T twice, O^T once).
 //
-// Numbers.  Every operand is fp16, and only P is rounded to it:
-//   K, V   an e4m3 code is an fp16 number; the block's power of two is left out
-//          of the product and applied to the score (K) or to the probability (V)
-//   Q      bf16 row times a power of two that puts its largest element into
-//          [2^14, 2^15): exact down to 2^-39 of that element
-//   tree   scratch rows likewise, K and V each, largest element in [2^8, 2^9)
-//   P      p * 2^(u - U + 7), u the exponent of the key's value row and U the
-//          largest u of the CTA's keys: rounded to 11 bits (2^-12), p below
-//          2^-32 (at the largest scale) to multiples of 2^-32.  The row sums take p before it
-//          is rounded.
-// A score is x = (S^T * (scale log2(e) 2^q_n)) * 2^k_key - m_n, in fp32.
+// Numbers.
+//   S^T    kind::f8f6f4: the K tile's codes as they are in the cache, and Q as
+//          the sum of two e4m3 numbers.  A bf16 row is first multiplied by the
+//          power of two that puts its largest element into [128, 256); hi =
+//          e4m3(x), lo = e4m3(x - hi).  x has 8 significant bits, hi 4, so
+//          x - hi needs 4: hi + lo = x, except where lo falls below e4m3's
+//          smallest step (elements below 2^-9 of the largest; off by at most
+//          2^-10, 2^-17 of the largest).  The block's power of two (K) and the
+//          row's (Q) are applied to the score in fp32.
+//   tree   scratch rows of K likewise as hi + lo (four products)
+//   V      fp16: a code is an fp16 number; scratch rows are scaled (largest
+//          element into [2^8, 2^9): exact down to 2^-33 of it)
+//   P      fp16: p * 2^(u - U + 7), u the exponent of the key's value row and U
+//          the largest u of the CTA's keys: rounded to 11 bits (2^-12), p below
+//          2^-32 (at the largest scale) to multiples of 2^-32.  The row sums
+//          take p before it is rounded.
+// A score is x = S^T * (2^k_key * scale log2(e) 2^q_n) - m_n, in fp32.
 //
-// Why the codes are widened by warps and not by the tensor core: kind::f8f6f4
-// would need P in 8 bits (4 significant ones), an error of 2^-4 per
-// probability.  Widening costs a tile 2 x 128 x d / 2 conversions, and the
-// 16-bit tiles need shared memory that no copy has to fill: the 8-bit rows come
-// straight from global memory into registers, one tile ahead (32 KB per SM in
-// flight), behind L2 prefetches of the tiles after it.
+// Why V is widened by warps and not taken in 8 bits: kind::f8f6f4 would need P
+// in 8 bits.  Two e4m3 terms as for Q do not do: P spans 2^-32..2^8, and what
+// lies below 2^-17 of the largest would be lost from long flat rows.
 //
 // Roles: WG warpgroups of softmax and epilogue (as in tsd_verify_tc.cu:
 // warpgroup w/4 owns N / WG of the columns, warp w%4 the TMEM lanes
 // 32(w%4)..+31, i.e. 32 keys of a tile or 32 dims of O^T); one warp owns the
-// tensor memory and issues the products; WW warps widen K and V tiles into
-// two stages each, laid out as the products read them (rows of 64 elements,
-// 128-byte swizzle).  P^T has two buffers.  mbarriers order widening -> S^T ->
-// softmax -> O^T; every wait is bounded as in the bf16 path.
+// tensor memory and issues the products; one thread loads K tiles by TMA into a
+// ring of four; WW warps load V tiles straight into registers, VD tiles ahead
+// (behind L2 prefetches), and widen them into two fp16 stages, laid out as the
+// product reads them (rows of 64 elements, 128-byte swizzle).  P^T has two
+// buffers.  mbarriers order K -> S^T -> softmax -> O^T and V -> O^T; every wait
+// is bounded as in the bf16 path.
 //
 // Softmax with keys on lanes: the running maximum of a column is lazy.  While
 // no x of a tile exceeds 8, the tile keeps the old maximum (p <= 256); else, and
@@ -49,23 +54,26 @@ namespace {
 
 constexpr int kKeys = 128;
 constexpr uint32_t kHalf = kKeys * 128;         // [128 rows][64 fp16]: 16 KB
-constexpr uint32_t kTile = 2 * kHalf;           // a widened K or V tile
+constexpr uint32_t kTile = 2 * kHalf;           // a widened V tile
+constexpr int kRing = 4;                        // K tiles
 constexpr float kOverflow = 8.0f;               // log2 headroom of the lazy maximum
 constexpr int kHeadroom = 7;                    // P^T's offset: 2^8 * 2^7 < 65504
 constexpr int kMaxTiles = 256;                  // prefix tiles of a split
-constexpr int kPrefetch = 3;                    // tiles that the L2 prefetch runs ahead
+constexpr int kPrefetch = 4;                    // tiles that V's L2 prefetch runs ahead
 
-// N packed rows, WG softmax warpgroups, WW widening warps.
-template <int N, int WG, int WW>
+// N packed rows of D dims, WG softmax warpgroups, WW widening warps.
+template <int N, int D, int WG, int WW>
 struct Q8Layout {
   static constexpr int soft_warps = 4 * WG;
-  static constexpr int threads = (soft_warps + 1 + WW) * 32;
+  static constexpr int threads = (soft_warps + 2 + WW) * 32;
+  static constexpr uint32_t k_bytes = kKeys * D;                 // a K tile: [128 keys][D] codes
+  static constexpr uint32_t q_bytes = N * D;                     // hi or lo of Q
   static constexpr uint32_t pt_bytes = 256u * N;                 // 128 keys x N fp16
   static constexpr uint32_t off_k = 0;
-  static constexpr uint32_t off_v = 2 * kTile;
-  static constexpr uint32_t off_p = 4 * kTile;
-  static constexpr uint32_t off_q = off_p + 2 * pt_bytes;        // 2 x [N][64] fp16
-  static constexpr uint32_t off_misc = off_q + 256u * N;
+  static constexpr uint32_t off_v = kRing * k_bytes;
+  static constexpr uint32_t off_p = off_v + 2 * kTile;
+  static constexpr uint32_t off_q = off_p + 2 * pt_bytes;        // hi, lo: [N][D] e4m3
+  static constexpr uint32_t off_misc = off_q + 2 * q_bytes;
   static constexpr int NH = N / WG;               // columns per warpgroup
   static constexpr int NO = NH / 8;               // column octets per warpgroup
   static constexpr bool HQ = NH % 8 != 0;         // plus one quad
@@ -88,7 +96,7 @@ struct Q8Layout {
   static constexpr uint32_t off_kex = off_tree + 16 * kKeys;           // u8[2 kMaxTiles]
   static constexpr uint32_t off_vex = off_kex + 2 * kMaxTiles;
   static constexpr uint32_t off_bar = off_vex + 2 * kMaxTiles;
-  static constexpr int nbar = 14;
+  static constexpr int nbar = 19;
   static constexpr uint32_t off_flags = off_bar + 8 * nbar;            // tmem, abort, U
   static constexpr uint32_t total = off_flags + 16;
   static_assert(total + 1024 <= 232448, "shared memory budget");
@@ -97,10 +105,52 @@ struct Q8Layout {
   }
 };
 
-// FULL: widened by the 8 warps; EMPTY: read by the product (V_EMPTY is also the
-// end of a tile's O^T product).
-enum { BAR_K_FULL = 0, BAR_K_EMPTY = 2, BAR_V_FULL = 4, BAR_V_EMPTY = 6, BAR_S_FULL = 8,
-       BAR_P_FULL = 10, BAR_FINAL = 12, BAR_O_DONE = 13 };
+// FULL: the copy landed or the warps wrote; EMPTY: read by the product (V_EMPTY
+// is also the end of a tile's O^T product); T_FULL: the scratch rows' keys, which
+// take the two K slots behind the last prefix tile (hi, lo).
+enum { BAR_K_FULL = 0, BAR_K_EMPTY = 4, BAR_V_FULL = 8, BAR_V_EMPTY = 10, BAR_S_FULL = 12,
+       BAR_P_FULL = 14, BAR_FINAL = 16, BAR_O_DONE = 17, BAR_T_FULL = 18 };
+
+// D (+)= A.B, 8-bit operands (e4m3), K = 32 per instruction.
+__device__ __forceinline__ void mma_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                       uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(acc));
+}
+
+// Byte offset of 16-byte unit u of row r in a K-major tile of D-byte rows
+// (128-byte swizzle for D = 128, 64-byte swizzle for D = 64), and the matrix
+// descriptor of such a tile.
+template <int D>
+__device__ __forceinline__ uint32_t unit_offset(int r, int u) {
+  return D == 128 ? r * 128 + ((u ^ (r & 7)) << 4) : r * 64 + ((u ^ ((r >> 1) & 3)) << 4);
+}
+template <int D>
+__device__ __forceinline__ uint64_t row_desc(uint32_t addr) {
+  if (D == 128) return smem_desc(addr, 16, 1024);
+  return (uint64_t)((addr >> 4) & 0x3FFF) | ((uint64_t)1 << 16) | ((uint64_t)(512 >> 4) << 32) |
+         (1ull << 46) | (4ull << 61);
+}
+
+// Sixteen bf16 times f as e4m3 numbers hi and lo with hi + lo = x f.
+__device__ __forceinline__ void split16(const uint4 (&w)[2], float f, uint4& hi, uint4& lo) {
+  uint32_t h[4], l[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint4& s = w[i >> 1];
+    const uint32_t a = (i & 1) ? s.z : s.x, b = (i & 1) ? s.w : s.y;
+    const float x[4] = {__uint_as_float(a << 16) * f, __uint_as_float(a & 0xffff0000u) * f,
+                        __uint_as_float(b << 16) * f, __uint_as_float(b & 0xffff0000u) * f};
+    float y[4];
+    h[i] = q8_pack4(x[0], x[1], x[2], x[3]);
+    q8_unpack4(h[i], y);
+    l[i] = q8_pack4(x[0] - y[0], x[1] - y[1], x[2] - y[2], x[3] - y[3]);
+  }
+  hi = make_uint4(h[0], h[1], h[2], h[3]);
+  lo = make_uint4(l[0], l[1], l[2], l[3]);
+}
 
 __device__ __forceinline__ uint4 ld_stream(const uint8_t* p) {
   uint4 v;
@@ -137,16 +187,17 @@ __device__ __forceinline__ uint4 scale8(const uint4& w, float f) {
 // the scale and its inverse are normal numbers.
 __device__ __forceinline__ int row_exponent(uint32_t top) { return max((int)(top >> 23), 15); }
 
-template <int N, int D, int WG, int WW>
-__global__ void __launch_bounds__(Q8Layout<N, WG, WW>::threads, 1)
-q8_tc_kernel(const __grid_constant__ Q8AttnArgs a) {
-  using L = Q8Layout<N, WG, WW>;
+template <int N, int D, int WG, int WW, int VD>
+__global__ void __launch_bounds__(Q8Layout<N, D, WG, WW>::threads, 1)
+q8_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ Q8AttnArgs a) {
+  using L = Q8Layout<N, D, WG, WW>;
   constexpr int kSoftWarps = L::soft_warps, kWideWarps = WW, kWideThreads = 32 * WW;
-  constexpr int kMmaWarp = kSoftWarps, kWideWarp0 = kSoftWarps + 1;
+  constexpr int kMmaWarp = kSoftWarps, kTmaWarp = kSoftWarps + 1, kWideWarp0 = kSoftWarps + 2;
   constexpr int NH = L::NH, NO = L::NO, NU = L::NU, U0 = L::U0, VMAX = L::VMAX;
   constexpr int CH = D / 16;                     // 16-code chunks of a row
   constexpr int kChunks = kKeys * CH;
   constexpr int NT = (kChunks + kWideThreads - 1) / kWideThreads;  // of a tile, per widening thread
+  if (threadIdx.x == kTmaWarp * 32) tma_desc_prefetch(&kmap);
   grid_dependency_sync();
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   const uint32_t raw = su32(smem_raw);
@@ -186,9 +237,11 @@ q8_tc_kernel(const __grid_constant__ Q8AttnArgs a) {
 
   // ---------------------------------------------------------------- set-up
   if (tid == kMmaWarp * 32) {
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(bar(BAR_K_FULL + i), kWideWarps);
+    for (int i = 0; i < kRing; ++i) {
+      mbar_init(bar(BAR_K_FULL + i), 1);
       mbar_init(bar(BAR_K_EMPTY + i), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
       mbar_init(bar(BAR_V_FULL + i), kWideWarps);
       mbar_init(bar(BAR_V_EMPTY + i), 1);
       mbar_init(bar(BAR_S_FULL + i), 1);
@@ -196,6 +249,7 @@ q8_tc_kernel(const __grid_constant__ Q8AttnArgs a) {
     }
     mbar_init(bar(BAR_FINAL), 1);
     mbar_init(bar(BAR_O_DONE), 1);
+    mbar_init(bar(BAR_T_FULL), kWideWarps);
     flags[1] = 0;
     *s_top = -1000;
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
@@ -221,25 +275,23 @@ q8_tc_kernel(const __grid_constant__ Q8AttnArgs a) {
     const int x = wt + kWideThreads * i;
     return D == 128 ? (x & 3) + 4 * ((x >> 3) & 1) : x & 3;
   };
-  uint4 kreg[NT], vreg[NT];
-  auto load_tile = [&](uint4 (&r)[NT], const uint8_t* base, long row, int nvalid) {
+  uint4 vreg[VD][NT];
+  auto load_v = [&](uint4 (&r)[NT], long row, int nvalid) {
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
       r[i] = make_uint4(0u, 0u, 0u, 0u);
       // (the last round may be short; a row past the tile is never valid)
       if (row >= 0 && chunk_row(i) < nvalid)
-        r[i] = ld_stream(base + (row + chunk_row(i)) * D + chunk_col(i) * 16);
+        r[i] = ld_stream(a.vc + (row + chunk_row(i)) * D + chunk_col(i) * 16);
     }
   };
   auto valid_of = [&](int t) { return min(kKeys, k1 - (k0 + t * kKeys)); };
 
   if (warp >= kWideWarp0) {
     // the first tile's loads go out before anything else
-    if (n_pre > 0) {
-      const long r0 = a.map.row(b, hk, k0);
-      load_tile(kreg, a.kc, r0, valid_of(0));
-      load_tile(vreg, a.vc, r0, valid_of(0));
-    }
+#pragma unroll
+    for (int i = 0; i < VD; ++i)
+      if (i < n_pre) load_v(vreg[i], a.map.row(b, hk, k0 + i * kKeys), valid_of(i));
     int top = -1000;
     for (int t = wt; t < n_pre; t += kWideThreads) {
       const int pos = k0 + t * kKeys;
@@ -292,10 +344,10 @@ q8_tc_kernel(const __grid_constant__ Q8AttnArgs a) {
         bad = (any >> (lane & 24)) & 0xffu;
         const int ek = row_exponent(kt), ev = row_exponent(vt);
         if (c == 0) {
-          // f = 2^(8 - (e - 127)), 1 / f = 2^(e - 127 - 8)
-          kt_in[j] = live && !bad ? q8_scale(262 - ek) : 0.f;
+          // K: 2^(7 - (e - 127)) and its inverse; V: 2^(8 - (e - 127))
+          kt_in[j] = live && !bad ? q8_scale(261 - ek) : 0.f;
           vt_in[j] = live && !bad ? q8_scale(262 - ev) : 0.f;
-          kt_out[j] = bad ? __int_as_float(0x7fffffff) : q8_scale(ek - 8);
+          kt_out[j] = bad ? __int_as_float(0x7fffffff) : q8_scale(ek - 7);
           vt_u[j] = live ? ev - 135 : -1000;
         }
         if (live) top = max(top, ev - 135);
@@ -310,10 +362,11 @@ q8_tc_kernel(const __grid_constant__ Q8AttnArgs a) {
       asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
     }
   } else if (warp < kSoftWarps) {
-    // Q^T as fp16, rows scaled (K-major, 128-byte swizzle): eight lanes per row
-    for (int x = tid; x < N * 8; x += kSoftWarps * 32) {
-      const int n = x >> 3, c = x & 7;
-      uint4 w[D / 64];
+    // Q as hi + lo, rows scaled: eight lanes per row (D = 64: four), 16 elements each
+    constexpr int QL = D / 16;
+    for (int x = tid; x < N * QL; x += kSoftWarps * 32) {
+      const int n = x / QL, c = x % QL;
+      uint4 w[2] = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
       uint32_t top = 0;
       bool bad = false;
       if (n < rows_here) {
@@ -321,30 +374,24 @@ q8_tc_kernel(const __grid_constant__ Q8AttnArgs a) {
         const int tr = p / a.g, qh = hk * a.g + p % a.g;
         const uint4* qp =
             (const uint4*)((const __nv_bfloat16*)a.q + (((long)b * a.R + tr) * a.Hq + qh) * D) +
-            c * (D / 64);
+            2 * c;
 #pragma unroll
-        for (int i = 0; i < D / 64; ++i) {
+        for (int i = 0; i < 2; ++i) {
           w[i] = __ldg(qp + i);
           scan8(w[i], top, bad);
         }
-      } else {
-#pragma unroll
-        for (int i = 0; i < D / 64; ++i) w[i] = make_uint4(0u, 0u, 0u, 0u);
       }
+      // (N * QL is a multiple of 32: whole warps take part)
 #pragma unroll
-      for (int o = 4; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(kFull, top, o));
+      for (int o = QL / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(kFull, top, o));
       const uint32_t any = __ballot_sync(kFull, bad);
-      bad = (any >> (lane & 24)) & 0xffu;
+      bad = (any >> (lane & (32 - QL))) & ((1u << QL) - 1u);
       const int e = row_exponent(top);
-      const float f = bad ? 0.f : q8_scale(268 - e);       // 2^(14 - (e - 127))
-#pragma unroll
-      for (int i = 0; i < D / 64; ++i) {
-        const int u = c * (D / 64) + i;                    // 8-element unit of the row
-        const uint4 v = bad ? make_uint4(0u, 0u, 0u, 0u) : scale8(w[i], f);
-        *(uint4*)(smem + L::off_q + (u >> 3) * (N * 128u) + n * 128u +
-                  (((u & 7) ^ (n & 7)) << 4)) = v;
-      }
-      if (c == 0) c2v[n] = bad ? __int_as_float(0x7fffffff) : a.qscale * q8_scale(e - 14);
+      uint4 hi = make_uint4(0u, 0u, 0u, 0u), lo = hi;
+      if (!bad) split16(w, q8_scale(261 - e), hi, lo);
+      *(uint4*)(smem + L::off_q + unit_offset<D>(n, c)) = hi;
+      *(uint4*)(smem + L::off_q + L::q_bytes + unit_offset<D>(n, c)) = lo;
+      if (c == 0) c2v[n] = bad ? __int_as_float(0x7fffffff) : a.qscale * q8_scale(e - 7);
     }
     for (int n = tid; n < N; n += kSoftWarps * 32) {
       uint64_t mk = 0ull;
@@ -366,14 +413,44 @@ q8_tc_kernel(const __grid_constant__ Q8AttnArgs a) {
   auto tm_s = [&](int i) { return tmem + (uint32_t)(i * N); };
   const uint32_t tm_o = tmem + 2u * N;
 
-  // -------------------------------------------------------------- widening
-  if (warp >= kWideWarp0) {
-    auto prefetch = [&](int t) {
-      if (t < n_pre && tile_row[t] >= 0) {
-        if (wt == 0) prefetch_l2(a.kc + tile_row[t] * D, (long)valid_of(t) * D);
-        if (wt == 32) prefetch_l2(a.vc + tile_row[t] * D, (long)valid_of(t) * D);
+  // -------------------------------------------------------------- K tiles
+  if (warp == kTmaWarp) {
+    if (lane == 0) {
+      int loaded = 0;
+      for (int t = 0; t < n_pre && !flags[1]; ++t) {
+        const int sl = t % kRing;
+        if (t >= kRing && !mbar_wait(bar(BAR_K_EMPTY + sl), (t / kRing - 1) & 1)) {
+          flags[1] = 1;
+          break;
+        }
+        // (a tile behind the cache's or page's last row reads zeros there; rows
+        // behind the prefix are masked later, whatever they hold; the rows of a
+        // missing page are those of page 0)
+        const int pos = k0 + t * kKeys;
+        int y = pos, z = b * a.map.Hkv + hk;
+        if (a.map.page_size) {
+          const long r = tile_row[t] < 0 ? 0 : tile_row[t];
+          y = (int)(r % a.map.page_size);
+          z = (int)(r / a.map.page_size);
+        }
+        mbar_expect_tx(bar(BAR_K_FULL + sl), L::k_bytes);
+        tma_3d(sbase + L::off_k + sl * L::k_bytes, &kmap, 0, y, z, bar(BAR_K_FULL + sl));
+        ++loaded;
+        if (t == 0)
+          for (int i = VD; i < kPrefetch; ++i)
+            if (i < n_pre && tile_row[i] >= 0) prefetch_l2(a.vc + tile_row[i] * D, (long)valid_of(i) * D);
+        const int i = t + kPrefetch;
+        if (i < n_pre && tile_row[i] >= 0) prefetch_l2(a.vc + tile_row[i] * D, (long)valid_of(i) * D);
       }
-    };
+      // no copy may be in flight when the CTA leaves
+      for (int sl = 0; sl < kRing && sl < loaded; ++sl)
+        mbar_wait(bar(BAR_K_FULL + sl), ((loaded - 1 - sl) / kRing) & 1);
+    }
+    __syncwarp();
+  }
+
+  // -------------------------------------------------------------- widening
+  else if (warp >= kWideWarp0) {
     auto widen = [&](const uint4 (&r)[NT], uint32_t stage) {
 #pragma unroll
       for (int i = 0; i < NT; ++i) {
@@ -390,65 +467,104 @@ q8_tc_kernel(const __grid_constant__ Q8AttnArgs a) {
       }
     };
     // the scratch rows of this head, scaled; rows that nobody sees are zeros
-    auto widen_tree = [&](const void* src, const float* in, uint32_t stage) {
+    auto tree_keys = [&](int s_hi, int s_lo) {
+      for (int x = wt; x < kKeys * (D / 16); x += kWideThreads) {
+        const int row = x / (D / 16), u = x % (D / 16);
+        uint4 hi = make_uint4(0u, 0u, 0u, 0u), lo = hi;
+        const float f = kt_in[row];
+        if (f != 0.f) {
+          const uint4* p = (const uint4*)((const __nv_bfloat16*)a.kt +
+                                          (((long)b * a.R + row) * a.map.Hkv + hk) * D) + 2 * u;
+          const uint4 w[2] = {__ldg(p), __ldg(p + 1)};
+          split16(w, f, hi, lo);
+        }
+        *(uint4*)(smem + L::off_k + s_hi * L::k_bytes + unit_offset<D>(row, u)) = hi;
+        *(uint4*)(smem + L::off_k + s_lo * L::k_bytes + unit_offset<D>(row, u)) = lo;
+      }
+      asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(BAR_T_FULL));
+    };
+    auto tree_values = [&](uint32_t stage) {
       for (int x = wt; x < kKeys * (D / 8); x += kWideThreads) {
         const int row = x / (D / 8), u = x % (D / 8);
-        const float f = in[row];
+        const float f = vt_in[row];
         uint4 v = make_uint4(0u, 0u, 0u, 0u);
         if (f != 0.f)
-          v = scale8(__ldg((const uint4*)((const __nv_bfloat16*)src +
+          v = scale8(__ldg((const uint4*)((const __nv_bfloat16*)a.vt +
                                           (((long)b * a.R + row) * a.map.Hkv + hk) * D) + u), f);
         *(uint4*)(smem + stage + (u >> 3) * kHalf + row * 128 + (((u & 7) ^ (row & 7)) << 4)) = v;
       }
     };
-    auto done = [&](int which) {
-      asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(which));
-    };
-    for (int t = 1; t < kPrefetch; ++t) prefetch(t);
-    for (int t = 0; t < ntiles; ++t) {
-      const int st = t & 1;
-      const uint32_t par = ((t >> 1) - 1) & 1;
-      if (t >= 2 && !__all_sync(kFull, mbar_wait(bar(BAR_K_EMPTY + st), par))) { flags[1] = 1; break; }
-      if (t < n_pre) widen(kreg, L::off_k + st * kTile);
-      else widen_tree(a.kt, kt_in, L::off_k + st * kTile);
-      done(BAR_K_FULL + st);
-      prefetch(t + kPrefetch);
-      if (t + 1 < n_pre) load_tile(kreg, a.kc, tile_row[t + 1], valid_of(t + 1));
-      if (t >= 2 && !__all_sync(kFull, mbar_wait(bar(BAR_V_EMPTY + st), par))) { flags[1] = 1; break; }
-      if (t < n_pre) widen(vreg, L::off_v + st * kTile);
-      else widen_tree(a.vt, vt_in, L::off_v + st * kTile);
-      done(BAR_V_FULL + st);
-      if (t + 1 < n_pre) load_tile(vreg, a.vc, tile_row[t + 1], valid_of(t + 1));
-      if (flags[1]) break;
+    const int tree_at = max(n_pre - 2, 0);     // the tree's keys are made two tiles early
+    bool ok = true;
+    for (int t0 = 0; ok && t0 < ntiles; t0 += VD) {
+#pragma unroll
+      for (int i = 0; i < VD; ++i) {           // (constant register indexes)
+        const int t = t0 + i, st = t & 1;
+        if (t >= ntiles) break;
+        if (with_tree && t == tree_at) {
+          const int s0 = n_pre, s1 = n_pre + 1;
+          if ((s0 >= kRing && !__all_sync(kFull, mbar_wait(bar(BAR_K_EMPTY + s0 % kRing),
+                                                           (s0 / kRing - 1) & 1))) ||
+              (s1 >= kRing && !__all_sync(kFull, mbar_wait(bar(BAR_K_EMPTY + s1 % kRing),
+                                                           (s1 / kRing - 1) & 1)))) {
+            flags[1] = 1;
+            ok = false;
+            break;
+          }
+          tree_keys(s0 % kRing, s1 % kRing);
+        }
+        if (t >= 2 && !__all_sync(kFull, mbar_wait(bar(BAR_V_EMPTY + st), ((t >> 1) - 1) & 1))) {
+          flags[1] = 1;
+          ok = false;
+          break;
+        }
+        if (t < n_pre) widen(vreg[i], L::off_v + st * kTile);
+        else tree_values(L::off_v + st * kTile);
+        asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(BAR_V_FULL + st));
+        if (t + VD < n_pre) load_v(vreg[i], tile_row[t + VD], valid_of(t + VD));
+        if (__any_sync(kFull, flags[1] != 0)) {
+          ok = false;
+          break;
+        }
+      }
     }
   }
 
   // ------------------------------------------------------------------ MMA
   else if (warp == kMmaWarp) {
     if (lane == 0) {
-      // fp16 operands, fp32 accumulator
+      // fp32 accumulators; e4m3 (S^T) and fp16 (O^T) operands are both format 0
       const uint32_t idesc_qk = (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(kKeys >> 4) << 24);
       const uint32_t idesc_pv = idesc_qk | (1u << 15) | (1u << 16);
-      const uint64_t kd0 = smem_desc(sbase + L::off_k, 16, 1024);
+      const uint64_t kd0 = row_desc<D>(sbase + L::off_k);
+      const uint64_t qd0 = row_desc<D>(sbase + L::off_q);
       const uint64_t vd0 = smem_desc(sbase + L::off_v, kHalf, 1024);
-      const uint64_t qd0 = smem_desc(sbase + L::off_q, 16, 1024);
       // P^T: 8x8 cores, the key groups of 8 columns contiguous (tsd_verify_tc.cu)
       const uint64_t pd0 = smem_desc_interleave(sbase + L::off_p, 128, 2048);
-      auto issue_qk = [&](int t) -> bool {
-        const int st = t & 1;
-        if (!mbar_wait(bar(BAR_K_FULL + st), (t >> 1) & 1)) return false;
-        fence_after();
-        const uint64_t kd = kd0 + (uint64_t)(st * (kTile >> 4));
-        const uint32_t ts = tm_s(st);
-        mma_f16(ts, kd, qd0, idesc_qk, 0u);
+      // S^T (+)= K slot x (Q hi + Q lo)
+      auto products = [&](uint32_t ts, int sl, bool first) {
+        const uint64_t kd = kd0 + (uint64_t)(sl * (L::k_bytes >> 4));
 #pragma unroll
-        for (int kk = 1; kk < D / 16; ++kk)
-          mma_f16_acc(ts, kd + (((kk >> 2) * kHalf + (kk & 3) * 32) >> 4),
-                      qd0 + (((kk >> 2) * (N * 128u) + (kk & 3) * 32) >> 4), idesc_qk);
+        for (int part = 0; part < 2; ++part)
+#pragma unroll
+          for (int kk = 0; kk < D / 32; ++kk)
+            mma_f8(ts, kd + 2 * kk, qd0 + (uint64_t)(part * (L::q_bytes >> 4)) + 2 * kk, idesc_qk,
+                   first && part == 0 && kk == 0 ? 0u : 1u);
+      };
+      auto issue_qk = [&](int t) -> bool {
+        const int st = t & 1, sl = t % kRing;
+        if (!(t < n_pre ? mbar_wait(bar(BAR_K_FULL + sl), (t / kRing) & 1)
+                        : mbar_wait(bar(BAR_T_FULL), 0)))
+          return false;
+        fence_after();
+        products(tm_s(st), sl, true);
+        if (t >= n_pre) products(tm_s(st), (t + 1) % kRing, false);
         mma_commit(bar(BAR_S_FULL + st));
-        mma_commit(bar(BAR_K_EMPTY + st));
+        mma_commit(bar(BAR_K_EMPTY + sl));
         return true;
       };
       bool ok = issue_qk(0);
@@ -752,25 +868,46 @@ q8_tc_kernel(const __grid_constant__ Q8AttnArgs a) {
   }
 }
 
-template <int N, int D, int WG, int WW>
-void launch_n(const Q8AttnArgs& a, const Q8Plan& p, cudaStream_t st) {
-  using L = Q8Layout<N, WG, WW>;
+template <int N, int D, int WG, int WW, int VD>
+void launch_n(const CUtensorMap& kmap, const Q8AttnArgs& a, const Q8Plan& p, cudaStream_t st) {
+  using L = Q8Layout<N, D, WG, WW>;
   const uint32_t smem = L::total + 1024;
-  const auto kern = q8_tc_kernel<N, D, WG, WW>;
+  const auto kern = q8_tc_kernel<N, D, WG, WW, VD>;
   cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  launch(kern, dim3(a.map.Hkv * p.nrg, p.nsplit, a.B), dim3(L::threads), smem, st, a);
+  launch(kern, dim3(a.map.Hkv * p.nrg, p.nsplit, a.B), dim3(L::threads), smem, st, kmap, a);
 }
 
+// K codes as (dims, rows of a head, heads): rows are those of a request's head,
+// or of a page's.
+bool encode_keys(CUtensorMap* m, const Q8AttnArgs& a, int D) {
+  const long rows = a.map.page_size > 0 ? a.map.page_size : a.map.cap;
+  const long heads = (a.map.page_size > 0 ? (long)a.map.num_pages : (long)a.B) * a.map.Hkv;
+  if (heads > 0x7fffffffl) return false;
+  const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)rows, (cuuint64_t)heads};
+  const cuuint64_t strides[2] = {(cuuint64_t)D, (cuuint64_t)rows * D};
+  const cuuint32_t box[3] = {(cuuint32_t)D, (cuuint32_t)kKeys, 1};
+  const cuuint32_t es[3] = {1, 1, 1};
+  return encode_fn()(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<uint8_t*>(a.kc), dims, strides,
+                     box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                     D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Softmax warpgroups: one per 32 columns or so, so that its fixed work per tile
+// (waits, one barrier) is shared by many columns and a thread's sums and scores
+// stay in registers; widening warps and tiles in flight: what is left of the
+// registers.
 template <int D>
-bool launch_d(const Q8AttnArgs& a, const Q8Plan& p, cudaStream_t st) {
+bool launch_d(const CUtensorMap& m, const Q8AttnArgs& a, const Q8Plan& p, cudaStream_t st) {
   switch (p.rb) {
-    case 16: launch_n<16, D, 1, 8>(a, p, st); return true;
-    case 32: launch_n<32, D, 1, 8>(a, p, st); return true;
-    case 48: launch_n<48, D, 2, 8>(a, p, st); return true;
-    case 64: launch_n<64, D, 2, 8>(a, p, st); return true;
-    case 80: launch_n<80, D, 4, 7>(a, p, st); return true;
-    case 96: launch_n<96, D, 4, 7>(a, p, st); return true;
-    case 112: launch_n<112, D, 4, 7>(a, p, st); return true;
+    case 16: launch_n<16, D, 1, 8, 2>(m, a, p, st); return true;
+    case 32: launch_n<32, D, 1, 8, 2>(m, a, p, st); return true;
+    case 48: launch_n<48, D, 2, 6, 1>(m, a, p, st); return true;
+    case 64: launch_n<64, D, 2, 6, 1>(m, a, p, st); return true;
+    case 80: launch_n<80, D, 4, 6, 1>(m, a, p, st); return true;
+    case 96: launch_n<96, D, 4, 6, 1>(m, a, p, st); return true;
+    case 112: launch_n<112, D, 4, 6, 1>(m, a, p, st); return true;
   }
   return false;
 }
@@ -778,7 +915,9 @@ bool launch_d(const Q8AttnArgs& a, const Q8Plan& p, cudaStream_t st) {
 }  // namespace
 
 bool launch_q8_tc(const tsd_attn_desc& d, const Q8AttnArgs& a, const Q8Plan& p, cudaStream_t st) {
-  return d.dk == 128 ? launch_d<128>(a, p, st) : launch_d<64>(a, p, st);
+  CUtensorMap m;
+  if (encode_fn() == nullptr || !encode_keys(&m, a, d.dk)) return false;
+  return d.dk == 128 ? launch_d<128>(m, a, p, st) : launch_d<64>(m, a, p, st);
 }
 
 }  // namespace tsd
