@@ -307,11 +307,12 @@ Q8Plan plan_q8(const tsd_attn_desc& d) {
   Q8Plan p{};
   const int M = d.R * (d.Hq / d.Hkv);
   if (d.dtype == TSD_BF16 && !d.v_aliases_k) {
-    // tcgen05: at most 112 packed rows per CTA (shared memory), in equal groups
-    p.path = kQ8Tc;
+    // tcgen05: few packed rows on the columns, more on the lanes, in equal
+    // groups of at most 128 per CTA
+    p.path = M <= kQ8FewRows ? kQ8Few : kQ8Rows;
     p.part_bytes = 2;
-    p.nrg = (int)ceil_div(M, 112);
-    p.rb = (int)ceil_div(ceil_div(M, p.nrg), 16) * 16;
+    p.nrg = (int)ceil_div(M, 128);
+    p.rb = p.path == kQ8Few ? (int)ceil_div(M, 16) * 16 : (int)ceil_div(M, p.nrg);
     // One CTA per SM.  The split count minimises the modelled time of requests
     // that fill the cache: waves of CTAs times (tiles of a CTA + 4 for its
     // set-up and epilogue).
@@ -420,8 +421,9 @@ extern "C" tsd_status tsd_tree_verify_attn_q8(const tsd_attn_desc* d, const void
   a.qscale = d->scale * 1.4426950408889634f;
   const cudaStream_t st = (cudaStream_t)stream;
   const bool f32 = d->dtype == TSD_F32;
-  if (p.path == kQ8Tc) {
-    if (!launch_q8_tc(*d, a, p, st)) return TSD_ERR_UNSUPPORTED;
+  if (p.path == kQ8Few || p.path == kQ8Rows) {
+    if (!(p.path == kQ8Few ? launch_q8_few(*d, a, p, st) : launch_q8_rows(*d, a, p, st)))
+      return TSD_ERR_UNSUPPORTED;
     if (d->dv == 128) launch_combine<__nv_bfloat16, 128, __half>(a, p, st);
     else launch_combine<__nv_bfloat16, 64, __half>(a, p, st);
   } else if (alias) {

@@ -26,7 +26,10 @@ struct Q8AttnArgs {
   float qscale;               // softmax scale * log2(e)
 };
 
-enum Q8Path { kQ8Simt = 0, kQ8Tc = 1, kQ8Latent = 2 };
+enum Q8Path { kQ8Simt = 0, kQ8Few = 1, kQ8Rows = 2, kQ8Latent = 3 };
+
+// Up to this many packed rows take the path with keys on lanes.
+constexpr int kQ8FewRows = 32;
 
 struct Q8Plan {
   int path;
@@ -43,7 +46,8 @@ __device__ __forceinline__ int q8_splits(const Q8AttnArgs& a, int P) {
   return a.tree_split ? npre + 1 : max(npre, 1);
 }
 
-bool launch_q8_tc(const tsd_attn_desc& d, const Q8AttnArgs& a, const Q8Plan& p, cudaStream_t st);
+bool launch_q8_few(const tsd_attn_desc& d, const Q8AttnArgs& a, const Q8Plan& p, cudaStream_t st);
+bool launch_q8_rows(const tsd_attn_desc& d, const Q8AttnArgs& a, const Q8Plan& p, cudaStream_t st);
 bool launch_q8_latent(const tsd_attn_desc& d, const Q8AttnArgs& a, const Q8Plan& p,
                       cudaStream_t st);
 

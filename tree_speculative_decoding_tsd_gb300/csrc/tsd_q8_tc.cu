@@ -1,13 +1,20 @@
-// tcgen05 path of tsd_tree_verify_attn_q8: bf16 heads of 64 or 128 dims.
+// tcgen05 path of tsd_tree_verify_attn_q8 for bf16 heads of 64 or 128 dims with
+// more packed rows (R tree rows x g query heads of a KV head) than
+// tsd_q8_few.cu takes: up to 128 per CTA, on the lanes of the tensor memory.
 //
-// Products, transposed so that the packed query rows of a KV head (R tree rows
-// x g query heads) are the MMA's N (a multiple of 16):
-//   S^T[key][n]  = K_tile . Q^T     M = 128 keys, N = packed rows, K = d
-//   O^T[dim][n] += V_tile^T . P^T   M = 128 dims, N = packed rows, K = 128 keys
-// with fp32 accumulators in tensor memory (S^T twice, O^T once).
+//   S[n][key]  = Q . K_tile^T      M = 128 packed rows, N = 128 keys, K = d
+//   O[n][dim] += P . V_tile        M = 128 packed rows, N = d, K = 128 keys
+//
+// A thread owns one packed row: its maximum, its sum and its rescaling need no
+// other thread (with keys on lanes, as in tsd_verify_tc.cu, each is a reduction
+// across a warpgroup, and a probability costs about twice the instructions: the
+// 65-row trees over 8 x 32k keys took 555 us that way).  P goes back to the
+// tensor memory, over the scores it came from, and is the product's left operand
+// there: no shared memory and no barrier among the softmax warps.  Warps whose 32
+// rows are all behind the last one do nothing.
 //
 // Numbers.
-//   S^T    kind::f8f6f4: the K tile's codes as they are in the cache, and Q as
+//   S      kind::f8f6f4: the K tile's codes as they are in the cache, and Q as
 //          the sum of two e4m3 numbers.  A bf16 row is first multiplied by the
 //          power of two that puts its largest element into [128, 256); hi =
 //          e4m3(x), lo = e4m3(x - hi).  x has 8 significant bits, hi 4, so
@@ -22,198 +29,115 @@
 //          the largest u of the CTA's keys: rounded to 11 bits (2^-12), p below
 //          2^-32 (at the largest scale) to multiples of 2^-32.  The row sums
 //          take p before it is rounded.
-// A score is x = S^T * (2^k_key * scale log2(e) 2^q_n) - m_n, in fp32.
+// V is widened by warps and not taken in 8 bits: kind::f8f6f4 would need P in 8
+// bits.  Two e4m3 terms as for Q do not do: P spans 2^-32..2^8, and what lies
+// below 2^-17 of the largest would be lost from long flat rows.
 //
-// Why V is widened by warps and not taken in 8 bits: kind::f8f6f4 would need P
-// in 8 bits.  Two e4m3 terms as for Q do not do: P spans 2^-32..2^8, and what
-// lies below 2^-17 of the largest would be lost from long flat rows.
+// Two streams.  Even and odd tiles have a softmax warpgroup, scores, an
+// accumulator, a maximum and a sum each (512 tensor-memory columns for d = 128),
+// joined at the end: while one stream is in its softmax the tensor core works
+// for the other.  The running maximum is lazy: a row keeps it until a tile's
+// largest score passes it by 8 (in log2), so that its accumulator is rescaled
+// rarely.
 //
-// Roles: WG warpgroups of softmax and epilogue (as in tsd_verify_tc.cu:
-// warpgroup w/4 owns N / WG of the columns, warp w%4 the TMEM lanes
-// 32(w%4)..+31, i.e. 32 keys of a tile or 32 dims of O^T); one warp owns the
-// tensor memory and issues the products; one thread loads K tiles by TMA into a
-// ring of four; WW warps load V tiles straight into registers, VD tiles ahead
-// (behind L2 prefetches), and widen them into two fp16 stages, laid out as the
-// product reads them (rows of 64 elements, 128-byte swizzle).  P^T has two
-// buffers.  mbarriers order K -> S^T -> softmax -> O^T and V -> O^T; every wait
-// is bounded as in the bf16 path.
+// Roles (512 threads): warps 0-3 and 4-7 softmax and epilogue; warp 8 owns the
+// tensor memory and issues the products; one thread of warp 9 loads K tiles by
+// TMA into a ring of four; warps 10-15 load V tiles straight into registers, a
+// tile ahead (behind L2 prefetches), and widen them into three fp16 stages, laid
+// out as the product reads them (rows of 64 elements, 128-byte swizzle).
+// mbarriers order K -> S -> softmax -> O and V -> O; every wait is bounded.
 //
-// Softmax with keys on lanes: the running maximum of a column is lazy.  While
-// no x of a tile exceeds 8, the tile keeps the old maximum (p <= 256); else, and
-// on the CTA's first tile, the warpgroup takes the tile's column maxima,
-// re-centres x, and scales the sums and the O^T columns.
-#include <cuda.h>
-
+// What bounds it: the products of a 128-key tile, 8 8-bit and 8 fp16 ones of M =
+// 128, N = 128 (about 70 cycles each), and behind them the softmax (128
+// exponentials per row at 16 a cycle and SM).
 #include "tsd_common.cuh"
 #include "tsd_host.h"
-#include "tsd_q8_attn.cuh"
-#include "tsd_tcgen05.cuh"
+#include "tsd_q8_tc.cuh"
 
 namespace tsd {
 namespace {
 
-constexpr int kKeys = 128;
-constexpr uint32_t kHalf = kKeys * 128;         // [128 rows][64 fp16]: 16 KB
-constexpr uint32_t kTile = 2 * kHalf;           // a widened V tile
-constexpr int kRing = 4;                        // K tiles
-constexpr float kOverflow = 8.0f;               // log2 headroom of the lazy maximum
-constexpr int kHeadroom = 7;                    // P^T's offset: 2^8 * 2^7 < 65504
-constexpr int kMaxTiles = 256;                  // prefix tiles of a split
-constexpr int kPrefetch = 4;                    // tiles that V's L2 prefetch runs ahead
+constexpr int kMma = 8, kTma = 9, kWide = 10, kWideWarps = 6;
+constexpr int kWideThreads = kWideWarps * 32;
+constexpr int kThreads = (kWide + kWideWarps) * 32;
+constexpr int kStages = 3;                      // widened V tiles
+constexpr int kRows = 128;
 
-// N packed rows of D dims, WG softmax warpgroups, WW widening warps.
-template <int N, int D, int WG, int WW>
-struct Q8Layout {
-  static constexpr int soft_warps = 4 * WG;
-  static constexpr int threads = (soft_warps + 2 + WW) * 32;
-  static constexpr uint32_t k_bytes = kKeys * D;                 // a K tile: [128 keys][D] codes
-  static constexpr uint32_t q_bytes = N * D;                     // hi or lo of Q
-  static constexpr uint32_t pt_bytes = 256u * N;                 // 128 keys x N fp16
+template <int D>
+struct RowLayout {
+  static constexpr uint32_t k_bytes = kKeys * D, q_bytes = kRows * D;
+  static constexpr uint32_t v_bytes = kKeys * D * 2;
   static constexpr uint32_t off_k = 0;
   static constexpr uint32_t off_v = kRing * k_bytes;
-  static constexpr uint32_t off_p = off_v + 2 * kTile;
-  static constexpr uint32_t off_q = off_p + 2 * pt_bytes;        // hi, lo: [N][D] e4m3
-  static constexpr uint32_t off_misc = off_q + 2 * q_bytes;
-  static constexpr int NH = N / WG;               // columns per warpgroup
-  static constexpr int NO = NH / 8;               // column octets per warpgroup
-  static constexpr bool HQ = NH % 8 != 0;         // plus one quad
-  static constexpr int NU = NO + (HQ ? 1 : 0);
-  // columns are taken in two halves where one would need too many registers
-  static constexpr int U0 = NH > 24 ? NU / 2 : 0; // units of the first half
-  static constexpr int V0 = 8 * U0, V1 = NH - V0;
-  static constexpr int VMAX = V0 > V1 ? V0 : V1;
-  static_assert(NH % 4 == 0, "columns per warpgroup");
-  static constexpr uint32_t off_m = off_misc;                          // float[N] running max
-  static constexpr uint32_t off_alpha = off_m + 4 * N;                 // float[N]
-  static constexpr uint32_t off_negm = off_alpha + 4 * N;              // float[N] -m (0 if -inf)
-  static constexpr uint32_t off_shift = off_negm + 4 * N;              // float[N]
-  static constexpr uint32_t off_c2 = off_shift + 4 * N;                // float[N] column scales
-  static constexpr uint32_t off_red = off_c2 + 4 * N;                  // float[4 WG][NH]
-  static constexpr uint32_t off_rmask = off_red + 4 * soft_warps * NH; // u64[N]
-  static constexpr uint32_t off_ooff = off_rmask + 8 * N;              // i64[N]
-  static constexpr uint32_t off_rows = off_ooff + 8 * N;               // i64[kMaxTiles]
+  static constexpr uint32_t off_q = off_v + kStages * v_bytes;         // hi, lo: [128][D] e4m3
+  static constexpr uint32_t off_c2 = off_q + 2 * q_bytes;              // float[128] row scales
+  static constexpr uint32_t off_ml = off_c2 + 4 * kRows;               // float2[2][128] (m, l)
+  static constexpr uint32_t off_rows = off_ml + 16 * kRows;            // i64[kMaxTiles]
   static constexpr uint32_t off_tree = off_rows + 8 * kMaxTiles;       // 4 x 32 bits [128]
   static constexpr uint32_t off_kex = off_tree + 16 * kKeys;           // u8[2 kMaxTiles]
   static constexpr uint32_t off_vex = off_kex + 2 * kMaxTiles;
   static constexpr uint32_t off_bar = off_vex + 2 * kMaxTiles;
-  static constexpr int nbar = 19;
+  static constexpr int nbar = 21;
   static constexpr uint32_t off_flags = off_bar + 8 * nbar;            // tmem, abort, U
   static constexpr uint32_t total = off_flags + 16;
   static_assert(total + 1024 <= 232448, "shared memory budget");
-  __device__ static int col(int lc, int wg) {
-    return lc < 8 * NO ? 8 * (WG * (lc >> 3) + wg) + (lc & 7) : 8 * WG * NO + 4 * wg + (lc - 8 * NO);
-  }
 };
 
 // FULL: the copy landed or the warps wrote; EMPTY: read by the product (V_EMPTY
-// is also the end of a tile's O^T product); T_FULL: the scratch rows' keys, which
+// is also the end of a tile's O product); T_FULL: the scratch rows' keys, which
 // take the two K slots behind the last prefix tile (hi, lo).
-enum { BAR_K_FULL = 0, BAR_K_EMPTY = 4, BAR_V_FULL = 8, BAR_V_EMPTY = 10, BAR_S_FULL = 12,
-       BAR_P_FULL = 14, BAR_FINAL = 16, BAR_O_DONE = 17, BAR_T_FULL = 18 };
+enum { BAR_K_FULL = 0, BAR_K_EMPTY = 4, BAR_V_FULL = 8, BAR_V_EMPTY = 11, BAR_S_FULL = 14,
+       BAR_P_FULL = 16, BAR_FINAL = 18, BAR_O_DONE = 19, BAR_T_FULL = 20 };
 
-// D (+)= A.B, 8-bit operands (e4m3), K = 32 per instruction.
-__device__ __forceinline__ void mma_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
-                                       uint32_t acc) {
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32]) {
+  uint32_t r[32];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
+      "%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]),
+        "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
+        "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+      "%14,%15,%16};\n" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+// D (+)= A.B with A (fp16) in tensor memory.
+__device__ __forceinline__ void mma_f16_ta(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+                                           uint32_t acc) {
   asm volatile(
       "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(acc));
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(acc));
 }
 
-// Byte offset of 16-byte unit u of row r in a K-major tile of D-byte rows
-// (128-byte swizzle for D = 128, 64-byte swizzle for D = 64), and the matrix
-// descriptor of such a tile.
 template <int D>
-__device__ __forceinline__ uint32_t unit_offset(int r, int u) {
-  return D == 128 ? r * 128 + ((u ^ (r & 7)) << 4) : r * 64 + ((u ^ ((r >> 1) & 3)) << 4);
-}
-template <int D>
-__device__ __forceinline__ uint64_t row_desc(uint32_t addr) {
-  if (D == 128) return smem_desc(addr, 16, 1024);
-  return (uint64_t)((addr >> 4) & 0x3FFF) | ((uint64_t)1 << 16) | ((uint64_t)(512 >> 4) << 32) |
-         (1ull << 46) | (4ull << 61);
-}
-
-// Sixteen bf16 times f as e4m3 numbers hi and lo with hi + lo = x f.
-__device__ __forceinline__ void split16(const uint4 (&w)[2], float f, uint4& hi, uint4& lo) {
-  uint32_t h[4], l[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint4& s = w[i >> 1];
-    const uint32_t a = (i & 1) ? s.z : s.x, b = (i & 1) ? s.w : s.y;
-    const float x[4] = {__uint_as_float(a << 16) * f, __uint_as_float(a & 0xffff0000u) * f,
-                        __uint_as_float(b << 16) * f, __uint_as_float(b & 0xffff0000u) * f};
-    float y[4];
-    h[i] = q8_pack4(x[0], x[1], x[2], x[3]);
-    q8_unpack4(h[i], y);
-    l[i] = q8_pack4(x[0] - y[0], x[1] - y[1], x[2] - y[2], x[3] - y[3]);
-  }
-  hi = make_uint4(h[0], h[1], h[2], h[3]);
-  lo = make_uint4(l[0], l[1], l[2], l[3]);
-}
-
-__device__ __forceinline__ uint4 ld_stream(const uint8_t* p) {
-  uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];\n"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(p));
-  return v;
-}
-__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
-  const __half2 v = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&v);
-}
-// Largest finite magnitude of eight bf16 (bits, as the high half of an fp32),
-// and whether one is not finite.
-__device__ __forceinline__ void scan8(const uint4& w, uint32_t& top, bool& bad) {
-  const uint32_t v[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t a = (v[i] << 16) & 0x7fffffffu, b = v[i] & 0x7fff0000u;
-    bad |= a >= 0x7f800000u || b >= 0x7f800000u;
-    top = max(top, max(a >= 0x7f800000u ? 0u : a, b >= 0x7f800000u ? 0u : b));
-  }
-}
-// Eight bf16 times f as fp16.
-__device__ __forceinline__ uint4 scale8(const uint4& w, float f) {
-  uint4 r;
-  r.x = pack_half2(__uint_as_float(w.x << 16) * f, __uint_as_float(w.x & 0xffff0000u) * f);
-  r.y = pack_half2(__uint_as_float(w.y << 16) * f, __uint_as_float(w.y & 0xffff0000u) * f);
-  r.z = pack_half2(__uint_as_float(w.z << 16) * f, __uint_as_float(w.z & 0xffff0000u) * f);
-  r.w = pack_half2(__uint_as_float(w.w << 16) * f, __uint_as_float(w.w & 0xffff0000u) * f);
-  return r;
-}
-// fp32 exponent field of a row's largest magnitude, at least 15 so that both
-// the scale and its inverse are normal numbers.
-__device__ __forceinline__ int row_exponent(uint32_t top) { return max((int)(top >> 23), 15); }
-
-template <int N, int D, int WG, int WW, int VD>
-__global__ void __launch_bounds__(Q8Layout<N, D, WG, WW>::threads, 1)
-q8_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ Q8AttnArgs a) {
-  using L = Q8Layout<N, D, WG, WW>;
-  constexpr int kSoftWarps = L::soft_warps, kWideWarps = WW, kWideThreads = 32 * WW;
-  constexpr int kMmaWarp = kSoftWarps, kTmaWarp = kSoftWarps + 1, kWideWarp0 = kSoftWarps + 2;
-  constexpr int NH = L::NH, NO = L::NO, NU = L::NU, U0 = L::U0, VMAX = L::VMAX;
+__global__ void __launch_bounds__(kThreads, 1)
+q8_rows_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ Q8AttnArgs a) {
+  using L = RowLayout<D>;
   constexpr int CH = D / 16;                     // 16-code chunks of a row
   constexpr int kChunks = kKeys * CH;
   constexpr int NT = (kChunks + kWideThreads - 1) / kWideThreads;  // of a tile, per widening thread
-  if (threadIdx.x == kTmaWarp * 32) tma_desc_prefetch(&kmap);
+  if (threadIdx.x == kTma * 32) tma_desc_prefetch(&kmap);
   grid_dependency_sync();
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   const uint32_t raw = su32(smem_raw);
   const uint32_t sbase = (raw + 1023u) & ~1023u;
   uint8_t* smem = smem_raw + (sbase - raw);
-  float* m_run = (float*)(smem + L::off_m);
-  float* alpha = (float*)(smem + L::off_alpha);
-  float* negm = (float*)(smem + L::off_negm);
-  float* shiftv = (float*)(smem + L::off_shift);
   float* c2v = (float*)(smem + L::off_c2);
-  float* red = (float*)(smem + L::off_red);
-  uint64_t* rmask = (uint64_t*)(smem + L::off_rmask);
-  long long* ooff = (long long*)(smem + L::off_ooff);
+  float2* s_ml = (float2*)(smem + L::off_ml);
   long long* tile_row = (long long*)(smem + L::off_rows);
-  float* kt_in = (float*)(smem + L::off_tree);      // tree rows: factor into fp16 (0: row of zeros)
-  float* vt_in = kt_in + kKeys;
+  float* kt_in = (float*)(smem + L::off_tree);      // tree rows: factor into e4m3 (0: row of zeros)
+  float* vt_in = kt_in + kKeys;                     // and into fp16
   float* kt_out = vt_in + kKeys;                    // factor of the scores (NaN: a row with a NaN or inf)
   int* vt_u = (int*)(kt_out + kKeys);               // exponent of the value row
   uint8_t* kex = smem + L::off_kex;
@@ -234,18 +158,22 @@ q8_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ Q
   const int ntiles = n_pre + (with_tree ? 1 : 0);
   const int row_base = rg * a.rb;
   const int rows_here = min(a.rb, a.M - row_base);
+  const int live_warps = (rows_here + 31) / 32;     // softmax warps of a stream with rows
+  auto valid_of = [&](int t) { return min(kKeys, k1 - (k0 + t * kKeys)); };
 
   // ---------------------------------------------------------------- set-up
-  if (tid == kMmaWarp * 32) {
+  if (tid == kMma * 32) {
     for (int i = 0; i < kRing; ++i) {
       mbar_init(bar(BAR_K_FULL + i), 1);
       mbar_init(bar(BAR_K_EMPTY + i), 1);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < kStages; ++i) {
       mbar_init(bar(BAR_V_FULL + i), kWideWarps);
       mbar_init(bar(BAR_V_EMPTY + i), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
       mbar_init(bar(BAR_S_FULL + i), 1);
-      mbar_init(bar(BAR_P_FULL + i), kSoftWarps);
+      mbar_init(bar(BAR_P_FULL + i), live_warps);
     }
     mbar_init(bar(BAR_FINAL), 1);
     mbar_init(bar(BAR_O_DONE), 1);
@@ -254,7 +182,7 @@ q8_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ Q
     *s_top = -1000;
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
   }
-  if (warp == kMmaWarp) {
+  if (warp == kMma) {
     __syncwarp();
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;\n" ::"r"(
         sbase + L::off_flags));
@@ -266,7 +194,7 @@ q8_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ Q
   // lanes that store together take chunks 0-3 of an even and an odd row (D =
   // 128), or of two rows (D = 64): eight different 16-byte columns of a
   // swizzled row pair, so the stores do not conflict
-  const int wt = tid - kWideWarp0 * 32;
+  const int wt = tid - kWide * 32;
   auto chunk_row = [&](int i) {
     const int x = wt + kWideThreads * i;
     return D == 128 ? 2 * (x >> 4) + ((x >> 2) & 1) : x >> 2;
@@ -275,23 +203,20 @@ q8_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ Q
     const int x = wt + kWideThreads * i;
     return D == 128 ? (x & 3) + 4 * ((x >> 3) & 1) : x & 3;
   };
-  uint4 vreg[VD][NT];
-  auto load_v = [&](uint4 (&r)[NT], long row, int nvalid) {
+  uint4 vreg[NT];
+  auto load_v = [&](long row, int nvalid) {
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
-      r[i] = make_uint4(0u, 0u, 0u, 0u);
+      vreg[i] = make_uint4(0u, 0u, 0u, 0u);
       // (the last round may be short; a row past the tile is never valid)
       if (row >= 0 && chunk_row(i) < nvalid)
-        r[i] = ld_stream(a.vc + (row + chunk_row(i)) * D + chunk_col(i) * 16);
+        vreg[i] = ld_stream(a.vc + (row + chunk_row(i)) * D + chunk_col(i) * 16);
     }
   };
-  auto valid_of = [&](int t) { return min(kKeys, k1 - (k0 + t * kKeys)); };
 
-  if (warp >= kWideWarp0) {
+  if (warp >= kWide) {
     // the first tile's loads go out before anything else
-#pragma unroll
-    for (int i = 0; i < VD; ++i)
-      if (i < n_pre) load_v(vreg[i], a.map.row(b, hk, k0 + i * kKeys), valid_of(i));
+    if (n_pre > 0) load_v(a.map.row(b, hk, k0), valid_of(0));
     int top = -1000;
     for (int t = wt; t < n_pre; t += kWideThreads) {
       const int pos = k0 + t * kKeys;
@@ -309,100 +234,12 @@ q8_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ Q
       vex[2 * t + 1] = (uint8_t)vb;
       top = max(top, max(va, vb) - 127);
     }
-    if (with_tree) {
-      // scratch rows: eight lanes per row
-      uint32_t lo = 0, hi = 0;
-      for (int r = lane; r < a.R; r += 32) {
-        const uint64_t m = r > 0 ? a.mask[(long)b * a.R + r] : 0ull;
-        lo |= (uint32_t)m;
-        hi |= (uint32_t)(m >> 32);
-      }
-      lo = __reduce_or_sync(kFull, lo);
-      hi = __reduce_or_sync(kFull, hi);
-      const uint64_t seen = ((uint64_t)hi << 32) | lo;
-      for (int x = wt; x < kKeys * 8; x += kWideThreads) {
-        const int j = x >> 3, c = x & 7;
-        const bool live = j < a.R && (j == 0 || ((seen >> (j - 1)) & 1ull));
-        uint32_t kt = 0, vt = 0;
-        bool bad = false;
-        if (live) {
-          const long row = ((long)b * a.R + j) * a.map.Hkv + hk;
-          const uint4* kp = (const uint4*)((const __nv_bfloat16*)a.kt + row * D) + c * (D / 64);
-          const uint4* vp = (const uint4*)((const __nv_bfloat16*)a.vt + row * D) + c * (D / 64);
-#pragma unroll
-          for (int i = 0; i < D / 64; ++i) {
-            scan8(__ldg(kp + i), kt, bad);
-            scan8(__ldg(vp + i), vt, bad);
-          }
-        }
-#pragma unroll
-        for (int o = 4; o > 0; o >>= 1) {
-          kt = max(kt, __shfl_xor_sync(kFull, kt, o));
-          vt = max(vt, __shfl_xor_sync(kFull, vt, o));
-        }
-        const uint32_t any = __ballot_sync(kFull, bad);
-        bad = (any >> (lane & 24)) & 0xffu;
-        const int ek = row_exponent(kt), ev = row_exponent(vt);
-        if (c == 0) {
-          // K: 2^(7 - (e - 127)) and its inverse; V: 2^(8 - (e - 127))
-          kt_in[j] = live && !bad ? q8_scale(261 - ek) : 0.f;
-          vt_in[j] = live && !bad ? q8_scale(262 - ev) : 0.f;
-          kt_out[j] = bad ? __int_as_float(0x7fffffff) : q8_scale(ek - 7);
-          vt_u[j] = live ? ev - 135 : -1000;
-        }
-        if (live) top = max(top, ev - 135);
-      }
-    }
+    if (with_tree) top = max(top, scan_tree<D>(a, b, hk, wt, kWideThreads, kt_in, vt_in, kt_out, vt_u));
     top = __reduce_max_sync(kFull, top);
     if (lane == 0) atomicMax(s_top, top);
-    if (D == 64) {       // the upper 64 dims of the value tiles stay zero
-      for (int x = wt; x < 2 * (int)(kHalf / 16); x += kWideThreads)
-        *(uint4*)(smem + L::off_v + (x >= (int)(kHalf / 16) ? kTile : 0u) + kHalf +
-                  (x % (int)(kHalf / 16)) * 16) = make_uint4(0u, 0u, 0u, 0u);
-      asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
-    }
-  } else if (warp < kSoftWarps) {
-    // Q as hi + lo, rows scaled: eight lanes per row (D = 64: four), 16 elements each
-    constexpr int QL = D / 16;
-    for (int x = tid; x < N * QL; x += kSoftWarps * 32) {
-      const int n = x / QL, c = x % QL;
-      uint4 w[2] = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
-      uint32_t top = 0;
-      bool bad = false;
-      if (n < rows_here) {
-        const int p = row_base + n;
-        const int tr = p / a.g, qh = hk * a.g + p % a.g;
-        const uint4* qp =
-            (const uint4*)((const __nv_bfloat16*)a.q + (((long)b * a.R + tr) * a.Hq + qh) * D) +
-            2 * c;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          w[i] = __ldg(qp + i);
-          scan8(w[i], top, bad);
-        }
-      }
-      // (N * QL is a multiple of 32: whole warps take part)
-#pragma unroll
-      for (int o = QL / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(kFull, top, o));
-      const uint32_t any = __ballot_sync(kFull, bad);
-      bad = (any >> (lane & (32 - QL))) & ((1u << QL) - 1u);
-      const int e = row_exponent(top);
-      uint4 hi = make_uint4(0u, 0u, 0u, 0u), lo = hi;
-      if (!bad) split16(w, q8_scale(261 - e), hi, lo);
-      *(uint4*)(smem + L::off_q + unit_offset<D>(n, c)) = hi;
-      *(uint4*)(smem + L::off_q + L::q_bytes + unit_offset<D>(n, c)) = lo;
-      if (c == 0) c2v[n] = bad ? __int_as_float(0x7fffffff) : a.qscale * q8_scale(e - 7);
-    }
-    for (int n = tid; n < N; n += kSoftWarps * 32) {
-      uint64_t mk = 0ull;
-      if (n < rows_here) {
-        const int tr = (row_base + n) / a.g;
-        mk = tr > 0 ? a.mask[(long)b * a.R + tr] : 0ull;
-      }
-      rmask[n] = mk;
-      m_run[n] = -INFINITY;
-      negm[n] = 0.f;
-    }
+  } else if (warp < 8) {
+    stage_q<D>(a, b, hk, row_base, rows_here, kRows, tid, 256, smem + L::off_q,
+               smem + L::off_q + L::q_bytes, c2v);
     asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
   }
   fence_before();
@@ -410,11 +247,11 @@ q8_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ Q
   fence_after();
   const uint32_t tmem = flags[0];
   const int U = *s_top;
-  auto tm_s = [&](int i) { return tmem + (uint32_t)(i * N); };
-  const uint32_t tm_o = tmem + 2u * N;
+  auto tm_s = [&](int p) { return tmem + (uint32_t)(p * kKeys); };
+  auto tm_o = [&](int p) { return tmem + 256u + (uint32_t)(p * D); };
 
   // -------------------------------------------------------------- K tiles
-  if (warp == kTmaWarp) {
+  if (warp == kTma) {
     if (lane == 0) {
       int loaded = 0;
       for (int t = 0; t < n_pre && !flags[1]; ++t) {
@@ -423,24 +260,11 @@ q8_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ Q
           flags[1] = 1;
           break;
         }
-        // (a tile behind the cache's or page's last row reads zeros there; rows
-        // behind the prefix are masked later, whatever they hold; the rows of a
-        // missing page are those of page 0)
-        const int pos = k0 + t * kKeys;
-        int y = pos, z = b * a.map.Hkv + hk;
-        if (a.map.page_size) {
-          const long r = tile_row[t] < 0 ? 0 : tile_row[t];
-          y = (int)(r % a.map.page_size);
-          z = (int)(r / a.map.page_size);
-        }
-        mbar_expect_tx(bar(BAR_K_FULL + sl), L::k_bytes);
-        tma_3d(sbase + L::off_k + sl * L::k_bytes, &kmap, 0, y, z, bar(BAR_K_FULL + sl));
+        load_keys(a, kmap, b, hk, k0 + t * kKeys, tile_row[t], sbase + L::off_k + sl * L::k_bytes,
+                  L::k_bytes, bar(BAR_K_FULL + sl));
         ++loaded;
-        if (t == 0)
-          for (int i = VD; i < kPrefetch; ++i)
-            if (i < n_pre && tile_row[i] >= 0) prefetch_l2(a.vc + tile_row[i] * D, (long)valid_of(i) * D);
-        const int i = t + kPrefetch;
-        if (i < n_pre && tile_row[i] >= 0) prefetch_l2(a.vc + tile_row[i] * D, (long)valid_of(i) * D);
+        for (int i = t == 0 ? 1 : t + kPrefetch; i <= t + kPrefetch; ++i)
+          if (i < n_pre && tile_row[i] >= 0) prefetch_l2(a.vc + tile_row[i] * D, (long)valid_of(i) * D);
       }
       // no copy may be in flight when the CTA leaves
       for (int sl = 0; sl < kRing && sl < loaded; ++sl)
@@ -450,142 +274,108 @@ q8_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ Q
   }
 
   // -------------------------------------------------------------- widening
-  else if (warp >= kWideWarp0) {
-    auto widen = [&](const uint4 (&r)[NT], uint32_t stage) {
-#pragma unroll
-      for (int i = 0; i < NT; ++i) {
-        if (kChunks % kWideThreads != 0 && wt + kWideThreads * i >= kChunks) break;
-        const int row = chunk_row(i), c = chunk_col(i);
-        const uint32_t w[4] = {r[i].x, r[i].y, r[i].z, r[i].w};
-        uint32_t h[8];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) q8_half4(w[j], h[2 * j], h[2 * j + 1]);
-        uint8_t* dst = smem + stage + (c >> 2) * kHalf + row * 128;
-        const int u = 2 * (c & 3);
-        *(uint4*)(dst + (((u + 0) ^ (row & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
-        *(uint4*)(dst + (((u + 1) ^ (row & 7)) << 4)) = make_uint4(h[4], h[5], h[6], h[7]);
-      }
-    };
-    // the scratch rows of this head, scaled; rows that nobody sees are zeros
-    auto tree_keys = [&](int s_hi, int s_lo) {
-      for (int x = wt; x < kKeys * (D / 16); x += kWideThreads) {
-        const int row = x / (D / 16), u = x % (D / 16);
-        uint4 hi = make_uint4(0u, 0u, 0u, 0u), lo = hi;
-        const float f = kt_in[row];
-        if (f != 0.f) {
-          const uint4* p = (const uint4*)((const __nv_bfloat16*)a.kt +
-                                          (((long)b * a.R + row) * a.map.Hkv + hk) * D) + 2 * u;
-          const uint4 w[2] = {__ldg(p), __ldg(p + 1)};
-          split16(w, f, hi, lo);
+  else if (warp >= kWide) {
+    const int tree_at = max(n_pre - 2, 0);     // the tree's keys are made two tiles early
+    for (int t = 0; t < ntiles; ++t) {
+      const int st = t % kStages;
+      if (with_tree && t == tree_at) {
+        const int s0 = n_pre, s1 = n_pre + 1;
+        if ((s0 >= kRing && !__all_sync(kFull, mbar_wait(bar(BAR_K_EMPTY + s0 % kRing),
+                                                         (s0 / kRing - 1) & 1))) ||
+            (s1 >= kRing && !__all_sync(kFull, mbar_wait(bar(BAR_K_EMPTY + s1 % kRing),
+                                                         (s1 / kRing - 1) & 1)))) {
+          flags[1] = 1;
+          break;
         }
-        *(uint4*)(smem + L::off_k + s_hi * L::k_bytes + unit_offset<D>(row, u)) = hi;
-        *(uint4*)(smem + L::off_k + s_lo * L::k_bytes + unit_offset<D>(row, u)) = lo;
+        tree_keys<D>(a, b, hk, wt, kWideThreads, kt_in, smem + L::off_k + (s0 % kRing) * L::k_bytes,
+                     smem + L::off_k + (s1 % kRing) * L::k_bytes);
+        asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(BAR_T_FULL));
+      }
+      if (t >= kStages &&
+          !__all_sync(kFull, mbar_wait(bar(BAR_V_EMPTY + st), (t / kStages - 1) & 1))) {
+        flags[1] = 1;
+        break;
+      }
+      uint8_t* const stage = smem + L::off_v + st * L::v_bytes;
+      if (t < n_pre) {
+#pragma unroll
+        for (int i = 0; i < NT; ++i) {
+          if (kChunks % kWideThreads != 0 && wt + kWideThreads * i >= kChunks) break;
+          const int row = chunk_row(i), c = chunk_col(i);
+          uint32_t h[8];
+          q8_half4(vreg[i].x, h[0], h[1]);
+          q8_half4(vreg[i].y, h[2], h[3]);
+          q8_half4(vreg[i].z, h[4], h[5]);
+          q8_half4(vreg[i].w, h[6], h[7]);
+          uint8_t* dst = stage + (c >> 2) * kHalf + row * 128;
+          const int u = 2 * (c & 3);
+          *(uint4*)(dst + (((u + 0) ^ (row & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
+          *(uint4*)(dst + (((u + 1) ^ (row & 7)) << 4)) = make_uint4(h[4], h[5], h[6], h[7]);
+        }
+      } else {
+        tree_values<D>(a, b, hk, wt, kWideThreads, vt_in, stage);
       }
       asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar(BAR_T_FULL));
-    };
-    auto tree_values = [&](uint32_t stage) {
-      for (int x = wt; x < kKeys * (D / 8); x += kWideThreads) {
-        const int row = x / (D / 8), u = x % (D / 8);
-        const float f = vt_in[row];
-        uint4 v = make_uint4(0u, 0u, 0u, 0u);
-        if (f != 0.f)
-          v = scale8(__ldg((const uint4*)((const __nv_bfloat16*)a.vt +
-                                          (((long)b * a.R + row) * a.map.Hkv + hk) * D) + u), f);
-        *(uint4*)(smem + stage + (u >> 3) * kHalf + row * 128 + (((u & 7) ^ (row & 7)) << 4)) = v;
-      }
-    };
-    const int tree_at = max(n_pre - 2, 0);     // the tree's keys are made two tiles early
-    bool ok = true;
-    for (int t0 = 0; ok && t0 < ntiles; t0 += VD) {
-#pragma unroll
-      for (int i = 0; i < VD; ++i) {           // (constant register indexes)
-        const int t = t0 + i, st = t & 1;
-        if (t >= ntiles) break;
-        if (with_tree && t == tree_at) {
-          const int s0 = n_pre, s1 = n_pre + 1;
-          if ((s0 >= kRing && !__all_sync(kFull, mbar_wait(bar(BAR_K_EMPTY + s0 % kRing),
-                                                           (s0 / kRing - 1) & 1))) ||
-              (s1 >= kRing && !__all_sync(kFull, mbar_wait(bar(BAR_K_EMPTY + s1 % kRing),
-                                                           (s1 / kRing - 1) & 1)))) {
-            flags[1] = 1;
-            ok = false;
-            break;
-          }
-          tree_keys(s0 % kRing, s1 % kRing);
-        }
-        if (t >= 2 && !__all_sync(kFull, mbar_wait(bar(BAR_V_EMPTY + st), ((t >> 1) - 1) & 1))) {
-          flags[1] = 1;
-          ok = false;
-          break;
-        }
-        if (t < n_pre) widen(vreg[i], L::off_v + st * kTile);
-        else tree_values(L::off_v + st * kTile);
-        asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(BAR_V_FULL + st));
-        if (t + VD < n_pre) load_v(vreg[i], tile_row[t + VD], valid_of(t + VD));
-        if (__any_sync(kFull, flags[1] != 0)) {
-          ok = false;
-          break;
-        }
-      }
+      if (lane == 0) mbar_arrive(bar(BAR_V_FULL + st));
+      if (t + 1 < n_pre) load_v(tile_row[t + 1], valid_of(t + 1));
+      if (__any_sync(kFull, flags[1] != 0)) break;
     }
   }
 
   // ------------------------------------------------------------------ MMA
-  else if (warp == kMmaWarp) {
+  else if (warp == kMma) {
     if (lane == 0) {
-      // fp32 accumulators; e4m3 (S^T) and fp16 (O^T) operands are both format 0
-      const uint32_t idesc_qk = (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(kKeys >> 4) << 24);
-      const uint32_t idesc_pv = idesc_qk | (1u << 15) | (1u << 16);
+      // fp32 accumulators; e4m3 (S) and fp16 (O) operands are both format 0
+      const uint32_t idesc_qk =
+          (1u << 4) | ((uint32_t)(kKeys >> 3) << 17) | ((uint32_t)(kRows >> 4) << 24);
+      const uint32_t idesc_pv =
+          (1u << 4) | (1u << 16) | ((uint32_t)(D >> 3) << 17) | ((uint32_t)(kRows >> 4) << 24);
       const uint64_t kd0 = row_desc<D>(sbase + L::off_k);
       const uint64_t qd0 = row_desc<D>(sbase + L::off_q);
       const uint64_t vd0 = smem_desc(sbase + L::off_v, kHalf, 1024);
-      // P^T: 8x8 cores, the key groups of 8 columns contiguous (tsd_verify_tc.cu)
-      const uint64_t pd0 = smem_desc_interleave(sbase + L::off_p, 128, 2048);
-      // S^T (+)= K slot x (Q hi + Q lo)
+      // S (+)= (Q hi + Q lo) x K slot
       auto products = [&](uint32_t ts, int sl, bool first) {
         const uint64_t kd = kd0 + (uint64_t)(sl * (L::k_bytes >> 4));
 #pragma unroll
         for (int part = 0; part < 2; ++part)
 #pragma unroll
           for (int kk = 0; kk < D / 32; ++kk)
-            mma_f8(ts, kd + 2 * kk, qd0 + (uint64_t)(part * (L::q_bytes >> 4)) + 2 * kk, idesc_qk,
+            mma_f8(ts, qd0 + (uint64_t)(part * (L::q_bytes >> 4)) + 2 * kk, kd + 2 * kk, idesc_qk,
                    first && part == 0 && kk == 0 ? 0u : 1u);
       };
       auto issue_qk = [&](int t) -> bool {
-        const int st = t & 1, sl = t % kRing;
+        const int sl = t % kRing;
         if (!(t < n_pre ? mbar_wait(bar(BAR_K_FULL + sl), (t / kRing) & 1)
                         : mbar_wait(bar(BAR_T_FULL), 0)))
           return false;
         fence_after();
-        products(tm_s(st), sl, true);
-        if (t >= n_pre) products(tm_s(st), (t + 1) % kRing, false);
-        mma_commit(bar(BAR_S_FULL + st));
+        products(tm_s(t & 1), sl, true);
+        if (t >= n_pre) products(tm_s(t & 1), (t + 1) % kRing, false);
+        mma_commit(bar(BAR_S_FULL + (t & 1)));
         mma_commit(bar(BAR_K_EMPTY + sl));
         return true;
       };
-      bool ok = issue_qk(0);
+      bool ok = issue_qk(0) && (ntiles < 2 || issue_qk(1));
       for (int t = 0; ok && t < ntiles; ++t) {
-        const int st = t & 1;
-        if (t + 1 < ntiles && !issue_qk(t + 1)) { ok = false; break; }
-        if (!mbar_wait(bar(BAR_P_FULL + st), (t >> 1) & 1) || flags[1] ||
-            !mbar_wait(bar(BAR_V_FULL + st), (t >> 1) & 1)) {
+        const int p = t & 1, st = t % kStages;
+        if (!mbar_wait(bar(BAR_P_FULL + p), (t >> 1) & 1) || flags[1] ||
+            !mbar_wait(bar(BAR_V_FULL + st), (t / kStages) & 1)) {
           ok = false;
           break;
         }
         fence_after();
-        const uint64_t vd = vd0 + (uint64_t)(st * (kTile >> 4));
-        const uint64_t pd = pd0 + (uint64_t)(st * (L::pt_bytes >> 4));
-        if (t == 0) mma_f16(tm_o, vd, pd, idesc_pv, 0u);
-        else mma_f16_acc(tm_o, vd, pd, idesc_pv);
+        const uint64_t vd = vd0 + (uint64_t)(st * (L::v_bytes >> 4));
 #pragma unroll
-        for (int kk = 1; kk < kKeys / 16; ++kk)
-          mma_f16_acc(tm_o, vd + 128 * kk, pd + (uint64_t)(16 * kk), idesc_pv);
+        for (int kk = 0; kk < kKeys / 16; ++kk)
+          mma_f16_ta(tm_o(p), tm_s(p) + 8 * kk, vd + 128 * kk, idesc_pv, t < 2 && kk == 0 ? 0u : 1u);
         mma_commit(bar(BAR_V_EMPTY + st));
         if (t == ntiles - 1) mma_commit(bar(BAR_O_DONE));
+        // the next scores of this stream go over P: its product must be done
+        if (t + 2 < ntiles)
+          ok = mbar_wait(bar(BAR_V_EMPTY + st), (t / kStages) & 1) && issue_qk(t + 2);
       }
       if (!ok) flags[1] = 1;
       // every product has completed once this commit lands
@@ -597,260 +387,214 @@ q8_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ Q
 
   // -------------------------------------------------------------- softmax
   else {
-    const int wg = warp >> 2, q = warp & 3;
-    const int key = q * 32 + lane;
+    const int p = warp >> 2, q = warp & 3, row = q * 32 + lane;
     const uint32_t lane_off = (uint32_t)(q * 32) << 16;
-    const int c_oct = 8 * wg, c_quad = 8 * WG * NO + 4 * wg;
-    const uint32_t pt_oct = (uint32_t)key * 16u + (uint32_t)wg * 2048u;
-    const uint32_t pt_quad =
-        (uint32_t)key * 16u + (uint32_t)(c_quad >> 3) * 2048u + (uint32_t)(c_quad & 4) * 2u;
-    float2 l2[NH / 2];
-#pragma unroll
-    for (int i = 0; i < NH / 2; ++i) l2[i] = make_float2(0.f, 0.f);
+    const uint32_t ts = tm_s(p) + lane_off;
+    float m = -INFINITY, l = 0.f;
     bool failed = false;
-
-    for (int t = 0; t < ntiles; ++t) {
-      const int st = t & 1;
-      const bool is_tree = t >= n_pre;
-      const int nvalid = is_tree ? a.R : valid_of(t);
-      float ck, fv;
-      if (is_tree) {
-        ck = kt_out[key];
-        fv = pow2i(max(vt_u[key], -900) - U + kHeadroom);
-      } else {
-        ck = q8_scale(kex[2 * t + (key >> 6)]);
-        fv = pow2i((int)vex[2 * t + (key >> 6)] - 127 - U + kHeadroom);
+    if (q < live_warps) {
+      const float c2 = c2v[row];
+      uint64_t mask = 0ull;
+      if (row < rows_here) {
+        const int tr = (row_base + row) / a.g;
+        mask = tr > 0 ? a.mask[(long)b * a.R + tr] : 0ull;
       }
-      const float2 ck2 = make_float2(ck, ck), fv2 = make_float2(fv, fv);
-      const bool ok = __all_sync(kFull, mbar_wait(bar(BAR_S_FULL + st), (t >> 1) & 1));
-      fence_after();
-      const uint32_t srow = tm_s(st) + lane_off;
-      uint8_t* pt = smem + L::off_p + st * L::pt_bytes;
-      bool stop_now = false;
-      bool p_free = t < 2;                   // O^T_(t-2) has read this P^T buffer
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int ua = h == 0 ? 0 : U0, ub = h == 0 ? U0 : NU;
-        if (ua >= ub) continue;
-        const int lc0 = 8 * ua;
-        const int ncol = (ub == NU && L::HQ) ? 8 * (ub - 1 - ua) + 4 : 8 * (ub - ua);
-        // x = S^T * scale - m, and the largest x
-        float v[VMAX];
-        if (ok) {
-#pragma unroll
-          for (int u = ua; u < ub; ++u) {
-            float* x = v + 8 * (u - ua);
-            if (u < NO) tmem_ld8(srow + (uint32_t)(8 * WG * u + c_oct), x);
-            else tmem_ld4(srow + (uint32_t)c_quad, x[0], x[1], x[2], x[3]);
-          }
-          tmem_wait_ld();
-        }
-#pragma unroll
-        for (int u = ua; u < ub; ++u) {
-          float* x = v + 8 * (u - ua);
-          const int nq = u < NO ? 2 : 1;
-          const int c = u < NO ? 8 * WG * u + c_oct : c_quad;
-#pragma unroll
-          for (int j = 0; j < nq; ++j) {
-            const float4 nm = *(const float4*)(negm + c + 4 * j);
-            const float4 c2 = *(const float4*)(c2v + c + 4 * j);
-            const float2 x01 = __ffma2_rn(make_float2(x[4 * j], x[4 * j + 1]),
-                                          __fmul2_rn(make_float2(c2.x, c2.y), ck2),
-                                          make_float2(nm.x, nm.y));
-            const float2 x23 = __ffma2_rn(make_float2(x[4 * j + 2], x[4 * j + 3]),
-                                          __fmul2_rn(make_float2(c2.z, c2.w), ck2),
-                                          make_float2(nm.z, nm.w));
-            x[4 * j] = x01.x;
-            x[4 * j + 1] = x01.y;
-            x[4 * j + 2] = x23.x;
-            x[4 * j + 3] = x23.y;
-          }
-        }
-        if (is_tree || nvalid < kKeys) {
-          if (key >= nvalid) {
-#pragma unroll
-            for (int e = 0; e < VMAX; ++e) v[e] = -INFINITY;
-          } else if (is_tree && key > 0) {
-            uint32_t vis = 0u;
+      // raise the maximum to X where it passes m by the headroom (or m is
+      // none), and rescale the sum and the accumulator
+      auto raise = [&](float X, bool first) {
+        const bool need = !(X <= m + kOverflow);
+        if (!__any_sync(kFull, need)) return;
+        const float m_new = need ? fmaxf(m, X) : m;
+        const float al = m_new == m ? 1.f : m == -INFINITY ? 0.f : ex2(m - m_new);
+        m = m_new;
+        l *= al;
+        if (first) return;
 #pragma unroll 1
-            for (int e = 0; e < ncol; ++e)
-              vis |= (uint32_t)((rmask[L::col(lc0 + e, wg)] >> (key - 1)) & 1ull) << e;
+        for (int c = 0; c < D; c += 32) {
+          float o[32];
+          tmem_ld32(tm_o(p) + lane_off + c, o);
+          tmem_wait_ld();
+          uint32_t w[16];
 #pragma unroll
-            for (int e = 0; e < VMAX; ++e)
-              if (!((vis >> e) & 1u)) v[e] = -INFINITY;
+          for (int half = 0; half < 2; ++half) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(o[16 * half + i] * al);
+            tmem_st16(tm_o(p) + lane_off + c + 16 * half, w);
           }
         }
-        float tmax = -INFINITY;
-#pragma unroll
-        for (int e = 0; e < VMAX; e += 2)
-          if (e < ncol) tmax = max3f(tmax, v[e], v[e + 1]);
+        tmem_wait_st();
+      };
 
-        const bool local_stop = ua == 0 && (!ok || failed || flags[1] != 0);
-        if (wg_bar_or(wg, local_stop || t == 0 || tmax > kOverflow)) {
-          if (ua == 0 && wg_bar_or(wg, local_stop)) {
-            stop_now = true;
-            break;
-          }
+      for (int t = p; t < ntiles; t += 2) {
+        if (!__all_sync(kFull, mbar_wait(bar(BAR_S_FULL + p), (t >> 1) & 1)) ||
+            __any_sync(kFull, flags[1] != 0)) {
+          failed = true;
+          break;
+        }
+        fence_after();
+        const bool is_tree = t >= n_pre;
+        const int nvalid = is_tree ? a.R : valid_of(t);
+        if (!is_tree && nvalid == kKeys) {
+          // two blocks of 64 keys: one factor and one offset each
+          const float f0 = c2 * q8_scale(kex[2 * t]), f1 = c2 * q8_scale(kex[2 * t + 1]);
+          // (an offset below -60 puts P under fp16's range: its exact value
+          // does not matter, and the sum stays within fp32)
+          const int d0 = max((int)vex[2 * t] - 127 - U + kHeadroom, -60);
+          const int d1 = max((int)vex[2 * t + 1] - 127 - U + kHeadroom, -60);
+          float top[2];
 #pragma unroll
-          for (int e4 = 0; e4 < VMAX / 4; ++e4) {
-            if (4 * e4 >= ncol) break;
-            float r4[4] = {v[4 * e4], v[4 * e4 + 1], v[4 * e4 + 2], v[4 * e4 + 3]};
-            const float r = warp_reduce_scatter<4, true>(r4, lane);
-            if (lane < 4) red[warp * NH + lc0 + 4 * e4 + lane] = r;
-          }
-          wg_bar(wg);
-          for (int n = lc0 + (tid & 127); n < lc0 + ncol; n += 128) {
-            const int col = L::col(n, wg);
-            float X = -INFINITY;
+          for (int h = 0; h < 2; ++h) {
+            float ta = -INFINITY, tb = -INFINITY;
 #pragma unroll
-            for (int w = 0; w < 4; ++w) X = fmaxf(X, red[(wg * 4 + w) * NH + n]);
-            const float m_old = m_run[col];
-            float m_new, sh, al;
-            if (m_old == -INFINITY) {
-              m_new = X;
-              sh = X == -INFINITY ? 0.f : X;
-              al = 0.f;
-            } else {
-              sh = fmaxf(X, 0.f);
-              m_new = m_old + sh;
-              al = ex2(-sh);
-            }
-            m_run[col] = m_new;
-            alpha[col] = al;
-            shiftv[col] = sh;
-            negm[col] = m_new == -INFINITY ? 0.f : -m_new;
-          }
-          wg_bar(wg);
-          if (t > 0) {
-            if (!__all_sync(kFull, mbar_wait(bar(BAR_V_EMPTY + ((t - 1) & 1)), ((t - 1) >> 1) & 1)))
-              failed = true;
-            fence_after();
-          }
-#pragma unroll
-          for (int u = ua; u < ub; ++u) {
-            float* x = v + 8 * (u - ua);
-            const int nq = u < NO ? 2 : 1;
-            const int c = u < NO ? 8 * WG * u + c_oct : c_quad;
-            const int li = u < NO ? 4 * u : 4 * NO;
-#pragma unroll
-            for (int j = 0; j < nq; ++j) {
-              const float4 sh = *(const float4*)(shiftv + c + 4 * j);
-              const float4 al = *(const float4*)(alpha + c + 4 * j);
-              x[4 * j] -= sh.x;
-              x[4 * j + 1] -= sh.y;
-              x[4 * j + 2] -= sh.z;
-              x[4 * j + 3] -= sh.w;
-              l2[li + 2 * j] = __fmul2_rn(l2[li + 2 * j], make_float2(al.x, al.y));
-              l2[li + 2 * j + 1] = __fmul2_rn(l2[li + 2 * j + 1], make_float2(al.z, al.w));
-            }
-            if (t > 0 && !failed) {
-              float o[8];
-              const uint32_t ta = tm_o + lane_off + (uint32_t)c;
-              if (u < NO) tmem_ld8(ta, o);
-              else tmem_ld4(ta, o[0], o[1], o[2], o[3]);
+            for (int c = 0; c < 64; c += 32) {
+              float v[32];
+              tmem_ld32(ts + 64 * h + c, v);
               tmem_wait_ld();
 #pragma unroll
-              for (int j = 0; j < nq; ++j) {
-                const float4 al = *(const float4*)(alpha + c + 4 * j);
-                o[4 * j] *= al.x;
-                o[4 * j + 1] *= al.y;
-                o[4 * j + 2] *= al.z;
-                o[4 * j + 3] *= al.w;
+              for (int i = 0; i < 32; i += 4) {
+                ta = max3f(ta, v[i], v[i + 1]);
+                tb = max3f(tb, v[i + 2], v[i + 3]);
               }
-              if (u < NO) tmem_st8(ta, o);
-              else tmem_st4(ta, o[0], o[1], o[2], o[3]);
             }
+            top[h] = fmaxf(ta, tb);
           }
-          tmem_wait_st();
-        }
-        if (!p_free) {
-          if (!__all_sync(kFull, mbar_wait(bar(BAR_V_EMPTY + st), ((t - 2) >> 1) & 1))) failed = true;
-          p_free = true;
-        }
-        // p = 2^x, its sums, and the P^T row of this key
+          raise(fmaxf(top[0] * f0, top[1] * f1), t < 2);
+          const float mm = m == -INFINITY ? 0.f : m;
 #pragma unroll
-        for (int u = ua; u < ub; ++u) {
-          const float* x = v + 8 * (u - ua);
-          const int li = u < NO ? 4 * u : 4 * NO;
-          const int np = u < NO ? 4 : 2;
-          uint32_t w[4];
+          for (int h = 0; h < 2; ++h) {
+            const float f = h == 0 ? f0 : f1, off = (float)(h == 0 ? d0 : d1) - mm;
+            const float2 f2 = make_float2(f, f), o2 = make_float2(off, off);
+            float2 sa = make_float2(0.f, 0.f), sb = sa;
 #pragma unroll
-          for (int i = 0; i < np; ++i) {
-            const float2 p = make_float2(ex2(x[2 * i]), ex2(x[2 * i + 1]));
-            l2[li + i] = __fadd2_rn(l2[li + i], p);
-            const float2 pv = __fmul2_rn(p, fv2);
-            w[i] = pack_half2(pv.x, pv.y);
+            for (int c = 0; c < 64; c += 32) {
+              float v[32];
+              uint32_t w[16];
+              tmem_ld32(ts + 64 * h + c, v);
+              tmem_wait_ld();
+#pragma unroll
+              for (int i = 0; i < 32; i += 4) {
+                const float2 xa = __ffma2_rn(make_float2(v[i], v[i + 1]), f2, o2);
+                const float2 xb = __ffma2_rn(make_float2(v[i + 2], v[i + 3]), f2, o2);
+                const float2 pa = make_float2(ex2(xa.x), ex2(xa.y));
+                const float2 pb = make_float2(ex2(xb.x), ex2(xb.y));
+                sa = __fadd2_rn(sa, pa);
+                sb = __fadd2_rn(sb, pb);
+                w[i / 2] = pack_half2(pa.x, pa.y);
+                w[i / 2 + 1] = pack_half2(pb.x, pb.y);
+              }
+              tmem_st16(ts + 32 * h + c / 2, w);
+            }
+            l = fmaf((sa.x + sa.y) + (sb.x + sb.y), pow2i(h == 0 ? -d0 : -d1), l);
           }
-          if (!failed) {
-            if (u < NO) *(uint4*)(pt + pt_oct + 2048u * WG * u) = make_uint4(w[0], w[1], w[2], w[3]);
-            else *(uint2*)(pt + pt_quad) = make_uint2(w[0], w[1]);
+        } else {
+          // the scratch rows, or a tile that the prefix does not fill: a factor
+          // per key, and masks
+          auto factor = [&](int key) {
+            return is_tree ? kt_out[key] : q8_scale(kex[2 * t + (key >> 6)]);
+          };
+          auto score = [&](float s, int key) {
+            const bool sees = key < nvalid &&
+                              (!is_tree || key == 0 || (((mask >> ((key - 1) & 63)) & 1ull) != 0));
+            return sees ? s * (c2 * factor(key)) : -INFINITY;
+          };
+          float top = -INFINITY;
+#pragma unroll 1
+          for (int c = 0; c < nvalid; c += 32) {
+            float v[32];
+            tmem_ld32(ts + c, v);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) top = fmaxf(top, score(v[i], c + i));
+          }
+          raise(top, t < 2);
+          const float mm = m == -INFINITY ? 0.f : m;
+#pragma unroll 1
+          for (int c = 0; c < kKeys; c += 32) {
+            uint32_t w[16];
+            if (c < nvalid) {
+              float v[32];
+              tmem_ld32(ts + c, v);
+              tmem_wait_ld();
+#pragma unroll
+              for (int i = 0; i < 32; i += 2) {
+                float pv[2];
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                  const int key = c + i + j;
+                  const float pr = ex2(score(v[i + j], key) - mm);
+                  const int u = is_tree ? vt_u[key] : (int)vex[2 * t + (key >> 6)] - 127;
+                  l += pr;
+                  pv[j] = pr * pow2i(u - U + kHeadroom);
+                }
+                w[i / 2] = pack_half2(pv[0], pv[1]);
+              }
+            } else {
+#pragma unroll
+              for (int i = 0; i < 16; ++i) w[i] = 0u;
+            }
+            tmem_st16(ts + c / 2, w);
           }
         }
+        tmem_wait_st();
+        fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(BAR_P_FULL + p));
       }
-      if (stop_now) {
-        failed = true;
-        break;
-      }
-      asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
-      fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(BAR_P_FULL + st));
     }
 
-    // ---------------------------------------------------------- epilogue
-    failed = __any_sync(kFull, failed);
+    // ------------------------------------- epilogue: the two streams joined
     const bool ok = !failed && __all_sync(kFull, mbar_wait(bar(BAR_O_DONE), 0));
     fence_after();
-    const bool stop = wg_bar_or(wg, !ok || flags[1] != 0);
-    if (!stop) {
-#pragma unroll
-      for (int i = 0; i < NH / 4; ++i) {
-        float r4[4] = {l2[2 * i].x, l2[2 * i].y, l2[2 * i + 1].x, l2[2 * i + 1].y};
-        const float r = warp_reduce_scatter<4, false>(r4, lane);
-        if (lane < 4) red[warp * NH + 4 * i + lane] = r;
+    s_ml[p * kRows + row] = make_float2(m, l);
+    uint32_t stop;
+    asm volatile(
+        "{\n .reg .pred pi, po;\n setp.ne.u32 pi, %1, 0;\n"
+        " bar.red.or.pred po, 1, 256, pi;\n selp.u32 %0, 1, 0, po;\n}\n"
+        : "=r"(stop)
+        : "r"((uint32_t)(!ok || flags[1] != 0))
+        : "memory");
+    if (stop == 0 && q < live_warps) {
+      const float2 s0 = s_ml[row], s1 = s_ml[kRows + row];
+      const float top = fmaxf(s0.x, s1.x);
+      const float w0 = s0.x == -INFINITY ? (s0.y != s0.y ? s0.y : 0.f) : ex2(s0.x - top);
+      const float w1 = s1.x == -INFINITY ? (s1.y != s1.y ? s1.y : 0.f) : ex2(s1.x - top);
+      const float total = w0 * s0.y + w1 * s1.y;
+      const float unit = pow2i(U), inv = pow2i(-kHeadroom) / total;
+      const float g0 = w0 * inv, g1 = w1 * inv;
+      const float lse2 = top + log2f(total);
+      const int pr = row_base + min(row, rows_here - 1);
+      const int tr = pr / a.g, qh = hk * a.g + pr % a.g;
+      const long orow = ((long)b * a.R + tr) * a.Hq + qh;
+      const long prow = (((long)b * a.Hq + qh) * a.R + tr) * a.nsplit + sp;
+      const bool mine = row < rows_here;
+      if (mine && p == 0) {
+        if (nsb == 1) a.lse[orow] = lse2 * 0.69314718055994531f;
+        else a.part_meta[prow] = make_float2(lse2, unit);
       }
-      wg_bar(wg);
-      const float unit = pow2i(U);
-      for (int n = tid & 127; n < NH; n += 128) {
-        const int col = L::col(n, wg);
-        float ls = 0.f;
-#pragma unroll
-        for (int w = 0; w < 4; ++w) ls += red[(wg * 4 + w) * NH + n];
-        alpha[col] = pow2i(-kHeadroom) / ls;
-        if (col < rows_here) {
-          const int p = row_base + col;
-          const int tr = p / a.g, qh = hk * a.g + p % a.g;
-          const float lse2 = m_run[col] + log2f(ls);
-          if (nsb == 1) {
-            const long orow = ((long)b * a.R + tr) * a.Hq + qh;
-            ooff[col] = orow * D;
-            a.lse[orow] = lse2 * 0.69314718055994531f;
-          } else {
-            const long prow = (((long)b * a.Hq + qh) * a.R + tr) * a.nsplit + sp;
-            ooff[col] = prow * D;
-            a.part_meta[prow] = make_float2(lse2, unit);
-          }
-        }
-      }
-      wg_bar(wg);
-      // O^T lane = dim.  A split's output, over 2^U, is a mean of numbers of
-      // magnitude < 512: fp16 holds it to 2^-12.
-      const int d = key;
-#pragma unroll
-      for (int u = 0; u < NU; ++u) {
-        float o[8];
-        const int c = u < NO ? 8 * WG * u + c_oct : c_quad;
-        if (u < NO) tmem_ld8(tm_o + lane_off + (uint32_t)c, o);
-        else tmem_ld4(tm_o + lane_off + (uint32_t)c, o[0], o[1], o[2], o[3]);
+      // stream p writes the dims [p D/2, (p + 1) D/2).  A split's output, over
+      // 2^U, is a mean of numbers of magnitude < 512: fp16 holds it to 2^-12.
+#pragma unroll 1
+      for (int c = p * (D / 2); c < (p + 1) * (D / 2); c += 32) {
+        float o0[32], o1[32];
+        tmem_ld32(tm_o(0) + lane_off + c, o0);
+        if (ntiles > 1) tmem_ld32(tm_o(1) + lane_off + c, o1);
         tmem_wait_ld();
-        if (D == 64 && d >= D) continue;     // (whole warps: lanes 64..127)
+        if (ntiles < 2) {
 #pragma unroll
-        for (int e = 0; e < (u < NO ? 8 : 4); ++e) {
-          const int col = c + e;
-          if (col >= rows_here) continue;
-          const float res = o[e] * alpha[col];
-          if (nsb == 1) ((__nv_bfloat16*)a.out)[ooff[col] + d] = __float2bfloat16_rn(res * unit);
-          else ((__half*)a.part_o)[ooff[col] + d] = __float2half_rn(res);
+          for (int i = 0; i < 32; ++i) o1[i] = 0.f;
+        }
+        uint32_t w[16];
+#pragma unroll
+        for (int i = 0; i < 32; i += 2) {
+          const float x = o0[i] * g0 + o1[i] * g1, y = o0[i + 1] * g0 + o1[i + 1] * g1;
+          w[i / 2] = nsb == 1 ? pack_bf16x2(x * unit, y * unit) : pack_half2(x, y);
+        }
+        if (mine) {
+          uint4* dst = nsb == 1 ? (uint4*)((__nv_bfloat16*)a.out + orow * D + c)
+                                : (uint4*)((__half*)a.part_o + prow * D + c);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            dst[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
         }
       }
     }
@@ -862,62 +606,28 @@ q8_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ Q
   __syncthreads();
   if (flags[1] && tid == 0) report_error(a.err, TSD_DEV_ERR_TIMEOUT, b);
   fence_after();
-  if (warp == kMmaWarp) {
+  if (warp == kMma) {
     __syncwarp();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;\n" ::"r"(tmem));
   }
 }
 
-template <int N, int D, int WG, int WW, int VD>
-void launch_n(const CUtensorMap& kmap, const Q8AttnArgs& a, const Q8Plan& p, cudaStream_t st) {
-  using L = Q8Layout<N, D, WG, WW>;
-  const uint32_t smem = L::total + 1024;
-  const auto kern = q8_tc_kernel<N, D, WG, WW, VD>;
-  cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  launch(kern, dim3(a.map.Hkv * p.nrg, p.nsplit, a.B), dim3(L::threads), smem, st, kmap, a);
-}
-
-// K codes as (dims, rows of a head, heads): rows are those of a request's head,
-// or of a page's.
-bool encode_keys(CUtensorMap* m, const Q8AttnArgs& a, int D) {
-  const long rows = a.map.page_size > 0 ? a.map.page_size : a.map.cap;
-  const long heads = (a.map.page_size > 0 ? (long)a.map.num_pages : (long)a.B) * a.map.Hkv;
-  if (heads > 0x7fffffffl) return false;
-  const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)rows, (cuuint64_t)heads};
-  const cuuint64_t strides[2] = {(cuuint64_t)D, (cuuint64_t)rows * D};
-  const cuuint32_t box[3] = {(cuuint32_t)D, (cuuint32_t)kKeys, 1};
-  const cuuint32_t es[3] = {1, 1, 1};
-  return encode_fn()(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<uint8_t*>(a.kc), dims, strides,
-                     box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                     D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
-                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-// Softmax warpgroups: one per 32 columns or so, so that its fixed work per tile
-// (waits, one barrier) is shared by many columns and a thread's sums and scores
-// stay in registers; widening warps and tiles in flight: what is left of the
-// registers.
 template <int D>
-bool launch_d(const CUtensorMap& m, const Q8AttnArgs& a, const Q8Plan& p, cudaStream_t st) {
-  switch (p.rb) {
-    case 16: launch_n<16, D, 1, 8, 2>(m, a, p, st); return true;
-    case 32: launch_n<32, D, 1, 8, 2>(m, a, p, st); return true;
-    case 48: launch_n<48, D, 2, 6, 1>(m, a, p, st); return true;
-    case 64: launch_n<64, D, 2, 6, 1>(m, a, p, st); return true;
-    case 80: launch_n<80, D, 4, 6, 1>(m, a, p, st); return true;
-    case 96: launch_n<96, D, 4, 6, 1>(m, a, p, st); return true;
-    case 112: launch_n<112, D, 4, 6, 1>(m, a, p, st); return true;
-  }
-  return false;
+void launch_rows(const CUtensorMap& kmap, const Q8AttnArgs& a, const Q8Plan& p, cudaStream_t st) {
+  const uint32_t smem = RowLayout<D>::total + 1024;
+  const auto kern = q8_rows_kernel<D>;
+  cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  launch(kern, dim3(a.map.Hkv * p.nrg, p.nsplit, a.B), dim3(kThreads), smem, st, kmap, a);
 }
 
 }  // namespace
 
-bool launch_q8_tc(const tsd_attn_desc& d, const Q8AttnArgs& a, const Q8Plan& p, cudaStream_t st) {
+bool launch_q8_rows(const tsd_attn_desc& d, const Q8AttnArgs& a, const Q8Plan& p, cudaStream_t st) {
   CUtensorMap m;
   if (encode_fn() == nullptr || !encode_keys(&m, a, d.dk)) return false;
-  return d.dk == 128 ? launch_d<128>(m, a, p, st) : launch_d<64>(m, a, p, st);
+  if (d.dk == 128) launch_rows<128>(m, a, p, st);
+  else launch_rows<64>(m, a, p, st);
+  return true;
 }
 
 }  // namespace tsd

@@ -1,0 +1,257 @@
+// Device pieces of the two tcgen05 paths over the 8-bit cache: 8-bit products,
+// operand layouts, the exact splits and scalings of bf16 rows, streaming loads;
+// and the host's tensor map of the K codes.
+#pragma once
+
+#include <cuda.h>
+
+#include "tsd_q8_attn.cuh"
+#include "tsd_tcgen05.cuh"
+
+namespace tsd {
+namespace {
+
+constexpr int kKeys = 128;                      // keys per tile
+constexpr uint32_t kHalf = kKeys * 128;         // [128 rows][64 fp16]: 16 KB
+constexpr uint32_t kTile = 2 * kHalf;           // a widened V tile
+constexpr int kRing = 4;                        // K tiles in shared memory
+constexpr float kOverflow = 8.0f;               // log2 headroom of the lazy maximum
+constexpr int kHeadroom = 7;                    // P's offset: 2^8 * 2^7 < 65504
+constexpr int kMaxTiles = 256;                  // prefix tiles of a split
+constexpr int kPrefetch = 4;                    // tiles that V's L2 prefetch runs ahead
+
+// D (+)= A.B, 8-bit operands (e4m3), K = 32 per instruction.
+__device__ __forceinline__ void mma_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                       uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(acc));
+}
+
+// Byte offset of 16-byte unit u of row r in a K-major tile of D-byte rows
+// (128-byte swizzle for D = 128, 64-byte swizzle for D = 64), and the matrix
+// descriptor of such a tile.
+template <int D>
+__device__ __forceinline__ uint32_t unit_offset(int r, int u) {
+  return D == 128 ? r * 128 + ((u ^ (r & 7)) << 4) : r * 64 + ((u ^ ((r >> 1) & 3)) << 4);
+}
+template <int D>
+__device__ __forceinline__ uint64_t row_desc(uint32_t addr) {
+  if (D == 128) return smem_desc(addr, 16, 1024);
+  return (uint64_t)((addr >> 4) & 0x3FFF) | ((uint64_t)1 << 16) | ((uint64_t)(512 >> 4) << 32) |
+         (1ull << 46) | (4ull << 61);
+}
+
+// Sixteen bf16 times f as e4m3 numbers hi and lo with hi + lo = x f.
+__device__ __forceinline__ void split16(const uint4 (&w)[2], float f, uint4& hi, uint4& lo) {
+  uint32_t h[4], l[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint4& s = w[i >> 1];
+    const uint32_t a = (i & 1) ? s.z : s.x, b = (i & 1) ? s.w : s.y;
+    const float x[4] = {__uint_as_float(a << 16) * f, __uint_as_float(a & 0xffff0000u) * f,
+                        __uint_as_float(b << 16) * f, __uint_as_float(b & 0xffff0000u) * f};
+    float y[4];
+    h[i] = q8_pack4(x[0], x[1], x[2], x[3]);
+    q8_unpack4(h[i], y);
+    l[i] = q8_pack4(x[0] - y[0], x[1] - y[1], x[2] - y[2], x[3] - y[3]);
+  }
+  hi = make_uint4(h[0], h[1], h[2], h[3]);
+  lo = make_uint4(l[0], l[1], l[2], l[3]);
+}
+
+__device__ __forceinline__ uint4 ld_stream(const uint8_t* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];\n"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
+  const __half2 v = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+// Largest finite magnitude of eight bf16 (bits, as the high half of an fp32),
+// and whether one is not finite.
+__device__ __forceinline__ void scan8(const uint4& w, uint32_t& top, bool& bad) {
+  const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t a = (v[i] << 16) & 0x7fffffffu, b = v[i] & 0x7fff0000u;
+    bad |= a >= 0x7f800000u || b >= 0x7f800000u;
+    top = max(top, max(a >= 0x7f800000u ? 0u : a, b >= 0x7f800000u ? 0u : b));
+  }
+}
+// Eight bf16 times f as fp16.
+__device__ __forceinline__ uint4 scale8(const uint4& w, float f) {
+  uint4 r;
+  r.x = pack_half2(__uint_as_float(w.x << 16) * f, __uint_as_float(w.x & 0xffff0000u) * f);
+  r.y = pack_half2(__uint_as_float(w.y << 16) * f, __uint_as_float(w.y & 0xffff0000u) * f);
+  r.z = pack_half2(__uint_as_float(w.z << 16) * f, __uint_as_float(w.z & 0xffff0000u) * f);
+  r.w = pack_half2(__uint_as_float(w.w << 16) * f, __uint_as_float(w.w & 0xffff0000u) * f);
+  return r;
+}
+// fp32 exponent field of a row's largest magnitude, at least 15 so that both
+// the scale and its inverse are normal numbers.
+__device__ __forceinline__ int row_exponent(uint32_t top) { return max((int)(top >> 23), 15); }
+
+// Scratch rows of (request b, head hk): eight lanes of the n threads per row.
+// Which ones some row sees, their factors, and (returned) this thread's largest
+// exponent of a value row.
+template <int D>
+__device__ __forceinline__ int scan_tree(const Q8AttnArgs& a, int b, int hk, int wt, int n,
+                                         float* kt_in, float* vt_in, float* kt_out, int* vt_u) {
+  const int lane = threadIdx.x & 31;
+  int best = -1000;
+  uint32_t lo = 0, hi = 0;
+  for (int r = lane; r < a.R; r += 32) {
+    const uint64_t m = r > 0 ? a.mask[(long)b * a.R + r] : 0ull;
+    lo |= (uint32_t)m;
+    hi |= (uint32_t)(m >> 32);
+  }
+  lo = __reduce_or_sync(kFull, lo);
+  hi = __reduce_or_sync(kFull, hi);
+  const uint64_t seen = ((uint64_t)hi << 32) | lo;
+  for (int x = wt; x < kKeys * 8; x += n) {
+    const int j = x >> 3, c = x & 7;
+    const bool live = j < a.R && (j == 0 || ((seen >> (j - 1)) & 1ull));
+    uint32_t kt = 0, vt = 0;
+    bool bad = false;
+    if (live) {
+      const long row = ((long)b * a.R + j) * a.map.Hkv + hk;
+      const uint4* kp = (const uint4*)((const __nv_bfloat16*)a.kt + row * D) + c * (D / 64);
+      const uint4* vp = (const uint4*)((const __nv_bfloat16*)a.vt + row * D) + c * (D / 64);
+#pragma unroll
+      for (int i = 0; i < D / 64; ++i) {
+        scan8(__ldg(kp + i), kt, bad);
+        scan8(__ldg(vp + i), vt, bad);
+      }
+    }
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) {
+      kt = max(kt, __shfl_xor_sync(kFull, kt, o));
+      vt = max(vt, __shfl_xor_sync(kFull, vt, o));
+    }
+    const uint32_t any = __ballot_sync(kFull, bad);
+    bad = (any >> (lane & 24)) & 0xffu;
+    const int ek = row_exponent(kt), ev = row_exponent(vt);
+    if (c == 0) {
+      // K: 2^(7 - (e - 127)) and its inverse; V: 2^(8 - (e - 127))
+      kt_in[j] = live && !bad ? q8_scale(261 - ek) : 0.f;
+      vt_in[j] = live && !bad ? q8_scale(262 - ev) : 0.f;
+      kt_out[j] = bad ? __int_as_float(0x7fffffff) : q8_scale(ek - 7);
+      vt_u[j] = live ? ev - 135 : -900;
+    }
+    if (live) best = max(best, ev - 135);
+  }
+  return best;
+}
+
+// The packed rows of a row group as hi + lo (n_rows of them, zeros behind the
+// last one) with their score factors: D / 16 lanes of the n threads per row.
+template <int D>
+__device__ __forceinline__ void stage_q(const Q8AttnArgs& a, int b, int hk, int row_base,
+                                        int rows_here, int n_rows, int tid, int n, uint8_t* hi_tile,
+                                        uint8_t* lo_tile, float* c2v) {
+  constexpr int QL = D / 16;
+  const int lane = threadIdx.x & 31;
+  for (int x = tid; x < n_rows * QL; x += n) {       // (whole warps: n_rows is a multiple of 16)
+    const int r = x / QL, c = x % QL;
+    uint4 w[2] = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
+    uint32_t top = 0;
+    bool bad = false;
+    if (r < rows_here) {
+      const int p = row_base + r;
+      const int tr = p / a.g, qh = hk * a.g + p % a.g;
+      const uint4* qp =
+          (const uint4*)((const __nv_bfloat16*)a.q + (((long)b * a.R + tr) * a.Hq + qh) * D) + 2 * c;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        w[i] = __ldg(qp + i);
+        scan8(w[i], top, bad);
+      }
+    }
+#pragma unroll
+    for (int o = QL / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(kFull, top, o));
+    const uint32_t any = __ballot_sync(kFull, bad);
+    bad = (any >> (lane & (32 - QL))) & ((1u << QL) - 1u);
+    const int e = row_exponent(top);
+    uint4 hi = make_uint4(0u, 0u, 0u, 0u), lo = hi;
+    if (!bad) split16(w, q8_scale(261 - e), hi, lo);
+    *(uint4*)(hi_tile + unit_offset<D>(r, c)) = hi;
+    *(uint4*)(lo_tile + unit_offset<D>(r, c)) = lo;
+    if (c == 0) c2v[r] = bad ? __int_as_float(0x7fffffff) : a.qscale * q8_scale(e - 7);
+  }
+}
+
+// The scratch rows' keys as hi + lo, and their values as fp16; rows that nobody
+// sees are zeros.
+template <int D>
+__device__ __forceinline__ void tree_keys(const Q8AttnArgs& a, int b, int hk, int wt, int n,
+                                          const float* kt_in, uint8_t* hi_tile, uint8_t* lo_tile) {
+  for (int x = wt; x < kKeys * (D / 16); x += n) {
+    const int row = x / (D / 16), u = x % (D / 16);
+    uint4 hi = make_uint4(0u, 0u, 0u, 0u), lo = hi;
+    const float f = kt_in[row];
+    if (f != 0.f) {
+      const uint4* p = (const uint4*)((const __nv_bfloat16*)a.kt +
+                                      (((long)b * a.R + row) * a.map.Hkv + hk) * D) + 2 * u;
+      const uint4 w[2] = {__ldg(p), __ldg(p + 1)};
+      split16(w, f, hi, lo);
+    }
+    *(uint4*)(hi_tile + unit_offset<D>(row, u)) = hi;
+    *(uint4*)(lo_tile + unit_offset<D>(row, u)) = lo;
+  }
+}
+template <int D>
+__device__ __forceinline__ void tree_values(const Q8AttnArgs& a, int b, int hk, int wt, int n,
+                                            const float* vt_in, uint8_t* stage) {
+  for (int x = wt; x < kKeys * (D / 8); x += n) {
+    const int row = x / (D / 8), u = x % (D / 8);
+    const float f = vt_in[row];
+    uint4 v = make_uint4(0u, 0u, 0u, 0u);
+    if (f != 0.f)
+      v = scale8(__ldg((const uint4*)((const __nv_bfloat16*)a.vt +
+                                      (((long)b * a.R + row) * a.map.Hkv + hk) * D) + u), f);
+    *(uint4*)(stage + (u >> 3) * kHalf + row * 128 + (((u & 7) ^ (row & 7)) << 4)) = v;
+  }
+}
+
+// The K tile of positions pos.. by TMA (cache row `row`, for a paged cache).  A
+// tile behind the cache's or page's last row reads zeros there; rows behind the
+// prefix are masked later, whatever they hold; the rows of a missing page are
+// those of page 0.
+__device__ __forceinline__ void load_keys(const Q8AttnArgs& a, const CUtensorMap& kmap, int b,
+                                          int hk, int pos, long long row, uint32_t dst,
+                                          uint32_t bytes, uint32_t full) {
+  int y = pos, z = b * a.map.Hkv + hk;
+  if (a.map.page_size) {
+    const long long r = row < 0 ? 0 : row;
+    y = (int)(r % a.map.page_size);
+    z = (int)(r / a.map.page_size);
+  }
+  mbar_expect_tx(full, bytes);
+  tma_3d(dst, &kmap, 0, y, z, full);
+}
+
+// K codes as (dims, rows of a head, heads): rows are those of a request's head,
+// or of a page's.
+bool encode_keys(CUtensorMap* m, const Q8AttnArgs& a, int D) {
+  const long rows = a.map.page_size > 0 ? a.map.page_size : a.map.cap;
+  const long heads = (a.map.page_size > 0 ? (long)a.map.num_pages : (long)a.B) * a.map.Hkv;
+  if (heads > 0x7fffffffl) return false;
+  const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)rows, (cuuint64_t)heads};
+  const cuuint64_t strides[2] = {(cuuint64_t)D, (cuuint64_t)rows * D};
+  const cuuint32_t box[3] = {(cuuint32_t)D, (cuuint32_t)kKeys, 1};
+  const cuuint32_t es[3] = {1, 1, 1};
+  return encode_fn()(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<uint8_t*>(a.kc), dims, strides,
+                     box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                     D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace
+
+}  // namespace tsd
