@@ -57,7 +57,7 @@
 namespace tsd {
 namespace {
 
-constexpr int kMma = 8, kTma = 9, kWide = 10, kWideWarps = 6;
+constexpr int kPv = 8, kQk = 10, kTma = 12, kWide = 13, kWideWarps = 7;
 constexpr int kWideThreads = kWideWarps * 32;
 constexpr int kThreads = (kWide + kWideWarps) * 32;
 constexpr int kStages = 3;                      // widened V tiles
@@ -77,17 +77,19 @@ struct RowLayout {
   static constexpr uint32_t off_kex = off_tree + 16 * kKeys;           // u8[2 kMaxTiles]
   static constexpr uint32_t off_vex = off_kex + 2 * kMaxTiles;
   static constexpr uint32_t off_bar = off_vex + 2 * kMaxTiles;
-  static constexpr int nbar = 21;
+  static constexpr int nbar = 32;
   static constexpr uint32_t off_flags = off_bar + 8 * nbar;            // tmem, abort, U
   static constexpr uint32_t total = off_flags + 16;
   static_assert(total + 1024 <= 232448, "shared memory budget");
 };
 
-// FULL: the copy landed or the warps wrote; EMPTY: read by the product (V_EMPTY
-// is also the end of a tile's O product); T_FULL: the scratch rows' keys, which
-// take the two K slots behind the last prefix tile (hi, lo).
+// FULL: the copy landed, the warps wrote or the product is done; EMPTY: read by
+// the product.  S_FULL, P_FULL and PV_DONE: one per stream and half tile (index 2
+// p + h).  T_FULL: the scratch rows' keys, which take the two K slots behind the
+// last prefix tile (hi, lo).
 enum { BAR_K_FULL = 0, BAR_K_EMPTY = 4, BAR_V_FULL = 8, BAR_V_EMPTY = 11, BAR_S_FULL = 14,
-       BAR_P_FULL = 16, BAR_FINAL = 18, BAR_O_DONE = 19, BAR_T_FULL = 20 };
+       BAR_P_FULL = 18, BAR_PV_DONE = 22, BAR_O_DONE = 26, BAR_T_FULL = 27,
+       BAR_FINAL = 28 };                        // one per issuing warp
 
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32]) {
   uint32_t r[32];
@@ -162,7 +164,7 @@ q8_rows_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
   auto valid_of = [&](int t) { return min(kKeys, k1 - (k0 + t * kKeys)); };
 
   // ---------------------------------------------------------------- set-up
-  if (tid == kMma * 32) {
+  if (tid == kPv * 32) {
     for (int i = 0; i < kRing; ++i) {
       mbar_init(bar(BAR_K_FULL + i), 1);
       mbar_init(bar(BAR_K_EMPTY + i), 1);
@@ -171,18 +173,19 @@ q8_rows_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
       mbar_init(bar(BAR_V_FULL + i), kWideWarps);
       mbar_init(bar(BAR_V_EMPTY + i), 1);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < 4; ++i) {
       mbar_init(bar(BAR_S_FULL + i), 1);
       mbar_init(bar(BAR_P_FULL + i), live_warps);
+      mbar_init(bar(BAR_PV_DONE + i), 1);
     }
-    mbar_init(bar(BAR_FINAL), 1);
-    mbar_init(bar(BAR_O_DONE), 1);
+    for (int i = 0; i < 4; ++i) mbar_init(bar(BAR_FINAL + i), 1);
+    mbar_init(bar(BAR_O_DONE), min(ntiles, 2));
     mbar_init(bar(BAR_T_FULL), kWideWarps);
     flags[1] = 0;
     *s_top = -1000;
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
   }
-  if (warp == kMma) {
+  if (warp == kPv) {
     __syncwarp();
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;\n" ::"r"(
         sbase + L::off_flags));
@@ -325,62 +328,79 @@ q8_rows_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
     }
   }
 
-  // ------------------------------------------------------------------ MMA
-  else if (warp == kMma) {
+  // ------------------------------------------------------ scores: warp kQk + p
+  // A stream's two half tiles (64 keys) are two products and two buffers: while
+  // the softmax works on one, the other is multiplied by V and filled again.
+  else if (warp >= kQk) {
     if (lane == 0) {
-      // fp32 accumulators; e4m3 (S) and fp16 (O) operands are both format 0
-      const uint32_t idesc_qk =
-          (1u << 4) | ((uint32_t)(kKeys >> 3) << 17) | ((uint32_t)(kRows >> 4) << 24);
-      const uint32_t idesc_pv =
-          (1u << 4) | (1u << 16) | ((uint32_t)(D >> 3) << 17) | ((uint32_t)(kRows >> 4) << 24);
+      const int p = warp - kQk;
+      // fp32 accumulator; e4m3 operands are format 0
+      const uint32_t idesc =
+          (1u << 4) | ((uint32_t)(64 >> 3) << 17) | ((uint32_t)(kRows >> 4) << 24);
       const uint64_t kd0 = row_desc<D>(sbase + L::off_k);
       const uint64_t qd0 = row_desc<D>(sbase + L::off_q);
-      const uint64_t vd0 = smem_desc(sbase + L::off_v, kHalf, 1024);
-      // S (+)= (Q hi + Q lo) x K slot
-      auto products = [&](uint32_t ts, int sl, bool first) {
-        const uint64_t kd = kd0 + (uint64_t)(sl * (L::k_bytes >> 4));
+      // S (+)= (Q hi + Q lo) x half h of a K slot
+      auto products = [&](uint32_t ts, int sl, int h, bool first) {
+        const uint64_t kd = kd0 + (uint64_t)((sl * L::k_bytes + h * 64 * D) >> 4);
 #pragma unroll
         for (int part = 0; part < 2; ++part)
 #pragma unroll
           for (int kk = 0; kk < D / 32; ++kk)
-            mma_f8(ts, qd0 + (uint64_t)(part * (L::q_bytes >> 4)) + 2 * kk, kd + 2 * kk, idesc_qk,
+            mma_f8(ts, qd0 + (uint64_t)(part * (L::q_bytes >> 4)) + 2 * kk, kd + 2 * kk, idesc,
                    first && part == 0 && kk == 0 ? 0u : 1u);
       };
-      auto issue_qk = [&](int t) -> bool {
+      bool ok = true;
+      for (int t = p; ok && t < ntiles; t += 2) {
         const int sl = t % kRing;
-        if (!(t < n_pre ? mbar_wait(bar(BAR_K_FULL + sl), (t / kRing) & 1)
-                        : mbar_wait(bar(BAR_T_FULL), 0)))
-          return false;
-        fence_after();
-        products(tm_s(t & 1), sl, true);
-        if (t >= n_pre) products(tm_s(t & 1), (t + 1) % kRing, false);
-        mma_commit(bar(BAR_S_FULL + (t & 1)));
-        mma_commit(bar(BAR_K_EMPTY + sl));
-        return true;
-      };
-      bool ok = issue_qk(0) && (ntiles < 2 || issue_qk(1));
-      for (int t = 0; ok && t < ntiles; ++t) {
-        const int p = t & 1, st = t % kStages;
-        if (!mbar_wait(bar(BAR_P_FULL + p), (t >> 1) & 1) || flags[1] ||
-            !mbar_wait(bar(BAR_V_FULL + st), (t / kStages) & 1)) {
-          ok = false;
-          break;
-        }
-        fence_after();
-        const uint64_t vd = vd0 + (uint64_t)(st * (L::v_bytes >> 4));
+        ok = t < n_pre ? mbar_wait(bar(BAR_K_FULL + sl), (t / kRing) & 1)
+                       : mbar_wait(bar(BAR_T_FULL), 0);
 #pragma unroll
-        for (int kk = 0; kk < kKeys / 16; ++kk)
-          mma_f16_ta(tm_o(p), tm_s(p) + 8 * kk, vd + 128 * kk, idesc_pv, t < 2 && kk == 0 ? 0u : 1u);
-        mma_commit(bar(BAR_V_EMPTY + st));
-        if (t == ntiles - 1) mma_commit(bar(BAR_O_DONE));
-        // the next scores of this stream go over P: its product must be done
-        if (t + 2 < ntiles)
-          ok = mbar_wait(bar(BAR_V_EMPTY + st), (t / kStages) & 1) && issue_qk(t + 2);
+        for (int h = 0; ok && h < 2; ++h) {
+          // the scores go over P of the stream's tile before: its product is done
+          if (t >= 2) ok = mbar_wait(bar(BAR_PV_DONE + 2 * p + h), ((t - 2) >> 1) & 1);
+          if (!ok || flags[1]) { ok = false; break; }
+          fence_after();
+          products(tm_s(p) + 64 * h, sl, h, true);
+          if (t >= n_pre) products(tm_s(p) + 64 * h, (t + 1) % kRing, h, false);
+          mma_commit(bar(BAR_S_FULL + 2 * p + h));
+        }
+        if (ok) mma_commit(bar(BAR_K_EMPTY + sl));
       }
       if (!ok) flags[1] = 1;
-      // every product has completed once this commit lands
-      mma_commit(bar(BAR_FINAL));
-      mbar_wait(bar(BAR_FINAL), 0);
+    }
+    __syncwarp();
+  }
+
+  // ----------------------------------------------------- outputs: warp kPv + p
+  else if (warp >= kPv) {
+    if (lane == 0) {
+      const int p = warp - kPv;
+      // fp16 operands are format 0; B (V) is N-major
+      const uint32_t idesc =
+          (1u << 4) | (1u << 16) | ((uint32_t)(D >> 3) << 17) | ((uint32_t)(kRows >> 4) << 24);
+      const uint64_t vd0 = smem_desc(sbase + L::off_v, kHalf, 1024);
+      bool ok = true;
+      for (int t = p; ok && t < ntiles; t += 2) {
+        const int st = t % kStages;
+        const uint64_t vd = vd0 + (uint64_t)(st * (L::v_bytes >> 4));
+        ok = mbar_wait(bar(BAR_V_FULL + st), (t / kStages) & 1);
+#pragma unroll
+        for (int h = 0; ok && h < 2; ++h) {
+          ok = mbar_wait(bar(BAR_P_FULL + 2 * p + h), (t >> 1) & 1) && !flags[1];
+          if (!ok) break;
+          fence_after();
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            mma_f16_ta(tm_o(p), tm_s(p) + 64 * h + 8 * kk, vd + 128 * (4 * h + kk), idesc,
+                       t < 2 && h == 0 && kk == 0 ? 0u : 1u);
+          mma_commit(bar(BAR_PV_DONE + 2 * p + h));
+        }
+        if (ok) {
+          mma_commit(bar(BAR_V_EMPTY + st));
+          if (t + 2 >= ntiles) mma_commit(bar(BAR_O_DONE));
+        }
+      }
+      if (!ok) flags[1] = 1;
     }
     __syncwarp();
   }
@@ -400,81 +420,76 @@ q8_rows_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
         mask = tr > 0 ? a.mask[(long)b * a.R + tr] : 0ull;
       }
       // raise the maximum to X where it passes m by the headroom (or m is
-      // none), and rescale the sum and the accumulator
-      auto raise = [&](float X, bool first) {
+      // none), and rescale the sum and the accumulator; (t, h): the half tile
+      auto raise = [&](float X, int t, int h) -> bool {
         const bool need = !(X <= m + kOverflow);
-        if (!__any_sync(kFull, need)) return;
+        if (!__any_sync(kFull, need)) return true;
         const float m_new = need ? fmaxf(m, X) : m;
         const float al = m_new == m ? 1.f : m == -INFINITY ? 0.f : ex2(m - m_new);
         m = m_new;
         l *= al;
-        if (first) return;
+        if (t < 2 && h == 0) return true;
+        // the products issued so far are done: the half before's is the last
+        if (!__all_sync(kFull, h == 0 ? mbar_wait(bar(BAR_PV_DONE + 2 * p + 1), ((t - 2) >> 1) & 1)
+                                      : mbar_wait(bar(BAR_PV_DONE + 2 * p), (t >> 1) & 1)))
+          return false;
+        fence_after();
 #pragma unroll 1
-        for (int c = 0; c < D; c += 32) {
-          float o[32];
-          tmem_ld32(tm_o(p) + lane_off + c, o);
-          tmem_wait_ld();
+        for (int c = 0; c < D; c += 16) {
+          float o[16];
           uint32_t w[16];
+          tmem_ld8(tm_o(p) + lane_off + c, o);
+          tmem_ld8(tm_o(p) + lane_off + c + 8, o + 8);
+          tmem_wait_ld();
 #pragma unroll
-          for (int half = 0; half < 2; ++half) {
-#pragma unroll
-            for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(o[16 * half + i] * al);
-            tmem_st16(tm_o(p) + lane_off + c + 16 * half, w);
-          }
+          for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(o[i] * al);
+          tmem_st16(tm_o(p) + lane_off + c, w);
         }
         tmem_wait_st();
+        return true;
       };
 
-      for (int t = p; t < ntiles; t += 2) {
-        if (!__all_sync(kFull, mbar_wait(bar(BAR_S_FULL + p), (t >> 1) & 1)) ||
-            __any_sync(kFull, flags[1] != 0)) {
-          failed = true;
-          break;
-        }
-        fence_after();
+      for (int t = p; t < ntiles && !failed; t += 2) {
         const bool is_tree = t >= n_pre;
         const int nvalid = is_tree ? a.R : valid_of(t);
-        if (!is_tree && nvalid == kKeys) {
-          // two blocks of 64 keys: one factor and one offset each
-          const float f0 = c2 * q8_scale(kex[2 * t]), f1 = c2 * q8_scale(kex[2 * t + 1]);
-          // (an offset below -60 puts P under fp16's range: its exact value
-          // does not matter, and the sum stays within fp32)
-          const int d0 = max((int)vex[2 * t] - 127 - U + kHeadroom, -60);
-          const int d1 = max((int)vex[2 * t + 1] - 127 - U + kHeadroom, -60);
-          float top[2];
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            float ta = -INFINITY, tb = -INFINITY;
-#pragma unroll
-            for (int c = 0; c < 64; c += 32) {
-              float v[32];
-              tmem_ld32(ts + 64 * h + c, v);
-              tmem_wait_ld();
-#pragma unroll
-              for (int i = 0; i < 32; i += 4) {
-                ta = max3f(ta, v[i], v[i + 1]);
-                tb = max3f(tb, v[i + 2], v[i + 3]);
-              }
-            }
-            top[h] = fmaxf(ta, tb);
+#pragma unroll 1
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t ts = tm_s(p) + lane_off + 64u * h;
+          if (!__all_sync(kFull, mbar_wait(bar(BAR_S_FULL + 2 * p + h), (t >> 1) & 1)) ||
+              __any_sync(kFull, flags[1] != 0)) {
+            failed = true;
+            break;
           }
-          raise(fmaxf(top[0] * f0, top[1] * f1), t < 2);
-          const float mm = m == -INFINITY ? 0.f : m;
+          fence_after();
+          if (!is_tree && nvalid == kKeys) {
+            // 64 keys of one block: one factor and one offset.  (An offset below
+            // -60 puts P under fp16's range: its exact value does not matter, and
+            // the sum stays within fp32.)
+            const float f = c2 * q8_scale(kex[2 * t + h]);
+            const int d = max((int)vex[2 * t + h] - 127 - U + kHeadroom, -60);
+            float v[64];
+            tmem_ld32(ts, *(float(*)[32])v);
+            tmem_ld32(ts + 32, *(float(*)[32])(v + 32));
+            tmem_wait_ld();
+            float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const float f = h == 0 ? f0 : f1, off = (float)(h == 0 ? d0 : d1) - mm;
+            for (int i = 0; i < 64; i += 8)
+#pragma unroll
+              for (int j = 0; j < 4; ++j) top[j] = max3f(top[j], v[i + 2 * j], v[i + 2 * j + 1]);
+            if (!raise(f * fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])), t, h)) {
+              failed = true;
+              break;
+            }
+            const float off = (float)d - (m == -INFINITY ? 0.f : m);
             const float2 f2 = make_float2(f, f), o2 = make_float2(off, off);
             float2 sa = make_float2(0.f, 0.f), sb = sa;
 #pragma unroll
             for (int c = 0; c < 64; c += 32) {
-              float v[32];
               uint32_t w[16];
-              tmem_ld32(ts + 64 * h + c, v);
-              tmem_wait_ld();
 #pragma unroll
               for (int i = 0; i < 32; i += 4) {
-                const float2 xa = __ffma2_rn(make_float2(v[i], v[i + 1]), f2, o2);
-                const float2 xb = __ffma2_rn(make_float2(v[i + 2], v[i + 3]), f2, o2);
+                const float2 xa = __ffma2_rn(make_float2(v[c + i], v[c + i + 1]), f2, o2);
+                const float2 xb = __ffma2_rn(make_float2(v[c + i + 2], v[c + i + 3]), f2, o2);
                 const float2 pa = make_float2(ex2(xa.x), ex2(xa.y));
                 const float2 pb = make_float2(ex2(xb.x), ex2(xb.y));
                 sa = __fadd2_rn(sa, pa);
@@ -482,63 +497,65 @@ q8_rows_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                 w[i / 2] = pack_half2(pa.x, pa.y);
                 w[i / 2 + 1] = pack_half2(pb.x, pb.y);
               }
-              tmem_st16(ts + 32 * h + c / 2, w);
+              tmem_st16(ts + c / 2, w);
             }
-            l = fmaf((sa.x + sa.y) + (sb.x + sb.y), pow2i(h == 0 ? -d0 : -d1), l);
-          }
-        } else {
-          // the scratch rows, or a tile that the prefix does not fill: a factor
-          // per key, and masks
-          auto factor = [&](int key) {
-            return is_tree ? kt_out[key] : q8_scale(kex[2 * t + (key >> 6)]);
-          };
-          auto score = [&](float s, int key) {
-            const bool sees = key < nvalid &&
-                              (!is_tree || key == 0 || (((mask >> ((key - 1) & 63)) & 1ull) != 0));
-            return sees ? s * (c2 * factor(key)) : -INFINITY;
-          };
-          float top = -INFINITY;
+            l = fmaf((sa.x + sa.y) + (sb.x + sb.y), pow2i(-d), l);
+          } else {
+            // the scratch rows, or a tile that the prefix does not fill: masks,
+            // and for scratch rows a factor per key
+            const int nv = min(max(nvalid - 64 * h, 0), 64);
+            const float fb = is_tree ? 0.f : q8_scale(kex[2 * t + h]);
+            const float vb = is_tree ? 0.f : pow2i((int)vex[2 * t + h] - 127 - U + kHeadroom);
+            auto score = [&](float s, int i) {     // key i of this half
+              const int key = 64 * h + i;
+              const bool sees = i < nv &&
+                                (!is_tree || key == 0 || (((mask >> ((key - 1) & 63)) & 1ull) != 0));
+              return sees ? s * (c2 * (is_tree ? kt_out[key] : fb)) : -INFINITY;
+            };
+            float top = -INFINITY;
 #pragma unroll 1
-          for (int c = 0; c < nvalid; c += 32) {
-            float v[32];
-            tmem_ld32(ts + c, v);
-            tmem_wait_ld();
-#pragma unroll
-            for (int i = 0; i < 32; ++i) top = fmaxf(top, score(v[i], c + i));
-          }
-          raise(top, t < 2);
-          const float mm = m == -INFINITY ? 0.f : m;
-#pragma unroll 1
-          for (int c = 0; c < kKeys; c += 32) {
-            uint32_t w[16];
-            if (c < nvalid) {
-              float v[32];
-              tmem_ld32(ts + c, v);
+            for (int c = 0; c < nv; c += 8) {
+              float v[8];
+              tmem_ld8(ts + c, v);
               tmem_wait_ld();
 #pragma unroll
-              for (int i = 0; i < 32; i += 2) {
-                float pv[2];
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                  const int key = c + i + j;
-                  const float pr = ex2(score(v[i + j], key) - mm);
-                  const int u = is_tree ? vt_u[key] : (int)vex[2 * t + (key >> 6)] - 127;
-                  l += pr;
-                  pv[j] = pr * pow2i(u - U + kHeadroom);
-                }
-                w[i / 2] = pack_half2(pv[0], pv[1]);
-              }
-            } else {
-#pragma unroll
-              for (int i = 0; i < 16; ++i) w[i] = 0u;
+              for (int i = 0; i < 8; ++i) top = fmaxf(top, score(v[i], c + i));
             }
-            tmem_st16(ts + c / 2, w);
+            if (!raise(top, t, h)) {
+              failed = true;
+              break;
+            }
+            const float mm = m == -INFINITY ? 0.f : m;
+#pragma unroll 1
+            for (int c = 0; c < 64; c += 32) {
+              uint32_t w[16];
+#pragma unroll
+              for (int e = 0; e < 32; e += 8) {
+                float v[8];
+                if (c + e < nv) {
+                  tmem_ld8(ts + c + e, v);
+                  tmem_wait_ld();
+#pragma unroll
+                  for (int i = 0; i < 8; ++i) {
+                    const float pr = ex2(score(v[i], c + e + i) - mm);
+                    l += pr;
+                    v[i] = pr * (is_tree ? pow2i(vt_u[64 * h + c + e + i] - U + kHeadroom) : vb);
+                  }
+                } else {
+#pragma unroll
+                  for (int i = 0; i < 8; ++i) v[i] = 0.f;
+                }
+#pragma unroll
+                for (int i = 0; i < 8; i += 2) w[(e + i) / 2] = pack_half2(v[i], v[i + 1]);
+              }
+              tmem_st16(ts + c / 2, w);
+            }
           }
+          tmem_wait_st();
+          fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(BAR_P_FULL + 2 * p + h));
         }
-        tmem_wait_st();
-        fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(BAR_P_FULL + p));
       }
     }
 
@@ -602,11 +619,17 @@ q8_rows_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
   }
 
   // --------------------------------------------------------------- teardown
+  // Products in flight: the issuing threads wait for a commit of their own.
+  if ((warp >= kPv && warp < kTma) && lane == 0) {
+    mma_commit(bar(BAR_FINAL + warp - kPv));
+    mbar_wait(bar(BAR_FINAL + warp - kPv), 0);
+  }
+  __syncwarp();
   fence_before();
   __syncthreads();
   if (flags[1] && tid == 0) report_error(a.err, TSD_DEV_ERR_TIMEOUT, b);
   fence_after();
-  if (warp == kMma) {
+  if (warp == kPv) {
     __syncwarp();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;\n" ::"r"(tmem));
   }
