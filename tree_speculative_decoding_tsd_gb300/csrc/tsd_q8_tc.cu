@@ -9,9 +9,9 @@
 // other thread (with keys on lanes, as in tsd_verify_tc.cu, each is a reduction
 // across a warpgroup, and a probability costs about twice the instructions: the
 // 65-row trees over 8 x 32k keys took 555 us that way).  P goes back to the
-// tensor memory, over the scores it came from, and is the product's left operand
-// there: no shared memory and no barrier among the softmax warps.  Warps whose 32
-// rows are all behind the last one do nothing.
+// tensor memory and is the product's left operand there: no shared memory and no
+// barrier among the softmax warps.  Warps whose 32 rows are all behind the last
+// one do nothing.
 //
 // Numbers.
 //   S      kind::f8f6f4: the K tile's codes as they are in the cache, and Q as
@@ -33,19 +33,23 @@
 // bits.  Two e4m3 terms as for Q do not do: P spans 2^-32..2^8, and what lies
 // below 2^-17 of the largest would be lost from long flat rows.
 //
-// Two streams.  Even and odd tiles have a softmax warpgroup, scores, an
-// accumulator, a maximum and a sum each (512 tensor-memory columns for d = 128),
-// joined at the end: while one stream is in its softmax the tensor core works
-// for the other.  The running maximum is lazy: a row keeps it until a tile's
-// largest score passes it by 8 (in log2), so that its accumulator is rescaled
-// rarely.
+// Two streams.  The two halves of a tile (64 keys each) have a softmax warpgroup,
+// P, an accumulator, a maximum and a sum each, joined at the end.  A softmax
+// thread first takes its 64 scores into registers, so that the tensor core can
+// compute the next tile's over them while the softmax runs.  (With P over the
+// scores it came from, the next scores waited for the product with V: 2000 cycles a
+// tile instead of the products' 1024.)  The running maximum is lazy: a row keeps it
+// until a tile's largest score passes it by 8 (in log2), so that its accumulator is
+// rescaled rarely.  Q (hi, lo) is in the tensor memory too, which leaves the shared
+// memory's 128 bytes a cycle to K and V.
 //
-// Roles (512 threads): warps 0-3 and 4-7 softmax and epilogue; warp 8 owns the
-// tensor memory and issues the products; one thread of warp 9 loads K tiles by
-// TMA into a ring of four; warps 10-15 load V tiles straight into registers, a
-// tile ahead (behind L2 prefetches), and widen them into three fp16 stages, laid
-// out as the product reads them (rows of 64 elements, 128-byte swizzle).
-// mbarriers order K -> S -> softmax -> O and V -> O; every wait is bounded.
+// Roles (608 threads): warps 0-3 and 4-7 softmax and epilogue; warp 8 issues the
+// products with V and owns the tensor memory, warp 9 those with Q; one thread of
+// warp 10 loads K tiles by TMA into a ring of four; warps 11-18 load V tiles
+// straight into registers, a tile ahead (behind L2 prefetches), and widen them
+// into three fp16 stages, laid out as the product reads them (rows of 64
+// elements, 128-byte swizzle).  mbarriers order K -> S -> softmax -> O and V ->
+// O; every wait is bounded.
 //
 // What bounds it: the products of a 128-key tile, 8 8-bit and 8 fp16 ones of M =
 // 128, N = 128 (about 70 cycles each), and behind them the softmax (128
@@ -57,39 +61,40 @@
 namespace tsd {
 namespace {
 
-constexpr int kPv = 8, kQk = 10, kTma = 12, kWide = 13, kWideWarps = 7;
+constexpr int kPv = 8, kQk = 9, kTma = 10, kWide = 11, kWideWarps = 8;
 constexpr int kWideThreads = kWideWarps * 32;
 constexpr int kThreads = (kWide + kWideWarps) * 32;
 constexpr int kStages = 3;                      // widened V tiles
 constexpr int kRows = 128;
+// Tensor memory columns: a tile's scores (128), Q (hi, lo: 64), the streams' P (32
+// each), the accumulators (d each).
+constexpr uint32_t kColQ = 128, kColP = 192, kColO = 256;
 
 template <int D>
 struct RowLayout {
-  static constexpr uint32_t k_bytes = kKeys * D, q_bytes = kRows * D;
+  static constexpr uint32_t k_bytes = kKeys * D;
   static constexpr uint32_t v_bytes = kKeys * D * 2;
   static constexpr uint32_t off_k = 0;
   static constexpr uint32_t off_v = kRing * k_bytes;
-  static constexpr uint32_t off_q = off_v + kStages * v_bytes;         // hi, lo: [128][D] e4m3
-  static constexpr uint32_t off_c2 = off_q + 2 * q_bytes;              // float[128] row scales
-  static constexpr uint32_t off_ml = off_c2 + 4 * kRows;               // float2[2][128] (m, l)
+  static constexpr uint32_t off_ml = off_v + kStages * v_bytes;        // float2[2][128] (m, l)
   static constexpr uint32_t off_rows = off_ml + 16 * kRows;            // i64[kMaxTiles]
   static constexpr uint32_t off_tree = off_rows + 8 * kMaxTiles;       // 4 x 32 bits [128]
   static constexpr uint32_t off_kex = off_tree + 16 * kKeys;           // u8[2 kMaxTiles]
   static constexpr uint32_t off_vex = off_kex + 2 * kMaxTiles;
   static constexpr uint32_t off_bar = off_vex + 2 * kMaxTiles;
-  static constexpr int nbar = 32;
+  static constexpr int nbar = 24;
   static constexpr uint32_t off_flags = off_bar + 8 * nbar;            // tmem, abort, U
   static constexpr uint32_t total = off_flags + 16;
   static_assert(total + 1024 <= 232448, "shared memory budget");
 };
 
 // FULL: the copy landed, the warps wrote or the product is done; EMPTY: read by
-// the product.  S_FULL, P_FULL and PV_DONE: one per stream and half tile (index 2
-// p + h).  T_FULL: the scratch rows' keys, which take the two K slots behind the
-// last prefix tile (hi, lo).
+// the product (S_EMPTY: by the softmax).  P_FULL and PV_DONE: one per stream.
+// T_FULL: the scratch rows' keys, which take the two K slots behind the last
+// prefix tile (hi, lo).  FINAL: one per issuing warp.
 enum { BAR_K_FULL = 0, BAR_K_EMPTY = 4, BAR_V_FULL = 8, BAR_V_EMPTY = 11, BAR_S_FULL = 14,
-       BAR_P_FULL = 18, BAR_PV_DONE = 22, BAR_O_DONE = 26, BAR_T_FULL = 27,
-       BAR_FINAL = 28 };                        // one per issuing warp
+       BAR_S_EMPTY = 15, BAR_P_FULL = 16, BAR_PV_DONE = 18, BAR_O_DONE = 20, BAR_T_FULL = 21,
+       BAR_FINAL = 22 };
 
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32]) {
   uint32_t r[32];
@@ -113,7 +118,14 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
       "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
-// D (+)= A.B with A (fp16) in tensor memory.
+// D (+)= A.B with A in tensor memory: fp16 (two to a column), or e4m3 (four).
+__device__ __forceinline__ void mma_f8_ta(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+                                          uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(acc));
+}
 __device__ __forceinline__ void mma_f16_ta(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
                                            uint32_t acc) {
   asm volatile(
@@ -135,7 +147,6 @@ q8_rows_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
   const uint32_t raw = su32(smem_raw);
   const uint32_t sbase = (raw + 1023u) & ~1023u;
   uint8_t* smem = smem_raw + (sbase - raw);
-  float* c2v = (float*)(smem + L::off_c2);
   float2* s_ml = (float2*)(smem + L::off_ml);
   long long* tile_row = (long long*)(smem + L::off_rows);
   float* kt_in = (float*)(smem + L::off_tree);      // tree rows: factor into e4m3 (0: row of zeros)
@@ -173,13 +184,14 @@ q8_rows_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
       mbar_init(bar(BAR_V_FULL + i), kWideWarps);
       mbar_init(bar(BAR_V_EMPTY + i), 1);
     }
-    for (int i = 0; i < 4; ++i) {
-      mbar_init(bar(BAR_S_FULL + i), 1);
+    for (int i = 0; i < 2; ++i) {
       mbar_init(bar(BAR_P_FULL + i), live_warps);
       mbar_init(bar(BAR_PV_DONE + i), 1);
+      mbar_init(bar(BAR_FINAL + i), 1);
     }
-    for (int i = 0; i < 4; ++i) mbar_init(bar(BAR_FINAL + i), 1);
-    mbar_init(bar(BAR_O_DONE), min(ntiles, 2));
+    mbar_init(bar(BAR_S_FULL), 1);
+    mbar_init(bar(BAR_S_EMPTY), 2 * live_warps);
+    mbar_init(bar(BAR_O_DONE), 1);
     mbar_init(bar(BAR_T_FULL), kWideWarps);
     flags[1] = 0;
     *s_top = -1000;
@@ -206,6 +218,7 @@ q8_rows_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
     const int x = wt + kWideThreads * i;
     return D == 128 ? (x & 3) + 4 * ((x >> 3) & 1) : x & 3;
   };
+  float c2 = 0.f;      // softmax threads: factor of the row's scores
   uint4 vreg[NT];
   auto load_v = [&](long row, int nvalid) {
 #pragma unroll
@@ -241,17 +254,51 @@ q8_rows_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
     top = __reduce_max_sync(kFull, top);
     if (lane == 0) atomicMax(s_top, top);
   } else if (warp < 8) {
-    stage_q<D>(a, b, hk, row_base, rows_here, kRows, tid, 256, smem + L::off_q,
-               smem + L::off_q + L::q_bytes, c2v);
-    asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
+    // Q into the tensor memory: a thread's row, hi from the first warpgroup and
+    // lo from the second
+    const int p = warp >> 2, row = (warp & 3) * 32 + lane;
+    if ((warp & 3) < live_warps) {
+      const uint4* qp = nullptr;
+      if (row < rows_here) {
+        const int pr = row_base + row;
+        const int tr = pr / a.g, qh = hk * a.g + pr % a.g;
+        qp = (const uint4*)((const __nv_bfloat16*)a.q + (((long)b * a.R + tr) * a.Hq + qh) * D);
+      }
+      uint32_t top = 0;
+      bool bad = false;
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i) scan8(qp ? __ldg(qp + i) : make_uint4(0u, 0u, 0u, 0u), top, bad);
+      const int e = row_exponent(top);
+      c2 = bad ? __int_as_float(0x7fffffff) : a.qscale * q8_scale(e - 7);
+      const float f = q8_scale(261 - e);
+      const uint32_t dst = flags[0] + kColQ + p * (D / 4) + ((uint32_t)((warp & 3) * 32) << 16);
+#pragma unroll
+      for (int c = 0; c < D / 16; c += 2) {
+        uint4 hi[2], lo[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          uint4 w[2] = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
+          if (qp && !bad) {
+            w[0] = __ldg(qp + 2 * (c + j));
+            w[1] = __ldg(qp + 2 * (c + j) + 1);
+          }
+          split16(w, f, hi[j], lo[j]);
+        }
+        const uint4 x = p == 0 ? hi[0] : lo[0], y = p == 0 ? hi[1] : lo[1];
+        const float v[8] = {__uint_as_float(x.x), __uint_as_float(x.y), __uint_as_float(x.z),
+                            __uint_as_float(x.w), __uint_as_float(y.x), __uint_as_float(y.y),
+                            __uint_as_float(y.z), __uint_as_float(y.w)};
+        tmem_st8(dst + 4 * c, v);
+      }
+      tmem_wait_st();
+    }
   }
   fence_before();
   __syncthreads();
   fence_after();
   const uint32_t tmem = flags[0];
   const int U = *s_top;
-  auto tm_s = [&](int p) { return tmem + (uint32_t)(p * kKeys); };
-  auto tm_o = [&](int p) { return tmem + 256u + (uint32_t)(p * D); };
+  auto tm_o = [&](int p) { return tmem + kColO + (uint32_t)(p * D); };
 
   // -------------------------------------------------------------- K tiles
   if (warp == kTma) {
@@ -328,79 +375,69 @@ q8_rows_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
     }
   }
 
-  // ------------------------------------------------------ scores: warp kQk + p
-  // A stream's two half tiles (64 keys) are two products and two buffers: while
-  // the softmax works on one, the other is multiplied by V and filled again.
-  else if (warp >= kQk) {
+  // ------------------------------------------------------------- scores
+  else if (warp == kQk) {
     if (lane == 0) {
-      const int p = warp - kQk;
       // fp32 accumulator; e4m3 operands are format 0
       const uint32_t idesc =
-          (1u << 4) | ((uint32_t)(64 >> 3) << 17) | ((uint32_t)(kRows >> 4) << 24);
+          (1u << 4) | ((uint32_t)(kKeys >> 3) << 17) | ((uint32_t)(kRows >> 4) << 24);
       const uint64_t kd0 = row_desc<D>(sbase + L::off_k);
-      const uint64_t qd0 = row_desc<D>(sbase + L::off_q);
-      // S (+)= (Q hi + Q lo) x half h of a K slot
-      auto products = [&](uint32_t ts, int sl, int h, bool first) {
-        const uint64_t kd = kd0 + (uint64_t)((sl * L::k_bytes + h * 64 * D) >> 4);
+      const uint32_t tq = tmem + kColQ;
+      // S (+)= (Q hi + Q lo) x K slot
+      auto products = [&](int sl, bool first) {
+        const uint64_t kd = kd0 + (uint64_t)(sl * (L::k_bytes >> 4));
 #pragma unroll
         for (int part = 0; part < 2; ++part)
 #pragma unroll
           for (int kk = 0; kk < D / 32; ++kk)
-            mma_f8(ts, qd0 + (uint64_t)(part * (L::q_bytes >> 4)) + 2 * kk, kd + 2 * kk, idesc,
-                   first && part == 0 && kk == 0 ? 0u : 1u);
+            mma_f8_ta(tmem, tq + part * (D / 4) + 8 * kk, kd + 2 * kk, idesc,
+                      first && part == 0 && kk == 0 ? 0u : 1u);
       };
       bool ok = true;
-      for (int t = p; ok && t < ntiles; t += 2) {
+      for (int t = 0; t < ntiles; ++t) {
         const int sl = t % kRing;
-        ok = t < n_pre ? mbar_wait(bar(BAR_K_FULL + sl), (t / kRing) & 1)
-                       : mbar_wait(bar(BAR_T_FULL), 0);
-#pragma unroll
-        for (int h = 0; ok && h < 2; ++h) {
-          // the scores go over P of the stream's tile before: its product is done
-          if (t >= 2) ok = mbar_wait(bar(BAR_PV_DONE + 2 * p + h), ((t - 2) >> 1) & 1);
-          if (!ok || flags[1]) { ok = false; break; }
-          fence_after();
-          products(tm_s(p) + 64 * h, sl, h, true);
-          if (t >= n_pre) products(tm_s(p) + 64 * h, (t + 1) % kRing, h, false);
-          mma_commit(bar(BAR_S_FULL + 2 * p + h));
-        }
-        if (ok) mma_commit(bar(BAR_K_EMPTY + sl));
+        ok = (t < n_pre ? mbar_wait(bar(BAR_K_FULL + sl), (t / kRing) & 1)
+                        : mbar_wait(bar(BAR_T_FULL), 0)) &&
+             (t == 0 || mbar_wait(bar(BAR_S_EMPTY), (t - 1) & 1)) && !flags[1];
+        if (!ok) break;
+        fence_after();
+        products(sl, true);
+        if (t >= n_pre) products((t + 1) % kRing, false);
+        mma_commit(bar(BAR_S_FULL));
+        mma_commit(bar(BAR_K_EMPTY + sl));
       }
       if (!ok) flags[1] = 1;
     }
     __syncwarp();
   }
 
-  // ----------------------------------------------------- outputs: warp kPv + p
-  else if (warp >= kPv) {
+  // ------------------------------------------------------------- outputs
+  else if (warp == kPv) {
     if (lane == 0) {
-      const int p = warp - kPv;
       // fp16 operands are format 0; B (V) is N-major
       const uint32_t idesc =
           (1u << 4) | (1u << 16) | ((uint32_t)(D >> 3) << 17) | ((uint32_t)(kRows >> 4) << 24);
       const uint64_t vd0 = smem_desc(sbase + L::off_v, kHalf, 1024);
       bool ok = true;
-      for (int t = p; ok && t < ntiles; t += 2) {
+      for (int t = 0; ok && t < ntiles; ++t) {
         const int st = t % kStages;
         const uint64_t vd = vd0 + (uint64_t)(st * (L::v_bytes >> 4));
         ok = mbar_wait(bar(BAR_V_FULL + st), (t / kStages) & 1);
 #pragma unroll
-        for (int h = 0; ok && h < 2; ++h) {
-          ok = mbar_wait(bar(BAR_P_FULL + 2 * p + h), (t >> 1) & 1) && !flags[1];
+        for (int p = 0; ok && p < 2; ++p) {
+          ok = mbar_wait(bar(BAR_P_FULL + p), t & 1) && !flags[1];
           if (!ok) break;
           fence_after();
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
-            mma_f16_ta(tm_o(p), tm_s(p) + 64 * h + 8 * kk, vd + 128 * (4 * h + kk), idesc,
-                       t < 2 && h == 0 && kk == 0 ? 0u : 1u);
-          mma_commit(bar(BAR_PV_DONE + 2 * p + h));
+            mma_f16_ta(tm_o(p), tmem + kColP + 32 * p + 8 * kk, vd + 128 * (4 * p + kk), idesc,
+                       t == 0 && kk == 0 ? 0u : 1u);
+          mma_commit(bar(BAR_PV_DONE + p));
         }
-        if (ok) {
-          mma_commit(bar(BAR_V_EMPTY + st));
-          if (t + 2 >= ntiles) mma_commit(bar(BAR_O_DONE));
-        }
+        if (ok) mma_commit(bar(BAR_V_EMPTY + st));
       }
-      if (!ok) flags[1] = 1;
+      if (ok) mma_commit(bar(BAR_O_DONE));
+      else flags[1] = 1;
     }
     __syncwarp();
   }
@@ -409,30 +446,26 @@ q8_rows_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
   else {
     const int p = warp >> 2, q = warp & 3, row = q * 32 + lane;
     const uint32_t lane_off = (uint32_t)(q * 32) << 16;
-    const uint32_t ts = tm_s(p) + lane_off;
     float m = -INFINITY, l = 0.f;
     bool failed = false;
     if (q < live_warps) {
-      const float c2 = c2v[row];
       uint64_t mask = 0ull;
       if (row < rows_here) {
         const int tr = (row_base + row) / a.g;
         mask = tr > 0 ? a.mask[(long)b * a.R + tr] : 0ull;
       }
-      // raise the maximum to X where it passes m by the headroom (or m is
-      // none), and rescale the sum and the accumulator; (t, h): the half tile
-      auto raise = [&](float X, int t, int h) -> bool {
+      // Before P of tile t is written: the stream's product before is done; the
+      // maximum is raised to X where X passes m by the headroom (or m is none),
+      // the sum and the accumulator are rescaled.
+      auto raise = [&](float X, int t) -> bool {
+        if (t > 0 && !__all_sync(kFull, mbar_wait(bar(BAR_PV_DONE + p), (t - 1) & 1))) return false;
         const bool need = !(X <= m + kOverflow);
         if (!__any_sync(kFull, need)) return true;
         const float m_new = need ? fmaxf(m, X) : m;
         const float al = m_new == m ? 1.f : m == -INFINITY ? 0.f : ex2(m - m_new);
         m = m_new;
         l *= al;
-        if (t < 2 && h == 0) return true;
-        // the products issued so far are done: the half before's is the last
-        if (!__all_sync(kFull, h == 0 ? mbar_wait(bar(BAR_PV_DONE + 2 * p + 1), ((t - 2) >> 1) & 1)
-                                      : mbar_wait(bar(BAR_PV_DONE + 2 * p), (t >> 1) & 1)))
-          return false;
+        if (t == 0) return true;
         fence_after();
 #pragma unroll 1
         for (int c = 0; c < D; c += 16) {
@@ -448,114 +481,120 @@ q8_rows_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
         tmem_wait_st();
         return true;
       };
+      // the scores have been read: their columns may take the next tile's
+      auto scores_read = [&] {
+        fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(BAR_S_EMPTY));
+      };
 
-      for (int t = p; t < ntiles && !failed; t += 2) {
+      const int h = p;                           // a stream takes one half of every tile
+      const uint32_t ts = tmem + lane_off + 64u * h, tp = tmem + lane_off + kColP + 32u * p;
+      for (int t = 0; t < ntiles; ++t) {
         const bool is_tree = t >= n_pre;
         const int nvalid = is_tree ? a.R : valid_of(t);
-#pragma unroll 1
-        for (int h = 0; h < 2; ++h) {
-          const uint32_t ts = tm_s(p) + lane_off + 64u * h;
-          if (!__all_sync(kFull, mbar_wait(bar(BAR_S_FULL + 2 * p + h), (t >> 1) & 1)) ||
-              __any_sync(kFull, flags[1] != 0)) {
+        if (!__all_sync(kFull, mbar_wait(bar(BAR_S_FULL), t & 1)) ||
+            __any_sync(kFull, flags[1] != 0)) {
+          failed = true;
+          break;
+        }
+        fence_after();
+        if (!is_tree && nvalid == kKeys) {
+          // 64 keys of one block: one factor and one offset.  (An offset below
+          // -60 puts P under fp16's range: its exact value does not matter, and
+          // the sum stays within fp32.)
+          const float f = c2 * q8_scale(kex[2 * t + h]);
+          const int d = max((int)vex[2 * t + h] - 127 - U + kHeadroom, -60);
+          float v[64];
+          tmem_ld32(ts, *(float(*)[32])v);
+          tmem_ld32(ts + 32, *(float(*)[32])(v + 32));
+          tmem_wait_ld();
+          scores_read();
+          float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int i = 0; i < 64; i += 8)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) top[j] = max3f(top[j], v[i + 2 * j], v[i + 2 * j + 1]);
+          if (!raise(f * fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])), t)) {
             failed = true;
             break;
           }
-          fence_after();
-          if (!is_tree && nvalid == kKeys) {
-            // 64 keys of one block: one factor and one offset.  (An offset below
-            // -60 puts P under fp16's range: its exact value does not matter, and
-            // the sum stays within fp32.)
-            const float f = c2 * q8_scale(kex[2 * t + h]);
-            const int d = max((int)vex[2 * t + h] - 127 - U + kHeadroom, -60);
-            float v[64];
-            tmem_ld32(ts, *(float(*)[32])v);
-            tmem_ld32(ts + 32, *(float(*)[32])(v + 32));
-            tmem_wait_ld();
-            float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+          const float off = (float)d - (m == -INFINITY ? 0.f : m);
+          const float2 f2 = make_float2(f, f), o2 = make_float2(off, off);
+          float2 sa = make_float2(0.f, 0.f), sb = sa;
 #pragma unroll
-            for (int i = 0; i < 64; i += 8)
+          for (int c = 0; c < 64; c += 32) {
+            uint32_t w[16];
 #pragma unroll
-              for (int j = 0; j < 4; ++j) top[j] = max3f(top[j], v[i + 2 * j], v[i + 2 * j + 1]);
-            if (!raise(f * fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])), t, h)) {
-              failed = true;
-              break;
+            for (int i = 0; i < 32; i += 4) {
+              const float2 xa = __ffma2_rn(make_float2(v[c + i], v[c + i + 1]), f2, o2);
+              const float2 xb = __ffma2_rn(make_float2(v[c + i + 2], v[c + i + 3]), f2, o2);
+              const float2 pa = make_float2(ex2(xa.x), ex2(xa.y));
+              const float2 pb = make_float2(ex2(xb.x), ex2(xb.y));
+              sa = __fadd2_rn(sa, pa);
+              sb = __fadd2_rn(sb, pb);
+              w[i / 2] = pack_half2(pa.x, pa.y);
+              w[i / 2 + 1] = pack_half2(pb.x, pb.y);
             }
-            const float off = (float)d - (m == -INFINITY ? 0.f : m);
-            const float2 f2 = make_float2(f, f), o2 = make_float2(off, off);
-            float2 sa = make_float2(0.f, 0.f), sb = sa;
-#pragma unroll
-            for (int c = 0; c < 64; c += 32) {
-              uint32_t w[16];
-#pragma unroll
-              for (int i = 0; i < 32; i += 4) {
-                const float2 xa = __ffma2_rn(make_float2(v[c + i], v[c + i + 1]), f2, o2);
-                const float2 xb = __ffma2_rn(make_float2(v[c + i + 2], v[c + i + 3]), f2, o2);
-                const float2 pa = make_float2(ex2(xa.x), ex2(xa.y));
-                const float2 pb = make_float2(ex2(xb.x), ex2(xb.y));
-                sa = __fadd2_rn(sa, pa);
-                sb = __fadd2_rn(sb, pb);
-                w[i / 2] = pack_half2(pa.x, pa.y);
-                w[i / 2 + 1] = pack_half2(pb.x, pb.y);
-              }
-              tmem_st16(ts + c / 2, w);
-            }
-            l = fmaf((sa.x + sa.y) + (sb.x + sb.y), pow2i(-d), l);
-          } else {
-            // the scratch rows, or a tile that the prefix does not fill: masks,
-            // and for scratch rows a factor per key
-            const int nv = min(max(nvalid - 64 * h, 0), 64);
-            const float fb = is_tree ? 0.f : q8_scale(kex[2 * t + h]);
-            const float vb = is_tree ? 0.f : pow2i((int)vex[2 * t + h] - 127 - U + kHeadroom);
-            auto score = [&](float s, int i) {     // key i of this half
-              const int key = 64 * h + i;
-              const bool sees = i < nv &&
-                                (!is_tree || key == 0 || (((mask >> ((key - 1) & 63)) & 1ull) != 0));
-              return sees ? s * (c2 * (is_tree ? kt_out[key] : fb)) : -INFINITY;
-            };
-            float top = -INFINITY;
-#pragma unroll 1
-            for (int c = 0; c < nv; c += 8) {
-              float v[8];
-              tmem_ld8(ts + c, v);
-              tmem_wait_ld();
-#pragma unroll
-              for (int i = 0; i < 8; ++i) top = fmaxf(top, score(v[i], c + i));
-            }
-            if (!raise(top, t, h)) {
-              failed = true;
-              break;
-            }
-            const float mm = m == -INFINITY ? 0.f : m;
-#pragma unroll 1
-            for (int c = 0; c < 64; c += 32) {
-              uint32_t w[16];
-#pragma unroll
-              for (int e = 0; e < 32; e += 8) {
-                float v[8];
-                if (c + e < nv) {
-                  tmem_ld8(ts + c + e, v);
-                  tmem_wait_ld();
-#pragma unroll
-                  for (int i = 0; i < 8; ++i) {
-                    const float pr = ex2(score(v[i], c + e + i) - mm);
-                    l += pr;
-                    v[i] = pr * (is_tree ? pow2i(vt_u[64 * h + c + e + i] - U + kHeadroom) : vb);
-                  }
-                } else {
-#pragma unroll
-                  for (int i = 0; i < 8; ++i) v[i] = 0.f;
-                }
-#pragma unroll
-                for (int i = 0; i < 8; i += 2) w[(e + i) / 2] = pack_half2(v[i], v[i + 1]);
-              }
-              tmem_st16(ts + c / 2, w);
-            }
+            tmem_st16(tp + c / 2, w);
           }
-          tmem_wait_st();
-          fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar(BAR_P_FULL + 2 * p + h));
+          l = fmaf((sa.x + sa.y) + (sb.x + sb.y), pow2i(-d), l);
+        } else {
+          // the scratch rows, or a tile that the prefix does not fill: masks,
+          // and for scratch rows a factor per key
+          const int nv = min(max(nvalid - 64 * h, 0), 64);
+          const float fb = is_tree ? 0.f : q8_scale(kex[2 * t + h]);
+          const float vb = is_tree ? 0.f : pow2i((int)vex[2 * t + h] - 127 - U + kHeadroom);
+          auto score = [&](float s, int i) {     // key i of this half
+            const int key = 64 * h + i;
+            const bool sees = i < nv &&
+                              (!is_tree || key == 0 || (((mask >> ((key - 1) & 63)) & 1ull) != 0));
+            return sees ? s * (c2 * (is_tree ? kt_out[key] : fb)) : -INFINITY;
+          };
+          float top = -INFINITY;
+#pragma unroll 1
+          for (int c = 0; c < nv; c += 8) {
+            float v[8];
+            tmem_ld8(ts + c, v);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 8; ++i) top = fmaxf(top, score(v[i], c + i));
+          }
+          if (!raise(top, t)) {
+            failed = true;
+            break;
+          }
+          const float mm = m == -INFINITY ? 0.f : m;
+#pragma unroll 1
+          for (int c = 0; c < 64; c += 32) {
+            uint32_t w[16];
+#pragma unroll
+            for (int e = 0; e < 32; e += 8) {
+              float v[8];
+              if (c + e < nv) {
+                tmem_ld8(ts + c + e, v);
+                tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                  const float pr = ex2(score(v[i], c + e + i) - mm);
+                  l += pr;
+                  v[i] = pr * (is_tree ? pow2i(vt_u[64 * h + c + e + i] - U + kHeadroom) : vb);
+                }
+              } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[i] = 0.f;
+              }
+#pragma unroll
+              for (int i = 0; i < 8; i += 2) w[(e + i) / 2] = pack_half2(v[i], v[i + 1]);
+            }
+            tmem_st16(tp + c / 2, w);
+          }
+          scores_read();
         }
+        tmem_wait_st();
+        fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(BAR_P_FULL + p));
       }
     }
 
@@ -594,12 +633,8 @@ q8_rows_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
       for (int c = p * (D / 2); c < (p + 1) * (D / 2); c += 32) {
         float o0[32], o1[32];
         tmem_ld32(tm_o(0) + lane_off + c, o0);
-        if (ntiles > 1) tmem_ld32(tm_o(1) + lane_off + c, o1);
+        tmem_ld32(tm_o(1) + lane_off + c, o1);
         tmem_wait_ld();
-        if (ntiles < 2) {
-#pragma unroll
-          for (int i = 0; i < 32; ++i) o1[i] = 0.f;
-        }
         uint32_t w[16];
 #pragma unroll
         for (int i = 0; i < 32; i += 2) {
