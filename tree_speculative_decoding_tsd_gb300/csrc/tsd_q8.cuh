@@ -36,6 +36,11 @@ struct CacheMap {
     if (pg < 0 || pg >= num_pages) return -1;
     return ((long)pg * Hkv + h) * page_size + pos % page_size;
   }
+  // Index of the exponent byte of position pos, whose row is `row` (not -1).
+  __device__ __forceinline__ long block_at(int b, int h, int pos, long row) const {
+    if (page_size) return row / kQ8Block;              // (pages are whole blocks)
+    return ((long)b * Hkv + h) * ((cap + kQ8Block - 1) / kQ8Block) + pos / kQ8Block;
+  }
   // Index of the exponent byte of position pos; -1 for a page outside the pool.
   __device__ __forceinline__ long block(int b, int h, int pos) const {
     if (page_size == 0)

@@ -54,6 +54,8 @@
 // What bounds it: the products of a 128-key tile, 8 8-bit and 8 fp16 ones of M =
 // 128, N = 128 (about 70 cycles each), and behind them the softmax (128
 // exponentials per row at 16 a cycle and SM).
+#include <type_traits>
+
 #include "tsd_common.cuh"
 #include "tsd_host.h"
 #include "tsd_q8_tc.cuh"
@@ -76,25 +78,29 @@ struct RowLayout {
   static constexpr uint32_t v_bytes = kKeys * D * 2;
   static constexpr uint32_t off_k = 0;
   static constexpr uint32_t off_v = kRing * k_bytes;
-  static constexpr uint32_t off_ml = off_v + kStages * v_bytes;        // float2[2][128] (m, l)
+  static constexpr uint32_t off_q = off_v + kStages * v_bytes;         // bf16 rows, padded
+  static constexpr uint32_t q_pitch = 2 * D + 16;
+  static constexpr uint32_t off_ml = off_q + kRows * q_pitch;          // float2[2][128] (m, l)
   static constexpr uint32_t off_rows = off_ml + 16 * kRows;            // i64[kMaxTiles]
   static constexpr uint32_t off_tree = off_rows + 8 * kMaxTiles;       // 4 x 32 bits [128]
   static constexpr uint32_t off_kex = off_tree + 16 * kKeys;           // u8[2 kMaxTiles]
   static constexpr uint32_t off_vex = off_kex + 2 * kMaxTiles;
   static constexpr uint32_t off_bar = off_vex + 2 * kMaxTiles;
-  static constexpr int nbar = 24;
-  static constexpr uint32_t off_flags = off_bar + 8 * nbar;            // tmem, abort, U
-  static constexpr uint32_t total = off_flags + 16;
+  static constexpr int nbar = 25;
+  static constexpr uint32_t off_flags = off_bar + 8 * nbar;            // tmem, abort
+  static constexpr uint32_t off_top = off_flags + 8;                   // int[kWideWarps]
+  static constexpr uint32_t total = off_top + 4 * kWideWarps;
   static_assert(total + 1024 <= 232448, "shared memory budget");
 };
 
 // FULL: the copy landed, the warps wrote or the product is done; EMPTY: read by
 // the product (S_EMPTY: by the softmax).  P_FULL and PV_DONE: one per stream.
 // T_FULL: the scratch rows' keys, which take the two K slots behind the last
-// prefix tile (hi, lo).  FINAL: one per issuing warp.
+// prefix tile (hi, lo).  Q_FULL: Q is in the tensor memory.  FINAL: one per
+// issuing warp.
 enum { BAR_K_FULL = 0, BAR_K_EMPTY = 4, BAR_V_FULL = 8, BAR_V_EMPTY = 11, BAR_S_FULL = 14,
        BAR_S_EMPTY = 15, BAR_P_FULL = 16, BAR_PV_DONE = 18, BAR_O_DONE = 20, BAR_T_FULL = 21,
-       BAR_FINAL = 22 };
+       BAR_FINAL = 22, BAR_Q_FULL = 24 };
 
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32]) {
   uint32_t r[32];
@@ -156,7 +162,7 @@ q8_rows_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
   uint8_t* kex = smem + L::off_kex;
   uint8_t* vex = smem + L::off_vex;
   volatile uint32_t* flags = (volatile uint32_t*)(smem + L::off_flags);
-  int* s_top = (int*)(smem + L::off_flags + 8);     // U
+  int* s_top = (int*)(smem + L::off_top);           // U by widening warp
   const uint32_t bar0 = sbase + L::off_bar;
   auto bar = [&](int i) { return bar0 + 8u * i; };
 
@@ -175,36 +181,8 @@ q8_rows_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
   auto valid_of = [&](int t) { return min(kKeys, k1 - (k0 + t * kKeys)); };
 
   // ---------------------------------------------------------------- set-up
-  if (tid == kPv * 32) {
-    for (int i = 0; i < kRing; ++i) {
-      mbar_init(bar(BAR_K_FULL + i), 1);
-      mbar_init(bar(BAR_K_EMPTY + i), 1);
-    }
-    for (int i = 0; i < kStages; ++i) {
-      mbar_init(bar(BAR_V_FULL + i), kWideWarps);
-      mbar_init(bar(BAR_V_EMPTY + i), 1);
-    }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(bar(BAR_P_FULL + i), live_warps);
-      mbar_init(bar(BAR_PV_DONE + i), 1);
-      mbar_init(bar(BAR_FINAL + i), 1);
-    }
-    mbar_init(bar(BAR_S_FULL), 1);
-    mbar_init(bar(BAR_S_EMPTY), 2 * live_warps);
-    mbar_init(bar(BAR_O_DONE), 1);
-    mbar_init(bar(BAR_T_FULL), kWideWarps);
-    flags[1] = 0;
-    *s_top = -1000;
-    asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
-  }
-  if (warp == kPv) {
-    __syncwarp();
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;\n" ::"r"(
-        sbase + L::off_flags));
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n");
-  }
-  __syncthreads();
-
+  // Everything that the first products need is requested at once, by the warps
+  // that will use it; one barrier, then Q's way into the tensor memory.
   // widening threads: chunk i of this thread is (row, 16-code chunk); eight
   // lanes that store together take chunks 0-3 of an even and an odd row (D =
   // 128), or of two rows (D = 64): eight different 16-byte columns of a
@@ -218,7 +196,7 @@ q8_rows_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
     const int x = wt + kWideThreads * i;
     return D == 128 ? (x & 3) + 4 * ((x >> 3) & 1) : x & 3;
   };
-  float c2 = 0.f;      // softmax threads: factor of the row's scores
+  uint64_t mask = 0ull;     // softmax threads: the scratch rows that the row sees
   uint4 vreg[NT];
   auto load_v = [&](long row, int nvalid) {
 #pragma unroll
@@ -231,15 +209,17 @@ q8_rows_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
   };
 
   if (warp >= kWide) {
-    // the first tile's loads go out before anything else
-    if (n_pre > 0) load_v(a.map.row(b, hk, k0), valid_of(0));
+    // the first V tile, the exponents and rows of the split's tiles, the scratch rows
+    const long r0 = n_pre > 0 ? a.map.row(b, hk, k0) : -1;
+    const long rt = wt < n_pre ? a.map.row(b, hk, k0 + wt * kKeys) : -1;
+    if (n_pre > 0) load_v(r0, valid_of(0));
     int top = -1000;
     for (int t = wt; t < n_pre; t += kWideThreads) {
       const int pos = k0 + t * kKeys;
-      const long r = a.map.row(b, hk, pos);
+      const long r = t == wt ? rt : a.map.row(b, hk, pos);
       tile_row[t] = r;
       if (r < 0) report_error(a.err, TSD_DEV_ERR_BAD_PAGE, b);
-      const long e = a.map.block(b, hk, pos);
+      const long e = a.map.block_at(b, hk, pos, r);
       const bool second = pos + kQ8Block < k1;      // (the last block of a tile may not exist)
       const int ka = r < 0 ? 127 : a.ke[e], va = r < 0 ? 127 : a.ve[e];
       const int kb = r < 0 || !second ? 127 : a.ke[e + 1];
@@ -252,69 +232,85 @@ q8_rows_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
     }
     if (with_tree) top = max(top, scan_tree<D>(a, b, hk, wt, kWideThreads, kt_in, vt_in, kt_out, vt_u));
     top = __reduce_max_sync(kFull, top);
-    if (lane == 0) atomicMax(s_top, top);
+    if (lane == 0) s_top[warp - kWide] = top;
   } else if (warp < 8) {
-    // Q into the tensor memory: a thread's row, hi from the first warpgroup and
-    // lo from the second
-    const int p = warp >> 2, row = (warp & 3) * 32 + lane;
-    if ((warp & 3) < live_warps) {
-      const uint4* qp = nullptr;
-      if (row < rows_here) {
-        const int pr = row_base + row;
+    // Q by coalesced copies, rows padded by 16 bytes, so that eight lanes' rows
+    // start in eight different banks; and what this thread's row sees
+    const int row = (warp & 3) * 32 + lane;
+    for (int x = tid; x < live_warps * 32 * (D / 8); x += 256) {
+      const int r = x / (D / 8), u = x % (D / 8);
+      const bool valid = r < rows_here;
+      const __nv_bfloat16* src = (const __nv_bfloat16*)a.q;
+      if (valid) {
+        const int pr = row_base + r;
         const int tr = pr / a.g, qh = hk * a.g + pr % a.g;
-        qp = (const uint4*)((const __nv_bfloat16*)a.q + (((long)b * a.R + tr) * a.Hq + qh) * D);
+        src += (((long)b * a.R + tr) * a.Hq + qh) * D + u * 8;
       }
-      uint32_t top = 0;
-      bool bad = false;
-#pragma unroll
-      for (int i = 0; i < D / 8; ++i) scan8(qp ? __ldg(qp + i) : make_uint4(0u, 0u, 0u, 0u), top, bad);
-      const int e = row_exponent(top);
-      c2 = bad ? __int_as_float(0x7fffffff) : a.qscale * q8_scale(e - 7);
-      const float f = q8_scale(261 - e);
-      const uint32_t dst = flags[0] + kColQ + p * (D / 4) + ((uint32_t)((warp & 3) * 32) << 16);
-#pragma unroll
-      for (int c = 0; c < D / 16; c += 2) {
-        uint4 hi[2], lo[2];
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          uint4 w[2] = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
-          if (qp && !bad) {
-            w[0] = __ldg(qp + 2 * (c + j));
-            w[1] = __ldg(qp + 2 * (c + j) + 1);
-          }
-          split16(w, f, hi[j], lo[j]);
-        }
-        const uint4 x = p == 0 ? hi[0] : lo[0], y = p == 0 ? hi[1] : lo[1];
-        const float v[8] = {__uint_as_float(x.x), __uint_as_float(x.y), __uint_as_float(x.z),
-                            __uint_as_float(x.w), __uint_as_float(y.x), __uint_as_float(y.y),
-                            __uint_as_float(y.z), __uint_as_float(y.w)};
-        tmem_st8(dst + 4 * c, v);
-      }
-      tmem_wait_st();
+      cp_async16(sbase + L::off_q + r * L::q_pitch + u * 16, src, valid);
     }
+    if (row < rows_here) {
+      const int tr = (row_base + row) / a.g;
+      mask = tr > 0 ? a.mask[(long)b * a.R + tr] : 0ull;
+    }
+    asm volatile("cp.async.commit_group;\n cp.async.wait_group 0;\n" ::: "memory");
+  } else if (warp == kTma) {
+    if (lane == 0) {
+      for (int i = 0; i < kRing; ++i) {
+        mbar_init(bar(BAR_K_FULL + i), 1);
+        mbar_init(bar(BAR_K_EMPTY + i), 1);
+      }
+      for (int i = 0; i < kStages; ++i) {
+        mbar_init(bar(BAR_V_FULL + i), kWideWarps);
+        mbar_init(bar(BAR_V_EMPTY + i), 1);
+      }
+      for (int i = 0; i < 2; ++i) {
+        mbar_init(bar(BAR_P_FULL + i), live_warps);
+        mbar_init(bar(BAR_PV_DONE + i), 1);
+        mbar_init(bar(BAR_FINAL + i), 1);
+      }
+      mbar_init(bar(BAR_S_FULL), 1);
+      mbar_init(bar(BAR_S_EMPTY), 2 * live_warps);
+      mbar_init(bar(BAR_O_DONE), 1);
+      mbar_init(bar(BAR_T_FULL), kWideWarps);
+      mbar_init(bar(BAR_Q_FULL), 2 * live_warps);
+      flags[1] = 0;
+      asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
+      for (int t = 0; t < kRing && t < n_pre; ++t)
+        load_keys(a, kmap, b, hk, k0 + t * kKeys,
+                  a.map.page_size ? a.map.row(b, hk, k0 + t * kKeys) : 0,
+                  sbase + L::off_k + t * L::k_bytes, L::k_bytes, bar(BAR_K_FULL + t));
+    }
+    __syncwarp();
+  } else if (warp == kPv) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;\n" ::"r"(
+        sbase + L::off_flags));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n");
   }
   fence_before();
   __syncthreads();
   fence_after();
   const uint32_t tmem = flags[0];
-  const int U = *s_top;
+  int U = s_top[0];
+#pragma unroll
+  for (int i = 1; i < kWideWarps; ++i) U = max(U, s_top[i]);
   auto tm_o = [&](int p) { return tmem + kColO + (uint32_t)(p * D); };
 
   // -------------------------------------------------------------- K tiles
   if (warp == kTma) {
     if (lane == 0) {
-      int loaded = 0;
-      for (int t = 0; t < n_pre && !flags[1]; ++t) {
+      for (int i = 1; i < kPrefetch; ++i)
+        if (i < n_pre && tile_row[i] >= 0) prefetch_l2(a.vc + tile_row[i] * D, (long)valid_of(i) * D);
+      int loaded = min(kRing, n_pre);          // by the set-up
+      for (int t = loaded; t < n_pre && !flags[1]; ++t) {
         const int sl = t % kRing;
-        if (t >= kRing && !mbar_wait(bar(BAR_K_EMPTY + sl), (t / kRing - 1) & 1)) {
+        if (!mbar_wait(bar(BAR_K_EMPTY + sl), (t / kRing - 1) & 1)) {
           flags[1] = 1;
           break;
         }
         load_keys(a, kmap, b, hk, k0 + t * kKeys, tile_row[t], sbase + L::off_k + sl * L::k_bytes,
                   L::k_bytes, bar(BAR_K_FULL + sl));
         ++loaded;
-        for (int i = t == 0 ? 1 : t + kPrefetch; i <= t + kPrefetch; ++i)
-          if (i < n_pre && tile_row[i] >= 0) prefetch_l2(a.vc + tile_row[i] * D, (long)valid_of(i) * D);
+        if (tile_row[t] >= 0) prefetch_l2(a.vc + tile_row[t] * D, (long)valid_of(t) * D);
       }
       // no copy may be in flight when the CTA leaves
       for (int sl = 0; sl < kRing && sl < loaded; ++sl)
@@ -393,8 +389,8 @@ q8_rows_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
             mma_f8_ta(tmem, tq + part * (D / 4) + 8 * kk, kd + 2 * kk, idesc,
                       first && part == 0 && kk == 0 ? 0u : 1u);
       };
-      bool ok = true;
-      for (int t = 0; t < ntiles; ++t) {
+      bool ok = mbar_wait(bar(BAR_Q_FULL), 0);
+      for (int t = 0; ok && t < ntiles; ++t) {
         const int sl = t % kRing;
         ok = (t < n_pre ? mbar_wait(bar(BAR_K_FULL + sl), (t / kRing) & 1)
                         : mbar_wait(bar(BAR_T_FULL), 0)) &&
@@ -449,11 +445,31 @@ q8_rows_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
     float m = -INFINITY, l = 0.f;
     bool failed = false;
     if (q < live_warps) {
-      uint64_t mask = 0ull;
-      if (row < rows_here) {
-        const int tr = (row_base + row) / a.g;
-        mask = tr > 0 ? a.mask[(long)b * a.R + tr] : 0ull;
+      // Q into the tensor memory: a thread takes its row's largest element and
+      // splits the stream's half of the row
+      const uint4* qp = (const uint4*)(smem + L::off_q + row * L::q_pitch);
+      uint32_t qtop = 0;
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i) qtop = top_pairs(qtop, qp[i]);
+      qtop = top_of(qtop);
+      const bool bad = qtop >= 0x7f800000u;
+      const int qe = row_exponent(qtop);
+      const float c2 = bad ? __int_as_float(0x7fffffff) : a.qscale * q8_scale(qe - 7);
+      const uint32_t tq = tmem + kColQ + p * (D / 8) + lane_off;
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) {           // 16 elements: four columns of hi, four of lo
+        uint4 w[2] = {qp[p * (D / 16) + 2 * c], qp[p * (D / 16) + 2 * c + 1]}, hi, lo;
+        if (bad) w[0] = w[1] = make_uint4(0u, 0u, 0u, 0u);
+        split16(w, q8_scale(261 - qe), hi, lo);
+        tmem_st4(tq + 4 * c, __uint_as_float(hi.x), __uint_as_float(hi.y), __uint_as_float(hi.z),
+                 __uint_as_float(hi.w));
+        tmem_st4(tq + D / 4 + 4 * c, __uint_as_float(lo.x), __uint_as_float(lo.y),
+                 __uint_as_float(lo.z), __uint_as_float(lo.w));
       }
+      tmem_wait_st();
+      fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(BAR_Q_FULL));
       // Before P of tile t is written: the stream's product before is done; the
       // maximum is raised to X where X passes m by the headroom (or m is none),
       // the sum and the accumulator are rescaled.
@@ -493,35 +509,61 @@ q8_rows_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
       for (int t = 0; t < ntiles; ++t) {
         const bool is_tree = t >= n_pre;
         const int nvalid = is_tree ? a.R : valid_of(t);
-        if (!__all_sync(kFull, mbar_wait(bar(BAR_S_FULL), t & 1)) ||
-            __any_sync(kFull, flags[1] != 0)) {
+        if (!__all_sync(kFull, mbar_wait(bar(BAR_S_FULL), t & 1))) {
           failed = true;
           break;
         }
         fence_after();
-        if (!is_tree && nvalid == kKeys) {
-          // 64 keys of one block: one factor and one offset.  (An offset below
-          // -60 puts P under fp16's range: its exact value does not matter, and
-          // the sum stays within fp32.)
-          const float f = c2 * q8_scale(kex[2 * t + h]);
-          const int d = max((int)vex[2 * t + h] - 127 - U + kHeadroom, -60);
-          float v[64];
-          tmem_ld32(ts, *(float(*)[32])v);
-          tmem_ld32(ts + 32, *(float(*)[32])(v + 32));
-          tmem_wait_ld();
-          scores_read();
-          float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        const int nv = min(nvalid - 64 * h, 64);   // keys of this half
+        float v[64];
+        tmem_ld32(ts, *(float(*)[32])v);
+        tmem_ld32(ts + 32, *(float(*)[32])(v + 32));
+        tmem_wait_ld();
+        scores_read();
+        // x = f v + off.  A prefix block has one factor and one offset.  (Not 0, so
+        // that -inf stays -inf; an offset below -60 puts P under fp16's range: its
+        // exact value does not matter, and the sum stays within fp32.)
+        float f = 1.f;
+        int d = 0;
+        if (!is_tree) {
+          f = c2 * q8_scale(kex[2 * t + h]);
+          f = f == 0.f ? 1.17549435e-38f : f;
+          d = max((int)vex[2 * t + h] - 127 - U + kHeadroom, -60);
+          if (nv < 64) {
 #pragma unroll
-          for (int i = 0; i < 64; i += 8)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) top[j] = max3f(top[j], v[i + 2 * j], v[i + 2 * j + 1]);
-          if (!raise(f * fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])), t)) {
-            failed = true;
-            break;
+            for (int i = 0; i < 64; ++i)
+              if (i >= nv) v[i] = -INFINITY;
           }
-          const float off = (float)d - (m == -INFINITY ? 0.f : m);
-          const float2 f2 = make_float2(f, f), o2 = make_float2(off, off);
-          float2 sa = make_float2(0.f, 0.f), sb = sa;
+        } else {
+          // scratch rows: a factor per key, and what this row sees (key 0: the root)
+          const uint64_t vis = nv <= 0 ? 0ull
+                               : (h == 0 ? (mask << 1) | 1ull : mask >> 63) & (~0ull >> (64 - nv));
+          const uint32_t vlo = (uint32_t)vis, vhi = (uint32_t)(vis >> 32);
+#pragma unroll
+          for (int i = 0; i < 64; i += 4) {
+            const float4 k4 = *(const float4*)(kt_out + 64 * h + i);
+            const float kf[4] = {k4.x, k4.y, k4.z, k4.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const uint32_t word = i + j < 32 ? vlo : vhi;
+              const bool sees = (word >> ((i + j) & 31)) & 1u;
+              v[i + j] = sees ? v[i + j] * (c2 * kf[j]) : -INFINITY;
+            }
+          }
+        }
+        float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int i = 0; i < 64; i += 8)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) top[j] = max3f(top[j], v[i + 2 * j], v[i + 2 * j + 1]);
+        if (!raise(f * fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])), t)) {
+          failed = true;
+          break;
+        }
+        const float off = (float)d - (m == -INFINITY ? 0.f : m);
+        const float2 f2 = make_float2(f, f), o2 = make_float2(off, off);
+        float2 sa = make_float2(0.f, 0.f), sb = sa;
+        auto weights = [&](auto scaled) {          // scaled: a factor per value row
 #pragma unroll
           for (int c = 0; c < 64; c += 32) {
             uint32_t w[16];
@@ -529,68 +571,26 @@ q8_rows_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
             for (int i = 0; i < 32; i += 4) {
               const float2 xa = __ffma2_rn(make_float2(v[c + i], v[c + i + 1]), f2, o2);
               const float2 xb = __ffma2_rn(make_float2(v[c + i + 2], v[c + i + 3]), f2, o2);
-              const float2 pa = make_float2(ex2(xa.x), ex2(xa.y));
-              const float2 pb = make_float2(ex2(xb.x), ex2(xb.y));
+              float2 pa = make_float2(ex2(xa.x), ex2(xa.y));
+              float2 pb = make_float2(ex2(xb.x), ex2(xb.y));
               sa = __fadd2_rn(sa, pa);
               sb = __fadd2_rn(sb, pb);
+              if constexpr (decltype(scaled)::value) {
+                const int4 u = *(const int4*)(vt_u + 64 * h + c + i);
+                pa.x *= pow2i(u.x - U + kHeadroom);
+                pa.y *= pow2i(u.y - U + kHeadroom);
+                pb.x *= pow2i(u.z - U + kHeadroom);
+                pb.y *= pow2i(u.w - U + kHeadroom);
+              }
               w[i / 2] = pack_half2(pa.x, pa.y);
               w[i / 2 + 1] = pack_half2(pb.x, pb.y);
             }
             tmem_st16(tp + c / 2, w);
           }
-          l = fmaf((sa.x + sa.y) + (sb.x + sb.y), pow2i(-d), l);
-        } else {
-          // the scratch rows, or a tile that the prefix does not fill: masks,
-          // and for scratch rows a factor per key
-          const int nv = min(max(nvalid - 64 * h, 0), 64);
-          const float fb = is_tree ? 0.f : q8_scale(kex[2 * t + h]);
-          const float vb = is_tree ? 0.f : pow2i((int)vex[2 * t + h] - 127 - U + kHeadroom);
-          auto score = [&](float s, int i) {     // key i of this half
-            const int key = 64 * h + i;
-            const bool sees = i < nv &&
-                              (!is_tree || key == 0 || (((mask >> ((key - 1) & 63)) & 1ull) != 0));
-            return sees ? s * (c2 * (is_tree ? kt_out[key] : fb)) : -INFINITY;
-          };
-          float top = -INFINITY;
-#pragma unroll 1
-          for (int c = 0; c < nv; c += 8) {
-            float v[8];
-            tmem_ld8(ts + c, v);
-            tmem_wait_ld();
-#pragma unroll
-            for (int i = 0; i < 8; ++i) top = fmaxf(top, score(v[i], c + i));
-          }
-          if (!raise(top, t)) {
-            failed = true;
-            break;
-          }
-          const float mm = m == -INFINITY ? 0.f : m;
-#pragma unroll 1
-          for (int c = 0; c < 64; c += 32) {
-            uint32_t w[16];
-#pragma unroll
-            for (int e = 0; e < 32; e += 8) {
-              float v[8];
-              if (c + e < nv) {
-                tmem_ld8(ts + c + e, v);
-                tmem_wait_ld();
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                  const float pr = ex2(score(v[i], c + e + i) - mm);
-                  l += pr;
-                  v[i] = pr * (is_tree ? pow2i(vt_u[64 * h + c + e + i] - U + kHeadroom) : vb);
-                }
-              } else {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) v[i] = 0.f;
-              }
-#pragma unroll
-              for (int i = 0; i < 8; i += 2) w[(e + i) / 2] = pack_half2(v[i], v[i + 1]);
-            }
-            tmem_st16(tp + c / 2, w);
-          }
-          scores_read();
-        }
+        };
+        if (is_tree) weights(std::true_type{});
+        else weights(std::false_type{});
+        l = fmaf((sa.x + sa.y) + (sb.x + sb.y), pow2i(-d), l);
         tmem_wait_st();
         fence_before();
         __syncwarp();

@@ -72,16 +72,16 @@ __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
   const __half2 v = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&v);
 }
-// Largest finite magnitude of eight bf16 (bits, as the high half of an fp32),
-// and whether one is not finite.
-__device__ __forceinline__ void scan8(const uint4& w, uint32_t& top, bool& bad) {
-  const uint32_t v[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t a = (v[i] << 16) & 0x7fffffffu, b = v[i] & 0x7fff0000u;
-    bad |= a >= 0x7f800000u || b >= 0x7f800000u;
-    top = max(top, max(a >= 0x7f800000u ? 0u : a, b >= 0x7f800000u ? 0u : b));
-  }
+// Running largest magnitude of bf16 pairs, the even and the odd elements apart.
+__device__ __forceinline__ uint32_t top_pairs(uint32_t top, const uint4& w) {
+  top = __vmaxu2(top, w.x & 0x7fff7fffu);
+  top = __vmaxu2(top, w.y & 0x7fff7fffu);
+  top = __vmaxu2(top, w.z & 0x7fff7fffu);
+  return __vmaxu2(top, w.w & 0x7fff7fffu);
+}
+// The larger of the two, as fp32 bits (at least 0x7f800000: not finite).
+__device__ __forceinline__ uint32_t top_of(uint32_t pairs) {
+  return max(pairs << 16, pairs & 0xffff0000u);
 }
 // Eight bf16 times f as fp16.
 __device__ __forceinline__ uint4 scale8(const uint4& w, float f) {
@@ -96,54 +96,74 @@ __device__ __forceinline__ uint4 scale8(const uint4& w, float f) {
 // the scale and its inverse are normal numbers.
 __device__ __forceinline__ int row_exponent(uint32_t top) { return max((int)(top >> 23), 15); }
 
-// Scratch rows of (request b, head hk): eight lanes of the n threads per row.
-// Which ones some row sees, their factors, and (returned) this thread's largest
-// exponent of a value row.
+// Scratch rows of (request b, head hk): eight lanes of the n threads (at least
+// 192) per row.  Which ones some row sees, their factors, and (returned) this
+// thread's largest exponent of a value row.
 template <int D>
 __device__ __forceinline__ int scan_tree(const Q8AttnArgs& a, int b, int hk, int wt, int n,
                                          float* kt_in, float* vt_in, float* kt_out, int* vt_u) {
+  constexpr int NV = D / 64;           // 16-byte vectors per lane and row
+  constexpr int kRounds = 3;           // 65 rows x 8 lanes over 192 threads
   const int lane = threadIdx.x & 31;
-  int best = -1000;
   uint32_t lo = 0, hi = 0;
-  for (int r = lane; r < a.R; r += 32) {
-    const uint64_t m = r > 0 ? a.mask[(long)b * a.R + r] : 0ull;
+#pragma unroll
+  for (int i = 0; i < 3; ++i) {
+    const int r = lane + 32 * i;
+    const uint64_t m = r > 0 && r < a.R ? a.mask[(long)b * a.R + r] : 0ull;
     lo |= (uint32_t)m;
     hi |= (uint32_t)(m >> 32);
+  }
+  uint4 kw[kRounds][NV], vw[kRounds][NV];
+#pragma unroll
+  for (int i = 0; i < kRounds; ++i) {
+    const int x = wt + n * i, j = x >> 3, c = x & 7;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      kw[i][v] = vw[i][v] = make_uint4(0u, 0u, 0u, 0u);
+      if (j < a.R) {
+        const long row = (((long)b * a.R + j) * a.map.Hkv + hk) * (D / 8) + c * NV + v;
+        kw[i][v] = __ldg((const uint4*)a.kt + row);
+        vw[i][v] = __ldg((const uint4*)a.vt + row);
+      }
+    }
   }
   lo = __reduce_or_sync(kFull, lo);
   hi = __reduce_or_sync(kFull, hi);
   const uint64_t seen = ((uint64_t)hi << 32) | lo;
-  for (int x = wt; x < kKeys * 8; x += n) {
-    const int j = x >> 3, c = x & 7;
-    const bool live = j < a.R && (j == 0 || ((seen >> (j - 1)) & 1ull));
-    uint32_t kt = 0, vt = 0;
-    bool bad = false;
-    if (live) {
-      const long row = ((long)b * a.R + j) * a.map.Hkv + hk;
-      const uint4* kp = (const uint4*)((const __nv_bfloat16*)a.kt + row * D) + c * (D / 64);
-      const uint4* vp = (const uint4*)((const __nv_bfloat16*)a.vt + row * D) + c * (D / 64);
+  int best = -1000;
 #pragma unroll
-      for (int i = 0; i < D / 64; ++i) {
-        scan8(__ldg(kp + i), kt, bad);
-        scan8(__ldg(vp + i), vt, bad);
-      }
+  for (int i = 0; i < kRounds; ++i) {
+    const int x = wt + n * i, j = x >> 3, c = x & 7;
+    uint32_t kt = 0, vt = 0;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      kt = top_pairs(kt, kw[i][v]);
+      vt = top_pairs(vt, vw[i][v]);
     }
+    kt = top_of(kt);
+    vt = top_of(vt);
 #pragma unroll
     for (int o = 4; o > 0; o >>= 1) {
       kt = max(kt, __shfl_xor_sync(kFull, kt, o));
       vt = max(vt, __shfl_xor_sync(kFull, vt, o));
     }
-    const uint32_t any = __ballot_sync(kFull, bad);
-    bad = (any >> (lane & 24)) & 0xffu;
+    if (j >= a.R) continue;
+    const bool live = j == 0 || ((seen >> (j - 1)) & 1ull);
+    const bool bad = kt >= 0x7f800000u || vt >= 0x7f800000u;
     const int ek = row_exponent(kt), ev = row_exponent(vt);
     if (c == 0) {
       // K: 2^(7 - (e - 127)) and its inverse; V: 2^(8 - (e - 127))
       kt_in[j] = live && !bad ? q8_scale(261 - ek) : 0.f;
       vt_in[j] = live && !bad ? q8_scale(262 - ev) : 0.f;
       kt_out[j] = bad ? __int_as_float(0x7fffffff) : q8_scale(ek - 7);
-      vt_u[j] = live ? ev - 135 : -900;
+      vt_u[j] = live && !bad ? ev - 135 : -900;
     }
-    if (live) best = max(best, ev - 135);
+    if (live && !bad) best = max(best, ev - 135);
+  }
+  for (int j = a.R + wt; j < kKeys; j += n) {      // rows that do not exist
+    kt_in[j] = vt_in[j] = 0.f;
+    kt_out[j] = 1.f;
+    vt_u[j] = -900;
   }
   return best;
 }
@@ -155,12 +175,10 @@ __device__ __forceinline__ void stage_q(const Q8AttnArgs& a, int b, int hk, int 
                                         int rows_here, int n_rows, int tid, int n, uint8_t* hi_tile,
                                         uint8_t* lo_tile, float* c2v) {
   constexpr int QL = D / 16;
-  const int lane = threadIdx.x & 31;
   for (int x = tid; x < n_rows * QL; x += n) {       // (whole warps: n_rows is a multiple of 16)
     const int r = x / QL, c = x % QL;
     uint4 w[2] = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
     uint32_t top = 0;
-    bool bad = false;
     if (r < rows_here) {
       const int p = row_base + r;
       const int tr = p / a.g, qh = hk * a.g + p % a.g;
@@ -169,13 +187,13 @@ __device__ __forceinline__ void stage_q(const Q8AttnArgs& a, int b, int hk, int 
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         w[i] = __ldg(qp + i);
-        scan8(w[i], top, bad);
+        top = top_pairs(top, w[i]);
       }
     }
+    top = top_of(top);
 #pragma unroll
     for (int o = QL / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(kFull, top, o));
-    const uint32_t any = __ballot_sync(kFull, bad);
-    bad = (any >> (lane & (32 - QL))) & ((1u << QL) - 1u);
+    const bool bad = top >= 0x7f800000u;
     const int e = row_exponent(top);
     uint4 hi = make_uint4(0u, 0u, 0u, 0u), lo = hi;
     if (!bad) split16(w, q8_scale(261 - e), hi, lo);
