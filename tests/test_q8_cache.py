@@ -197,7 +197,13 @@ class Setup:
         and the sums' last bits (fp32 sums of n terms: n 2^-24 more), and 2^-12 where
         it is rounded to fp16; a split's output is rounded to fp16 (2^-12) once
         more.  Means of v move by those shares of A = the weighted mean of |v|.  bf16 outputs are
-        rounded once: 2^-8 of the value (fp32: 2^-24)."""
+        rounded once: 2^-8 of the value (fp32: 2^-24).
+        fp16 has a smallest step, 2^-24, and a probability p is held as p 2^(u - U + 7), u the
+        exponent of its value row and U the largest one: half a step is 2^-25, worth 2^-25
+        2^(U - 7) |code| <= 2^-32 2^U 512 of the sum over p v, whose divisor is at least 1 (the
+        running maximum is at most the largest score).  So n keys add at most n 2^-32 top, with
+        top = 512 * 2^U, or twice the largest scratch value; a split's output over 2^U, rounded
+        to at least 2^-25, stays below one key's share."""
         g = self.Hq // self.Hkv
         for b in requests if requests is not None else range(self.B):
             P = min(self.lens[b], self.cap)
@@ -218,7 +224,13 @@ class Setup:
                 fine = o.isfinite().all(-1)
                 low = 2.0 ** -8 if self.dt == torch.bfloat16 else 2.0 ** -24
                 p16 = 2.0 ** -11 if self.dt == torch.bfloat16 else 0.0
-                tol = low * o.abs() + (rel + p16)[:, None] * A * 1.01 + 1e-37
+                which = "k" if self.latent else "v"
+                vt = (self.kt if self.latent else self.vt)[b, :, h, : self.dv].double()
+                top = 2 * float(vt[vt.isfinite()].abs().max()) if p16 else 0.0
+                if p16 and P:
+                    e = self.cache(which).exps(b, h)[: -(-P // BLOCK)]
+                    top = max(top, 512 * 2.0 ** (int(e.max()) - 127))
+                tol = low * o.abs() + (rel + p16)[:, None] * A * 1.01 + n * 2.0 ** -32 * top + 1e-37
                 assert not got[fine].isnan().any()
                 bad = ((got - o).abs() > tol)[fine]
                 assert not bad.any(), (b, h, float(((got - o).abs() / tol)[fine].max()))

@@ -35,13 +35,6 @@ __device__ __forceinline__ void load4(const float* p, float (&x)[4]) {
   const float4 v = __ldg((const float4*)p);
   x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
 }
-__device__ __forceinline__ void load4(const __nv_bfloat16* p, float (&x)[4]) {
-  const uint2 v = __ldg((const uint2*)p);
-  x[0] = __uint_as_float(v.x << 16);
-  x[1] = __uint_as_float(v.x & 0xffff0000u);
-  x[2] = __uint_as_float(v.y << 16);
-  x[3] = __uint_as_float(v.y & 0xffff0000u);
-}
 __device__ __forceinline__ void store_out(float* p, float x) { *p = x; }
 __device__ __forceinline__ void store_out(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
 
@@ -306,13 +299,23 @@ __global__ void __launch_bounds__(128) q8_combine_kernel(const __grid_constant__
 Q8Plan plan_q8(const tsd_attn_desc& d) {
   Q8Plan p{};
   const int M = d.R * (d.Hq / d.Hkv);
-  if (d.dtype == TSD_BF16 && !d.v_aliases_k) {
+  if (d.dtype == TSD_BF16) {
     // tcgen05: few packed rows on the columns, more on the lanes, in equal
-    // groups of at most 128 per CTA
-    p.path = M <= kQ8FewRows ? kQ8Few : kQ8Rows;
+    // groups of at most 128 per CTA; latent heads 64 per CTA
     p.part_bytes = 2;
-    p.nrg = (int)ceil_div(M, 128);
-    p.rb = p.path == kQ8Few ? (int)ceil_div(M, 16) * 16 : (int)ceil_div(M, p.nrg);
+    if (d.v_aliases_k) {
+      p.path = kQ8Latent;
+      p.rb = 64;
+      p.nrg = (int)ceil_div(M, 64);
+    } else if (M <= kQ8FewRows) {
+      p.path = kQ8Few;
+      p.nrg = 1;
+      p.rb = (int)ceil_div(M, 16) * 16;
+    } else {
+      p.path = kQ8Rows;
+      p.nrg = (int)ceil_div(M, 128);
+      p.rb = (int)ceil_div(M, p.nrg);
+    }
     // One CTA per SM.  The split count minimises the modelled time of requests
     // that fill the cache: waves of CTAs times (tiles of a CTA + 4 for its
     // set-up and epilogue).
@@ -420,15 +423,16 @@ extern "C" tsd_status tsd_tree_verify_attn_q8(const tsd_attn_desc* d, const void
   a.tree_split = p.tree_split;
   a.qscale = d->scale * 1.4426950408889634f;
   const cudaStream_t st = (cudaStream_t)stream;
-  const bool f32 = d->dtype == TSD_F32;
-  if (p.path == kQ8Few || p.path == kQ8Rows) {
-    if (!(p.path == kQ8Few ? launch_q8_few(*d, a, p, st) : launch_q8_rows(*d, a, p, st)))
-      return TSD_ERR_UNSUPPORTED;
-    if (d->dv == 128) launch_combine<__nv_bfloat16, 128, __half>(a, p, st);
+  if (p.path != kQ8Simt) {
+    const bool launched = p.path == kQ8Latent ? launch_q8_latent(*d, a, p, st)
+                          : p.path == kQ8Few  ? launch_q8_few(*d, a, p, st)
+                                              : launch_q8_rows(*d, a, p, st);
+    if (!launched) return TSD_ERR_UNSUPPORTED;
+    if (alias) launch_combine<__nv_bfloat16, 512, __half>(a, p, st);
+    else if (d->dv == 128) launch_combine<__nv_bfloat16, 128, __half>(a, p, st);
     else launch_combine<__nv_bfloat16, 64, __half>(a, p, st);
   } else if (alias) {
-    if (f32) launch_simt<float, 576, 512, 2, true>(a, p, st);
-    else launch_simt<__nv_bfloat16, 576, 512, 2, true>(a, p, st);
+    launch_simt<float, 576, 512, 2, true>(a, p, st);
   } else if (d->dk == 128) {
     launch_simt<float, 128, 128, 4, false>(a, p, st);
   } else {

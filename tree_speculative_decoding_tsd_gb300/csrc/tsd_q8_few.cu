@@ -703,7 +703,7 @@ bool launch_d(const CUtensorMap& m, const Q8AttnArgs& a, const Q8Plan& p, cudaSt
 
 bool launch_q8_few(const tsd_attn_desc& d, const Q8AttnArgs& a, const Q8Plan& p, cudaStream_t st) {
   CUtensorMap m;
-  if (encode_fn() == nullptr || !encode_keys(&m, a, d.dk)) return false;
+  if (encode_fn() == nullptr || !encode_keys(&m, a, d.dk, d.dk)) return false;
   return d.dk == 128 ? launch_d<128>(m, a, p, st) : launch_d<64>(m, a, p, st);
 }
 

@@ -682,7 +682,7 @@ void launch_rows(const CUtensorMap& kmap, const Q8AttnArgs& a, const Q8Plan& p, 
 
 bool launch_q8_rows(const tsd_attn_desc& d, const Q8AttnArgs& a, const Q8Plan& p, cudaStream_t st) {
   CUtensorMap m;
-  if (encode_fn() == nullptr || !encode_keys(&m, a, d.dk)) return false;
+  if (encode_fn() == nullptr || !encode_keys(&m, a, d.dk, d.dk)) return false;
   if (d.dk == 128) launch_rows<128>(m, a, p, st);
   else launch_rows<64>(m, a, p, st);
   return true;

@@ -253,19 +253,20 @@ __device__ __forceinline__ void load_keys(const Q8AttnArgs& a, const CUtensorMap
   tma_3d(dst, &kmap, 0, y, z, full);
 }
 
-// K codes as (dims, rows of a head, heads): rows are those of a request's head,
-// or of a page's.
-bool encode_keys(CUtensorMap* m, const Q8AttnArgs& a, int D) {
+// K codes of D dims as (dims, rows of a head, heads), in boxes of 128 rows and 128
+// or 64 dims (swizzled to their width): rows are those of a request's head, or of a
+// page's.
+bool encode_keys(CUtensorMap* m, const Q8AttnArgs& a, int D, int width) {
   const long rows = a.map.page_size > 0 ? a.map.page_size : a.map.cap;
   const long heads = (a.map.page_size > 0 ? (long)a.map.num_pages : (long)a.B) * a.map.Hkv;
   if (heads > 0x7fffffffl) return false;
   const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)rows, (cuuint64_t)heads};
   const cuuint64_t strides[2] = {(cuuint64_t)D, (cuuint64_t)rows * D};
-  const cuuint32_t box[3] = {(cuuint32_t)D, (cuuint32_t)kKeys, 1};
+  const cuuint32_t box[3] = {(cuuint32_t)width, (cuuint32_t)kKeys, 1};
   const cuuint32_t es[3] = {1, 1, 1};
   return encode_fn()(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<uint8_t*>(a.kc), dims, strides,
                      box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                     D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                     width == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
                      CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
