@@ -179,6 +179,7 @@ tsd_status weights_impl(const tsd_attn_desc* d, int S, const void* q, const void
   a.qscale = d->scale * kLog2e;
   const cudaStream_t st = (cudaStream_t)stream;
   const bool f32 = d->dtype == TSD_F32;
+  if (launch_weights_tc(*d, a, st)) return cuda_status();
   if (d->dk == 576) {
     if (f32) launch_simt<float, 576>(*d, a, st);
     else launch_simt<__nv_bfloat16, 576>(*d, a, st);
