@@ -26,7 +26,7 @@ namespace {
 
 constexpr int kSumWarps = 8, kMma = 8, kTma = 9;
 constexpr int kThreads = 10 * 32;
-constexpr int kMaxCols = 288, kBufCols = 256;
+constexpr int kMaxCols = 288;
 constexpr int kMaxRing = 12;
 
 struct WeightSmem {        // behind the ring and Q
@@ -46,8 +46,10 @@ struct WeightPlan {
   int cols, ring;          // columns at most (a multiple of 16); K slots
 };
 
-template <int D, bool kQ8>
-__global__ void __launch_bounds__(kThreads, 1)
+// kBufCols: columns of a score buffer; 128 where the columns fit, so that two CTAs
+// share an SM (one's set-up behind the other's work), else 256.
+template <int D, bool kQ8, int kBufCols>
+__global__ void __launch_bounds__(kThreads, kBufCols == 128 ? 2 : 1)
 weights_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ WeightArgs a,
                   WeightPlan p) {
   constexpr uint32_t kTileBytes = kWeightKeys * D * (kQ8 ? 1 : 2);
@@ -114,8 +116,8 @@ weights_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
     }
     __syncwarp();
   } else if (warp == kMma) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;\n" ::"r"(
-        su32(&s.tmem)));
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;\n" ::"r"(
+        su32(&s.tmem)), "n"(2 * kBufCols));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n");
   } else {
     // Q: the path's rows, D / 16 lanes each, 16 elements a lane
@@ -351,7 +353,8 @@ weights_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
   fence_after();
   if (warp == kMma) {
     __syncwarp();
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;\n" ::"r"(tmem));
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;\n" ::"r"(tmem),
+                 "n"(2 * kBufCols));
   }
 }
 
@@ -381,30 +384,37 @@ bool encode_cache(CUtensorMap* m, const WeightArgs& a, int B, int D, bool q8) {
                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D, bool kQ8>
-bool launch_d(const tsd_attn_desc& d, const WeightArgs& a, cudaStream_t st) {
+template <int D, bool kQ8, int kBufCols>
+bool launch_d(const tsd_attn_desc& d, const WeightArgs& a, int cols, cudaStream_t st) {
   CUtensorMap m;
   if (!encode_cache(&m, a, d.B, D, kQ8)) return false;
+  constexpr int kPerSm = kBufCols == 128 ? 2 : 1;
   WeightPlan p{};
-  p.cols = (int)ceil_div((long)(a.S + 1) * a.g, 16) * 16;
-  const long tile = kWeightKeys * D * (kQ8 ? 1 : 2), q = (long)p.cols * D * 2;
-  p.ring = (int)((220 * 1024 - q - (long)sizeof(WeightSmem)) / tile);
+  p.cols = cols;
+  const long tile = kWeightKeys * D * (kQ8 ? 1 : 2), q = (long)cols * D * 2;
+  p.ring = (int)((220 * 1024 / kPerSm - q - (long)sizeof(WeightSmem) - 1024) / tile);
   if (p.ring > kMaxRing) p.ring = kMaxRing;
-  // One CTA per SM: splits as for the attention, a CTA's set-up worth about six
-  // of its tiles.
+  // Splits as for the attention: waves of CTAs times (tiles of a CTA and about six
+  // more for its set-up).
   const long units = (long)d.B * d.Hkv, tiles = ceil_div(d.cap, kWeightKeys);
   long best = -1;
   for (long n = 1; n <= 64 && n <= tiles; ++n) {
     const long per = ceil_div(tiles, n);
-    const long cost = ceil_div(units * ceil_div(tiles, per), 152L) * (per + 6);
+    const long cost = ceil_div(units * ceil_div(tiles, per), 152L * kPerSm) * (per + 6);
     if (best < 0 || cost < best) { best = cost; p.tiles = (int)per; }
   }
   p.nsplit = (int)ceil_div(tiles, p.tiles);
   const size_t smem = (size_t)p.ring * tile + q + sizeof(WeightSmem) + 1024;
-  const auto kern = weights_tc_kernel<D, kQ8>;
+  const auto kern = weights_tc_kernel<D, kQ8, kBufCols>;
   cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   launch(kern, dim3(p.nsplit, d.Hkv, d.B), dim3(kThreads), smem, st, m, a, p);
   return true;
+}
+
+template <int D, bool kQ8>
+bool launch_cols(const tsd_attn_desc& d, const WeightArgs& a, cudaStream_t st) {
+  const int cols = (int)ceil_div((long)(a.S + 1) * a.g, 16) * 16;
+  return cols <= 128 ? launch_d<D, kQ8, 128>(d, a, cols, st) : launch_d<D, kQ8, 256>(d, a, cols, st);
 }
 
 }  // namespace
@@ -413,8 +423,8 @@ bool launch_weights_tc(const tsd_attn_desc& d, const WeightArgs& a, cudaStream_t
   if (d.dtype != TSD_BF16 || (d.dk != 64 && d.dk != 128)) return false;
   if ((long)(a.S + 1) * a.g > kMaxCols || encode_fn() == nullptr) return false;
   if (d.dk == 128)
-    return a.ke != nullptr ? launch_d<128, true>(d, a, st) : launch_d<128, false>(d, a, st);
-  return a.ke != nullptr ? launch_d<64, true>(d, a, st) : launch_d<64, false>(d, a, st);
+    return a.ke != nullptr ? launch_cols<128, true>(d, a, st) : launch_cols<128, false>(d, a, st);
+  return a.ke != nullptr ? launch_cols<64, true>(d, a, st) : launch_cols<64, false>(d, a, st);
 }
 
 }  // namespace tsd
