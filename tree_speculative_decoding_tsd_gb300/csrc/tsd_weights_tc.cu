@@ -70,28 +70,18 @@ weights_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int sp = blockIdx.x, hk = blockIdx.y, b = blockIdx.z;
   const int P = a.plen[b];
-  const int total = P > 0 ? (int)min(((long)P + kWeightKeys - 1) / kWeightKeys, (long)p.nsplit * p.tiles) : 0;
+  const int total = P > 0 ? (min(P, a.map.cap) + kWeightKeys - 1) / kWeightKeys : 0;
   const int t0 = sp * p.tiles, n_pre = max(min(total - t0, p.tiles), 0);
   // the first CTA behind or at the end of the prefix takes the path's rows
   const bool with_path = sp == max((total + p.tiles - 1) / p.tiles - 1, 0);
   if (n_pre == 0 && !with_path) return;
   const int slots0 = with_path ? kPathSlots : 0;            // ring slots taken before the prefix
-  const int L = weight_path(a, b, P, s.path);
-  if (L < 0) {                                              // the whole request is skipped
-    if (with_path && tid == 0) report_error(a.err, -L, b);
-    return;
-  }
-  const int ncol = (L + 1) * a.g, pad = (ncol + 15) / 16 * 16;
-  const int ntiles = n_pre + (with_path ? 1 : 0);           // tile 0 is the path's, if any
-  const int chunks = (pad + kBufCols - 1) / kBufCols;       // of columns
   const long head = (long)b * a.map.Hkv + hk;
-
-  // ---------------------------------------------------------------- set-up
   auto load_k = [&](int t) {                                // prefix tile t of this CTA
     const int pos = (t0 + t) * kWeightKeys, g = slots0 + t, sl = g % p.ring;
     int y = pos, z = (int)head;
     if (a.map.page_size) {
-      const long r = a.map.row(b, hk, pos);                 // (checked by weight_path)
+      const long r = max(a.map.row(b, hk, pos), 0l);        // (weight_path refuses missing pages)
       y = (int)(r % a.map.page_size);
       z = (int)(r / a.map.page_size);
     }
@@ -99,27 +89,39 @@ weights_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
     if (kQ8) tma_3d(sbase + sl * kTileBytes, &kmap, 0, y, z, bar(BAR_FULL + sl));
     else tma_4d(sbase + sl * kTileBytes, &kmap, 0, y, z, 0, bar(BAR_FULL + sl));
   };
-  if (warp == kTma) {
-    if (lane == 0) {
-      for (int i = 0; i < p.ring; ++i) {
-        mbar_init(bar(BAR_FULL + i), 1);
-        mbar_init(bar(BAR_EMPTY + i), 1);
-      }
-      for (int i = 0; i < 2; ++i) {
-        mbar_init(bar(BAR_S_FULL + i), 1);
-        mbar_init(bar(BAR_S_EMPTY + i), 4);
-      }
-      mbar_init(bar(BAR_FINAL), 1);
-      *abort = 0;
-      asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
-      for (int t = 0; t < n_pre && slots0 + t < p.ring; ++t) load_k(t);
+  // The first K tiles are on their way before the path is known.
+  const int early = min(n_pre, p.ring - slots0);
+  if (tid == kTma * 32) {
+    for (int i = 0; i < p.ring; ++i) {
+      mbar_init(bar(BAR_FULL + i), 1);
+      mbar_init(bar(BAR_EMPTY + i), 1);
     }
-    __syncwarp();
-  } else if (warp == kMma) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar(BAR_S_FULL + i), 1);
+      mbar_init(bar(BAR_S_EMPTY + i), 4);
+    }
+    mbar_init(bar(BAR_FINAL), 1);
+    *abort = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
+    for (int t = 0; t < early; ++t) load_k(t);
+  }
+  const int L = weight_path(a, b, P, s.path);
+  if (L < 0) {                                              // the whole request is skipped
+    if (with_path && tid == 0) report_error(a.err, -L, b);
+    if (tid == kTma * 32)
+      for (int t = 0; t < early; ++t) mbar_wait(bar(BAR_FULL + slots0 + t), 0);
+    return;
+  }
+  const int ncol = (L + 1) * a.g, pad = (ncol + 15) / 16 * 16;
+  const int ntiles = n_pre + (with_path ? 1 : 0);           // tile 0 is the path's, if any
+  const int chunks = (pad + kBufCols - 1) / kBufCols;       // of columns
+
+  // ---------------------------------------------------------------- set-up
+  if (warp == kMma) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;\n" ::"r"(
         su32(&s.tmem)), "n"(2 * kBufCols));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n");
-  } else {
+  } else if (warp < kSumWarps) {
     // Q: the path's rows, D / 16 lanes each, 16 elements a lane
     constexpr int QL = D / 16;
     for (int x = tid; x < pad * QL; x += kSumWarps * 32) {  // (whole warps)
@@ -196,7 +198,7 @@ weights_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
   // -------------------------------------------------------------- K tiles
   if (warp == kTma) {
     if (lane == 0) {
-      int loaded = min(n_pre, p.ring - slots0);             // by the set-up
+      int loaded = early;
       for (int t = loaded; t < n_pre && !*abort; ++t) {
         const int g = slots0 + t;
         if (!mbar_wait(bar(BAR_EMPTY + g % p.ring), (g / p.ring - 1) & 1)) {
