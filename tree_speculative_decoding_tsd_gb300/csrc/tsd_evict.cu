@@ -10,21 +10,21 @@
 // rows a round) only as many rows move as arrived.  Attention does not depend
 // on the order of the cached rows; `pos` carries each row's token position.
 //
-// select_kernel, one CTA per (head, request): the keep-th largest 32-bit key by
-// four 8-bit histogram rounds.  The histograms are private to each lane (bin x
-// lane, so a warp's 32 counts never meet in a bank, and equal exponents, the
-// usual case for weights, do not serialise); then ties, holes and movers are
-// numbered by ballots and one scan over the warps.  A warp takes consecutive
-// rows and keeps their keys in registers (up to 32 per thread; longer caches
-// are read again by each round).  Bounded by latency: four rounds over 8 bytes
-// a row.
+// select_kernel, a cluster of 1 to 8 CTAs per (head, request): the keep-th largest
+// 32-bit key by four 8-bit histogram rounds.  The histograms are private to 16 lanes
+// of a warp (bin x lane, so that equal exponents, the usual case for weights, meet
+// in pairs only); the CTAs of a cluster exchange their 256 totals through distributed
+// shared memory.  Then ties, holes and movers are numbered by ballots and sums over
+// warps and CTAs.  A warp takes consecutive rows and keeps their keys in registers
+// (up to 16 per thread; longer caches are read again by each round).  Bounded by
+// latency: four rounds over 8 bytes a row.
 //
-// move_kernel: 16-byte vectors, one row (K and V) per warp and step, four
-// steps in flight.  move_q8_kernel: one CTA per block of 64 places, because an
-// incoming row with a larger exponent raises the block's:
+// move_kernel: a warp takes 32 moves, eight of them (K and V, 4 KB) in flight.
+// move_q8_kernel: one CTA per block of 64 places, because an incoming row with a
+// larger exponent raises the block's:
 //   e' = max of the exponents that the block's rows had before the call,
-// and every code c becomes e4m3(c * 2^(e - e')).  Both are bounded by memory:
-// each moved row is read and written once.
+// and every code c becomes e4m3(c * 2^(e - e')).  Both are bounded by memory: each
+// moved row is read and written once.
 #include <cuda_bf16.h>
 
 #include "tsd_host.h"
@@ -33,7 +33,7 @@
 namespace tsd {
 namespace {
 
-constexpr int kSelThreads = 1024, kSelWarps = 32;
+constexpr int kSelThreads = 512, kSelWarps = 16, kSelLanes = 16, kMaxCluster = 8;
 
 struct EvictArgs {
   float* acc;
@@ -58,57 +58,83 @@ struct EvictArgs {
   int list, nblk;
 };
 
-// Exclusive sum over the 32 warps of one value per warp; `total` gets the sum.
-__device__ __forceinline__ int warps_before(int v, int* sm, int warp, int lane, int& total) {
+// Shared memory of a CTA, and of the others of its cluster by rank.
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;\n" ::: "memory");
+}
+__device__ __forceinline__ void store_at(const void* local, int rank, uint32_t v) {
+  const uint32_t a = (uint32_t)__cvta_generic_to_shared(local);
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;\n" : "=r"(r) : "r"(a), "r"(rank));
+  asm volatile("st.shared::cluster.u32 [%0], %1;\n" ::"r"(r), "r"(v) : "memory");
+}
+
+struct SelectSmem {
+  uint32_t hist[256 * kSelLanes];
+  uint32_t totals[2][kMaxCluster][256];       // by rank, two sets in turn
+  uint32_t counts[3][kMaxCluster];            // ties, holes, movers by rank
+  uint32_t bins[256];
+  int warps[2][kSelWarps];
+  uint32_t prefix, need;
+  int bad;
+};
+
+// Exclusive sums over the warps of two values per warp (the same on all lanes).
+__device__ __forceinline__ void warps_before(SelectSmem& s, int warp, int lane, int x, int y,
+                                             int& bx, int& by, int& tx, int& ty) {
   __syncthreads();
-  if (lane == 0) sm[warp] = v;
+  if (lane == 0) {
+    s.warps[0][warp] = x;
+    s.warps[1][warp] = y;
+  }
   __syncthreads();
-  const int x = sm[lane];
-  total = __reduce_add_sync(kFull, x);
-  return __reduce_add_sync(kFull, lane < warp ? x : 0);
+  const int u = lane < kSelWarps ? s.warps[0][lane] : 0, v = lane < kSelWarps ? s.warps[1][lane] : 0;
+  tx = __reduce_add_sync(kFull, u);
+  ty = __reduce_add_sync(kFull, v);
+  bx = __reduce_add_sync(kFull, lane < warp ? u : 0);
+  by = __reduce_add_sync(kFull, lane < warp ? v : 0);
 }
 
 template <int ITEMS, bool kQ8>
-__global__ void __launch_bounds__(kSelThreads, 1)
+__global__ void __launch_bounds__(kSelThreads, 2)
 select_kernel(const __grid_constant__ EvictArgs a) {
-  __shared__ uint32_t hist[256 * 32];
-  __shared__ int sums[kSelWarps];
-  __shared__ uint32_t total_of[256];
-  __shared__ uint32_t s_prefix, s_need;
-  __shared__ int s_bad;
+  __shared__ SelectSmem s;
   constexpr int kSpan = kSelThreads * ITEMS;
   grid_dependency_sync();
-  const int h = blockIdx.x, b = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int ranks = gridDim.x, rank = blockIdx.x;           // the cluster spans grid x
+  const int h = blockIdx.y, b = blockIdx.z, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const long bh = (long)b * a.map.Hkv + h;
+  const float* acc = a.acc + bh * a.map.cap;
+  const int32_t* pos = a.pos + bh * a.map.cap;
   const int P = a.prefix_len[b];
-  if (tid == 0) s_bad = 0;
+  const long recent0 = (long)a.seen[bh] - a.recent;
+  if (tid == 0) s.bad = 0;
   __syncthreads();
   if (P < 0 || P > a.map.cap) {
-    if (tid == 0) s_bad = TSD_DEV_ERR_CAPACITY;
+    if (tid == 0) s.bad = TSD_DEV_ERR_CAPACITY;
   } else if (a.map.page_size && P > a.keep) {
     for (int p = tid; p < (P + a.map.page_size - 1) / a.map.page_size; p += kSelThreads) {
       const int pg = a.map.page_table[(long)b * a.map.max_pages + p];
-      if (pg < 0 || pg >= a.map.num_pages) s_bad = TSD_DEV_ERR_BAD_PAGE;
+      if (pg < 0 || pg >= a.map.num_pages) s.bad = TSD_DEV_ERR_BAD_PAGE;
     }
   }
   __syncthreads();
-  if (s_bad != 0 || P <= a.keep) {
-    if (tid == 0) {
+  if (s.bad != 0 || P <= a.keep) {                          // (the same in every CTA of the cluster)
+    if (tid == 0 && rank == 0) {
       a.count[bh] = -1;
-      if (s_bad != 0) report_error(a.err, s_bad, b);
+      if (s.bad != 0) report_error(a.err, s.bad, b);
     }
     return;
   }
-  const float* acc = a.acc + bh * a.map.cap;
-  const int32_t* pos = a.pos + bh * a.map.cap;
-  const long recent0 = (long)a.seen[bh] - a.recent;
-  const int rounds = (P + kSpan - 1) / kSpan;
+  // this CTA's rows: `rounds` spans from `begin`
+  const int rounds = (P + ranks * kSpan - 1) / (ranks * kSpan);
+  const int begin = rank * rounds * kSpan;
 
-  // keys of the rows base + 32 it + lane of one span (0 past the end)
+  // keys of the rows base + 32 it + lane of span r (0 past the end)
   uint32_t key[ITEMS];
   auto load = [&](int r) {
-    const int base = r * kSpan + warp * 32 * ITEMS + lane;
-    constexpr int kBatch = ITEMS < 8 ? ITEMS : 8;     // loads in flight per thread and array
+    const int base = begin + r * kSpan + warp * 32 * ITEMS + lane;
+    constexpr int kBatch = ITEMS < 8 ? ITEMS : 8;           // loads in flight per thread and array
 #pragma unroll
     for (int i0 = 0; i0 < ITEMS; i0 += kBatch) {
       float w[kBatch];
@@ -132,19 +158,22 @@ select_kernel(const __grid_constant__ EvictArgs a) {
   load(0);
 
   if constexpr (kQ8) {   // the exponents of before, which the moves read while others write
-    for (int j = tid; j * kQ8Block < P; j += kSelThreads) {
+    for (int j = rank * kSelThreads + tid; j * (long)kQ8Block < P; j += ranks * kSelThreads) {
       const long e = a.map.block(b, h, j * kQ8Block);
       a.kexp_old[bh * a.nblk + j] = a.kexp[e];
       if (a.vrow) a.vexp_old[bh * a.nblk + j] = a.vexp[e];
     }
   }
 
+  cluster_sync();        // (every CTA of the cluster runs: its shared memory may be written)
+
   // ---- the keep-th largest key: prefix holds its digits found so far, need
   // the rank of the key among those that share them
   uint32_t prefix = 0, need = (uint32_t)a.keep;
 #pragma unroll 1
   for (int shift = 24; shift >= 0; shift -= 8) {
-    for (int i = tid; i < 256 * 32; i += kSelThreads) hist[i] = 0;
+    const int set = (shift >> 3) & 1;
+    for (int i = tid; i < 64 * kSelLanes; i += kSelThreads) ((uint4*)s.hist)[i] = make_uint4(0u, 0u, 0u, 0u);
     __syncthreads();
     for (int r = 0; r < rounds; ++r) {
       if (rounds > 1) load(r);
@@ -152,21 +181,31 @@ select_kernel(const __grid_constant__ EvictArgs a) {
       for (int it = 0; it < ITEMS; ++it) {
         // (rows past the end have key 0 and are left out: a row's is at least 1)
         const bool in = key[it] != 0 && (shift == 24 || (key[it] >> (shift + 8)) == prefix);
-        if (in) atomicAdd(&hist[((key[it] >> shift) & 255u) * 32 + lane], 1u);
+        if (in) atomicAdd(&s.hist[((key[it] >> shift) & 255u) * kSelLanes + (lane & (kSelLanes - 1))], 1u);
       }
     }
     __syncthreads();
+    if (tid < 256) {
+      uint32_t t = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const uint32_t s = __reduce_add_sync(kFull, hist[(warp * 8 + i) * 32 + lane]);
-      if (lane == 0) total_of[warp * 8 + i] = s;
+      for (int i = 0; i < kSelLanes / 4; ++i) {
+        const uint4 v = ((const uint4*)s.hist)[tid * (kSelLanes / 4) + ((i + tid) & (kSelLanes / 4 - 1))];
+        t += v.x + v.y + v.z + v.w;
+      }
+      for (int k = 0; k < ranks; ++k) store_at(&s.totals[set][rank][tid], k, t);
+    }
+    cluster_sync();
+    if (tid < 256) {
+      uint32_t t = 0;
+      for (int k = 0; k < ranks; ++k) t += s.totals[set][k][tid];
+      s.bins[tid] = t;
     }
     __syncthreads();
     if (warp == 0) {       // lane l takes the bins 255 - 8l .. 248 - 8l, from the largest digit down
       uint32_t c[8], mine = 0;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        c[i] = total_of[255 - (8 * lane + i)];
+        c[i] = s.bins[255 - (8 * lane + i)];
         mine += c[i];
       }
       uint32_t incl = mine;
@@ -179,56 +218,108 @@ select_kernel(const __grid_constant__ EvictArgs a) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         if (before < need && need <= before + c[i]) {
-          s_prefix = (prefix << 8) | (uint32_t)(255 - (8 * lane + i));
-          s_need = need - before;
+          s.prefix = (prefix << 8) | (uint32_t)(255 - (8 * lane + i));
+          s.need = need - before;
         }
         before += c[i];
       }
     }
     __syncthreads();
-    prefix = s_prefix;
-    need = s_need;
+    prefix = s.prefix;
+    need = s.need;
   }
   const uint32_t cut = prefix;   // the smallest kept key; `need` rows that equal it stay
 
-  // ---- number the ties, then the holes and the movers, in index order
-  int ties_before = 0, holes_before = 0, movers_before = 0;
-#pragma unroll 1
-  for (int r = 0; r < rounds; ++r) {
-    if (rounds > 1) load(r);
-    const int base = r * kSpan + warp * 32 * ITEMS;
-    int t = 0;
-#pragma unroll
-    for (int it = 0; it < ITEMS; ++it) t += __popc(__ballot_sync(kFull, key[it] == cut));
-    int total;
-    int tie = ties_before + warps_before(t, sums, warp, lane, total);
-    ties_before += total;
-    uint32_t mine = 0;           // bit it: this lane's row of group it stays
-    int nh = 0, nm = 0;
+  // ---- number the ties, then the holes and the movers, in index order: counts of
+  // the CTA, then (of the cluster) what lies before it
+  int ties = 0, holes = 0, movers = 0;           // before the current span
+  auto share = [&](int which, uint32_t mine) {   // the CTA's count to every CTA
+    if (tid < ranks) store_at(&s.counts[which][rank], tid, mine);
+  };
+  auto before_rank = [&](int which, uint32_t& total) {
+    uint32_t x = 0, t = 0;
+    for (int k = 0; k < ranks; ++k) {
+      const uint32_t v = s.counts[which][k];
+      t += v;
+      if (k < rank) x += v;
+    }
+    total = t;
+    return (int)x;
+  };
+  uint32_t mine = 0;             // bit it: this lane's row of group it stays
+  int bx, by, tx, ty;
+  uint32_t total;
+  // what stays of span r (ties numbered from `tie`), and its holes and movers
+  auto keep_span = [&](int r, int tie, int& nh, int& nm) {
+    const int base = begin + r * kSpan + warp * 32 * ITEMS;
+    mine = 0;
+    nh = nm = 0;
 #pragma unroll
     for (int it = 0; it < ITEMS; ++it) {
       const uint32_t eq = __ballot_sync(kFull, key[it] == cut);
-      const int rank = tie + __popc(eq & ((1u << lane) - 1u));
-      const bool k = key[it] > cut || (key[it] == cut && rank < (int)need);
+      const int rank_of = tie + __popc(eq & ((1u << lane) - 1u));
+      const bool k = key[it] > cut || (key[it] == cut && rank_of < (int)need);
       const uint32_t kept = __ballot_sync(kFull, k);
       mine |= (uint32_t)k << it;
       tie += __popc(eq);
-      const int i0 = base + 32 * it;
-      const int below = min(max(a.keep - i0, 0), 32);          // positions of the 32 below keep
+      const int below = min(max(a.keep - (base + 32 * it), 0), 32);   // positions of the 32 below keep
       const uint32_t lo = below == 32 ? 0xffffffffu : (1u << below) - 1u;
       nh += __popc(~kept & lo);
       nm += __popc(kept & ~lo);
     }
-    int hole = holes_before + warps_before(nh, sums, warp, lane, total);
-    holes_before += total;
-    int mover = movers_before + warps_before(nm, sums, warp, lane, total);
-    movers_before += total;
+  };
+  auto span_ties = [&] {
+    int t = 0;
+#pragma unroll
+    for (int it = 0; it < ITEMS; ++it) t += __popc(__ballot_sync(kFull, key[it] == cut));
+    return t;
+  };
+  for (int r = 0; r < rounds; ++r) {
+    if (rounds > 1) load(r);
+    warps_before(s, warp, lane, span_ties(), 0, bx, by, tx, ty);
+    ties += tx;
+  }
+  share(0, ties);
+  cluster_sync();
+  const int ties0 = before_rank(0, total);
+  int nh = 0, nm = 0, tie = 0;
+  ties = ties0;
+  for (int r = 0; r < rounds; ++r) {
+    if (rounds > 1) load(r);
+    warps_before(s, warp, lane, span_ties(), 0, bx, by, tx, ty);
+    tie = ties + bx;
+    ties += tx;
+    keep_span(r, tie, nh, nm);
+    warps_before(s, warp, lane, nh, nm, bx, by, tx, ty);
+    holes += tx;
+    movers += ty;
+  }
+  share(1, holes);
+  share(2, movers);
+  cluster_sync();
+  holes = before_rank(1, total);
+  const uint32_t moved = total;
+  movers = before_rank(2, total);
+  ties = ties0;
+  for (int r = 0; r < rounds; ++r) {
+    if (rounds > 1) {
+      load(r);
+      warps_before(s, warp, lane, span_ties(), 0, bx, by, tx, ty);
+      tie = ties + bx;
+      ties += tx;
+      keep_span(r, tie, nh, nm);
+      warps_before(s, warp, lane, nh, nm, bx, by, tx, ty);
+    }
+    const int base = begin + r * kSpan + warp * 32 * ITEMS;
+    int hole = holes + bx, mover = movers + by;
+    holes += tx;
+    movers += ty;
 #pragma unroll
     for (int it = 0; it < ITEMS; ++it) {
+      const uint32_t kept = __ballot_sync(kFull, (mine >> it) & 1u);
       const int i0 = base + 32 * it, i = i0 + lane;
       const int below = min(max(a.keep - i0, 0), 32);
       const uint32_t lo = below == 32 ? 0xffffffffu : (1u << below) - 1u;
-      const uint32_t kept = __ballot_sync(kFull, (mine >> it) & 1u);
       const uint32_t hm = ~kept & lo, mm = kept & ~lo;
       const uint32_t lt = (1u << lane) - 1u;
       if (kQ8 && lane == 0 && i0 % kQ8Block == 0 && i0 / kQ8Block <= a.nblk)
@@ -239,11 +330,11 @@ select_kernel(const __grid_constant__ EvictArgs a) {
       mover += __popc(mm);
     }
   }
-  if (tid == 0) {
-    a.count[bh] = holes_before;
+  if (tid == 0 && rank == 0) {
+    a.count[bh] = (int)moved;
     if (kQ8) {      // the entry behind the last block of places (a span may end below it)
       const int j = (a.keep + kQ8Block - 1) / kQ8Block;
-      a.starts[bh * (a.nblk + 1) + j] = holes_before;
+      a.starts[bh * (a.nblk + 1) + j] = (int)moved;
     }
   }
 }
@@ -254,7 +345,7 @@ __device__ __forceinline__ void move_meta(const EvictArgs& a, long bh, int from,
   a.pos[bh * a.map.cap + to] = a.pos[bh * a.map.cap + from];
 }
 
-constexpr int kMoveThreads = 256, kMoveUnroll = 4;
+constexpr int kMoveThreads = 256, kMoveUnroll = 8;
 
 __global__ void __launch_bounds__(kMoveThreads) move_kernel(const __grid_constant__ EvictArgs a) {
   grid_dependency_sync();
@@ -264,32 +355,35 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(const __grid_constan
   if (n < 0) return;
   if (blockIdx.x == 0 && h == 0 && threadIdx.x == 0) a.prefix_len[b] = a.keep;
   const int kv = (int)(a.krow / 16), vv = (int)(a.vrow / 16);
-  const int step = gridDim.x * (kMoveThreads / 32);
-  for (int m0 = blockIdx.x * (kMoveThreads / 32) + warp; m0 < n; m0 += step * kMoveUnroll) {
-    long from[kMoveUnroll], to[kMoveUnroll];
-#pragma unroll
-    for (int u = 0; u < kMoveUnroll; ++u) {
-      const int m = m0 + u * step;
-      from[u] = -1;
-      if (m < n) {
-        const int f = a.movers[bh * a.list + m], t = a.holes[bh * a.list + m];
-        from[u] = a.map.row(b, h, f);
-        to[u] = a.map.row(b, h, t);
-        if (lane == 0) move_meta(a, bh, f, t);
-      }
+  const int step = gridDim.x * kMoveThreads;
+  // lane l holds move m0 + l
+  for (int m0 = (blockIdx.x * (kMoveThreads / 32) + warp) * 32; m0 < n; m0 += step) {
+    const int moves = min(32, n - m0);
+    long from = -1, to = 0;
+    if (lane < moves) {
+      const int f = a.movers[bh * a.list + m0 + lane], t = a.holes[bh * a.list + m0 + lane];
+      from = a.map.row(b, h, f);
+      to = a.map.row(b, h, t);
+      move_meta(a, bh, f, t);
     }
-    for (int c = lane; c < kv + vv; c += 32) {
-      const bool is_k = c < kv;
-      char* const p = is_k ? a.k : a.v;
-      const long row = is_k ? a.krow : a.vrow;
-      const long off = (long)(is_k ? c : c - kv) * 16;
-      int4 x[kMoveUnroll];
+    for (int u0 = 0; u0 < moves; u0 += kMoveUnroll) {
+      for (int c = lane; c - lane < kv + vv; c += 32) {     // (whole warps, for the shuffles)
+        const bool is_k = c < kv, in = c < kv + vv;
+        char* const p = is_k ? a.k : a.v;
+        const long row = is_k ? a.krow : a.vrow;
+        const long off = (long)(is_k ? c : c - kv) * 16;
+        int4 x[kMoveUnroll];
 #pragma unroll
-      for (int u = 0; u < kMoveUnroll; ++u)
-        if (from[u] >= 0) x[u] = *(const int4*)(p + from[u] * row + off);
+        for (int u = 0; u < kMoveUnroll; ++u) {
+          const long f = __shfl_sync(kFull, from, u0 + u);  // (u0 + u < 32; -1 past the end)
+          if (in && f >= 0) x[u] = *(const int4*)(p + f * row + off);
+        }
 #pragma unroll
-      for (int u = 0; u < kMoveUnroll; ++u)
-        if (from[u] >= 0) *(int4*)(p + to[u] * row + off) = x[u];
+        for (int u = 0; u < kMoveUnroll; ++u) {
+          const long f = __shfl_sync(kFull, from, u0 + u), t = __shfl_sync(kFull, to, u0 + u);
+          if (in && f >= 0) *(int4*)(p + t * row + off) = x[u];
+        }
+      }
     }
   }
 }
@@ -308,10 +402,20 @@ move_q8_kernel(const __grid_constant__ EvictArgs a) {
   const long bh = (long)b * a.map.Hkv + h;
   if (a.count[bh] < 0) return;
   if (blockIdx.x == 0 && h == 0 && tid == 0) a.prefix_len[b] = a.keep;
+  uint32_t todo = 0;
   const int parts = a.vrow ? 2 : 1;
-  for (int j = blockIdx.x; j * kQ8Block < a.keep; j += gridDim.x) {
-    const int h0 = a.starts[bh * (a.nblk + 1) + j], n = a.starts[bh * (a.nblk + 1) + j + 1] - h0;
-    if (n == 0) continue;              // (the same for the whole CTA)
+  const int32_t* const starts = a.starts + bh * (a.nblk + 1);
+  const int blocks = (a.keep + kQ8Block - 1) / kQ8Block;
+  for (int j = blockIdx.x; j < blocks; j += gridDim.x) {
+    // 32 of this CTA's blocks at a time: which ones have holes (a block has 64 at
+    // most; the same answer in every warp)
+    if ((j - (int)blockIdx.x) / (int)gridDim.x % 32 == 0) {
+      const long l = j + (long)(tid & 31) * gridDim.x;
+      todo = __ballot_sync(kFull, l < blocks && starts[l] != starts[l + 1]);
+    }
+    const bool has = (todo >> ((j - (int)blockIdx.x) / (int)gridDim.x % 32)) & 1u;
+    if (!has) continue;                // (the same for the whole CTA)
+    const int h0 = starts[j], n = starts[j + 1] - h0;
     const int rows = min(kQ8Block, a.keep - j * kQ8Block);
     __syncthreads();                   // the block before is done with the shared arrays
     if (tid < 2) s_max[tid] = 0;
@@ -396,18 +500,34 @@ EvictPlan plan_evict(const tsd_attn_desc& d) {
   return p;
 }
 
+template <int ITEMS, bool kQ8>
+void launch_cluster(const EvictArgs& a, int B, int ranks, cudaStream_t st) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ranks, a.map.Hkv, B);
+  cfg.blockDim = dim3(kSelThreads);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = ranks;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  cudaLaunchKernelEx(&cfg, select_kernel<ITEMS, kQ8>, a);
+}
+
 template <bool kQ8>
 void launch_select(const EvictArgs& a, int B, cudaStream_t st) {
-  const dim3 grid(a.map.Hkv, B);
-  // keys per thread: enough registers for the whole cache up to 32 Ki rows
-  if (a.map.cap <= 4 * kSelThreads)
-    launch(select_kernel<4, kQ8>, grid, dim3(kSelThreads), 0, st, a);
-  else if (a.map.cap <= 8 * kSelThreads)
-    launch(select_kernel<8, kQ8>, grid, dim3(kSelThreads), 0, st, a);
-  else if (a.map.cap <= 16 * kSelThreads)
-    launch(select_kernel<16, kQ8>, grid, dim3(kSelThreads), 0, st, a);
-  else
-    launch(select_kernel<32, kQ8>, grid, dim3(kSelThreads), 0, st, a);
+  // CTAs of a cluster: more while a CTA keeps at least 2048 rows and all of them
+  // are resident at once (two per SM)
+  int ranks = 1;
+  while (ranks < kMaxCluster && a.map.cap > ranks * 2048 && (long)a.map.Hkv * B * ranks * 2 <= 304)
+    ranks *= 2;
+  const long rows = ceil_div(a.map.cap, ranks);
+  if (rows <= 4 * kSelThreads) launch_cluster<4, kQ8>(a, B, ranks, st);
+  else if (rows <= 8 * kSelThreads) launch_cluster<8, kQ8>(a, B, ranks, st);
+  else launch_cluster<16, kQ8>(a, B, ranks, st);
 }
 
 tsd_status evict_impl(const tsd_attn_desc* d, int keep, int sink, int recent, float* acc,
@@ -466,7 +586,7 @@ tsd_status evict_impl(const tsd_attn_desc* d, int keep, int sink, int recent, fl
   } else {
     launch_select<false>(a, d->B, st);
     long x = ceil_div(152L * 8, heads);
-    const long most = ceil_div(p.list, kMoveThreads / 32);
+    const long most = ceil_div(p.list, kMoveThreads);
     if (x > most) x = most;
     launch(move_kernel, dim3((unsigned)x, d->Hkv, d->B), dim3(kMoveThreads), 0, st, a);
   }

@@ -17,6 +17,8 @@
 #include <cuda_bf16.h>
 #include <math.h>
 
+#include <type_traits>
+
 #include "tsd_host.h"
 #include "tsd_q8_attn.cuh"
 
@@ -36,7 +38,6 @@ __device__ __forceinline__ void load4(const float* p, float (&x)[4]) {
   x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
 }
 __device__ __forceinline__ void store_out(float* p, float x) { *p = x; }
-__device__ __forceinline__ void store_out(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
 
 // DV <= DK; ALIAS: the value is the first DV entries of the key.
 template <typename T, int DK, int DV, int RB, bool ALIAS>
@@ -246,53 +247,104 @@ q8_simt_kernel(const __grid_constant__ Q8AttnArgs a) {
   }
 }
 
-// Merge of the splits of one output row by one warp: with L_s the log2-sum-exp
-// and c_s the scale of split s, out = sum_s 2^(L_s - L) c_s O_s and
-// L = log2 sum_s 2^(L_s).  PT: element type of the partial outputs.
+// W words of a split's output: four fp32, or eight fp16.
+__device__ __forceinline__ void part_values(const uint4& w, float (&x)[4], float) {
+  x[0] = __uint_as_float(w.x);
+  x[1] = __uint_as_float(w.y);
+  x[2] = __uint_as_float(w.z);
+  x[3] = __uint_as_float(w.w);
+}
+__device__ __forceinline__ void part_values(const uint2& w, float (&x)[4], __half) {
+  const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&w.x));
+  const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&w.y));
+  x[0] = a.x; x[1] = a.y; x[2] = b.x; x[3] = b.y;
+}
+__device__ __forceinline__ void store4(float* p, const float (&x)[4]) {
+  *(float4*)p = make_float4(x[0], x[1], x[2], x[3]);
+}
+__device__ __forceinline__ void store4(__nv_bfloat16* p, const float (&x)[4]) {
+  const __nv_bfloat162 a = __floats2bfloat162_rn(x[0], x[1]), b = __floats2bfloat162_rn(x[2], x[3]);
+  *(uint2*)p = make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+}
+
+// Merge of the splits of one output row: with L_s the log2-sum-exp and c_s the
+// scale of split s, out = sum_s 2^(L_s - L) c_s O_s and L = log2 sum_s 2^(L_s).
+// One warp per row, four dims per lane and step.  Bounded by latency, so the outputs of the first kBatch splits are
+// requested together with the sums, before any weight is known.  PT: element type
+// of the splits' outputs.
 template <typename T, int DV, typename PT>
 __global__ void __launch_bounds__(128) q8_combine_kernel(const __grid_constant__ Q8AttnArgs a) {
+  using Word = typename std::conditional<sizeof(PT) == 4, uint4, uint2>::type;
+  constexpr int kStep = DV / 128 > 0 ? DV / 128 : 1;   // words of four dims per lane
+  constexpr int kBatch = kStep > 1 ? 8 : 16;
   grid_dependency_sync();
-  constexpr int NV = DV / 32;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const long row = (long)blockIdx.x * 4 + warp;
   if (row >= (long)a.B * a.R * a.Hq) return;
   const int b = (int)(row / ((long)a.R * a.Hq)), r = (int)((row / a.Hq) % a.R), h = (int)(row % a.Hq);
+  const long base = (((long)b * a.Hq + h) * a.R + r) * a.nsplit;
+  const PT* const parts = (const PT*)a.part_o + base * DV;
+  const bool active = DV >= 128 || lane < DV / 4;
+  // (the workspace holds nsplit entries per row; those of splits without work are
+  // read, too, and left out)
+  float2 meta = lane < a.nsplit ? a.part_meta[base + lane] : make_float2(-INFINITY, 0.f);
+  Word w[kBatch][kStep];
+#pragma unroll
+  for (int s = 0; s < kBatch; ++s)
+#pragma unroll
+    for (int i = 0; i < kStep; ++i)
+      if (s < a.nsplit && active) w[s][i] = *(const Word*)(parts + (long)s * DV + 128 * i + 4 * lane);
   const int P = min(max(a.plen[b], 0), a.map.cap);
   const int n = q8_splits(a, P);
   if (n == 1) return;                    // written by its only split
-  const long base = (((long)b * a.Hq + h) * a.R + r) * a.nsplit;
-  float mx = -INFINITY;
-  for (int s = lane; s < n; s += 32) mx = fmaxf(mx, a.part_meta[base + s].x);
+  if (lane >= n) meta.x = -INFINITY;
+  float mx = meta.x;
+  for (int s = lane + 32; s < n; s += 32) mx = fmaxf(mx, a.part_meta[base + s].x);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, o));
-  float sum = 0.f;
-  for (int s = lane; s < n; s += 32) {
+  float sum = meta.x == -INFINITY ? 0.f : exp2f(meta.x - mx);
+  for (int s = lane + 32; s < n; s += 32) {
     const float L = a.part_meta[base + s].x;
     if (L != -INFINITY) sum += exp2f(L - mx);
   }
   sum = warp_total(sum);
-  float acc[NV];
+  // the weight first, then the scale: each alone may be far from 1
+  float wt = meta.x == -INFINITY ? 0.f : exp2f(meta.x - mx) / sum * meta.y;
+  float acc[kStep][4];
 #pragma unroll
-  for (int t = 0; t < NV; ++t) acc[t] = 0.f;
-  const PT* parts = (const PT*)a.part_o + base * DV;
-  for (int s0 = 0; s0 < n; s0 += 32) {
-    float w = 0.f;
-    if (s0 + lane < n) {
-      const float2 meta = a.part_meta[base + s0 + lane];
-      // the weight first, then the scale: each alone may be far from 1
-      w = meta.x == -INFINITY ? 0.f : exp2f(meta.x - mx) / sum * meta.y;
+  for (int i = 0; i < kStep; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
+  for (int s0 = 0; s0 < n; s0 += kBatch) {
+    if (s0 > 0) {
+#pragma unroll
+      for (int s = 0; s < kBatch; ++s)
+#pragma unroll
+        for (int i = 0; i < kStep; ++i)
+          if (s0 + s < n && active) w[s][i] = *(const Word*)(parts + (long)(s0 + s) * DV + 128 * i + 4 * lane);
+      if (s0 % 32 == 0) {
+        meta = s0 + lane < n ? a.part_meta[base + s0 + lane] : make_float2(-INFINITY, 0.f);
+        wt = meta.x == -INFINITY ? 0.f : exp2f(meta.x - mx) / sum * meta.y;
+      }
     }
-    const int m = min(32, n - s0);
-#pragma unroll 4
-    for (int s = 0; s < m; ++s) {
-      const float ws = __shfl_sync(kFull, w, s);
 #pragma unroll
-      for (int t = 0; t < NV; ++t)
-        acc[t] = fmaf(ws, (float)parts[(long)(s0 + s) * DV + lane + 32 * t], acc[t]);
+    for (int s = 0; s < kBatch; ++s) {
+      const float ws = __shfl_sync(kFull, wt, (s0 + s) & 31);
+      if (s0 + s < n) {
+#pragma unroll
+        for (int i = 0; i < kStep; ++i) {
+          float x[4];
+          part_values(w[s][i], x, PT());
+#pragma unroll
+          for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(ws, x[j], acc[i][j]);
+        }
+      }
     }
   }
+  if (active) {
 #pragma unroll
-  for (int t = 0; t < NV; ++t) store_out((T*)a.out + row * DV + lane + 32 * t, acc[t]);
+    for (int i = 0; i < kStep; ++i) store4((T*)a.out + row * DV + 128 * i + 4 * lane, acc[i]);
+  }
   if (lane == 0) a.lse[row] = (mx + log2f(sum)) * 0.69314718055994531f;
 }
 

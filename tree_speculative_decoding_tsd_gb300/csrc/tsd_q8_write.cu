@@ -19,6 +19,8 @@
 // element.
 #include <cuda_bf16.h>
 
+#include <type_traits>
+
 #include "tsd_host.h"
 #include "tsd_q8.cuh"
 
@@ -43,87 +45,126 @@ constexpr int kNoCode = 0x7fffffff;
 template <int D> constexpr int kWriteThreads = D > 128 ? 512 : 256;
 template <int D> constexpr int kWriteVecs = kQ8Block * D / 8 / kWriteThreads<D>;
 
+struct WriteSmem {
+  int code;
+  int32_t path[17];        // commit: source rows
+  uint32_t warp_max[32];
+};
+
 // Rows that request b appends (0 for none), or minus the error code that makes
-// the request be skipped: every thread of the CTA gets the same answer.
+// the request be skipped: every thread of the CTA gets the same answer.  c: its
+// count, r: its path entry threadIdx.x (commit; requested with the lengths).
 template <bool kCommit>
-__device__ __forceinline__ int write_rows(const Q8WriteArgs& a, int b, int P, int& shared_code) {
-  if (threadIdx.x == 0) shared_code = kNoCode;
+__device__ __forceinline__ int write_rows(const Q8WriteArgs& a, int b, int P, int c, int r,
+                                          WriteSmem& s) {
+  const int tid = threadIdx.x;
+  if (tid == 0) s.code = kNoCode;
   __syncthreads();
-  const int c = a.count[b];
   int code = 0;
   const long n = kCommit ? (long)c + 1 : c;
   if (kCommit && (c < 0 || c > a.S)) code = TSD_DEV_ERR_BAD_TREE;
   else if (!kCommit && (c < 0 || c > a.rows)) code = TSD_DEV_ERR_CAPACITY;
   else if (P < 0 || P + n > a.map.cap) code = TSD_DEV_ERR_CAPACITY;
   else {
-    if (kCommit)
-      for (int i = threadIdx.x; i < n; i += blockDim.x) {
-        const int r = a.path[(long)b * (a.S + 1) + i];
-        if (r < 0 || r >= a.rows) code = TSD_DEV_ERR_BAD_TREE;
-      }
+    if (kCommit && tid < n) {
+      if (r < 0 || r >= a.rows) code = TSD_DEV_ERR_BAD_TREE;
+      s.path[tid] = r;
+    }
     if (a.map.page_size && n > 0) {
       const int p1 = (int)((P + n - 1) / a.map.page_size);
-      for (int p = P / a.map.page_size + threadIdx.x; p <= p1; p += blockDim.x) {
+      for (int p = P / a.map.page_size + tid; p <= p1; p += blockDim.x) {
         const int pg = a.map.page_table[(long)b * a.map.max_pages + p];
         if ((pg < 0 || pg >= a.map.num_pages) && code == 0) code = TSD_DEV_ERR_BAD_PAGE;
       }
     }
   }
-  if (code != 0) atomicMin(&shared_code, code);
+  if (code != 0) atomicMin(&s.code, code);
   __syncthreads();
-  code = shared_code;
+  code = s.code;
   return code != kNoCode ? -code : (int)n;
 }
+
+// Eight elements as they are in memory, and as fp32.
+struct RawF32 {
+  uint4 a, b;
+  __device__ __forceinline__ void load(const float* p) {
+    a = __ldg((const uint4*)p);
+    b = __ldg((const uint4*)p + 1);
+  }
+  __device__ __forceinline__ void clear() { a = b = make_uint4(0u, 0u, 0u, 0u); }
+  __device__ __forceinline__ void values(float (&x)[8]) const {
+    const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(w[i]);
+  }
+};
+struct RawBf16 {
+  uint4 a;
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) { a = __ldg((const uint4*)p); }
+  __device__ __forceinline__ void clear() { a = make_uint4(0u, 0u, 0u, 0u); }
+  __device__ __forceinline__ void values(float (&x)[8]) const {
+    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x[2 * i] = __uint_as_float(w[i] << 16);
+      x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+  }
+};
 
 // Block `blk` (positions 64 blk ..) of head h of request b, part 0 (K) or 1 (V).
 template <typename T, int D, bool kCommit>
 __device__ __forceinline__ void write_block(const Q8WriteArgs& a, int b, int h, int part, int blk,
-                                            int P, int n, uint32_t* warp_max) {
+                                            int P, int n, WriteSmem& s) {
+  using Raw = typename std::conditional<sizeof(T) == 4, RawF32, RawBf16>::type;
   constexpr int kThreads = kWriteThreads<D>, kVecs = kWriteVecs<D>, VR = D / 8;
   const int tid = threadIdx.x;
   const int first = blk * kQ8Block;
   const int r0 = max(P - first, 0);                  // the block's earlier rows end here
   const int r1 = min(P + n - first, kQ8Block);       // and its new ones here
-  float x[kVecs][8];
-  uint32_t m = 0;
+  Raw raw[kVecs];
 #pragma unroll
   for (int i = 0; i < kVecs; ++i) {
     const int r = (tid + i * kThreads) / VR, c = (tid + i * kThreads) % VR;
+    raw[i].clear();
     if (r >= r0 && r < r1) {
       int t = first + r - P;
-      if (kCommit) t = a.path[(long)b * (a.S + 1) + t];
-      load8((const T*)a.src[part] + (((long)b * a.rows + t) * a.map.Hkv + h) * D + c * 8, x[i]);
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) x[i][j] = 0.f;
+      if (kCommit) t = s.path[t];
+      raw[i].load((const T*)a.src[part] + (((long)b * a.rows + t) * a.map.Hkv + h) * D + c * 8);
     }
   }
+  uint8_t* const ep = a.exps[part] + a.map.block(b, h, first);
+  const int e_old = r0 > 0 ? *ep : 0;
+  uint8_t* const row0 = a.codes[part] + a.map.row(b, h, first) * D;
+  uint32_t m = 0;
 #pragma unroll
-  for (int i = 0; i < kVecs; ++i)
+  for (int i = 0; i < kVecs; ++i) {
+    float x[8];
+    raw[i].values(x);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const uint32_t u = __float_as_uint(x[i][j]) & 0x7fffffffu;
+      const uint32_t u = __float_as_uint(x[j]) & 0x7fffffffu;
       m = max(m, u < 0x7f800000u ? u : 0u);          // infinities and NaN do not count
     }
+  }
   m = __reduce_max_sync(kFull, m);
   __syncthreads();                                   // (warp_max of the task before)
-  if ((tid & 31) == 0) warp_max[tid >> 5] = m;
+  if ((tid & 31) == 0) s.warp_max[tid >> 5] = m;
   __syncthreads();
   m = 0;
 #pragma unroll
-  for (int w = 0; w < kThreads / 32; ++w) m = max(m, warp_max[w]);
-  uint8_t* const ep = a.exps[part] + a.map.block(b, h, first);
-  const int e_old = r0 > 0 ? *ep : 0;
+  for (int w = 0; w < kThreads / 32; ++w) m = max(m, s.warp_max[w]);
   const int e = max(q8_need(__uint_as_float(m)), e_old);
   const float inv = q8_scale(254 - min(e, kQ8ExpMax));  // 2^(127 - e)
-  uint8_t* const row0 = a.codes[part] + a.map.row(b, h, first) * D;
 #pragma unroll
   for (int i = 0; i < kVecs; ++i) {
     const int v = tid + i * kThreads, r = v / VR;
     if (r >= r0 && r < r1) {
+      float x[8];
+      raw[i].values(x);
       uint2 w;
-      w.x = q8_pack4(x[i][0] * inv, x[i][1] * inv, x[i][2] * inv, x[i][3] * inv);
-      w.y = q8_pack4(x[i][4] * inv, x[i][5] * inv, x[i][6] * inv, x[i][7] * inv);
+      w.x = q8_pack4(x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv);
+      w.y = q8_pack4(x[4] * inv, x[5] * inv, x[6] * inv, x[7] * inv);
       *(uint2*)(row0 + (long)v * 8) = w;
     }
   }
@@ -148,22 +189,21 @@ __device__ __forceinline__ void write_block(const Q8WriteArgs& a, int b, int h, 
 template <typename T, int D>
 __global__ void __launch_bounds__(kWriteThreads<D>)
 write_q8_kernel(const __grid_constant__ Q8WriteArgs a) {
-  __shared__ int code;
-  __shared__ uint32_t warp_max[32];
+  __shared__ WriteSmem s;
   grid_dependency_sync();
-  const int b = blockIdx.z, P = a.prefix_len[b];
-  const int n = write_rows<false>(a, b, P, code);
+  const int b = blockIdx.z, P = a.prefix_len[b], c = a.count[b];
+  const int n = write_rows<false>(a, b, P, c, 0, s);
   if (n <= 0) return;
   const int blk = P / kQ8Block + blockIdx.x;
   if (blk * (long)kQ8Block >= (long)P + n) return;
-  write_block<T, D, false>(a, b, blockIdx.y / a.parts, blockIdx.y % a.parts, blk, P, n, warp_max);
+  write_block<T, D, false>(a, b, blockIdx.y / a.parts, blockIdx.y % a.parts, blk, P, n, s);
 }
 
 __global__ void __launch_bounds__(128) write_advance_kernel(const __grid_constant__ Q8WriteArgs a) {
-  __shared__ int code;
+  __shared__ WriteSmem s;
   grid_dependency_sync();
-  const int b = blockIdx.x, P = a.prefix_len[b];
-  const int n = write_rows<false>(a, b, P, code);
+  const int b = blockIdx.x, P = a.prefix_len[b], c = a.count[b];
+  const int n = write_rows<false>(a, b, P, c, 0, s);
   if (threadIdx.x != 0) return;
   if (n < 0) report_error(a.err, -n, b);
   else a.prefix_len[b] = P + n;
@@ -178,18 +218,18 @@ constexpr int kCommitCtas = 8;
 template <typename T, int D>
 __global__ void __cluster_dims__(kCommitCtas, 1, 1) __launch_bounds__(kWriteThreads<D>)
 commit_q8_kernel(const __grid_constant__ Q8WriteArgs a) {
-  __shared__ int code;
-  __shared__ uint32_t warp_max[32];
+  __shared__ WriteSmem s;
   grid_dependency_sync();
-  const int b = blockIdx.y, P = a.prefix_len[b];
-  const int n = write_rows<true>(a, b, P, code);     // (its barrier: the whole CTA has read P)
+  const int b = blockIdx.y, P = a.prefix_len[b], c = a.count[b];
+  const int r = threadIdx.x <= a.S ? a.path[(long)b * (a.S + 1) + threadIdx.x] : 0;
+  const int n = write_rows<true>(a, b, P, c, r, s);  // (its barrier: the whole CTA has read P)
   asm volatile("barrier.cluster.arrive.aligned;\n" ::: "memory");
   if (n > 0) {
     const int blk0 = P / kQ8Block, nb = (P + n - 1) / kQ8Block - blk0 + 1;
     const int tasks = nb * a.map.Hkv * a.parts;
     for (int t = blockIdx.x; t < tasks; t += kCommitCtas) {
       const int hp = t / nb;
-      write_block<T, D, true>(a, b, hp / a.parts, hp % a.parts, blk0 + t % nb, P, n, warp_max);
+      write_block<T, D, true>(a, b, hp / a.parts, hp % a.parts, blk0 + t % nb, P, n, s);
     }
   }
   asm volatile("barrier.cluster.wait.aligned;\n" ::: "memory");
