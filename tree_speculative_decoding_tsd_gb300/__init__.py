@@ -500,12 +500,38 @@ _CODES = (torch.uint8, torch.float8_e4m3fn)
 _EXPS = (torch.uint8,) + ((torch.float8_e8m0fnu,) if hasattr(torch, "float8_e8m0fnu") else ())
 
 
-def _here(*tensors):
-    """The calls launch on the current device: every tensor has to live there."""
-    cur = torch.cuda.current_device()
-    for t in tensors:
-        if t is not None and t.is_cuda and t.device.index != cur:
-            raise ValueError(f"tensor on {t.device}, but the current device is cuda:{cur}")
+def _p(t, name, dtypes, shape, dev):
+    """Address of ``t`` after checking its element type, shape, density and device (the
+    current one, ``dev``, where the call launches).  None passes through as NULL."""
+    if t is None:
+        return None
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name}: element type {t.dtype}, expected "
+                        f"{' or '.join(str(d) for d in dtypes)}")
+    if t.shape != shape:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name}: tensor on {t.device}, but the current device is cuda:{dev}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: tensor must be contiguous")
+    return t.data_ptr()
+
+
+_I32T, _F32T = (_I32,), (_F32,)
+
+
+def _scratch(ws, err, dev):
+    """(workspace address, its bytes), error word address."""
+    if ws is not None and (ws.get_device() != dev or not ws.is_contiguous()):
+        raise ValueError(f"ws: a contiguous tensor on cuda:{dev} is needed")
+    return ((None, 0) if ws is None else (ws.data_ptr(), _nbytes(ws)),
+            None if err is None else _p(err, "err", _I32T, err.shape, dev))
+
+
+def _raw_stream(stream, dev):
+    if stream is None:
+        stream = torch.cuda.current_stream(dev)
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 def q8_blocks(cap) -> int:
@@ -513,53 +539,61 @@ def q8_blocks(cap) -> int:
     return -(-int(cap) // TSD_Q8_BLOCK)
 
 
-def _cache_shapes(d, kcache, page_table, page_size):
+def _cache_shapes(d, kcache, page_table, page_size, dev):
     """(leading dims, rows) of a contiguous or paged cache, and its page arguments."""
     if page_table is None:
         if page_size:
             raise ValueError("page_size without a page_table")
         return (d.B, d.Hkv), d.cap, (None, 0, 0, 0)
     npg, mp = kcache.shape[0], page_table.shape[1]
-    return (npg, d.Hkv), page_size, (_t(page_table, "page_table", _I32, (d.B, mp)), mp, page_size,
-                                     npg)
+    return (npg, d.Hkv), page_size, (_p(page_table, "page_table", _I32T, (d.B, mp), dev), mp,
+                                     page_size, npg)
 
 
-def _q8_cache(d, kq, vq, kexp, vexp, page_table, page_size):
-    lead, rows, paging = _cache_shapes(d, kq, page_table, page_size)
+def _q8_cache(d, kq, vq, kexp, vexp, page_table, page_size, dev):
+    lead, rows, paging = _cache_shapes(d, kq, page_table, page_size, dev)
     nb = q8_blocks(rows)
-    alias = bool(d.v_aliases_k)
-    return (_t(kq, "kq", _CODES, (*lead, rows, d.dk)),
-            None if alias else _t(vq, "vq", _CODES, (*lead, rows, d.dv)),
-            _t(kexp, "kexp", _EXPS, (*lead, nb)),
-            None if alias else _t(vexp, "vexp", _EXPS, (*lead, nb)), paging)
+    if d.v_aliases_k:
+        vq = vexp = None
+    elif vq is None or vexp is None:
+        raise ValueError("vq, vexp: needed unless V aliases K")
+    return (_p(kq, "kq", _CODES, (*lead, rows, d.dk), dev),
+            _p(vq, "vq", _CODES, (*lead, rows, d.dv), dev),
+            _p(kexp, "kexp", _EXPS, (*lead, nb), dev), _p(vexp, "vexp", _EXPS, (*lead, nb), dev),
+            paging)
+
+
+def _rows(d, k, v, names, n, dev):
+    """Addresses of new rows [B][n][Hkv][dk | dv]."""
+    dt = (_attn_dtype(d),)
+    return (_p(k, names[0], dt, (d.B, n, d.Hkv, d.dk), dev),
+            None if d.v_aliases_k else _p(v, names[1], dt, (d.B, n, d.Hkv, d.dv), dev))
 
 
 def tsd_cache_write_q8(desc, knew, vnew, new_len, kq, vq, kexp, vexp, prefix_len, err=None,
                        stream=None, page_table=None, page_size=0):
     """Append rows knew/vnew [B][T][Hkv][d], new_len[b] of them, to the 8-bit cache."""
-    d = desc
-    dt = _attn_dtype(d)
-    _here(knew, vnew, new_len, kq, vq, kexp, vexp, prefix_len, err, page_table)
+    d, dev = desc, torch.cuda.current_device()
     T = knew.shape[1]
-    pk, pv, pke, pve, paging = _q8_cache(d, kq, vq, kexp, vexp, page_table, page_size)
+    rows = _rows(d, knew, vnew, ("knew", "vnew"), T, dev)
+    pk, pv, pke, pve, paging = _q8_cache(d, kq, vq, kexp, vexp, page_table, page_size, dev)
     _check("tsd_cache_write_q8", _L().tsd_cache_write_q8(
-        ctypes.byref(d), T, _t(knew, "knew", dt, (d.B, T, d.Hkv, d.dk)),
-        None if d.v_aliases_k else _t(vnew, "vnew", dt, (d.B, T, d.Hkv, d.dv)),
-        _t(new_len, "new_len", _I32, (d.B,)), pk, pv, pke, pve, *paging,
-        _t(prefix_len, "prefix_len", _I32, (d.B,)), _err(err), _stream(stream)))
+        ctypes.byref(d), T, *rows, _p(new_len, "new_len", _I32T, (d.B,), dev), pk, pv, pke, pve,
+        *paging, _p(prefix_len, "prefix_len", _I32T, (d.B,), dev), _scratch(None, err, dev)[1],
+        _raw_stream(stream, dev)))
 
 
 def tsd_commit_path_q8(desc, S, ktree, vtree, accept_rows, accept_len, kq, vq, kexp, vexp,
                        prefix_len, err=None, stream=None, page_table=None, page_size=0):
     """tsd_commit_path into the 8-bit cache."""
-    d = desc
-    _here(ktree, vtree, accept_rows, accept_len, kq, vq, kexp, vexp, prefix_len, err, page_table)
-    pkt, pvt, par, pal, ppl = _commit_common(d, S, ktree, vtree, accept_rows, accept_len,
-                                             prefix_len)
-    pk, pv, pke, pve, paging = _q8_cache(d, kq, vq, kexp, vexp, page_table, page_size)
+    d, dev = desc, torch.cuda.current_device()
+    rows = _rows(d, ktree, vtree, ("ktree", "vtree"), d.R, dev)
+    pk, pv, pke, pve, paging = _q8_cache(d, kq, vq, kexp, vexp, page_table, page_size, dev)
     _check("tsd_commit_path_q8", _L().tsd_commit_path_q8(
-        ctypes.byref(d), S, pkt, pvt, par, pal, pk, pv, pke, pve, *paging, ppl, _err(err),
-        _stream(stream)))
+        ctypes.byref(d), S, *rows, _p(accept_rows, "accept_rows", _I32T, (d.B, S + 1), dev),
+        _p(accept_len, "accept_len", _I32T, (d.B,), dev), pk, pv, pke, pve, *paging,
+        _p(prefix_len, "prefix_len", _I32T, (d.B,), dev), _scratch(None, err, dev)[1],
+        _raw_stream(stream, dev)))
 
 
 def tsd_verify_q8_workspace_size(desc: tsd_attn_desc) -> int:
@@ -569,87 +603,86 @@ def tsd_verify_q8_workspace_size(desc: tsd_attn_desc) -> int:
 def tsd_tree_verify_attn_q8(desc, q, kq, vq, kexp, vexp, prefix_len, ktree, vtree, mask, out, lse,
                             ws, err=None, stream=None, page_table=None, page_size=0):
     """tsd_tree_verify_attn over the 8-bit cache (contiguous, or pages with ``page_table``)."""
-    d = desc
-    _here(q, kq, vq, kexp, vexp, prefix_len, ktree, vtree, mask, out, lse, ws, err, page_table)
-    pq, pl, pkt, pvt, pm, po, pls = _verify_common(d, q, prefix_len, ktree, vtree, mask, out, lse)
-    pk, pv, pke, pve, paging = _q8_cache(d, kq, vq, kexp, vexp, page_table, page_size)
+    d, dev = desc, torch.cuda.current_device()
+    B, R, Hq = d.B, d.R, d.Hq
+    dt = (_attn_dtype(d),)
+    pk, pv, pke, pve, paging = _q8_cache(d, kq, vq, kexp, vexp, page_table, page_size, dev)
+    rows = _rows(d, ktree, vtree, ("ktree", "vtree"), R, dev)
+    (pws, nws), perr = _scratch(ws, err, dev)
     _check("tsd_tree_verify_attn_q8", _L().tsd_tree_verify_attn_q8(
-        ctypes.byref(d), pq, pk, pv, pke, pve, *paging, pl, pkt, pvt, pm, po, pls, _ptr(ws),
-        _nbytes(ws), _err(err), _stream(stream)))
+        ctypes.byref(d), _p(q, "q", dt, (B, R, Hq, d.dk), dev), pk, pv, pke, pve, *paging,
+        _p(prefix_len, "prefix_len", _I32T, (B,), dev), *rows, _p(mask, "mask", _MASK, (B, R), dev),
+        _p(out, "out", dt, (B, R, Hq, d.dv), dev), _p(lse, "lse", _F32T, (B, R, Hq), dev), pws, nws,
+        perr, _raw_stream(stream, dev)))
 
 
-def _weight_args(d, S, prefix_len, ktree, accept_rows, accept_len, lse, decay, acc, pos, seen):
-    return (_t(prefix_len, "prefix_len", _I32, (d.B,)),
-            _t(ktree, "ktree", _attn_dtype(d), (d.B, d.R, d.Hkv, d.dk)),
-            _t(accept_rows, "accept_rows", _I32, (d.B, S + 1)),
-            _t(accept_len, "accept_len", _I32, (d.B,)), _t(lse, "lse", _F32, (d.B, d.R, d.Hq)),
-            float(decay), _t(acc, "acc", _F32, (d.B, d.Hkv, d.cap)),
-            _t(pos, "pos", _I32, (d.B, d.Hkv, d.cap)), _t(seen, "seen", _I32, (d.B, d.Hkv)))
+def _weight_args(d, S, prefix_len, ktree, accept_rows, accept_len, lse, decay, acc, pos, seen, dev):
+    return (_p(prefix_len, "prefix_len", _I32T, (d.B,), dev),
+            _p(ktree, "ktree", (_attn_dtype(d),), (d.B, d.R, d.Hkv, d.dk), dev),
+            _p(accept_rows, "accept_rows", _I32T, (d.B, S + 1), dev),
+            _p(accept_len, "accept_len", _I32T, (d.B,), dev),
+            _p(lse, "lse", _F32T, (d.B, d.R, d.Hq), dev), float(decay),
+            *_evict_state(d, acc, pos, seen, dev))
+
+
+def _evict_state(d, acc, pos, seen, dev):
+    return (_p(acc, "acc", _F32T, (d.B, d.Hkv, d.cap), dev),
+            _p(pos, "pos", _I32T, (d.B, d.Hkv, d.cap), dev),
+            _p(seen, "seen", _I32T, (d.B, d.Hkv), dev))
 
 
 def tsd_cache_weights(desc, S, q, kcache, prefix_len, ktree, accept_rows, accept_len, lse, decay,
                       acc, pos, seen, err=None, stream=None, page_table=None, page_size=0):
     """Add the attention weight that the accepted rows gave each cached row to ``acc``."""
-    d = desc
-    dt = _attn_dtype(d)
-    _here(q, kcache, prefix_len, ktree, accept_rows, accept_len, lse, acc, pos, seen, err,
-          page_table)
-    args = _weight_args(d, S, prefix_len, ktree, accept_rows, accept_len, lse, decay, acc, pos,
-                        seen)
-    lead, rows, paging = _cache_shapes(d, kcache, page_table, page_size)
+    d, dev = desc, torch.cuda.current_device()
+    dt = (_attn_dtype(d),)
+    lead, rows, paging = _cache_shapes(d, kcache, page_table, page_size, dev)
     _check("tsd_cache_weights", _L().tsd_cache_weights(
-        ctypes.byref(d), S, _t(q, "q", dt, (d.B, d.R, d.Hq, d.dk)),
-        _t(kcache, "kcache", dt, (*lead, rows, d.dk)), *paging, *args, _err(err),
-        _stream(stream)))
+        ctypes.byref(d), S, _p(q, "q", dt, (d.B, d.R, d.Hq, d.dk), dev),
+        _p(kcache, "kcache", dt, (*lead, rows, d.dk), dev), *paging,
+        *_weight_args(d, S, prefix_len, ktree, accept_rows, accept_len, lse, decay, acc, pos, seen,
+                      dev), _scratch(None, err, dev)[1], _raw_stream(stream, dev)))
 
 
 def tsd_cache_weights_q8(desc, S, q, kq, kexp, prefix_len, ktree, accept_rows, accept_len, lse,
                          decay, acc, pos, seen, err=None, stream=None, page_table=None,
                          page_size=0):
     """tsd_cache_weights for the 8-bit cache."""
-    d = desc
-    _here(q, kq, kexp, prefix_len, ktree, accept_rows, accept_len, lse, acc, pos, seen, err,
-          page_table)
-    args = _weight_args(d, S, prefix_len, ktree, accept_rows, accept_len, lse, decay, acc, pos,
-                        seen)
-    lead, rows, paging = _cache_shapes(d, kq, page_table, page_size)
+    d, dev = desc, torch.cuda.current_device()
+    lead, rows, paging = _cache_shapes(d, kq, page_table, page_size, dev)
     _check("tsd_cache_weights_q8", _L().tsd_cache_weights_q8(
-        ctypes.byref(d), S, _t(q, "q", _attn_dtype(d), (d.B, d.R, d.Hq, d.dk)),
-        _t(kq, "kq", _CODES, (*lead, rows, d.dk)), _t(kexp, "kexp", _EXPS, (*lead, q8_blocks(rows))),
-        *paging, *args, _err(err), _stream(stream)))
+        ctypes.byref(d), S, _p(q, "q", (_attn_dtype(d),), (d.B, d.R, d.Hq, d.dk), dev),
+        _p(kq, "kq", _CODES, (*lead, rows, d.dk), dev),
+        _p(kexp, "kexp", _EXPS, (*lead, q8_blocks(rows)), dev), *paging,
+        *_weight_args(d, S, prefix_len, ktree, accept_rows, accept_len, lse, decay, acc, pos, seen,
+                      dev), _scratch(None, err, dev)[1], _raw_stream(stream, dev)))
 
 
 def tsd_cache_evict_workspace_size(desc: tsd_attn_desc) -> int:
     return _L().tsd_cache_evict_workspace_size(ctypes.byref(desc))
 
 
-def _evict_state(d, acc, pos, seen):
-    return (_t(acc, "acc", _F32, (d.B, d.Hkv, d.cap)), _t(pos, "pos", _I32, (d.B, d.Hkv, d.cap)),
-            _t(seen, "seen", _I32, (d.B, d.Hkv)))
-
-
 def tsd_cache_evict(desc, keep, sink, recent, acc, pos, seen, kcache, vcache, prefix_len, ws,
                     err=None, stream=None, page_table=None, page_size=0):
     """Cut every request of more than ``keep`` cached rows to the ``keep`` heaviest ones."""
-    d = desc
-    dt = _attn_dtype(d)
-    _here(acc, pos, seen, kcache, vcache, prefix_len, ws, err, page_table)
-    lead, rows, paging = _cache_shapes(d, kcache, page_table, page_size)
+    d, dev = desc, torch.cuda.current_device()
+    dt = (_attn_dtype(d),)
+    lead, rows, paging = _cache_shapes(d, kcache, page_table, page_size, dev)
+    (pws, nws), perr = _scratch(ws, err, dev)
     _check("tsd_cache_evict", _L().tsd_cache_evict(
-        ctypes.byref(d), keep, sink, recent, *_evict_state(d, acc, pos, seen),
-        _t(kcache, "kcache", dt, (*lead, rows, d.dk)),
-        None if d.v_aliases_k else _t(vcache, "vcache", dt, (*lead, rows, d.dv)), *paging,
-        _t(prefix_len, "prefix_len", _I32, (d.B,)), _ptr(ws), _nbytes(ws), _err(err),
-        _stream(stream)))
+        ctypes.byref(d), keep, sink, recent, *_evict_state(d, acc, pos, seen, dev),
+        _p(kcache, "kcache", dt, (*lead, rows, d.dk), dev),
+        None if d.v_aliases_k else _p(vcache, "vcache", dt, (*lead, rows, d.dv), dev), *paging,
+        _p(prefix_len, "prefix_len", _I32T, (d.B,), dev), pws, nws, perr, _raw_stream(stream, dev)))
 
 
 def tsd_cache_evict_q8(desc, keep, sink, recent, acc, pos, seen, kq, vq, kexp, vexp, prefix_len,
                        ws, err=None, stream=None, page_table=None, page_size=0):
     """tsd_cache_evict for the 8-bit cache."""
-    d = desc
-    _here(acc, pos, seen, kq, vq, kexp, vexp, prefix_len, ws, err, page_table)
-    pk, pv, pke, pve, paging = _q8_cache(d, kq, vq, kexp, vexp, page_table, page_size)
+    d, dev = desc, torch.cuda.current_device()
+    pk, pv, pke, pve, paging = _q8_cache(d, kq, vq, kexp, vexp, page_table, page_size, dev)
+    (pws, nws), perr = _scratch(ws, err, dev)
     _check("tsd_cache_evict_q8", _L().tsd_cache_evict_q8(
-        ctypes.byref(d), keep, sink, recent, *_evict_state(d, acc, pos, seen), pk, pv, pke, pve,
-        *paging, _t(prefix_len, "prefix_len", _I32, (d.B,)), _ptr(ws), _nbytes(ws), _err(err),
-        _stream(stream)))
+        ctypes.byref(d), keep, sink, recent, *_evict_state(d, acc, pos, seen, dev), pk, pv, pke,
+        pve, *paging, _p(prefix_len, "prefix_len", _I32T, (d.B,), dev), pws, nws, perr,
+        _raw_stream(stream, dev)))

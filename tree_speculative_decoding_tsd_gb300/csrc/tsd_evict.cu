@@ -76,7 +76,7 @@ struct SelectSmem {
   uint32_t bins[256];
   int warps[2][kSelWarps];
   uint32_t prefix, need;
-  int bad;
+  int bad, split;          // split: not all rows that equal the cut stay
 };
 
 // Exclusive sums over the warps of two values per warp (the same on all lanes).
@@ -134,7 +134,7 @@ select_kernel(const __grid_constant__ EvictArgs a) {
   uint32_t key[ITEMS];
   auto load = [&](int r) {
     const int base = begin + r * kSpan + warp * 32 * ITEMS + lane;
-    constexpr int kBatch = ITEMS < 8 ? ITEMS : 8;           // loads in flight per thread and array
+    constexpr int kBatch = ITEMS == 12 ? 6 : ITEMS < 8 ? ITEMS : 8;   // loads in flight per thread and array
 #pragma unroll
     for (int i0 = 0; i0 < ITEMS; i0 += kBatch) {
       float w[kBatch];
@@ -220,6 +220,7 @@ select_kernel(const __grid_constant__ EvictArgs a) {
         if (before < need && need <= before + c[i]) {
           s.prefix = (prefix << 8) | (uint32_t)(255 - (8 * lane + i));
           s.need = need - before;
+          s.split = need - before != c[i];
         }
         before += c[i];
       }
@@ -229,6 +230,7 @@ select_kernel(const __grid_constant__ EvictArgs a) {
     need = s.need;
   }
   const uint32_t cut = prefix;   // the smallest kept key; `need` rows that equal it stay
+  const bool split = s.split != 0;
 
   // ---- number the ties, then the holes and the movers, in index order: counts of
   // the CTA, then (of the cluster) what lies before it
@@ -256,12 +258,14 @@ select_kernel(const __grid_constant__ EvictArgs a) {
     nh = nm = 0;
 #pragma unroll
     for (int it = 0; it < ITEMS; ++it) {
-      const uint32_t eq = __ballot_sync(kFull, key[it] == cut);
-      const int rank_of = tie + __popc(eq & ((1u << lane) - 1u));
-      const bool k = key[it] > cut || (key[it] == cut && rank_of < (int)need);
+      bool k = key[it] >= cut;
+      if (split) {
+        const uint32_t eq = __ballot_sync(kFull, key[it] == cut);
+        k = key[it] > cut || (key[it] == cut && tie + __popc(eq & ((1u << lane) - 1u)) < (int)need);
+        tie += __popc(eq);
+      }
       const uint32_t kept = __ballot_sync(kFull, k);
       mine |= (uint32_t)k << it;
-      tie += __popc(eq);
       const int below = min(max(a.keep - (base + 32 * it), 0), 32);   // positions of the 32 below keep
       const uint32_t lo = below == 32 ? 0xffffffffu : (1u << below) - 1u;
       nh += __popc(~kept & lo);
@@ -274,22 +278,29 @@ select_kernel(const __grid_constant__ EvictArgs a) {
     for (int it = 0; it < ITEMS; ++it) t += __popc(__ballot_sync(kFull, key[it] == cut));
     return t;
   };
-  for (int r = 0; r < rounds; ++r) {
-    if (rounds > 1) load(r);
+  // the ties before this warp's rows of a span (only where they decide)
+  auto ties_before = [&] {
+    if (!split) return 0;
     warps_before(s, warp, lane, span_ties(), 0, bx, by, tx, ty);
+    const int t = ties + bx;
     ties += tx;
+    return t;
+  };
+  int ties0 = 0;
+  if (split) {                   // (the same in every CTA of the cluster)
+    for (int r = 0; r < rounds; ++r) {
+      if (rounds > 1) load(r);
+      ties_before();
+    }
+    share(0, ties);
+    cluster_sync();
+    ties0 = before_rank(0, total);
   }
-  share(0, ties);
-  cluster_sync();
-  const int ties0 = before_rank(0, total);
-  int nh = 0, nm = 0, tie = 0;
+  int nh = 0, nm = 0;
   ties = ties0;
   for (int r = 0; r < rounds; ++r) {
     if (rounds > 1) load(r);
-    warps_before(s, warp, lane, span_ties(), 0, bx, by, tx, ty);
-    tie = ties + bx;
-    ties += tx;
-    keep_span(r, tie, nh, nm);
+    keep_span(r, ties_before(), nh, nm);
     warps_before(s, warp, lane, nh, nm, bx, by, tx, ty);
     holes += tx;
     movers += ty;
@@ -304,10 +315,7 @@ select_kernel(const __grid_constant__ EvictArgs a) {
   for (int r = 0; r < rounds; ++r) {
     if (rounds > 1) {
       load(r);
-      warps_before(s, warp, lane, span_ties(), 0, bx, by, tx, ty);
-      tie = ties + bx;
-      ties += tx;
-      keep_span(r, tie, nh, nm);
+      keep_span(r, ties_before(), nh, nm);
       warps_before(s, warp, lane, nh, nm, bx, by, tx, ty);
     }
     const int base = begin + r * kSpan + warp * 32 * ITEMS;
@@ -527,6 +535,7 @@ void launch_select(const EvictArgs& a, int B, cudaStream_t st) {
   const long rows = ceil_div(a.map.cap, ranks);
   if (rows <= 4 * kSelThreads) launch_cluster<4, kQ8>(a, B, ranks, st);
   else if (rows <= 8 * kSelThreads) launch_cluster<8, kQ8>(a, B, ranks, st);
+  else if (rows <= 12 * kSelThreads) launch_cluster<12, kQ8>(a, B, ranks, st);
   else launch_cluster<16, kQ8>(a, B, ranks, st);
 }
 
@@ -579,7 +588,8 @@ tsd_status evict_impl(const tsd_attn_desc* d, int keep, int sink, int recent, fl
   // about eight CTAs per SM over all heads, no more than there can be work for
   if (q8) {
     launch_select<true>(a, d->B, st);
-    long x = ceil_div(152L * 8, heads);
+    // (more than are resident: most CTAs of a small cut find no hole)
+    long x = ceil_div(152L * 32, heads);
     const long most = ceil_div(keep, kQ8Block);
     if (x > most) x = most;
     launch(move_q8_kernel, dim3((unsigned)x, d->Hkv, d->B), dim3(kMoveQ8Threads), 0, st, a);

@@ -329,15 +329,14 @@ __global__ void __launch_bounds__(128) q8_combine_kernel(const __grid_constant__
     }
 #pragma unroll
     for (int s = 0; s < kBatch; ++s) {
+      if (s0 + s >= n) break;            // (the same for the whole warp)
       const float ws = __shfl_sync(kFull, wt, (s0 + s) & 31);
-      if (s0 + s < n) {
 #pragma unroll
-        for (int i = 0; i < kStep; ++i) {
-          float x[4];
-          part_values(w[s][i], x, PT());
+      for (int i = 0; i < kStep; ++i) {
+        float x[4];
+        part_values(w[s][i], x, PT());
 #pragma unroll
-          for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(ws, x[j], acc[i][j]);
-        }
+        for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(ws, x[j], acc[i][j]);
       }
     }
   }
@@ -370,13 +369,13 @@ Q8Plan plan_q8(const tsd_attn_desc& d) {
     }
     // One CTA per SM.  The split count minimises the modelled time of requests
     // that fill the cache: waves of CTAs times (tiles of a CTA + 4 for its
-    // set-up and epilogue).
+    // set-up and epilogue), and 5 tiles' time for the merge.
     const long units = (long)d.B * d.Hkv * p.nrg, tiles = ceil_div(d.cap, 128);
     const long lo = ceil_div(tiles, 256), hi = lo > 64 ? lo : tiles < 64 ? tiles : 64;
     long best = -1, best_per = tiles;
     for (long n = lo; n <= hi; ++n) {
       const long per = ceil_div(tiles, n);
-      const long cost = ceil_div(units * ceil_div(tiles, per), 152L) * (per + 4);
+      const long cost = ceil_div(units * ceil_div(tiles, per), 152L) * (per + 4) + (per < tiles ? 5 : 0);
       if (best < 0 || cost < best) { best = cost; best_per = per; }
     }
     p.split_len = (int)best_per * 128;
