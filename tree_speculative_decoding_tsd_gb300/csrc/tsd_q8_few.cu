@@ -23,9 +23,9 @@
 // old maximum (p <= 256); else, and on the stream's first tile, the warpgroup takes
 // the tile's column maxima, re-centres x, and scales the sums and the O^T columns.
 //
-// Roles (576 threads): warps 0-3 and 4-7 softmax and epilogue; warp 8 issues the
-// products and owns the tensor memory; one thread of warp 9 loads K tiles by TMA into
-// a ring of four; warps 10-17 load V tiles straight into registers, two tiles ahead
+// Roles (608 threads): warps 0-3 and 4-7 softmax and epilogue; warp 8 issues the
+// products with Q and owns the tensor memory, warp 9 those with V; one thread of
+// warp 10 loads K tiles by TMA into a ring of four; warps 11-18 load V tiles straight into registers, two tiles ahead
 // (behind L2 prefetches), and widen them into two fp16 stages, laid out as the
 // product reads them (rows of 64 elements, 128-byte swizzle).  mbarriers order K ->
 // S^T -> softmax -> O^T and V -> O^T; every wait is bounded.
@@ -36,7 +36,7 @@
 namespace tsd {
 namespace {
 
-constexpr int kMma = 8, kTma = 9, kWide = 10, kWideWarps = 8;
+constexpr int kQk = 8, kPv = 9, kTma = 10, kWide = 11, kWideWarps = 8;
 constexpr int kWideThreads = kWideWarps * 32;
 constexpr int kThreads = (kWide + kWideWarps) * 32;
 constexpr int kDepth = 2;                        // V tiles in registers
@@ -64,7 +64,7 @@ struct FewLayout {
   static constexpr uint32_t off_kex = off_tree + 16 * kKeys;     // u8[2 kMaxTiles]
   static constexpr uint32_t off_vex = off_kex + 2 * kMaxTiles;
   static constexpr uint32_t off_bar = off_vex + 2 * kMaxTiles;
-  static constexpr int nbar = 19;
+  static constexpr int nbar = 20;
   static constexpr uint32_t off_flags = off_bar + 8 * nbar;      // tmem, abort
   static constexpr uint32_t off_top = off_flags + 8;             // int[kWideWarps]
   static constexpr uint32_t total = off_top + 4 * kWideWarps;
@@ -73,9 +73,10 @@ struct FewLayout {
 
 // FULL: the copy landed or the warps wrote; EMPTY: read by the product (V_EMPTY
 // is also the end of a tile's O^T product); T_FULL: the scratch rows' keys, which
-// take the two K slots behind the last prefix tile (hi, lo).
+// take the two K slots behind the last prefix tile (hi, lo); FINAL: one per issuing
+// warp.
 enum { BAR_K_FULL = 0, BAR_K_EMPTY = 4, BAR_V_FULL = 8, BAR_V_EMPTY = 10, BAR_S_FULL = 12,
-       BAR_P_FULL = 14, BAR_FINAL = 16, BAR_O_DONE = 17, BAR_T_FULL = 18 };
+       BAR_P_FULL = 14, BAR_FINAL = 16, BAR_O_DONE = 18, BAR_T_FULL = 19 };
 
 template <int N, int D>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -196,8 +197,8 @@ q8_few_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
         mbar_init(bar(BAR_V_EMPTY + i), 1);
         mbar_init(bar(BAR_S_FULL + i), 1);
         mbar_init(bar(BAR_P_FULL + i), 4);
+        mbar_init(bar(BAR_FINAL + i), 1);
       }
-      mbar_init(bar(BAR_FINAL), 1);
       mbar_init(bar(BAR_O_DONE), 1);
       mbar_init(bar(BAR_T_FULL), kWideWarps);
       flags[1] = 0;
@@ -208,7 +209,7 @@ q8_few_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
                   sbase + L::off_k + t * L::k_bytes, L::k_bytes, bar(BAR_K_FULL + t));
     }
     __syncwarp();
-  } else {
+  } else if (warp == kQk) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 128;\n" ::"r"(
         sbase + L::off_flags));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n");
@@ -307,63 +308,76 @@ q8_few_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
     if (!ok) flags[1] = 1;
   }
 
-  // ------------------------------------------------------------- products
-  else if (warp == kMma) {
-    if (lane == 0) {
-      // fp32 accumulators; e4m3 (S^T) and fp16 (O^T) operands are both format 0
-      const uint32_t idesc_qk = (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(kKeys >> 4) << 24);
-      const uint32_t idesc_pv = idesc_qk | (1u << 15) | (1u << 16);
-      const uint64_t kd0 = row_desc<D>(sbase + L::off_k);
-      const uint64_t qd0 = row_desc<D>(sbase + L::off_q);
-      const uint64_t vd0 = smem_desc(sbase + L::off_v, kHalf, 1024);
-      // P^T: 8x8 cores, the key groups of 8 columns contiguous (tsd_verify_tc.cu)
-      const uint64_t pd0 = smem_desc_interleave(sbase + L::off_p, 128, 2048);
-      // S^T (+)= K slot x (Q hi + Q lo)
-      auto products = [&](uint32_t ts, int sl, bool first) {
-        const uint64_t kd = kd0 + (uint64_t)(sl * (L::k_bytes >> 4));
+  // ------------------------------------------------------------- scores
+  else if (warp == kQk) {
+    // fp32 accumulators; e4m3 (S^T) and fp16 (O^T) operands are both format 0
+    constexpr uint32_t idesc = (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(kKeys >> 4) << 24);
+    const uint64_t kd0 = row_desc<D>(sbase + L::off_k);
+    const uint64_t qd0 = row_desc<D>(sbase + L::off_q);
+    const bool one = elect_one();
+    bool ok = true;
+    for (int t = 0; t < ntiles; ++t) {
+      const int p = t & 1, sl = t % kRing;
+      // (the stream's scores before have been read once its P^T is there)
+      ok = (t < n_pre ? wait_ready(bar(BAR_K_FULL + sl), (t / kRing) & 1) : wait_ready(bar(BAR_T_FULL), 0)) &&
+           (t < 2 || wait_ready(bar(BAR_P_FULL + p), ((t - 2) >> 1) & 1));
+      if (!__all_sync(kFull, ok)) break;
+      fence_after();
+      const uint32_t ts = tmem + (uint32_t)(p * N);
+      const uint64_t kd = kd0 + (uint64_t)(sl * (L::k_bytes >> 4));
+      if (one) {
+        // S^T = K slot x (Q hi + Q lo); the scratch rows' second slot adds their lo
 #pragma unroll
         for (int part = 0; part < 2; ++part)
 #pragma unroll
           for (int kk = 0; kk < D / 32; ++kk)
-            mma_f8(ts, kd + 2 * kk, qd0 + (uint64_t)(part * (L::q_bytes >> 4)) + 2 * kk, idesc_qk,
-                   first && part == 0 && kk == 0 ? 0u : 1u);
-      };
-      auto issue_qk = [&](int t) -> bool {
-        const int sl = t % kRing;
-        if (!(t < n_pre ? mbar_wait(bar(BAR_K_FULL + sl), (t / kRing) & 1)
-                        : mbar_wait(bar(BAR_T_FULL), 0)))
-          return false;
-        fence_after();
-        products(tm_s(t & 1), sl, true);
-        if (t >= n_pre) products(tm_s(t & 1), (t + 1) % kRing, false);
-        mma_commit(bar(BAR_S_FULL + (t & 1)));
+            mma_f8(ts, kd + 2 * kk, qd0 + (uint64_t)(part * (L::q_bytes >> 4)) + 2 * kk, idesc,
+                   part + kk == 0 ? 0u : 1u);
+        if (t >= n_pre) {
+          const uint64_t k2 = kd0 + (uint64_t)(((t + 1) % kRing) * (L::k_bytes >> 4));
+#pragma unroll
+          for (int part = 0; part < 2; ++part)
+#pragma unroll
+            for (int kk = 0; kk < D / 32; ++kk)
+              mma_f8(ts, k2 + 2 * kk, qd0 + (uint64_t)(part * (L::q_bytes >> 4)) + 2 * kk, idesc, 1u);
+        }
+        mma_commit(bar(BAR_S_FULL + p));
         mma_commit(bar(BAR_K_EMPTY + sl));
-        return true;
-      };
-      bool ok = issue_qk(0) && (ntiles < 2 || issue_qk(1));
-      for (int t = 0; ok && t < ntiles; ++t) {
-        const int p = t & 1;
-        // a stream's scores have been read once its P^T is there
-        ok = mbar_wait(bar(BAR_P_FULL + p), (t >> 1) & 1) && !flags[1] &&
-             (t + 2 >= ntiles || issue_qk(t + 2)) && mbar_wait(bar(BAR_V_FULL + p), (t >> 1) & 1);
-        if (!ok) break;
-        fence_after();
-        const uint64_t vd = vd0 + (uint64_t)(p * (kTile >> 4));
-        const uint64_t pd = pd0 + (uint64_t)(p * (L::pt_bytes >> 4));
-        if (t < 2) mma_f16(tm_o(p), vd, pd, idesc_pv, 0u);
-        else mma_f16_acc(tm_o(p), vd, pd, idesc_pv);
+      }
+      __syncwarp();
+    }
+    if (!ok) flags[1] = 1;
+  }
+
+  // ------------------------------------------------------------- outputs
+  else if (warp == kPv) {
+    constexpr uint32_t idesc = (1u << 4) | (1u << 15) | (1u << 16) | ((uint32_t)(N >> 3) << 17) |
+                               ((uint32_t)(kKeys >> 4) << 24);
+    const uint64_t vd0 = smem_desc(sbase + L::off_v, kHalf, 1024);
+    // P^T: 8x8 cores, the key groups of 8 columns contiguous (tsd_verify_tc.cu)
+    const uint64_t pd0 = smem_desc_interleave(sbase + L::off_p, 128, 2048);
+    const bool one = elect_one();
+    bool ok = true;
+    for (int t = 0; t < ntiles; ++t) {
+      const int p = t & 1;
+      const uint32_t par = (t >> 1) & 1;
+      ok = wait_ready(bar(BAR_V_FULL + p), par) && wait_ready(bar(BAR_P_FULL + p), par) && !flags[1];
+      if (!__all_sync(kFull, ok)) break;
+      fence_after();
+      const uint64_t vd = vd0 + (uint64_t)(p * (kTile >> 4));
+      const uint64_t pd = pd0 + (uint64_t)(p * (L::pt_bytes >> 4));
+      const uint32_t to = tmem + (uint32_t)((2 + p) * N);
+      if (one) {
+        mma_f16(to, vd, pd, idesc, t < 2 ? 0u : 1u);
 #pragma unroll
         for (int kk = 1; kk < kKeys / 16; ++kk)
-          mma_f16_acc(tm_o(p), vd + 128 * kk, pd + (uint64_t)(16 * kk), idesc_pv);
+          mma_f16_acc(to, vd + 128 * kk, pd + (uint64_t)(16 * kk), idesc);
         mma_commit(bar(BAR_V_EMPTY + p));
+        if (t == ntiles - 1) mma_commit(bar(BAR_O_DONE));
       }
-      if (ok) mma_commit(bar(BAR_O_DONE));
-      else flags[1] = 1;
-      // every product has completed once this commit lands
-      mma_commit(bar(BAR_FINAL));
-      mbar_wait(bar(BAR_FINAL), 0);
+      __syncwarp();
     }
-    __syncwarp();
+    if (!ok) flags[1] = 1;
   }
 
   // -------------------------------------------------------------- softmax
@@ -394,7 +408,7 @@ q8_few_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
         fv = pow2i((int)vex[2 * t + (key >> 6)] - 127 - U + kHeadroom);
       }
       const float2 ck2 = make_float2(ck, ck), fv2 = make_float2(fv, fv);
-      const bool ok = __all_sync(kFull, mbar_wait(bar(BAR_S_FULL + p), (t >> 1) & 1));
+      const bool ok = __all_sync(kFull, wait_ready(bar(BAR_S_FULL + p), (t >> 1) & 1));
       fence_after();
       // x = S^T * scale - m, and the largest x
       float v[N];
@@ -466,7 +480,7 @@ q8_few_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
         }
         wg_bar(p);
         // the stream's product before must be done before its columns are scaled
-        if (t > p && !__all_sync(kFull, mbar_wait(bar(BAR_V_EMPTY + p), ((t - 2) >> 1) & 1)))
+        if (t > p && !__all_sync(kFull, wait_ready(bar(BAR_V_EMPTY + p), ((t - 2) >> 1) & 1)))
           failed = true;
         fence_after();
 #pragma unroll
@@ -490,7 +504,7 @@ q8_few_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
         }
       }
       // P^T's buffer was last read by the stream's product before
-      if (t > p && !__all_sync(kFull, mbar_wait(bar(BAR_V_EMPTY + p), ((t - 2) >> 1) & 1))) failed = true;
+      if (t > p && !__all_sync(kFull, wait_ready(bar(BAR_V_EMPTY + p), ((t - 2) >> 1) & 1))) failed = true;
 #pragma unroll
       for (int u = 0; u < N; u += 8) {
         uint32_t w[4];
@@ -578,11 +592,18 @@ q8_few_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
   }
 
   // --------------------------------------------------------------- teardown
+  // Products in flight: the issuing warps wait for a commit of their own.
+  if (warp == kQk || warp == kPv) {
+    if (elect_one()) mma_commit(bar(BAR_FINAL + warp - kQk));
+    __syncwarp();
+    mbar_wait(bar(BAR_FINAL + warp - kQk), 0);
+  }
+  __syncwarp();
   fence_before();
   __syncthreads();
   if (flags[1] && tid == 0) report_error(a.err, TSD_DEV_ERR_TIMEOUT, b);
   fence_after();
-  if (warp == kMma) {
+  if (warp == kQk) {
     __syncwarp();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 128;\n" ::"r"(tmem));
   }

@@ -20,6 +20,27 @@ constexpr int kHeadroom = 7;                    // P's offset: 2^8 * 2^7 < 65504
 constexpr int kMaxTiles = 256;                  // prefix tiles of a split
 constexpr int kPrefetch = 4;                    // tiles that V's L2 prefetch runs ahead
 
+// Wait for a phase that is usually complete already: one look before the timed
+// wait.
+__device__ __forceinline__ bool wait_ready(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+      " selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok || mbar_wait(bar, parity);
+}
+// One lane of a converged warp.  A warp that issues products runs its loop on all
+// lanes, so that descriptors and addresses are uniform values, and issues on this
+// lane.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
+  return p != 0;
+}
+
 // D (+)= A.B, 8-bit operands (e4m3), K = 32 per instruction.
 __device__ __forceinline__ void mma_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
                                        uint32_t acc) {
