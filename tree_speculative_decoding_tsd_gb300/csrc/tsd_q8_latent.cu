@@ -396,75 +396,82 @@ q8_latent_kernel(const __grid_constant__ LatentMaps maps, const __grid_constant_
 
   // ------------------------------------------------------------- scores
   else if (warp == kQk) {
-    if (lane == 0) {
-      const uint32_t idesc =
-          (1u << 4) | ((uint32_t)(2 * kN >> 3) << 17) | ((uint32_t)(kKeys >> 4) << 24);
-      // S^T (+)= K piece j in slot sl x Q piece j
-      auto products = [&](uint32_t ts, int sl, int j, bool first) {
-        const uint32_t k = sbase + kOffK + sl * kPiece, q = sbase + kOffQ + j * kPiece;
-        if (j < 4) {
-          const uint64_t kd = row_desc<128>(k), qd = row_desc<128>(q);
+    constexpr uint32_t idesc =
+        (1u << 4) | ((uint32_t)(2 * kN >> 3) << 17) | ((uint32_t)(kKeys >> 4) << 24);
+    const bool one = elect_one();
+    // S^T (+)= K piece j in slot sl x Q piece j
+    auto products = [&](uint32_t ts, int sl, int j, bool first) {
+      const uint32_t k = sbase + kOffK + sl * kPiece, q = sbase + kOffQ + j * kPiece;
+      if (j < 4) {
+        const uint64_t kd = row_desc<128>(k), qd = row_desc<128>(q);
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            mma_f8(ts, kd + 2 * kk, qd + 2 * kk, idesc, first && kk == 0 ? 0u : 1u);
-        } else {
-          const uint64_t kd = row_desc<64>(k), qd = row_desc<64>(q);
+        for (int kk = 0; kk < 4; ++kk)
+          mma_f8(ts, kd + 2 * kk, qd + 2 * kk, idesc, first && kk == 0 ? 0u : 1u);
+      } else {
+        const uint64_t kd = row_desc<64>(k), qd = row_desc<64>(q);
 #pragma unroll
-          for (int kk = 0; kk < 2; ++kk) mma_f8(ts, kd + 2 * kk, qd + 2 * kk, idesc, 1u);
-        }
-      };
-      bool ok = true;
-      for (int t = 0; ok && t < ntiles; ++t) {
-        const int st = t & 1;
-        // the buffer's scores of tile t - 2 have been read once its P is there
-        if (t >= 2) ok = mbar_wait(bar(BAR_P_FULL + st), ((t - 2) >> 1) & 1);
-        const int n = t < n_pre ? kPieces : 2 * kPieces;
-        for (int i = 0; ok && i < n; ++i) {
-          const int g = kPieces * t + i, sl = g % kSlots;
-          ok = (t < n_pre ? mbar_wait(bar(BAR_K_FULL + sl), (g / kSlots) & 1)
-                          : mbar_wait(bar(BAR_T_FULL + sl), (i / kSlots) & 1)) && !flags[1];
-          if (!ok) break;
-          fence_after();
-          products(tm_s(st), sl, i % kPieces, i == 0);
-          mma_commit(bar(BAR_K_EMPTY + sl));
-        }
-        if (ok) mma_commit(bar(BAR_S_FULL + st));
+        for (int kk = 0; kk < 2; ++kk) mma_f8(ts, kd + 2 * kk, qd + 2 * kk, idesc, 1u);
       }
-      if (!ok) flags[1] = 1;
+    };
+    bool ok = true;
+    for (int t = 0; ok && t < ntiles; ++t) {
+      const int st = t & 1;
+      // the buffer's scores of tile t - 2 have been read once its P is there
+      if (t >= 2) ok = wait_ready(bar(BAR_P_FULL + st), ((t - 2) >> 1) & 1);
+      const int n = t < n_pre ? kPieces : 2 * kPieces;
+      for (int i = 0; i < n; ++i) {
+        const int g = kPieces * t + i, sl = g % kSlots;
+        ok = ok && (t < n_pre ? wait_ready(bar(BAR_K_FULL + sl), (g / kSlots) & 1)
+                              : wait_ready(bar(BAR_T_FULL + sl), (i / kSlots) & 1));
+        ok = __all_sync(kFull, ok);
+        if (!ok) break;
+        fence_after();
+        if (one) {
+          products(tmem + (uint32_t)(st * 2 * kN), sl, i % kPieces, i == 0);
+          mma_commit(bar(BAR_K_EMPTY + sl));
+          if (i == n - 1) mma_commit(bar(BAR_S_FULL + st));
+        }
+        __syncwarp();
+      }
     }
-    __syncwarp();
+    if (!ok) flags[1] = 1;
   }
 
   // ------------------------------------------------------------- outputs
   else if (warp == kPv) {
-    if (lane == 0) {
-      const uint32_t idesc = (1u << 4) | (1u << 15) | (1u << 16) | ((uint32_t)(kN >> 3) << 17) |
-                             ((uint32_t)(kKeys >> 4) << 24);
-      const uint64_t vd0 = smem_desc(sbase + kOffV, kHalf, 1024);
-      const uint64_t pd0 = smem_desc_interleave(sbase + kOffP, 128, 2048);
-      bool ok = true;
-      for (int t = 0; ok && t < ntiles; ++t) {
-        ok = mbar_wait(bar(BAR_P_FULL + (t & 1)), (t >> 1) & 1);
-        const uint64_t pd = pd0 + (uint64_t)((t & 1) * (kPtBytes >> 4));
-        for (int u = 0; ok && u < kUnits; ++u) {
-          const int g = kUnits * t + u;
-          ok = mbar_wait(bar(BAR_V_FULL + (g & 1)), (g >> 1) & 1) && !flags[1];
-          if (!ok) break;
-          fence_after();
-          const uint64_t vd = vd0 + (uint64_t)((g & 1) * (kTile >> 4));
-          if (t == 0) mma_f16(tm_o(u), vd, pd, idesc, 0u);
-          else mma_f16_acc(tm_o(u), vd, pd, idesc);
+    constexpr uint32_t idesc = (1u << 4) | (1u << 15) | (1u << 16) | ((uint32_t)(kN >> 3) << 17) |
+                               ((uint32_t)(kKeys >> 4) << 24);
+    const uint64_t vd0 = smem_desc(sbase + kOffV, kHalf, 1024);
+    const uint64_t pd0 = smem_desc_interleave(sbase + kOffP, 128, 2048);
+    const bool one = elect_one();
+    bool ok = true;
+    for (int t = 0; ok && t < ntiles; ++t) {
+      ok = wait_ready(bar(BAR_P_FULL + (t & 1)), (t >> 1) & 1) && !flags[1];
+      const uint64_t pd = pd0 + (uint64_t)((t & 1) * (kPtBytes >> 4));
+#pragma unroll
+      for (int u = 0; u < kUnits; ++u) {
+        const int st = u & 1;                    // (four boxes a tile)
+        ok = ok && wait_ready(bar(BAR_V_FULL + st), (2 * t + (u >> 1)) & 1);
+        ok = __all_sync(kFull, ok);
+        if (!ok) break;
+        fence_after();
+        const uint64_t vd = vd0 + (uint64_t)(st * (kTile >> 4));
+        const uint32_t to = tmem + 4u * kN + (uint32_t)(u * kN);
+        if (one) {
+          mma_f16(to, vd, pd, idesc, t == 0 ? 0u : 1u);
 #pragma unroll
           for (int kk = 1; kk < kKeys / 16; ++kk)
-            mma_f16_acc(tm_o(u), vd + 128 * kk, pd + (uint64_t)(16 * kk), idesc);
-          mma_commit(bar(BAR_V_EMPTY + (g & 1)));
+            mma_f16_acc(to, vd + 128 * kk, pd + (uint64_t)(16 * kk), idesc);
+          mma_commit(bar(BAR_V_EMPTY + st));
+          if (u == kUnits - 1) {
+            mma_commit(bar(BAR_PV_DONE + (t & 1)));
+            if (t == ntiles - 1) mma_commit(bar(BAR_O_DONE));
+          }
         }
-        if (ok) mma_commit(bar(BAR_PV_DONE + (t & 1)));
+        __syncwarp();
       }
-      if (ok) mma_commit(bar(BAR_O_DONE));
-      else flags[1] = 1;
     }
-    __syncwarp();
+    if (!ok) flags[1] = 1;
   }
 
   // -------------------------------------------------------------- softmax
@@ -493,7 +500,7 @@ q8_latent_kernel(const __grid_constant__ LatentMaps maps, const __grid_constant_
         fv = pow2i((int)kex[2 * t + (key >> 6)] - 127 - U + kHeadroom);
       }
       const float2 ck2 = make_float2(ck, ck), fv2 = make_float2(fv, fv);
-      const bool ok = __all_sync(kFull, mbar_wait(bar(BAR_S_FULL + st), (t >> 1) & 1));
+      const bool ok = __all_sync(kFull, wait_ready(bar(BAR_S_FULL + st), (t >> 1) & 1));
       fence_after();
       const uint32_t srow = tm_s(st) + lane_off + (uint32_t)c0;
       float v[kNH];
@@ -571,7 +578,7 @@ q8_latent_kernel(const __grid_constant__ LatentMaps maps, const __grid_constant_
           negm[col] = m_new == -INFINITY ? 0.f : -m_new;
         }
         wg_bar(wg);
-        if (t > 0 && !__all_sync(kFull, mbar_wait(bar(BAR_PV_DONE + ((t - 1) & 1)), ((t - 1) >> 1) & 1)))
+        if (t > 0 && !__all_sync(kFull, wait_ready(bar(BAR_PV_DONE + ((t - 1) & 1)), ((t - 1) >> 1) & 1)))
           failed = true;
         fence_after();
 #pragma unroll
@@ -599,7 +606,7 @@ q8_latent_kernel(const __grid_constant__ LatentMaps maps, const __grid_constant_
         }
       }
       // P^T buffer st was last read by tile t - 2's products
-      if (t >= 2 && !__all_sync(kFull, mbar_wait(bar(BAR_PV_DONE + st), ((t - 2) >> 1) & 1)))
+      if (t >= 2 && !__all_sync(kFull, wait_ready(bar(BAR_PV_DONE + st), ((t - 2) >> 1) & 1)))
         failed = true;
       uint32_t w[kNH / 2];
 #pragma unroll
@@ -677,9 +684,10 @@ q8_latent_kernel(const __grid_constant__ LatentMaps maps, const __grid_constant_
   }
 
   // --------------------------------------------------------------- teardown
-  // Products in flight: the issuing threads wait for a commit of their own.
-  if ((warp == kQk || warp == kPv) && lane == 0) {
-    mma_commit(bar(BAR_FINAL + warp - kQk));
+  // Products in flight: the issuing warps wait for a commit of their own.
+  if (warp == kQk || warp == kPv) {
+    if (elect_one()) mma_commit(bar(BAR_FINAL + warp - kQk));
+    __syncwarp();
     mbar_wait(bar(BAR_FINAL + warp - kQk), 0);
   }
   __syncwarp();

@@ -373,69 +373,77 @@ q8_rows_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
 
   // ------------------------------------------------------------- scores
   else if (warp == kQk) {
-    if (lane == 0) {
-      // fp32 accumulator; e4m3 operands are format 0
-      const uint32_t idesc =
-          (1u << 4) | ((uint32_t)(kKeys >> 3) << 17) | ((uint32_t)(kRows >> 4) << 24);
-      const uint64_t kd0 = row_desc<D>(sbase + L::off_k);
-      const uint32_t tq = tmem + kColQ;
-      // S (+)= (Q hi + Q lo) x K slot
-      auto products = [&](int sl, bool first) {
-        const uint64_t kd = kd0 + (uint64_t)(sl * (L::k_bytes >> 4));
+    // fp32 accumulator; e4m3 operands are format 0
+    constexpr uint32_t idesc =
+        (1u << 4) | ((uint32_t)(kKeys >> 3) << 17) | ((uint32_t)(kRows >> 4) << 24);
+    const uint64_t kd0 = row_desc<D>(sbase + L::off_k);
+    const uint32_t tq = tmem + kColQ;
+    const bool one = elect_one();
+    bool ok = wait_ready(bar(BAR_Q_FULL), 0);
+    for (int t = 0; t < ntiles; ++t) {
+      const int sl = t % kRing;
+      ok = ok && (t < n_pre ? wait_ready(bar(BAR_K_FULL + sl), (t / kRing) & 1)
+                            : wait_ready(bar(BAR_T_FULL), 0)) &&
+           (t == 0 || wait_ready(bar(BAR_S_EMPTY), (t - 1) & 1));
+      if (!__all_sync(kFull, ok)) break;
+      fence_after();
+      const uint64_t kd = kd0 + (uint64_t)(sl * (L::k_bytes >> 4));
+      if (one) {
+        // S = (Q hi + Q lo) x K slot; the scratch rows' second slot adds their lo
 #pragma unroll
         for (int part = 0; part < 2; ++part)
 #pragma unroll
           for (int kk = 0; kk < D / 32; ++kk)
-            mma_f8_ta(tmem, tq + part * (D / 4) + 8 * kk, kd + 2 * kk, idesc,
-                      first && part == 0 && kk == 0 ? 0u : 1u);
-      };
-      bool ok = mbar_wait(bar(BAR_Q_FULL), 0);
-      for (int t = 0; ok && t < ntiles; ++t) {
-        const int sl = t % kRing;
-        ok = (t < n_pre ? mbar_wait(bar(BAR_K_FULL + sl), (t / kRing) & 1)
-                        : mbar_wait(bar(BAR_T_FULL), 0)) &&
-             (t == 0 || mbar_wait(bar(BAR_S_EMPTY), (t - 1) & 1)) && !flags[1];
-        if (!ok) break;
-        fence_after();
-        products(sl, true);
-        if (t >= n_pre) products((t + 1) % kRing, false);
+            mma_f8_ta(tmem, tq + part * (D / 4) + 8 * kk, kd + 2 * kk, idesc, part + kk == 0 ? 0u : 1u);
+        if (t >= n_pre) {
+          const uint64_t k2 = kd0 + (uint64_t)(((t + 1) % kRing) * (L::k_bytes >> 4));
+#pragma unroll
+          for (int part = 0; part < 2; ++part)
+#pragma unroll
+            for (int kk = 0; kk < D / 32; ++kk)
+              mma_f8_ta(tmem, tq + part * (D / 4) + 8 * kk, k2 + 2 * kk, idesc, 1u);
+        }
         mma_commit(bar(BAR_S_FULL));
         mma_commit(bar(BAR_K_EMPTY + sl));
       }
-      if (!ok) flags[1] = 1;
+      __syncwarp();
     }
-    __syncwarp();
+    if (!ok) flags[1] = 1;
   }
 
   // ------------------------------------------------------------- outputs
   else if (warp == kPv) {
-    if (lane == 0) {
-      // fp16 operands are format 0; B (V) is N-major
-      const uint32_t idesc =
-          (1u << 4) | (1u << 16) | ((uint32_t)(D >> 3) << 17) | ((uint32_t)(kRows >> 4) << 24);
-      const uint64_t vd0 = smem_desc(sbase + L::off_v, kHalf, 1024);
-      bool ok = true;
-      for (int t = 0; ok && t < ntiles; ++t) {
-        const int st = t % kStages;
-        const uint64_t vd = vd0 + (uint64_t)(st * (L::v_bytes >> 4));
-        ok = mbar_wait(bar(BAR_V_FULL + st), (t / kStages) & 1);
+    // fp16 operands are format 0; B (V) is N-major
+    constexpr uint32_t idesc =
+        (1u << 4) | (1u << 16) | ((uint32_t)(D >> 3) << 17) | ((uint32_t)(kRows >> 4) << 24);
+    const uint64_t vd0 = smem_desc(sbase + L::off_v, kHalf, 1024);
+    const bool one = elect_one();
+    bool ok = true;
+    for (int t = 0; ok && t < ntiles; ++t) {
+      const int st = t % kStages;
+      const uint64_t vd = vd0 + (uint64_t)(st * (L::v_bytes >> 4));
+      ok = wait_ready(bar(BAR_V_FULL + st), (t / kStages) & 1) && !flags[1];
 #pragma unroll
-        for (int p = 0; ok && p < 2; ++p) {
-          ok = mbar_wait(bar(BAR_P_FULL + p), t & 1) && !flags[1];
-          if (!ok) break;
-          fence_after();
+      for (int p = 0; p < 2; ++p) {
+        ok = ok && wait_ready(bar(BAR_P_FULL + p), t & 1);
+        ok = __all_sync(kFull, ok);
+        if (!ok) break;
+        fence_after();
+        if (one) {
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
             mma_f16_ta(tm_o(p), tmem + kColP + 32 * p + 8 * kk, vd + 128 * (4 * p + kk), idesc,
                        t == 0 && kk == 0 ? 0u : 1u);
           mma_commit(bar(BAR_PV_DONE + p));
+          if (p == 1) {
+            mma_commit(bar(BAR_V_EMPTY + st));
+            if (t == ntiles - 1) mma_commit(bar(BAR_O_DONE));
+          }
         }
-        if (ok) mma_commit(bar(BAR_V_EMPTY + st));
+        __syncwarp();
       }
-      if (ok) mma_commit(bar(BAR_O_DONE));
-      else flags[1] = 1;
     }
-    __syncwarp();
+    if (!ok) flags[1] = 1;
   }
 
   // -------------------------------------------------------------- softmax
@@ -474,7 +482,7 @@ q8_rows_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
       // maximum is raised to X where X passes m by the headroom (or m is none),
       // the sum and the accumulator are rescaled.
       auto raise = [&](float X, int t) -> bool {
-        if (t > 0 && !__all_sync(kFull, mbar_wait(bar(BAR_PV_DONE + p), (t - 1) & 1))) return false;
+        if (t > 0 && !__all_sync(kFull, wait_ready(bar(BAR_PV_DONE + p), (t - 1) & 1))) return false;
         const bool need = !(X <= m + kOverflow);
         if (!__any_sync(kFull, need)) return true;
         const float m_new = need ? fmaxf(m, X) : m;
@@ -509,7 +517,7 @@ q8_rows_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
       for (int t = 0; t < ntiles; ++t) {
         const bool is_tree = t >= n_pre;
         const int nvalid = is_tree ? a.R : valid_of(t);
-        if (!__all_sync(kFull, mbar_wait(bar(BAR_S_FULL), t & 1))) {
+        if (!__all_sync(kFull, wait_ready(bar(BAR_S_FULL), t & 1))) {
           failed = true;
           break;
         }
@@ -654,9 +662,10 @@ q8_rows_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
   }
 
   // --------------------------------------------------------------- teardown
-  // Products in flight: the issuing threads wait for a commit of their own.
-  if ((warp >= kPv && warp < kTma) && lane == 0) {
-    mma_commit(bar(BAR_FINAL + warp - kPv));
+  // Products in flight: the issuing warps wait for a commit of their own.
+  if (warp == kPv || warp == kQk) {
+    if (elect_one()) mma_commit(bar(BAR_FINAL + warp - kPv));
+    __syncwarp();
     mbar_wait(bar(BAR_FINAL + warp - kPv), 0);
   }
   __syncwarp();

@@ -217,28 +217,30 @@ weights_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
 
   // ------------------------------------------------------------- products
   else if (warp == kMma) {
-    if (lane == 0) {
-      bool ok = true;
-      int item = 0;                                         // (tile, chunk of columns)
-      for (int i = 0; ok && i < ntiles; ++i) {
-        const bool is_path = with_path && i == 0;
-        const int g = is_path ? 0 : slots0 + i - (with_path ? 1 : 0), sl = g % p.ring;
-        // (the path's slots were written before the barrier: phase 0 of theirs is
-        // completed here, so that later uses count from it)
-        if (is_path)
-          for (int j = 0; j < kPathSlots; ++j) mbar_arrive(bar(BAR_FULL + j));
-        ok = mbar_wait(bar(BAR_FULL + sl), (g / p.ring) & 1);
-        for (int c = 0; ok && c < chunks; ++c, ++item) {
-          const int n = min(pad - c * kBufCols, kBufCols), buf = i & 1;
-          // the buffer's scores of its item before have been read
-          const int before = (i >> 1) * chunks + c;         // items of this buffer so far
-          if (before > 0) ok = mbar_wait(bar(BAR_S_EMPTY + buf), (before - 1) & 1);
-          if (!ok || *abort) { ok = false; break; }
-          fence_after();
-          const uint32_t ts = tmem + (uint32_t)(buf * kBufCols);
-          const uint32_t idesc = (1u << 4) | ((uint32_t)(n >> 3) << 17) |
-                                 ((uint32_t)(kWeightKeys >> 4) << 24) |
-                                 (kQ8 ? 0u : (1u << 7) | (1u << 10));       // bf16 operands
+    const bool one = elect_one();
+    // (the path's slots were written before the barrier: phase 0 of theirs is
+    // completed here, so that later uses count from it)
+    if (one && with_path)
+      for (int j = 0; j < kPathSlots; ++j) mbar_arrive(bar(BAR_FULL + j));
+    __syncwarp();
+    bool ok = true;
+    for (int i = 0; ok && i < ntiles; ++i) {
+      const bool is_path = with_path && i == 0;
+      const int g = is_path ? 0 : slots0 + i - (with_path ? 1 : 0), sl = g % p.ring;
+      ok = wait_ready(bar(BAR_FULL + sl), (g / p.ring) & 1);
+      for (int c = 0; c < chunks; ++c) {
+        const int n = min(pad - c * kBufCols, kBufCols), buf = i & 1;
+        // the buffer's scores of its item before have been read
+        const int before = (i >> 1) * chunks + c;           // items of this buffer so far
+        if (before > 0) ok = ok && wait_ready(bar(BAR_S_EMPTY + buf), (before - 1) & 1);
+        ok = __all_sync(kFull, ok);
+        if (!ok) break;
+        fence_after();
+        const uint32_t ts = tmem + (uint32_t)(buf * kBufCols);
+        const uint32_t idesc = (1u << 4) | ((uint32_t)(n >> 3) << 17) |
+                               ((uint32_t)(kWeightKeys >> 4) << 24) |
+                               (kQ8 ? 0u : (1u << 7) | (1u << 10));         // bf16 operands
+        if (one) {
           if constexpr (kQ8) {
             for (int kp = 0; kp < (is_path ? 2 : 1); ++kp) {
               const uint64_t kd = row_desc<D>(sbase + (is_path ? kp : sl) * kTileBytes);
@@ -260,17 +262,19 @@ weights_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
                       kk == 0 ? 0u : 1u);
           }
           mma_commit(bar(BAR_S_FULL + buf));
+          if (c == chunks - 1) {
+            mma_commit(bar(BAR_EMPTY + sl));
+            if (is_path && kPathSlots == 2) mma_commit(bar(BAR_EMPTY + 1));
+          }
         }
-        if (ok) {
-          mma_commit(bar(BAR_EMPTY + sl));
-          if (is_path && kPathSlots == 2) mma_commit(bar(BAR_EMPTY + 1));
-        }
+        __syncwarp();
       }
-      if (!ok) *abort = 1;
-      // every product has completed once this commit lands
-      mma_commit(bar(BAR_FINAL));
-      mbar_wait(bar(BAR_FINAL), 0);
     }
+    if (!ok) *abort = 1;
+    // every product has completed once this commit lands
+    if (one) mma_commit(bar(BAR_FINAL));
+    __syncwarp();
+    mbar_wait(bar(BAR_FINAL), 0);
     __syncwarp();
   }
 
@@ -294,7 +298,7 @@ weights_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
       float2 s0 = make_float2(0.f, 0.f), s1 = s0;
       for (int c = 0; c < chunks; ++c, ++done) {
         const int n = min(pad - c * kBufCols, kBufCols);
-        if (!__all_sync(kFull, mbar_wait(bar(BAR_S_FULL + wg), done & 1))) {
+        if (!__all_sync(kFull, wait_ready(bar(BAR_S_FULL + wg), done & 1))) {
           ok = false;
           break;
         }
