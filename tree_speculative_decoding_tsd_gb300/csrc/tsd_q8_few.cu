@@ -82,8 +82,6 @@ template <int N, int D>
 __global__ void __launch_bounds__(kThreads, 1)
 q8_few_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ Q8AttnArgs a) {
   using L = FewLayout<N, D>;
-  constexpr int CH = D / 16;                     // 16-code chunks of a row
-  constexpr int NT = kKeys * CH / kWideThreads;  // of a tile, per widening thread
   if (threadIdx.x == kTma * 32) tma_desc_prefetch(&kmap);
   grid_dependency_sync();
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -115,27 +113,13 @@ q8_few_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
   const int ntiles = n_pre + (with_tree ? 1 : 0);
   auto valid_of = [&](int t) { return min(kKeys, k1 - (k0 + t * kKeys)); };
 
-  // widening threads: chunk i of this thread is (row, 16-code chunk); eight
-  // lanes that store together take chunks 0-3 of an even and an odd row (D =
-  // 128), or of two rows (D = 64): eight different 16-byte columns of a
-  // swizzled row pair, so the stores do not conflict
   const int wt = tid - kWide * 32;
-  auto chunk_row = [&](int i) {
-    const int x = wt + kWideThreads * i;
-    return D == 128 ? 2 * (x >> 4) + ((x >> 2) & 1) : x >> 2;
-  };
-  auto chunk_col = [&](int i) {
-    const int x = wt + kWideThreads * i;
-    return D == 128 ? (x & 3) + 4 * ((x >> 3) & 1) : x & 3;
-  };
-  uint4 vreg[kDepth][NT];
-  auto load_v = [&](uint4 (&r)[NT], long row, int nvalid) {
-#pragma unroll
-    for (int i = 0; i < NT; ++i) {
-      r[i] = make_uint4(0u, 0u, 0u, 0u);
-      if (row >= 0 && chunk_row(i) < nvalid)
-        r[i] = ld_stream(a.vc + (row + chunk_row(i)) * D + chunk_col(i) * 16);
-    }
+  using Share = WideShare<D / 16, kWideThreads>;
+  const Share share(wt);
+  uint4 vreg[kDepth][Share::kCount];
+  // the tile at cache row `row` (a missing page: none)
+  auto load_v = [&](uint4 (&r)[Share::kCount], long row, int nvalid) {
+    share.template load<D>(r, a.vc + (row < 0 ? 0 : row) * D, row < 0 ? 0 : nvalid);
   };
 
   // ---------------------------------------------------------------- set-up
@@ -278,20 +262,7 @@ q8_few_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
         }
         uint8_t* const stage = smem + L::off_v + st * kTile;
         if (t < n_pre) {
-#pragma unroll
-          for (int c0 = 0; c0 < NT; ++c0) {
-            const int row = chunk_row(c0), c = chunk_col(c0);
-            const uint4& w = vreg[i][c0];
-            uint32_t h[8];
-            q8_half4(w.x, h[0], h[1]);
-            q8_half4(w.y, h[2], h[3]);
-            q8_half4(w.z, h[4], h[5]);
-            q8_half4(w.w, h[6], h[7]);
-            uint8_t* dst = stage + (c >> 2) * kHalf + row * 128;
-            const int u = 2 * (c & 3);
-            *(uint4*)(dst + (((u + 0) ^ (row & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
-            *(uint4*)(dst + (((u + 1) ^ (row & 7)) << 4)) = make_uint4(h[4], h[5], h[6], h[7]);
-          }
+          share.widen(vreg[i], stage);
         } else {
           tree_values<D>(a, b, hk, wt, kWideThreads, vt_in, stage);
         }

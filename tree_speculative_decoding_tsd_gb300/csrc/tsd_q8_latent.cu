@@ -41,8 +41,6 @@ constexpr int kWG = 4, kNH = kN / kWG;
 constexpr int kSoftWarps = 16, kQk = 16, kPv = 17, kTma = 18, kWide = 19, kWideWarps = 5;
 constexpr int kWideThreads = kWideWarps * 32;
 constexpr int kThreads = (kWide + kWideWarps) * 32;
-constexpr int kChunks = kKeys * 8;              // 16-code chunks of a V box
-constexpr int kNT = (kChunks + kWideThreads - 1) / kWideThreads;
 constexpr uint32_t kPiece = kKeys * 128;        // 16 KB
 constexpr uint32_t kPtBytes = 256u * kN;
 
@@ -128,26 +126,13 @@ q8_latent_kernel(const __grid_constant__ LatentMaps maps, const __grid_constant_
   const __nv_bfloat16* const tree = (const __nv_bfloat16*)a.kt + ((long)b * a.R * a.map.Hkv + hk) * kDK;
   const long tree_pitch = (long)a.map.Hkv * kDK;
 
-  // widening threads: as in tsd_q8_tc.cu, eight lanes that store together take
-  // chunks 0-3 or 4-7 of an even and an odd row
   const int wt = tid - kWide * 32;
-  auto chunk_row = [&](int i) {
-    const int x = wt + kWideThreads * i;
-    return 2 * (x >> 4) + ((x >> 2) & 1);
-  };
-  auto chunk_col = [&](int i) {
-    const int x = wt + kWideThreads * i;
-    return (x & 3) + 4 * ((x >> 3) & 1);
-  };
-  uint4 vreg[kNT];
+  using Share = WideShare<8, kWideThreads>;
+  const Share share(wt);
+  uint4 vreg[Share::kCount];
+  // 128 dims from 128 u of the tile at cache row `row` (a missing page: none)
   auto load_v = [&](long row, int nvalid, int u) {
-#pragma unroll
-    for (int i = 0; i < kNT; ++i) {
-      vreg[i] = make_uint4(0u, 0u, 0u, 0u);
-      // (the last round is short; a row past the tile is never valid)
-      if (row >= 0 && chunk_row(i) < nvalid)
-        vreg[i] = ld_stream(a.kc + (row + chunk_row(i)) * kDK + u * 128 + chunk_col(i) * 16);
-    }
+    share.load<kDK>(vreg, a.kc + (row < 0 ? 0 : row) * kDK + u * 128, row < 0 ? 0 : nvalid);
   };
   // K piece g (piece g % 5 of tile g / 5) by TMA into slot g % 3
   auto load_piece = [&](int g, long long row) {
@@ -360,20 +345,7 @@ q8_latent_kernel(const __grid_constant__ LatentMaps maps, const __grid_constant_
         }
         uint8_t* const stage = smem + kOffV + st * kTile;
         if (t < n_pre) {
-#pragma unroll
-          for (int i = 0; i < kNT; ++i) {
-            if (wt + kWideThreads * i >= kChunks) break;
-            const int row = chunk_row(i), c = chunk_col(i);
-            uint32_t h[8];
-            q8_half4(vreg[i].x, h[0], h[1]);
-            q8_half4(vreg[i].y, h[2], h[3]);
-            q8_half4(vreg[i].z, h[4], h[5]);
-            q8_half4(vreg[i].w, h[6], h[7]);
-            uint8_t* dst = stage + (c >> 2) * kHalf + row * 128;
-            const int x = 2 * (c & 3);
-            *(uint4*)(dst + (((x + 0) ^ (row & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
-            *(uint4*)(dst + (((x + 1) ^ (row & 7)) << 4)) = make_uint4(h[4], h[5], h[6], h[7]);
-          }
+          share.widen(vreg, stage);
         } else {
           for (int x = wt; x < kKeys * 16; x += kWideThreads) {
             const int row = x >> 4, c = x & 15;

@@ -144,9 +144,6 @@ template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
 q8_rows_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ Q8AttnArgs a) {
   using L = RowLayout<D>;
-  constexpr int CH = D / 16;                     // 16-code chunks of a row
-  constexpr int kChunks = kKeys * CH;
-  constexpr int NT = (kChunks + kWideThreads - 1) / kWideThreads;  // of a tile, per widening thread
   if (threadIdx.x == kTma * 32) tma_desc_prefetch(&kmap);
   grid_dependency_sync();
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -183,29 +180,14 @@ q8_rows_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
   // ---------------------------------------------------------------- set-up
   // Everything that the first products need is requested at once, by the warps
   // that will use it; one barrier, then Q's way into the tensor memory.
-  // widening threads: chunk i of this thread is (row, 16-code chunk); eight
-  // lanes that store together take chunks 0-3 of an even and an odd row (D =
-  // 128), or of two rows (D = 64): eight different 16-byte columns of a
-  // swizzled row pair, so the stores do not conflict
   const int wt = tid - kWide * 32;
-  auto chunk_row = [&](int i) {
-    const int x = wt + kWideThreads * i;
-    return D == 128 ? 2 * (x >> 4) + ((x >> 2) & 1) : x >> 2;
-  };
-  auto chunk_col = [&](int i) {
-    const int x = wt + kWideThreads * i;
-    return D == 128 ? (x & 3) + 4 * ((x >> 3) & 1) : x & 3;
-  };
+  using Share = WideShare<D / 16, kWideThreads>;
+  const Share share(wt);
   uint64_t mask = 0ull;     // softmax threads: the scratch rows that the row sees
-  uint4 vreg[NT];
+  uint4 vreg[Share::kCount];
+  // the tile at cache row `row` (a missing page: none)
   auto load_v = [&](long row, int nvalid) {
-#pragma unroll
-    for (int i = 0; i < NT; ++i) {
-      vreg[i] = make_uint4(0u, 0u, 0u, 0u);
-      // (the last round may be short; a row past the tile is never valid)
-      if (row >= 0 && chunk_row(i) < nvalid)
-        vreg[i] = ld_stream(a.vc + (row + chunk_row(i)) * D + chunk_col(i) * 16);
-    }
+    share.template load<D>(vreg, a.vc + (row < 0 ? 0 : row) * D, row < 0 ? 0 : nvalid);
   };
 
   if (warp >= kWide) {
@@ -346,20 +328,7 @@ q8_rows_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
       }
       uint8_t* const stage = smem + L::off_v + st * L::v_bytes;
       if (t < n_pre) {
-#pragma unroll
-        for (int i = 0; i < NT; ++i) {
-          if (kChunks % kWideThreads != 0 && wt + kWideThreads * i >= kChunks) break;
-          const int row = chunk_row(i), c = chunk_col(i);
-          uint32_t h[8];
-          q8_half4(vreg[i].x, h[0], h[1]);
-          q8_half4(vreg[i].y, h[2], h[3]);
-          q8_half4(vreg[i].z, h[4], h[5]);
-          q8_half4(vreg[i].w, h[6], h[7]);
-          uint8_t* dst = stage + (c >> 2) * kHalf + row * 128;
-          const int u = 2 * (c & 3);
-          *(uint4*)(dst + (((u + 0) ^ (row & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
-          *(uint4*)(dst + (((u + 1) ^ (row & 7)) << 4)) = make_uint4(h[4], h[5], h[6], h[7]);
-        }
+        share.widen(vreg, stage);
       } else {
         tree_values<D>(a, b, hk, wt, kWideThreads, vt_in, stage);
       }

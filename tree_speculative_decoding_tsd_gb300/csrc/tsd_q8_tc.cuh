@@ -104,6 +104,33 @@ __device__ __forceinline__ uint32_t top_pairs(uint32_t top, const uint4& w) {
 __device__ __forceinline__ uint32_t top_of(uint32_t pairs) {
   return max(pairs << 16, pairs & 0xffff0000u);
 }
+// A widening thread's share of a V tile (128 keys x 16 W codes, W = 4 or 8): chunks
+// of 16 codes, `T` threads.  Eight lanes that store together take four chunks of an
+// even and of an odd row (W = 8: chunks 0-3 or 4-7; W = 4: two rows): eight different
+// 16-byte columns of a swizzled row pair, so the stores do not conflict.  A thread's
+// chunks are T / W rows apart, which keeps its addresses at fixed distances.
+template <int W, int T>
+struct WideShare {
+  static constexpr int kCount = (kKeys * W + T - 1) / T;
+  static constexpr int kStep = T / W;              // rows between a thread's chunks
+  static_assert(T % (4 * W) == 0, "whole swizzle halves");
+  int row, col;                                    // first chunk
+  uint32_t dst0, dst1;                             // its two 16-byte units in a stage
+  __device__ __forceinline__ explicit WideShare(int wt) {
+    row = W == 8 ? 2 * (wt >> 4) + ((wt >> 2) & 1) : wt >> 2;
+    col = W == 8 ? (wt & 3) + 4 * ((wt >> 3) & 1) : wt & 3;
+    const uint32_t base = (uint32_t)((col >> 2) * kHalf + row * 128);
+    const int u = 2 * (col & 3);
+    dst0 = base + (uint32_t)((u ^ (row & 7)) << 4);
+    dst1 = base + (uint32_t)(((u + 1) ^ (row & 7)) << 4);
+  }
+  // chunks of the rows below nvalid from `src`, the tile's first code of this share
+  // (rows of `pitch` codes), zeros behind them
+  template <int kPitch>
+  __device__ __forceinline__ void load(uint4 (&r)[kCount], const uint8_t* src, int nvalid) const;
+  __device__ __forceinline__ void widen(const uint4 (&r)[kCount], uint8_t* stage) const;
+};
+
 // Eight bf16 times f as fp16.
 __device__ __forceinline__ uint4 scale8(const uint4& w, float f) {
   uint4 r;
@@ -116,6 +143,41 @@ __device__ __forceinline__ uint4 scale8(const uint4& w, float f) {
 // fp32 exponent field of a row's largest magnitude, at least 15 so that both
 // the scale and its inverse are normal numbers.
 __device__ __forceinline__ int row_exponent(uint32_t top) { return max((int)(top >> 23), 15); }
+
+template <int W, int T>
+template <int kPitch>
+__device__ __forceinline__ void WideShare<W, T>::load(uint4 (&r)[kCount], const uint8_t* src,
+                                                      int nvalid) const {
+  const uint8_t* const p = src + (long)row * kPitch + col * 16;
+  if (nvalid >= kKeys) {
+#pragma unroll
+    for (int i = 0; i < kCount; ++i)
+      if ((i + 1) * kStep <= kKeys || row + i * kStep < kKeys) r[i] = ld_stream(p + i * kStep * kPitch);
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < kCount; ++i) {
+    r[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (row + i * kStep < nvalid) r[i] = ld_stream(p + i * kStep * kPitch);
+  }
+}
+template <int W, int T>
+__device__ __forceinline__ void WideShare<W, T>::widen(const uint4 (&r)[kCount], uint8_t* stage) const {
+#pragma unroll
+  for (int i = 0; i < kCount; ++i) {
+    if ((i + 1) * kStep > kKeys && row + i * kStep >= kKeys) break;    // (a short last round)
+    uint32_t h[8];
+    q8_half4(r[i].x, h[0], h[1]);
+    q8_half4(r[i].y, h[2], h[3]);
+    q8_half4(r[i].z, h[4], h[5]);
+    q8_half4(r[i].w, h[6], h[7]);
+    // (kStep is a multiple of 4: the swizzle of row + i kStep differs in bit 2 at most)
+    const uint32_t flip = (uint32_t)((i * kStep) & 4) << 4;
+    uint8_t* const d = stage + i * kStep * 128;
+    *(uint4*)(d + (dst0 ^ flip)) = make_uint4(h[0], h[1], h[2], h[3]);
+    *(uint4*)(d + (dst1 ^ flip)) = make_uint4(h[4], h[5], h[6], h[7]);
+  }
+}
 
 // Scratch rows of (request b, head hk): eight lanes of the n threads (at least
 // 192) per row.  Which ones some row sees, their factors, and (returned) this
