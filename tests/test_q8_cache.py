@@ -731,6 +731,7 @@ WEIGHTS = [("gqa", 3, 20, [700, 1, 128], 8, {}), ("gqa", 2, 65, [300, 0], 16, di
            ("narrow", 3, 9, [130, 63, 900], 5, {}), ("wide", 2, 33, [257], 16, dict(page=256)),
            ("one", 4, 2, [5, 127, 128, 129], 1, {}), ("latent", 2, 4, [150, 300], 3, {}),
            ("latent", 1, 20, [515], 16, dict(page=128)),
+           ("latent-few", 2, 12, [200, 64], 6, {}), ("latent", 2, 5, [129], 2, dict(dtype=torch.float32)),
            ("gqa", 2, 7, [200], 3, dict(dtype=torch.float32)), ("gqa", 33, 5, [300, 20], 4, {})]
 
 

@@ -10,8 +10,8 @@
 //
 // The sum over the columns (accepted rows x heads of the group) belongs to one
 // cached row, so with the scores transposed (keys on lanes) no reduction
-// crosses a thread.  Paths: tsd_weights_tc.cu (tcgen05, bf16 heads), and
-// weights_simt_kernel here: fp32 inputs and what the tensor cores do not take.
+// crosses a thread.  Paths: tsd_weights_tc.cu and tsd_weights_latent.cu (tcgen05,
+// bf16), and weights_simt_kernel here: fp32 inputs and what the tensor cores do not take.
 // It is a blocked fp32 product: 128 keys x 32 columns per CTA and step, 64 dims
 // at a time in shared memory (rows padded to 68 floats: 16-byte loads of eight
 // consecutive keys then start in eight different banks); a thread owns one key
@@ -179,7 +179,7 @@ tsd_status weights_impl(const tsd_attn_desc* d, int S, const void* q, const void
   a.qscale = d->scale * kLog2e;
   const cudaStream_t st = (cudaStream_t)stream;
   const bool f32 = d->dtype == TSD_F32;
-  if (launch_weights_tc(*d, a, st)) return cuda_status();
+  if (launch_weights_tc(*d, a, st) || launch_weights_latent(*d, a, st)) return cuda_status();
   if (d->dk == 576) {
     if (f32) launch_simt<float, 576>(*d, a, st);
     else launch_simt<__nv_bfloat16, 576>(*d, a, st);

@@ -65,5 +65,6 @@ __device__ __forceinline__ int weight_path(const WeightArgs& a, int b, int P, Pa
 }
 
 bool launch_weights_tc(const tsd_attn_desc& d, const WeightArgs& a, cudaStream_t st);
+bool launch_weights_latent(const tsd_attn_desc& d, const WeightArgs& a, cudaStream_t st);
 
 }  // namespace tsd
