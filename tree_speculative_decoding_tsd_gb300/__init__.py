@@ -539,61 +539,74 @@ def q8_blocks(cap) -> int:
     return -(-int(cap) // TSD_Q8_BLOCK)
 
 
-def _cache_shapes(d, kcache, page_table, page_size, dev):
-    """(leading dims, rows) of a contiguous or paged cache, and its page arguments."""
+class _Dims:
+    """A descriptor's fields, read once, with the current device."""
+
+    __slots__ = ("B", "R", "Hq", "Hkv", "dk", "dv", "cap", "alias", "dt", "dev", "ref")
+
+    def __init__(self, desc):
+        self.B, self.R, self.Hq, self.Hkv = desc.B, desc.R, desc.Hq, desc.Hkv
+        self.dk, self.dv, self.cap = desc.dk, desc.dv, desc.cap
+        self.alias = bool(desc.v_aliases_k)
+        self.dt = (_attn_dtype(desc),)
+        self.dev = torch.cuda.current_device()
+        self.ref = ctypes.byref(desc)
+
+
+def _cache_shapes(d, kcache, page_table, page_size):
+    """Leading dims and rows of a contiguous or paged cache, and its page arguments."""
     if page_table is None:
         if page_size:
             raise ValueError("page_size without a page_table")
-        return (d.B, d.Hkv), d.cap, (None, 0, 0, 0)
+        return (d.B, d.Hkv, d.cap), (None, 0, 0, 0)
     npg, mp = kcache.shape[0], page_table.shape[1]
-    return (npg, d.Hkv), page_size, (_p(page_table, "page_table", _I32T, (d.B, mp), dev), mp,
+    return (npg, d.Hkv, page_size), (_p(page_table, "page_table", _I32T, (d.B, mp), d.dev), mp,
                                      page_size, npg)
 
 
-def _q8_cache(d, kq, vq, kexp, vexp, page_table, page_size, dev):
-    lead, rows, paging = _cache_shapes(d, kq, page_table, page_size, dev)
-    nb = q8_blocks(rows)
-    if d.v_aliases_k:
-        vq = vexp = None
-    elif vq is None or vexp is None:
+def _q8_cache(d, kq, vq, kexp, vexp, page_table, page_size):
+    lead, paging = _cache_shapes(d, kq, page_table, page_size)
+    dev, exps = d.dev, (lead[0], lead[1], q8_blocks(lead[2]))
+    pk = _p(kq, "kq", _CODES, (*lead, d.dk), dev)
+    pke = _p(kexp, "kexp", _EXPS, exps, dev)
+    if d.alias:
+        return (pk, None, pke, None), paging
+    if vq is None or vexp is None:
         raise ValueError("vq, vexp: needed unless V aliases K")
-    return (_p(kq, "kq", _CODES, (*lead, rows, d.dk), dev),
-            _p(vq, "vq", _CODES, (*lead, rows, d.dv), dev),
-            _p(kexp, "kexp", _EXPS, (*lead, nb), dev), _p(vexp, "vexp", _EXPS, (*lead, nb), dev),
-            paging)
+    return (pk, _p(vq, "vq", _CODES, (*lead, d.dv), dev), pke,
+            _p(vexp, "vexp", _EXPS, exps, dev)), paging
 
 
-def _rows(d, k, v, names, n, dev):
+def _rows(d, k, v, names, n):
     """Addresses of new rows [B][n][Hkv][dk | dv]."""
-    dt = (_attn_dtype(d),)
-    return (_p(k, names[0], dt, (d.B, n, d.Hkv, d.dk), dev),
-            None if d.v_aliases_k else _p(v, names[1], dt, (d.B, n, d.Hkv, d.dv), dev))
+    return (_p(k, names[0], d.dt, (d.B, n, d.Hkv, d.dk), d.dev),
+            None if d.alias else _p(v, names[1], d.dt, (d.B, n, d.Hkv, d.dv), d.dev))
 
 
 def tsd_cache_write_q8(desc, knew, vnew, new_len, kq, vq, kexp, vexp, prefix_len, err=None,
                        stream=None, page_table=None, page_size=0):
     """Append rows knew/vnew [B][T][Hkv][d], new_len[b] of them, to the 8-bit cache."""
-    d, dev = desc, torch.cuda.current_device()
-    T = knew.shape[1]
-    rows = _rows(d, knew, vnew, ("knew", "vnew"), T, dev)
-    pk, pv, pke, pve, paging = _q8_cache(d, kq, vq, kexp, vexp, page_table, page_size, dev)
+    d = _Dims(desc)
+    T, one = knew.shape[1], (d.B,)
+    cache, paging = _q8_cache(d, kq, vq, kexp, vexp, page_table, page_size)
     _check("tsd_cache_write_q8", _L().tsd_cache_write_q8(
-        ctypes.byref(d), T, *rows, _p(new_len, "new_len", _I32T, (d.B,), dev), pk, pv, pke, pve,
-        *paging, _p(prefix_len, "prefix_len", _I32T, (d.B,), dev), _scratch(None, err, dev)[1],
-        _raw_stream(stream, dev)))
+        d.ref, T, *_rows(d, knew, vnew, ("knew", "vnew"), T), _p(new_len, "new_len", _I32T, one, d.dev),
+        *cache, *paging, _p(prefix_len, "prefix_len", _I32T, one, d.dev),
+        _scratch(None, err, d.dev)[1], _raw_stream(stream, d.dev)))
 
 
 def tsd_commit_path_q8(desc, S, ktree, vtree, accept_rows, accept_len, kq, vq, kexp, vexp,
                        prefix_len, err=None, stream=None, page_table=None, page_size=0):
     """tsd_commit_path into the 8-bit cache."""
-    d, dev = desc, torch.cuda.current_device()
-    rows = _rows(d, ktree, vtree, ("ktree", "vtree"), d.R, dev)
-    pk, pv, pke, pve, paging = _q8_cache(d, kq, vq, kexp, vexp, page_table, page_size, dev)
+    d = _Dims(desc)
+    one = (d.B,)
+    cache, paging = _q8_cache(d, kq, vq, kexp, vexp, page_table, page_size)
     _check("tsd_commit_path_q8", _L().tsd_commit_path_q8(
-        ctypes.byref(d), S, *rows, _p(accept_rows, "accept_rows", _I32T, (d.B, S + 1), dev),
-        _p(accept_len, "accept_len", _I32T, (d.B,), dev), pk, pv, pke, pve, *paging,
-        _p(prefix_len, "prefix_len", _I32T, (d.B,), dev), _scratch(None, err, dev)[1],
-        _raw_stream(stream, dev)))
+        d.ref, S, *_rows(d, ktree, vtree, ("ktree", "vtree"), d.R),
+        _p(accept_rows, "accept_rows", _I32T, (d.B, S + 1), d.dev),
+        _p(accept_len, "accept_len", _I32T, one, d.dev), *cache, *paging,
+        _p(prefix_len, "prefix_len", _I32T, one, d.dev), _scratch(None, err, d.dev)[1],
+        _raw_stream(stream, d.dev)))
 
 
 def tsd_verify_q8_workspace_size(desc: tsd_attn_desc) -> int:
@@ -603,59 +616,57 @@ def tsd_verify_q8_workspace_size(desc: tsd_attn_desc) -> int:
 def tsd_tree_verify_attn_q8(desc, q, kq, vq, kexp, vexp, prefix_len, ktree, vtree, mask, out, lse,
                             ws, err=None, stream=None, page_table=None, page_size=0):
     """tsd_tree_verify_attn over the 8-bit cache (contiguous, or pages with ``page_table``)."""
-    d, dev = desc, torch.cuda.current_device()
-    B, R, Hq = d.B, d.R, d.Hq
-    dt = (_attn_dtype(d),)
-    pk, pv, pke, pve, paging = _q8_cache(d, kq, vq, kexp, vexp, page_table, page_size, dev)
-    rows = _rows(d, ktree, vtree, ("ktree", "vtree"), R, dev)
+    d = _Dims(desc)
+    B, R, Hq, dev = d.B, d.R, d.Hq, d.dev
+    cache, paging = _q8_cache(d, kq, vq, kexp, vexp, page_table, page_size)
     (pws, nws), perr = _scratch(ws, err, dev)
     _check("tsd_tree_verify_attn_q8", _L().tsd_tree_verify_attn_q8(
-        ctypes.byref(d), _p(q, "q", dt, (B, R, Hq, d.dk), dev), pk, pv, pke, pve, *paging,
-        _p(prefix_len, "prefix_len", _I32T, (B,), dev), *rows, _p(mask, "mask", _MASK, (B, R), dev),
-        _p(out, "out", dt, (B, R, Hq, d.dv), dev), _p(lse, "lse", _F32T, (B, R, Hq), dev), pws, nws,
-        perr, _raw_stream(stream, dev)))
+        d.ref, _p(q, "q", d.dt, (B, R, Hq, d.dk), dev), *cache, *paging,
+        _p(prefix_len, "prefix_len", _I32T, (B,), dev), *_rows(d, ktree, vtree, ("ktree", "vtree"), R),
+        _p(mask, "mask", _MASK, (B, R), dev), _p(out, "out", d.dt, (B, R, Hq, d.dv), dev),
+        _p(lse, "lse", _F32T, (B, R, Hq), dev), pws, nws, perr, _raw_stream(stream, dev)))
 
 
-def _weight_args(d, S, prefix_len, ktree, accept_rows, accept_len, lse, decay, acc, pos, seen, dev):
+def _weight_args(d, S, prefix_len, ktree, accept_rows, accept_len, lse, decay, acc, pos, seen):
+    dev = d.dev
     return (_p(prefix_len, "prefix_len", _I32T, (d.B,), dev),
-            _p(ktree, "ktree", (_attn_dtype(d),), (d.B, d.R, d.Hkv, d.dk), dev),
+            _p(ktree, "ktree", d.dt, (d.B, d.R, d.Hkv, d.dk), dev),
             _p(accept_rows, "accept_rows", _I32T, (d.B, S + 1), dev),
             _p(accept_len, "accept_len", _I32T, (d.B,), dev),
             _p(lse, "lse", _F32T, (d.B, d.R, d.Hq), dev), float(decay),
-            *_evict_state(d, acc, pos, seen, dev))
+            *_evict_state(d, acc, pos, seen))
 
 
-def _evict_state(d, acc, pos, seen, dev):
-    return (_p(acc, "acc", _F32T, (d.B, d.Hkv, d.cap), dev),
-            _p(pos, "pos", _I32T, (d.B, d.Hkv, d.cap), dev),
-            _p(seen, "seen", _I32T, (d.B, d.Hkv), dev))
+def _evict_state(d, acc, pos, seen):
+    rows = (d.B, d.Hkv, d.cap)
+    return (_p(acc, "acc", _F32T, rows, d.dev), _p(pos, "pos", _I32T, rows, d.dev),
+            _p(seen, "seen", _I32T, (d.B, d.Hkv), d.dev))
 
 
 def tsd_cache_weights(desc, S, q, kcache, prefix_len, ktree, accept_rows, accept_len, lse, decay,
                       acc, pos, seen, err=None, stream=None, page_table=None, page_size=0):
     """Add the attention weight that the accepted rows gave each cached row to ``acc``."""
-    d, dev = desc, torch.cuda.current_device()
-    dt = (_attn_dtype(d),)
-    lead, rows, paging = _cache_shapes(d, kcache, page_table, page_size, dev)
+    d = _Dims(desc)
+    lead, paging = _cache_shapes(d, kcache, page_table, page_size)
     _check("tsd_cache_weights", _L().tsd_cache_weights(
-        ctypes.byref(d), S, _p(q, "q", dt, (d.B, d.R, d.Hq, d.dk), dev),
-        _p(kcache, "kcache", dt, (*lead, rows, d.dk), dev), *paging,
-        *_weight_args(d, S, prefix_len, ktree, accept_rows, accept_len, lse, decay, acc, pos, seen,
-                      dev), _scratch(None, err, dev)[1], _raw_stream(stream, dev)))
+        d.ref, S, _p(q, "q", d.dt, (d.B, d.R, d.Hq, d.dk), d.dev),
+        _p(kcache, "kcache", d.dt, (*lead, d.dk), d.dev), *paging,
+        *_weight_args(d, S, prefix_len, ktree, accept_rows, accept_len, lse, decay, acc, pos, seen),
+        _scratch(None, err, d.dev)[1], _raw_stream(stream, d.dev)))
 
 
 def tsd_cache_weights_q8(desc, S, q, kq, kexp, prefix_len, ktree, accept_rows, accept_len, lse,
                          decay, acc, pos, seen, err=None, stream=None, page_table=None,
                          page_size=0):
     """tsd_cache_weights for the 8-bit cache."""
-    d, dev = desc, torch.cuda.current_device()
-    lead, rows, paging = _cache_shapes(d, kq, page_table, page_size, dev)
+    d = _Dims(desc)
+    lead, paging = _cache_shapes(d, kq, page_table, page_size)
     _check("tsd_cache_weights_q8", _L().tsd_cache_weights_q8(
-        ctypes.byref(d), S, _p(q, "q", (_attn_dtype(d),), (d.B, d.R, d.Hq, d.dk), dev),
-        _p(kq, "kq", _CODES, (*lead, rows, d.dk), dev),
-        _p(kexp, "kexp", _EXPS, (*lead, q8_blocks(rows)), dev), *paging,
-        *_weight_args(d, S, prefix_len, ktree, accept_rows, accept_len, lse, decay, acc, pos, seen,
-                      dev), _scratch(None, err, dev)[1], _raw_stream(stream, dev)))
+        d.ref, S, _p(q, "q", d.dt, (d.B, d.R, d.Hq, d.dk), d.dev),
+        _p(kq, "kq", _CODES, (*lead, d.dk), d.dev),
+        _p(kexp, "kexp", _EXPS, (lead[0], lead[1], q8_blocks(lead[2])), d.dev), *paging,
+        *_weight_args(d, S, prefix_len, ktree, accept_rows, accept_len, lse, decay, acc, pos, seen),
+        _scratch(None, err, d.dev)[1], _raw_stream(stream, d.dev)))
 
 
 def tsd_cache_evict_workspace_size(desc: tsd_attn_desc) -> int:
@@ -665,24 +676,24 @@ def tsd_cache_evict_workspace_size(desc: tsd_attn_desc) -> int:
 def tsd_cache_evict(desc, keep, sink, recent, acc, pos, seen, kcache, vcache, prefix_len, ws,
                     err=None, stream=None, page_table=None, page_size=0):
     """Cut every request of more than ``keep`` cached rows to the ``keep`` heaviest ones."""
-    d, dev = desc, torch.cuda.current_device()
-    dt = (_attn_dtype(d),)
-    lead, rows, paging = _cache_shapes(d, kcache, page_table, page_size, dev)
-    (pws, nws), perr = _scratch(ws, err, dev)
+    d = _Dims(desc)
+    lead, paging = _cache_shapes(d, kcache, page_table, page_size)
+    (pws, nws), perr = _scratch(ws, err, d.dev)
     _check("tsd_cache_evict", _L().tsd_cache_evict(
-        ctypes.byref(d), keep, sink, recent, *_evict_state(d, acc, pos, seen, dev),
-        _p(kcache, "kcache", dt, (*lead, rows, d.dk), dev),
-        None if d.v_aliases_k else _p(vcache, "vcache", dt, (*lead, rows, d.dv), dev), *paging,
-        _p(prefix_len, "prefix_len", _I32T, (d.B,), dev), pws, nws, perr, _raw_stream(stream, dev)))
+        d.ref, keep, sink, recent, *_evict_state(d, acc, pos, seen),
+        _p(kcache, "kcache", d.dt, (*lead, d.dk), d.dev),
+        None if d.alias else _p(vcache, "vcache", d.dt, (*lead, d.dv), d.dev), *paging,
+        _p(prefix_len, "prefix_len", _I32T, (d.B,), d.dev), pws, nws, perr,
+        _raw_stream(stream, d.dev)))
 
 
 def tsd_cache_evict_q8(desc, keep, sink, recent, acc, pos, seen, kq, vq, kexp, vexp, prefix_len,
                        ws, err=None, stream=None, page_table=None, page_size=0):
     """tsd_cache_evict for the 8-bit cache."""
-    d, dev = desc, torch.cuda.current_device()
-    pk, pv, pke, pve, paging = _q8_cache(d, kq, vq, kexp, vexp, page_table, page_size, dev)
-    (pws, nws), perr = _scratch(ws, err, dev)
+    d = _Dims(desc)
+    cache, paging = _q8_cache(d, kq, vq, kexp, vexp, page_table, page_size)
+    (pws, nws), perr = _scratch(ws, err, d.dev)
     _check("tsd_cache_evict_q8", _L().tsd_cache_evict_q8(
-        ctypes.byref(d), keep, sink, recent, *_evict_state(d, acc, pos, seen, dev), pk, pv, pke,
-        pve, *paging, _p(prefix_len, "prefix_len", _I32T, (d.B,), dev), pws, nws, perr,
-        _raw_stream(stream, dev)))
+        d.ref, keep, sink, recent, *_evict_state(d, acc, pos, seen), *cache, *paging,
+        _p(prefix_len, "prefix_len", _I32T, (d.B,), d.dev), pws, nws, perr,
+        _raw_stream(stream, d.dev)))

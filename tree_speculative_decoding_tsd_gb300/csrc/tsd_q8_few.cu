@@ -584,7 +584,8 @@ template <int N, int D>
 void launch_n(const CUtensorMap& kmap, const Q8AttnArgs& a, const Q8Plan& p, cudaStream_t st) {
   const uint32_t smem = FewLayout<N, D>::total + 1024;
   const auto kern = q8_few_kernel<N, D>;
-  cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  static std::atomic<uint64_t> done{0};
+  allow_smem(kern, smem, done);
   launch(kern, dim3(a.map.Hkv, p.nsplit, a.B), dim3(kThreads), smem, st, kmap, a);
 }
 

@@ -12,11 +12,12 @@
 // Products with powers of two are exact in fp32, so each code is rounded once
 // (an earlier code only where it becomes subnormal).
 //
-// write_block: one CTA takes a (block, head, K or V): the new rows stay in
-// registers between the maximum and the conversion, so the source is read
-// once and the codes are written once; earlier rows are read only when the
-// exponent grows.  Bounded by memory: 2 (or 4) bytes read and 1 written per
-// element.
+// Prefill: a CTA takes a (block, head, K or V); the new rows stay in registers
+// between the maximum and the conversion, so the source is read once and the codes
+// are written once; earlier rows are read only when the exponent grows.  Bounded by
+// memory: 2 (or 4) bytes read and 1 written per element (4 x 8192 rows at most of 8
+// heads: 37 us with the length's update, 22 us by the bytes).  Commit: a warp takes a
+// (block, head, K or V); bounded by latency.
 #include <cuda_bf16.h>
 
 #include <type_traits>
@@ -113,7 +114,7 @@ struct RawBf16 {
 };
 
 // Block `blk` (positions 64 blk ..) of head h of request b, part 0 (K) or 1 (V).
-template <typename T, int D, bool kCommit>
+template <typename T, int D>
 __device__ __forceinline__ void write_block(const Q8WriteArgs& a, int b, int h, int part, int blk,
                                             int P, int n, WriteSmem& s) {
   using Raw = typename std::conditional<sizeof(T) == 4, RawF32, RawBf16>::type;
@@ -128,8 +129,7 @@ __device__ __forceinline__ void write_block(const Q8WriteArgs& a, int b, int h, 
     const int r = (tid + i * kThreads) / VR, c = (tid + i * kThreads) % VR;
     raw[i].clear();
     if (r >= r0 && r < r1) {
-      int t = first + r - P;
-      if (kCommit) t = s.path[t];
+      const int t = first + r - P;
       raw[i].load((const T*)a.src[part] + (((long)b * a.rows + t) * a.map.Hkv + h) * D + c * 8);
     }
   }
@@ -196,7 +196,7 @@ write_q8_kernel(const __grid_constant__ Q8WriteArgs a) {
   if (n <= 0) return;
   const int blk = P / kQ8Block + blockIdx.x;
   if (blk * (long)kQ8Block >= (long)P + n) return;
-  write_block<T, D, false>(a, b, blockIdx.y / a.parts, blockIdx.y % a.parts, blk, P, n, s);
+  write_block<T, D>(a, b, blockIdx.y / a.parts, blockIdx.y % a.parts, blk, P, n, s);
 }
 
 __global__ void __launch_bounds__(128) write_advance_kernel(const __grid_constant__ Q8WriteArgs a) {
@@ -209,40 +209,121 @@ __global__ void __launch_bounds__(128) write_advance_kernel(const __grid_constan
   else a.prefix_len[b] = P + n;
 }
 
-// Commit: at most 17 rows, so at most two blocks per head and part.  One
-// cluster of kCommitCtas CTAs per request shares the (block, head, part) tasks;
-// the cluster barrier lets rank 0 advance the prefix length after every CTA
-// has read it, which saves a second launch (about 2 us of a 4 us call).
-constexpr int kCommitCtas = 8;
+// Commit: at most 17 rows, so at most two blocks per head and part.  One CTA per
+// request, a warp per (block, head, part): the prefix length is read and advanced by
+// the same CTA, and no launch or cluster is needed to order the two.  (A cluster of
+// eight CTAs took as long on the device, 13.4 us with the advance inside a graph, and
+// 1 us more to launch.)  Rows of up to 128 bf16 dims stay in registers between the maximum and the
+// conversion; wider ones are read again, from L1.
+constexpr int kCommitThreads = 1024;
 
 template <typename T, int D>
-__global__ void __cluster_dims__(kCommitCtas, 1, 1) __launch_bounds__(kWriteThreads<D>)
+__device__ __forceinline__ void commit_block(const Q8WriteArgs& a, const WriteSmem& s, int b, int h,
+                                             int part, int blk, int P, int n) {
+  using Raw = typename std::conditional<sizeof(T) == 4, RawF32, RawBf16>::type;
+  constexpr int VR = D / 8;                          // 8-element vectors of a row
+  constexpr int kVecs = (17 * VR + 31) / 32;         // of the new rows, per lane
+  constexpr bool kKeep = sizeof(T) == 2 && D <= 128;
+  const int lane = threadIdx.x & 31;
+  const int first = blk * kQ8Block;
+  const int r0 = max(P - first, 0), r1 = min(P + n - first, kQ8Block);
+  const int work = (r1 - r0) * VR;
+  uint8_t* const ep = a.exps[part] + a.map.block(b, h, first);
+  uint8_t* const row0 = a.codes[part] + a.map.row(b, h, first) * D;
+  const int e_old = r0 > 0 ? *ep : 0;
+  auto source = [&](int v) {
+    const int t = first + r0 + v / VR - P;
+    return (const T*)a.src[part] + (((long)b * a.rows + s.path[t]) * a.map.Hkv + h) * D + v % VR * 8;
+  };
+  auto magnitude = [](const Raw& w, uint32_t m) {
+    float x[8];
+    w.values(x);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const uint32_t u = __float_as_uint(x[j]) & 0x7fffffffu;
+      m = max(m, u < 0x7f800000u ? u : 0u);          // infinities and NaN do not count
+    }
+    return m;
+  };
+  Raw raw[kKeep ? kVecs : 1];
+  uint32_t m = 0;
+  if constexpr (kKeep) {
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i) {
+      raw[i].clear();
+      if (lane + 32 * i < work) raw[i].load(source(lane + 32 * i));
+    }
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i) m = magnitude(raw[i], m);
+  } else {
+#pragma unroll 4
+    for (int v = lane; v < work; v += 32) {
+      raw[0].load(source(v));
+      m = magnitude(raw[0], m);
+    }
+  }
+  m = __reduce_max_sync(kFull, m);
+  const int e = max(q8_need(__uint_as_float(m)), e_old);
+  const float inv = q8_scale(254 - min(e, kQ8ExpMax));  // 2^(127 - e)
+  auto put = [&](const Raw& w, int v) {
+    float x[8];
+    w.values(x);
+    uint2 o;
+    o.x = q8_pack4(x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv);
+    o.y = q8_pack4(x[4] * inv, x[5] * inv, x[6] * inv, x[7] * inv);
+    *(uint2*)(row0 + ((long)r0 * VR + v) * 8) = o;
+  };
+  if constexpr (kKeep) {
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i)
+      if (lane + 32 * i < work) put(raw[i], lane + 32 * i);
+  } else {
+#pragma unroll 4
+    for (int v = lane; v < work; v += 32) {
+      raw[0].load(source(v));
+      put(raw[0], v);
+    }
+  }
+  if (r0 > 0 && e != e_old) {
+    const float f = pow2i(e_old - e);
+#pragma unroll 4
+    for (int v = lane; v < r0 * (D / 16); v += 32) {
+      uint4 w = *(uint4*)(row0 + (long)v * 16);
+      w.x = q8_rescale4(w.x, f);
+      w.y = q8_rescale4(w.y, f);
+      w.z = q8_rescale4(w.z, f);
+      w.w = q8_rescale4(w.w, f);
+      *(uint4*)(row0 + (long)v * 16) = w;
+    }
+  }
+  __syncwarp();                                      // (every lane has read the exponent)
+  if (lane == 0 && (r0 == 0 || e != e_old)) *ep = (uint8_t)e;
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kCommitThreads)
 commit_q8_kernel(const __grid_constant__ Q8WriteArgs a) {
   __shared__ WriteSmem s;
   grid_dependency_sync();
-  const int b = blockIdx.y, P = a.prefix_len[b], c = a.count[b];
+  const int b = blockIdx.x, P = a.prefix_len[b], c = a.count[b];
   const int r = threadIdx.x <= a.S ? a.path[(long)b * (a.S + 1) + threadIdx.x] : 0;
   const int n = write_rows<true>(a, b, P, c, r, s);  // (its barrier: the whole CTA has read P)
-  asm volatile("barrier.cluster.arrive.aligned;\n" ::: "memory");
-  if (n > 0) {
-    const int blk0 = P / kQ8Block, nb = (P + n - 1) / kQ8Block - blk0 + 1;
-    const int tasks = nb * a.map.Hkv * a.parts;
-    for (int t = blockIdx.x; t < tasks; t += kCommitCtas) {
-      const int hp = t / nb;
-      write_block<T, D, true>(a, b, hp / a.parts, hp % a.parts, blk0 + t % nb, P, n, s);
-    }
-  }
-  asm volatile("barrier.cluster.wait.aligned;\n" ::: "memory");
-  if (blockIdx.x == 0 && threadIdx.x == 0) {
+  if (threadIdx.x == 0) {
     if (n < 0) report_error(a.err, -n, b);
     else a.prefix_len[b] = P + n;
+  }
+  if (n <= 0) return;
+  const int blk0 = P / kQ8Block, nb = (P + n - 1) / kQ8Block - blk0 + 1;
+  for (int t = threadIdx.x >> 5; t < nb * a.map.Hkv * a.parts; t += kCommitThreads / 32) {
+    const int hp = t / nb;
+    commit_block<T, D>(a, s, b, hp / a.parts, hp % a.parts, blk0 + t % nb, P, n);
   }
 }
 
 template <typename T, int D>
 void launch_write(const Q8WriteArgs& a, int B, int nblk, bool commit, cudaStream_t st) {
   if (commit) {
-    launch(commit_q8_kernel<T, D>, dim3(kCommitCtas, B), dim3(kWriteThreads<D>), 0, st, a);
+    launch(commit_q8_kernel<T, D>, dim3(B), dim3(kCommitThreads), 0, st, a);
     return;
   }
   launch(write_q8_kernel<T, D>, dim3(nblk, a.map.Hkv * a.parts, B), dim3(kWriteThreads<D>), 0, st, a);
