@@ -149,7 +149,7 @@ q8_few_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
       vex[2 * wt + 1] = (uint8_t)vb;
       top = max(va, vb) - 127;
     }
-    if (with_tree) top = max(top, scan_tree<D>(a, b, hk, wt, kWideThreads, kt_in, vt_in, kt_out, vt_u));
+    if (with_tree) top = max(top, scan_tree<D, kWideThreads>(a, b, hk, wt, kt_in, vt_in, kt_out, vt_u));
     top = __reduce_max_sync(kFull, top);
     if (lane == 0) s_top[warp - kWide] = top;
     if (D == 64) {       // the upper 64 dims of the value tiles stay zero

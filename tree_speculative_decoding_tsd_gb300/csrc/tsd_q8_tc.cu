@@ -63,7 +63,7 @@
 namespace tsd {
 namespace {
 
-constexpr int kPv = 8, kQk = 9, kTma = 10, kWide = 11, kWideWarps = 8;
+constexpr int kPv = 8, kQk = 9, kTma = 10, kWide = 11, kWideWarps = 5;
 constexpr int kWideThreads = kWideWarps * 32;
 constexpr int kThreads = (kWide + kWideWarps) * 32;
 constexpr int kStages = 3;                      // widened V tiles
@@ -86,7 +86,7 @@ struct RowLayout {
   static constexpr uint32_t off_kex = off_tree + 16 * kKeys;           // u8[2 kMaxTiles]
   static constexpr uint32_t off_vex = off_kex + 2 * kMaxTiles;
   static constexpr uint32_t off_bar = off_vex + 2 * kMaxTiles;
-  static constexpr int nbar = 25;
+  static constexpr int nbar = 27;
   static constexpr uint32_t off_flags = off_bar + 8 * nbar;            // tmem, abort
   static constexpr uint32_t off_top = off_flags + 8;                   // int[kWideWarps]
   static constexpr uint32_t total = off_top + 4 * kWideWarps;
@@ -94,13 +94,13 @@ struct RowLayout {
 };
 
 // FULL: the copy landed, the warps wrote or the product is done; EMPTY: read by
-// the product (S_EMPTY: by the softmax).  P_FULL and PV_DONE: one per stream.
+// the product (S_EMPTY: by the softmax).  S, P_FULL and PV_DONE: one per stream.
 // T_FULL: the scratch rows' keys, which take the two K slots behind the last
 // prefix tile (hi, lo).  Q_FULL: Q is in the tensor memory.  FINAL: one per
 // issuing warp.
 enum { BAR_K_FULL = 0, BAR_K_EMPTY = 4, BAR_V_FULL = 8, BAR_V_EMPTY = 11, BAR_S_FULL = 14,
-       BAR_S_EMPTY = 15, BAR_P_FULL = 16, BAR_PV_DONE = 18, BAR_O_DONE = 20, BAR_T_FULL = 21,
-       BAR_FINAL = 22, BAR_Q_FULL = 24 };
+       BAR_S_EMPTY = 16, BAR_P_FULL = 18, BAR_PV_DONE = 20, BAR_O_DONE = 22, BAR_T_FULL = 23,
+       BAR_FINAL = 24, BAR_Q_FULL = 26 };
 
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32]) {
   uint32_t r[32];
@@ -212,7 +212,7 @@ q8_rows_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
       vex[2 * t + 1] = (uint8_t)vb;
       top = max(top, max(va, vb) - 127);
     }
-    if (with_tree) top = max(top, scan_tree<D>(a, b, hk, wt, kWideThreads, kt_in, vt_in, kt_out, vt_u));
+    if (with_tree) top = max(top, scan_tree<D, kWideThreads>(a, b, hk, wt, kt_in, vt_in, kt_out, vt_u));
     top = __reduce_max_sync(kFull, top);
     if (lane == 0) s_top[warp - kWide] = top;
   } else if (warp < 8) {
@@ -249,9 +249,9 @@ q8_rows_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
         mbar_init(bar(BAR_P_FULL + i), live_warps);
         mbar_init(bar(BAR_PV_DONE + i), 1);
         mbar_init(bar(BAR_FINAL + i), 1);
+        mbar_init(bar(BAR_S_FULL + i), 1);
+        mbar_init(bar(BAR_S_EMPTY + i), live_warps);
       }
-      mbar_init(bar(BAR_S_FULL), 1);
-      mbar_init(bar(BAR_S_EMPTY), 2 * live_warps);
       mbar_init(bar(BAR_O_DONE), 1);
       mbar_init(bar(BAR_T_FULL), kWideWarps);
       mbar_init(bar(BAR_Q_FULL), 2 * live_warps);
@@ -344,38 +344,44 @@ q8_rows_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
   else if (warp == kQk) {
     // fp32 accumulator; e4m3 operands are format 0
     constexpr uint32_t idesc =
-        (1u << 4) | ((uint32_t)(kKeys >> 3) << 17) | ((uint32_t)(kRows >> 4) << 24);
+        (1u << 4) | ((uint32_t)(kKeys / 2 >> 3) << 17) | ((uint32_t)(kRows >> 4) << 24);
+    constexpr uint32_t kHalfTile = L::k_bytes / 2 >> 4;
     const uint64_t kd0 = row_desc<D>(sbase + L::off_k);
     const uint32_t tq = tmem + kColQ;
     const bool one = elect_one();
     bool ok = wait_ready(bar(BAR_Q_FULL), 0);
-    for (int t = 0; t < ntiles; ++t) {
+    for (int t = 0; ok && t < ntiles; ++t) {
       const int sl = t % kRing;
-      ok = ok && (t < n_pre ? wait_ready(bar(BAR_K_FULL + sl), (t / kRing) & 1)
-                            : wait_ready(bar(BAR_T_FULL), 0)) &&
-           (t == 0 || wait_ready(bar(BAR_S_EMPTY), (t - 1) & 1));
-      if (!__all_sync(kFull, ok)) break;
-      fence_after();
-      const uint64_t kd = kd0 + (uint64_t)(sl * (L::k_bytes >> 4));
-      if (one) {
-        // S = (Q hi + Q lo) x K slot; the scratch rows' second slot adds their lo
+      ok = t < n_pre ? wait_ready(bar(BAR_K_FULL + sl), (t / kRing) & 1)
+                     : wait_ready(bar(BAR_T_FULL), 0);
 #pragma unroll
-        for (int part = 0; part < 2; ++part)
-#pragma unroll
-          for (int kk = 0; kk < D / 32; ++kk)
-            mma_f8_ta(tmem, tq + part * (D / 4) + 8 * kk, kd + 2 * kk, idesc, part + kk == 0 ? 0u : 1u);
-        if (t >= n_pre) {
-          const uint64_t k2 = kd0 + (uint64_t)(((t + 1) % kRing) * (L::k_bytes >> 4));
+      for (int p = 0; p < 2; ++p) {
+        ok = ok && (t == 0 || wait_ready(bar(BAR_S_EMPTY + p), (t - 1) & 1));
+        ok = __all_sync(kFull, ok);
+        if (!ok) break;
+        fence_after();
+        const uint64_t kd = kd0 + (uint64_t)(sl * (L::k_bytes >> 4) + p * kHalfTile);
+        const uint32_t ts = tmem + 64u * p;
+        if (one) {
+          // S = (Q hi + Q lo) x K slot; the scratch rows' second slot adds their lo
 #pragma unroll
           for (int part = 0; part < 2; ++part)
 #pragma unroll
             for (int kk = 0; kk < D / 32; ++kk)
-              mma_f8_ta(tmem, tq + part * (D / 4) + 8 * kk, k2 + 2 * kk, idesc, 1u);
+              mma_f8_ta(ts, tq + part * (D / 4) + 8 * kk, kd + 2 * kk, idesc, part + kk == 0 ? 0u : 1u);
+          if (t >= n_pre) {
+            const uint64_t k2 = kd0 + (uint64_t)(((t + 1) % kRing) * (L::k_bytes >> 4) + p * kHalfTile);
+#pragma unroll
+            for (int part = 0; part < 2; ++part)
+#pragma unroll
+              for (int kk = 0; kk < D / 32; ++kk)
+                mma_f8_ta(ts, tq + part * (D / 4) + 8 * kk, k2 + 2 * kk, idesc, 1u);
+          }
+          mma_commit(bar(BAR_S_FULL + p));
+          if (p == 1) mma_commit(bar(BAR_K_EMPTY + sl));
         }
-        mma_commit(bar(BAR_S_FULL));
-        mma_commit(bar(BAR_K_EMPTY + sl));
+        __syncwarp();
       }
-      __syncwarp();
     }
     if (!ok) flags[1] = 1;
   }
@@ -447,13 +453,17 @@ q8_rows_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
       fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(BAR_Q_FULL));
-      // Before P of tile t is written: the stream's product before is done; the
-      // maximum is raised to X where X passes m by the headroom (or m is none),
+      // The stream's product of the tile before: done before its P is written over
+      // or its accumulator is rescaled.
+      auto product_done = [&](int t) -> bool {
+        return t == 0 || __all_sync(kFull, wait_ready(bar(BAR_PV_DONE + p), (t - 1) & 1));
+      };
+      // The maximum is raised to X where X passes m by the headroom (or m is none),
       // the sum and the accumulator are rescaled.
       auto raise = [&](float X, int t) -> bool {
-        if (t > 0 && !__all_sync(kFull, wait_ready(bar(BAR_PV_DONE + p), (t - 1) & 1))) return false;
         const bool need = !(X <= m + kOverflow);
         if (!__any_sync(kFull, need)) return true;
+        if (!product_done(t)) return false;
         const float m_new = need ? fmaxf(m, X) : m;
         const float al = m_new == m ? 1.f : m == -INFINITY ? 0.f : ex2(m - m_new);
         m = m_new;
@@ -478,7 +488,7 @@ q8_rows_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
       auto scores_read = [&] {
         fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(BAR_S_EMPTY));
+        if (lane == 0) mbar_arrive(bar(BAR_S_EMPTY + p));
       };
 
       const int h = p;                           // a stream takes one half of every tile
@@ -486,7 +496,7 @@ q8_rows_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
       for (int t = 0; t < ntiles; ++t) {
         const bool is_tree = t >= n_pre;
         const int nvalid = is_tree ? a.R : valid_of(t);
-        if (!__all_sync(kFull, wait_ready(bar(BAR_S_FULL), t & 1))) {
+        if (!__all_sync(kFull, wait_ready(bar(BAR_S_FULL + p), t & 1))) {
           failed = true;
           break;
         }
@@ -543,7 +553,7 @@ q8_rows_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
         auto weights = [&](auto scaled) {          // scaled: a factor per value row
 #pragma unroll
           for (int c = 0; c < 64; c += 32) {
-            uint32_t w[16];
+            uint32_t w[16];                        // (32 exponentials hide the product's wait)
 #pragma unroll
             for (int i = 0; i < 32; i += 4) {
               const float2 xa = __ffma2_rn(make_float2(v[c + i], v[c + i + 1]), f2, o2);
@@ -562,11 +572,18 @@ q8_rows_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
               w[i / 2] = pack_half2(pa.x, pa.y);
               w[i / 2 + 1] = pack_half2(pb.x, pb.y);
             }
+            if (c == 0) {
+              if (!product_done(t)) return false;
+              fence_after();
+            }
             tmem_st16(tp + c / 2, w);
           }
+          return true;
         };
-        if (is_tree) weights(std::true_type{});
-        else weights(std::false_type{});
+        if (!(is_tree ? weights(std::true_type{}) : weights(std::false_type{}))) {
+          failed = true;
+          break;
+        }
         l = fmaf((sa.x + sa.y) + (sb.x + sb.y), pow2i(-d), l);
         tmem_wait_st();
         fence_before();

@@ -179,14 +179,14 @@ __device__ __forceinline__ void WideShare<W, T>::widen(const uint4 (&r)[kCount],
   }
 }
 
-// Scratch rows of (request b, head hk): eight lanes of the n threads (at least
-// 192) per row.  Which ones some row sees, their factors, and (returned) this
-// thread's largest exponent of a value row.
-template <int D>
-__device__ __forceinline__ int scan_tree(const Q8AttnArgs& a, int b, int hk, int wt, int n,
-                                         float* kt_in, float* vt_in, float* kt_out, int* vt_u) {
+// Scratch rows of (request b, head hk): eight lanes of the N threads per row.  Which
+// ones some row sees, their factors, and (returned) this thread's largest exponent of
+// a value row.
+template <int D, int N>
+__device__ __forceinline__ int scan_tree(const Q8AttnArgs& a, int b, int hk, int wt, float* kt_in,
+                                         float* vt_in, float* kt_out, int* vt_u) {
   constexpr int NV = D / 64;           // 16-byte vectors per lane and row
-  constexpr int kRounds = 3;           // 65 rows x 8 lanes over 192 threads
+  constexpr int kRounds = (65 * 8 + N - 1) / N;
   const int lane = threadIdx.x & 31;
   uint32_t lo = 0, hi = 0;
 #pragma unroll
@@ -199,7 +199,7 @@ __device__ __forceinline__ int scan_tree(const Q8AttnArgs& a, int b, int hk, int
   uint4 kw[kRounds][NV], vw[kRounds][NV];
 #pragma unroll
   for (int i = 0; i < kRounds; ++i) {
-    const int x = wt + n * i, j = x >> 3, c = x & 7;
+    const int x = wt + N * i, j = x >> 3, c = x & 7;
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
       kw[i][v] = vw[i][v] = make_uint4(0u, 0u, 0u, 0u);
@@ -216,7 +216,7 @@ __device__ __forceinline__ int scan_tree(const Q8AttnArgs& a, int b, int hk, int
   int best = -1000;
 #pragma unroll
   for (int i = 0; i < kRounds; ++i) {
-    const int x = wt + n * i, j = x >> 3, c = x & 7;
+    const int x = wt + N * i, j = x >> 3, c = x & 7;
     uint32_t kt = 0, vt = 0;
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
@@ -243,7 +243,7 @@ __device__ __forceinline__ int scan_tree(const Q8AttnArgs& a, int b, int hk, int
     }
     if (live && !bad) best = max(best, ev - 135);
   }
-  for (int j = a.R + wt; j < kKeys; j += n) {      // rows that do not exist
+  for (int j = a.R + wt; j < kKeys; j += N) {      // rows that do not exist
     kt_in[j] = vt_in[j] = 0.f;
     kt_out[j] = 1.f;
     vt_u[j] = -900;
