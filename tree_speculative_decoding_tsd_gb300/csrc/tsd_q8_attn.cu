@@ -361,7 +361,7 @@ Q8Plan plan_q8(const tsd_attn_desc& d) {
     } else if (M <= kQ8FewRows) {
       p.path = kQ8Few;
       p.nrg = 1;
-      p.rb = (int)ceil_div(M, 16) * 16;
+      p.rb = M;
     } else {
       p.path = kQ8Rows;
       p.nrg = (int)ceil_div(M, 128);

@@ -1,10 +1,9 @@
 // tcgen05 path of tsd_tree_verify_attn_q8 for bf16 heads of 64 or 128 dims with few
 // packed rows (R tree rows x g query heads of a KV head): decoding, small trees.
 //
-// Products, transposed so that the packed rows are the columns (N = 16 or 32; the
-// tensor core takes 45 cycles for an instruction of 128 x N up to N = 48, so the
-// layout of tsd_q8_tc.cu, 128 rows whether they are there or not, would cost half
-// as much again):
+// Products, transposed so that the packed rows are the columns (N = 16; the tensor
+// core takes 45 cycles for an instruction of 128 x 16, and 48 to 64 in the layout of
+// tsd_q8_tc.cu, 128 rows whether they are there or not):
 //   S^T[key][n]  = K_tile . Q^T     M = 128 keys, N = packed rows, K = d
 //   O^T[dim][n] += V_tile^T . P^T   M = 128 dims, N = packed rows, K = 128 keys
 //
@@ -15,8 +14,9 @@
 // measured 6.8 TB/s over 152 SMs).  A tile's way through the scores, the softmax and
 // the product with V takes longer than that, so even and odd tiles are two streams
 // with a softmax warpgroup, a score buffer, a P^T buffer, a maximum, sums and an
-// accumulator each, joined at the end.  (One stream: 226 us for one token of 16
-// requests over 20k to 32k keys, 128 us by the bytes.)
+// accumulator each, joined at the end.  One token of 16 requests of 32 heads over 20k
+// to 32k keys: 177 us, 4.9 TB/s, 128 us by the bytes (one stream: 226 us; rows on
+// lanes: 188 us).
 //
 // Softmax with keys on lanes: a column's maximum is a reduction over the warpgroup,
 // so the running maximum is lazy: while no x of a tile exceeds 8, the tile keeps the
@@ -25,10 +25,10 @@
 //
 // Roles (608 threads): warps 0-3 and 4-7 softmax and epilogue; warp 8 issues the
 // products with Q and owns the tensor memory, warp 9 those with V; one thread of
-// warp 10 loads K tiles by TMA into a ring of four; warps 11-18 load V tiles straight into registers, two tiles ahead
-// (behind L2 prefetches), and widen them into two fp16 stages, laid out as the
-// product reads them (rows of 64 elements, 128-byte swizzle).  mbarriers order K ->
-// S^T -> softmax -> O^T and V -> O^T; every wait is bounded.
+// warp 10 loads K tiles by TMA into a ring of four; warps 11-18 load V tiles straight
+// into registers, two tiles ahead (behind L2 prefetches), and widen them into two fp16
+// stages, laid out as the product reads them (rows of 64 elements, 128-byte swizzle).
+// mbarriers order K -> S^T -> softmax -> O^T and V -> O^T; every wait is bounded.
 #include "tsd_common.cuh"
 #include "tsd_host.h"
 #include "tsd_q8_tc.cuh"
@@ -40,8 +40,9 @@ constexpr int kQk = 8, kPv = 9, kTma = 10, kWide = 11, kWideWarps = 8;
 constexpr int kWideThreads = kWideWarps * 32;
 constexpr int kThreads = (kWide + kWideWarps) * 32;
 constexpr int kDepth = 2;                        // V tiles in registers
+constexpr int N = kQ8FewRows;                    // columns of the products
 
-template <int N, int D>
+template <int D>
 struct FewLayout {
   static constexpr uint32_t k_bytes = kKeys * D;                 // a K tile: [128 keys][D] codes
   static constexpr uint32_t q_bytes = N * D;                     // hi or lo of Q
@@ -78,10 +79,10 @@ struct FewLayout {
 enum { BAR_K_FULL = 0, BAR_K_EMPTY = 4, BAR_V_FULL = 8, BAR_V_EMPTY = 10, BAR_S_FULL = 12,
        BAR_P_FULL = 14, BAR_FINAL = 16, BAR_O_DONE = 18, BAR_T_FULL = 19 };
 
-template <int N, int D>
+template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
 q8_few_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ Q8AttnArgs a) {
-  using L = FewLayout<N, D>;
+  using L = FewLayout<D>;
   if (threadIdx.x == kTma * 32) tma_desc_prefetch(&kmap);
   grid_dependency_sync();
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -126,6 +127,8 @@ q8_few_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
   // Everything that the first products need is requested at once, by the warps
   // that will use it; one barrier.
   if (warp >= kWide) {
+    TreeScan<D, kWideThreads> tree;
+    if (with_tree) tree.load(a, b, hk, wt);
     long r[kDepth];
 #pragma unroll
     for (int i = 0; i < kDepth; ++i) r[i] = i < n_pre ? a.map.row(b, hk, k0 + i * kKeys) : -1;
@@ -149,7 +152,7 @@ q8_few_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
       vex[2 * wt + 1] = (uint8_t)vb;
       top = max(va, vb) - 127;
     }
-    if (with_tree) top = max(top, scan_tree<D, kWideThreads>(a, b, hk, wt, kt_in, vt_in, kt_out, vt_u));
+    if (with_tree) top = max(top, tree.finish(a, wt, kt_in, vt_in, kt_out, vt_u));
     top = __reduce_max_sync(kFull, top);
     if (lane == 0) s_top[warp - kWide] = top;
     if (D == 64) {       // the upper 64 dims of the value tiles stay zero
@@ -580,10 +583,10 @@ q8_few_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
   }
 }
 
-template <int N, int D>
-void launch_n(const CUtensorMap& kmap, const Q8AttnArgs& a, const Q8Plan& p, cudaStream_t st) {
-  const uint32_t smem = FewLayout<N, D>::total + 1024;
-  const auto kern = q8_few_kernel<N, D>;
+template <int D>
+void launch_few(const CUtensorMap& kmap, const Q8AttnArgs& a, const Q8Plan& p, cudaStream_t st) {
+  const uint32_t smem = FewLayout<D>::total + 1024;
+  const auto kern = q8_few_kernel<D>;
   static std::atomic<uint64_t> done{0};
   allow_smem(kern, smem, done);
   launch(kern, dim3(a.map.Hkv, p.nsplit, a.B), dim3(kThreads), smem, st, kmap, a);
@@ -594,13 +597,8 @@ void launch_n(const CUtensorMap& kmap, const Q8AttnArgs& a, const Q8Plan& p, cud
 bool launch_q8_few(const tsd_attn_desc& d, const Q8AttnArgs& a, const Q8Plan& p, cudaStream_t st) {
   CUtensorMap m;
   if (encode_fn() == nullptr || !encode_keys(&m, a, d.dk, d.dk)) return false;
-  if (p.rb == 16) {
-    if (d.dk == 128) launch_n<16, 128>(m, a, p, st);
-    else launch_n<16, 64>(m, a, p, st);
-  } else {
-    if (d.dk == 128) launch_n<32, 128>(m, a, p, st);
-    else launch_n<32, 64>(m, a, p, st);
-  }
+  if (d.dk == 128) launch_few<128>(m, a, p, st);
+  else launch_few<64>(m, a, p, st);
   return true;
 }
 

@@ -33,27 +33,33 @@
 // bits.  Two e4m3 terms as for Q do not do: P spans 2^-32..2^8, and what lies
 // below 2^-17 of the largest would be lost from long flat rows.
 //
-// Two streams.  The two halves of a tile (64 keys each) have a softmax warpgroup,
-// P, an accumulator, a maximum and a sum each, joined at the end.  A softmax
+// Two streams.  The two halves of a tile (64 keys each) have scores, a softmax
+// warpgroup, P, an accumulator, a maximum and a sum each, joined at the end.  A softmax
 // thread first takes its 64 scores into registers, so that the tensor core can
-// compute the next tile's over them while the softmax runs.  (With P over the
-// scores it came from, the next scores waited for the product with V: 2000 cycles a
-// tile instead of the products' 1024.)  The running maximum is lazy: a row keeps it
-// until a tile's largest score passes it by 8 (in log2), so that its accumulator is
-// rescaled rarely.  Q (hi, lo) is in the tensor memory too, which leaves the shared
-// memory's 128 bytes a cycle to K and V.
+// compute the next tile's over them while the softmax runs, and waits for its
+// product before only behind the first 32 exponentials.  (With P over the scores it
+// came from, the next scores waited for the product with V; with one product for both
+// halves' scores, the streams waited for each other.)  The running maximum is lazy: a
+// row keeps it until a tile's largest score passes it by 8 (in log2), so that its
+// accumulator is rescaled rarely.  Q (hi, lo) is in the tensor memory too, which
+// leaves the shared memory's 128 bytes a cycle to K and V.
 //
-// Roles (608 threads): warps 0-3 and 4-7 softmax and epilogue; warp 8 issues the
-// products with V and owns the tensor memory, warp 9 those with Q; one thread of
-// warp 10 loads K tiles by TMA into a ring of four; warps 11-18 load V tiles
-// straight into registers, a tile ahead (behind L2 prefetches), and widen them
-// into three fp16 stages, laid out as the product reads them (rows of 64
-// elements, 128-byte swizzle).  mbarriers order K -> S -> softmax -> O and V ->
-// O; every wait is bounded.
+// Roles (512 threads: 128 registers each, which the softmax needs; with three more
+// widening warps and 96 registers a tile took 10% longer): warps 0-3 and 4-7 softmax
+// and epilogue; warp 8 issues the products with V and owns the tensor memory, warp 9
+// those with Q; one thread of warp 10 loads K tiles by TMA into a ring of four; warps
+// 11-15 load V tiles straight into registers, a tile ahead (behind L2 prefetches), and
+// widen them into three fp16 stages, laid out as the product reads them (rows of 64
+// elements, 128-byte swizzle).  mbarriers order K -> S -> softmax -> O and V -> O;
+// every wait is bounded.
 //
-// What bounds it: the products of a 128-key tile, 8 8-bit and 8 fp16 ones of M =
-// 128, N = 128 (about 70 cycles each), and behind them the softmax (128
-// exponentials per row at 16 a cycle and SM).
+// What bounds it: the softmax of a tile, about 1750 cycles from its scores to its P
+// with two warps on each scheduler, while the tensor core needs 1280 (8 products with
+// Q of 128 x 64 at 48 cycles for each half, 8 with V of 128 x 128 at 64) and is busy
+// for 52% of the time; and 9600 cycles of set-up (lengths, pages and exponents, one
+// behind the other) and 3500 of epilogue per CTA.  8 x 65 rows of 32 heads over 32k
+// keys: 341 us, 820 TFLOP/s; 32 x 33 rows over 1k to 4k keys: 111 us; 8 x 8 rows over
+// 32k keys: 124 us, 4.3 TB/s of cache.
 #include <type_traits>
 
 #include "tsd_common.cuh"
@@ -78,15 +84,13 @@ struct RowLayout {
   static constexpr uint32_t v_bytes = kKeys * D * 2;
   static constexpr uint32_t off_k = 0;
   static constexpr uint32_t off_v = kRing * k_bytes;
-  static constexpr uint32_t off_q = off_v + kStages * v_bytes;         // bf16 rows, padded
-  static constexpr uint32_t q_pitch = 2 * D + 16;
-  static constexpr uint32_t off_ml = off_q + kRows * q_pitch;          // float2[2][128] (m, l)
+  static constexpr uint32_t off_ml = off_v + kStages * v_bytes;        // float2[2][128] (m, l)
   static constexpr uint32_t off_rows = off_ml + 16 * kRows;            // i64[kMaxTiles]
   static constexpr uint32_t off_tree = off_rows + 8 * kMaxTiles;       // 4 x 32 bits [128]
   static constexpr uint32_t off_kex = off_tree + 16 * kKeys;           // u8[2 kMaxTiles]
   static constexpr uint32_t off_vex = off_kex + 2 * kMaxTiles;
   static constexpr uint32_t off_bar = off_vex + 2 * kMaxTiles;
-  static constexpr int nbar = 27;
+  static constexpr int nbar = 26;
   static constexpr uint32_t off_flags = off_bar + 8 * nbar;            // tmem, abort
   static constexpr uint32_t off_top = off_flags + 8;                   // int[kWideWarps]
   static constexpr uint32_t total = off_top + 4 * kWideWarps;
@@ -96,11 +100,10 @@ struct RowLayout {
 // FULL: the copy landed, the warps wrote or the product is done; EMPTY: read by
 // the product (S_EMPTY: by the softmax).  S, P_FULL and PV_DONE: one per stream.
 // T_FULL: the scratch rows' keys, which take the two K slots behind the last
-// prefix tile (hi, lo).  Q_FULL: Q is in the tensor memory.  FINAL: one per
-// issuing warp.
+// prefix tile (hi, lo).  FINAL: one per issuing warp.
 enum { BAR_K_FULL = 0, BAR_K_EMPTY = 4, BAR_V_FULL = 8, BAR_V_EMPTY = 11, BAR_S_FULL = 14,
        BAR_S_EMPTY = 16, BAR_P_FULL = 18, BAR_PV_DONE = 20, BAR_O_DONE = 22, BAR_T_FULL = 23,
-       BAR_FINAL = 24, BAR_Q_FULL = 26 };
+       BAR_FINAL = 24 };
 
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32]) {
   uint32_t r[32];
@@ -179,11 +182,12 @@ q8_rows_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
 
   // ---------------------------------------------------------------- set-up
   // Everything that the first products need is requested at once, by the warps
-  // that will use it; one barrier, then Q's way into the tensor memory.
+  // that will use it, and ready at one barrier.
   const int wt = tid - kWide * 32;
   using Share = WideShare<D / 16, kWideThreads>;
   const Share share(wt);
-  uint64_t mask = 0ull;     // softmax threads: the scratch rows that the row sees
+  uint64_t mask = 0ull;     // softmax threads: the scratch rows that the row sees,
+  float c2 = 0.f;           // and the factor of its scores
   uint4 vreg[Share::kCount];
   // the tile at cache row `row` (a missing page: none)
   auto load_v = [&](long row, int nvalid) {
@@ -192,6 +196,7 @@ q8_rows_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
 
   if (warp >= kWide) {
     // the first V tile, the exponents and rows of the split's tiles, the scratch rows
+    TreeScan<D, kWideThreads> tree;
     const long r0 = n_pre > 0 ? a.map.row(b, hk, k0) : -1;
     const long rt = wt < n_pre ? a.map.row(b, hk, k0 + wt * kKeys) : -1;
     if (n_pre > 0) load_v(r0, valid_of(0));
@@ -212,30 +217,53 @@ q8_rows_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
       vex[2 * t + 1] = (uint8_t)vb;
       top = max(top, max(va, vb) - 127);
     }
-    if (with_tree) top = max(top, scan_tree<D, kWideThreads>(a, b, hk, wt, kt_in, vt_in, kt_out, vt_u));
+    if (with_tree) tree.load(a, b, hk, wt);
+    if (with_tree) top = max(top, tree.finish(a, wt, kt_in, vt_in, kt_out, vt_u));
     top = __reduce_max_sync(kFull, top);
     if (lane == 0) s_top[warp - kWide] = top;
   } else if (warp < 8) {
-    // Q by coalesced copies, rows padded by 16 bytes, so that eight lanes' rows
-    // start in eight different banks; and what this thread's row sees
-    const int row = (warp & 3) * 32 + lane;
-    for (int x = tid; x < live_warps * 32 * (D / 8); x += 256) {
-      const int r = x / (D / 8), u = x % (D / 8);
-      const bool valid = r < rows_here;
-      const __nv_bfloat16* src = (const __nv_bfloat16*)a.q;
-      if (valid) {
-        const int pr = row_base + r;
-        const int tr = pr / a.g, qh = hk * a.g + pr % a.g;
-        src += (((long)b * a.R + tr) * a.Hq + qh) * D + u * 8;
+    // Q into the tensor memory: a thread takes its packed row, whose largest element
+    // scales it, and splits the stream's half of it; and what the row sees
+    const int q = warp & 3, p = warp >> 2, row = q * 32 + lane;
+    if (q < live_warps) {
+      uint4 w[D / 8];
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i) w[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (row < rows_here) {
+        const int pr = row_base + row, tr = pr / a.g, qh = hk * a.g + pr % a.g;
+        const uint4* src =
+            (const uint4*)((const __nv_bfloat16*)a.q + (((long)b * a.R + tr) * a.Hq + qh) * D);
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) w[i] = __ldg(src + i);
+        mask = tr > 0 ? a.mask[(long)b * a.R + tr] : 0ull;
       }
-      cp_async16(sbase + L::off_q + r * L::q_pitch + u * 16, src, valid);
+      uint32_t qtop = 0;
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i) qtop = top_pairs(qtop, w[i]);
+      qtop = top_of(qtop);
+      const bool bad = qtop >= 0x7f800000u;
+      const int qe = row_exponent(qtop);
+      const float f = bad ? 0.f : q8_scale(261 - qe);
+      c2 = bad ? __int_as_float(0x7fffffff) : a.qscale * q8_scale(qe - 7);
+      __syncwarp();
+      asm volatile("bar.sync 2, %0;\n" ::"r"(64 * live_warps + 32) : "memory");   // (allocated)
+      const uint32_t tq = flags[0] + kColQ + p * (D / 8) + ((uint32_t)(q * 32) << 16);
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) {           // 16 elements: four columns of hi, four of lo
+        uint4 x[2] = {p ? w[D / 16 + 2 * c] : w[2 * c], p ? w[D / 16 + 2 * c + 1] : w[2 * c + 1]};
+        if (bad) x[0] = x[1] = make_uint4(0u, 0u, 0u, 0u);
+        uint4 hi, lo;
+        split16(x, f, hi, lo);
+        tmem_st4(tq + 4 * c, __uint_as_float(hi.x), __uint_as_float(hi.y), __uint_as_float(hi.z),
+                 __uint_as_float(hi.w));
+        tmem_st4(tq + D / 4 + 4 * c, __uint_as_float(lo.x), __uint_as_float(lo.y),
+                 __uint_as_float(lo.z), __uint_as_float(lo.w));
+      }
+      tmem_wait_st();
     }
-    if (row < rows_here) {
-      const int tr = (row_base + row) / a.g;
-      mask = tr > 0 ? a.mask[(long)b * a.R + tr] : 0ull;
-    }
-    asm volatile("cp.async.commit_group;\n cp.async.wait_group 0;\n" ::: "memory");
   } else if (warp == kTma) {
+    long row = 0;                                    // of the ring's tiles
+    if (a.map.page_size && lane < kRing && lane < n_pre) row = a.map.row(b, hk, k0 + lane * kKeys);
     if (lane == 0) {
       for (int i = 0; i < kRing; ++i) {
         mbar_init(bar(BAR_K_FULL + i), 1);
@@ -254,19 +282,22 @@ q8_rows_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
       }
       mbar_init(bar(BAR_O_DONE), 1);
       mbar_init(bar(BAR_T_FULL), kWideWarps);
-      mbar_init(bar(BAR_Q_FULL), 2 * live_warps);
       flags[1] = 0;
       asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
-      for (int t = 0; t < kRing && t < n_pre; ++t)
-        load_keys(a, kmap, b, hk, k0 + t * kKeys,
-                  a.map.page_size ? a.map.row(b, hk, k0 + t * kKeys) : 0,
-                  sbase + L::off_k + t * L::k_bytes, L::k_bytes, bar(BAR_K_FULL + t));
+    }
+    __syncwarp();
+    for (int t = 0; t < kRing && t < n_pre; ++t) {
+      const long r = __shfl_sync(kFull, row, t);
+      if (lane == 0)
+        load_keys(a, kmap, b, hk, k0 + t * kKeys, r, sbase + L::off_k + t * L::k_bytes, L::k_bytes,
+                  bar(BAR_K_FULL + t));
     }
     __syncwarp();
   } else if (warp == kPv) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;\n" ::"r"(
         sbase + L::off_flags));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n");
+    asm volatile("bar.arrive 2, %0;\n" ::"r"(64 * live_warps + 32) : "memory");
   }
   fence_before();
   __syncthreads();
@@ -349,7 +380,7 @@ q8_rows_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
     const uint64_t kd0 = row_desc<D>(sbase + L::off_k);
     const uint32_t tq = tmem + kColQ;
     const bool one = elect_one();
-    bool ok = wait_ready(bar(BAR_Q_FULL), 0);
+    bool ok = true;
     for (int t = 0; ok && t < ntiles; ++t) {
       const int sl = t % kRing;
       ok = t < n_pre ? wait_ready(bar(BAR_K_FULL + sl), (t / kRing) & 1)
@@ -428,31 +459,6 @@ q8_rows_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
     float m = -INFINITY, l = 0.f;
     bool failed = false;
     if (q < live_warps) {
-      // Q into the tensor memory: a thread takes its row's largest element and
-      // splits the stream's half of the row
-      const uint4* qp = (const uint4*)(smem + L::off_q + row * L::q_pitch);
-      uint32_t qtop = 0;
-#pragma unroll
-      for (int i = 0; i < D / 8; ++i) qtop = top_pairs(qtop, qp[i]);
-      qtop = top_of(qtop);
-      const bool bad = qtop >= 0x7f800000u;
-      const int qe = row_exponent(qtop);
-      const float c2 = bad ? __int_as_float(0x7fffffff) : a.qscale * q8_scale(qe - 7);
-      const uint32_t tq = tmem + kColQ + p * (D / 8) + lane_off;
-#pragma unroll
-      for (int c = 0; c < D / 32; ++c) {           // 16 elements: four columns of hi, four of lo
-        uint4 w[2] = {qp[p * (D / 16) + 2 * c], qp[p * (D / 16) + 2 * c + 1]}, hi, lo;
-        if (bad) w[0] = w[1] = make_uint4(0u, 0u, 0u, 0u);
-        split16(w, q8_scale(261 - qe), hi, lo);
-        tmem_st4(tq + 4 * c, __uint_as_float(hi.x), __uint_as_float(hi.y), __uint_as_float(hi.z),
-                 __uint_as_float(hi.w));
-        tmem_st4(tq + D / 4 + 4 * c, __uint_as_float(lo.x), __uint_as_float(lo.y),
-                 __uint_as_float(lo.z), __uint_as_float(lo.w));
-      }
-      tmem_wait_st();
-      fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(BAR_Q_FULL));
       // The stream's product of the tile before: done before its P is written over
       // or its accumulator is rescaled.
       auto product_done = [&](int t) -> bool {

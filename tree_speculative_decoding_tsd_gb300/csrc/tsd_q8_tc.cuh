@@ -179,77 +179,83 @@ __device__ __forceinline__ void WideShare<W, T>::widen(const uint4 (&r)[kCount],
   }
 }
 
-// Scratch rows of (request b, head hk): eight lanes of the N threads per row.  Which
-// ones some row sees, their factors, and (returned) this thread's largest exponent of
-// a value row.
+// Scratch rows of (request b, head hk), eight lanes of the N threads per row: loaded
+// early, looked at later.
 template <int D, int N>
-__device__ __forceinline__ int scan_tree(const Q8AttnArgs& a, int b, int hk, int wt, float* kt_in,
-                                         float* vt_in, float* kt_out, int* vt_u) {
-  constexpr int NV = D / 64;           // 16-byte vectors per lane and row
-  constexpr int kRounds = (65 * 8 + N - 1) / N;
-  const int lane = threadIdx.x & 31;
-  uint32_t lo = 0, hi = 0;
-#pragma unroll
-  for (int i = 0; i < 3; ++i) {
-    const int r = lane + 32 * i;
-    const uint64_t m = r > 0 && r < a.R ? a.mask[(long)b * a.R + r] : 0ull;
-    lo |= (uint32_t)m;
-    hi |= (uint32_t)(m >> 32);
-  }
+struct TreeScan {
+  static constexpr int NV = D / 64;    // 16-byte vectors per lane and row
+  static constexpr int kRounds = (65 * 8 + N - 1) / N;
   uint4 kw[kRounds][NV], vw[kRounds][NV];
+  uint32_t lo, hi;                     // rows that this lane's tree rows see
+
+  __device__ __forceinline__ void load(const Q8AttnArgs& a, int b, int hk, int wt) {
+    const int lane = threadIdx.x & 31;
+    lo = hi = 0;
 #pragma unroll
-  for (int i = 0; i < kRounds; ++i) {
-    const int x = wt + N * i, j = x >> 3, c = x & 7;
+    for (int i = 0; i < 3; ++i) {
+      const int r = lane + 32 * i;
+      const uint64_t m = r > 0 && r < a.R ? a.mask[(long)b * a.R + r] : 0ull;
+      lo |= (uint32_t)m;
+      hi |= (uint32_t)(m >> 32);
+    }
 #pragma unroll
-    for (int v = 0; v < NV; ++v) {
-      kw[i][v] = vw[i][v] = make_uint4(0u, 0u, 0u, 0u);
-      if (j < a.R) {
-        const long row = (((long)b * a.R + j) * a.map.Hkv + hk) * (D / 8) + c * NV + v;
-        kw[i][v] = __ldg((const uint4*)a.kt + row);
-        vw[i][v] = __ldg((const uint4*)a.vt + row);
+    for (int i = 0; i < kRounds; ++i) {
+      const int x = wt + N * i, j = x >> 3, c = x & 7;
+#pragma unroll
+      for (int v = 0; v < NV; ++v) {
+        kw[i][v] = vw[i][v] = make_uint4(0u, 0u, 0u, 0u);
+        if (j < a.R) {
+          const long row = (((long)b * a.R + j) * a.map.Hkv + hk) * (D / 8) + c * NV + v;
+          kw[i][v] = __ldg((const uint4*)a.kt + row);
+          vw[i][v] = __ldg((const uint4*)a.vt + row);
+        }
       }
     }
   }
-  lo = __reduce_or_sync(kFull, lo);
-  hi = __reduce_or_sync(kFull, hi);
-  const uint64_t seen = ((uint64_t)hi << 32) | lo;
-  int best = -1000;
+  // Which rows some row sees, their factors, and (returned) this thread's largest
+  // exponent of a value row.
+  __device__ __forceinline__ int finish(const Q8AttnArgs& a, int wt, float* kt_in, float* vt_in,
+                                        float* kt_out, int* vt_u) const {
+    const uint64_t seen =
+        ((uint64_t)__reduce_or_sync(kFull, hi) << 32) | __reduce_or_sync(kFull, lo);
+    int best = -1000;
 #pragma unroll
-  for (int i = 0; i < kRounds; ++i) {
-    const int x = wt + N * i, j = x >> 3, c = x & 7;
-    uint32_t kt = 0, vt = 0;
+    for (int i = 0; i < kRounds; ++i) {
+      const int x = wt + N * i, j = x >> 3, c = x & 7;
+      uint32_t kt = 0, vt = 0;
 #pragma unroll
-    for (int v = 0; v < NV; ++v) {
-      kt = top_pairs(kt, kw[i][v]);
-      vt = top_pairs(vt, vw[i][v]);
-    }
-    kt = top_of(kt);
-    vt = top_of(vt);
+      for (int v = 0; v < NV; ++v) {
+        kt = top_pairs(kt, kw[i][v]);
+        vt = top_pairs(vt, vw[i][v]);
+      }
+      kt = top_of(kt);
+      vt = top_of(vt);
 #pragma unroll
-    for (int o = 4; o > 0; o >>= 1) {
-      kt = max(kt, __shfl_xor_sync(kFull, kt, o));
-      vt = max(vt, __shfl_xor_sync(kFull, vt, o));
+      for (int o = 4; o > 0; o >>= 1) {
+        kt = max(kt, __shfl_xor_sync(kFull, kt, o));
+        vt = max(vt, __shfl_xor_sync(kFull, vt, o));
+      }
+      if (j >= a.R) continue;
+      const bool live = j == 0 || ((seen >> (j - 1)) & 1ull);
+      const bool bad = kt >= 0x7f800000u || vt >= 0x7f800000u;
+      const int ek = row_exponent(kt), ev = row_exponent(vt);
+      if (c == 0) {
+        // K: 2^(7 - (e - 127)) and its inverse; V: 2^(8 - (e - 127))
+        kt_in[j] = live && !bad ? q8_scale(261 - ek) : 0.f;
+        vt_in[j] = live && !bad ? q8_scale(262 - ev) : 0.f;
+        kt_out[j] = bad ? __int_as_float(0x7fffffff) : q8_scale(ek - 7);
+        vt_u[j] = live && !bad ? ev - 135 : -900;
+      }
+      if (live && !bad) best = max(best, ev - 135);
     }
-    if (j >= a.R) continue;
-    const bool live = j == 0 || ((seen >> (j - 1)) & 1ull);
-    const bool bad = kt >= 0x7f800000u || vt >= 0x7f800000u;
-    const int ek = row_exponent(kt), ev = row_exponent(vt);
-    if (c == 0) {
-      // K: 2^(7 - (e - 127)) and its inverse; V: 2^(8 - (e - 127))
-      kt_in[j] = live && !bad ? q8_scale(261 - ek) : 0.f;
-      vt_in[j] = live && !bad ? q8_scale(262 - ev) : 0.f;
-      kt_out[j] = bad ? __int_as_float(0x7fffffff) : q8_scale(ek - 7);
-      vt_u[j] = live && !bad ? ev - 135 : -900;
+    for (int j = a.R + wt; j < kKeys; j += N) {      // rows that do not exist
+      kt_in[j] = vt_in[j] = 0.f;
+      kt_out[j] = 1.f;
+      vt_u[j] = -900;
     }
-    if (live && !bad) best = max(best, ev - 135);
+    return best;
   }
-  for (int j = a.R + wt; j < kKeys; j += N) {      // rows that do not exist
-    kt_in[j] = vt_in[j] = 0.f;
-    kt_out[j] = 1.f;
-    vt_u[j] = -900;
-  }
-  return best;
-}
+};
 
 // The packed rows of a row group as hi + lo (n_rows of them, zeros behind the
 // last one) with their score factors: D / 16 lanes of the n threads per row.
