@@ -16,7 +16,7 @@
 // between the maximum and the conversion, so the source is read once and the codes
 // are written once; earlier rows are read only when the exponent grows.  Bounded by
 // memory: 2 (or 4) bytes read and 1 written per element (4 x 8192 rows at most of 8
-// heads: 37 us with the length's update, 22 us by the bytes).  Commit: a warp takes a
+// heads: 34 us with the length's update, 22 us by the bytes).  Commit: a warp takes a
 // (block, head, K or V); bounded by latency.
 #include <cuda_bf16.h>
 
@@ -45,6 +45,10 @@ constexpr int kNoCode = 0x7fffffff;
 // Threads of a CTA, and 8-element vectors of a block per thread.
 template <int D> constexpr int kWriteThreads = D > 128 ? 512 : 256;
 template <int D> constexpr int kWriteVecs = kQ8Block * D / 8 / kWriteThreads<D>;
+
+// CTAs per SM to fit the registers to.  (4 x 8192 rows of 128 bf16 dims: 42 us at six,
+// 46 at the compiler's five; rows of 576 dims need the registers for their vectors.)
+template <int D> constexpr int kWriteCtas = D > 128 ? 1 : 6;
 
 struct WriteSmem {
   int code;
@@ -187,7 +191,7 @@ __device__ __forceinline__ void write_block(const Q8WriteArgs& a, int b, int h, 
 // Prefill: grid (blocks, part x head, request).  prefix_len changes only in
 // write_advance_kernel, so every CTA reads the length of before.
 template <typename T, int D>
-__global__ void __launch_bounds__(kWriteThreads<D>)
+__global__ void __launch_bounds__(kWriteThreads<D>, kWriteCtas<D>)
 write_q8_kernel(const __grid_constant__ Q8WriteArgs a) {
   __shared__ WriteSmem s;
   grid_dependency_sync();
@@ -213,9 +217,9 @@ __global__ void __launch_bounds__(128) write_advance_kernel(const __grid_constan
 // request, a warp per (block, head, part): the prefix length is read and advanced by
 // the same CTA, and no launch or cluster is needed to order the two.  (A cluster of
 // eight CTAs took as long on the device, 13.4 us with the advance inside a graph, and
-// 1 us more to launch.)  Rows of up to 128 bf16 dims stay in registers between the maximum and the
-// conversion; wider ones are read again, from L1.
-constexpr int kCommitThreads = 1024;
+// 1 us more to launch.)  Rows of up to 128 bf16 dims stay in registers between the
+// maximum and the conversion; wider ones are read again, from L1.
+constexpr int kCommitThreads = 512;
 
 template <typename T, int D>
 __device__ __forceinline__ void commit_block(const Q8WriteArgs& a, const WriteSmem& s, int b, int h,
