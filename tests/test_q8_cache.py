@@ -480,7 +480,9 @@ ATTN = [("gqa", 1, 1, [2048], {}), ("gqa", 3, 17, [700, 1, 129], {}), ("gqa", 2,
         ("one", 4, 1, [3, 127, 128, 129], {}), ("wide", 1, 65, [900], {}), ("wide", 2, 2, [4000], dict(page=128)),
         ("latent", 2, 1, [300, 1000], {}), ("latent", 1, 9, [515], dict(page=128)), ("latent-few", 2, 3, [200], {}),
         ("gqa", 2, 5, [777], dict(dtype=torch.float32)), ("narrow", 2, 3, [90], dict(dtype=torch.float32, page=128)),
-        ("latent-few", 1, 2, [333], dict(dtype=torch.float32)), ("gqa", 40, 2, [500, 90, 1], {})]
+        ("latent-few", 1, 2, [333], dict(dtype=torch.float32)), ("gqa", 40, 2, [500, 90, 1], {}),
+        ("gqa", 3, 4, [130, 2500, 1], {}), ("gqa", 3, 5, [130, 2500, 1], dict(page=128)), ("gqa", 2, 8, [400], {}),
+        ("narrow", 2, 3, [777, 64], {})]
 
 
 @gpu

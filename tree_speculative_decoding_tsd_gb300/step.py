@@ -4,6 +4,9 @@
 fixed configuration, so repeated steps allocate nothing.  The inputs of a
 step (draft marginals, root tokens, queries, scratch-pad K/V, target logits)
 and the persistent state (KV cache, prefix lengths) are caller tensors.
+
+``Q8TreeVerifyStep`` is the same step over an 8-bit cache, which it can hold at a
+budget of rows (``Q8Cache`` and ``RowWeights`` are its persistent state).
 """
 
 from __future__ import annotations
@@ -12,10 +15,12 @@ import dataclasses
 
 import torch
 
-from . import (make_desc, tsd_accept_commit, tsd_accept_walk, tsd_accept_walk_workspace_size,
-               tsd_commit_path, tsd_target_argmax, tsd_walk_commit,
-               tsd_tree_build, tsd_tree_build_adaptive, tsd_tree_build_conditioned,
-               tsd_tree_build_workspace_size, tsd_tree_verify_attn, tsd_verify_workspace_size,
+from . import (make_desc, q8_blocks, tsd_accept_commit, tsd_accept_walk,
+               tsd_accept_walk_workspace_size, tsd_cache_evict_q8, tsd_cache_evict_workspace_size,
+               tsd_cache_weights_q8, tsd_cache_write_q8, tsd_commit_path, tsd_commit_path_q8,
+               tsd_target_argmax, tsd_walk_commit, tsd_tree_build, tsd_tree_build_adaptive,
+               tsd_tree_build_conditioned, tsd_tree_build_workspace_size, tsd_tree_verify_attn,
+               tsd_tree_verify_attn_q8, tsd_verify_q8_workspace_size, tsd_verify_workspace_size,
                workspace)
 
 
@@ -184,3 +189,137 @@ class TreeVerifyStep:
     def for_workload(cls, w, device="cuda", overlap_argmax=None):
         return cls(w.B, w.S, w.V, w.k, w.D, w.Hq, w.Hkv, w.dk, w.dv, w.cap, w.torch_dtype,
                    w.v_aliases_k, w.scale, device, overlap_argmax)
+
+
+@dataclasses.dataclass
+class Q8Cache:
+    """Codes [B][Hkv][cap][dk | dv] (uint8) and block exponents [B][Hkv][ceil(cap / 64)]
+    (uint8); vq and vexp are None where V aliases K.  With a page table: pools of pages
+    [num_pages][Hkv][page_size][dk | dv] and [num_pages][Hkv][page_size / 64]."""
+
+    kq: torch.Tensor
+    vq: torch.Tensor | None
+    kexp: torch.Tensor
+    vexp: torch.Tensor | None
+    page_table: torch.Tensor | None = None
+    page_size: int = 0
+
+    def paging(self):
+        return dict(page_table=self.page_table, page_size=self.page_size)
+
+
+@dataclasses.dataclass
+class RowWeights:
+    """Attention weight (fp32) and token position (int32) of every cached row
+    [B][Hkv][cap], and the tokens that each head's request has had [B][Hkv]."""
+
+    acc: torch.Tensor
+    pos: torch.Tensor
+    seen: torch.Tensor
+
+
+class Q8TreeVerifyStep(TreeVerifyStep):
+    """The step over an 8-bit cache: build -> verify -> walk -> commit.
+
+    With ``keep`` the cache is held at that many rows per request: a round also adds
+    the accepted rows' attention weights to ``RowWeights`` (older ones times ``decay``)
+    and then drops the lightest rows past ``keep``, never one of the request's first
+    ``sink`` or last ``recent`` tokens.  A round needs room for keep + S + 1 rows.
+    """
+
+    def __init__(self, B, S, V, k, D, Hq, Hkv, dk, dv, cap, dtype, v_aliases_k, scale,
+                 device="cuda", keep=0, sink=0, recent=0, decay=1.0):
+        if keep and (keep + S + 1 > cap or keep < 1 or sink < 0 or recent < 0 or
+                     sink + recent > keep or not 0.0 <= decay <= 1.0):
+            raise ValueError(f"keep {keep}, sink {sink}, recent {recent}, decay {decay}: need "
+                             f"sink + recent <= keep <= cap - S - 1 and 0 <= decay <= 1")
+        super().__init__(B, S, V, k, D, Hq, Hkv, dk, dv, cap, dtype, v_aliases_k, scale, device)
+        self.keep, self.sink, self.recent, self.decay = keep, sink, recent, decay
+        dev = self.out.device
+        self.ws_verify = workspace(tsd_verify_q8_workspace_size(self.desc), dev)
+        self.ws_evict = workspace(tsd_cache_evict_workspace_size(self.desc), dev) if keep else None
+
+    def new_cache(self):
+        """An empty contiguous cache, and the weights of its rows (None without ``keep``)."""
+        dev, lead, nb = self.out.device, (self.B, self.Hkv), q8_blocks(self.cap)
+
+        def zeros(*shape, dtype=torch.uint8):
+            return torch.zeros(shape, dtype=dtype, device=dev)
+
+        alias = self.v_aliases_k
+        cache = Q8Cache(zeros(*lead, self.cap, self.dk),
+                        None if alias else zeros(*lead, self.cap, self.dv), zeros(*lead, nb),
+                        None if alias else zeros(*lead, nb))
+        if not self.keep:
+            return cache, None
+        return cache, RowWeights(zeros(*lead, self.cap, dtype=torch.float32),
+                                 zeros(*lead, self.cap, dtype=torch.int32),
+                                 zeros(*lead, dtype=torch.int32))
+
+    def append(self, knew, vnew, new_len, cache, prefix_len, stream=None):
+        """Rows [B][T][Hkv][d], ``new_len[b]`` of them, behind the prefix (a prompt).  With
+        ``keep``, the caller then sets their ``RowWeights``."""
+        tsd_cache_write_q8(self.desc, knew, vnew, new_len, cache.kq, cache.vq, cache.kexp,
+                           cache.vexp, prefix_len, self.err, stream, **cache.paging())
+
+    def verify(self, q, cache, prefix_len, ktree, vtree, stream=None):
+        tsd_tree_verify_attn_q8(self.desc, q, cache.kq, cache.vq, cache.kexp, cache.vexp,
+                                prefix_len, ktree, vtree, self.tree.mask, self.out, self.lse,
+                                self.ws_verify, self.err, stream, **cache.paging())
+
+    def weigh(self, q, cache, prefix_len, ktree, weights, stream=None):
+        """The accepted rows' attention weights, between the walk and the commit."""
+        w = self.walk
+        tsd_cache_weights_q8(self.desc, self.S, q, cache.kq, cache.kexp, prefix_len, ktree,
+                             w.accept_rows, w.accept_len, self.lse, self.decay, weights.acc,
+                             weights.pos, weights.seen, self.err, stream, **cache.paging())
+
+    def commit(self, ktree, vtree, cache, prefix_len, stream=None):
+        w = self.walk
+        tsd_commit_path_q8(self.desc, self.S, ktree, vtree, w.accept_rows, w.accept_len,
+                           cache.kq, cache.vq, cache.kexp, cache.vexp, prefix_len, self.err,
+                           stream, **cache.paging())
+
+    def evict(self, cache, prefix_len, weights, stream=None):
+        """Requests of more than ``keep`` rows cut to the ``keep`` heaviest."""
+        tsd_cache_evict_q8(self.desc, self.keep, self.sink, self.recent, weights.acc, weights.pos,
+                           weights.seen, cache.kq, cache.vq, cache.kexp, cache.vexp, prefix_len,
+                           self.ws_evict, self.err, stream, **cache.paging())
+
+    def run(self, probs, root_tok, q, cache, prefix_len, ktree, vtree, logits, weights=None,
+            stream=None):
+        """The whole step (asynchronous): build -> verify -> walk -> commit, and with
+        ``keep`` the weights before the commit and the eviction behind it."""
+        if (weights is None) != (not self.keep):
+            raise ValueError("weights: needed with keep, and only then")
+        self.build(probs, root_tok, stream)
+        self.verify(q, cache, prefix_len, ktree, vtree, stream)
+        self.accept(logits, stream)
+        if weights is not None:
+            self.weigh(q, cache, prefix_len, ktree, weights, stream)
+        self.commit(ktree, vtree, cache, prefix_len, stream)
+        if weights is not None:
+            self.evict(cache, prefix_len, weights, stream)
+
+    def accept_commit(self, *args, **kw):
+        raise NotImplementedError("the 8-bit cache takes accept() and commit()")
+
+    def capture(self, probs, root_tok, q, cache, prefix_len, ktree, vtree, logits, weights=None,
+                stream=None):
+        """Record ``run`` on the given tensors as one CUDA graph, as TreeVerifyStep.capture
+        (one round runs before the recording)."""
+        if stream is None:
+            stream = torch.cuda.Stream(device=probs.device)
+        args = (probs, root_tok, q, cache, prefix_len, ktree, vtree, logits, weights, stream)
+        with torch.cuda.stream(stream):
+            self.run(*args)
+        stream.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=stream):
+            self.run(*args)
+        return graph
+
+    @classmethod
+    def for_workload(cls, w, device="cuda", **held):
+        return cls(w.B, w.S, w.V, w.k, w.D, w.Hq, w.Hkv, w.dk, w.dv, w.cap, w.torch_dtype,
+                   w.v_aliases_k, w.scale, device, **held)
