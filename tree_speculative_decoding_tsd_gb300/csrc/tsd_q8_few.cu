@@ -70,6 +70,8 @@ struct FewLayout {
   static constexpr uint32_t off_top = off_flags + 8;             // int[kWideWarps]
   static constexpr uint32_t total = off_top + 4 * kWideWarps;
   static_assert(total + 1024 <= 232448, "shared memory budget");
+  // (at D = 64 the upper half of a value tile is zeroed while other warps still scan)
+  static_assert(kTreeBytes<D> <= (D == 64 ? kHalf : kTile), "the scan's rows");
 };
 
 // FULL: the copy landed or the warps wrote; EMPTY: read by the product (V_EMPTY
@@ -127,8 +129,7 @@ q8_few_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
   // Everything that the first products need is requested at once, by the warps
   // that will use it; one barrier.
   if (warp >= kWide) {
-    TreeScan<D, kWideThreads> tree;
-    if (with_tree) tree.load(a, b, hk, wt);
+    if (with_tree) tree_fetch<D, kWideThreads>(a, b, hk, wt, sbase + L::off_v, kTile);
     long r[kDepth];
 #pragma unroll
     for (int i = 0; i < kDepth; ++i) r[i] = i < n_pre ? a.map.row(b, hk, k0 + i * kKeys) : -1;
@@ -152,7 +153,9 @@ q8_few_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
       vex[2 * wt + 1] = (uint8_t)vb;
       top = max(va, vb) - 127;
     }
-    if (with_tree) top = max(top, tree.finish(a, wt, kt_in, vt_in, kt_out, vt_u));
+    if (with_tree)
+      top = max(top, tree_scan<D, kWideThreads>(a, b, wt, smem + L::off_v, kTile, kt_in, vt_in, kt_out,
+                                                vt_u));
     top = __reduce_max_sync(kFull, top);
     if (lane == 0) s_top[warp - kWide] = top;
     if (D == 64) {       // the upper 64 dims of the value tiles stay zero
@@ -174,6 +177,8 @@ q8_few_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
     }
     asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
   } else if (warp == kTma) {
+    long row = 0;                                    // of the ring's tiles
+    if (a.map.page_size && lane < kRing && lane < n_pre) row = a.map.row(b, hk, k0 + lane * kKeys);
     if (lane == 0) {
       for (int i = 0; i < kRing; ++i) {
         mbar_init(bar(BAR_K_FULL + i), 1);
@@ -190,10 +195,14 @@ q8_few_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
       mbar_init(bar(BAR_T_FULL), kWideWarps);
       flags[1] = 0;
       asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
-      for (int t = 0; t < kRing && t < n_pre; ++t)
-        load_keys(a, kmap, b, hk, k0 + t * kKeys,
-                  a.map.page_size ? a.map.row(b, hk, k0 + t * kKeys) : 0,
-                  sbase + L::off_k + t * L::k_bytes, L::k_bytes, bar(BAR_K_FULL + t));
+    }
+    __syncwarp();
+#pragma unroll 1
+    for (int t = 0; t < kRing && t < n_pre; ++t) {
+      const long r = __shfl_sync(kFull, row, t);
+      if (lane == 0)
+        load_keys(a, kmap, b, hk, k0 + t * kKeys, r, sbase + L::off_k + t * L::k_bytes, L::k_bytes,
+                  bar(BAR_K_FULL + t));
     }
     __syncwarp();
   } else if (warp == kQk) {
@@ -237,46 +246,49 @@ q8_few_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
 
   // -------------------------------------------------------------- widening
   else if (warp >= kWide) {
-    const int tree_at = max(n_pre - 2, 0);     // the tree's keys are made two tiles early
+    const int tree_at = max(n_pre - 2, 0) & ~1; // the tree's keys are made two tiles early
     bool ok = true;
-    for (int t0 = 0; ok && t0 < ntiles; t0 += kDepth) {
-#pragma unroll
-      for (int i = 0; i < kDepth; ++i) {       // (constant register indexes)
-        const int t = t0 + i, st = t & 1;
-        if (t >= ntiles) break;
-        if (with_tree && t == tree_at) {
-          const int s0 = n_pre, s1 = n_pre + 1;
-          if ((s0 >= kRing && !__all_sync(kFull, mbar_wait(bar(BAR_K_EMPTY + s0 % kRing),
-                                                           (s0 / kRing - 1) & 1))) ||
-              (s1 >= kRing && !__all_sync(kFull, mbar_wait(bar(BAR_K_EMPTY + s1 % kRing),
-                                                           (s1 / kRing - 1) & 1)))) {
-            ok = false;
-            break;
-          }
-          tree_keys<D>(a, b, hk, wt, kWideThreads, kt_in, smem + L::off_k + (s0 % kRing) * L::k_bytes,
-                       smem + L::off_k + (s1 % kRing) * L::k_bytes);
-          asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar(BAR_T_FULL));
-        }
-        if (t >= 2 && !__all_sync(kFull, mbar_wait(bar(BAR_V_EMPTY + st), ((t >> 1) - 1) & 1))) {
-          ok = false;
-          break;
-        }
-        uint8_t* const stage = smem + L::off_v + st * kTile;
-        if (t < n_pre) {
-          share.widen(vreg[i], stage);
-        } else {
-          tree_values<D>(a, b, hk, wt, kWideThreads, vt_in, stage);
-        }
+    auto stage_free = [&](int t) {
+      return t < 2 || __all_sync(kFull, mbar_wait(bar(BAR_V_EMPTY + (t & 1)), ((t >> 1) - 1) & 1));
+    };
+    auto stage_written = [&](int t) {
+      asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(BAR_V_FULL + (t & 1)));
+    };
+    for (int t0 = 0; ok && t0 < max(n_pre, 1); t0 += kDepth) {
+      if (with_tree && t0 == tree_at) {
+        const int s0 = n_pre, s1 = n_pre + 1;
+        ok = (s0 < kRing || __all_sync(kFull, mbar_wait(bar(BAR_K_EMPTY + s0 % kRing),
+                                                        (s0 / kRing - 1) & 1))) &&
+             (s1 < kRing || __all_sync(kFull, mbar_wait(bar(BAR_K_EMPTY + s1 % kRing),
+                                                        (s1 / kRing - 1) & 1)));
+        if (!ok) break;
+        tree_keys<D>(a, b, hk, wt, kWideThreads, kt_in,
+                     smem + L::off_k + (s0 % kRing) * L::k_bytes,
+                     smem + L::off_k + (s1 % kRing) * L::k_bytes);
         asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(BAR_V_FULL + st));
+        if (lane == 0) mbar_arrive(bar(BAR_T_FULL));
+      }
+#pragma unroll
+      for (int i = 0; i < kDepth; ++i) {       // (constant register indexes)
+        const int t = t0 + i;
+        if (t >= n_pre) break;
+        ok = stage_free(t);
+        if (!ok) break;
+        share.widen(vreg[i], smem + L::off_v + (t & 1) * kTile);
+        stage_written(t);
         if (t + kDepth < n_pre) load_v(vreg[i], tile_row[t + kDepth], valid_of(t + kDepth));
-        if (__any_sync(kFull, flags[1] != 0)) {
-          ok = false;
-          break;
-        }
+        ok = !__any_sync(kFull, flags[1] != 0);
+        if (!ok) break;
+      }
+    }
+    if (with_tree && ok) {
+      ok = stage_free(n_pre);
+      if (ok) {
+        tree_values<D>(a, b, hk, wt, kWideThreads, vt_in, smem + L::off_v + (n_pre & 1) * kTile);
+        stage_written(n_pre);
       }
     }
     if (!ok) flags[1] = 1;
@@ -523,9 +535,30 @@ q8_few_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
         : "r"((uint32_t)(!ok || flags[1] != 0))
         : "memory");
     if (stop == 0) {
+      // a thread per column: the streams' shares, and where the column goes
       const float unit = pow2i(U);
-      const float* const ms = (const float*)(smem + L::off_m);
-      const float* const ls = (const float*)(smem + L::off_l);
+      float* const share0 = (float*)(smem + L::off_alpha);
+      long long* const to = (long long*)rmask;
+      if (tid < a.M) {
+        const float* const ms = (const float*)(smem + L::off_m);
+        const float* const ls = (const float*)(smem + L::off_l);
+        const float m0 = ms[tid], m1 = ms[N + tid], top = fmaxf(m0, m1);
+        // (a NaN sum stays one)
+        const float w0 = m0 == -INFINITY ? (ls[tid] != ls[tid] ? ls[tid] : 0.f) : ex2(m0 - top);
+        const float w1 = m1 == -INFINITY ? (ls[N + tid] != ls[N + tid] ? ls[N + tid] : 0.f) : ex2(m1 - top);
+        const float total = w0 * ls[tid] + w1 * ls[N + tid];
+        const float inv = pow2i(-kHeadroom) / total;
+        share0[tid] = w0 * inv;
+        share0[N + tid] = w1 * inv;
+        const float lse2 = top + log2f(total);
+        const int tr = tid / a.g, qh = hk * a.g + tid % a.g;
+        const long orow = ((long)b * a.R + tr) * a.Hq + qh;
+        const long prow = (((long)b * a.Hq + qh) * a.R + tr) * a.nsplit + sp;
+        to[tid] = (nsb == 1 ? orow : prow) * D;
+        if (nsb == 1) a.lse[orow] = lse2 * 0.69314718055994531f;
+        else a.part_meta[prow] = make_float2(lse2, unit);
+      }
+      asm volatile("bar.sync 3, 256;\n" ::: "memory");
       // O^T lane = dim; stream p writes the octets of columns of its parity.  A
       // split's output, over 2^U, is a mean of numbers of magnitude < 512: fp16
       // holds it to 2^-12.
@@ -538,27 +571,11 @@ q8_few_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           const int col = u + e;
-          if (col >= a.M) break;
-          const float m0 = ms[col], m1 = ms[N + col], top = fmaxf(m0, m1);
-          // (a NaN sum stays one)
-          const float w0 = m0 == -INFINITY ? (ls[col] != ls[col] ? ls[col] : 0.f) : ex2(m0 - top);
-          const float w1 = m1 == -INFINITY ? (ls[N + col] != ls[N + col] ? ls[N + col] : 0.f) : ex2(m1 - top);
-          const float total = w0 * ls[col] + w1 * ls[N + col];
-          const float inv = pow2i(-kHeadroom) / total;
-          float res = o0[e] * (w0 * inv);
-          if (ntiles > 1) res += o1[e] * (w1 * inv);
-          const int tr = col / a.g, qh = hk * a.g + col % a.g;
-          const long orow = ((long)b * a.R + tr) * a.Hq + qh;
-          const long prow = (((long)b * a.Hq + qh) * a.R + tr) * a.nsplit + sp;
-          if (key < D) {
-            if (nsb == 1) ((__nv_bfloat16*)a.out)[orow * D + key] = __float2bfloat16_rn(res * unit);
-            else ((__half*)a.part_o)[prow * D + key] = __float2half_rn(res);
-          }
-          if (key == 0) {
-            const float lse2 = top + log2f(total);
-            if (nsb == 1) a.lse[orow] = lse2 * 0.69314718055994531f;
-            else a.part_meta[prow] = make_float2(lse2, unit);
-          }
+          if (col >= a.M || key >= D) break;
+          float res = o0[e] * share0[col];
+          if (ntiles > 1) res += o1[e] * share0[N + col];
+          if (nsb == 1) ((__nv_bfloat16*)a.out)[to[col] + key] = __float2bfloat16_rn(res * unit);
+          else ((__half*)a.part_o)[to[col] + key] = __float2half_rn(res);
         }
       }
     }

@@ -95,6 +95,7 @@ struct RowLayout {
   static constexpr uint32_t off_top = off_flags + 8;                   // int[kWideWarps]
   static constexpr uint32_t total = off_top + 4 * kWideWarps;
   static_assert(total + 1024 <= 232448, "shared memory budget");
+  static_assert(kTreeBytes<D> <= v_bytes && kStages > 1, "the scan's rows");
 };
 
 // FULL: the copy landed, the warps wrote or the product is done; EMPTY: read by
@@ -196,11 +197,12 @@ q8_rows_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
 
   if (warp >= kWide) {
     // the first V tile, the exponents and rows of the split's tiles, the scratch rows
-    TreeScan<D, kWideThreads> tree;
+    if (with_tree) tree_fetch<D, kWideThreads>(a, b, hk, wt, sbase + L::off_v, L::v_bytes);
     const long r0 = n_pre > 0 ? a.map.row(b, hk, k0) : -1;
     const long rt = wt < n_pre ? a.map.row(b, hk, k0 + wt * kKeys) : -1;
     if (n_pre > 0) load_v(r0, valid_of(0));
     int top = -1000;
+#pragma unroll 1
     for (int t = wt; t < n_pre; t += kWideThreads) {
       const int pos = k0 + t * kKeys;
       const long r = t == wt ? rt : a.map.row(b, hk, pos);
@@ -217,8 +219,9 @@ q8_rows_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
       vex[2 * t + 1] = (uint8_t)vb;
       top = max(top, max(va, vb) - 127);
     }
-    if (with_tree) tree.load(a, b, hk, wt);
-    if (with_tree) top = max(top, tree.finish(a, wt, kt_in, vt_in, kt_out, vt_u));
+    if (with_tree)
+      top = max(top, tree_scan<D, kWideThreads>(a, b, wt, smem + L::off_v, L::v_bytes, kt_in, vt_in,
+                                                kt_out, vt_u));
     top = __reduce_max_sync(kFull, top);
     if (lane == 0) s_top[warp - kWide] = top;
   } else if (warp < 8) {
@@ -248,16 +251,22 @@ q8_rows_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
       __syncwarp();
       asm volatile("bar.sync 2, %0;\n" ::"r"(64 * live_warps + 32) : "memory");   // (allocated)
       const uint32_t tq = flags[0] + kColQ + p * (D / 8) + ((uint32_t)(q * 32) << 16);
+      uint4 x[D / 16];                             // the stream's half
 #pragma unroll
+      for (int i = 0; i < D / 16; ++i) {
+        x[i] = p ? w[D / 16 + i] : w[i];
+        if (bad) x[i] = make_uint4(0u, 0u, 0u, 0u);
+      }
+#pragma unroll 1
       for (int c = 0; c < D / 32; ++c) {           // 16 elements: four columns of hi, four of lo
-        uint4 x[2] = {p ? w[D / 16 + 2 * c] : w[2 * c], p ? w[D / 16 + 2 * c + 1] : w[2 * c + 1]};
-        if (bad) x[0] = x[1] = make_uint4(0u, 0u, 0u, 0u);
         uint4 hi, lo;
-        split16(x, f, hi, lo);
+        split16({x[0], x[1]}, f, hi, lo);
         tmem_st4(tq + 4 * c, __uint_as_float(hi.x), __uint_as_float(hi.y), __uint_as_float(hi.z),
                  __uint_as_float(hi.w));
         tmem_st4(tq + D / 4 + 4 * c, __uint_as_float(lo.x), __uint_as_float(lo.y),
                  __uint_as_float(lo.z), __uint_as_float(lo.w));
+#pragma unroll
+        for (int i = 0; i + 2 < D / 16; ++i) x[i] = x[i + 2];
       }
       tmem_wait_st();
     }
@@ -286,6 +295,7 @@ q8_rows_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
       asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
     }
     __syncwarp();
+#pragma unroll 1
     for (int t = 0; t < kRing && t < n_pre; ++t) {
       const long r = __shfl_sync(kFull, row, t);
       if (lane == 0)
@@ -346,7 +356,8 @@ q8_rows_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
           flags[1] = 1;
           break;
         }
-        tree_keys<D>(a, b, hk, wt, kWideThreads, kt_in, smem + L::off_k + (s0 % kRing) * L::k_bytes,
+        tree_keys<D>(a, b, hk, wt, kWideThreads, kt_in,
+                     smem + L::off_k + (s0 % kRing) * L::k_bytes,
                      smem + L::off_k + (s1 % kRing) * L::k_bytes);
         asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
         __syncwarp();
@@ -461,14 +472,15 @@ q8_rows_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
     if (q < live_warps) {
       // The stream's product of the tile before: done before its P is written over
       // or its accumulator is rescaled.
+      bool done = true;
       auto product_done = [&](int t) -> bool {
-        return t == 0 || __all_sync(kFull, wait_ready(bar(BAR_PV_DONE + p), (t - 1) & 1));
+        return __all_sync(kFull, done || wait_ready(bar(BAR_PV_DONE + p), (t - 1) & 1));
       };
       // The maximum is raised to X where X passes m by the headroom (or m is none),
       // the sum and the accumulator are rescaled.
       auto raise = [&](float X, int t) -> bool {
         const bool need = !(X <= m + kOverflow);
-        if (!__any_sync(kFull, need)) return true;
+        if (__builtin_expect(!__any_sync(kFull, need), 1)) return true;
         if (!product_done(t)) return false;
         const float m_new = need ? fmaxf(m, X) : m;
         const float al = m_new == m ? 1.f : m == -INFINITY ? 0.f : ex2(m - m_new);
@@ -499,103 +511,144 @@ q8_rows_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
 
       const int h = p;                           // a stream takes one half of every tile
       const uint32_t ts = tmem + lane_off + 64u * h, tp = tmem + lane_off + kColP + 32u * p;
-      for (int t = 0; t < ntiles; ++t) {
-        const bool is_tree = t >= n_pre;
-        const int nvalid = is_tree ? a.R : valid_of(t);
-        if (!__all_sync(kFull, wait_ready(bar(BAR_S_FULL + p), t & 1))) {
-          failed = true;
-          break;
-        }
+      // what the next tile needs from shared memory is asked for a tile early
+      bool ready = false;                        // its scores
+      int ke = kex[h], ve = vex[h];              // its exponents
+      // The stream's product of the tile before is looked at, then this tile's scores.
+      auto scores_ready = [&](int t) -> bool {
+        if (t > 0) done = complete(bar(BAR_PV_DONE + p), (t - 1) & 1);
+        const bool ok = __all_sync(kFull, ready || wait_ready(bar(BAR_S_FULL + p), t & 1));
+        ready = false;
         fence_after();
-        const int nv = min(nvalid - 64 * h, 64);   // keys of this half
+        return ok;
+      };
+      auto weights_written = [&] {
+        tmem_wait_st();
+        fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(BAR_P_FULL + p));
+      };
+      // 64 keys of the prefix, in registers.  x = f v + off: a prefix block has one
+      // factor and one offset.  (f is not 0, so that -inf stays -inf; an offset below
+      // -60 puts P under fp16's range: its exact value does not matter, and the sum
+      // stays within fp32.)
+      auto block_factor = [&](int e) {
+        const float f = c2 * q8_scale(e);
+        return f == 0.f ? 1.17549435e-38f : f;
+      };
+      auto block_offset = [&](int e) { return max(e - 127 - U + kHeadroom, -60); };
+      auto full_half = [&](int t) -> bool {
+        if (!scores_ready(t)) return false;
         float v[64];
         tmem_ld32(ts, *(float(*)[32])v);
         tmem_ld32(ts + 32, *(float(*)[32])(v + 32));
         tmem_wait_ld();
         scores_read();
-        // x = f v + off.  A prefix block has one factor and one offset.  (Not 0, so
-        // that -inf stays -inf; an offset below -60 puts P under fp16's range: its
-        // exact value does not matter, and the sum stays within fp32.)
-        float f = 1.f;
-        int d = 0;
-        if (!is_tree) {
-          f = c2 * q8_scale(kex[2 * t + h]);
-          f = f == 0.f ? 1.17549435e-38f : f;
-          d = max((int)vex[2 * t + h] - 127 - U + kHeadroom, -60);
-          if (nv < 64) {
-#pragma unroll
-            for (int i = 0; i < 64; ++i)
-              if (i >= nv) v[i] = -INFINITY;
-          }
-        } else {
-          // scratch rows: a factor per key, and what this row sees (key 0: the root)
-          const uint64_t vis = nv <= 0 ? 0ull
-                               : (h == 0 ? (mask << 1) | 1ull : mask >> 63) & (~0ull >> (64 - nv));
-          const uint32_t vlo = (uint32_t)vis, vhi = (uint32_t)(vis >> 32);
-#pragma unroll
-          for (int i = 0; i < 64; i += 4) {
-            const float4 k4 = *(const float4*)(kt_out + 64 * h + i);
-            const float kf[4] = {k4.x, k4.y, k4.z, k4.w};
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const uint32_t word = i + j < 32 ? vlo : vhi;
-              const bool sees = (word >> ((i + j) & 31)) & 1u;
-              v[i + j] = sees ? v[i + j] * (c2 * kf[j]) : -INFINITY;
-            }
-          }
-        }
+        const float f = block_factor(ke);
+        const int d = block_offset(ve);
+        const int next = 2 * min(t + 1, kMaxTiles - 1) + h;
+        ke = kex[next];
+        ve = vex[next];
         float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
         for (int i = 0; i < 64; i += 8)
 #pragma unroll
           for (int j = 0; j < 4; ++j) top[j] = max3f(top[j], v[i + 2 * j], v[i + 2 * j + 1]);
-        if (!raise(f * fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])), t)) {
-          failed = true;
-          break;
-        }
+        if (!raise(f * fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])), t)) return false;
         const float off = (float)d - (m == -INFINITY ? 0.f : m);
         const float2 f2 = make_float2(f, f), o2 = make_float2(off, off);
         float2 sa = make_float2(0.f, 0.f), sb = sa;
-        auto weights = [&](auto scaled) {          // scaled: a factor per value row
 #pragma unroll
-          for (int c = 0; c < 64; c += 32) {
-            uint32_t w[16];                        // (32 exponentials hide the product's wait)
+        for (int c = 0; c < 64; c += 32) {
+          uint32_t w[16];                          // (32 exponentials hide the product's wait)
 #pragma unroll
-            for (int i = 0; i < 32; i += 4) {
-              const float2 xa = __ffma2_rn(make_float2(v[c + i], v[c + i + 1]), f2, o2);
-              const float2 xb = __ffma2_rn(make_float2(v[c + i + 2], v[c + i + 3]), f2, o2);
-              float2 pa = make_float2(ex2(xa.x), ex2(xa.y));
-              float2 pb = make_float2(ex2(xb.x), ex2(xb.y));
-              sa = __fadd2_rn(sa, pa);
-              sb = __fadd2_rn(sb, pb);
-              if constexpr (decltype(scaled)::value) {
-                const int4 u = *(const int4*)(vt_u + 64 * h + c + i);
-                pa.x *= pow2i(u.x - U + kHeadroom);
-                pa.y *= pow2i(u.y - U + kHeadroom);
-                pb.x *= pow2i(u.z - U + kHeadroom);
-                pb.y *= pow2i(u.w - U + kHeadroom);
-              }
-              w[i / 2] = pack_half2(pa.x, pa.y);
-              w[i / 2 + 1] = pack_half2(pb.x, pb.y);
-            }
-            if (c == 0) {
-              if (!product_done(t)) return false;
-              fence_after();
-            }
-            tmem_st16(tp + c / 2, w);
+          for (int i = 0; i < 32; i += 4) {
+            const float2 xa = __ffma2_rn(make_float2(v[c + i], v[c + i + 1]), f2, o2);
+            const float2 xb = __ffma2_rn(make_float2(v[c + i + 2], v[c + i + 3]), f2, o2);
+            const float2 pa = make_float2(ex2(xa.x), ex2(xa.y));
+            const float2 pb = make_float2(ex2(xb.x), ex2(xb.y));
+            sa = __fadd2_rn(sa, pa);
+            sb = __fadd2_rn(sb, pb);
+            w[i / 2] = pack_half2(pa.x, pa.y);
+            w[i / 2 + 1] = pack_half2(pb.x, pb.y);
           }
-          return true;
-        };
-        if (!(is_tree ? weights(std::true_type{}) : weights(std::false_type{}))) {
-          failed = true;
-          break;
+          if (c == 0) {
+            if (!product_done(t)) return false;
+            fence_after();
+          }
+          tmem_st16(tp + c / 2, w);
+          if (c == 0) ready = complete(bar(BAR_S_FULL + p), (t + 1) & 1);
         }
         l = fmaf((sa.x + sa.y) + (sb.x + sb.y), pow2i(-d), l);
-        tmem_wait_st();
-        fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(BAR_P_FULL + p));
-      }
+        weights_written();
+        return true;
+      };
+      // Every other half, once or twice per CTA: a prefix's last keys, or the scratch
+      // rows, with a factor per key and value row and what this row sees (key 0: the
+      // root).  Code of its own, so that the loop over full halves stays small.
+      auto odd_half = [&](int t) -> bool {
+        if (!scores_ready(t)) return false;
+        float v[64];
+        tmem_ld32(ts, *(float(*)[32])v);
+        tmem_ld32(ts + 32, *(float(*)[32])(v + 32));
+        tmem_wait_ld();
+        scores_read();
+        const bool is_tree = t >= n_pre;
+        const int nv = min((is_tree ? a.R : valid_of(t)) - 64 * h, 64);
+        const uint64_t sees = !is_tree ? ~0ull : h == 0 ? (mask << 1) | 1ull : mask >> 63;
+        const uint64_t vis = nv <= 0 ? 0ull : sees & (~0ull >> (64 - nv));
+        const uint32_t vlo = (uint32_t)vis, vhi = (uint32_t)(vis >> 32);
+        const float f = is_tree ? c2 : block_factor(ke);
+        const int d = is_tree ? 0 : block_offset(ve);
+        const int next = 2 * min(t + 1, kMaxTiles - 1) + h;
+        ke = kex[next];
+        ve = vex[next];
+        float top = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < 64; i += 4) {
+          float4 k4 = make_float4(1.f, 1.f, 1.f, 1.f);
+          if (is_tree) k4 = *(const float4*)(kt_out + 64 * h + i);
+          const float kf[4] = {k4.x, k4.y, k4.z, k4.w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint32_t word = i + j < 32 ? vlo : vhi;
+            v[i + j] = (word >> ((i + j) & 31)) & 1u ? v[i + j] * (f * kf[j]) : -INFINITY;
+          }
+          top = max3f(max3f(top, v[i], v[i + 1]), v[i + 2], v[i + 3]);
+        }
+        if (!raise(top, t) || !product_done(t)) return false;
+        fence_after();
+        const float off = (float)d - (m == -INFINITY ? 0.f : m);
+        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int c = 0; c < 64; c += 32) {
+          uint32_t w[16];
+#pragma unroll
+          for (int i = 0; i < 32; i += 4) {
+            float x[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              x[j] = ex2(v[c + i + j] + off);
+              sum[j] += x[j];
+            }
+            if (is_tree) {
+              const int4 u = *(const int4*)(vt_u + 64 * h + c + i);
+              x[0] *= pow2i(u.x - U + kHeadroom);
+              x[1] *= pow2i(u.y - U + kHeadroom);
+              x[2] *= pow2i(u.z - U + kHeadroom);
+              x[3] *= pow2i(u.w - U + kHeadroom);
+            }
+            w[i / 2] = pack_half2(x[0], x[1]);
+            w[i / 2 + 1] = pack_half2(x[2], x[3]);
+          }
+          tmem_st16(tp + c / 2, w);
+        }
+        l = fmaf((sum[0] + sum[1]) + (sum[2] + sum[3]), pow2i(-d), l);
+        weights_written();
+        return true;
+      };
+      for (int t = 0; t < ntiles && !failed; ++t)
+        failed = !(t < n_pre && valid_of(t) >= 64 * (h + 1) ? full_half(t) : odd_half(t));
     }
 
     // ------------------------------------- epilogue: the two streams joined

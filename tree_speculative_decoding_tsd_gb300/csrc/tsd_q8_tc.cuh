@@ -32,6 +32,19 @@ __device__ __forceinline__ bool wait_ready(uint32_t bar, uint32_t parity) {
       : "memory");
   return ok || mbar_wait(bar, parity);
 }
+// Whether a phase is complete, looked at early: an access to shared memory takes about
+// 300 cycles while widened tiles are stored and products read theirs, which a warp
+// spends on other work.
+__device__ __forceinline__ bool complete(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+      " selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok;
+}
 // One lane of a converged warp.  A warp that issues products runs its loop on all
 // lanes, so that descriptors and addresses are uniform values, and issues on this
 // lane.
@@ -179,83 +192,85 @@ __device__ __forceinline__ void WideShare<W, T>::widen(const uint4 (&r)[kCount],
   }
 }
 
-// Scratch rows of (request b, head hk), eight lanes of the N threads per row: loaded
-// early, looked at later.
-template <int D, int N>
-struct TreeScan {
-  static constexpr int NV = D / 64;    // 16-byte vectors per lane and row
-  static constexpr int kRounds = (65 * 8 + N - 1) / N;
-  uint4 kw[kRounds][NV], vw[kRounds][NV];
-  uint32_t lo, hi;                     // rows that this lane's tree rows see
+// Scratch rows of (request b, head hk) in shared memory for the scan, [65][D] bf16: K
+// where the first widened tile will be, V at the second one (`apart` bytes on).  N
+// threads, eight per row; a thread scans what it copied itself.
+template <int D>
+constexpr uint32_t kTreeBytes = 65u * D * 2;
 
-  __device__ __forceinline__ void load(const Q8AttnArgs& a, int b, int hk, int wt) {
-    const int lane = threadIdx.x & 31;
-    lo = hi = 0;
+template <int D, int N>
+__device__ __forceinline__ void tree_fetch(const Q8AttnArgs& a, int b, int hk, int wt, uint32_t dst,
+                                           uint32_t apart) {
+#pragma unroll 1
+  for (int x = wt; x < a.R * 8; x += N) {
+    const int j = x >> 3, c = x & 7;
+    const long row = (((long)b * a.R + j) * a.map.Hkv + hk) * (D / 8) + c;
 #pragma unroll
-    for (int i = 0; i < 3; ++i) {
-      const int r = lane + 32 * i;
-      const uint64_t m = r > 0 && r < a.R ? a.mask[(long)b * a.R + r] : 0ull;
-      lo |= (uint32_t)m;
-      hi |= (uint32_t)(m >> 32);
-    }
-#pragma unroll
-    for (int i = 0; i < kRounds; ++i) {
-      const int x = wt + N * i, j = x >> 3, c = x & 7;
-#pragma unroll
-      for (int v = 0; v < NV; ++v) {
-        kw[i][v] = vw[i][v] = make_uint4(0u, 0u, 0u, 0u);
-        if (j < a.R) {
-          const long row = (((long)b * a.R + j) * a.map.Hkv + hk) * (D / 8) + c * NV + v;
-          kw[i][v] = __ldg((const uint4*)a.kt + row);
-          vw[i][v] = __ldg((const uint4*)a.vt + row);
-        }
-      }
+    for (int v = 0; v < D / 64; ++v) {
+      const uint32_t to = dst + (uint32_t)(j * (D / 8) + c + 8 * v) * 16u;
+      cp_async16(to, (const uint4*)a.kt + row + 8 * v, true);
+      cp_async16(to + apart, (const uint4*)a.vt + row + 8 * v, true);
     }
   }
-  // Which rows some row sees, their factors, and (returned) this thread's largest
-  // exponent of a value row.
-  __device__ __forceinline__ int finish(const Q8AttnArgs& a, int wt, float* kt_in, float* vt_in,
-                                        float* kt_out, int* vt_u) const {
-    const uint64_t seen =
-        ((uint64_t)__reduce_or_sync(kFull, hi) << 32) | __reduce_or_sync(kFull, lo);
-    int best = -1000;
+  asm volatile("cp.async.commit_group;\n" ::: "memory");
+}
+
+// Which rows some row sees, their factors, and (returned) this thread's largest
+// exponent of a value row.
+template <int D, int N>
+__device__ __forceinline__ int tree_scan(const Q8AttnArgs& a, int b, int wt, const uint8_t* rows,
+                                         uint32_t apart, float* kt_in, float* vt_in, float* kt_out, int* vt_u) {
+  const int lane = threadIdx.x & 31;
+  uint32_t lo = 0, hi = 0;
 #pragma unroll
-    for (int i = 0; i < kRounds; ++i) {
-      const int x = wt + N * i, j = x >> 3, c = x & 7;
-      uint32_t kt = 0, vt = 0;
-#pragma unroll
-      for (int v = 0; v < NV; ++v) {
-        kt = top_pairs(kt, kw[i][v]);
-        vt = top_pairs(vt, vw[i][v]);
-      }
-      kt = top_of(kt);
-      vt = top_of(vt);
-#pragma unroll
-      for (int o = 4; o > 0; o >>= 1) {
-        kt = max(kt, __shfl_xor_sync(kFull, kt, o));
-        vt = max(vt, __shfl_xor_sync(kFull, vt, o));
-      }
-      if (j >= a.R) continue;
-      const bool live = j == 0 || ((seen >> (j - 1)) & 1ull);
-      const bool bad = kt >= 0x7f800000u || vt >= 0x7f800000u;
-      const int ek = row_exponent(kt), ev = row_exponent(vt);
-      if (c == 0) {
-        // K: 2^(7 - (e - 127)) and its inverse; V: 2^(8 - (e - 127))
-        kt_in[j] = live && !bad ? q8_scale(261 - ek) : 0.f;
-        vt_in[j] = live && !bad ? q8_scale(262 - ev) : 0.f;
-        kt_out[j] = bad ? __int_as_float(0x7fffffff) : q8_scale(ek - 7);
-        vt_u[j] = live && !bad ? ev - 135 : -900;
-      }
-      if (live && !bad) best = max(best, ev - 135);
-    }
-    for (int j = a.R + wt; j < kKeys; j += N) {      // rows that do not exist
-      kt_in[j] = vt_in[j] = 0.f;
-      kt_out[j] = 1.f;
-      vt_u[j] = -900;
-    }
-    return best;
+  for (int i = 0; i < 3; ++i) {
+    const int r = lane + 32 * i;
+    const uint64_t m = r > 0 && r < a.R ? a.mask[(long)b * a.R + r] : 0ull;
+    lo |= (uint32_t)m;
+    hi |= (uint32_t)(m >> 32);
   }
-};
+  asm volatile("cp.async.wait_group 0;\n" ::: "memory");
+  const uint64_t seen = ((uint64_t)__reduce_or_sync(kFull, hi) << 32) | __reduce_or_sync(kFull, lo);
+  int best = -1000;
+#pragma unroll 1
+  for (int x0 = wt - lane; x0 < a.R * 8; x0 += N) {  // (whole warps)
+    const int j = (x0 + lane) >> 3, c = lane & 7;
+    uint32_t kt = 0, vt = 0;
+    if (j < a.R) {
+      const uint4* p = (const uint4*)rows + j * (D / 8) + c;
+#pragma unroll
+      for (int v = 0; v < D / 64; ++v) {
+        kt = top_pairs(kt, p[8 * v]);
+        vt = top_pairs(vt, p[8 * v + apart / 16]);
+      }
+    }
+    kt = top_of(kt);
+    vt = top_of(vt);
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) {
+      kt = max(kt, __shfl_xor_sync(kFull, kt, o));
+      vt = max(vt, __shfl_xor_sync(kFull, vt, o));
+    }
+    if (j >= a.R) continue;
+    const bool live = j == 0 || ((seen >> (j - 1)) & 1ull);
+    const bool bad = kt >= 0x7f800000u || vt >= 0x7f800000u;
+    const int ek = row_exponent(kt), ev = row_exponent(vt);
+    if (c == 0) {
+      // K: 2^(7 - (e - 127)) and its inverse; V: 2^(8 - (e - 127))
+      kt_in[j] = live && !bad ? q8_scale(261 - ek) : 0.f;
+      vt_in[j] = live && !bad ? q8_scale(262 - ev) : 0.f;
+      kt_out[j] = bad ? __int_as_float(0x7fffffff) : q8_scale(ek - 7);
+      vt_u[j] = live && !bad ? ev - 135 : -900;
+    }
+    if (live && !bad) best = max(best, ev - 135);
+  }
+  for (int j = a.R + wt; j < kKeys; j += N) {        // rows that do not exist (N > 128)
+    kt_in[j] = vt_in[j] = 0.f;
+    kt_out[j] = 1.f;
+    vt_u[j] = -900;
+  }
+  return best;
+}
 
 // The packed rows of a row group as hi + lo (n_rows of them, zeros behind the
 // last one) with their score factors: D / 16 lanes of the n threads per row.
@@ -264,6 +279,7 @@ __device__ __forceinline__ void stage_q(const Q8AttnArgs& a, int b, int hk, int 
                                         int rows_here, int n_rows, int tid, int n, uint8_t* hi_tile,
                                         uint8_t* lo_tile, float* c2v) {
   constexpr int QL = D / 16;
+#pragma unroll 1
   for (int x = tid; x < n_rows * QL; x += n) {       // (whole warps: n_rows is a multiple of 16)
     const int r = x / QL, c = x % QL;
     uint4 w[2] = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
@@ -297,6 +313,7 @@ __device__ __forceinline__ void stage_q(const Q8AttnArgs& a, int b, int hk, int 
 template <int D>
 __device__ __forceinline__ void tree_keys(const Q8AttnArgs& a, int b, int hk, int wt, int n,
                                           const float* kt_in, uint8_t* hi_tile, uint8_t* lo_tile) {
+#pragma unroll 1
   for (int x = wt; x < kKeys * (D / 16); x += n) {
     const int row = x / (D / 16), u = x % (D / 16);
     uint4 hi = make_uint4(0u, 0u, 0u, 0u), lo = hi;
@@ -314,6 +331,7 @@ __device__ __forceinline__ void tree_keys(const Q8AttnArgs& a, int b, int hk, in
 template <int D>
 __device__ __forceinline__ void tree_values(const Q8AttnArgs& a, int b, int hk, int wt, int n,
                                             const float* vt_in, uint8_t* stage) {
+#pragma unroll 2
   for (int x = wt; x < kKeys * (D / 8); x += n) {
     const int row = x / (D / 8), u = x % (D / 8);
     const float f = vt_in[row];
@@ -325,6 +343,10 @@ __device__ __forceinline__ void tree_values(const Q8AttnArgs& a, int b, int hk, 
   }
 }
 
+// n / d, exact and below 2^31: a function of its own, because an inlined 64-bit division
+// is 100 instructions.
+__device__ __noinline__ int quotient(long long n, int d) { return (int)(n / d); }
+
 // The K tile of positions pos.. by TMA (cache row `row`, for a paged cache).  A
 // tile behind the cache's or page's last row reads zeros there; rows behind the
 // prefix are masked later, whatever they hold; the rows of a missing page are
@@ -334,9 +356,8 @@ __device__ __forceinline__ void load_keys(const Q8AttnArgs& a, const CUtensorMap
                                           uint32_t bytes, uint32_t full) {
   int y = pos, z = b * a.map.Hkv + hk;
   if (a.map.page_size) {
-    const long long r = row < 0 ? 0 : row;
-    y = (int)(r % a.map.page_size);
-    z = (int)(r / a.map.page_size);
+    y = (int)((uint32_t)pos % (uint32_t)a.map.page_size);
+    z = row < 0 ? 0 : quotient(row - y, a.map.page_size);
   }
   mbar_expect_tx(full, bytes);
   tma_3d(dst, &kmap, 0, y, z, full);
