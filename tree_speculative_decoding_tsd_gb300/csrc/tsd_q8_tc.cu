@@ -514,41 +514,53 @@ q8_rows_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
       // what the next tile needs from shared memory is asked for a tile early
       bool ready = false;                        // its scores
       int ke = kex[h], ve = vex[h];              // its exponents
-      // The stream's product of the tile before is looked at, then this tile's scores.
-      auto scores_ready = [&](int t) -> bool {
+      // (the scratch rows' tile has code of its own: the loop over the prefix stays small)
+      auto tile = [&](int t, auto tree) -> bool {
+        constexpr bool is_tree = decltype(tree)::value;
+        const int nvalid = is_tree ? a.R : valid_of(t);
         if (t > 0) done = complete(bar(BAR_PV_DONE + p), (t - 1) & 1);
-        const bool ok = __all_sync(kFull, ready || wait_ready(bar(BAR_S_FULL + p), t & 1));
-        ready = false;
+        if (!__all_sync(kFull, ready || wait_ready(bar(BAR_S_FULL + p), t & 1))) return false;
         fence_after();
-        return ok;
-      };
-      auto weights_written = [&] {
-        tmem_wait_st();
-        fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(BAR_P_FULL + p));
-      };
-      // 64 keys of the prefix, in registers.  x = f v + off: a prefix block has one
-      // factor and one offset.  (f is not 0, so that -inf stays -inf; an offset below
-      // -60 puts P under fp16's range: its exact value does not matter, and the sum
-      // stays within fp32.)
-      auto block_factor = [&](int e) {
-        const float f = c2 * q8_scale(e);
-        return f == 0.f ? 1.17549435e-38f : f;
-      };
-      auto block_offset = [&](int e) { return max(e - 127 - U + kHeadroom, -60); };
-      auto full_half = [&](int t) -> bool {
-        if (!scores_ready(t)) return false;
+        const int nv = min(nvalid - 64 * h, 64);   // keys of this half
         float v[64];
         tmem_ld32(ts, *(float(*)[32])v);
         tmem_ld32(ts + 32, *(float(*)[32])(v + 32));
         tmem_wait_ld();
         scores_read();
-        const float f = block_factor(ke);
-        const int d = block_offset(ve);
-        const int next = 2 * min(t + 1, kMaxTiles - 1) + h;
-        ke = kex[next];
-        ve = vex[next];
+        // x = f v + off.  A prefix block has one factor and one offset.  (Not 0, so
+        // that -inf stays -inf; an offset below -60 puts P under fp16's range: its
+        // exact value does not matter, and the sum stays within fp32.)
+        float f = 1.f;
+        int d = 0;
+        if constexpr (!is_tree) {
+          f = c2 * q8_scale(ke);
+          f = f == 0.f ? 1.17549435e-38f : f;
+          d = max(ve - 127 - U + kHeadroom, -60);
+          const int next = 2 * min(t + 1, kMaxTiles - 1) + h;
+          ke = kex[next];
+          ve = vex[next];
+          if (__builtin_expect(nv < 64, 0)) {
+#pragma unroll
+            for (int i = 0; i < 64; ++i)
+              if (i >= nv) v[i] = -INFINITY;
+          }
+        } else {
+          // scratch rows: a factor per key, and what this row sees (key 0: the root)
+          const uint64_t vis = nv <= 0 ? 0ull
+                               : (h == 0 ? (mask << 1) | 1ull : mask >> 63) & (~0ull >> (64 - nv));
+          const uint32_t vlo = (uint32_t)vis, vhi = (uint32_t)(vis >> 32);
+#pragma unroll
+          for (int i = 0; i < 64; i += 4) {
+            const float4 k4 = *(const float4*)(kt_out + 64 * h + i);
+            const float kf[4] = {k4.x, k4.y, k4.z, k4.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const uint32_t word = i + j < 32 ? vlo : vhi;
+              const bool sees = (word >> ((i + j) & 31)) & 1u;
+              v[i + j] = sees ? v[i + j] * (c2 * kf[j]) : -INFINITY;
+            }
+          }
+        }
         float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
         for (int i = 0; i < 64; i += 8)
@@ -558,97 +570,47 @@ q8_rows_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
         const float off = (float)d - (m == -INFINITY ? 0.f : m);
         const float2 f2 = make_float2(f, f), o2 = make_float2(off, off);
         float2 sa = make_float2(0.f, 0.f), sb = sa;
+        auto weights = [&](auto scaled) {          // scaled: a factor per value row
 #pragma unroll
-        for (int c = 0; c < 64; c += 32) {
-          uint32_t w[16];                          // (32 exponentials hide the product's wait)
+          for (int c = 0; c < 64; c += 32) {
+            uint32_t w[16];                        // (32 exponentials hide the product's wait)
 #pragma unroll
-          for (int i = 0; i < 32; i += 4) {
-            const float2 xa = __ffma2_rn(make_float2(v[c + i], v[c + i + 1]), f2, o2);
-            const float2 xb = __ffma2_rn(make_float2(v[c + i + 2], v[c + i + 3]), f2, o2);
-            const float2 pa = make_float2(ex2(xa.x), ex2(xa.y));
-            const float2 pb = make_float2(ex2(xb.x), ex2(xb.y));
-            sa = __fadd2_rn(sa, pa);
-            sb = __fadd2_rn(sb, pb);
-            w[i / 2] = pack_half2(pa.x, pa.y);
-            w[i / 2 + 1] = pack_half2(pb.x, pb.y);
+            for (int i = 0; i < 32; i += 4) {
+              const float2 xa = __ffma2_rn(make_float2(v[c + i], v[c + i + 1]), f2, o2);
+              const float2 xb = __ffma2_rn(make_float2(v[c + i + 2], v[c + i + 3]), f2, o2);
+              float2 pa = make_float2(ex2(xa.x), ex2(xa.y));
+              float2 pb = make_float2(ex2(xb.x), ex2(xb.y));
+              sa = __fadd2_rn(sa, pa);
+              sb = __fadd2_rn(sb, pb);
+              if constexpr (decltype(scaled)::value) {
+                const int4 u = *(const int4*)(vt_u + 64 * h + c + i);
+                pa.x *= pow2i(u.x - U + kHeadroom);
+                pa.y *= pow2i(u.y - U + kHeadroom);
+                pb.x *= pow2i(u.z - U + kHeadroom);
+                pb.y *= pow2i(u.w - U + kHeadroom);
+              }
+              w[i / 2] = pack_half2(pa.x, pa.y);
+              w[i / 2 + 1] = pack_half2(pb.x, pb.y);
+            }
+            if (c == 0) {
+              if (!product_done(t)) return false;
+              fence_after();
+            }
+            tmem_st16(tp + c / 2, w);
+            if (c == 0) ready = complete(bar(BAR_S_FULL + p), (t + 1) & 1);
           }
-          if (c == 0) {
-            if (!product_done(t)) return false;
-            fence_after();
-          }
-          tmem_st16(tp + c / 2, w);
-          if (c == 0) ready = complete(bar(BAR_S_FULL + p), (t + 1) & 1);
-        }
+          return true;
+        };
+        if (!weights(tree)) return false;
         l = fmaf((sa.x + sa.y) + (sb.x + sb.y), pow2i(-d), l);
-        weights_written();
+        tmem_wait_st();
+        fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(BAR_P_FULL + p));
         return true;
       };
-      // Every other half, once or twice per CTA: a prefix's last keys, or the scratch
-      // rows, with a factor per key and value row and what this row sees (key 0: the
-      // root).  Code of its own, so that the loop over full halves stays small.
-      auto odd_half = [&](int t) -> bool {
-        if (!scores_ready(t)) return false;
-        float v[64];
-        tmem_ld32(ts, *(float(*)[32])v);
-        tmem_ld32(ts + 32, *(float(*)[32])(v + 32));
-        tmem_wait_ld();
-        scores_read();
-        const bool is_tree = t >= n_pre;
-        const int nv = min((is_tree ? a.R : valid_of(t)) - 64 * h, 64);
-        const uint64_t sees = !is_tree ? ~0ull : h == 0 ? (mask << 1) | 1ull : mask >> 63;
-        const uint64_t vis = nv <= 0 ? 0ull : sees & (~0ull >> (64 - nv));
-        const uint32_t vlo = (uint32_t)vis, vhi = (uint32_t)(vis >> 32);
-        const float f = is_tree ? c2 : block_factor(ke);
-        const int d = is_tree ? 0 : block_offset(ve);
-        const int next = 2 * min(t + 1, kMaxTiles - 1) + h;
-        ke = kex[next];
-        ve = vex[next];
-        float top = -INFINITY;
-#pragma unroll
-        for (int i = 0; i < 64; i += 4) {
-          float4 k4 = make_float4(1.f, 1.f, 1.f, 1.f);
-          if (is_tree) k4 = *(const float4*)(kt_out + 64 * h + i);
-          const float kf[4] = {k4.x, k4.y, k4.z, k4.w};
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const uint32_t word = i + j < 32 ? vlo : vhi;
-            v[i + j] = (word >> ((i + j) & 31)) & 1u ? v[i + j] * (f * kf[j]) : -INFINITY;
-          }
-          top = max3f(max3f(top, v[i], v[i + 1]), v[i + 2], v[i + 3]);
-        }
-        if (!raise(top, t) || !product_done(t)) return false;
-        fence_after();
-        const float off = (float)d - (m == -INFINITY ? 0.f : m);
-        float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int c = 0; c < 64; c += 32) {
-          uint32_t w[16];
-#pragma unroll
-          for (int i = 0; i < 32; i += 4) {
-            float x[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              x[j] = ex2(v[c + i + j] + off);
-              sum[j] += x[j];
-            }
-            if (is_tree) {
-              const int4 u = *(const int4*)(vt_u + 64 * h + c + i);
-              x[0] *= pow2i(u.x - U + kHeadroom);
-              x[1] *= pow2i(u.y - U + kHeadroom);
-              x[2] *= pow2i(u.z - U + kHeadroom);
-              x[3] *= pow2i(u.w - U + kHeadroom);
-            }
-            w[i / 2] = pack_half2(x[0], x[1]);
-            w[i / 2 + 1] = pack_half2(x[2], x[3]);
-          }
-          tmem_st16(tp + c / 2, w);
-        }
-        l = fmaf((sum[0] + sum[1]) + (sum[2] + sum[3]), pow2i(-d), l);
-        weights_written();
-        return true;
-      };
-      for (int t = 0; t < ntiles && !failed; ++t)
-        failed = !(t < n_pre && valid_of(t) >= 64 * (h + 1) ? full_half(t) : odd_half(t));
+      for (int t = 0; t < n_pre && !failed; ++t) failed = !tile(t, std::false_type{});
+      if (with_tree && !failed) failed = !tile(n_pre, std::true_type{});
     }
 
     // ------------------------------------- epilogue: the two streams joined
