@@ -139,9 +139,8 @@ q8_latent_kernel(const __grid_constant__ LatentMaps maps, const __grid_constant_
     const int t = g / kPieces, j = g - t * kPieces, sl = g % kSlots;
     int y = k0 + t * kKeys, z = b * a.map.Hkv + hk;
     if (a.map.page_size) {
-      const long long r = row < 0 ? 0 : row;
-      y = (int)(r % a.map.page_size);
-      z = (int)(r / a.map.page_size);
+      y = (int)((uint32_t)y % (uint32_t)a.map.page_size);
+      z = row < 0 ? 0 : quotient(row - y, a.map.page_size);
     }
     const uint32_t dst = sbase + kOffK + sl * kPiece, full = bar(BAR_K_FULL + sl);
     mbar_expect_tx(full, j < 4 ? kPiece : kPiece / 2);
@@ -154,6 +153,7 @@ q8_latent_kernel(const __grid_constant__ LatentMaps maps, const __grid_constant_
     const long r0 = n_pre > 0 ? a.map.row(b, hk, k0) : -1;
     if (n_pre > 0) load_v(r0, valid_of(0), 0);
     int top = -1000;
+#pragma unroll 1
     for (int t = wt; t < n_pre; t += kWideThreads) {
       const int pos = k0 + t * kKeys;
       const long r = a.map.row(b, hk, pos);
@@ -311,6 +311,7 @@ q8_latent_kernel(const __grid_constant__ LatentMaps maps, const __grid_constant_
     for (int t = 0; ok && t < ntiles; ++t) {
       if (with_tree && t == tree_at) {
         // the scratch rows' keys, hi pieces then lo pieces, through the K ring
+#pragma unroll 1
         for (int i = 0; i < 2 * kPieces; ++i) {
           const int g = kPieces * n_pre + i, sl = g % kSlots;
           if (g >= kSlots &&
@@ -319,6 +320,7 @@ q8_latent_kernel(const __grid_constant__ LatentMaps maps, const __grid_constant_
             break;
           }
           const int j = i % kPieces, units = j < 4 ? 8 : 4;
+#pragma unroll 1
           for (int x = wt; x < kKeys * units; x += kWideThreads) {
             const int r = x / units, u = x % units;
             uint4 hi = make_uint4(0u, 0u, 0u, 0u), lo = hi;
@@ -337,6 +339,7 @@ q8_latent_kernel(const __grid_constant__ LatentMaps maps, const __grid_constant_
         }
         if (!ok) break;
       }
+#pragma unroll 1
       for (int u = 0; u < kUnits; ++u) {
         const int g = kUnits * t + u, st = g & 1;
         if (g >= 2 && !__all_sync(kFull, mbar_wait(bar(BAR_V_EMPTY + st), ((g >> 1) - 1) & 1))) {
@@ -347,6 +350,7 @@ q8_latent_kernel(const __grid_constant__ LatentMaps maps, const __grid_constant_
         if (t < n_pre) {
           share.widen(vreg, stage);
         } else {
+#pragma unroll 2
           for (int x = wt; x < kKeys * 16; x += kWideThreads) {
             const int row = x >> 4, c = x & 15;
             const float f = vt_in[row];
