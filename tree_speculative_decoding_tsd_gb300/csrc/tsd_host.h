@@ -4,8 +4,6 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
-#include <atomic>
-
 #include "tsd.h"
 
 namespace tsd {
@@ -67,19 +65,6 @@ template <typename... KArgs, typename... Args>
 inline void launch_plain(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem,
                          cudaStream_t st, Args... args) {
   launch_with(false, kern, grid, block, smem, st, args...);
-}
-
-// Allow a kernel `bytes` of dynamic shared memory: one runtime call per kernel and
-// device (`done`: a mask of devices, kept by the caller beside the kernel).
-template <typename Kern>
-inline void allow_smem(Kern kern, size_t bytes, std::atomic<uint64_t>& done) {
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return;
-  const uint64_t bit = 1ull << (dev & 63);
-  if (dev < 64 && (done.load(std::memory_order_relaxed) & bit)) return;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) == cudaSuccess &&
-      dev < 64)
-    done.fetch_or(bit, std::memory_order_relaxed);
 }
 
 }  // namespace tsd

@@ -604,8 +604,7 @@ template <int D>
 void launch_few(const CUtensorMap& kmap, const Q8AttnArgs& a, const Q8Plan& p, cudaStream_t st) {
   const uint32_t smem = FewLayout<D>::total + 1024;
   const auto kern = q8_few_kernel<D>;
-  static std::atomic<uint64_t> done{0};
-  allow_smem(kern, smem, done);
+  cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   launch(kern, dim3(a.map.Hkv, p.nsplit, a.B), dim3(kThreads), smem, st, kmap, a);
 }
 

@@ -685,8 +685,8 @@ bool launch_q8_latent(const tsd_attn_desc& d, const Q8AttnArgs& a, const Q8Plan&
   if (encode_fn() == nullptr || !encode_keys(&m.wide, a, kDK, 128) ||
       !encode_keys(&m.last, a, kDK, 64))
     return false;
-  static std::atomic<uint64_t> done{0};
-  allow_smem(q8_latent_kernel, kTotal + 1024, done);
+  cudaFuncSetAttribute(q8_latent_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                       (int)kTotal + 1024);
   launch(q8_latent_kernel, dim3(p.nsplit, a.map.Hkv * p.nrg, a.B), dim3(kThreads), kTotal + 1024, st,
          m, a);
   return true;

@@ -690,8 +690,7 @@ template <int D>
 void launch_rows(const CUtensorMap& kmap, const Q8AttnArgs& a, const Q8Plan& p, cudaStream_t st) {
   const uint32_t smem = RowLayout<D>::total + 1024;
   const auto kern = q8_rows_kernel<D>;
-  static std::atomic<uint64_t> done{0};
-  allow_smem(kern, smem, done);
+  cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   launch(kern, dim3(a.map.Hkv * p.nrg, p.nsplit, a.B), dim3(kThreads), smem, st, kmap, a);
 }
 

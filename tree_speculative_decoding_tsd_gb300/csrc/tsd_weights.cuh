@@ -35,7 +35,7 @@ struct PathSmem {
 };
 
 // Read the path of request b and check it, its length, the capacity and the
-// pages of the prefix; the same answer on every thread and in every CTA of the
+// pages of the prefix and of the path; the same answer on every thread and in every CTA of the
 // request, so that a request with an error is skipped as a whole.  Returns the
 // path length L, or minus the error code.
 __device__ __forceinline__ int weight_path(const WeightArgs& a, int b, int P, PathSmem& s) {
@@ -53,7 +53,7 @@ __device__ __forceinline__ int weight_path(const WeightArgs& a, int b, int P, Pa
       s.rows[tid] = r;
     }
     if (a.map.page_size)
-      for (int p = tid; p < (P + a.map.page_size - 1) / a.map.page_size; p += blockDim.x) {
+      for (int p = tid; p <= (P + L) / a.map.page_size; p += blockDim.x) {   // (the commit's too)
         const int pg = a.map.page_table[(long)b * a.map.max_pages + p];
         if ((pg < 0 || pg >= a.map.num_pages) && code == 0) code = TSD_DEV_ERR_BAD_PAGE;
       }

@@ -337,8 +337,7 @@ bool launch_latent(const tsd_attn_desc& d, const WeightArgs& a, cudaStream_t st)
   if (kQ8) k = q;                                           // (not used)
   else if (!encode_latent(&k, a, d.B)) return false;
   const auto kern = weights_latent_kernel<kQ8>;
-  static std::atomic<uint64_t> done{0};
-  allow_smem(kern, kTotal + 1024, done);
+  cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kTotal + 1024);
   const dim3 grid((unsigned)ceil_div(d.cap, kWeightKeys) + 1, d.Hkv, d.B);
   launch(kern, grid, dim3(kThreads), kTotal + 1024, st, k, q, a);
   return true;

@@ -412,8 +412,7 @@ bool launch_d(const tsd_attn_desc& d, const WeightArgs& a, int cols, cudaStream_
   p.nsplit = (int)ceil_div(tiles, p.tiles);
   const size_t smem = (size_t)p.ring * tile + q + sizeof(WeightSmem) + 1024;
   const auto kern = weights_tc_kernel<D, kQ8, kBufCols>;
-  static std::atomic<uint64_t> done{0};          // (the most that any call asks for)
-  allow_smem(kern, kPerSm == 2 ? 113 * 1024 : 226 * 1024, done);
+  cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   launch(kern, dim3(p.nsplit, d.Hkv, d.B), dim3(kThreads), smem, st, m, a, p);
   return true;
 }
