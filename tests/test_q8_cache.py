@@ -795,6 +795,21 @@ def test_weights_skip_requests_with_errors(q8):
 
 @gpu
 @pytest.mark.parametrize("q8", [True, False])
+@pytest.mark.parametrize("kind", ["gqa", "latent"])
+def test_weights_skip_a_request_whose_commit_has_no_page(kind, q8):
+    s = Setup(kind, 2, 4, [126], extra=100, page=128, seed=27, q8=q8)
+    _weights_state(s, 3, [3, 3])
+    s.table[0, 1] = s.k.shape[0]                  # positions 126..129 need page 1
+    acc0, seen0 = s.acc.clone(), s.seen.clone()
+    _weights(s, 3, 0.5)
+    torch.cuda.synchronize()
+    assert int(s.err) & T.TSD_DEV_ERR_MASK == T.TSD_DEV_ERR_BAD_PAGE
+    assert torch.equal(s.acc[0], acc0[0]) and torch.equal(s.seen[0], seen0[0])
+    assert torch.equal(s.seen[1], seen0[1] + 4)
+
+
+@gpu
+@pytest.mark.parametrize("q8", [True, False])
 def test_weights_ignore_what_lies_behind_the_prefix(q8):
     s = Setup("gqa", 2, 5, [130, 64], extra=200, seed=23, q8=q8)
     _weights_state(s, 4, [2, 4])
