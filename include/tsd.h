@@ -545,8 +545,8 @@ tsd_status tsd_tree_verify_attn_q8(const tsd_attn_desc* desc, const void* q, con
  * q, ktree, lse as given to and left by the verify call ([B][R][Hq][dk],
  * [B][R][Hkv][dk], [B][R][Hq]); 0 <= decay <= 1; accept_rows [B][S+1],
  * accept_len [B].  The other entries are left as they are.  A request whose
- * P + 1 + L passes cap, with a bad path or a bad page, is skipped and reported
- * as by the commit.  No workspace.
+ * P + 1 + L passes cap, with a bad path or a bad page (the commit's among them), is
+ * skipped and reported as by the commit.  No workspace.
  *
  * tsd_cache_evict cuts every request that holds more than `keep` rows to
  * `keep`, in place.  Each head ranks its rows by (protected first, acc desc,
@@ -559,8 +559,10 @@ tsd_status tsd_tree_verify_attn_q8(const tsd_attn_desc* desc, const void* q, con
  * ranks above infinity.  In an 8-bit cache the exponent of a block that gets a
  * row becomes the largest that its rows had before the call, and codes are
  * rescaled to it as by a write.  A request with prefix_len outside 0..cap or a
- * bad page is skipped and reported (CAPACITY, BAD_PAGE).  A page may be in the
- * table once only.  ws: tsd_cache_evict_workspace_size(desc) bytes.
+ * bad page is skipped and reported (CAPACITY, BAD_PAGE).  With keep >= cap nothing
+ * is done.  A page may be in the table once only.  ws:
+ * tsd_cache_evict_workspace_size(desc) bytes; calls that may overlap, captured ones
+ * among them, each need their own.
  *
  * Page arguments and desc (dtype: that of q and of the cache; of q alone where
  * the cache is 8-bit) as above; R, Hq, scale are not used by the eviction.

@@ -25,6 +25,11 @@
 //   e' = max of the exponents that the block's rows had before the call,
 // and every code c becomes e4m3(c * 2^(e - e')).  Both are bounded by memory: each
 // moved row is read and written once.
+//
+// 4 requests of 8 heads, 32k bf16 rows cut to half: selection 19 us, moves 57 us (4
+// TB/s: rows of 256 bytes here and there; 4 or 16 moves in flight and twice the CTAs
+// measured the same, fewer CTAs 70 us).  32 requests of 4k 8-bit rows, 5 dropped each:
+// 16 us and 12 us.
 #include <cuda_bf16.h>
 
 #include "tsd_host.h"

@@ -8,7 +8,8 @@
 // maximum: out = sum p v / sum p, lse = m + log sum p, in one pass over the
 // keys; splits of the prefix are merged by q8_combine_kernel.
 //
-// Paths: tsd_q8_tc.cu (tcgen05, bf16 heads of 64 or 128 dims), and
+// Paths: tcgen05 for bf16 inputs (tsd_q8_few.cu and tsd_q8_tc.cu, heads of 64 or 128
+// dims with few or more packed rows; tsd_q8_latent.cu, 576/512), and
 // q8_simt_kernel here: fp32 inputs, computed in fp32 on the CUDA cores.  Its
 // CTA takes up to RB packed rows, one KV head and one split; a warp takes four
 // keys at a time, its lanes split the dims in words of four codes, and the

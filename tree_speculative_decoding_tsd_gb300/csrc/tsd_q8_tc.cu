@@ -39,27 +39,31 @@
 // compute the next tile's over them while the softmax runs, and waits for its
 // product before only behind the first 32 exponentials.  (With P over the scores it
 // came from, the next scores waited for the product with V; with one product for both
-// halves' scores, the streams waited for each other.)  The running maximum is lazy: a
-// row keeps it until a tile's largest score passes it by 8 (in log2), so that its
-// accumulator is rescaled rarely.  Q (hi, lo) is in the tensor memory too, which
-// leaves the shared memory's 128 bytes a cycle to K and V.
+// halves' scores, the streams wait for each other: 329 us instead of 321 for the
+// 65-row trees below, although the tensor core then needs 1024 cycles a tile and not
+// 1280.)  The running maximum is lazy: a row keeps it until a tile's largest score
+// passes it by 8 (in log2), so that its accumulator is rescaled rarely.  Q (hi, lo) is
+// in the tensor memory too, which leaves the shared memory's 128 bytes a cycle to K
+// and V.
 //
 // Roles (512 threads: 128 registers each, which the softmax needs; with three more
 // widening warps and 96 registers a tile took 10% longer): warps 0-3 and 4-7 softmax
 // and epilogue; warp 8 issues the products with V and owns the tensor memory, warp 9
 // those with Q; one thread of warp 10 loads K tiles by TMA into a ring of four; warps
 // 11-15 load V tiles straight into registers, a tile ahead (behind L2 prefetches), and
-// widen them into three fp16 stages, laid out as the product reads them (rows of 64
-// elements, 128-byte swizzle).  mbarriers order K -> S -> softmax -> O and V -> O;
-// every wait is bounded.
+// widen them into three fp16 stages (two: 325 us), laid out as the product reads them
+// (rows of 64 elements, 128-byte swizzle).  mbarriers order K -> S -> softmax -> O and
+// V -> O; every wait is bounded.
 //
-// What bounds it: the softmax of a tile, about 1750 cycles from its scores to its P
-// with two warps on each scheduler, while the tensor core needs 1280 (8 products with
-// Q of 128 x 64 at 48 cycles for each half, 8 with V of 128 x 128 at 64) and is busy
-// for 52% of the time; and 9600 cycles of set-up (lengths, pages and exponents, one
-// behind the other) and 3500 of epilogue per CTA.  8 x 65 rows of 32 heads over 32k
-// keys: 341 us, 820 TFLOP/s; 32 x 33 rows over 1k to 4k keys: 111 us; 8 x 8 rows over
-// 32k keys: 124 us, 4.3 TB/s of cache.
+// What bounds it: the way of a tile through a stream, about 1600 cycles from its scores
+// to its P with few warps to hide latencies: an access to shared memory takes 300
+// cycles beside the widening's stores and the products' reads, and five roles of
+// unrolled code pass through the instruction cache (which is why set-up loops are
+// rolled and the scratch rows' tile has code of its own: 341 -> 321 us).  The tensor
+// core needs 1280 cycles (8 products with Q of 128 x 64 at 48 cycles for each half, 8
+// with V of 128 x 128 at 64), the cache's bytes 1405.  Set-up and epilogue take 13000
+// cycles per CTA.  8 x 65 rows of 32 heads over 32k keys: 321 us, 870 TFLOP/s; 32 x 33
+// rows over 1k to 4k keys: 104 us; 8 x 8 rows over 32k keys: 121 us, 4.4 TB/s.
 #include <type_traits>
 
 #include "tsd_common.cuh"
@@ -364,7 +368,7 @@ q8_rows_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
         if (lane == 0) mbar_arrive(bar(BAR_T_FULL));
       }
       if (t >= kStages &&
-          !__all_sync(kFull, mbar_wait(bar(BAR_V_EMPTY + st), (t / kStages - 1) & 1))) {
+          !__all_sync(kFull, wait_ready(bar(BAR_V_EMPTY + st), (t / kStages - 1) & 1))) {
         flags[1] = 1;
         break;
       }

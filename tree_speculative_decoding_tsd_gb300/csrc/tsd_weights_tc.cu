@@ -6,8 +6,10 @@
 // A tensor-memory lane is a cached row and a thread owns a lane, so the sum over
 // the columns stays in one thread: no reduction, no second pass, and nothing but K
 // is read per key (and 8 bytes of acc).  Bound by memory: per 128-key tile 32 KB
-// (bf16) or 16 KB (8-bit codes) of K arrive, while a thread's exponentials (8 cycles
-// each and warp) take 288 cycles for 36 columns.
+// (bf16) or 16 KB (8-bit codes) of K arrive, while a thread's exponentials take 150 to
+// 290 cycles for 36 columns.  4 requests of 8 heads, 32k bf16 rows, 36 columns: 45 us,
+// 5.9 TB/s; 32 requests of 1k to 4k 8-bit rows: 29 us, as long as its longest request's
+// CTA takes (splitting them further: 30 us, and 3 to 9% more where all are full).
 //
 // 8-bit cache: kind::f8f6f4 on the codes, Q as the sum of two e4m3 numbers, powers
 // of two in fp32 (tsd_q8_tc.cu).  bf16 cache: kind::f16.
@@ -420,6 +422,9 @@ bool launch_d(const tsd_attn_desc& d, const WeightArgs& a, int cols, cudaStream_
 template <int D, bool kQ8>
 bool launch_cols(const tsd_attn_desc& d, const WeightArgs& a, cudaStream_t st) {
   const int cols = (int)ceil_div((long)(a.S + 1) * a.g, 16) * 16;
+  // Up to 128 columns two CTAs share an SM: score buffers of 128 columns, half the
+  // ring.  (32 requests of 1k to 4k 8-bit rows, 32 columns: 40 us in a graph so, 54 us
+  // with one; 4 x 32k bf16 rows, 36 columns: 61 and 65 us.)
   return cols <= 128 ? launch_d<D, kQ8, 128>(d, a, cols, st) : launch_d<D, kQ8, 256>(d, a, cols, st);
 }
 
