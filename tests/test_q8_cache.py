@@ -482,7 +482,8 @@ ATTN = [("gqa", 1, 1, [2048], {}), ("gqa", 3, 17, [700, 1, 129], {}), ("gqa", 2,
         ("gqa", 2, 5, [777], dict(dtype=torch.float32)), ("narrow", 2, 3, [90], dict(dtype=torch.float32, page=128)),
         ("latent-few", 1, 2, [333], dict(dtype=torch.float32)), ("gqa", 40, 2, [500, 90, 1], {}),
         ("gqa", 3, 4, [130, 2500, 1], {}), ("gqa", 3, 5, [130, 2500, 1], dict(page=128)), ("gqa", 2, 8, [400], {}),
-        ("narrow", 2, 3, [777, 64], {})]
+        ("narrow", 2, 3, [777, 64], {}), ("gqa", 24, 9, [300, 1, 130], dict(page=128)),
+        ("latent", 10, 9, [300, 10, 129], {})]
 
 
 @gpu

@@ -23,6 +23,7 @@ struct Q8AttnArgs {
   CacheMap map;
   int B, R, Hq, g, M;
   int nsplit, split_len, nrg, rb, tree_split;
+  int by_length;              // grid z is a rank in (prefix length desc, index asc) order
   float qscale;               // softmax scale * log2(e)
 };
 
@@ -37,6 +38,7 @@ struct Q8Plan {
   int path;
   int rb, nrg;                // packed rows per CTA, row groups per KV head
   int nsplit, split_len;
+  int by_length;              // requests are taken longest first
   int tree_split;             // the tree rows are a split of their own, behind the prefix splits
   int part_bytes;             // element size of a split's output: 4 (fp32) or 2 (fp16)
   size_t ws_bytes;

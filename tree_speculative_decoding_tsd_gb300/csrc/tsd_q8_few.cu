@@ -69,7 +69,8 @@ struct FewLayout {
   static constexpr int nbar = 20;
   static constexpr uint32_t off_flags = off_bar + 8 * nbar;      // tmem, abort
   static constexpr uint32_t off_top = off_flags + 8;             // int[kWideWarps]
-  static constexpr uint32_t total = off_top + 4 * kWideWarps;
+  static constexpr uint32_t off_req = off_top + 4 * kWideWarps;  // request, its length
+  static constexpr uint32_t total = off_req + 8;
   static_assert(total + 1024 <= 232448, "shared memory budget");
   // (at D = 64 the upper half of a value tile is zeroed while other warps still scan)
   static_assert(kTreeBytes<D> <= (D == 64 ? kHalf : kTile), "the scan's rows");
@@ -107,8 +108,9 @@ q8_few_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
   auto bar = [&](int i) { return bar0 + 8u * i; };
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int hk = blockIdx.x, sp = blockIdx.y, b = blockIdx.z;
-  const int P = min(max(a.plen[b], 0), a.map.cap);
+  const int hk = blockIdx.x, sp = blockIdx.y;
+  int P;
+  const int b = request_at(a, blockIdx.z, P, (volatile int*)(smem + L::off_req));
   const int nsb = q8_splits(a, P);
   if (sp >= nsb) return;
   const int k0 = min(sp * a.split_len, P), k1 = min(P, k0 + a.split_len);

@@ -64,7 +64,8 @@ constexpr uint32_t kOffBar = kOffKex + 2 * kMaxTiles;
 constexpr int kBars = 22;
 constexpr uint32_t kOffFlags = kOffBar + 8 * kBars;             // tmem, abort
 constexpr uint32_t kOffTop = kOffFlags + 8;
-constexpr uint32_t kTotal = kOffTop + 4 * kWideWarps;
+constexpr uint32_t kOffReq = kOffTop + 4 * kWideWarps;           // request, its length
+constexpr uint32_t kTotal = kOffReq + 8;
 static_assert(kTotal + 1024 <= 232448, "shared memory budget");
 
 // FULL: the copy landed or the warps wrote (T_FULL: scratch rows' keys, through
@@ -113,8 +114,9 @@ q8_latent_kernel(const __grid_constant__ LatentMaps maps, const __grid_constant_
   auto bar = [&](int i) { return bar0 + 8u * i; };
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int hk = blockIdx.y / a.nrg, rg = blockIdx.y % a.nrg, sp = blockIdx.x, b = blockIdx.z;
-  const int P = min(max(a.plen[b], 0), a.map.cap);
+  const int hk = blockIdx.y / a.nrg, rg = blockIdx.y % a.nrg, sp = blockIdx.x;
+  int P;
+  const int b = request_at(a, blockIdx.z, P, (volatile int*)(smem + kOffReq));
   const int nsb = q8_splits(a, P);
   if (sp >= nsb) return;
   const int k0 = min(sp * a.split_len, P), k1 = min(P, k0 + a.split_len);

@@ -20,6 +20,49 @@ constexpr int kHeadroom = 7;                    // P's offset: 2^8 * 2^7 < 65504
 constexpr int kMaxTiles = 256;                  // prefix tiles of a split
 constexpr int kPrefetch = 4;                    // tiles that V's L2 prefetch runs ahead
 
+// The request of grid index z, and its prefix length within the cache.  By length
+// (batches of up to 64): the one of rank z, which warp 0 finds and leaves in `slot`.
+// For the whole CTA, before its threads part.
+__device__ __forceinline__ int request_at(const Q8AttnArgs& a, int z, int& P, volatile int* slot) {
+  int b = z;
+  if (a.by_length) {
+    if (threadIdx.x < 32) {
+      const int lane = threadIdx.x;
+      const int p0 = lane < a.B ? min(max(a.plen[lane], 0), a.map.cap) : -1;
+      const int p1 = lane + 32 < a.B ? min(max(a.plen[lane + 32], 0), a.map.cap) : -1;
+      int r0 = 0, r1 = 0;              // requests before this lane's two: longer, or as long and earlier
+#pragma unroll
+      for (int j = 0; j < 32; ++j) {
+        const int x = __shfl_sync(kFull, p0, j);
+        r0 += x > p0 || (x == p0 && j < lane);
+        r1 += x >= p1;
+      }
+      if (a.B > 32) {
+#pragma unroll 8
+        for (int j = 0; j < 32; ++j) {
+          const int x = __shfl_sync(kFull, p1, j);
+          r0 += x > p0;
+          r1 += x > p1 || (x == p1 && j < lane);
+        }
+      }
+      if (p0 >= 0 && r0 == z) {
+        slot[0] = lane;
+        slot[1] = p0;
+      }
+      if (p1 >= 0 && r1 == z) {
+        slot[0] = lane + 32;
+        slot[1] = p1;
+      }
+    }
+    __syncthreads();
+    b = slot[0];
+    P = slot[1];
+  } else {
+    P = min(max(a.plen[b], 0), a.map.cap);
+  }
+  return b;
+}
+
 // Wait for a phase that is usually complete already: one look before the timed
 // wait.
 __device__ __forceinline__ bool wait_ready(uint32_t bar, uint32_t parity) {
