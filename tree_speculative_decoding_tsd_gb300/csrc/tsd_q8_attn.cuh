@@ -30,8 +30,9 @@ struct Q8AttnArgs {
 enum Q8Path { kQ8Simt = 0, kQ8Few = 1, kQ8Rows = 2, kQ8Latent = 3 };
 
 // Up to this many packed rows take the path with keys on lanes.  (4 rows, 16 requests
-// over 20k to 32k keys: 165 us so and 179 us with the rows on lanes; 16 rows, 32 requests
-// over 1k to 4k keys: 56 and 65 us; 32 rows of them: 67 and 65 us.)
+// over 20k to 32k keys: 165 us so and 179 us with the rows on lanes; 16 rows, 8 requests
+// over 32k keys: 112 and 118 us, 32 over 1k to 4k: 50 and 54 us; 32 rows of them, with
+// 32 columns: 59 and 56 us.)
 constexpr int kQ8FewRows = 16;
 
 struct Q8Plan {

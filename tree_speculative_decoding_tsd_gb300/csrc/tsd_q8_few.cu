@@ -16,8 +16,8 @@
 // with a softmax warpgroup, a score buffer, a P^T buffer, a maximum, sums and an
 // accumulator each, joined at the end.  One token of 16 requests of 32 heads over 20k
 // to 32k keys: 165 us with the launch, 5.2 TB/s, 128 us by the bytes (one stream: 226
-// us; rows on lanes: 179 us; with 30% more unrolled code: 177 us, so set-up loops are
-// rolled and the scratch rows are outside the loop over tiles).
+// us; with 30% more unrolled code, for the instruction cache: 177 us, so set-up loops
+// are rolled and the scratch rows are outside the loop over tiles).
 //
 // Softmax with keys on lanes: a column's maximum is a reduction over the warpgroup,
 // so the running maximum is lazy: while no x of a tile exceeds 8, the tile keeps the
@@ -42,6 +42,7 @@ constexpr int kWideThreads = kWideWarps * 32;
 constexpr int kThreads = (kWide + kWideWarps) * 32;
 constexpr int kDepth = 2;                        // V tiles in registers
 constexpr int N = kQ8FewRows;                    // columns of the products
+static_assert(kMaxTiles <= kWideThreads, "a widening thread per tile in the set-up");
 
 template <int D>
 struct FewLayout {
