@@ -17,7 +17,7 @@
 // each, the widened values are written (128 KB) and the 32 products of O^T read 6 KB
 // each: 536 KB, about 4200 cycles; a tile takes 5200.  (Widened keys would be 144 KB
 // written and 216 KB read instead of the 216 KB.)  64 x 9 rows of 128 heads over 8k
-// keys: 1.50 ms, 875 TFLOP/s.
+// keys: 1.53 ms, 858 TFLOP/s.
 //
 // Roles (768 threads): warps 0-15 softmax and epilogue (warpgroup w/4 owns 16
 // columns, warp w%4 the TMEM lanes 32(w%4)..+31); warp 16 issues the products of
@@ -126,8 +126,9 @@ q8_latent_kernel(const __grid_constant__ LatentMaps maps, const __grid_constant_
   const int row_base = rg * kN;
   const int rows_here = min(kN, a.M - row_base);
   auto valid_of = [&](int t) { return min(kKeys, k1 - (k0 + t * kKeys)); };
-  const __nv_bfloat16* const tree = (const __nv_bfloat16*)a.kt + ((long)b * a.R * a.map.Hkv + hk) * kDK;
-  const long tree_pitch = (long)a.map.Hkv * kDK;
+  auto tree_row = [&](int j) {                       // scratch row j
+    return (const uint4*)((const __nv_bfloat16*)a.kt + (((long)b * a.R + j) * a.map.Hkv + hk) * kDK);
+  };
 
   const int wt = tid - kWide * 32;
   using Share = WideShare<8, kWideThreads>;
@@ -186,7 +187,7 @@ q8_latent_kernel(const __grid_constant__ LatentMaps maps, const __grid_constant_
         const bool live = j < a.R && (j == 0 || ((seen >> (j - 1)) & 1ull));
         uint32_t kt = 0, vt = 0;
         if (live) {
-          const uint4* p = (const uint4*)(tree + j * tree_pitch);
+          const uint4* p = tree_row(j);
           vt = top_pairs(top_pairs(0u, __ldg(p + lane)), __ldg(p + 32 + lane));
           kt = lane < 8 ? top_pairs(vt, __ldg(p + 64 + lane)) : vt;
         }
@@ -329,7 +330,7 @@ q8_latent_kernel(const __grid_constant__ LatentMaps maps, const __grid_constant_
             uint4 hi = make_uint4(0u, 0u, 0u, 0u), lo = hi;
             const float f = kt_in[r];
             if (f != 0.f) {
-              const uint4* p = (const uint4*)(tree + r * tree_pitch) + 16 * j + 2 * u;
+              const uint4* p = tree_row(r) + 16 * j + 2 * u;
               const uint4 w[2] = {__ldg(p), __ldg(p + 1)};
               split16(w, f, hi, lo);
             }
@@ -358,7 +359,7 @@ q8_latent_kernel(const __grid_constant__ LatentMaps maps, const __grid_constant_
             const int row = x >> 4, c = x & 15;
             const float f = vt_in[row];
             uint4 v = make_uint4(0u, 0u, 0u, 0u);
-            if (f != 0.f) v = scale8(__ldg((const uint4*)(tree + row * tree_pitch) + 16 * u + c), f);
+            if (f != 0.f) v = scale8(__ldg(tree_row(row) + 16 * u + c), f);
             *(uint4*)(stage + (c >> 3) * kHalf + row * 128 + (((c & 7) ^ (row & 7)) << 4)) = v;
           }
         }

@@ -55,8 +55,9 @@ __device__ __forceinline__ int request_at(const Q8AttnArgs& a, int z, int& P, vo
       }
     }
     __syncthreads();
-    b = slot[0];
-    P = slot[1];
+    // (a reduction's result is a uniform value, which spares registers)
+    b = __reduce_max_sync(kFull, (int)slot[0]);
+    P = __reduce_max_sync(kFull, (int)slot[1]);
   } else {
     P = min(max(a.plen[b], 0), a.map.cap);
   }
