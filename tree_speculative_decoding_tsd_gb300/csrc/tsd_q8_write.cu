@@ -16,7 +16,7 @@
 // between the maximum and the conversion, so the source is read once and the codes
 // are written once; earlier rows are read only when the exponent grows.  Bounded by
 // memory: 2 (or 4) bytes read and 1 written per element (4 x 8192 rows at most of 8
-// heads: 34 us with the length's update, 22 us by the bytes).  Commit: a warp takes a
+// heads: 31 us with the length's update, 22 us by the bytes).  Commit: a warp takes a
 // (block, head, K or V); bounded by latency.
 #include <cuda_bf16.h>
 
@@ -46,9 +46,10 @@ constexpr int kNoCode = 0x7fffffff;
 template <int D> constexpr int kWriteThreads = D > 128 ? 512 : 256;
 template <int D> constexpr int kWriteVecs = kQ8Block * D / 8 / kWriteThreads<D>;
 
-// CTAs per SM to fit the registers to.  (4 x 8192 rows of 128 bf16 dims: 42 us at six,
-// 46 at the compiler's five; rows of 576 dims need the registers for their vectors.)
-template <int D> constexpr int kWriteCtas = D > 128 ? 1 : 6;
+// CTAs per SM to fit the registers to.  (4 x 8192 rows at most of 128 dims, in a graph:
+// bf16 38 us at six, 40 at eight, 41 as the compiler has it; fp32 56 us at five, 57 at
+// four, 61 at three.  Rows of 576 dims need the registers for their vectors.)
+template <typename T, int D> constexpr int kWriteCtas = D > 128 ? 1 : sizeof(T) * D > 256 ? 5 : 6;
 
 struct WriteSmem {
   int code;
@@ -89,7 +90,8 @@ __device__ __forceinline__ int write_rows(const Q8WriteArgs& a, int b, int P, in
   return code != kNoCode ? -code : (int)n;
 }
 
-// Eight elements as they are in memory, and as fp32.
+// Eight elements as they are in memory, and as fp32.  `top` runs the largest magnitude
+// in a form of the type's own (bf16: two at a time), `bits` gives it as fp32 bits.
 struct RawF32 {
   uint4 a, b;
   __device__ __forceinline__ void load(const float* p) {
@@ -102,6 +104,13 @@ struct RawF32 {
 #pragma unroll
     for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(w[i]);
   }
+  __device__ __forceinline__ uint32_t top(uint32_t t) const {
+    const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) t = max(t, w[i] & 0x7fffffffu);
+    return t;
+  }
+  static __device__ __forceinline__ uint32_t bits(uint32_t t) { return t; }
 };
 struct RawBf16 {
   uint4 a;
@@ -115,7 +124,36 @@ struct RawBf16 {
       x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
     }
   }
+  __device__ __forceinline__ uint32_t top(uint32_t t) const {
+    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) t = __vmaxu2(t, w[i] & 0x7fff7fffu);
+    return t;
+  }
+  static __device__ __forceinline__ uint32_t bits(uint32_t t) { return max(t << 16, t & 0xffff0000u); }
 };
+template <typename Raw>
+__device__ __forceinline__ uint2 to_codes(const Raw& raw, float f) {
+  float x[8];
+  raw.values(x);
+  float2 y[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) y[i] = __fmul2_rn(make_float2(x[2 * i], x[2 * i + 1]), make_float2(f, f));
+  return make_uint2(q8_pack4(y[0].x, y[0].y, y[1].x, y[1].y), q8_pack4(y[2].x, y[2].y, y[3].x, y[3].y));
+}
+// The largest finite magnitude, for a block that holds an infinity or a NaN.
+constexpr uint32_t kInf = 0x7f800000u;
+template <typename Raw>
+__device__ __forceinline__ uint32_t finite_top(const Raw& raw, uint32_t t) {
+  float x[8];
+  raw.values(x);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const uint32_t u = __float_as_uint(x[j]) & 0x7fffffffu;
+    t = max(t, u < kInf ? u : 0u);
+  }
+  return t;
+}
 
 // Block `blk` (positions 64 blk ..) of head h of request b, part 0 (K) or 1 (V).
 template <typename T, int D>
@@ -140,36 +178,33 @@ __device__ __forceinline__ void write_block(const Q8WriteArgs& a, int b, int h, 
   uint8_t* const ep = a.exps[part] + a.map.block(b, h, first);
   const int e_old = r0 > 0 ? *ep : 0;
   uint8_t* const row0 = a.codes[part] + a.map.row(b, h, first) * D;
+  auto block_max = [&](uint32_t x) {
+    x = __reduce_max_sync(kFull, x);
+    if ((tid & 31) == 0) s.warp_max[tid >> 5] = x;
+    __syncthreads();
+    x = 0;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) x = max(x, s.warp_max[w]);
+    return x;
+  };
   uint32_t m = 0;
 #pragma unroll
-  for (int i = 0; i < kVecs; ++i) {
-    float x[8];
-    raw[i].values(x);
+  for (int i = 0; i < kVecs; ++i) m = raw[i].top(m);
+  m = block_max(Raw::bits(m));
+  if (m >= kInf) {                                   // (the same in the whole CTA)
+    m = 0;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const uint32_t u = __float_as_uint(x[j]) & 0x7fffffffu;
-      m = max(m, u < 0x7f800000u ? u : 0u);          // infinities and NaN do not count
-    }
+    for (int i = 0; i < kVecs; ++i) m = finite_top(raw[i], m);
+    __syncthreads();                                 // warp_max has been read
+    m = block_max(m);
   }
-  m = __reduce_max_sync(kFull, m);
-  __syncthreads();                                   // (warp_max of the task before)
-  if ((tid & 31) == 0) s.warp_max[tid >> 5] = m;
-  __syncthreads();
-  m = 0;
-#pragma unroll
-  for (int w = 0; w < kThreads / 32; ++w) m = max(m, s.warp_max[w]);
   const int e = max(q8_need(__uint_as_float(m)), e_old);
   const float inv = q8_scale(254 - min(e, kQ8ExpMax));  // 2^(127 - e)
 #pragma unroll
   for (int i = 0; i < kVecs; ++i) {
     const int v = tid + i * kThreads, r = v / VR;
     if (r >= r0 && r < r1) {
-      float x[8];
-      raw[i].values(x);
-      uint2 w;
-      w.x = q8_pack4(x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv);
-      w.y = q8_pack4(x[4] * inv, x[5] * inv, x[6] * inv, x[7] * inv);
-      *(uint2*)(row0 + (long)v * 8) = w;
+      *(uint2*)(row0 + (long)v * 8) = to_codes(raw[i], inv);
     }
   }
   if (r0 > 0 && e != e_old) {
@@ -191,7 +226,7 @@ __device__ __forceinline__ void write_block(const Q8WriteArgs& a, int b, int h, 
 // Prefill: grid (blocks, part x head, request).  prefix_len changes only in
 // write_advance_kernel, so every CTA reads the length of before.
 template <typename T, int D>
-__global__ void __launch_bounds__(kWriteThreads<D>, kWriteCtas<D>)
+__global__ void __launch_bounds__(kWriteThreads<D>, kWriteCtas<T, D>)
 write_q8_kernel(const __grid_constant__ Q8WriteArgs a) {
   __shared__ WriteSmem s;
   grid_dependency_sync();
@@ -239,16 +274,6 @@ __device__ __forceinline__ void commit_block(const Q8WriteArgs& a, const WriteSm
     const int t = first + r0 + v / VR - P;
     return (const T*)a.src[part] + (((long)b * a.rows + s.path[t]) * a.map.Hkv + h) * D + v % VR * 8;
   };
-  auto magnitude = [](const Raw& w, uint32_t m) {
-    float x[8];
-    w.values(x);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const uint32_t u = __float_as_uint(x[j]) & 0x7fffffffu;
-      m = max(m, u < 0x7f800000u ? u : 0u);          // infinities and NaN do not count
-    }
-    return m;
-  };
   Raw raw[kKeep ? kVecs : 1];
   uint32_t m = 0;
   if constexpr (kKeep) {
@@ -258,24 +283,28 @@ __device__ __forceinline__ void commit_block(const Q8WriteArgs& a, const WriteSm
       if (lane + 32 * i < work) raw[i].load(source(lane + 32 * i));
     }
 #pragma unroll
-    for (int i = 0; i < kVecs; ++i) m = magnitude(raw[i], m);
+    for (int i = 0; i < kVecs; ++i) m = raw[i].top(m);
   } else {
 #pragma unroll 4
     for (int v = lane; v < work; v += 32) {
       raw[0].load(source(v));
-      m = magnitude(raw[0], m);
+      m = raw[0].top(m);
     }
   }
-  m = __reduce_max_sync(kFull, m);
+  m = __reduce_max_sync(kFull, Raw::bits(m));
+  if (m >= kInf) {
+    m = 0;
+    for (int v = lane; v < work; v += 32) {
+      Raw again;
+      again.load(source(v));
+      m = finite_top(again, m);
+    }
+    m = __reduce_max_sync(kFull, m);
+  }
   const int e = max(q8_need(__uint_as_float(m)), e_old);
   const float inv = q8_scale(254 - min(e, kQ8ExpMax));  // 2^(127 - e)
   auto put = [&](const Raw& w, int v) {
-    float x[8];
-    w.values(x);
-    uint2 o;
-    o.x = q8_pack4(x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv);
-    o.y = q8_pack4(x[4] * inv, x[5] * inv, x[6] * inv, x[7] * inv);
-    *(uint2*)(row0 + ((long)r0 * VR + v) * 8) = o;
+    *(uint2*)(row0 + ((long)r0 * VR + v) * 8) = to_codes(w, inv);
   };
   if constexpr (kKeep) {
 #pragma unroll
