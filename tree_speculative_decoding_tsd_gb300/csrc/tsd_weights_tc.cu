@@ -287,14 +287,26 @@ weights_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
     float* const acc = a.acc + head * a.map.cap;
     int done = 0;                                           // items of this buffer
     bool ok = true;
+    // this lane's row of item i, its weight so far and its factor: requested an item
+    // ahead of its scores
+    auto place = [&](int i) {
+      return with_path && i == 0 ? P + key : (t0 + i - (with_path ? 1 : 0)) * kWeightKeys + key;
+    };
+    float next_old = 0.f, next_ck = 1.f;
+    auto request = [&](int i) {
+      const bool is_path = with_path && i == 0;
+      const int pos = place(i);
+      const bool mine = i < ntiles && (is_path ? key <= L : pos < P);
+      next_old = mine && !is_path ? acc[pos] : 0.f;
+      if (kQ8) next_ck = !mine ? 1.f : is_path ? s.kt_out[key] : q8_scale(a.ke[a.map.block(b, hk, pos)]);
+    };
+    request(wg);
     for (int i = wg; ok && i < ntiles; i += 2) {
       const bool is_path = with_path && i == 0;
-      const int pos = is_path ? P + key : (t0 + i - (with_path ? 1 : 0)) * kWeightKeys + key;
+      const int pos = place(i);
       const bool mine = is_path ? key <= L : pos < P;
-      // (requested before the scores are waited for)
-      const float old = mine && !is_path ? acc[pos] : 0.f;
-      float ck = 1.f;
-      if (kQ8 && mine) ck = is_path ? s.kt_out[key] : q8_scale(a.ke[a.map.block(b, hk, pos)]);
+      const float old = next_old, ck = next_ck;
+      request(i + 2);
       const int first = is_path ? key * a.g : 0;            // row i of the path sees rows j <= i
       const float2 ck2 = make_float2(ck, ck);
       float2 s0 = make_float2(0.f, 0.f), s1 = s0;
@@ -307,7 +319,7 @@ weights_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
         fence_after();
         const float* const f = s.f + c * kBufCols;
         const float* const nl = s.nl + c * kBufCols;
-#pragma unroll 2
+#pragma unroll 1
         for (int j = 0; j < n; j += 16) {
           float v[16];
           tmem_ld8(src + j, v);
