@@ -139,15 +139,15 @@ q8_simt_kernel(const __grid_constant__ Q8AttnArgs a) {
     float k[kSimtKeys][WK][4], v[kSimtKeys][WV][4];
     bool live[kSimtKeys];
     uint32_t kw[kSimtKeys][WK], vw[kSimtKeys][WV];
-    float fk[kSimtKeys], fv[kSimtKeys];
+    // (four keys from a multiple of four are of one block)
+    const long row0 = a.map.row(b, hk, j);
+    if (row0 < 0 && lane == 0) report_error(a.err, TSD_DEV_ERR_BAD_PAGE, b);
+    const long blk = row0 < 0 ? 0 : a.map.block_at(b, hk, j, row0);
+    const float fk = q8_scale(a.ke[blk]), fv = ALIAS ? fk : q8_scale(a.ve[blk]);
 #pragma unroll
     for (int u = 0; u < kSimtKeys; ++u) {
-      const long row = j + u < k1 ? a.map.row(b, hk, j + u) : -1;
-      live[u] = row >= 0;
-      if (j + u < k1 && row < 0 && lane == 0) report_error(a.err, TSD_DEV_ERR_BAD_PAGE, b);
-      const long blk = live[u] ? a.map.block(b, hk, j + u) : 0;
-      fk[u] = live[u] ? q8_scale(a.ke[blk]) : 0.f;
-      fv[u] = ALIAS || !live[u] ? fk[u] : q8_scale(a.ve[blk]);
+      const long row = row0 + u;
+      live[u] = row0 >= 0 && j + u < k1;
 #pragma unroll
       for (int t = 0; t < WK; ++t) {
         const int w = lane + 32 * t;
@@ -166,13 +166,13 @@ q8_simt_kernel(const __grid_constant__ Q8AttnArgs a) {
       for (int t = 0; t < WK; ++t) {
         q8_unpack4(kw[u][t], k[u][t]);
 #pragma unroll
-        for (int x = 0; x < 4; ++x) k[u][t][x] *= fk[u];
+        for (int x = 0; x < 4; ++x) k[u][t][x] *= fk;
       }
 #pragma unroll
       for (int t = 0; t < WV; ++t) {
         q8_unpack4(vw[u][t], v[u][t]);
 #pragma unroll
-        for (int x = 0; x < 4; ++x) v[u][t][x] *= fv[u];
+        for (int x = 0; x < 4; ++x) v[u][t][x] *= fv;
       }
     }
     visit(k, v, live, false, 0);
@@ -399,7 +399,7 @@ Q8Plan plan_q8(const tsd_attn_desc& d) {
     long ns = ceil_div(152L * 4, (long)d.B * d.Hkv * p.nrg);
     const long most = ceil_div(d.cap, 64);
     if (ns > most) ns = most;
-    p.split_len = (int)ceil_div(d.cap, ns);
+    p.split_len = (int)ceil_div(ceil_div(d.cap, ns), 64) * 64;        // (whole blocks)
     p.nsplit = (int)ceil_div(d.cap, p.split_len);
   }
   p.ws_bytes = p.nsplit > 1 ? (size_t)d.B * d.Hq * d.R * p.nsplit *
