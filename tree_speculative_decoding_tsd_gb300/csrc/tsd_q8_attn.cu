@@ -12,16 +12,20 @@
 // dims with few or more packed rows; tsd_q8_latent.cu, 576/512), and
 // q8_simt_kernel here: fp32 inputs, computed in fp32 on the CUDA cores.  Its
 // CTA takes up to RB packed rows, one KV head and one split; a warp takes four
-// keys at a time, its lanes split the dims in words of four codes, and the
-// four dot products share their shuffles.  Bound by the shuffles and the
-// multiply-adds (RB x 2 d per key), not by the cache's bytes.
+// keys at a time and its lanes split the dims in words of four codes.  The 4 RB dot
+// products are summed over the lanes together, each halving of the lanes leaving half
+// the products on a lane, so that a lane ends with one (row, key) and computes that
+// one's exponential; the weights go back by one shuffle each.  Bound by instructions
+// (RB x 2 d multiply-adds per key and about as many again), not by the cache's bytes.
 #include <cuda_bf16.h>
 #include <math.h>
 
 #include <type_traits>
 
+#include "tsd_common.cuh"
 #include "tsd_host.h"
 #include "tsd_q8_attn.cuh"
+#include "tsd_tcgen05.cuh"
 
 namespace tsd {
 namespace {
@@ -55,8 +59,11 @@ q8_simt_kernel(const __grid_constant__ Q8AttnArgs a) {
   if (sp >= nsb) return;
   const int k0 = min(sp * a.split_len, P), k1 = min(P, k0 + a.split_len);
 
-  float qv[RB][WK][4], o[RB][WV][4], m[RB], l[RB];
-  uint64_t rmask[RB];
+  // the (row, key of four) that this lane's score is of; the row's maximum, the sum of
+  // its keys' weights, and what the row sees
+  const int mi = (lane >> 2) & (RB - 1), mu = lane & 3;
+  float m = -INFINITY, l = 0.f;
+  float qv[RB][WK][4], o[RB][WV][4];
   const int nrows = min(RB, a.M - rg * RB);
 #pragma unroll
   for (int i = 0; i < RB; ++i) {
@@ -72,92 +79,89 @@ q8_simt_kernel(const __grid_constant__ Q8AttnArgs a) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) qv[i][t][j] = x[j];
     }
-    rmask[i] = valid && r > 0 ? a.mask[(long)b * a.R + r] : 0ull;
-    m[i] = -INFINITY;
-    l[i] = 0.f;
 #pragma unroll
     for (int t = 0; t < WV; ++t)
 #pragma unroll
       for (int j = 0; j < 4; ++j) o[i][t][j] = 0.f;
   }
 
-  // four keys with their values (zero where there is none), their weights of
-  // the scores, and for the tree the rows they are (-1: none)
-  auto visit = [&](float (&k)[kSimtKeys][WK][4], float (&v)[kSimtKeys][WV][4],
-                   const bool (&live)[kSimtKeys], bool tree, int j0) {
+  const int tr = mi < nrows ? (rg * RB + mi) / a.g : 0;
+  const uint64_t rmask = tr > 0 ? a.mask[(long)b * a.R + tr] : 0ull;
+
+  // four keys with their values (zero where there is none), the first `live` of them
+  // there; for the tree, from row j0
+  auto visit = [&](float (&k)[kSimtKeys][WK][4], float (&v)[kSimtKeys][WV][4], int live, bool tree,
+                   int j0) {
+    float s[RB * kSimtKeys];
 #pragma unroll
-    for (int i = 0; i < RB; ++i) {
-      if (i >= nrows) break;
-      float s[kSimtKeys];
+    for (int i = 0; i < RB; ++i)
 #pragma unroll
       for (int u = 0; u < kSimtKeys; ++u) {
-        s[u] = 0.f;
+        float x = 0.f;
 #pragma unroll
         for (int t = 0; t < WK; ++t)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) s[u] = fmaf(qv[i][t][j], k[u][t][j], s[u]);
+          for (int j = 0; j < 4; ++j) x = fmaf(qv[i][t][j], k[u][t][j], x);
+        s[i * kSimtKeys + u] = x;
       }
+    const float dot = warp_reduce_scatter<RB * kSimtKeys, false>(s, lane);
+    const int j = j0 + mu;
+    const bool sees = mi < nrows && mu < live && (!tree || j == 0 || ((rmask >> (j - 1)) & 1ull));
+    const float x = sees ? dot * a.qscale : -INFINITY;
+    float mx = fmaxf(x, __shfl_xor_sync(kFull, x, 1));
+    mx = fmaxf(fmaxf(mx, __shfl_xor_sync(kFull, mx, 2)), m);
+    // (a score of -inf does not count, whatever its value; one that is NaN does)
+    const bool counts = !(x == -INFINITY);
+    const float al = mx == m ? 1.f : m == -INFINITY ? 0.f : exp2f(m - mx);
+    const float p = counts ? exp2f(x - mx) : 0.f;
+    m = mx;
+    l = fmaf(l, al, p);
+    if (__any_sync(kFull, al != 1.f)) {
 #pragma unroll
-      for (int x = 16; x > 0; x >>= 1)
-#pragma unroll
-        for (int u = 0; u < kSimtKeys; ++u) s[u] += __shfl_xor_sync(kFull, s[u], x);
-      float mx = m[i];
-#pragma unroll
-      for (int u = 0; u < kSimtKeys; ++u) {
-        const int j = j0 + u;
-        const bool sees = live[u] && (!tree || j == 0 || ((rmask[i] >> (j - 1)) & 1ull));
-        s[u] = sees ? s[u] * a.qscale : -INFINITY;
-        mx = fmaxf(mx, s[u]);
-      }
-      if (mx == -INFINITY) {                               // nothing seen yet, or only NaN
-        bool any = false;
-#pragma unroll
-        for (int u = 0; u < kSimtKeys; ++u) any |= s[u] != s[u];
-        if (!any) continue;
-      }
-      const float al = m[i] == -INFINITY ? 0.f : exp2f(m[i] - mx);
-      m[i] = mx;
-      l[i] *= al;
-#pragma unroll
-      for (int t = 0; t < WV; ++t)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) o[i][t][j] *= al;
-#pragma unroll
-      for (int u = 0; u < kSimtKeys; ++u) {
-        if (s[u] == -INFINITY) continue;                   // (its value may be anything)
-        const float p = exp2f(s[u] - mx);
-        l[i] += p;
+      for (int i = 0; i < RB; ++i) {
+        const float f = __shfl_sync(kFull, al, i * kSimtKeys);
 #pragma unroll
         for (int t = 0; t < WV; ++t)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) o[i][t][j] = fmaf(p, v[u][t][j], o[i][t][j]);
+          for (int c = 0; c < 4; ++c) o[i][t][c] *= f;
       }
     }
+    const uint32_t seen = __ballot_sync(kFull, counts);
+#pragma unroll
+    for (int i = 0; i < RB; ++i)
+#pragma unroll
+      for (int u = 0; u < kSimtKeys; ++u) {
+        if (!((seen >> (i * kSimtKeys + u)) & 1u)) continue;
+        const float f = __shfl_sync(kFull, p, i * kSimtKeys + u);
+#pragma unroll
+        for (int t = 0; t < WV; ++t)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) o[i][t][c] = fmaf(f, v[u][t][c], o[i][t][c]);
+      }
   };
 
   for (int j = k0 + warp * kSimtKeys; j < k1; j += kSimtWarps * kSimtKeys) {
     float k[kSimtKeys][WK][4], v[kSimtKeys][WV][4];
-    bool live[kSimtKeys];
     uint32_t kw[kSimtKeys][WK], vw[kSimtKeys][WV];
     // (four keys from a multiple of four are of one block)
     const long row0 = a.map.row(b, hk, j);
     if (row0 < 0 && lane == 0) report_error(a.err, TSD_DEV_ERR_BAD_PAGE, b);
     const long blk = row0 < 0 ? 0 : a.map.block_at(b, hk, j, row0);
     const float fk = q8_scale(a.ke[blk]), fv = ALIAS ? fk : q8_scale(a.ve[blk]);
+    const int live = row0 < 0 ? 0 : k1 - j;
 #pragma unroll
     for (int u = 0; u < kSimtKeys; ++u) {
       const long row = row0 + u;
-      live[u] = row0 >= 0 && j + u < k1;
 #pragma unroll
       for (int t = 0; t < WK; ++t) {
         const int w = lane + 32 * t;
-        kw[u][t] = live[u] && w < DK / 4 ? __ldg((const uint32_t*)(a.kc + row * DK) + w) : 0u;
+        kw[u][t] = u < live && w < DK / 4 ? __ldg((const uint32_t*)(a.kc + row * DK) + w) : 0u;
       }
 #pragma unroll
       for (int t = 0; t < WV; ++t) {
         const int w = lane + 32 * t;
         vw[u][t] = ALIAS ? kw[u][t]
-                         : live[u] && w < DV / 4 ? __ldg((const uint32_t*)(a.vc + row * DV) + w) : 0u;
+                         : u < live && w < DV / 4 ? __ldg((const uint32_t*)(a.vc + row * DV) + w) : 0u;
       }
     }
 #pragma unroll
@@ -183,15 +187,14 @@ q8_simt_kernel(const __grid_constant__ Q8AttnArgs a) {
     constexpr int VS = ALIAS ? DK : DV;
     for (int j = warp * kSimtKeys; j < a.R; j += kSimtWarps * kSimtKeys) {
       float k[kSimtKeys][WK][4], v[kSimtKeys][WV][4];
-      bool live[kSimtKeys];
+      const int live = a.R - j;
 #pragma unroll
       for (int u = 0; u < kSimtKeys; ++u) {
-        live[u] = j + u < a.R;
 #pragma unroll
         for (int t = 0; t < WK; ++t) {
           const int w = lane + 32 * t;
           float x[4] = {0.f, 0.f, 0.f, 0.f};
-          if (live[u] && w < DK / 4) load4(kt + (long)(j + u) * a.map.Hkv * DK + 4 * w, x);
+          if (u < live && w < DK / 4) load4(kt + (long)(j + u) * a.map.Hkv * DK + 4 * w, x);
 #pragma unroll
           for (int c = 0; c < 4; ++c) k[u][t][c] = x[c];
         }
@@ -199,7 +202,7 @@ q8_simt_kernel(const __grid_constant__ Q8AttnArgs a) {
         for (int t = 0; t < WV; ++t) {
           const int w = lane + 32 * t;
           float x[4] = {0.f, 0.f, 0.f, 0.f};
-          if (live[u] && w < DV / 4) load4(vt + (long)(j + u) * a.map.Hkv * VS + 4 * w, x);
+          if (u < live && w < DV / 4) load4(vt + (long)(j + u) * a.map.Hkv * VS + 4 * w, x);
 #pragma unroll
           for (int c = 0; c < 4; ++c) v[u][t][c] = x[c];
         }
@@ -209,9 +212,14 @@ q8_simt_kernel(const __grid_constant__ Q8AttnArgs a) {
   }
 
   // merge the four warps' running states
+  l += __shfl_xor_sync(kFull, l, 1);
+  l += __shfl_xor_sync(kFull, l, 2);
+  if (lane < RB * kSimtKeys && mu == 0) {
+    sm_m[warp][mi] = m;
+    sm_l[warp][mi] = l;
+  }
 #pragma unroll
   for (int i = 0; i < RB; ++i) {
-    if (lane == 0) { sm_m[warp][i] = m[i]; sm_l[warp][i] = l[i]; }
 #pragma unroll
     for (int t = 0; t < WV; ++t)
       if (lane + 32 * t < DV / 4)
