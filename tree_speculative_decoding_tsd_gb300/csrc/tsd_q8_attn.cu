@@ -401,7 +401,7 @@ Q8Plan plan_q8(const tsd_attn_desc& d) {
   } else {
     p.path = kQ8Simt;
     p.part_bytes = 4;
-    p.rb = d.dk > 128 ? 2 : 4;
+    p.rb = d.dk > 128 ? 4 : M > 4 ? 8 : 4;
     p.nrg = (int)ceil_div(M, p.rb);
     // about four CTAs per SM over the whole batch, splits of at least 64 keys
     long ns = ceil_div(152L * 4, (long)d.B * d.Hkv * p.nrg);
@@ -499,11 +499,13 @@ extern "C" tsd_status tsd_tree_verify_attn_q8(const tsd_attn_desc* d, const void
     else if (d->dv == 128) launch_combine<__nv_bfloat16, 128, __half>(a, p, st);
     else launch_combine<__nv_bfloat16, 64, __half>(a, p, st);
   } else if (alias) {
-    launch_simt<float, 576, 512, 2, true>(a, p, st);
+    launch_simt<float, 576, 512, 4, true>(a, p, st);
   } else if (d->dk == 128) {
-    launch_simt<float, 128, 128, 4, false>(a, p, st);
+    if (p.rb == 8) launch_simt<float, 128, 128, 8, false>(a, p, st);
+    else launch_simt<float, 128, 128, 4, false>(a, p, st);
   } else {
-    launch_simt<float, 64, 64, 4, false>(a, p, st);
+    if (p.rb == 8) launch_simt<float, 64, 64, 8, false>(a, p, st);
+    else launch_simt<float, 64, 64, 4, false>(a, p, st);
   }
   return cuda_status();
 }
