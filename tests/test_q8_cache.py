@@ -645,6 +645,44 @@ def test_attention_on_a_stream_and_in_a_graph(kind):
 
 
 @gpu
+@pytest.mark.parametrize("kinds", [("gqa", "latent"), ("gqa", "gqa"), ("narrow", "one")])
+def test_two_streams_at_once(kinds):
+    """Attention, then eviction, on two streams with state and workspaces of their own: the
+    results of one at a time."""
+    sets = [Setup(k, 6, 5 + i, [900, 40, 333], extra=16, seed=60 + i) for i, k in enumerate(kinds)]
+    for s in sets:
+        _evict_state(s)
+        s.out = torch.empty(s.B, s.R, s.Hq, s.dv, dtype=s.dt, device=DEV)
+        s.ws = T.workspace(T.tsd_verify_q8_workspace_size(s.desc))
+        s.ws_evict = T.workspace(T.tsd_cache_evict_workspace_size(s.desc))
+        s.lse = torch.empty(s.B, s.R, s.Hq, device=DEV)
+        s.state = [t for t in (s.k, s.v, s.ke, s.ve, s.acc, s.pos, s.plen) if t is not None]
+        s.before = [t.clone() for t in s.state]
+
+    def round_of(s):
+        for t, b in zip(s.state, s.before):
+            t.copy_(b)
+        s.attn_into(s.out, s.lse, s.ws)
+        T.tsd_cache_evict_q8(s.desc, 200, 2, 20, s.acc, s.pos, s.seen, s.k, s.v, s.ke, s.ve, s.plen,
+                             s.ws_evict, s.err)
+
+    want = []
+    for s in sets:
+        round_of(s)
+        torch.cuda.synchronize()
+        want.append([t.clone() for t in [s.out, s.lse] + s.state])
+    streams = [torch.cuda.Stream() for _ in sets]
+    for _ in range(3):
+        for s, stream in zip(sets, streams):
+            with torch.cuda.stream(stream):
+                round_of(s)
+    torch.cuda.synchronize()
+    for s, w in zip(sets, want):
+        assert all(torch.equal(t, x) for t, x in zip([s.out, s.lse] + s.state, w))
+        assert int(s.err) == 0
+
+
+@gpu
 def test_attention_is_the_same_twice_and_for_any_rows_of_a_tree():
     s = Setup("gqa", 3, 33, [1000, 700, 65], seed=16)
     a, b = s.attn(), s.attn()
