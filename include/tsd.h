@@ -555,14 +555,14 @@ tsd_status tsd_tree_verify_attn_q8(const tsd_attn_desc* desc, const void* q, con
  * `keep` move, in index order, into the places below `keep` that the dropped
  * rows leave, in index order, K, V, acc and pos together; then prefix_len[b] =
  * keep.  Rows behind the new length are left as they were.  The cache is then
- * no longer in token order, which attention does not depend on.  A NaN in acc
- * ranks above infinity.  In an 8-bit cache the exponent of a block that gets a
- * row becomes the largest that its rows had before the call, and codes are
- * rescaled to it as by a write.  A request with prefix_len outside 0..cap or a
- * bad page is skipped and reported (CAPACITY, BAD_PAGE).  With keep >= cap nothing
- * is done.  A page may be in the table once only.  ws:
- * tsd_cache_evict_workspace_size(desc) bytes; calls that may overlap, captured ones
- * among them, each need their own.
+ * no longer in token order, which attention does not depend on.  Any NaN in acc,
+ * of either sign, ranks above infinity and behind the protected rows.  In an 8-bit
+ * cache the exponent of a block that gets a row becomes the largest that its rows
+ * had before the call, and codes are rescaled to it as by a write.  A request with
+ * prefix_len outside 0..cap or a bad page is skipped and reported (CAPACITY,
+ * BAD_PAGE).  With keep >= cap nothing is done.  A page may be in the table once
+ * only.  ws: tsd_cache_evict_workspace_size(desc) bytes; calls that may overlap,
+ * captured ones among them, each need their own.
  *
  * Page arguments and desc (dtype: that of q and of the cache; of q alone where
  * the cache is 8-bit) as above; R, Hq, scale are not used by the eviction.

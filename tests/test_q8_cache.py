@@ -975,6 +975,80 @@ def test_evict_keeps_nan_weights_and_all_protected_rows():
     assert torch.equal(s.k[1, :, :101], k0[1, :, :101])
 
 
+NAN_BITS = [0x7FFFFFFF, -1, 0x7FC00000, -0x400000, 0x7F800001]   # (0xffffffff, 0xffc00000)
+
+
+def plain_evict_any(P, keep, sink, recent, acc, pos, seen):
+    """plain_evict with NaN weights: behind the protected rows, before infinity, by index."""
+    def key(i):
+        nan = acc[i] != acc[i]
+        return (not (pos[i] < sink or pos[i] >= seen - recent), not nan, 0.0 if nan else -acc[i], i)
+
+    kept = set(sorted(range(P), key=key)[:keep])
+    return ([i for i in range(keep) if i not in kept], [i for i in range(keep, P) if i in kept])
+
+
+@gpu
+@pytest.mark.parametrize("q8", [True, False])
+@pytest.mark.parametrize("bits", [[b] for b in NAN_BITS] + [NAN_BITS])
+def test_evict_keeps_protected_rows_beside_any_nan(bits, q8):
+    """NaN weights of either sign and any payload (0x7fffffff is what the device's arithmetic
+    gives), more of them than places, the protected rows at the highest indexes: the protected
+    stay, then NaN by index, then infinities."""
+    s = Setup("one", 3, 1, [300, 300, 200], seed=36, q8=q8)
+    _evict_state(s)
+    s.acc[0] = INF
+    some = torch.tensor(bits, dtype=torch.int32, device=DEV)
+    for b, n in enumerate((260, 40, 90)):         # more than places, fewer, nearly all of them
+        at = torch.randperm(s.lens[b] - 20, generator=s.g, device=DEV)[:n]
+        pick = torch.randint(0, len(bits), (s.Hkv, n), generator=s.g, device=DEV)
+        s.acc[b].view(torch.int32)[:, at] = some[pick]
+    s.pos.copy_(torch.arange(s.cap, device=DEV).int().expand_as(s.pos))
+    s.seen.copy_(torch.tensor(s.lens, device=DEV).int()[:, None].expand_as(s.seen))
+    snap = _snapshot(s)
+    _evict(s, 100, 3, 20)
+    assert int(s.err) == 0 and s.plen.tolist() == [100, 100, 100]
+    for b, P in enumerate(s.lens):
+        for h in range(s.Hkv):
+            acc, pos = snap["acc"][b, h], snap["pos"][b, h]
+            holes, movers = plain_evict_any(P, 100, 3, 20, acc[:P].tolist(), pos[:P].tolist(), P)
+            src = torch.arange(s.cap, device=DEV)
+            src[holes] = torch.tensor(movers, dtype=torch.long, device=DEV)
+            assert torch.equal(s.pos[b, h], pos[src]), (b, h)
+            assert torch.equal(s.acc[b, h].view(torch.int32), acc[src].view(torch.int32))
+            have = set(s.pos[b, h, :100].tolist())
+            assert {0, 1, 2} | set(range(P - 20, P)) <= have
+            if not q8:
+                assert torch.equal(s.cache("k").rows(b, h), snap["k"][b][h][0][src])
+
+
+@gpu
+@pytest.mark.parametrize("kind,dtype", [("gqa", torch.bfloat16), ("latent", torch.bfloat16),
+                                        ("one", torch.float32)])
+def test_evict_after_the_weights_of_an_infinite_query(kind, dtype):
+    """One accepted query row is infinite: every weight of its KV head is NaN from then
+    on.  Rounds of weights, commit and eviction go on taking in the newest rows."""
+    s = Setup(kind, 1, 4, [120], extra=8, dtype=dtype, seed=37)
+    _weights_state(s, 3, [3])
+    s.acc.zero_()
+    s.pos.copy_(torch.arange(s.cap, device=DEV).int().expand_as(s.pos))
+    s.seen.fill_(120)
+    s.q[0, 0, 0] = INF                        # row 0 is on every path
+    for step in range(3):
+        _weights(s, 3, 0.5)
+        T.tsd_commit_path_q8(s.desc, 3, s.kt, s.vt, s.path, s.plength, s.k, s.v, s.ke, s.ve, s.plen,
+                             s.err, **s.paging)
+        torch.cuda.synchronize()
+        P, n = int(s.plen), int(s.seen[0, 0])
+        assert s.acc[0, 0, :P].isnan().sum() >= P - 3      # (row 0 weighs nothing behind itself)
+        _evict(s, 100, 2, 16)
+        for h in range(s.Hkv):
+            have = s.pos[0, h, :100].tolist()
+            assert len(set(have)) == 100
+            assert {0, 1} | set(range(n - 16, n)) <= set(have), (step, h)
+    assert int(s.err) == 0 and int(s.plen) == 100
+
+
 @gpu
 @pytest.mark.parametrize("q8", [True, False])
 def test_evict_again_and_again_at_a_budget(q8):

@@ -2,13 +2,14 @@
 // rows by the attention weight each cached token has received.
 //
 // For a request with more than `keep` rows, each KV head ranks its rows by
-// (protected first, weight desc, index asc) and keeps the first `keep`.  A row
-// is protected if its token is one of the first `sink` or the last `recent`
-// ones.  The kept rows that lie at or behind `keep` move, in order, into the
-// places (in order) of the dropped rows below it: no row that is read is also
-// written, no row that stays is touched, and in the steady state (a few new
-// rows a round) only as many rows move as arrived.  Attention does not depend
-// on the order of the cached rows; `pos` carries each row's token position.
+// (protected first, weight desc, index asc) and keeps the first `keep`; NaN, of
+// either sign, counts as more than infinity.  A row is protected if its token is
+// one of the first `sink` or the last `recent` ones.  The kept rows that lie at or
+// behind `keep` move, in order, into the places (in order) of the dropped rows
+// below it: no row that is read is also written, no row that stays is touched, and
+// in the steady state (a few new rows a round) only as many rows move as arrived.
+// Attention does not depend on the order of the cached rows; `pos` carries each
+// row's token position.
 //
 // select_kernel, a cluster of 1 to 8 CTAs per (head, request): the keep-th largest
 // 32-bit key by four 8-bit histogram rounds.  The histograms are private to 16 lanes
@@ -153,10 +154,12 @@ select_kernel(const __grid_constant__ EvictArgs a) {
 #pragma unroll
       for (int j = 0; j < kBatch; ++j) {
         const bool safe = p[j] < a.sink || p[j] >= recent0;
-        // (order keys of rows are above 0: the smallest is that of -NaN)
+        // (every NaN, of either sign, has one key, below the protected rows' and above
+        // infinity's; keys of rows are above 0: the smallest is that of -infinity)
         key[i0 + j] = base + 32 * (i0 + j) >= P ? 0u
                       : safe                    ? 0xffffffffu
-                                                : max(f32_order_key(w[j]), 1u);
+                      : w[j] != w[j]            ? 0xfffffffeu
+                                                : f32_order_key(w[j]);
       }
     }
   };
