@@ -147,20 +147,26 @@ class TreeVerifyStep:
         returned graph.  With ``cost_d``/``cost_v`` the tree is built by the
         cost-aware rule (rows past each request's count are padding).
         """
-        import torch
+        return self._record(probs.device, stream, lambda main: self._round(
+            probs, root_tok, q, kcache, vcache, prefix_len, ktree, vtree, logits, cost_d, cost_v,
+            main))
 
+    @staticmethod
+    def _record(device, stream, round_on):
+        """``round_on(stream)`` once as it is, then recorded as a CUDA graph."""
         if stream is None:
-            stream = torch.cuda.Stream(device=probs.device)
+            stream = torch.cuda.Stream(device=device)
+        # The round reads and writes what work queued on the caller's stream may
+        # still be reading and writing.
+        stream.wait_stream(torch.cuda.current_stream(device))
         # one eager warm-up: lazy set-up (function attributes, tensor-map
         # encoder lookup) must not happen during capture
         with torch.cuda.stream(stream):
-            self._round(probs, root_tok, q, kcache, vcache, prefix_len, ktree, vtree, logits,
-                        cost_d, cost_v, stream)
+            round_on(stream)
         stream.synchronize()
         graph = torch.cuda.CUDAGraph()
         with torch.cuda.graph(graph, stream=stream):
-            self._round(probs, root_tok, q, kcache, vcache, prefix_len, ktree, vtree, logits,
-                        cost_d, cost_v, stream)
+            round_on(stream)
         return graph
 
     def _round(self, probs, root_tok, q, kcache, vcache, prefix_len, ktree, vtree, logits,
@@ -307,17 +313,9 @@ class Q8TreeVerifyStep(TreeVerifyStep):
     def capture(self, probs, root_tok, q, cache, prefix_len, ktree, vtree, logits, weights=None,
                 stream=None):
         """Record ``run`` on the given tensors as one CUDA graph, as TreeVerifyStep.capture
-        (one round runs before the recording)."""
-        if stream is None:
-            stream = torch.cuda.Stream(device=probs.device)
-        args = (probs, root_tok, q, cache, prefix_len, ktree, vtree, logits, weights, stream)
-        with torch.cuda.stream(stream):
-            self.run(*args)
-        stream.synchronize()
-        graph = torch.cuda.CUDAGraph()
-        with torch.cuda.graph(graph, stream=stream):
-            self.run(*args)
-        return graph
+        (one round runs before the recording, behind the caller's queued work)."""
+        return self._record(probs.device, stream, lambda main: self.run(
+            probs, root_tok, q, cache, prefix_len, ktree, vtree, logits, weights, main))
 
     @classmethod
     def for_workload(cls, w, device="cuda", **held):
