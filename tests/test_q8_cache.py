@@ -8,6 +8,7 @@ kernels compute is held to bounds derived beside each check.
 import ctypes
 import math
 import random
+import threading
 
 import pytest
 import torch
@@ -845,6 +846,46 @@ def test_weights_skip_a_request_whose_commit_has_no_page(kind, q8):
     assert int(s.err) & T.TSD_DEV_ERR_MASK == T.TSD_DEV_ERR_BAD_PAGE
     assert torch.equal(s.acc[0], acc0[0]) and torch.equal(s.seen[0], seen0[0])
     assert torch.equal(s.seen[1], seen0[1] + 4)
+
+
+@gpu
+@pytest.mark.parametrize("kind,S", [("wide", (1, 7)), ("narrow", (1, 15)), ("wide", (9, 16))])
+def test_weights_from_two_host_threads(kind, S):
+    """Calls of different column counts, which take different amounts of shared memory, from
+    two host threads with streams and state of their own."""
+    sets = []
+    for i, n in enumerate(S):
+        s = Setup(kind, 1, 17, [200], extra=20, seed=70 + i)
+        _weights_state(s, n, [n])
+        s.S, s.stream, s.bad = n, torch.cuda.Stream(), []
+        s.state = (s.acc.clone(), s.pos.clone(), s.seen.clone())
+        sets.append(s)
+    torch.cuda.synchronize()
+
+    def run(s):
+        def p(t):
+            return ctypes.c_void_p(t.data_ptr())
+
+        args = (ctypes.byref(s.desc), s.S, p(s.q), p(s.k), p(s.ke), None, 0, 0, 0, p(s.plen), p(s.kt),
+                p(s.path), p(s.plength), p(s.lse), 0.0, p(s.acc), p(s.pos), p(s.seen), p(s.err),
+                ctypes.c_void_p(s.stream.cuda_stream))
+        for _ in range(6000):
+            status = T.lib.tsd_cache_weights_q8(*args)
+            if status != T.TSD_OK:
+                s.bad.append(status)
+
+    threads = [threading.Thread(target=run, args=(s,)) for s in sets]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert [len(s.bad) for s in sets] == [0, 0]
+    for s in sets:
+        assert int(s.err) == 0
+        acc0, pos0, seen0 = s.state
+        seen0 += 5999 * (s.S + 1)                 # (the last call's positions; decay 0)
+        _check_weights(s, acc0, pos0, seen0, 0.0)
 
 
 @gpu

@@ -409,10 +409,11 @@ bool launch_d(const tsd_attn_desc& d, const WeightArgs& a, int cols, cudaStream_
   CUtensorMap m;
   if (!encode_cache(&m, a, d.B, D, kQ8)) return false;
   constexpr int kPerSm = kBufCols == 128 ? 2 : 1;
+  constexpr long kSmem = 220 * 1024 / kPerSm;
   WeightPlan p{};
   p.cols = cols;
   const long tile = kWeightKeys * D * (kQ8 ? 1 : 2), q = (long)cols * D * 2;
-  p.ring = (int)((220 * 1024 / kPerSm - q - (long)sizeof(WeightSmem) - 1024) / tile);
+  p.ring = (int)((kSmem - q - (long)sizeof(WeightSmem) - 1024) / tile);
   if (p.ring > kMaxRing) p.ring = kMaxRing;
   // Splits as for the attention: waves of CTAs times (tiles of a CTA and about six
   // more for its set-up).
@@ -426,7 +427,8 @@ bool launch_d(const tsd_attn_desc& d, const WeightArgs& a, int cols, cudaStream_
   p.nsplit = (int)ceil_div(tiles, p.tiles);
   const size_t smem = (size_t)p.ring * tile + q + sizeof(WeightSmem) + 1024;
   const auto kern = weights_tc_kernel<D, kQ8, kBufCols>;
-  cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  // (the same for every call: another thread's may come between this and the launch)
+  cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
   launch(kern, dim3(p.nsplit, d.Hkv, d.B), dim3(kThreads), smem, st, m, a, p);
   return true;
 }
