@@ -544,9 +544,12 @@ tsd_status tsd_tree_verify_attn_q8(const tsd_attn_desc* desc, const void* q, con
  *   pos[P + j] = seen + j, then seen += L + 1
  * q, ktree, lse as given to and left by the verify call ([B][R][Hq][dk],
  * [B][R][Hkv][dk], [B][R][Hq]); 0 <= decay <= 1; accept_rows [B][S+1],
- * accept_len [B].  The other entries are left as they are.  A request whose
- * P + 1 + L passes cap, with a bad path or a bad page (the commit's among them), is
- * skipped and reported as by the commit.  No workspace.
+ * accept_len [B].  The other entries are left as they are.  A request that the
+ * commit skips (P + 1 + L past cap, a bad path, a bad page of the positions P..P+L)
+ * is skipped and reported as there.  A bad page that holds nothing but prefix does
+ * not stop the commit: it is reported as TSD_DEV_ERR_BAD_PAGE, acc[p], p < P, stays
+ * as it is (the round's lse is not valid), acc[P + j] = 0, pos and seen as above.
+ * No workspace.
  *
  * tsd_cache_evict cuts every request that holds more than `keep` rows to
  * `keep`, in place.  Each head ranks its rows by (protected first, acc desc,

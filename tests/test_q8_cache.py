@@ -849,6 +849,43 @@ def test_weights_skip_a_request_whose_commit_has_no_page(kind, q8):
 
 
 @gpu
+@pytest.mark.parametrize("q8", [True, False])
+@pytest.mark.parametrize("kind,dtype", [("gqa", torch.bfloat16), ("latent", torch.bfloat16),
+                                        ("one", torch.float32)])
+def test_weights_and_commit_take_the_same_requests(kind, dtype, q8):
+    """A page missing early in the prefix does not stop the commit, so the new rows get their
+    positions, and weight 0; the request's other weights stay as they were.  The rest of the
+    batch is as without that page missing."""
+    def one(bad):
+        s = Setup(kind, 3, 4, [300], extra=84, page=128, dtype=dtype, seed=28, q8=q8)
+        _weights_state(s, 3, [2, 1, 3])
+        if bad:
+            s.table[1, 0] = bad
+        before = [t.clone() for t in (s.acc, s.pos, s.seen)]
+        _weights(s, 3, 0.5)
+        if q8:
+            T.tsd_commit_path_q8(s.desc, 3, s.kt, s.vt, s.path, s.plength, s.k, s.v, s.ke, s.ve,
+                                 s.plen, s.err, **s.paging)
+        else:
+            T.tsd_commit_path_paged(s.desc, 3, s.kt, s.vt, s.path, s.plength, s.k, s.v, s.table,
+                                    s.page, s.plen, s.err)
+        torch.cuda.synchronize()
+        return s, before
+
+    good, _ = one(0)
+    assert int(good.err) == 0
+    for bad in (-1, 10 ** 6):
+        s, (acc0, pos0, seen0) = one(bad)
+        assert int(s.err) == T.TSD_DEV_ERR_BAD_PAGE | 1
+        assert s.plen.tolist() == [303, 302, 304] == good.plen.tolist()
+        assert torch.equal(s.seen, good.seen) and torch.equal(s.pos, good.pos)
+        assert torch.equal(s.acc[[0, 2]], good.acc[[0, 2]])
+        want = acc0[1].clone()
+        want[:, 300:302] = 0.0
+        assert torch.equal(s.acc[1], want)
+
+
+@gpu
 @pytest.mark.parametrize("kind,S", [("wide", (1, 7)), ("narrow", (1, 15)), ("wide", (9, 16))])
 def test_weights_from_two_host_threads(kind, S):
     """Calls of different column counts, which take different amounts of shared memory, from

@@ -45,6 +45,10 @@ weights_simt_kernel(const __grid_constant__ WeightArgs a) {
     if (on_path && tid == 0) report_error(a.err, -L, b);
     return;
   }
+  if (path.blind) {
+    if (on_path) unweighed_path(a, b, hk, P, L);
+    return;
+  }
   const int nkeys = on_path ? L + 1 : min(kWeightKeys, P - k0);
   const int key = tid & (kWeightKeys - 1), half = tid >> 7;
   const int ncol = (L + 1) * a.g;

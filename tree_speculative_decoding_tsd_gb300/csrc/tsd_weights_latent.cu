@@ -72,6 +72,10 @@ weights_latent_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_con
     if (on_path && tid == 0) report_error(a.err, -L, b);
     return;
   }
+  if (s.path.blind) {
+    if (on_path) unweighed_path(a, b, hk, P, L);
+    return;
+  }
   const int nkeys = on_path ? L + 1 : min(kWeightKeys, P - k0);
   const int ncol = (L + 1) * a.g, groups = (ncol + kCols - 1) / kCols;
   const long head = (long)b * a.map.Hkv + hk;

@@ -83,7 +83,7 @@ weights_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
     const int pos = (t0 + t) * kWeightKeys, g = slots0 + t, sl = g % p.ring;
     int y = pos, z = (int)head;
     if (a.map.page_size) {
-      const long r = max(a.map.row(b, hk, pos), 0l);        // (weight_path refuses missing pages)
+      const long r = max(a.map.row(b, hk, pos), 0l);        // (weight_path finds missing pages)
       y = (int)(r % a.map.page_size);
       z = (int)(r / a.map.page_size);
     }
@@ -108,8 +108,9 @@ weights_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
     for (int t = 0; t < early; ++t) load_k(t);
   }
   const int L = weight_path(a, b, P, s.path);
-  if (L < 0) {                                              // the whole request is skipped
-    if (with_path && tid == 0) report_error(a.err, -L, b);
+  if (L < 0 || s.path.blind) {                              // nothing is weighed
+    if (L >= 0 && with_path) unweighed_path(a, b, hk, P, L);
+    else if (with_path && tid == 0) report_error(a.err, -L, b);
     if (tid == kTma * 32)
       for (int t = 0; t < early; ++t) mbar_wait(bar(BAR_FULL + slots0 + t), 0);
     return;
