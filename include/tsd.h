@@ -497,7 +497,10 @@ tsd_status tsd_commit_path(const tsd_attn_desc* desc, int S, const void* ktree,
  * are in dtype.  Rows behind prefix_len are not used, whatever they hold; nor
  * are scratch rows that no row sees.  A NaN or an infinity in a scratch row
  * reaches the outputs of the rows that see it and no others.  fp32 inputs are
- * computed in fp32.  ws: tsd_verify_q8_workspace_size(desc) bytes (0 is a valid size);
+ * computed in fp32.  bf16 rows of q and ktree enter the scores as two e4m3 numbers per
+ * element: exactly, but for elements below 2^-9 of their row's largest magnitude, which
+ * are off by at most 2^-17 of it (tsd_cache_weights_q8 of heads of 64 and 128 dims: the
+ * same).  ws: tsd_verify_q8_workspace_size(desc) bytes (0 is a valid size);
  * calls that may overlap, captured ones among them, each need their own.
  * -------------------------------------------------------------------------- */
 #define TSD_Q8_BLOCK 64

@@ -945,6 +945,63 @@ def test_weights_ignore_what_lies_behind_the_prefix(q8):
     _check_weights(s, acc0, pos0, seen0, 1.0)
 
 
+def as_two_codes(x):
+    """bf16 rows [..][d] as the sums of two e4m3 numbers that the products take, by their
+    definition: the largest element scaled into [2^7, 2^8), the nearest code, and the nearest
+    code of what is left.  Off by at most half of e4m3's smallest step, 2^-10, where the
+    largest is at least 2^7: 2^-17 of it."""
+    y = x.double()
+    top = y.abs().amax(-1, keepdim=True)
+    f = torch.exp2(8.0 - torch.frexp(top).exponent.double())
+    hi = nearest_code(y * f)
+    z = (hi + nearest_code(y * f - hi)) / f
+    assert ((z - y).abs() <= 2.0 ** -17 * top).all()
+    assert torch.equal(z.to(x.dtype).double(), z)          # (no more bits than before)
+    return z.to(x.dtype)
+
+
+def _dominant(s, by):
+    """Each row of q (of ktree, unless it is also a value) gets one element `by` times its
+    others, where every key (query) is zero: the others alone make the scores.  Then the rows
+    as the products take them."""
+    s.q[..., 3] = by
+    s.k[..., 3] = 0
+    s.kt[..., 3] = 0
+    if s.latent:
+        return as_two_codes(s.q), s.kt
+    s.q[..., -1] = 0
+    s.kt[..., -1] = by
+    return as_two_codes(s.q), as_two_codes(s.kt)
+
+
+@gpu
+@pytest.mark.parametrize("kind,R", [("gqa", 2), ("gqa", 20), ("narrow", 2), ("narrow", 9), ("latent", 2),
+                                    ("latent-few", 3)])
+@pytest.mark.parametrize("by", [2.0 ** 8, 2.0 ** 12, 2.0 ** 15])
+def test_attention_of_rows_with_a_dominant_element(kind, R, by):
+    """The small elements are rounded as documented, and by nothing else: the outputs are
+    within the bounds of the rounded rows."""
+    s = Setup(kind, 2, R, [400, 90], seed=17)
+    q, kt = _dominant(s, by)
+    assert not torch.equal(q, s.q)
+    got = s.attn()
+    s.q, s.kt = q, kt
+    s.check_attn(*got)
+
+
+@gpu
+@pytest.mark.parametrize("kind", ["gqa", "narrow", "wide"])
+def test_weights_of_rows_with_a_dominant_element(kind):
+    s = Setup(kind, 2, 9, [300, 64], extra=20, seed=29)
+    _weights_state(s, 4, [4, 2])
+    rounded = _dominant(s, 2.0 ** 12)
+    acc0, pos0, seen0 = s.acc.clone(), s.pos.clone(), s.seen.clone()
+    _weights(s, 4, 0.5)
+    torch.cuda.synchronize()
+    s.q, s.kt = rounded
+    _check_weights(s, acc0, pos0, seen0, 0.5)
+
+
 # --------------------------------------------------------------- eviction --
 
 def _evict_state(s, sharp=True):

@@ -121,7 +121,9 @@ __device__ __forceinline__ uint64_t row_desc(uint32_t addr) {
          (1ull << 46) | (4ull << 61);
 }
 
-// Sixteen bf16 times f as e4m3 numbers hi and lo with hi + lo = x f.
+// Sixteen bf16 times f, which puts their row's largest into [128, 256), as e4m3 numbers
+// hi and lo.  hi + lo = x f down to e4m3's smallest step: off by at most 2^-10, 2^-17 of
+// the largest, for elements below 2^-9 of it (tsd_q8_tc.cu).
 __device__ __forceinline__ void split16(const uint4 (&w)[2], float f, uint4& hi, uint4& lo) {
   uint32_t h[4], l[4];
 #pragma unroll
