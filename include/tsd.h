@@ -500,7 +500,12 @@ tsd_status tsd_commit_path(const tsd_attn_desc* desc, int S, const void* ktree,
  * computed in fp32.  bf16 rows of q and ktree enter the scores as two e4m3 numbers per
  * element: exactly, but for elements below 2^-9 of their row's largest magnitude, which
  * are off by at most 2^-17 of it (tsd_cache_weights_q8 of heads of 64 and 128 dims: the
- * same).  ws: tsd_verify_q8_workspace_size(desc) bytes (0 is a valid size);
+ * same).  bf16 inputs: probabilities enter the products with the values in fp16, to
+ * 2^-12 of each and, where that is more, so that an output is off by n 2^-23 2^u at most:
+ * n the keys, u the largest over the request's value blocks (e - 127) and over the
+ * scratch rows that some row sees (largest magnitude in [2^(u+8), 2^(u+9))).  Values 2^20
+ * and more below the largest that the request holds lose bits to that, also in rows that
+ * give the largest no weight.  ws: tsd_verify_q8_workspace_size(desc) bytes (0 is a valid size);
  * calls that may overlap, captured ones among them, each need their own.
  * -------------------------------------------------------------------------- */
 #define TSD_Q8_BLOCK 64

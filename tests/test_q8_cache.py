@@ -523,6 +523,26 @@ def test_attention_keeps_small_values_beside_large_ones(kind):
 
 
 @gpu
+@pytest.mark.parametrize("kind,R", [("gqa", 2), ("gqa", 20), ("narrow", 3), ("latent", 2)])
+@pytest.mark.parametrize("tree", [False, True])
+def test_attention_of_values_far_below_the_largest(kind, R, tree):
+    """Value blocks (or one scratch row that one row sees) up to 2^24 times the others: what
+    the small ones lose stays within the documented bound."""
+    s = Setup(kind, 2, R, [1500, 300], seed=18, spread=0)
+    if tree:
+        s.set_masks([[0] + [1 << (r - 1) for r in range(1, R)]] * 2)
+        (s.kt if s.latent else s.vt)[:, -1, :, : s.dv] *= 2.0 ** (2 if s.latent else 24)
+    elif s.latent:
+        s.ke[..., ::5] += 6
+    else:
+        s.ve[..., ::3] += 24
+    if s.latent:
+        s.q.mul_(2.0 ** -6)
+    out, lse = s.attn()
+    s.check_attn(out, lse)
+
+
+@gpu
 @pytest.mark.parametrize("kind,dtype", [("gqa", torch.bfloat16), ("latent", torch.bfloat16),
                                         ("gqa", torch.float32), ("latent-few", torch.bfloat16)])
 def test_attention_leaves_out_what_no_row_sees(kind, dtype):
