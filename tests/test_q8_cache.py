@@ -9,6 +9,7 @@ import ctypes
 import math
 import random
 import threading
+import time
 
 import pytest
 import torch
@@ -619,6 +620,28 @@ def test_attention_with_late_large_scores(kind):
 
 
 @gpu
+@pytest.mark.parametrize("kind,R,page", [("gqa", 1, 0), ("gqa", 20, 128), ("narrow", 2, 128),
+                                         ("narrow", 20, 0), ("latent", 3, 0), ("latent-few", 2, 128)])
+def test_attention_waits_give_up_at_the_budget(kind, R, page):
+    """A budget of a few clock cycles: the softmax's first wait on a product gives up, every
+    role stops, and the kernel ends at once with a code in err.  The next call is as ever."""
+    s = Setup(kind, 3, R, [2500, 700, 0], page=page, seed=19)
+    want = s.attn()
+    start = time.monotonic()
+    with T.wait_budget(16):
+        s.attn()
+    assert time.monotonic() - start < 0.9             # (no wait of the default budget ran out)
+    e = int(s.err)
+    assert e & T.TSD_DEV_ERR_MASK == T.TSD_DEV_ERR_TIMEOUT and e & 0xFFFFFF < 3, hex(e)
+    assert T.tsd_set_wait_budget(0) == 0              # the context manager restored it
+    s.err.zero_()
+    got = s.attn()
+    assert int(s.err) == 0
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    s.check_attn(*got)
+
+
+@gpu
 @pytest.mark.parametrize("kind,page", [("gqa", 128), ("latent", 128), ("one", 256)])
 def test_attention_reports_a_page_outside_the_pool(kind, page):
     s = Setup(kind, 2, 3, [600, 500], page=page, seed=12)
@@ -943,6 +966,34 @@ def test_weights_from_two_host_threads(kind, S):
         acc0, pos0, seen0 = s.state
         seen0 += 5999 * (s.S + 1)                 # (the last call's positions; decay 0)
         _check_weights(s, acc0, pos0, seen0, 0.0)
+
+
+@gpu
+@pytest.mark.parametrize("q8", [True, False])
+@pytest.mark.parametrize("kind,S", [("gqa", 3), ("wide", 9), ("narrow", 4)])
+def test_weights_waits_give_up_at_the_budget(kind, S, q8):
+    """As the attention's; the tokens seen stay as they were, and a call on the state of before
+    is exact."""
+    s = Setup(kind, 2, 10, [2500, 700], extra=20, seed=30, q8=q8)
+    _weights_state(s, S, [S, 1])
+    state = (s.acc, s.pos, s.seen)
+    before = [t.clone() for t in state]
+    torch.cuda.synchronize()
+    start = time.monotonic()
+    with T.wait_budget(16):
+        _weights(s, S, 0.5)
+        torch.cuda.synchronize()
+    assert time.monotonic() - start < 0.9
+    e = int(s.err)
+    assert e & T.TSD_DEV_ERR_MASK == T.TSD_DEV_ERR_TIMEOUT and e & 0xFFFFFF < 2, hex(e)
+    assert torch.equal(s.seen[e & 1], before[2][e & 1])
+    s.err.zero_()
+    for t, b in zip(state, before):
+        t.copy_(b)
+    _weights(s, S, 0.5)
+    torch.cuda.synchronize()
+    assert int(s.err) == 0
+    _check_weights(s, *before, 0.5)
 
 
 @gpu

@@ -191,16 +191,16 @@ class verify_path:
 
 
 def tsd_set_wait_budget(cycles: int) -> int:
-    """Budget (SM clock cycles) of the tcgen05 verify kernel's pipeline waits
-    for the calls that follow; 0 restores the default.  Returns the previous
-    setting."""
+    """Budget (SM clock cycles) of the pipeline waits of the tcgen05 verify, 8-bit
+    attention and weights kernels for the calls that follow; 0 restores the
+    default.  Returns the previous setting."""
     if int(cycles) < 0:
         raise ValueError("wait budget must be >= 0")
     return int(_L().tsd_set_wait_budget(int(cycles)))
 
 
 class wait_budget:
-    """Context manager: the verify calls inside use the given wait budget."""
+    """Context manager: the calls inside use the given wait budget."""
 
     def __init__(self, cycles):
         self.cycles = cycles

@@ -8,6 +8,10 @@
 
 namespace tsd {
 
+// Clock cycles that a pipeline wait of a tcgen05 kernel may take: what
+// tsd_set_wait_budget has set, kWaitCycles by default.
+long long wait_budget();
+
 // Non-null and 16-byte aligned.
 inline bool ok_ptr(const void* p) { return p != nullptr && (((uintptr_t)p) & 15u) == 0; }
 

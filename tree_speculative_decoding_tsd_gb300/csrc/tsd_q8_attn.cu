@@ -494,6 +494,7 @@ extern "C" tsd_status tsd_tree_verify_attn_q8(const tsd_attn_desc* d, const void
   a.tree_split = p.tree_split;
   a.by_length = p.by_length;
   a.qscale = d->scale * 1.4426950408889634f;
+  a.wait_cycles = wait_budget();
   const cudaStream_t st = (cudaStream_t)stream;
   if (p.path != kQ8Simt) {
     const bool launched = p.path == kQ8Latent ? launch_q8_latent(*d, a, p, st)

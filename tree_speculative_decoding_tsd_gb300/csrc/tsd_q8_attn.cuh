@@ -25,6 +25,7 @@ struct Q8AttnArgs {
   int nsplit, split_len, nrg, rb, tree_split;
   int by_length;              // grid z is a rank in (prefix length desc, index asc) order
   float qscale;               // softmax scale * log2(e)
+  long long wait_cycles;      // of a pipeline wait (kernels that poll)
 };
 
 enum Q8Path { kQ8Simt = 0, kQ8Few = 1, kQ8Rows = 2, kQ8Latent = 3 };

@@ -84,7 +84,7 @@ struct FewLayout {
 enum { BAR_K_FULL = 0, BAR_K_EMPTY = 4, BAR_V_FULL = 8, BAR_V_EMPTY = 10, BAR_S_FULL = 12,
        BAR_P_FULL = 14, BAR_FINAL = 16, BAR_O_DONE = 18, BAR_T_FULL = 19 };
 
-template <int D>
+template <int D, bool kPoll>
 __global__ void __launch_bounds__(kThreads, 1)
 q8_few_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ Q8AttnArgs a) {
   using L = FewLayout<D>;
@@ -107,6 +107,12 @@ q8_few_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
   int* s_top = (int*)(smem + L::off_top);           // U by widening warp
   const uint32_t bar0 = sbase + L::off_bar;
   auto bar = [&](int i) { return bar0 + 8u * i; };
+  auto wait_ready = [&](uint32_t at, uint32_t parity) {
+    return phase_ready<kPoll>(at, parity, a.wait_cycles);
+  };
+  auto wait_timed = [&](uint32_t at, uint32_t parity) {
+    return phase_timed<kPoll>(at, parity, a.wait_cycles);
+  };
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int hk = blockIdx.x, sp = blockIdx.y;
@@ -232,7 +238,7 @@ q8_few_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
       int loaded = min(kRing, n_pre);          // by the set-up
       for (int t = loaded; t < n_pre && !flags[1]; ++t) {
         const int sl = t % kRing;
-        if (!mbar_wait(bar(BAR_K_EMPTY + sl), (t / kRing - 1) & 1)) {
+        if (!wait_timed(bar(BAR_K_EMPTY + sl), (t / kRing - 1) & 1)) {
           flags[1] = 1;
           break;
         }
@@ -253,7 +259,7 @@ q8_few_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
     const int tree_at = max(n_pre - 2, 0) & ~1; // the tree's keys are made two tiles early
     bool ok = true;
     auto stage_free = [&](int t) {
-      return t < 2 || __all_sync(kFull, mbar_wait(bar(BAR_V_EMPTY + (t & 1)), ((t >> 1) - 1) & 1));
+      return t < 2 || __all_sync(kFull, wait_timed(bar(BAR_V_EMPTY + (t & 1)), ((t >> 1) - 1) & 1));
     };
     auto stage_written = [&](int t) {
       asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
@@ -263,9 +269,9 @@ q8_few_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
     for (int t0 = 0; ok && t0 < max(n_pre, 1); t0 += kDepth) {
       if (with_tree && t0 == tree_at) {
         const int s0 = n_pre, s1 = n_pre + 1;
-        ok = (s0 < kRing || __all_sync(kFull, mbar_wait(bar(BAR_K_EMPTY + s0 % kRing),
+        ok = (s0 < kRing || __all_sync(kFull, wait_timed(bar(BAR_K_EMPTY + s0 % kRing),
                                                         (s0 / kRing - 1) & 1))) &&
-             (s1 < kRing || __all_sync(kFull, mbar_wait(bar(BAR_K_EMPTY + s1 % kRing),
+             (s1 < kRing || __all_sync(kFull, wait_timed(bar(BAR_K_EMPTY + s1 % kRing),
                                                         (s1 / kRing - 1) & 1)));
         if (!ok) break;
         tree_keys<D>(a, b, hk, wt, kWideThreads, kt_in,
@@ -515,7 +521,7 @@ q8_few_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
 
     // ------------------------------------- epilogue: the two streams joined
     failed = __any_sync(kFull, failed);
-    const bool ok = !failed && __all_sync(kFull, mbar_wait(bar(BAR_O_DONE), 0));
+    const bool ok = !failed && __all_sync(kFull, wait_timed(bar(BAR_O_DONE), 0));
     fence_after();
 #pragma unroll
     for (int i = 0; i < N; i += 4) {
@@ -607,7 +613,7 @@ q8_few_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
 template <int D>
 void launch_few(const CUtensorMap& kmap, const Q8AttnArgs& a, const Q8Plan& p, cudaStream_t st) {
   const uint32_t smem = FewLayout<D>::total + 1024;
-  const auto kern = q8_few_kernel<D>;
+  const auto kern = a.wait_cycles < kWaitCycles ? q8_few_kernel<D, true> : q8_few_kernel<D, false>;
   cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   launch(kern, dim3(a.map.Hkv, p.nsplit, a.B), dim3(kThreads), smem, st, kmap, a);
 }

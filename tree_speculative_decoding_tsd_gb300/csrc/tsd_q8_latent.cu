@@ -83,6 +83,7 @@ __device__ __forceinline__ uint32_t piece_offset(int r, int u) {
                 : 4 * kPiece + unit_offset<64>(r, u - 32);
 }
 
+template <bool kPoll>
 __global__ void __launch_bounds__(kThreads, 1)
 q8_latent_kernel(const __grid_constant__ LatentMaps maps, const __grid_constant__ Q8AttnArgs a) {
   if (threadIdx.x == kTma * 32) {
@@ -112,6 +113,12 @@ q8_latent_kernel(const __grid_constant__ LatentMaps maps, const __grid_constant_
   int* s_top = (int*)(smem + kOffTop);
   const uint32_t bar0 = sbase + kOffBar;
   auto bar = [&](int i) { return bar0 + 8u * i; };
+  auto wait_ready = [&](uint32_t at, uint32_t parity) {
+    return phase_ready<kPoll>(at, parity, a.wait_cycles);
+  };
+  auto wait_timed = [&](uint32_t at, uint32_t parity) {
+    return phase_timed<kPoll>(at, parity, a.wait_cycles);
+  };
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int hk = blockIdx.y / a.nrg, rg = blockIdx.y % a.nrg, sp = blockIdx.x;
@@ -294,7 +301,7 @@ q8_latent_kernel(const __grid_constant__ LatentMaps maps, const __grid_constant_
       const int total = kPieces * n_pre;
       int loaded = min(kSlots, total);         // by the set-up
       for (int g = loaded; g < total && !flags[1]; ++g) {
-        if (!mbar_wait(bar(BAR_K_EMPTY + g % kSlots), (g / kSlots - 1) & 1)) {
+        if (!wait_timed(bar(BAR_K_EMPTY + g % kSlots), (g / kSlots - 1) & 1)) {
           flags[1] = 1;
           break;
         }
@@ -319,7 +326,7 @@ q8_latent_kernel(const __grid_constant__ LatentMaps maps, const __grid_constant_
         for (int i = 0; i < 2 * kPieces; ++i) {
           const int g = kPieces * n_pre + i, sl = g % kSlots;
           if (g >= kSlots &&
-              !__all_sync(kFull, mbar_wait(bar(BAR_K_EMPTY + sl), (g / kSlots - 1) & 1))) {
+              !__all_sync(kFull, wait_timed(bar(BAR_K_EMPTY + sl), (g / kSlots - 1) & 1))) {
             ok = false;
             break;
           }
@@ -346,7 +353,7 @@ q8_latent_kernel(const __grid_constant__ LatentMaps maps, const __grid_constant_
 #pragma unroll 1
       for (int u = 0; u < kUnits; ++u) {
         const int g = kUnits * t + u, st = g & 1;
-        if (g >= 2 && !__all_sync(kFull, mbar_wait(bar(BAR_V_EMPTY + st), ((g >> 1) - 1) & 1))) {
+        if (g >= 2 && !__all_sync(kFull, wait_timed(bar(BAR_V_EMPTY + st), ((g >> 1) - 1) & 1))) {
           ok = false;
           break;
         }
@@ -609,7 +616,7 @@ q8_latent_kernel(const __grid_constant__ LatentMaps maps, const __grid_constant_
 
     // ---------------------------------------------------------- epilogue
     failed = __any_sync(kFull, failed);
-    const bool ok = !failed && __all_sync(kFull, mbar_wait(bar(BAR_O_DONE), 0));
+    const bool ok = !failed && __all_sync(kFull, wait_timed(bar(BAR_O_DONE), 0));
     fence_after();
     const bool stop = wg_bar_or(wg, !ok || flags[1] != 0);
     if (!stop) {
@@ -689,9 +696,9 @@ bool launch_q8_latent(const tsd_attn_desc& d, const Q8AttnArgs& a, const Q8Plan&
   if (encode_fn() == nullptr || !encode_keys(&m.wide, a, kDK, 128) ||
       !encode_keys(&m.last, a, kDK, 64))
     return false;
-  cudaFuncSetAttribute(q8_latent_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                       (int)kTotal + 1024);
-  launch(q8_latent_kernel, dim3(p.nsplit, a.map.Hkv * p.nrg, a.B), dim3(kThreads), kTotal + 1024, st,
+  const auto kern = a.wait_cycles < kWaitCycles ? q8_latent_kernel<true> : q8_latent_kernel<false>;
+  cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kTotal + 1024);
+  launch(kern, dim3(p.nsplit, a.map.Hkv * p.nrg, a.B), dim3(kThreads), kTotal + 1024, st,
          m, a);
   return true;
 }

@@ -149,7 +149,7 @@ __device__ __forceinline__ void mma_f16_ta(uint32_t d, uint32_t a, uint64_t b, u
       "r"(a), "l"(b), "r"(idesc), "r"(acc));
 }
 
-template <int D>
+template <int D, bool kPoll>
 __global__ void __launch_bounds__(kThreads, 1)
 q8_rows_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ Q8AttnArgs a) {
   using L = RowLayout<D>;
@@ -171,6 +171,12 @@ q8_rows_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
   int* s_top = (int*)(smem + L::off_top);           // U by widening warp
   const uint32_t bar0 = sbase + L::off_bar;
   auto bar = [&](int i) { return bar0 + 8u * i; };
+  auto wait_ready = [&](uint32_t at, uint32_t parity) {
+    return phase_ready<kPoll>(at, parity, a.wait_cycles);
+  };
+  auto wait_timed = [&](uint32_t at, uint32_t parity) {
+    return phase_timed<kPoll>(at, parity, a.wait_cycles);
+  };
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int hk = blockIdx.x / a.nrg, rg = blockIdx.x % a.nrg, sp = blockIdx.y;
@@ -332,7 +338,7 @@ q8_rows_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
       int loaded = min(kRing, n_pre);          // by the set-up
       for (int t = loaded; t < n_pre && !flags[1]; ++t) {
         const int sl = t % kRing;
-        if (!mbar_wait(bar(BAR_K_EMPTY + sl), (t / kRing - 1) & 1)) {
+        if (!wait_timed(bar(BAR_K_EMPTY + sl), (t / kRing - 1) & 1)) {
           flags[1] = 1;
           break;
         }
@@ -355,9 +361,9 @@ q8_rows_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
       const int st = t % kStages;
       if (with_tree && t == tree_at) {
         const int s0 = n_pre, s1 = n_pre + 1;
-        if ((s0 >= kRing && !__all_sync(kFull, mbar_wait(bar(BAR_K_EMPTY + s0 % kRing),
+        if ((s0 >= kRing && !__all_sync(kFull, wait_timed(bar(BAR_K_EMPTY + s0 % kRing),
                                                          (s0 / kRing - 1) & 1))) ||
-            (s1 >= kRing && !__all_sync(kFull, mbar_wait(bar(BAR_K_EMPTY + s1 % kRing),
+            (s1 >= kRing && !__all_sync(kFull, wait_timed(bar(BAR_K_EMPTY + s1 % kRing),
                                                          (s1 / kRing - 1) & 1)))) {
           flags[1] = 1;
           break;
@@ -620,7 +626,7 @@ q8_rows_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
     }
 
     // ------------------------------------- epilogue: the two streams joined
-    const bool ok = !failed && __all_sync(kFull, mbar_wait(bar(BAR_O_DONE), 0));
+    const bool ok = !failed && __all_sync(kFull, wait_timed(bar(BAR_O_DONE), 0));
     fence_after();
     s_ml[p * kRows + row] = make_float2(m, l);
     uint32_t stop;
@@ -695,7 +701,7 @@ q8_rows_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
 template <int D>
 void launch_rows(const CUtensorMap& kmap, const Q8AttnArgs& a, const Q8Plan& p, cudaStream_t st) {
   const uint32_t smem = RowLayout<D>::total + 1024;
-  const auto kern = q8_rows_kernel<D>;
+  const auto kern = a.wait_cycles < kWaitCycles ? q8_rows_kernel<D, true> : q8_rows_kernel<D, false>;
   cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   launch(kern, dim3(a.map.Hkv * p.nrg, p.nsplit, a.B), dim3(kThreads), smem, st, kmap, a);
 }

@@ -64,9 +64,20 @@ __device__ __forceinline__ int request_at(const Q8AttnArgs& a, int z, int& P, vo
   return b;
 }
 
-// Wait for a phase that is usually complete already: one look before the timed
+// The kernels' pipeline waits.  kPoll: with the budget of tsd_set_wait_budget, in an
+// instantiation of its own, so that the usual one has neither the budget nor the polling
+// loop in its code (65-row trees over 8 x 32k keys: 321 us so, 324 us with the limit and
+// the sleep as kernel arguments).
+template <bool kPoll>
+__device__ __forceinline__ bool phase_timed(uint32_t bar, uint32_t parity, long long budget) {
+  if constexpr (kPoll) return mbar_poll(bar, parity, budget);
+  else return mbar_wait(bar, parity);
+}
+// The same for a phase that is usually complete already: one look before the timed
 // wait.
-__device__ __forceinline__ bool wait_ready(uint32_t bar, uint32_t parity) {
+template <bool kPoll>
+__device__ __forceinline__ bool phase_ready(uint32_t bar, uint32_t parity, long long budget) {
+  if constexpr (kPoll) return mbar_poll(bar, parity, budget);
   uint32_t ok;
   asm volatile(
       "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"

@@ -180,6 +180,10 @@ verify_generic_kernel(const __grid_constant__ VerifyArgs a) {
 static std::atomic<int> g_forced_path{TSD_PATH_AUTO};
 // Budget of the tcgen05 kernels' pipeline waits, in clock cycles (0 = default).
 static std::atomic<long long> g_wait_budget{0};
+long long wait_budget() {
+  const long long wb = g_wait_budget.load(std::memory_order_relaxed);
+  return wb > 0 && wb < kWaitCycles ? wb : kWaitCycles;
+}
 
 static int choose_path(const tsd_attn_desc& d, int M) {
   const bool gqa_bf16 = d.dtype == TSD_BF16 && !d.v_aliases_k && d.dk == d.dv;
@@ -394,10 +398,7 @@ static tsd_status verify_impl(const tsd_attn_desc* d, const void* q, const void*
   a.tree_split = p.tree_split;
   a.qscale = d->scale * 1.4426950408889634f;
   a.err = err;
-  {
-    const long long wb = g_wait_budget.load(std::memory_order_relaxed);
-    a.wait_cycles = wb > 0 && wb < kWaitCycles ? wb : kWaitCycles;
-  }
+  a.wait_cycles = wait_budget();
   a.page_table = paged ? page_table : nullptr;
   a.max_pages = paged ? max_pages : 0;
   a.page_size = paged ? page_size : 0;

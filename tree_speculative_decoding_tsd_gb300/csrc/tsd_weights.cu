@@ -181,6 +181,7 @@ tsd_status weights_impl(const tsd_attn_desc* d, int S, const void* q, const void
   a.S = S;
   a.decay = decay;
   a.qscale = d->scale * kLog2e;
+  a.wait_cycles = wait_budget();
   const cudaStream_t st = (cudaStream_t)stream;
   const bool f32 = d->dtype == TSD_F32;
   if (launch_weights_tc(*d, a, st) || launch_weights_latent(*d, a, st)) return cuda_status();

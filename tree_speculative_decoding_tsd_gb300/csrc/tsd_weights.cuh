@@ -22,6 +22,7 @@ struct WeightArgs {
   int R, Hq, g, S;
   float decay;
   float qscale;              // softmax scale * log2(e)
+  long long wait_cycles;     // of a pipeline wait (kernels that poll)
 };
 
 constexpr int kWeightKeys = 128;     // cached rows per tile

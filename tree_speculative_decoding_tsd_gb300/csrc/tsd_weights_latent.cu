@@ -44,7 +44,7 @@ static_assert(kTotal + 1024 <= 232448, "shared memory budget");
 enum { BAR_Q_FULL = 0, BAR_Q_EMPTY = kPieces, BAR_S_FULL = 2 * kPieces, BAR_S_EMPTY = BAR_S_FULL + 2,
        BAR_K_FULL = BAR_S_EMPTY + 2, BAR_FINAL = BAR_K_FULL + 1 };
 
-template <bool kQ8>
+template <bool kQ8, bool kPoll>
 __global__ void __launch_bounds__(kThreads, 1)
 weights_latent_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap qmap,
                       const __grid_constant__ WeightArgs a) {
@@ -60,6 +60,12 @@ weights_latent_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_con
   LatentSmem& s = *(LatentSmem*)(smem + kOffMisc);
   volatile uint32_t* abort = &s.abort;
   auto bar = [&](int i) { return su32(&s.bars[i]); };
+  auto wait_ready = [&](uint32_t at, uint32_t parity) {
+    return phase_ready<kPoll>(at, parity, a.wait_cycles);
+  };
+  auto wait_timed = [&](uint32_t at, uint32_t parity) {
+    return phase_timed<kPoll>(at, parity, a.wait_cycles);
+  };
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int hk = blockIdx.y, b = blockIdx.z;
@@ -180,7 +186,7 @@ weights_latent_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_con
       bool ok = true;
       for (int n = 1; ok && n < groups && !*abort; ++n) {
         for (int j = 0; j < kPieces; ++j) {
-          if (!mbar_wait(bar(BAR_Q_EMPTY + j), (n - 1) & 1)) {
+          if (!wait_timed(bar(BAR_Q_EMPTY + j), (n - 1) & 1)) {
             ok = false;
             // (the pieces of this group before j are in flight)
             for (int i = 0; i < j; ++i) mbar_wait(bar(BAR_Q_FULL + i), n & 1);
@@ -341,7 +347,8 @@ bool launch_latent(const tsd_attn_desc& d, const WeightArgs& a, cudaStream_t st)
   if (!encode_queries(&q, a, d.B)) return false;
   if (kQ8) k = q;                                           // (not used)
   else if (!encode_latent(&k, a, d.B)) return false;
-  const auto kern = weights_latent_kernel<kQ8>;
+  const auto kern = a.wait_cycles < kWaitCycles ? weights_latent_kernel<kQ8, true>
+                                                : weights_latent_kernel<kQ8, false>;
   cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kTotal + 1024);
   const dim3 grid((unsigned)ceil_div(d.cap, kWeightKeys) + 1, d.Hkv, d.B);
   launch(kern, grid, dim3(kThreads), kTotal + 1024, st, k, q, a);

@@ -50,7 +50,7 @@ struct WeightPlan {
 
 // kBufCols: columns of a score buffer; 128 where the columns fit, so that two CTAs
 // share an SM (one's set-up behind the other's work), else 256.
-template <int D, bool kQ8, int kBufCols>
+template <int D, bool kQ8, int kBufCols, bool kPoll>
 __global__ void __launch_bounds__(kThreads, kBufCols == 128 ? 2 : 1)
 weights_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ WeightArgs a,
                   WeightPlan p) {
@@ -68,6 +68,12 @@ weights_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
   WeightSmem& s = *(WeightSmem*)(smem + off_q + (kQ8 ? 2 : 1) * q_bytes);
   volatile uint32_t* abort = &s.abort;
   auto bar = [&](int i) { return su32(&s.bars[i]); };
+  auto wait_ready = [&](uint32_t at, uint32_t parity) {
+    return phase_ready<kPoll>(at, parity, a.wait_cycles);
+  };
+  auto wait_timed = [&](uint32_t at, uint32_t parity) {
+    return phase_timed<kPoll>(at, parity, a.wait_cycles);
+  };
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int sp = blockIdx.x, hk = blockIdx.y, b = blockIdx.z;
@@ -204,7 +210,7 @@ weights_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
       int loaded = early;
       for (int t = loaded; t < n_pre && !*abort; ++t) {
         const int g = slots0 + t;
-        if (!mbar_wait(bar(BAR_EMPTY + g % p.ring), (g / p.ring - 1) & 1)) {
+        if (!wait_timed(bar(BAR_EMPTY + g % p.ring), (g / p.ring - 1) & 1)) {
           *abort = 1;
           break;
         }
@@ -427,7 +433,8 @@ bool launch_d(const tsd_attn_desc& d, const WeightArgs& a, int cols, cudaStream_
   }
   p.nsplit = (int)ceil_div(tiles, p.tiles);
   const size_t smem = (size_t)p.ring * tile + q + sizeof(WeightSmem) + 1024;
-  const auto kern = weights_tc_kernel<D, kQ8, kBufCols>;
+  const auto kern = a.wait_cycles < kWaitCycles ? weights_tc_kernel<D, kQ8, kBufCols, true>
+                                                : weights_tc_kernel<D, kQ8, kBufCols, false>;
   // (the same for every call: another thread's may come between this and the launch)
   cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
   launch(kern, dim3(p.nsplit, d.Hkv, d.B), dim3(kThreads), smem, st, m, a, p);
