@@ -998,6 +998,15 @@ def test_weights_waits_give_up_at_the_budget(kind, S, q8):
 
 @gpu
 @pytest.mark.parametrize("q8", [True, False])
+@pytest.mark.parametrize("kind,S", [("latent", 3), ("latent", 9), ("latent-few", 9)])
+def test_latent_weights_waits_give_up_at_the_budget(kind, S, q8):
+    """Whatever piece of Q the loading warp gives up at, no wait for a copy that was never
+    requested: the kernel ends within the budget and the copies' time."""
+    test_weights_waits_give_up_at_the_budget(kind, S, q8)
+
+
+@gpu
+@pytest.mark.parametrize("q8", [True, False])
 def test_weights_ignore_what_lies_behind_the_prefix(q8):
     s = Setup("gqa", 2, 5, [130, 64], extra=200, seed=23, q8=q8)
     _weights_state(s, 4, [2, 4])

@@ -182,23 +182,21 @@ weights_latent_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_con
   // ------------------------------------------------------------- Q pieces
   if (warp == kTma) {
     if (lane == 0) {
-      int last = 1;                                         // groups whose pieces were requested
-      bool ok = true;
-      for (int n = 1; ok && n < groups && !*abort; ++n) {
-        for (int j = 0; j < kPieces; ++j) {
-          if (!wait_timed(bar(BAR_Q_EMPTY + j), (n - 1) & 1)) {
-            ok = false;
-            // (the pieces of this group before j are in flight)
-            for (int i = 0; i < j; ++i) mbar_wait(bar(BAR_Q_FULL + i), n & 1);
-            break;
-          }
-          load_q(n, j);
+      // the first piece not requested: piece j of group n
+      int n = 1, j = 0;
+      while (n < groups && !*abort) {
+        if (!wait_timed(bar(BAR_Q_EMPTY + j), (n - 1) & 1)) {
+          *abort = 1;
+          break;
         }
-        if (ok) last = n + 1;
+        load_q(n, j);
+        if (++j == kPieces) {
+          j = 0;
+          ++n;
+        }
       }
-      if (!ok) *abort = 1;
       // no copy may be in flight when the CTA leaves
-      for (int j = 0; j < kPieces; ++j) mbar_wait(bar(BAR_Q_FULL + j), (last - 1) & 1);
+      for (int i = 0; i < kPieces; ++i) mbar_wait(bar(BAR_Q_FULL + i), (i < j ? n : n - 1) & 1);
       if (!kQ8 && !on_path) mbar_wait(bar(BAR_K_FULL), 0);
     }
     __syncwarp();
