@@ -562,9 +562,9 @@ tsd_status tsd_tree_verify_attn_q8(const tsd_attn_desc* desc, const void* q, con
  * No workspace.
  *
  * tsd_cache_evict cuts every request that holds more than `keep` rows to
- * `keep`, in place.  Each head ranks its rows by (protected first, acc desc,
- * index asc) and keeps the first `keep`; a row is protected if pos < sink or
- * pos >= seen - recent (sink + recent <= keep).  The kept rows at or behind
+ * `keep`, in place.  Each head ranks its rows, the protected ones first and by
+ * index, the others by (acc desc, index asc), and keeps the first `keep`; a row is
+ * protected if pos < sink or pos >= seen - recent (sink + recent <= keep).  The kept rows at or behind
  * `keep` move, in index order, into the places below `keep` that the dropped
  * rows leave, in index order, K, V, acc and pos together; then prefix_len[b] =
  * keep.  Rows behind the new length are left as they were.  The cache is then

@@ -1194,10 +1194,12 @@ NAN_BITS = [0x7FFFFFFF, -1, 0x7FC00000, -0x400000, 0x7F800001]   # (0xffffffff, 
 
 
 def plain_evict_any(P, keep, sink, recent, acc, pos, seen):
-    """plain_evict with NaN weights: behind the protected rows, before infinity, by index."""
+    """plain_evict with NaN weights: behind the protected rows, before infinity, by index; and
+    with more protected rows than places, the first of which stay."""
     def key(i):
-        nan = acc[i] != acc[i]
-        return (not (pos[i] < sink or pos[i] >= seen - recent), not nan, 0.0 if nan else -acc[i], i)
+        if pos[i] < sink or pos[i] >= seen - recent:
+            return (0, 0.0, i)
+        return (1, -INF, i) if acc[i] != acc[i] else (2, -acc[i], i)
 
     kept = set(sorted(range(P), key=key)[:keep])
     return ([i for i in range(keep) if i not in kept], [i for i in range(keep, P) if i in kept])
@@ -1319,6 +1321,81 @@ def test_evict_with_room_to_spare_does_nothing():
     for keep in (100, s.cap, s.cap + 50):
         _evict(s, keep, 0, 0)
         _check_evict(s, snap, 100, 0, 0)
+
+
+# groups of query heads that take other paths, or other splits of them, than KINDS
+GROUPS = {"mqa32": (32, 1, 128, 128), "mqa71": (71, 1, 64, 64), "mha": (40, 40, 64, 64),
+          "latent24": (24, 1, 576, 512), "latent4": (4, 1, 576, 512), "latent-two": (32, 2, 576, 512)}
+
+
+@gpu
+@pytest.mark.parametrize("kind,B,R,lens,S,kw", [("mqa32", 2, 12, [300, 64], 9, {}), ("mqa71", 1, 9, [130], 5, dict(page=128)),
+                                                ("mha", 2, 3, [200, 1], 2, {}), ("latent24", 2, 5, [140, 64], 3, {}),
+                                                ("latent4", 2, 6, [129, 0], 4, dict(page=128)),
+                                                ("latent-two", 1, 4, [200], 3, {})])
+def test_other_groups_of_heads(kind, B, R, lens, S, kw, monkeypatch):
+    """Attention, weights (of more columns than the tensor memory takes, and of latent groups
+    that are no run of 64: the CUDA cores), commit and eviction (of rows whose positions
+    repeat, so that many are protected)."""
+    monkeypatch.setitem(KINDS, kind, GROUPS[kind])
+    monkeypatch.setitem(globals(), "plain_evict", plain_evict_any)
+    for q8 in (True, False):
+        s = Setup(kind, B, R, lens, extra=20, seed=40 + R, q8=q8, **kw)
+        _weights_state(s, S)
+        if q8:
+            out, s.lse = s.attn()
+            s.check_attn(out, s.lse)
+        acc0, pos0, seen0 = s.acc.clone(), s.pos.clone(), s.seen.clone()
+        _weights(s, S, 0.5)
+        torch.cuda.synchronize()
+        assert int(s.err) == 0
+        _check_weights(s, acc0, pos0, seen0, 0.5)
+        if q8:
+            before = _write(s, s.kt, s.vt, None, (s.path, s.plength, S))
+            _check_write(s, before, lambda b, h, w: (s.kt if w == "k" else s.vt)[b, s.paths[b], h].double())
+            s.lens = s.plen.tolist()
+        snap = _snapshot(s)
+        _evict(s, 100, 2, 20)
+        _check_evict(s, snap, 100, 2, 20)
+
+
+@gpu
+@pytest.mark.parametrize("kind,page", [("gqa", 0), ("narrow", 128), ("latent-few", 0)])
+def test_commit_of_fp32_rows(kind, page):
+    s = Setup(kind, 3, 40, [0, 60, 250], extra=17, page=page, dtype=torch.float32, seed=6)
+    s.kt[1] *= 50.0
+    s.kt[2, 3, 0, 5] = INF
+    paths = [[0], [0] + list(range(2, 18)), [0, 3, 9]]
+    rows = torch.tensor([p + [-1] * (17 - len(p)) for p in paths], dtype=torch.int32, device=DEV)
+    length = torch.tensor([len(p) - 1 for p in paths], dtype=torch.int32, device=DEV)
+    before = _write(s, s.kt, s.vt, None, (rows, length, 16))
+    assert int(s.err) == 0
+    _check_write(s, before, lambda b, h, w: (s.kt if w == "k" else s.vt)[b, paths[b], h].double())
+
+
+@gpu
+@pytest.mark.parametrize("kind,page", [("gqa", 128), ("narrow", 0), ("latent-few", 128)])
+def test_a_row_is_the_same_wherever_it_stands_in_its_tree(kind, page):
+    """The rows of a tree in another order (parents before children): each row's output is
+    within the bounds in both."""
+    s = Setup(kind, 2, 30, [700, 65], page=page, seed=20)
+    s.check_attn(*s.attn())
+    order = [0]
+    while len(order) < 30:                # any row whose ancestors, in both trees, are there
+        there = sum(1 << (r - 1) for r in order[1:])
+        order.append(s.rnd.choice([r for r in range(1, 30) if r not in order and all(
+            m[r] & ~there == 1 << (r - 1) for m in s.masks)]))
+    assert order != sorted(order)
+    place = {r: i for i, r in enumerate(order)}
+
+    def moved(v):
+        return sum(1 << (place[j] - 1) for j in range(1, 30) if v >> (j - 1) & 1)
+
+    s.set_masks([[moved(m[r]) for r in order] for m in s.masks])
+    at = torch.tensor(order, device=DEV)
+    s.q, s.kt = s.q[:, at].contiguous(), s.kt[:, at].contiguous()
+    s.vt = None if s.latent else s.vt[:, at].contiguous()
+    s.check_attn(*s.attn())
 
 
 # ------------------------------------------------------------ all together --

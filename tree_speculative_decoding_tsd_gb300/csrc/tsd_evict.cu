@@ -1,9 +1,9 @@
 // tsd_cache_evict, tsd_cache_evict_q8: the cache of every head cut to `keep`
 // rows by the attention weight each cached token has received.
 //
-// For a request with more than `keep` rows, each KV head ranks its rows by
-// (protected first, weight desc, index asc) and keeps the first `keep`; NaN, of
-// either sign, counts as more than infinity.  A row is protected if its token is
+// For a request with more than `keep` rows, each KV head ranks its rows, the
+// protected ones first and by index, the others by (weight desc, index asc), and
+// keeps the first `keep`; NaN, of either sign, counts as more than infinity.  A row is protected if its token is
 // one of the first `sink` or the last `recent` ones.  The kept rows that lie at or
 // behind `keep` move, in order, into the places (in order) of the dropped rows
 // below it: no row that is read is also written, no row that stays is touched, and
