@@ -12,12 +12,14 @@
 // to fp16, the powers of two applied to scores and probabilities in fp32.
 //
 // Why 64 rows and codes for the keys: the tensor memory holds O^T of 512 x 64 (256
-// columns) beside two score buffers (2 x 128).  Shared memory delivers 128 bytes a
-// cycle; per 128-key tile the codes arrive (72 KB), the 18 products of S^T read 8 KB
-// each, the widened values are written (128 KB) and the 32 products of O^T read 6 KB
-// each: 536 KB, about 4200 cycles; a tile takes 5200.  (Widened keys would be 144 KB
-// written and 216 KB read instead of the 216 KB.)  64 x 9 rows of 128 heads over 8k
-// keys: 1.53 ms, 858 TFLOP/s.
+// columns) beside two score buffers (2 x 128).  Per 128-key tile the codes arrive in
+// shared memory (72 KB), the 18 products of S^T read 8 KB each, the widened values are
+// written (128 KB) and the 32 products of O^T read 6 KB each: 536 KB, about 4200 cycles
+// if all of it shares 128 bytes a cycle; a tile takes 5200.  (Widened keys would be 144
+// KB written and 216 KB read instead of the 216 KB.)  The counters show 36% for the
+// warps' own accesses, without the products' reads, and the tensor core 40% active: a
+// tile's latency through the roles may bind as well.  64 x 9 rows of 128 heads over 8k
+// keys: 1.51 ms, 870 TFLOP/s.
 //
 // Roles (768 threads): warps 0-15 softmax and epilogue (warpgroup w/4 owns 16
 // columns, warp w%4 the TMEM lanes 32(w%4)..+31); warp 16 issues the products of

@@ -231,6 +231,7 @@ class Q8TreeVerifyStep(TreeVerifyStep):
     the accepted rows' attention weights to ``RowWeights`` (older ones times ``decay``)
     and then drops the lightest rows past ``keep``, never one of the request's first
     ``sink`` or last ``recent`` tokens.  A round needs room for keep + S + 1 rows.
+    All of a round is on one stream (no ``overlap_argmax``), and its tree is build()'s.
     """
 
     def __init__(self, B, S, V, k, D, Hq, Hkv, dk, dv, cap, dtype, v_aliases_k, scale,
