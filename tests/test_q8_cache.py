@@ -627,8 +627,9 @@ def test_attention_waits_give_up_at_the_budget(kind, R, page):
     role stops, and the kernel ends at once with a code in err.  The next call is as ever."""
     s = Setup(kind, 3, R, [2500, 700, 0], page=page, seed=19)
     want = s.attn()
-    start = time.monotonic()
     with T.wait_budget(16):
+        s.attn()                                      # (loads the kernel)
+        start = time.monotonic()
         s.attn()
     assert time.monotonic() - start < 0.9             # (no wait of the default budget ran out)
     e = int(s.err)
@@ -978,11 +979,12 @@ def test_weights_waits_give_up_at_the_budget(kind, S, q8):
     _weights_state(s, S, [S, 1])
     state = (s.acc, s.pos, s.seen)
     before = [t.clone() for t in state]
-    torch.cuda.synchronize()
-    start = time.monotonic()
     with T.wait_budget(16):
-        _weights(s, S, 0.5)
-        torch.cuda.synchronize()
+        for _ in range(2):                            # (the first loads the kernel)
+            torch.cuda.synchronize()
+            start = time.monotonic()
+            _weights(s, S, 0.5)
+            torch.cuda.synchronize()
     assert time.monotonic() - start < 0.9
     e = int(s.err)
     assert e & T.TSD_DEV_ERR_MASK == T.TSD_DEV_ERR_TIMEOUT and e & 0xFFFFFF < 2, hex(e)
