@@ -610,6 +610,131 @@ tsd_status tsd_cache_evict_q8(const tsd_attn_desc* desc, int keep, int sink, int
                               int page_size, int num_pages, int32_t* prefix_len, void* ws,
                               size_t ws_bytes, int32_t* err, tsd_stream_t stream);
 
+/* --------------------------------------------------------------------------
+ * The 4-bit KV cache: tsd_cache_write_q4, tsd_commit_path_q4, tsd_cache_read_q4,
+ * tsd_tree_verify_attn_q4
+ *
+ * The cache at 4.5 bits a value: a row of d dims (one token, one head, K or V) has d
+ * codes c in 0..15 and a bf16 scale s for each TSD_Q4_GROUP = 32 dims.
+ *   value = (c - 8) * s
+ * Rows do not depend on one another: an append leaves all earlier rows as they are.
+ *
+ * kq, vq      contiguous [B][Hkv][cap][d / 2] bytes, or pages
+ *             [num_pages][Hkv][page_size][d / 2].  A 32-bit word w of a row (little
+ *             endian) has dims 8w..8w+7: dim 8w + 2i in bits 4i..4i+3, dim 8w + 2i + 1
+ *             in bits 16+4i..19+4i.
+ * kscale, vscale  contiguous [B][Hkv][cap][d / 32] bf16, or pages
+ *             [num_pages][Hkv][page_size][d / 32]
+ * page arguments and desc as for the 8-bit cache; heads of dk == dv in {64, 128} (latent
+ * heads, v_aliases_k: TSD_ERR_UNSUPPORTED).
+ *
+ * tsd_cache_write_q4 and tsd_commit_path_q4 append rows as tsd_cache_write_q8 and
+ * tsd_commit_path_q8 do, with the same errors.  Per group of 32 elements x, with hi and lo
+ * its largest and smallest:
+ *   x* = hi if hi >= -lo, else lo;     s = bf16(-x* / 8), rounded to nearest even
+ *   inv = 1 / s, rounded to fp32;      c = clamp(round(x * inv), -8, 7) + 8
+ * round: the exact product to the nearest whole number, ties to even.  |x*| < 2^-90: s =
+ * 0 and all c = 8.  A group with an infinity or a NaN: s = NaN and all c = 8 (its values
+ * are read as NaN).
+ *
+ * tsd_cache_read_q4 reads rows back: for request b, positions first[b]..first[b]+count[b]-1
+ * to rows 0..count[b]-1 of kout[b], vout[b] ([B][T][Hkv][d], dtype; each value rounded
+ * once); rows behind them are left as they were.  A request with prefix_len outside
+ * 0..cap, count outside 0..T, first < 0 or first + count > prefix_len is skipped and
+ * reported as TSD_DEV_ERR_CAPACITY, one with a page outside the pool as
+ * TSD_DEV_ERR_BAD_PAGE.  No workspace.
+ *
+ * tsd_tree_verify_attn_q4 is tsd_tree_verify_attn over the 4-bit cache: the prefix keys
+ * and values are the codes' values, the scratch rows ktree, vtree are in dtype.  Rows
+ * behind prefix_len are not used, whatever they hold; nor are scratch rows that no row
+ * sees.  fp32 inputs are computed in fp32.  ws: tsd_verify_q4_workspace_size(desc) bytes
+ * (0 is a valid size); calls that may overlap, captured ones among them, each need their
+ * own.
+ * -------------------------------------------------------------------------- */
+#define TSD_Q4_GROUP 32
+
+tsd_status tsd_cache_write_q4(const tsd_attn_desc* desc, int T, const void* knew,
+                              const void* vnew, const int32_t* new_len, void* kq, void* vq,
+                              void* kscale, void* vscale, const int32_t* page_table,
+                              int max_pages, int page_size, int num_pages, int32_t* prefix_len,
+                              int32_t* err, tsd_stream_t stream);
+
+tsd_status tsd_commit_path_q4(const tsd_attn_desc* desc, int S, const void* ktree,
+                              const void* vtree, const int32_t* accept_rows,
+                              const int32_t* accept_len, void* kq, void* vq, void* kscale,
+                              void* vscale, const int32_t* page_table, int max_pages,
+                              int page_size, int num_pages, int32_t* prefix_len, int32_t* err,
+                              tsd_stream_t stream);
+
+tsd_status tsd_cache_read_q4(const tsd_attn_desc* desc, int T, const void* kq, const void* vq,
+                             const void* kscale, const void* vscale, const int32_t* page_table,
+                             int max_pages, int page_size, int num_pages,
+                             const int32_t* prefix_len, const int32_t* first,
+                             const int32_t* count, void* kout, void* vout, int32_t* err,
+                             tsd_stream_t stream);
+
+size_t tsd_verify_q4_workspace_size(const tsd_attn_desc* desc);
+
+tsd_status tsd_tree_verify_attn_q4(const tsd_attn_desc* desc, const void* q, const void* kq,
+                                   const void* vq, const void* kscale, const void* vscale,
+                                   const int32_t* page_table, int max_pages, int page_size,
+                                   int num_pages, const int32_t* prefix_len, const void* ktree,
+                                   const void* vtree, const uint64_t* mask, void* out,
+                                   float* lse, void* ws, size_t ws_bytes, int32_t* err,
+                                   tsd_stream_t stream);
+
+/* --------------------------------------------------------------------------
+ * tsd_qk_norm_rope
+ *
+ * What the attention and the cache take, from a layer's projections: RMS norm of every
+ * head's query and key, and the position rotation, in one pass.  Sources as for tsd_tree_verify_attn: a tree's row has the position of its
+ * depth behind the prefix, whatever its place in the tree, so start = prefix_len (of an
+ * evicted cache: the tokens seen) and offset = depth.
+ *
+ * For request b and token t < count[b], every head's row x of d dims of q and k:
+ *   y = x / sqrt(mean(x^2) + eps) * weight        (desc->norm; else y = x)
+ *   pair i of the first rot dims, (y_i, y_(i + rot/2)), or with desc->neighbours
+ *   (y_2i, y_(2i+1)), is turned by the angle
+ *     t_i = sum over axes a of position_a * turns[a][i],
+ *     position_a = start[b] + offset[a][b][t],
+ *   (u, w) -> amplitude * (u cos t_i - w sin t_i, u sin t_i + w cos t_i)
+ * computed in fp32 and rounded once.  Rows of v are copied.  Rows t >= count[b] are
+ * neither read nor written.
+ *
+ * q, k, v    rows [B][T][H][d] whose tokens lie q_stride, k_stride, v_stride elements
+ *            apart (b-th request's first one T strides behind the request before), for
+ *            example views of a fused projection; strides are multiples of 16 bytes and
+ *            at least a row.  v and v_out may be NULL together.
+ * q_weight, k_weight  [d] of dtype; NULL: 1 (required without desc->norm)
+ * turns      [axes][rot / 2] uint64: turns per position as a fraction of 2^64 (a whole
+ *            turn is 0), so that far positions keep their angle to 2^-32 turns.  A pair
+ *            that does not turn with an axis has 0 there: the sections, in any order, of
+ *            a model's position axes (time, height, width).
+ * start      [B] int32, NULL: 0.      offset [axes][B][T] int32, NULL: 0..T-1 on each axis
+ * count      [B] int32, NULL: T
+ * q_out, k_out, v_out  dense [B][T][H][d].  They may be q, k, v themselves where those are
+ *            dense; otherwise they do not overlap the inputs.
+ * Limits: d in {64, 128}, rot a multiple of 8 in 0..d (0: no rotation, turns unused),
+ * 1 <= axes <= 4.
+ * -------------------------------------------------------------------------- */
+typedef struct {
+  int B, T;         /* requests, rows per request */
+  int Hq, Hkv, d;   /* query heads, KV heads, head dim */
+  int dtype;        /* TSD_F32 or TSD_BF16 */
+  int rot;          /* rotated dims, the first ones of a head */
+  int neighbours;   /* 1: pairs (2i, 2i + 1); 0: pairs (i, i + rot / 2) */
+  int axes;         /* position axes */
+  int norm;         /* 1: RMS norm first */
+  float eps;        /* of the norm, >= 0 */
+  float amplitude;  /* factor of the rotated dims, usually 1 */
+} tsd_rope_desc;
+
+tsd_status tsd_qk_norm_rope(const tsd_rope_desc* desc, const void* q, int64_t q_stride,
+                            const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                            const void* q_weight, const void* k_weight, const uint64_t* turns,
+                            const int32_t* start, const int32_t* offset, const int32_t* count,
+                            void* q_out, void* k_out, void* v_out, tsd_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

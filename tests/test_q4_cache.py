@@ -1,0 +1,548 @@
+"""The 4-bit KV cache (writes, commits, reads, tree attention) against plain 64-bit code.
+
+The plain forms here work per request and head in float64.  Codes and scales have to be
+equal; what the kernels compute is held to bounds derived beside each check.
+"""
+
+import ctypes
+import math
+import random
+
+import pytest
+import torch
+
+import tree_speculative_decoding_tsd_gb300 as T
+
+DEV = "cuda:0"
+NAN, INF = float("nan"), float("inf")
+G = T.TSD_Q4_GROUP
+gpu = pytest.mark.gpu
+
+
+# ------------------------------------------------------------ plain forms --
+
+def unpack(x):
+    """Packed codes [..][d / 2] (uint8) as whole numbers [..][d]."""
+    word = sum(x[..., i::4].long() << (8 * i) for i in range(4))
+    out = torch.empty(*word.shape, 8, dtype=torch.int64, device=x.device)
+    for i in range(4):
+        out[..., 2 * i] = (word >> (4 * i)) & 15
+        out[..., 2 * i + 1] = (word >> (16 + 4 * i)) & 15
+    return out.flatten(-2)
+
+
+def quantise(x):
+    """Rows [n][d] (float64, each an element of the input type) as codes [n][d], scales [n][d / 32]."""
+    x = x.view(x.shape[0], -1, G)
+    bad = ~x.isfinite().all(-1)
+    y = torch.where(bad[..., None], torch.zeros_like(x), x)
+    hi, lo = y.amax(-1), y.amin(-1)
+    top = torch.where(hi >= -lo, hi, lo)
+    s = (top / -8).float().bfloat16().double()        # (an element over 8 is exact in fp32)
+    s[top.abs() < 2.0 ** -90] = 0
+    inv = torch.where(s == 0, torch.zeros_like(s), 1 / s).float().double()
+    c = (y * inv[..., None]).round().clamp(-8, 7).long() + 8
+    c[bad | (s == 0)] = 8
+    s[bad] = NAN
+    return c.flatten(1), s
+
+
+class Cache:
+    """A contiguous or paged cache of one array (K or V): rows by (request, head)."""
+
+    def __init__(self, x, s, table):
+        self.x, self.s, self.table = x, s, table
+
+    def pages(self, b):
+        return [b] if self.table is None else self.table[b].tolist()
+
+    def codes(self, b, h):
+        return unpack(torch.cat([self.x[p, h] for p in self.pages(b)]))
+
+    def scales(self, b, h):
+        return torch.cat([self.s[p, h] for p in self.pages(b)]).double()
+
+    def values(self, b, h):
+        return (self.codes(b, h) - 8).double() * self.scales(b, h).repeat_interleave(G, 1)
+
+
+def plain_attn(q, k, v, sees, scale):
+    """q [n][d], k [m][d], v [m][d], sees [n][m] -> out, lse, weights, the weighted mean of
+    |v| and the largest scale * sum |q_d k_d| (what the bounds need)."""
+    s = (q @ k.T * scale).masked_fill(~sees, -INF)
+    lse = torch.logsumexp(s, -1)
+    p = torch.exp(s - lse[:, None])
+    big = (q.abs() @ k.abs().T * scale).masked_fill(~sees, 0).amax(-1)
+    return p @ v, lse, p @ v.abs(), big
+
+
+# ----------------------------------------------------------------- inputs --
+
+KINDS = {"gqa": (32, 8, 128), "narrow": (14, 2, 64), "one": (2, 2, 128), "wide": (16, 1, 128),
+         "wide64": (24, 2, 64), "odd": (3, 1, 64)}
+
+
+class Setup:
+    """Random cache, scratch pad, tree and lengths for one configuration."""
+
+    def __init__(self, kind, B, R, lens, extra=8, dtype=torch.bfloat16, page=0, seed=0, spread=2):
+        self.Hq, self.Hkv, self.d = KINDS[kind]
+        self.B, self.R, self.dt, self.page = B, R, dtype, page
+        self.g = torch.Generator(device=DEV).manual_seed(seed * 1000 + 11)
+        self.rnd = random.Random(seed)
+        self.lens = [lens[b % len(lens)] for b in range(B)]
+        cap = max(max(self.lens) + extra, 1)
+        if page:
+            cap = -(-cap // page) * page
+        self.cap = cap
+        self.scale = float(torch.tensor(1 / math.sqrt(self.d), dtype=torch.float32))
+        self.table = None
+        lead, rows = (B, self.Hkv), cap
+        if page:
+            per = cap // page
+            order = self.rnd.sample(range(B * per + 2), B * per)
+            self.table = torch.tensor(order, dtype=torch.int32, device=DEV).view(B, per)
+            lead, rows = (B * per + 2, self.Hkv), page
+        self.lead, self.rows = lead, rows
+
+        def codes():
+            return torch.randint(0, 256, (*lead, rows, self.d // 2), generator=self.g, device=DEV,
+                                 dtype=torch.uint8)
+
+        def scales():
+            shape = (*lead, rows, self.d // G)
+            x = torch.rand(shape, generator=self.g, device=DEV) * 0.2 + 0.1
+            e = torch.randint(-spread, 1, shape, generator=self.g, device=DEV)
+            sign = torch.randint(0, 2, shape, generator=self.g, device=DEV) * 2 - 1
+            return (x * sign * torch.exp2(e.float())).bfloat16()
+
+        self.k, self.ks, self.v, self.vs = codes(), scales(), codes(), scales()
+        self.plen = torch.tensor(self.lens, dtype=torch.int32, device=DEV)
+        self.q = self.normal(B, R, self.Hq, self.d)
+        self.kt, self.vt = self.normal(B, R, self.Hkv, self.d), self.normal(B, R, self.Hkv, self.d)
+        masks = []
+        for _ in range(B):
+            m = [0]
+            for r in range(1, R):
+                m.append(m[self.rnd.randrange(max(0, r - 5), r)] | (1 << (r - 1)))
+            masks.append(m)
+        self.set_masks(masks)
+        self.err = torch.zeros(1, dtype=torch.int32, device=DEV)
+        self.desc = T.make_desc(B, R, self.Hq, self.Hkv, self.d, self.d, cap, dtype, False, self.scale)
+        self.paging = dict(page_table=self.table, page_size=page)
+
+    def normal(self, *shape, std=1.0):
+        return (torch.randn(*shape, generator=self.g, device=DEV) * std).to(self.dt)
+
+    def set_masks(self, masks):
+        self.masks = masks
+        self.mask = torch.tensor([[v - (1 << 64) if v >> 63 else v for v in m] for m in masks],
+                                 dtype=torch.int64, device=DEV)
+
+    def cache(self, which):
+        return Cache(self.k, self.ks, self.table) if which == "k" else Cache(self.v, self.vs, self.table)
+
+    def arrays(self):
+        return self.k, self.v, self.ks, self.vs
+
+    def attn(self, stream=None):
+        out = torch.full((self.B, self.R, self.Hq, self.d), 7.0, dtype=self.dt, device=DEV)
+        lse = torch.full((self.B, self.R, self.Hq), 7.0, device=DEV)
+        ws = T.workspace(T.tsd_verify_q4_workspace_size(self.desc))
+        self.attn_into(out, lse, ws, stream)
+        torch.cuda.synchronize()
+        return out, lse
+
+    def attn_into(self, out, lse, ws, stream=None):
+        T.tsd_tree_verify_attn_q4(self.desc, self.q, *self.arrays(), self.plen, self.kt, self.vt,
+                                  self.mask, out, lse, ws, self.err, stream, **self.paging)
+
+    def sees(self, b):
+        R = self.R
+        return torch.tensor([[j == 0 or (i > 0 and self.masks[b][i] >> (j - 1) & 1 == 1)
+                              for j in range(R)] for i in range(R)], device=DEV)
+
+    def check_attn(self, out, lse, requests=None, heads=None):
+        """Bounds.  fp32 arithmetic: a score is a sum of d products, in any order and possibly
+        truncated, of codes 0..15 from which 8 times the sum of q is taken (whose terms are at
+        most 15 / 8 of |c - 8| at their largest: S below takes 16 |s| for every |c - 8| |s|): off
+        by at most (d + 16) 2^-23 S, S = scale sum |q| 16 |s|.  A probability is then off by that,
+        relatively, plus 2^-20 for the exponential and the sums' last bits (n terms: n 2^-24
+        more).
+        bf16 inputs: tensor-core paths round keys (c - 8) s to fp16 (2^-12 of each: 2^-12 of
+        scale sum |q k|), values (2^-12) and probabilities (2^-12), and a split's output (2^-12).
+        fp16's smallest step is 2^-24: a key or value of a tile of at most 128 rows is held over
+        2^E with |s| 2^-E < 1 for the tile's largest scale, as (c - 8) s 2^-E 2^-9 or more, so it is
+        off by at most 2^-25 2^9 2^E = 2^-16 2^E, which is at most 2^-15 of the largest |s| of
+        the tile; scratch rows of the last one by 2^-24 of the largest element.  A
+        probability times 2^E is held relative to the largest such product met so far times
+        2^-8 .. 1, in steps of 2^-24, off by at most 2^-25 2^8 of it: n 2^-17 of a weight 1 over
+        the keys times ... - only products 2^-16 below the largest are touched; the sum of n of
+        them is off by at most n 2^-25 top, top = the largest |v| of any tile times its weight,
+        of which the denominator holds at least the weight.
+        """
+        g = self.Hq // self.Hkv
+        f32 = self.dt == torch.float32
+        for b in requests if requests is not None else range(self.B):
+            P = min(self.lens[b], self.cap)
+            sees = torch.cat([torch.ones(self.R, P, dtype=torch.bool, device=DEV), self.sees(b)], 1)
+            live = sees.any(0)
+            for h in heads if heads is not None else range(self.Hkv):
+                ck, cv = self.cache("k"), self.cache("v")
+                kt, vt = self.kt[b, :, h].double(), self.vt[b, :, h].double()
+                k, v = torch.cat([ck.values(b, h)[:P], kt]), torch.cat([cv.values(b, h)[:P], vt])
+                wide = torch.cat([16 * ck.scales(b, h)[:P].abs().repeat_interleave(G, 1), kt.abs()])
+                k, v, wide = k[live], v[live], wide[live]
+                seen = sees[:, live].repeat_interleave(g, 0)
+                hs = slice(h * g, (h + 1) * g)
+                q = self.q[b, :, hs].double().reshape(-1, self.d)
+                o, l, A, S = plain_attn(q, k, v, seen, self.scale)
+                n = k.shape[0]
+                W = (q.abs() @ wide.T * self.scale).masked_fill(~seen, 0).nan_to_num(0).amax(-1)
+                ds = (self.d + 16) * 2.0 ** -23 * W
+                p16 = 0.0
+                low_k = low_v = torch.zeros((), dtype=torch.float64, device=DEV)
+                if not f32:
+                    p16 = 3 * 2.0 ** -12
+                    big_k = ck.scales(b, h)[:P].abs().nan_to_num(0)
+                    big_v = cv.scales(b, h)[:P].abs().nan_to_num(0)
+                    top_k = max(float(big_k.max()) if P else 0.0, float(kt[kt.isfinite()].abs().max()))
+                    top_v = max(float(big_v.max()) if P else 0.0, float(vt[vt.isfinite()].abs().max()))
+                    ds = ds + 2.0 ** -12 * S + 2.0 ** -15 * top_k * self.scale * q.abs().sum(-1)
+                    low_v = 2.0 ** -15 * top_v + n * 2.0 ** -25 * 16 * top_v
+                rel = 2 * ds + 2.0 ** -20 + n * 2.0 ** -24
+                got = out[b, :, hs].double().reshape(-1, self.d)
+                fine = o.isfinite().all(-1)
+                low = 2.0 ** -24 if f32 else 2.0 ** -8
+                tol = low * o.abs() + (rel + p16)[:, None] * A * 1.01 + low_v + 1e-37
+                assert not got[fine].isnan().any()
+                bad = ((got - o).abs() > tol)[fine]
+                assert not bad.any(), (b, h, float(((got - o).abs() / tol)[fine].max()))
+                assert not got[~fine].isfinite().all(-1).any()
+                gl = lse[b, :, hs].double().reshape(-1)
+                tl = rel + 2.0 ** -22 * l.abs() + 2.0 ** -20
+                assert ((gl - l).abs() <= tl)[l.isfinite()].all(), (b, h)
+
+
+# ------------------------------------------------- refusals (on the host) --
+
+A, U, N = ctypes.c_void_p(0x10000), ctypes.c_void_p(0x10004), None
+
+
+def _desc(**kw):
+    base = dict(B=2, R=5, Hq=4, Hkv=2, dk=128, dv=128, cap=256, dtype=T.TSD_BF16, v_aliases_k=0,
+                scale=0.088)
+    base.update(kw)
+    return T.tsd_attn_desc(**base)
+
+
+def _calls(d, table=N, mp=0, ps=0, npg=0, x=A, y=A, S=3, rows=4, ws=1 << 40):
+    r, pg, L = ctypes.byref(d), (table, mp, ps, npg), T.lib
+    return {
+        "write": lambda: L.tsd_cache_write_q4(r, rows, x, A, A, A, A, A, y, *pg, A, N, N),
+        "commit": lambda: L.tsd_commit_path_q4(r, S, x, A, A, A, A, A, A, y, *pg, A, N, N),
+        "read": lambda: L.tsd_cache_read_q4(r, rows, x, A, A, A, *pg, A, A, A, A, y, N, N),
+        "attn": lambda: L.tsd_tree_verify_attn_q4(r, x, A, A, A, y, *pg, A, A, A, A, A, A, A, ws, N, N)}
+
+
+ALL = list(_calls(_desc()))
+
+
+@pytest.mark.parametrize("name", ALL)
+@pytest.mark.parametrize("kw", [dict(B=0), dict(B=65536), dict(R=0), dict(R=66), dict(Hq=3),
+                                dict(Hkv=0), dict(dk=96, dv=96), dict(dk=128, dv=64), dict(dtype=7),
+                                dict(cap=0), dict(v_aliases_k=1)])
+def test_calls_reject_bad_descriptors(name, kw):
+    assert _calls(_desc(**kw))[name]() == T.TSD_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("name", ALL)
+def test_calls_do_not_take_latent_heads(name):
+    d = _desc(dk=576, dv=512, v_aliases_k=1)
+    assert _calls(d)[name]() == T.TSD_ERR_UNSUPPORTED
+    assert T.tsd_verify_q4_workspace_size(d) == 0
+
+
+@pytest.mark.parametrize("name", ALL)
+@pytest.mark.parametrize("kw", [dict(x=N), dict(x=U), dict(y=N), dict(y=U), dict(ps=-1),
+                                dict(ps=64, table=A, mp=4, npg=8), dict(ps=128, table=A, mp=3, npg=8),
+                                dict(ps=128, table=N, mp=2, npg=8), dict(ps=128, table=U, mp=2, npg=8),
+                                dict(ps=128, table=A, mp=2)])
+def test_calls_reject_bad_pointers_and_pages(name, kw):
+    assert _calls(_desc(), **kw)[name]() == T.TSD_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("name,kw", [("commit", dict(S=0)), ("commit", dict(S=17)), ("write", dict(rows=0)),
+                                     ("read", dict(rows=0))])
+def test_calls_reject_bad_numbers(name, kw):
+    assert _calls(_desc(), **kw)[name]() == T.TSD_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("scale", [0.0, -1.0, NAN, INF])
+def test_attention_rejects_bad_scales(scale):
+    assert _calls(_desc(scale=scale))["attn"]() == T.TSD_ERR_INVALID_ARG
+
+
+def test_attention_rejects_a_short_workspace():
+    d = _desc(B=1, R=9, Hq=8, Hkv=1, cap=8192)
+    need = T.tsd_verify_q4_workspace_size(d)
+    assert need > 0
+    assert _calls(d, ws=need - 1)["attn"]() == T.TSD_ERR_INVALID_ARG
+
+
+@gpu
+def test_binding_rejects_types_shapes_and_pages():
+    s = Setup("one", 2, 3, [40])
+    out = torch.empty(2, 3, 2, 128, dtype=s.dt, device=DEV)
+    lse = torch.empty(2, 3, 2, device=DEV)
+    ws = T.workspace(T.tsd_verify_q4_workspace_size(s.desc))
+
+    def call(**kw):
+        a = dict(q=s.q, kq=s.k, vq=s.v, kscale=s.ks, vscale=s.vs, prefix_len=s.plen, ktree=s.kt,
+                 vtree=s.vt, mask=s.mask, out=out, lse=lse, ws=ws)
+        a.update(kw)
+        T.tsd_tree_verify_attn_q4(s.desc, **a)
+
+    call()
+    for kw in (dict(q=s.q.float()), dict(kq=s.k.float()), dict(kscale=s.ks.float()),
+               dict(prefix_len=s.plen.long())):
+        with pytest.raises(TypeError):
+            call(**kw)
+    for kw in (dict(q=s.q[:, :2]), dict(kq=s.k[:, :, :-1]), dict(vscale=s.vs[..., :2]),
+               dict(vscale=s.vs.cpu()), dict(lse=lse[:, :, :1]), dict(page_size=128),
+               dict(kq=s.k.transpose(0, 1)), dict(ws=ws.cpu())):
+        with pytest.raises(ValueError):
+            call(**kw)
+    torch.cuda.synchronize()
+
+
+# ---------------------------------------------------------- writes, reads --
+
+def _append(s, new, vnew, n, commit=None):
+    before = [t.clone() for t in s.arrays()]
+    p0 = s.plen.clone()
+    if commit is None:
+        T.tsd_cache_write_q4(s.desc, new, vnew, n, *s.arrays(), s.plen, s.err, **s.paging)
+    else:
+        T.tsd_commit_path_q4(s.desc, commit.shape[1] - 1, new, vnew, commit, n, *s.arrays(), s.plen,
+                             s.err, **s.paging)
+    torch.cuda.synchronize()
+    return before, p0
+
+
+def _check_append(s, before, p0, rows_of):
+    """rows_of(b) -> (K rows, V rows) [n][Hkv][d] in order, or None for a skipped request.
+    Every array against the plain form, whole."""
+    want = [t.clone() for t in before]
+    for b in range(s.B):
+        rows = rows_of(b)
+        P = int(p0[b])
+        if rows is None:
+            assert int(s.plen[b]) == P
+            continue
+        assert int(s.plen[b]) == P + rows[0].shape[0]
+        for part in range(2):
+            for i in range(rows[part].shape[0]):
+                c, f = quantise(rows[part][i].double())
+                pg, at = (b, P + i) if s.table is None else \
+                    (int(s.table[b, (P + i) // s.page]), (P + i) % s.page)
+                got = unpack((s.k, s.v)[part][pg, :, at])
+                assert torch.equal(got, c), (b, part, i)
+                assert torch.equal((s.ks, s.vs)[part][pg, :, at].double().nan_to_num(9.0), f.nan_to_num(9.0))
+                want[part][pg, :, at] = (s.k, s.v)[part][pg, :, at]
+                want[2 + part][pg, :, at] = (s.ks, s.vs)[part][pg, :, at]
+    for x, y in zip(s.arrays(), want):
+        assert torch.equal(x.view(torch.uint8), y.view(torch.uint8))
+
+
+@gpu
+@pytest.mark.parametrize("kind,dtype,page", [("gqa", torch.bfloat16, 0), ("narrow", torch.float32, 128),
+                                             ("one", torch.float32, 0), ("odd", torch.bfloat16, 256)])
+@pytest.mark.parametrize("Tn", [1, 17, 18, 67, 131])
+def test_write_appends_rows_of_every_length(kind, dtype, page, Tn):
+    lens = [0, 1, 63, 127, 128, 130, 255]
+    s = Setup(kind, 7, 1, lens, extra=Tn, dtype=dtype, page=page, seed=Tn)
+    x, y = s.normal(7, Tn, s.Hkv, s.d), s.normal(7, Tn, s.Hkv, s.d, std=3)
+    n = torch.tensor([Tn, 0, Tn, 1, max(Tn - 1, 0), Tn // 2, Tn], dtype=torch.int32, device=DEV)
+    before, p0 = _append(s, x, y, n)
+    _check_append(s, before, p0, lambda b: (x[b, : int(n[b])], y[b, : int(n[b])]))
+    assert int(s.err) == 0
+
+
+@gpu
+@pytest.mark.parametrize("kind,dtype,page", [("gqa", torch.bfloat16, 0), ("narrow", torch.bfloat16, 128),
+                                             ("wide", torch.float32, 256)])
+def test_commit_writes_the_accepted_rows(kind, dtype, page):
+    s = Setup(kind, 4, 20, [0, 60, 120, 250], extra=20, dtype=dtype, page=page, seed=3)
+    S = 9
+    path = torch.full((4, S + 1), -1, dtype=torch.int32)
+    lens = [0, 9, 4, 7]
+    for b, L in enumerate(lens):
+        path[b, : L + 1] = torch.tensor([0] + sorted(s.rnd.sample(range(1, 20), L)))
+    L = torch.tensor(lens, dtype=torch.int32, device=DEV)
+    before, p0 = _append(s, s.kt, s.vt, L, path.to(DEV))
+    _check_append(s, before, p0, lambda b: (s.kt[b, path[b, : lens[b] + 1].long()],
+                                            s.vt[b, path[b, : lens[b] + 1].long()]))
+    assert int(s.err) == 0
+
+
+@gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("Tn", [4, 40])
+def test_write_takes_values_at_the_ends_of_the_format(dtype, Tn):
+    s = Setup("one", 1, 1, [5], extra=Tn, dtype=dtype)
+    x = s.normal(1, Tn, 2, 128)
+    top = float(torch.finfo(dtype).max)
+    r = x[0, :, 0]
+    r[0, :32] = 0                                  # zeros
+    r[0, 32:64] = torch.where(r[0, 32:64] > 0, 2.0 ** -91, -2.0 ** -91)
+    r[0, 64:96] = 2.0 ** -90                       # the smallest group that is held
+    r[0, 96:] = -0.0
+    r[1, :32] = top
+    r[1, 32:64] *= 1e38
+    r[1, 64] = INF                                 # NaN groups, beside others
+    r[1, 100] = NAN
+    r[2, :32] = 3.0                                # ties of the largest magnitude, both signs
+    r[2, 5] = -3.0
+    r[2, 32:64] = torch.arange(32, device=DEV) / 4 - 4.0    # ties between two codes
+    r[2, 64] = -INF
+    r[2, 96:] = torch.arange(32, device=DEV).to(dtype) / -4 + 4.0
+    r[3] *= 2.0 ** -88
+    y = s.normal(1, Tn, 2, 128)
+    n = torch.tensor([Tn], dtype=torch.int32, device=DEV)
+    before, p0 = _append(s, x, y, n)
+    _check_append(s, before, p0, lambda b: (x[b], y[b]))
+    assert s.ks[0, 0, 6, 2].isnan() and s.ks[0, 0, 6, 3].isnan() and not s.ks[0, 0, 6, :2].isnan().any()
+
+
+@gpu
+@pytest.mark.parametrize("Tn", [6, 30])
+def test_append_skips_requests_with_errors(Tn):
+    s = Setup("gqa", 5, 9, [100, 120, 30, 128, 3], extra=0, page=128, seed=2)
+    cap = s.cap
+    x, y = s.normal(5, Tn, s.Hkv, s.d), s.normal(5, Tn, s.Hkv, s.d)
+    s.plen[3] = cap - Tn + 1                        # passes the cache
+    s.table[2, 0] = s.k.shape[0]                    # a page outside the pool
+    for n in ([Tn, -1, Tn, Tn, Tn + 1], [0, Tn, -5, Tn, 2]):
+        s.err.zero_()
+        before, p0 = _append(s, x, y, torch.tensor(n, dtype=torch.int32, device=DEV))
+        assert int(s.err) != 0
+        bad = [b for b in range(5) if not 0 <= n[b] <= Tn or b == 2 or int(p0[b]) + n[b] > cap]
+        table = s.table
+        s.table = torch.where(s.table >= s.k.shape[0], 0, s.table)
+        _check_append(s, before, p0, lambda b: None if b in bad else (x[b, : n[b]], y[b, : n[b]]))
+        s.table = table
+    path = torch.tensor([[0, 3, 9, -1], [0, 1, 2, 3], [0, -1, -1, -1], [0, 1, 2, 3], [0, 5, -1, -1]],
+                        dtype=torch.int32, device=DEV)
+    L = torch.tensor([2, 4, 0, 3, 1], dtype=torch.int32, device=DEV)
+    s.plen[3] = cap - 3
+    s.err.zero_()
+    before, p0 = _append(s, s.kt, s.vt, L, path)
+    s.table[2, 0] = 0
+    _check_append(s, before, p0, lambda b: (s.kt[b, [0, 5]], s.vt[b, [0, 5]]) if b == 4 else None)
+    assert int(s.err) & T.TSD_DEV_ERR_MASK in (T.TSD_DEV_ERR_BAD_TREE, T.TSD_DEV_ERR_CAPACITY,
+                                               T.TSD_DEV_ERR_BAD_PAGE)
+
+
+def _read(s, first, count, Tn):
+    out = [torch.full((s.B, Tn, s.Hkv, s.d), 7.0, dtype=s.dt, device=DEV) for _ in range(2)]
+    i32 = dict(dtype=torch.int32, device=DEV)
+    T.tsd_cache_read_q4(s.desc, *s.arrays(), s.plen, torch.tensor(first, **i32),
+                        torch.tensor(count, **i32), *out, s.err, **s.paging)
+    torch.cuda.synchronize()
+    return out
+
+
+@gpu
+@pytest.mark.parametrize("kind,dtype,page", [("gqa", torch.bfloat16, 0), ("narrow", torch.float32, 128),
+                                             ("one", torch.float32, 0), ("odd", torch.bfloat16, 256)])
+def test_read_gives_the_values(kind, dtype, page):
+    s = Setup(kind, 5, 1, [0, 1, 130, 255, 300], dtype=dtype, page=page, seed=4)
+    first, count = [0, 0, 129, 0, 37], [0, 1, 1, 255, 200]
+    s.ks[tuple(0 for _ in s.ks.shape)] = NAN
+    for Tn in (255, 256, 300):
+        out = _read(s, first, count, Tn)
+        for b in range(5):
+            n = count[b]
+            assert (out[0][b, n:] == 7).all() and (out[1][b, n:] == 7).all()
+            for h in range(s.Hkv):
+                for which, got in zip("kv", out):
+                    want = s.cache(which).values(b, h)[first[b]: first[b] + n].to(dtype)
+                    assert torch.equal(got[b, :n, h].nan_to_num(9.5), want.nan_to_num(9.5)), (b, h, which)
+    assert int(s.err) == 0
+
+
+@gpu
+@pytest.mark.parametrize("bad", [(-1, 3), (5, -1), (5, 33), (90, 11), (2 ** 31 - 1, 2), (0, 2 ** 31 - 1)])
+def test_read_skips_requests_with_errors(bad):
+    s = Setup("one", 3, 1, [100], seed=5)
+    out = _read(s, [0, bad[0], 70], [32, bad[1], 30], 32)
+    assert int(s.err) == T.TSD_DEV_ERR_CAPACITY | 1
+    assert (out[0][1] == 7).all() and (out[1][1] == 7).all()
+    assert torch.equal(out[0][2, :30, 1].double(), s.cache("k").values(2, 1)[70:100].to(s.dt).double())
+
+
+@gpu
+def test_read_reports_pages_outside_the_pool_that_it_needs():
+    s = Setup("one", 2, 1, [300], page=128, seed=6)
+    s.table[0, 0] = -1
+    s.table[1, 2] = s.k.shape[0]
+    out = _read(s, [128, 0], [100, 256], 256)
+    assert int(s.err) == 0 and not (out[1] == 7).all()
+    out = _read(s, [100, 0], [100, 256], 256)
+    assert int(s.err) == T.TSD_DEV_ERR_BAD_PAGE | 0 and (out[0][0] == 7).all()
+    s.plen[1] = s.cap + 1
+    s.err.zero_()
+    _read(s, [128, 0], [100, 256], 256)
+    assert int(s.err) == T.TSD_DEV_ERR_CAPACITY | 1
+
+
+@gpu
+@pytest.mark.parametrize("kind", ["gqa", "narrow"])
+def test_rows_written_are_read_back(kind):
+    """With a the group's largest magnitude, s = a / 8 but for its rounding, 2^-8 of it.  An
+    element next to a on the side where the codes end at 7 is held as 7 s: off by at most
+    a - 7 a / 8 (1 - 2^-8) = a / 8 (1 + 7 2^-8).  The others are off by half a step, or, at the
+    codes' end 8 s, by 2^-8 a: less than that."""
+    s = Setup(kind, 2, 1, [7], extra=100, dtype=torch.float32)
+    x, y = s.normal(2, 100, s.Hkv, s.d), s.normal(2, 100, s.Hkv, s.d)
+    _append(s, x, y, torch.tensor([100, 50], dtype=torch.int32, device=DEV))
+    out = _read(s, [7, 7], [100, 50], 100)
+    for b, n in ((0, 100), (1, 50)):
+        for got, new in zip(out, (x, y)):
+            g, w = (t[b, :n].double().view(n, s.Hkv, -1, G) for t in (got, new))
+            big = w.abs().amax(-1, keepdim=True)
+            assert ((g - w).abs() <= big / 8 * (1 + 7 * 2.0 ** -8) + 1e-30).all()
+            assert ((g - w).square().mean().sqrt() < 0.12 * w.square().mean().sqrt())
+
+
+# -------------------------------------------------------------- attention --
+
+ATTN = [("gqa", 3, 1, [2048, 700, 5], {}), ("gqa", 2, 1, [4100], {}), ("gqa", 2, 4, [1300, 129], {}),
+        ("gqa", 1, 17, [2048], {}), ("gqa", 4, 33, [1024, 257, 130, 900], dict(page=128)),
+        ("gqa", 2, 65, [3000, 128], {}), ("narrow", 3, 1, [1999, 64, 2], {}),
+        ("narrow", 2, 9, [700, 1025], dict(page=256)), ("narrow", 2, 33, [600, 50], {}),
+        ("one", 5, 1, [127, 128, 129, 1, 3], {}), ("one", 2, 16, [500], {}), ("one", 2, 17, [500], {}),
+        ("wide", 2, 1, [5000, 33], dict(page=128)), ("wide", 2, 8, [900], {}), ("wide", 1, 65, [400], {}),
+        ("wide64", 2, 1, [640, 15], {}), ("wide64", 3, 11, [640, 15, 16], {}), ("odd", 3, 5, [77, 0, 401], {}),
+        ("odd", 2, 6, [333], {}), ("gqa", 33, 2, [65, 200, 511, 1, 90], dict(page=128)),
+        ("gqa", 70, 1, [100, 40], {}),
+        ("gqa", 2, 5, [900, 100], dict(dtype=torch.float32)), ("narrow", 2, 3, [500, 64], dict(dtype=torch.float32)),
+        ("wide", 2, 1, [900, 100], dict(dtype=torch.float32, page=128))]
+
+
+@gpu
+@pytest.mark.parametrize("kind,B,R,lens,kw", ATTN)
+def test_attention_matches_plain(kind, B, R, lens, kw):
+    s = Setup(kind, B, R, lens, seed=len(lens) + R, **kw)
+    s.check_attn(*s.attn())
+    assert int(s.err) == 0
+
+
+@gpu
+@pytest.mark.parametrize("kind,R", [("gqa", 1), ("gqa", 4), ("gqa", 20), ("narrow", 2), ("narrow", 30)])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_attention_of_empty_and_tiny_prefixes(kind, R, dtype):
+    s = Setup(kind, 7, R, [0, 1, 2, 15, 16, 17, 31], dtype=dtype, seed=8)
+    s.check_attn(*s.attn())
+    assert int(s.err) == 0

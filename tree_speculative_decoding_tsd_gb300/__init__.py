@@ -26,6 +26,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+from fractions import Fraction
 
 import torch
 
@@ -47,6 +48,7 @@ TSD_DEV_ERR_MASK = 0x7F000000
 TSD_F32 = 0
 TSD_BF16 = 1
 TSD_Q8_BLOCK = 64
+TSD_Q4_GROUP = 32
 VERIFY_PATHS = {"auto": 0, "generic": 1, "mma": 2, "tc": 3}   # TSD_PATH_* of tsd.h
 
 # every symbol the header declares
@@ -59,7 +61,9 @@ EXPORTED = ("tsd_status_string", "tsd_version", "tsd_tree_build_workspace_size",
             "tsd_set_verify_path", "tsd_set_wait_budget",
             "tsd_cache_write_q8", "tsd_commit_path_q8", "tsd_verify_q8_workspace_size",
             "tsd_tree_verify_attn_q8", "tsd_cache_weights", "tsd_cache_weights_q8",
-            "tsd_cache_evict_workspace_size", "tsd_cache_evict", "tsd_cache_evict_q8")
+            "tsd_cache_evict_workspace_size", "tsd_cache_evict", "tsd_cache_evict_q8",
+            "tsd_cache_write_q4", "tsd_commit_path_q4", "tsd_cache_read_q4",
+            "tsd_verify_q4_workspace_size", "tsd_tree_verify_attn_q4", "tsd_qk_norm_rope")
 
 
 class TsdError(RuntimeError):
@@ -73,6 +77,13 @@ class tsd_attn_desc(ctypes.Structure):
                 ("Hkv", ctypes.c_int), ("dk", ctypes.c_int), ("dv", ctypes.c_int),
                 ("cap", ctypes.c_int), ("dtype", ctypes.c_int), ("v_aliases_k", ctypes.c_int),
                 ("scale", ctypes.c_float)]
+
+
+class tsd_rope_desc(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int), ("T", ctypes.c_int), ("Hq", ctypes.c_int),
+                ("Hkv", ctypes.c_int), ("d", ctypes.c_int), ("dtype", ctypes.c_int),
+                ("rot", ctypes.c_int), ("neighbours", ctypes.c_int), ("axes", ctypes.c_int),
+                ("norm", ctypes.c_int), ("eps", ctypes.c_float), ("amplitude", ctypes.c_float)]
 
 
 def _load():
@@ -141,6 +152,20 @@ def _load():
     lib.tsd_cache_evict.restype = I
     lib.tsd_cache_evict_q8.argtypes = [D, I, I, I, P, P, P, P, P, P, P, *paging, P, P, Z, P, P]
     lib.tsd_cache_evict_q8.restype = I
+    lib.tsd_cache_write_q4.argtypes = [D, I, P, P, P, P, P, P, P, *paging, P, P, P]
+    lib.tsd_cache_write_q4.restype = I
+    lib.tsd_commit_path_q4.argtypes = [D, I, P, P, P, P, P, P, P, P, *paging, P, P, P]
+    lib.tsd_commit_path_q4.restype = I
+    lib.tsd_cache_read_q4.argtypes = [D, I, P, P, P, P, *paging, P, P, P, P, P, P, P]
+    lib.tsd_cache_read_q4.restype = I
+    lib.tsd_verify_q4_workspace_size.argtypes = [D]
+    lib.tsd_verify_q4_workspace_size.restype = Z
+    lib.tsd_tree_verify_attn_q4.argtypes = [D, P, P, P, P, P, *paging, P, P, P, P, P, P, P, Z, P, P]
+    lib.tsd_tree_verify_attn_q4.restype = I
+    L = ctypes.c_int64
+    lib.tsd_qk_norm_rope.argtypes = [ctypes.POINTER(tsd_rope_desc), P, L, P, L, P, L, P, P, P, P, P,
+                                     P, P, P, P, P]
+    lib.tsd_qk_norm_rope.restype = I
     lib.tsd_set_verify_path.argtypes = [I]
     lib.tsd_set_verify_path.restype = I
     lib.tsd_set_wait_budget.argtypes = [ctypes.c_longlong]
@@ -697,3 +722,136 @@ def tsd_cache_evict_q8(desc, keep, sink, recent, acc, pos, seen, kq, vq, kexp, v
         d.ref, keep, sink, recent, *_evict_state(d, acc, pos, seen), *cache, *paging,
         _p(prefix_len, "prefix_len", _I32T, (d.B,), d.dev), pws, nws, perr,
         _raw_stream(stream, d.dev)))
+
+
+# ------------------------------------------- the 4-bit cache, and rotation --
+
+_BF16 = (torch.bfloat16,)
+
+
+def _q4_cache(d, kq, vq, kscale, vscale, page_table, page_size):
+    lead, paging = _cache_shapes(d, kq, page_table, page_size)
+    codes, scales, dev = (*lead, d.dk // 2), (*lead, d.dk // TSD_Q4_GROUP), d.dev
+    return (_p(kq, "kq", (_U8,), codes, dev), _p(vq, "vq", (_U8,), codes, dev),
+            _p(kscale, "kscale", _BF16, scales, dev),
+            _p(vscale, "vscale", _BF16, scales, dev)), paging
+
+
+def tsd_cache_write_q4(desc, knew, vnew, new_len, kq, vq, kscale, vscale, prefix_len, err=None,
+                       stream=None, page_table=None, page_size=0):
+    """Append rows knew/vnew [B][T][Hkv][d], new_len[b] of them, to the 4-bit cache."""
+    d = _Dims(desc)
+    T, one = knew.shape[1], (d.B,)
+    cache, paging = _q4_cache(d, kq, vq, kscale, vscale, page_table, page_size)
+    _check("tsd_cache_write_q4", _L().tsd_cache_write_q4(
+        d.ref, T, *_rows(d, knew, vnew, ("knew", "vnew"), T), _p(new_len, "new_len", _I32T, one, d.dev),
+        *cache, *paging, _p(prefix_len, "prefix_len", _I32T, one, d.dev),
+        _scratch(None, err, d.dev)[1], _raw_stream(stream, d.dev)))
+
+
+def tsd_commit_path_q4(desc, S, ktree, vtree, accept_rows, accept_len, kq, vq, kscale, vscale,
+                       prefix_len, err=None, stream=None, page_table=None, page_size=0):
+    """tsd_commit_path into the 4-bit cache."""
+    d = _Dims(desc)
+    one = (d.B,)
+    cache, paging = _q4_cache(d, kq, vq, kscale, vscale, page_table, page_size)
+    _check("tsd_commit_path_q4", _L().tsd_commit_path_q4(
+        d.ref, S, *_rows(d, ktree, vtree, ("ktree", "vtree"), d.R),
+        _p(accept_rows, "accept_rows", _I32T, (d.B, S + 1), d.dev),
+        _p(accept_len, "accept_len", _I32T, one, d.dev), *cache, *paging,
+        _p(prefix_len, "prefix_len", _I32T, one, d.dev), _scratch(None, err, d.dev)[1],
+        _raw_stream(stream, d.dev)))
+
+
+def tsd_cache_read_q4(desc, kq, vq, kscale, vscale, prefix_len, first, count, kout, vout, err=None,
+                      stream=None, page_table=None, page_size=0):
+    """Rows first[b] .. first[b] + count[b] - 1 of the 4-bit cache to kout/vout [B][T][Hkv][d]."""
+    d = _Dims(desc)
+    T, one = kout.shape[1], (d.B,)
+    cache, paging = _q4_cache(d, kq, vq, kscale, vscale, page_table, page_size)
+    _check("tsd_cache_read_q4", _L().tsd_cache_read_q4(
+        d.ref, T, *cache, *paging, _p(prefix_len, "prefix_len", _I32T, one, d.dev),
+        _p(first, "first", _I32T, one, d.dev), _p(count, "count", _I32T, one, d.dev),
+        *_rows(d, kout, vout, ("kout", "vout"), T), _scratch(None, err, d.dev)[1],
+        _raw_stream(stream, d.dev)))
+
+
+def tsd_verify_q4_workspace_size(desc: tsd_attn_desc) -> int:
+    return _L().tsd_verify_q4_workspace_size(ctypes.byref(desc))
+
+
+def tsd_tree_verify_attn_q4(desc, q, kq, vq, kscale, vscale, prefix_len, ktree, vtree, mask, out,
+                            lse, ws, err=None, stream=None, page_table=None, page_size=0):
+    """tsd_tree_verify_attn over the 4-bit cache (contiguous, or pages with ``page_table``)."""
+    d = _Dims(desc)
+    B, R, Hq, dev = d.B, d.R, d.Hq, d.dev
+    cache, paging = _q4_cache(d, kq, vq, kscale, vscale, page_table, page_size)
+    (pws, nws), perr = _scratch(ws, err, dev)
+    _check("tsd_tree_verify_attn_q4", _L().tsd_tree_verify_attn_q4(
+        d.ref, _p(q, "q", d.dt, (B, R, Hq, d.dk), dev), *cache, *paging,
+        _p(prefix_len, "prefix_len", _I32T, (B,), dev), *_rows(d, ktree, vtree, ("ktree", "vtree"), R),
+        _p(mask, "mask", _MASK, (B, R), dev), _p(out, "out", d.dt, (B, R, Hq, d.dv), dev),
+        _p(lse, "lse", _F32T, (B, R, Hq), dev), pws, nws, perr, _raw_stream(stream, dev)))
+
+
+def make_rope_desc(B, T, Hq, Hkv, d, dtype, rot=None, axes=1, neighbours=False, norm=True, eps=1e-6,
+                   amplitude=1.0) -> tsd_rope_desc:
+    """``rot`` dims of a head are rotated (all of them by default)."""
+    return tsd_rope_desc(B, T, Hq, Hkv, d, TSD_BF16 if dtype == torch.bfloat16 else TSD_F32,
+                         d if rot is None else rot, int(neighbours), axes, int(norm), eps, amplitude)
+
+
+def rope_turns(freq, device=None):
+    """``turns`` of tsd_qk_norm_rope from radians per position, [rot / 2] or [axes][rot / 2]
+    (float64): int64 with the bits of the fraction of a turn times 2^64.  A host computation;
+    ``device`` is that of freq by default."""
+    freq = torch.as_tensor(freq, dtype=torch.float64)
+    device = freq.device if device is None else device
+    two_pi = Fraction("6.28318530717958647692528676655900576839433879875021164194989")
+    whole = 1 << 64
+    if not bool(freq.isfinite().all()):
+        raise ValueError("freq: a frequency is not finite")
+    bits = [round(Fraction(x) / two_pi * whole) % whole for x in freq.flatten().tolist()]
+    bits = [b - whole if b >> 63 else b for b in bits]
+    return torch.tensor(bits, dtype=torch.int64).view(-1, freq.shape[-1]).to(device)
+
+
+_TURNS = _MASK
+
+
+def _strided_rows(t, name, dt, shape, dev):
+    """(address, elements between two tokens) of rows [B][T][H][d] that may be a view of a
+    wider array; (None, 0) for None."""
+    if t is None:
+        return None, 0
+    if t.dtype not in dt:
+        raise TypeError(f"{name}: element type {t.dtype}, expected {dt[0]}")
+    if t.shape != shape:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name}: tensor on {t.device}, but the current device is cuda:{dev}")
+    B, T, H, d = shape
+    sb, st, sh, sd = t.stride()
+    if T == 1:
+        st = sb if B > 1 else H * d
+    if sd != 1 or (H > 1 and sh != d) or (B > 1 and sb != T * st):
+        raise ValueError(f"{name}: strides {t.stride()}; tokens have to lie at one distance and a "
+                         f"token's heads side by side")
+    return t.data_ptr(), st
+
+
+def tsd_qk_norm_rope(desc, q, k, v, turns, q_out, k_out, v_out, q_weight=None, k_weight=None,
+                     start=None, offset=None, count=None, stream=None):
+    """RMS norm of every head's query and key and the position rotation; v is copied (v and
+    v_out may be None).  q, k, v [B][T][H][d] may be views of a fused projection."""
+    B, T, Hq, Hkv, d, axes = desc.B, desc.T, desc.Hq, desc.Hkv, desc.d, desc.axes
+    dt, dev = (_attn_dtype(desc),), torch.cuda.current_device()
+    rows_q, rows_k, one = (B, T, Hq, d), (B, T, Hkv, d), (B,)
+    _check("tsd_qk_norm_rope", _L().tsd_qk_norm_rope(
+        ctypes.byref(desc), *_strided_rows(q, "q", dt, rows_q, dev),
+        *_strided_rows(k, "k", dt, rows_k, dev), *_strided_rows(v, "v", dt, rows_k, dev),
+        _p(q_weight, "q_weight", dt, (d,), dev), _p(k_weight, "k_weight", dt, (d,), dev),
+        _p(turns, "turns", _TURNS, (axes, desc.rot // 2), dev), _p(start, "start", _I32T, one, dev),
+        _p(offset, "offset", _I32T, (axes, B, T), dev), _p(count, "count", _I32T, one, dev),
+        _p(q_out, "q_out", dt, rows_q, dev), _p(k_out, "k_out", dt, rows_k, dev),
+        _p(v_out, "v_out", dt, rows_k, dev), _raw_stream(stream, dev)))

@@ -1,0 +1,143 @@
+// tsd_tree_verify_attn_q4: branch-aware tree attention over a 4-bit prefix cache
+// (tsd_q4.cuh) plus the scratch pad's rows in the element type of q.
+//
+// Source: "Adapting Tree-Structured Speculative Decoding to DeepSeek-V4"
+// (review), research gap item 1 and "How it works" steps 3 and 5, as for
+// tsd_tree_verify_attn.  With s = scale q . k, p = exp(s - m), m the running
+// maximum: out = sum p v / sum p, lse = m + log sum p, in one pass over the
+// keys; splits of the prefix are merged by combine_kernel.
+#include "tsd_q4.cuh"
+#include "tsd_simt_attn.cuh"
+
+namespace tsd {
+namespace {
+
+// Four keys of the 4-bit cache, for tsd_simt_attn.cuh: a lane's four dims are half of the
+// codes of a word.
+template <int D>
+struct Q4Keys {
+  static constexpr int kDk = D, kDv = D;
+  static constexpr bool kAlias = false;
+  static __device__ __forceinline__ void values(uint32_t w, float f, int lane, float (&x)[4]) {
+    w >>= 8 * (lane & 1);
+    x[0] = ((int)(w & 15u) - 8) * f;
+    x[1] = ((int)(w >> 16 & 15u) - 8) * f;
+    x[2] = ((int)(w >> 4 & 15u) - 8) * f;
+    x[3] = ((int)(w >> 20 & 15u) - 8) * f;
+  }
+  static __device__ __forceinline__ void read(const Q8AttnArgs& a, int, int, int, long row0, int live,
+                                              int lane, float (&k)[kSimtKeys][1][4],
+                                              float (&v)[kSimtKeys][1][4]) {
+    uint32_t kw[kSimtKeys], vw[kSimtKeys];
+    uint16_t ks[kSimtKeys], vs[kSimtKeys];
+#pragma unroll
+    for (int u = 0; u < kSimtKeys; ++u) {
+      const bool there = u < live && lane < D / 4;
+      const long w = (row0 + u) * (D / 8) + (lane >> 1), s = (row0 + u) * (D / kQ4Group) + (lane >> 3);
+      kw[u] = there ? __ldg((const uint32_t*)a.kc + w) : 0u;
+      vw[u] = there ? __ldg((const uint32_t*)a.vc + w) : 0u;
+      ks[u] = there ? __ldg((const uint16_t*)a.ke + s) : (uint16_t)0;
+      vs[u] = there ? __ldg((const uint16_t*)a.ve + s) : (uint16_t)0;
+    }
+#pragma unroll
+    for (int u = 0; u < kSimtKeys; ++u) {
+      values(kw[u], bf16_value(ks[u]), lane, k[u][0]);
+      values(vw[u], bf16_value(vs[u]), lane, v[u][0]);
+    }
+  }
+};
+
+Q8Plan plan_q4(const tsd_attn_desc& d) {
+  Q8Plan p{};
+  const int M = d.R * (d.Hq / d.Hkv);
+  p.path = kQ8Simt;
+  p.part_bytes = 4;
+  p.rb = M <= 4 ? 4 : 8;
+  p.nrg = (int)ceil_div(M, p.rb);
+  // about four CTAs per SM over the whole batch, splits of at least 64 keys
+  long ns = ceil_div(152L * 4, (long)d.B * d.Hkv * p.nrg);
+  const long most = ceil_div(d.cap, 64);
+  if (ns > most) ns = most;
+  p.split_len = (int)ceil_div(ceil_div(d.cap, ns), 64) * 64;
+  p.nsplit = (int)ceil_div(d.cap, p.split_len);
+  p.ws_bytes = p.nsplit > 1 ? (size_t)d.B * d.Hq * d.R * p.nsplit *
+                                  (d.dv * (size_t)p.part_bytes + sizeof(float2))
+                            : 0;
+  return p;
+}
+
+template <typename T, int D>
+void launch_simt_q4(const Q8AttnArgs& a, const Q8Plan& p, cudaStream_t st) {
+  if (p.rb == 8) launch_simt<T, 8, Q4Keys<D>>(a, p, st);
+  else launch_simt<T, 4, Q4Keys<D>>(a, p, st);
+}
+
+}  // namespace
+}  // namespace tsd
+
+using namespace tsd;
+
+extern "C" size_t tsd_verify_q4_workspace_size(const tsd_attn_desc* d) {
+  if (q4_desc_status(d, true) != TSD_OK) return 0;
+  return plan_q4(*d).ws_bytes;
+}
+
+extern "C" tsd_status tsd_tree_verify_attn_q4(const tsd_attn_desc* d, const void* q,
+                                              const void* kq, const void* vq, const void* kscale,
+                                              const void* vscale, const int32_t* page_table,
+                                              int max_pages, int page_size, int num_pages,
+                                              const int32_t* prefix_len, const void* ktree,
+                                              const void* vtree, const uint64_t* mask, void* out,
+                                              float* lse, void* ws, size_t ws_bytes, int32_t* err,
+                                              tsd_stream_t stream) {
+  const tsd_status ok = q4_desc_status(d, true);
+  if (ok != TSD_OK) return ok;
+  if ((((uintptr_t)err) & 3u) != 0 || !ok_ptr(q) || !ok_ptr(kq) || !ok_ptr(vq) || !ok_ptr(kscale) ||
+      !ok_ptr(vscale) || !ok_ptr(prefix_len) || !ok_ptr(ktree) || !ok_ptr(vtree) || !ok_ptr(mask) ||
+      !ok_ptr(out) || !ok_ptr(lse) || !paging_ok(d, page_table, max_pages, page_size, num_pages))
+    return TSD_ERR_INVALID_ARG;
+  const Q8Plan p = plan_q4(*d);
+  if ((long)d->Hkv * p.nrg > 65535 || p.nsplit > 65535) return TSD_ERR_INVALID_ARG;
+  if (ws_bytes < p.ws_bytes || (p.ws_bytes > 0 && !ok_ptr(ws))) return TSD_ERR_INVALID_ARG;
+  Q8AttnArgs a{};
+  a.q = q;
+  a.kc = (const uint8_t*)kq;
+  a.vc = (const uint8_t*)vq;
+  a.ke = (const uint8_t*)kscale;
+  a.ve = (const uint8_t*)vscale;
+  a.plen = prefix_len;
+  a.kt = ktree;
+  a.vt = vtree;
+  a.mask = mask;
+  a.out = out;
+  a.lse = lse;
+  if (p.nsplit > 1) {
+    const size_t parts = (size_t)d->B * d->Hq * d->R * p.nsplit;
+    a.part_o = ws;
+    a.part_meta = (float2*)((char*)ws + parts * d->dv * p.part_bytes);
+  }
+  a.err = err;
+  a.map = cache_map(d, page_table, max_pages, page_size, num_pages);
+  a.B = d->B;
+  a.R = d->R;
+  a.Hq = d->Hq;
+  a.g = d->Hq / d->Hkv;
+  a.M = d->R * a.g;
+  a.nsplit = p.nsplit;
+  a.split_len = p.split_len;
+  a.nrg = p.nrg;
+  a.rb = p.rb;
+  a.tree_split = p.tree_split;
+  a.by_length = p.by_length;
+  a.qscale = d->scale * 1.4426950408889634f;
+  a.wait_cycles = wait_budget();
+  const cudaStream_t st = (cudaStream_t)stream;
+  if (d->dtype == TSD_F32) {
+    if (d->dk == 128) launch_simt_q4<float, 128>(a, p, st);
+    else launch_simt_q4<float, 64>(a, p, st);
+  } else {
+    if (d->dk == 128) launch_simt_q4<__nv_bfloat16, 128>(a, p, st);
+    else launch_simt_q4<__nv_bfloat16, 64>(a, p, st);
+  }
+  return cuda_status();
+}

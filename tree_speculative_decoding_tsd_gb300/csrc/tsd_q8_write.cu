@@ -22,8 +22,8 @@
 
 #include <type_traits>
 
+#include "tsd_append.cuh"
 #include "tsd_host.h"
-#include "tsd_q8.cuh"
 
 namespace tsd {
 namespace {
@@ -40,8 +40,6 @@ struct Q8WriteArgs {
   int rows, S, parts;      // source rows per request; path length bound; 1 (latent) or 2
 };
 
-constexpr int kNoCode = 0x7fffffff;
-
 // Threads of a CTA, and 8-element vectors of a block per thread.
 template <int D> constexpr int kWriteThreads = D > 128 ? 512 : 256;
 template <int D> constexpr int kWriteVecs = kQ8Block * D / 8 / kWriteThreads<D>;
@@ -51,44 +49,9 @@ template <int D> constexpr int kWriteVecs = kQ8Block * D / 8 / kWriteThreads<D>;
 // four, 61 at three.  Rows of 576 dims need the registers for their vectors.)
 template <typename T, int D> constexpr int kWriteCtas = D > 128 ? 1 : sizeof(T) * D > 256 ? 5 : 6;
 
-struct WriteSmem {
-  int code;
-  int32_t path[17];        // commit: source rows
+struct WriteSmem : AppendSmem {
   uint32_t warp_max[32];
 };
-
-// Rows that request b appends (0 for none), or minus the error code that makes
-// the request be skipped: every thread of the CTA gets the same answer.  c: its
-// count, r: its path entry threadIdx.x (commit; requested with the lengths).
-template <bool kCommit>
-__device__ __forceinline__ int write_rows(const Q8WriteArgs& a, int b, int P, int c, int r,
-                                          WriteSmem& s) {
-  const int tid = threadIdx.x;
-  if (tid == 0) s.code = kNoCode;
-  __syncthreads();
-  int code = 0;
-  const long n = kCommit ? (long)c + 1 : c;
-  if (kCommit && (c < 0 || c > a.S)) code = TSD_DEV_ERR_BAD_TREE;
-  else if (!kCommit && (c < 0 || c > a.rows)) code = TSD_DEV_ERR_CAPACITY;
-  else if (P < 0 || P + n > a.map.cap) code = TSD_DEV_ERR_CAPACITY;
-  else {
-    if (kCommit && tid < n) {
-      if (r < 0 || r >= a.rows) code = TSD_DEV_ERR_BAD_TREE;
-      s.path[tid] = r;
-    }
-    if (a.map.page_size && n > 0) {
-      const int p1 = (int)((P + n - 1) / a.map.page_size);
-      for (int p = P / a.map.page_size + tid; p <= p1; p += blockDim.x) {
-        const int pg = a.map.page_table[(long)b * a.map.max_pages + p];
-        if ((pg < 0 || pg >= a.map.num_pages) && code == 0) code = TSD_DEV_ERR_BAD_PAGE;
-      }
-    }
-  }
-  if (code != 0) atomicMin(&s.code, code);
-  __syncthreads();
-  code = s.code;
-  return code != kNoCode ? -code : (int)n;
-}
 
 // Eight elements as they are in memory, and as fp32.  `top` runs the largest magnitude
 // in a form of the type's own (bf16: two at a time), `bits` gives it as fp32 bits.
@@ -231,7 +194,7 @@ write_q8_kernel(const __grid_constant__ Q8WriteArgs a) {
   __shared__ WriteSmem s;
   grid_dependency_sync();
   const int b = blockIdx.z, P = a.prefix_len[b], c = a.count[b];
-  const int n = write_rows<false>(a, b, P, c, 0, s);
+  const int n = append_rows<false>(a, b, P, c, 0, s);
   if (n <= 0) return;
   const int blk = P / kQ8Block + blockIdx.x;
   if (blk * (long)kQ8Block >= (long)P + n) return;
@@ -242,7 +205,7 @@ __global__ void __launch_bounds__(128) write_advance_kernel(const __grid_constan
   __shared__ WriteSmem s;
   grid_dependency_sync();
   const int b = blockIdx.x, P = a.prefix_len[b], c = a.count[b];
-  const int n = write_rows<false>(a, b, P, c, 0, s);
+  const int n = append_rows<false>(a, b, P, c, 0, s);
   if (threadIdx.x != 0) return;
   if (n < 0) report_error(a.err, -n, b);
   else a.prefix_len[b] = P + n;
@@ -340,7 +303,7 @@ commit_q8_kernel(const __grid_constant__ Q8WriteArgs a) {
   grid_dependency_sync();
   const int b = blockIdx.x, P = a.prefix_len[b], c = a.count[b];
   const int r = threadIdx.x <= a.S ? a.path[(long)b * (a.S + 1) + threadIdx.x] : 0;
-  const int n = write_rows<true>(a, b, P, c, r, s);  // (its barrier: the whole CTA has read P)
+  const int n = append_rows<true>(a, b, P, c, r, s);  // (its barrier: the whole CTA has read P)
   if (threadIdx.x == 0) {
     if (n < 0) report_error(a.err, -n, b);
     else a.prefix_len[b] = P + n;
