@@ -546,3 +546,186 @@ def test_attention_of_empty_and_tiny_prefixes(kind, R, dtype):
     s = Setup(kind, 7, R, [0, 1, 2, 15, 16, 17, 31], dtype=dtype, seed=8)
     s.check_attn(*s.attn())
     assert int(s.err) == 0
+
+
+@gpu
+@pytest.mark.parametrize("kind,R,page", [("gqa", 1, 0), ("gqa", 4, 128), ("narrow", 2, 0), ("gqa", 20, 128),
+                                         ("narrow", 20, 0)])
+def test_attention_leaves_out_what_no_row_sees(kind, R, page):
+    """NaN scales and any codes behind the prefix, and NaN in scratch rows that nobody sees."""
+    s = Setup(kind, 4, R, [0, 100, 129, 240], page=page, seed=21)
+    for b in range(4):
+        for p in range(s.lens[b], s.cap):
+            pg, at = (b, p) if s.table is None else (int(s.table[b, p // page]), p % page)
+            s.ks[pg, :, at], s.vs[pg, :, at] = NAN, INF
+    if R > 2:
+        masks = [[m & ~1 for m in row] for row in s.masks]      # row 1 is seen by no row
+        s.set_masks(masks)
+        s.kt[:, 1], s.vt[:, 1] = NAN, INF
+    out, lse = s.attn()
+    assert out.isfinite().all() and lse.isfinite().all()
+    s.check_attn(out, lse)
+
+
+@gpu
+@pytest.mark.parametrize("kind,R,dtype", [("gqa", 1, torch.bfloat16), ("gqa", 3, torch.bfloat16),
+                                          ("narrow", 2, torch.bfloat16), ("gqa", 20, torch.bfloat16),
+                                          ("gqa", 3, torch.float32)])
+def test_attention_keeps_nan_to_the_rows_that_see_it(kind, R, dtype):
+    s = Setup(kind, 3, R, [200, 300, 50], dtype=dtype, seed=22)
+    s.ks[0, 1, 77, 0] = NAN                         # a key: every row of its head
+    s.vs[0, 0, 5, 1] = NAN                          # a value: its group's dims
+    s.q[1, 0, 3, 9] = NAN
+    s.q[1, R - 1, 5, 0] = INF
+    if R > 1:
+        s.kt[2, R - 1, 0, 3] = NAN
+    out, lse = s.attn()
+    g = s.Hq // s.Hkv
+    assert out[0, :, g: 2 * g].isnan().all() and lse[0, :, g: 2 * g].isnan().all()
+    assert out[0, :, :g, 32:64].isnan().all() and out[0, :, :g, :32].isfinite().all()
+    assert lse[0, :, :g].isfinite().all()
+    assert out[1, 0, 3].isnan().all() and out[1, R - 1, 5].isnan().all()
+    sees = s.sees(2)[:, R - 1] if R > 1 else torch.zeros(1, dtype=torch.bool, device=DEV)
+    assert out[2, sees][:, :g].isnan().all() and out[2, ~sees].isfinite().all()
+    s.check_attn(out, lse)
+
+
+@gpu
+@pytest.mark.parametrize("kind,R", [("gqa", 1), ("gqa", 4), ("gqa", 20), ("narrow", 2), ("narrow", 12)])
+def test_attention_with_late_large_scores(kind, R):
+    """Scores that grow along the cache by far more than the running bound's headroom."""
+    s = Setup(kind, 2, R, [1500, 333], seed=23)
+    ramp = torch.exp2(torch.linspace(-3, 5, s.rows, device=DEV)).bfloat16()
+    s.ks *= ramp[:, None]
+    s.vs *= ramp.flip(0)[:, None]
+    s.check_attn(*s.attn())
+
+
+@gpu
+@pytest.mark.parametrize("kind,R", [("gqa", 1), ("gqa", 3), ("gqa", 20), ("narrow", 2), ("narrow", 12)])
+@pytest.mark.parametrize("power", [-80, -40, 40, 80])
+def test_attention_of_very_small_and_large_values(kind, R, power):
+    s = Setup(kind, 2, R, [700, 40], seed=24)
+    f = 2.0 ** power
+    s.vs *= f
+    s.vt *= f
+    s.check_attn(*s.attn())
+    s = Setup(kind, 2, R, [700, 40], seed=25)
+    s.ks *= f
+    s.kt *= f
+    s.q /= f
+    s.check_attn(*s.attn())
+
+
+@gpu
+def test_attention_of_zero_rows():
+    for R in (1, 20):
+        s = Setup("gqa", 2, R, [300, 20], seed=26)
+        s.vs[:, :, 10:200] = 0
+        s.ks[:, 0] = 0
+        s.q[0, 0, 0] = 0
+        s.check_attn(*s.attn())
+        s.vs.zero_()
+        s.vt.zero_()
+        out, lse = s.attn()
+        assert (out == 0).all() and lse.isfinite().all()
+
+
+@gpu
+@pytest.mark.parametrize("R", [1, 4, 20])
+def test_attention_of_very_large_rows_of_q(R):
+    s = Setup("gqa", 2, R, [200, 30], seed=27)
+    s.q[0, R - 1, 2, 7] = 2.0 ** 117                # a row that one key of its own settles
+    s.q[1, 0, 1] *= 2.0 ** 85
+    s.q[1, R - 1, 5] *= 2.0 ** 124
+    s.ks[1] *= 2.0 ** -85
+    s.kt[1] *= 2.0 ** -85
+    out, lse = s.attn()
+    assert out.isfinite().all() and lse.isfinite().all()
+    s.check_attn(out, lse, requests=[1], heads=[0])
+
+
+@gpu
+@pytest.mark.parametrize("kind,R", [("gqa", 1), ("gqa", 4), ("one", 30), ("gqa", 20)])
+def test_attention_reports_a_page_outside_the_pool(kind, R):
+    s = Setup(kind, 3, R, [300, 500, 200], page=128, seed=28)
+    s.table[1, 2] = s.k.shape[0]
+    s.table[0, 3] = -1                              # not needed
+    out, lse = s.attn()
+    assert int(s.err) == T.TSD_DEV_ERR_BAD_PAGE | 1
+    s.check_attn(out, lse, requests=[0, 2])
+
+
+@gpu
+def test_attention_clamps_lengths_to_the_cache():
+    for R in (1, 20):
+        s = Setup("gqa", 2, R, [140, 140], extra=0, seed=29)
+        s.plen.copy_(torch.tensor([1000, -5], dtype=torch.int32))
+        s.lens = [140, 0]
+        s.check_attn(*s.attn())
+
+
+@gpu
+@pytest.mark.parametrize("R", [1, 3, 20])
+def test_attention_on_streams_and_in_graphs(R):
+    a, b = Setup("gqa", 3, R, [2000, 700, 5], seed=30), Setup("narrow", 2, R, [900, 1500], seed=31)
+    want = [x.attn() for x in (a, b)]
+    bufs = [(torch.zeros_like(o), torch.zeros_like(l), T.workspace(T.tsd_verify_q4_workspace_size(x.desc)))
+            for x, (o, l) in zip((a, b), want)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for x, buf, st in zip((a, b), bufs, streams):
+            x.attn_into(*buf, st)
+    torch.cuda.synchronize()
+    for buf, w in zip(bufs, want):
+        assert torch.equal(buf[0], w[0]) and torch.equal(buf[1], w[1])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        a.attn_into(*bufs[0])
+    a.q.copy_(a.normal(*a.q.shape))
+    a.plen.copy_(torch.tensor([1500, 1, 0], dtype=torch.int32))
+    a.lens = [1500, 1, 0]
+    graph.replay()
+    torch.cuda.synchronize()
+    a.check_attn(*bufs[0][:2])
+
+
+@gpu
+def test_attention_past_32_bit_offsets():
+    """A pool whose codes pass 2^32 bytes, the request's pages at its end."""
+    pages = (1 << 32) // (8 * 128 * 64) + 40
+    for R in (1, 20):
+        s = Setup("gqa", 1, R, [300], page=128, seed=32)
+        k, v = (torch.zeros(pages, 8, 128, 64, dtype=torch.uint8, device=DEV) for _ in range(2))
+        ks, vs = (torch.zeros(pages, 8, 128, 4, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+        new = s.table.long() + pages - s.k.shape[0]
+        for big, small in ((k, s.k), (v, s.v), (ks, s.ks), (vs, s.vs)):
+            big[new[0]] = small[s.table[0].long()]
+        s.k, s.v, s.ks, s.vs, s.table = k, v, ks, vs, new.int()
+        s.paging["page_table"] = s.table
+        s.check_attn(*s.attn(), heads=[0, 7])
+        x, y = s.normal(1, R, 8, 128), s.normal(1, R, 8, 128)
+        n = torch.tensor([R], dtype=torch.int32, device=DEV)
+        T.tsd_cache_write_q4(s.desc, x, y, n, *s.arrays(), s.plen, s.err, **s.paging) if R < 8 else \
+            T.tsd_cache_write_q4(s.desc, x[:, :8].contiguous(), y[:, :8].contiguous(), n.clamp(max=8), *s.arrays(),
+                                 s.plen, s.err, **s.paging)
+        out = _read(s, [299], [2], 2)
+        c, f = quantise(x[0, 0].double())
+        want = ((c - 8).double() * f.repeat_interleave(G, 1)).to(s.dt)
+        assert torch.equal(out[0][0, 1], want) and int(s.err) == 0
+        del k, v, ks, vs
+
+
+@gpu
+@pytest.mark.parametrize("kind,R,page", [("gqa", 20, 128), ("narrow", 20, 0), ("gqa", 5, 0)])
+def test_attention_waits_give_up_at_the_budget(kind, R, page):
+    """A budget of a few cycles: every wait that is not met at once gives up, the error word
+    says so, the call ends soon, and the next call is exact."""
+    s = Setup(kind, 2, R, [900, 300], page=page, seed=33)
+    with T.wait_budget(4):
+        s.attn()
+        assert int(s.err) & T.TSD_DEV_ERR_MASK == T.TSD_DEV_ERR_TIMEOUT
+    s.err.zero_()
+    s.check_attn(*s.attn())
+    assert int(s.err) == 0

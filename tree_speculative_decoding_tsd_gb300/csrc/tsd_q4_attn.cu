@@ -6,7 +6,7 @@
 // tsd_tree_verify_attn.  With s = scale q . k, p = exp(s - m), m the running
 // maximum: out = sum p v / sum p, lse = m + log sum p, in one pass over the
 // keys; splits of the prefix are merged by combine_kernel.
-#include "tsd_q4.cuh"
+#include "tsd_q4_attn.cuh"
 #include "tsd_simt_attn.cuh"
 
 namespace tsd {
@@ -50,26 +50,52 @@ struct Q4Keys {
 Q8Plan plan_q4(const tsd_attn_desc& d) {
   Q8Plan p{};
   const int M = d.R * (d.Hq / d.Hkv);
-  p.path = kQ8Simt;
-  p.part_bytes = 4;
-  p.rb = M <= 4 ? 4 : 8;
-  p.nrg = (int)ceil_div(M, p.rb);
-  // about four CTAs per SM over the whole batch, splits of at least 64 keys
-  long ns = ceil_div(152L * 4, (long)d.B * d.Hkv * p.nrg);
-  const long most = ceil_div(d.cap, 64);
-  if (ns > most) ns = most;
-  p.split_len = (int)ceil_div(ceil_div(d.cap, ns), 64) * 64;
-  p.nsplit = (int)ceil_div(d.cap, p.split_len);
+  const long heads = (long)d.B * d.Hkv;
+  if (d.dtype == TSD_BF16) {
+    const bool few = M <= kQ4FewRows;
+    p.path = few ? kQ8Few : kQ8Rows;
+    p.part_bytes = few ? 4 : 2;
+    p.nrg = few ? 1 : (int)ceil_div(M, 128);
+    p.rb = (int)ceil_div(M, p.nrg);
+    // The split count minimises the modelled time of requests that fill the cache: waves of
+    // CTAs times (tiles of 128 keys + a CTA's set-up and end), and the merge.
+    const long slots = 152L * (few && M <= 8 ? 2 : 1), ends = few ? 6 : 4, merge = few ? 6 : 5;
+    const long units = heads * p.nrg, tiles = ceil_div(d.cap, 128);
+    const long lo = ceil_div(tiles, 256), hi = lo > 64 ? lo : tiles < 64 ? tiles : 64;
+    long best = -1, best_per = tiles;
+    for (long n = lo; n <= hi; ++n) {
+      const long per = ceil_div(tiles, n);
+      const long cost = ceil_div(units * ceil_div(tiles, per), slots) * (per + ends) + (per < tiles ? merge : 0);
+      if (best < 0 || cost < best) { best = cost; best_per = per; }
+    }
+    p.split_len = (int)best_per * 128;
+    p.nsplit = (int)ceil_div(d.cap, p.split_len);
+    p.tree_split = !few && p.nsplit > 1 && best_per <= 8 ? 1 : 0;
+    p.nsplit += p.tree_split;
+    // More CTAs than run at once and a request's keys in one: the longest requests first.
+    p.by_length = p.nsplit == 1 && d.B > 1 && d.B <= 64 && units > slots;
+  } else {
+    p.path = kQ8Simt;
+    p.part_bytes = 4;
+    p.rb = M <= 4 ? 4 : 8;
+    p.nrg = (int)ceil_div(M, p.rb);
+    // about four CTAs per SM over the whole batch, splits of at least 64 keys
+    long ns = ceil_div(152L * 4, heads * p.nrg);
+    const long most = ceil_div(d.cap, 64);
+    if (ns > most) ns = most;
+    p.split_len = (int)ceil_div(ceil_div(d.cap, ns), 64) * 64;
+    p.nsplit = (int)ceil_div(d.cap, p.split_len);
+  }
   p.ws_bytes = p.nsplit > 1 ? (size_t)d.B * d.Hq * d.R * p.nsplit *
                                   (d.dv * (size_t)p.part_bytes + sizeof(float2))
                             : 0;
   return p;
 }
 
-template <typename T, int D>
+template <int D>
 void launch_simt_q4(const Q8AttnArgs& a, const Q8Plan& p, cudaStream_t st) {
-  if (p.rb == 8) launch_simt<T, 8, Q4Keys<D>>(a, p, st);
-  else launch_simt<T, 4, Q4Keys<D>>(a, p, st);
+  if (p.rb == 8) launch_simt<float, 8, Q4Keys<D>>(a, p, st);
+  else launch_simt<float, 4, Q4Keys<D>>(a, p, st);
 }
 
 }  // namespace
@@ -132,12 +158,18 @@ extern "C" tsd_status tsd_tree_verify_attn_q4(const tsd_attn_desc* d, const void
   a.qscale = d->scale * 1.4426950408889634f;
   a.wait_cycles = wait_budget();
   const cudaStream_t st = (cudaStream_t)stream;
-  if (d->dtype == TSD_F32) {
-    if (d->dk == 128) launch_simt_q4<float, 128>(a, p, st);
-    else launch_simt_q4<float, 64>(a, p, st);
+  if (p.path == kQ8Few) {
+    launch_q4_few(a, p, d->dk, st);
+    if (d->dk == 128) launch_combine<__nv_bfloat16, 128, float>(a, p, st);
+    else launch_combine<__nv_bfloat16, 64, float>(a, p, st);
+  } else if (p.path == kQ8Rows) {
+    launch_q4_rows(a, p, d->dk, st);
+    if (d->dk == 128) launch_combine<__nv_bfloat16, 128, __half>(a, p, st);
+    else launch_combine<__nv_bfloat16, 64, __half>(a, p, st);
+  } else if (d->dk == 128) {
+    launch_simt_q4<128>(a, p, st);
   } else {
-    if (d->dk == 128) launch_simt_q4<__nv_bfloat16, 128>(a, p, st);
-    else launch_simt_q4<__nv_bfloat16, 64>(a, p, st);
+    launch_simt_q4<64>(a, p, st);
   }
   return cuda_status();
 }

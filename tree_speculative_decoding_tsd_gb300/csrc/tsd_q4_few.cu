@@ -1,0 +1,519 @@
+// Path of tsd_tree_verify_attn_q4 for bf16 heads of 64 or 128 dims with few packed rows
+// (R tree rows x g query heads of a KV head): decoding, small trees.
+//
+//   S[key][n]  = K . Q^T      16 keys x 8 columns x 16 dims per instruction
+//   O[dim][n] += V^T . P^T    16 dims x 8 columns x 16 keys
+//
+// Widening is what this path has to do cheaply: codes go from shared memory straight into
+// the operand registers of mma.sync (tcgen05 takes operands from shared or tensor memory,
+// so that every widened element would be written and read once more; the products of
+// few columns are far from binding here).  A warp works alone on chunks of 16 keys, which it
+// copies itself, several ahead, into a ring of its own: no barrier between the first
+// chunk and the last.
+//
+// Numbers.
+//   K   a word's masked halves are fp16 numbers as they stand, c * 2^-24 or c * 2^-20
+//       (tsd_q4.cuh), exact; columns of Q carry the factor between the two.  Each group
+//       of 32 dims has its own product, begun at -8 sum(q): (c - 8) . q in fp32, then times
+//       the group's scale: no rounding.
+//   Q   fp16 times a power of two of its row: exact for elements down to 2^-29 of the
+//       row's largest, off by 2^-35 of it at most below.
+//   V   fp16, one fused multiply-add: (c - 8) s 2^(-E - 9), E the exponent above the chunk's
+//       largest scale: 2^-12, or 2^-25 (2^-18 of the chunk's largest value) where that is more.
+//   P   fp16: 2^(x + E - m), m a running bound of x + E over the warp's keys (raised
+//       where a chunk passes it by 8): 2^-12, and steps of 2^-24, 2^-32 of the largest at most.
+//   scratch rows: fp32 on the CUDA cores, a warp per packed row, while the first chunks are
+//       under way.
+// Each warp's sum, bound and output are joined at the end, in fp32.
+#include "tsd_host.h"
+#include "tsd_q4.cuh"
+#include "tsd_q4_attn.cuh"
+#include "tsd_q8_tc.cuh"
+
+namespace tsd {
+namespace {
+
+constexpr int kChunk = 16;                         // keys of a chunk
+
+template <int D, int NT, int W, int S>
+struct FewLayout {
+  static constexpr int NG = D / kQ4Group;
+  static constexpr uint32_t codes = kChunk * D / 2, scales = kChunk * NG * 2;
+  static constexpr uint32_t stage = 2 * codes + 2 * scales;
+  static constexpr uint32_t ring = W * S * stage;
+  static constexpr int pitch = D + 4;              // floats of a row in the joint
+  static constexpr uint32_t joint = W * NT * 8 * pitch * 4;
+  static constexpr uint32_t off_tree = ring > joint ? ring : joint;     // float [8 NT][D]
+  static constexpr uint32_t off_ml = off_tree + NT * 8 * D * 4;         // float2 [W + 1][8 NT]
+  static constexpr uint32_t off_req = off_ml + (W + 1) * NT * 8 * 8;
+  static constexpr uint32_t total = off_req + 16;
+  static_assert(stage % 128 == 0, "whole lines");
+};
+
+__device__ __forceinline__ void cp_async_z(uint32_t dst, const void* src, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst), "l"(src),
+               "r"(there ? 16 : 0) : "memory");
+}
+template <int N>
+__device__ __forceinline__ void cp_async_small(uint32_t dst, const void* src, bool there) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;\n" ::"r"(dst), "l"(src), "n"(N),
+               "r"(there ? N : 0) : "memory");
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t at) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];\n" : "=r"(v) : "r"(at));
+  return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t at) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];\n" : "=r"(v.x), "=r"(v.y) : "r"(at));
+  return v;
+}
+__device__ __forceinline__ uint32_t lds16(uint32_t at) {
+  uint16_t v;
+  asm volatile("ld.shared.u16 %0, [%1];\n" : "=h"(v) : "r"(at));
+  return v;
+}
+__device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                          uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};\n"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// An 8 x 8 matrix of 16-bit elements, a row on four lanes, transposed.
+__device__ __forceinline__ uint32_t transposed(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;\n" : "=r"(y) : "r"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t d;
+  asm("fma.rn.f16x2 %0, %1, %2, %3;\n" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+  return d;
+}
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.f16x2 %0, %1, %2;\n" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+
+// Where 16-byte unit u of row r of a chunk's codes lies: rows side by side, two (D = 128) or
+// four to a line of 128 bytes, the units of a line permuted so that neither way of
+// reading (K: a unit of eight rows; V: a run of units of four even or four odd rows) meets
+// a bank twice.
+template <int D, bool kV>
+__device__ __forceinline__ uint32_t unit_at(int r, int u) {
+  constexpr int U = D / 32;                        // units of a row
+  const int line = r * U >> 3, at = r * U + u & 7;
+  const int x = line & (U - 1);
+  return (uint32_t)(line * 128 + ((at ^ (kV ? 2 * x : x)) << 4));
+}
+
+template <int D, int NT, int W, int S, int kCtas>
+__global__ void __launch_bounds__(W * 32, kCtas) q4_few_kernel(const __grid_constant__ Q8AttnArgs a) {
+  using L = FewLayout<D, NT, W, S>;
+  constexpr int NG = L::NG, NW = D / 64;           // groups; words of V per lane and key
+  extern __shared__ __align__(128) uint8_t smem[];
+  grid_dependency_sync();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
+  const int hk = blockIdx.x, sp = blockIdx.y;
+  int P;
+  const int b = request_at(a, blockIdx.z, P, (volatile int*)(smem + L::off_req));
+  const int nsb = q8_splits(a, P);
+  if (sp >= nsb) return;
+  const int k0 = min(sp * a.split_len, P), k1 = min(P, k0 + a.split_len);
+  const bool with_tree = sp == nsb - 1;
+
+  // ------------------------------------------------------------- the ring
+  const uint32_t ring = su32(smem) + warp * (S * L::stage);
+  const int last = (k1 - k0 + kChunk - 1) / kChunk;   // chunks of the split
+  uint32_t missing = 0;                               // chunks of the ring without a page
+  long row_next = warp < last ? a.map.row(b, hk, k0 + warp * kChunk) : 0;
+  auto request = [&](int c, int slot) {
+    if (c < last) {
+      const long row = row_next;
+      const int pos = k0 + c * kChunk;
+      int nv = min(kChunk, k1 - pos);
+      missing &= ~(1u << slot);
+      if (row < 0) {
+        nv = 0;
+        missing |= 1u << slot;
+        if (lane == 0) report_error(a.err, TSD_DEV_ERR_BAD_PAGE, b);
+      }
+      if (c + W < last) row_next = a.map.row(b, hk, pos + W * kChunk);
+      const uint32_t st = ring + slot * L::stage;
+      const long r0 = row < 0 ? 0 : row;
+#pragma unroll
+      for (int i = 0; i < D / 64; ++i) {
+        const int x = lane + 32 * i, r = x / (D / 32), u = x % (D / 32);
+        const bool there = r < nv;
+        const long at = (r0 + (there ? r : 0)) * (D / 2) + u * 16;
+        cp_async_z(st + unit_at<D, false>(r, u), a.kc + at, there);
+        cp_async_z(st + L::codes + unit_at<D, true>(r, u), a.vc + at, there);
+      }
+      const int r = lane & 15;
+      const bool there = r < nv;
+      const uint8_t* src = (lane < 16 ? a.ke : a.ve) + (r0 + (there ? r : 0)) * (NG * 2);
+      cp_async_small<NG * 2>(st + 2 * L::codes + lane * (NG * 2), src, there);
+    }
+    asm volatile("cp.async.commit_group;\n" ::: "memory");
+  };
+#pragma unroll
+  for (int i = 0; i < S - 1; ++i) request(warp + i * W, i);
+
+  // ------------------------------------------------------ Q as the B operand
+  // lane (g, t): column g, and of each group j the dims of word 4 j + t
+  uint32_t qb[NT][NG][4];
+  float qs[NT][NG][2], c2[NT][2];
+  bool huge = false;                               // a row from 2^117 on (its factor in two steps)
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    const int n = nt * 8 + g;
+    uint4 w[NG];
+    uint32_t top = 0;
+#pragma unroll
+    for (int j = 0; j < NG; ++j) w[j] = make_uint4(0u, 0u, 0u, 0u);
+    if (n < a.M) {
+      const int tr = n / a.g, qh = hk * a.g + n % a.g;
+      const uint4* src = (const uint4*)((const __nv_bfloat16*)a.q + (((long)b * a.R + tr) * a.Hq + qh) * D);
+#pragma unroll
+      for (int j = 0; j < NG; ++j) {
+        w[j] = __ldg(src + 4 * j + t);
+        top = top_pairs(top, w[j]);
+      }
+    }
+    top = top_of(top);
+#pragma unroll
+    for (int o = 1; o < 4; o <<= 1) top = max(top, __shfl_xor_sync(kFull, top, o));
+    // the largest element into [2^14, 2^15)
+    const bool bad = top >= 0x7f800000u;
+    const int e = row_exponent(top);
+    const float f = bad ? 0.f : q8_scale(268 - e);
+    huge = huge || __any_sync(kFull, !bad && e >= 244);
+    // 2^(e - 127) of the row, over 2^14; 2^24 of the codes
+    const float c = bad ? __int_as_float(0x7fffffff) : a.qscale * q8_scale(e);
+#pragma unroll
+    for (int j = 0; j < NG; ++j) {
+      const uint32_t in[4] = {w[j].x, w[j].y, w[j].z, w[j].w};
+      float sum = 0.f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float h = i & 1 ? f * 0.0625f : f;
+        const uint32_t bits = bad ? 0u : in[i];
+        qb[nt][j][i] = pack_half2(__uint_as_float(bits << 16) * h, __uint_as_float(bits & 0xffff0000u) * h);
+        const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&qb[nt][j][i]));
+        sum = fmaf(i & 1 ? 16.f : 1.f, y.x + y.y, sum);
+      }
+#pragma unroll
+      for (int o = 1; o < 4; o <<= 1) sum += __shfl_xor_sync(kFull, sum, o);
+      sum *= -8.f * 5.9604644775390625e-08f;       // -8 * 2^-24
+      qs[nt][j][0] = __shfl_sync(kFull, sum, 8 * t);
+      qs[nt][j][1] = __shfl_sync(kFull, sum, 8 * t + 4);
+    }
+    c2[nt][0] = __shfl_sync(kFull, c, 8 * t);
+    c2[nt][1] = __shfl_sync(kFull, c, 8 * t + 4);
+  }
+
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int x = 0; x < 2; ++x)
+      if (!huge) c2[nt][x] *= 1024.f;
+
+  // --------------------------------------------------------- scratch rows
+  float* const tree_o = (float*)(smem + L::off_tree);
+  float2* const s_ml = (float2*)(smem + L::off_ml);
+  if (with_tree) {
+    constexpr int E = D / 32;                      // dims of a lane
+#pragma unroll 1
+    for (int n = warp; n < a.M; n += W) {
+      const int tr = n / a.g, qh = hk * a.g + n % a.g;
+      const uint64_t vis = (tr > 0 ? a.mask[(long)b * a.R + tr] << 1 : 0ull) | 1ull;
+      auto row4 = [&](const void* base, long row, float (&x)[E]) {
+        const uint32_t* p = (const uint32_t*)((const __nv_bfloat16*)base + row * D) + lane * (E / 2);
+#pragma unroll
+        for (int i = 0; i < E / 2; ++i) {
+          const uint32_t v = __ldg(p + i);
+          x[2 * i] = __uint_as_float(v << 16);
+          x[2 * i + 1] = __uint_as_float(v & 0xffff0000u);
+        }
+      };
+      float q[E], o[E], m = -INFINITY, l = 0.f;
+      row4(a.q, ((long)b * a.R + tr) * a.Hq + qh, q);
+#pragma unroll
+      for (int i = 0; i < E; ++i) o[i] = 0.f;
+#pragma unroll 1
+      for (int j0 = 0; j0 < a.R; j0 += 4) {
+        float k[4][E], v[4][E], s[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const long row = ((long)b * a.R + min(j0 + u, a.R - 1)) * a.map.Hkv + hk;
+          row4(a.kt, row, k[u]);
+          row4(a.vt, row, v[u]);
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          s[u] = 0.f;
+#pragma unroll
+          for (int i = 0; i < E; ++i) s[u] = fmaf(q[i], k[u][i], s[u]);
+        }
+#pragma unroll
+        for (int o2 = 16; o2 > 0; o2 >>= 1)
+#pragma unroll
+          for (int u = 0; u < 4; ++u) s[u] += __shfl_xor_sync(kFull, s[u], o2);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int j = j0 + u;
+          if (j >= a.R || !((vis >> j) & 1ull)) continue;      // (the same for the whole warp)
+          const float x = s[u] * a.qscale;
+          if (x == -INFINITY) continue;
+          const float mn = fmaxf(m, x);
+          const float al = mn == m ? 1.f : ex2(m - mn), p = ex2(x - mn);
+          m = mn;
+          l = fmaf(l, al, p);
+#pragma unroll
+          for (int i = 0; i < E; ++i) o[i] = fmaf(o[i], al, p * v[u][i]);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < E; ++i) tree_o[n * D + lane * E + i] = o[i] * 0.001953125f;   // 2^-9
+      if (lane == 0) s_ml[W * NT * 8 + n] = make_float2(m, l);
+    }
+  }
+
+  // ------------------------------------------------------------ the chunks
+  float acc[NT][NW * 4][4], m[NT][2], l[NT][2];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+    for (int i = 0; i < NW * 4; ++i)
+#pragma unroll
+      for (int x = 0; x < 4; ++x) acc[nt][i][x] = 0.f;
+    m[nt][0] = m[nt][1] = -INFINITY;
+    l[nt][0] = l[nt][1] = 0.f;
+  }
+  int slot = 0;
+#pragma unroll 1
+  for (int c = warp; c < last; c += W) {
+    asm volatile("cp.async.wait_group %0;\n" ::"n"(S - 2) : "memory");
+    __syncwarp();
+    const int nv = (missing >> slot) & 1u ? 0 : min(kChunk, k1 - (k0 + c * kChunk));
+    request(c + (S - 1) * W, slot == 0 ? S - 1 : slot - 1);
+    const uint32_t st = ring + slot * L::stage;
+    slot = slot == S - 1 ? 0 : slot + 1;
+
+    // scores of keys g and g + 8, columns 2 t and 2 t + 1
+    float s[NT][4];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int x = 0; x < 4; ++x) s[nt][x] = 0.f;
+    uint32_t ks[2][NG / 2];
+    if constexpr (NG == 4) {
+      const uint2 x = lds64(st + 2 * L::codes + g * 8), y = lds64(st + 2 * L::codes + g * 8 + 64);
+      ks[0][0] = x.x; ks[0][1] = x.y; ks[1][0] = y.x; ks[1][1] = y.y;
+    } else {
+      ks[0][0] = lds32(st + 2 * L::codes + g * 4);
+      ks[1][0] = lds32(st + 2 * L::codes + g * 4 + 32);
+    }
+#pragma unroll
+    for (int j = 0; j < NG; ++j) {
+      const uint32_t w0 = lds32(st + unit_at<D, false>(g, j) + 4 * t);
+      const uint32_t w1 = lds32(st + unit_at<D, false>(g + 8, j) + 4 * t);
+      const uint32_t h0 = w0 >> 8, h1 = w1 >> 8;
+      const float s0 = j & 1 ? __uint_as_float(ks[0][j / 2] & 0xffff0000u) : __uint_as_float(ks[0][j / 2] << 16);
+      const float s1 = j & 1 ? __uint_as_float(ks[1][j / 2] & 0xffff0000u) : __uint_as_float(ks[1][j / 2] << 16);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        float d[4] = {qs[nt][j][0], qs[nt][j][1], qs[nt][j][0], qs[nt][j][1]};
+        mma_16816(d, w0 & 0x000f000fu, w1 & 0x000f000fu, w0 & 0x00f000f0u, w1 & 0x00f000f0u,
+                  qb[nt][j][0], qb[nt][j][1]);
+        mma_16816(d, h0 & 0x000f000fu, h1 & 0x000f000fu, h0 & 0x00f000f0u, h1 & 0x00f000f0u,
+                  qb[nt][j][2], qb[nt][j][3]);
+        s[nt][0] = fmaf(d[0], s0, s[nt][0]);
+        s[nt][1] = fmaf(d[1], s0, s[nt][1]);
+        s[nt][2] = fmaf(d[2], s1, s[nt][2]);
+        s[nt][3] = fmaf(d[3], s1, s[nt][3]);
+      }
+    }
+
+    // the exponent above the chunk's largest value scale
+    const uint32_t sv = st + 2 * L::codes + L::scales;
+    int E;
+    {
+      const uint32_t w = lds32(sv + (lane & (8 * NG - 1)) * 4);
+      const uint32_t lo = w & 0x7fffu, hi = w >> 16 & 0x7fffu;
+      const uint32_t top = max(lo < 0x7f80u ? lo : 0u, hi < 0x7f80u ? hi : 0u);
+      E = min(max((int)(__reduce_max_sync(kFull, top) >> 7) - 126, kQ4MinExp), kQ4MaxExp);
+    }
+    const float fE = (float)E;
+
+    // P, in the layout of the scores
+    uint32_t pb[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      float y[4];
+      if (huge) {
+#pragma unroll
+        for (int x = 0; x < 4; ++x) s[nt][x] *= 1024.f;
+      }
+#pragma unroll
+      for (int x = 0; x < 4; ++x) y[x] = fmaf(s[nt][x], c2[nt][x & 1], fE);
+      if (nv < kChunk) {
+        if (g >= nv) y[0] = y[1] = -INFINITY;
+        if (g + 8 >= nv) y[2] = y[3] = -INFINITY;
+      }
+      const float y0 = fmaxf(y[0], y[2]), y1 = fmaxf(y[1], y[3]);
+      if (__any_sync(kFull, !(y0 <= m[nt][0] + kOverflow) || !(y1 <= m[nt][1] + kOverflow))) {
+        float top[2] = {y0, y1};
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+#pragma unroll
+          for (int o = 4; o < 32; o <<= 1) top[x] = fmaxf(top[x], __shfl_xor_sync(kFull, top[x], o));
+          const float mn = fmaxf(m[nt][x], top[x]);
+          const float al = mn == m[nt][x] ? 1.f : ex2(m[nt][x] - mn);
+          m[nt][x] = mn;
+          l[nt][x] *= al;
+#pragma unroll
+          for (int i = 0; i < NW * 4; ++i) {
+            acc[nt][i][x] *= al;
+            acc[nt][i][x + 2] *= al;
+          }
+        }
+      }
+      const float m0 = m[nt][0] == -INFINITY ? 0.f : m[nt][0], m1 = m[nt][1] == -INFINITY ? 0.f : m[nt][1];
+      const float p0 = ex2(y[0] - m0), p1 = ex2(y[1] - m1), p2 = ex2(y[2] - m0), p3 = ex2(y[3] - m1);
+      const float down = q8_scale(127 - E);
+      l[nt][0] = fmaf(p0 + p2, down, l[nt][0]);
+      l[nt][1] = fmaf(p1 + p3, down, l[nt][1]);
+      pb[nt][0] = transposed(pack_half2(p0, p1));
+      pb[nt][1] = transposed(pack_half2(p2, p3));
+    }
+
+    // V: lane (g, t) takes dims 8 NW g .. of keys 2 t, 2 t + 1 and 2 t + 8, 2 t + 9
+    uint32_t f0[2], f1[2], z[2], v[4][NW];
+    const float up = q8_scale(127 + 15 - E);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int r = 2 * t + 8 * i;
+      const uint32_t at = sv + r * (NG * 2) + (NG == 4 ? g >> 1 : g >> 2) * 2;
+      f0[i] = pack_half2(bf16_value(lds16(at)) * up, bf16_value(lds16(at + NG * 2)) * up);
+      f1[i] = hmul2(f0[i], 0x2c002c00u);           // 2^-4
+      z[i] = hmul2(f0[i], 0x80088008u);            // -2^-21
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        if constexpr (NW == 2) {
+          const uint2 y = lds64(st + L::codes + unit_at<D, true>(r + x, g >> 1) + 8 * (g & 1));
+          v[2 * i + x][0] = y.x;
+          v[2 * i + x][NW - 1] = y.y;
+        } else {
+          v[2 * i + x][0] = lds32(st + L::codes + unit_at<D, true>(r + x, g >> 2) + 4 * (g & 3));
+        }
+      }
+    }
+#pragma unroll
+    for (int w = 0; w < NW; ++w) {
+      // the halves of two keys: even dims, odd dims
+      uint32_t ea = __byte_perm(v[0][w], v[1][w], 0x5410), oa = __byte_perm(v[0][w], v[1][w], 0x7632);
+      uint32_t eb = __byte_perm(v[2][w], v[3][w], 0x5410), ob = __byte_perm(v[2][w], v[3][w], 0x7632);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t mask = i & 1 ? 0x00f000f0u : 0x000f000fu;
+        const uint32_t* const f = i & 1 ? f1 : f0;
+        const uint32_t a0 = hfma2(ea & mask, f[0], z[0]), a1 = hfma2(oa & mask, f[0], z[0]);
+        const uint32_t a2 = hfma2(eb & mask, f[1], z[1]), a3 = hfma2(ob & mask, f[1], z[1]);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) mma_16816(acc[nt][4 * w + i], a0, a1, a2, a3, pb[nt][0], pb[nt][1]);
+        if (i == 1) {
+          ea >>= 8;
+          oa >>= 8;
+          eb >>= 8;
+          ob >>= 8;
+        }
+      }
+    }
+  }
+
+  // ------------------------------------------------------------- the joint
+  asm volatile("cp.async.wait_group 0;\n" ::: "memory");
+  __syncthreads();                                 // the ring has been read
+  float* const s_o = (float*)smem;
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      float sum = l[nt][x];
+#pragma unroll
+      for (int o = 4; o < 32; o <<= 1) sum += __shfl_xor_sync(kFull, sum, o);
+      const int n = nt * 8 + 2 * t + x;
+      if (g == 0) s_ml[warp * NT * 8 + n] = make_float2(m[nt][x], sum);
+      float* const dst = s_o + (warp * NT * 8 + n) * L::pitch + 8 * NW * g;
+#pragma unroll
+      for (int i = 0; i < NW * 4; ++i)
+        *(float2*)(dst + 2 * i) = make_float2(acc[nt][i][x], acc[nt][i][x + 2]);
+    }
+  __syncthreads();
+  for (int i = tid; i < a.M * (D / 2); i += W * 32) {
+    const int n = i / (D / 2), c = i % (D / 2) * 2;
+    float2 ml[W + 1];
+    float top = -INFINITY;
+#pragma unroll
+    for (int w = 0; w <= W; ++w) {
+      ml[w] = w < W || with_tree ? s_ml[w * NT * 8 + n] : make_float2(-INFINITY, 0.f);
+      top = fmaxf(top, ml[w].x);
+    }
+    float total = 0.f;
+    float2 o = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int w = 0; w <= W; ++w) {
+      if (w == W && !with_tree) break;
+      // (no bound: nothing seen, or scores that are all NaN)
+      const float f = ml[w].x == -INFINITY ? (ml[w].y != ml[w].y ? ml[w].y : 0.f) : ex2(ml[w].x - top);
+      const float2 x = w < W ? *(const float2*)(s_o + (w * NT * 8 + n) * L::pitch + c)
+                             : *(const float2*)(tree_o + n * D + c);
+      total = fmaf(f, ml[w].y, total);
+      if (f != 0.f) {
+        o.x = fmaf(f, x.x, o.x);
+        o.y = fmaf(f, x.y, o.y);
+      }
+    }
+    const float inv = total == 0.f ? 0.f : 512.f / total;
+    o.x *= inv;
+    o.y *= inv;
+    const float lse2 = top + log2f(total);
+    const int tr = n / a.g, qh = hk * a.g + n % a.g;
+    if (nsb == 1) {
+      const long orow = ((long)b * a.R + tr) * a.Hq + qh;
+      *(uint32_t*)((__nv_bfloat16*)a.out + orow * D + c) = pack_bf16x2(o.x, o.y);
+      if (c == 0) a.lse[orow] = lse2 * 0.69314718055994531f;
+    } else {
+      const long prow = (((long)b * a.Hq + qh) * a.R + tr) * a.nsplit + sp;
+      *(float2*)((float*)a.part_o + prow * D + c) = o;
+      if (c == 0) a.part_meta[prow] = make_float2(lse2, 1.f);
+    }
+  }
+}
+
+template <int D, int NT, int W, int S, int kCtas>
+void launch_few(const Q8AttnArgs& a, const Q8Plan& p, cudaStream_t st) {
+  const uint32_t smem = FewLayout<D, NT, W, S>::total;
+  const auto kern = q4_few_kernel<D, NT, W, S, kCtas>;
+  cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  launch(kern, dim3(a.map.Hkv, p.nsplit, a.B), dim3(W * 32), smem, st, a);
+}
+
+}  // namespace
+
+void launch_q4_few(const Q8AttnArgs& a, const Q8Plan& p, int D, cudaStream_t st) {
+  if (D == 128) {
+    if (a.M <= 8) launch_few<128, 1, 8, 5, 2>(a, p, st);
+    else launch_few<128, 2, 8, 6, 1>(a, p, st);
+  } else {
+    if (a.M <= 8) launch_few<64, 1, 8, 6, 2>(a, p, st);
+    else launch_few<64, 2, 8, 6, 1>(a, p, st);
+  }
+}
+
+}  // namespace tsd

@@ -1,0 +1,791 @@
+// tcgen05 path of tsd_tree_verify_attn_q4 for bf16 heads of 64 or 128 dims with more packed
+// rows (R tree rows x g query heads of a KV head) than tsd_q4_few.cu takes: up to 128 per
+// CTA, on the lanes of the tensor memory.
+//
+//   S[n][key]  = Q . K_tile^T      M = 128 packed rows, N = 128 keys, K = d
+//   O[n][dim] += P . V_tile        M = 128 packed rows, N = d, K = 128 keys
+//
+// The layout, the two streams (the halves of a tile have a softmax warpgroup, scores, P, an
+// accumulator, a bound and a sum each) and the lazy bound are those of tsd_q8_tc.cu.  Here
+// both K and V are widened to fp16 by warps, straight from global memory through
+// registers into shared memory (rows of 64 elements, 128-byte swizzle: the same layout
+// serves K, whose rows are the product's columns, and V, whose rows are summed over).
+//
+// Numbers.
+//   K, V   fp16: (c - 8) s 2^(-E - 9), E the exponent above the tile's largest scale (K and V
+//          apart), by one fused multiply-add of a masked word (tsd_q4.cuh): 2^-12, or 2^-25
+//          (2^-18 of the tile's largest value) where that is more.
+//   Q      fp16 times a power of two of its row (largest element into [2^14, 2^15)): exact
+//          down to 2^-29 of it
+//   tree   scratch rows of K and V in fp16, each times a power of two of its own
+//   P      fp16: 2^(x + E - m + 7), m a running bound of x + E: 2^-12, and steps of 2^-24, 2^-39
+//          of the largest
+// A score's factor takes the tile's and the row's power of two in fp32.
+//
+// Roles (512 threads, 128 registers each): warps 0-3 and 4-7 softmax and epilogue; warp 8
+// issues the products with V and owns the tensor memory, warp 9 those with Q; warp 10 reads
+// the tiles' scales ahead, finds E and leaves fp16 factors in a ring; warps 11-15 widen, K a
+// tile ahead of V.  mbarriers order scales -> K -> S -> softmax -> O and V -> O; every wait
+// is bounded.
+#include <type_traits>
+
+#include "tsd_common.cuh"
+#include "tsd_host.h"
+#include "tsd_q4.cuh"
+#include "tsd_q4_attn.cuh"
+#include "tsd_q8_tc.cuh"
+
+namespace tsd {
+namespace {
+
+constexpr int kPv = 8, kQk = 9, kScale = 10, kWide = 11, kWideWarps = 5;
+constexpr int kWideThreads = kWideWarps * 32;
+constexpr int kThreads = (kWide + kWideWarps) * 32;
+constexpr int kStages = 3;                      // widened tiles of K, and of V
+constexpr int kScaleRing = 4;                   // tiles of factors
+constexpr int kRows = 128;
+// Tensor memory columns: a tile's scores (128), Q (64), the streams' P (32 each), the
+// accumulators (d each).
+constexpr uint32_t kColQ = 128, kColP = 192, kColO = 256;
+
+template <int D>
+struct RowLayout {
+  static constexpr int NG = D / kQ4Group;
+  static constexpr uint32_t t_bytes = kKeys * D * 2;                   // a widened tile
+  static constexpr uint32_t f_bytes = kKeys * NG * 2;                  // a tile's factors of K, or of V
+  static constexpr uint32_t off_k = 0;
+  static constexpr uint32_t off_v = kStages * t_bytes;
+  static constexpr uint32_t off_f = off_v + kStages * t_bytes;         // fp16 [ring][K, V][128][NG]
+  static constexpr uint32_t off_ml = off_f + kScaleRing * 2 * f_bytes; // float2[2][128] (m, l)
+  static constexpr uint32_t off_rows = off_ml + 16 * kRows;            // i64[kMaxTiles]
+  static constexpr uint32_t off_tree = off_rows + 8 * kMaxTiles;       // 4 x 32 bits [128]
+  static constexpr uint32_t off_ek = off_tree + 16 * kKeys;            // i8[kMaxTiles]: E of K
+  static constexpr uint32_t off_ev = off_ek + kMaxTiles;               // and of V
+  static constexpr uint32_t off_bar = off_ev + kMaxTiles;
+  static constexpr int nbar = 32;
+  static constexpr uint32_t off_flags = off_bar + 8 * nbar;            // tmem, abort
+  static constexpr uint32_t off_top = off_flags + 8;                   // int[kWideWarps]
+  static constexpr uint32_t off_req = off_top + 4 * kWideWarps;        // request, its length
+  static constexpr uint32_t total = off_req + 8;
+  static_assert(total + 1024 <= 232448, "shared memory budget");
+  static_assert(kTreeBytes<D> <= t_bytes && kStages > 1, "the scan's rows");
+};
+
+// FULL: written, or the product is done; EMPTY: read (F_EMPTY: by the widening warps,
+// S_EMPTY: by the softmax, the others: by the product).  S, P_FULL and PV_DONE: one per
+// stream.  FINAL: one per issuing warp.
+enum { BAR_K_FULL = 0, BAR_K_EMPTY = 3, BAR_V_FULL = 6, BAR_V_EMPTY = 9, BAR_F_FULL = 12,
+       BAR_F_EMPTY = 16, BAR_S_FULL = 20, BAR_S_EMPTY = 22, BAR_P_FULL = 24, BAR_PV_DONE = 26,
+       BAR_O_DONE = 28, BAR_FINAL = 29 };
+
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32]) {
+  uint32_t r[32];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
+      "%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]),
+        "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
+        "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+      "%14,%15,%16};\n" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+// D (+)= A.B, fp16, with A in tensor memory (two elements to a column).
+__device__ __forceinline__ void mma_f16_ta(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+                                           uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(acc));
+}
+__device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t d;
+  asm("fma.rn.f16x2 %0, %1, %2, %3;\n" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+  return d;
+}
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.f16x2 %0, %1, %2;\n" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+
+// A widening warp's share of a tile: 16-byte chunks (the 32 codes of a group) of eight (D =
+// 128) or sixteen rows at a time, every kWideWarps-th such block.  Eight lanes that store
+// together hold two groups of a half row and four rows: their 16-byte units, permuted by
+// the swizzle, fall on eight different columns.
+template <int D>
+struct Share4 {
+  static constexpr int NG = D / kQ4Group;
+  static constexpr int kBlockRows = 32 / NG, kBlocks = kKeys / kBlockRows;
+  static constexpr int kCount = (kBlocks + kWideWarps - 1) / kWideWarps;
+  int row, grp, first;                             // within a block; the warp's first block
+  uint32_t dst;                                    // the chunk's place in a stage, but for the units
+  __device__ __forceinline__ Share4(int warp, int lane) {
+    const int r = (lane >> 1) & 3, h = lane >> 3;
+    grp = NG == 4 ? (lane & 1) + 2 * (h & 1) : lane & 1;
+    row = NG == 4 ? 4 * (h >> 1) + r : 4 * h + r;
+    first = warp;
+    dst = (uint32_t)((grp >> 1) * kHalf + row * 128);
+  }
+  // chunks of the rows below nvalid of the tile whose codes start at `src`
+  __device__ __forceinline__ void load(uint4 (&w)[kCount], const uint8_t* src, int nvalid) const {
+#pragma unroll
+    for (int i = 0; i < kCount; ++i) {
+      const int r = (first + i * kWideWarps) * kBlockRows + row;
+      w[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (r < nvalid) w[i] = ld_stream(src + (long)r * (D / 2) + grp * 16);
+    }
+  }
+  // factors: fp16 s 2^(15 - E) [128][NG], 0 for rows that are not there
+  __device__ __forceinline__ void widen(const uint4 (&w)[kCount], const uint8_t* factors,
+                                        uint8_t* stage) const {
+#pragma unroll
+    for (int i = 0; i < kCount; ++i) {
+      const int blk = first + i * kWideWarps;
+      if (blk >= kBlocks) break;                   // (a short last round)
+      const int r = blk * kBlockRows + row;
+      const uint32_t f = *(const uint16_t*)(factors + (r * NG + grp) * 2);
+      const uint32_t f0 = f | f << 16, f1 = hmul2(f0, 0x2c002c00u), z = hmul2(f0, 0x80088008u);
+      uint8_t* const d = stage + blk * (kBlockRows * 128) + dst;
+      const uint32_t in[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const uint32_t a = in[u], b = a >> 8;
+        const uint4 h = make_uint4(hfma2(a & 0x000f000fu, f0, z), hfma2(a & 0x00f000f0u, f1, z),
+                                   hfma2(b & 0x000f000fu, f0, z), hfma2(b & 0x00f000f0u, f1, z));
+        // (the block's rows start at a multiple of eight: the swizzle is that of `row`)
+        *(uint4*)(d + (((4 * (grp & 1) + u) ^ (row & 7)) << 4)) = h;
+      }
+    }
+  }
+};
+
+// The scratch rows' keys as fp16, where a K tile would be.
+template <int D>
+__device__ __forceinline__ void tree_rows(const Q8AttnArgs& a, const void* src, int b, int hk, int wt,
+                                          const float* in, uint8_t* stage) {
+#pragma unroll 2
+  for (int x = wt; x < kKeys * (D / 8); x += kWideThreads) {
+    const int row = x / (D / 8), u = x % (D / 8);
+    const float f = in[row];
+    uint4 v = make_uint4(0u, 0u, 0u, 0u);
+    if (f != 0.f)
+      v = scale8(__ldg((const uint4*)((const __nv_bfloat16*)src +
+                                      (((long)b * a.R + row) * a.map.Hkv + hk) * D) + u), f);
+    *(uint4*)(stage + (u >> 3) * kHalf + row * 128 + (((u & 7) ^ (row & 7)) << 4)) = v;
+  }
+}
+
+// A lane's four rows of a tile's scales: a word or two each.
+template <int D>
+struct Scales {
+  static constexpr int NW = D / 64;                // words of a row
+  uint32_t w[4][NW];
+  __device__ __forceinline__ void load(const uint8_t* src, int nvalid, int lane) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = lane + 32 * i;
+#pragma unroll
+      for (int x = 0; x < NW; ++x) w[i][x] = 0u;
+      if (r < nvalid) {
+        if constexpr (NW == 2) {
+          const uint2 v = __ldg((const uint2*)src + r);
+          w[i][0] = v.x;
+          w[i][NW - 1] = v.y;
+        } else {
+          w[i][0] = __ldg((const uint32_t*)src + r);
+        }
+      }
+    }
+  }
+  // the exponent above the largest finite one (of the whole warp's)
+  __device__ __forceinline__ int exponent() const {
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int x = 0; x < NW; ++x) {
+        const uint32_t lo = w[i][x] & 0x7fffu, hi = w[i][x] >> 16 & 0x7fffu;
+        top = max(top, max(lo < 0x7f80u ? lo : 0u, hi < 0x7f80u ? hi : 0u));
+      }
+    return min(max((int)(__reduce_max_sync(kFull, top) >> 7) - 126, kQ4MinExp), kQ4MaxExp);
+  }
+  // s 2^(15 - E) in fp16: exact down to 2^-29 2^E
+  __device__ __forceinline__ void store(uint8_t* dst, int E, int lane) const {
+    const float up = q8_scale(127 + 15 - E);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int x = 0; x < NW; ++x)
+        ((uint32_t*)dst)[(lane + 32 * i) * NW + x] =
+            pack_half2(__uint_as_float(w[i][x] << 16) * up, __uint_as_float(w[i][x] & 0xffff0000u) * up);
+  }
+};
+
+template <int D, bool kPoll>
+__global__ void __launch_bounds__(kThreads, 1) q4_rows_kernel(const __grid_constant__ Q8AttnArgs a) {
+  using L = RowLayout<D>;
+  constexpr int NG = L::NG;
+  grid_dependency_sync();
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  const uint32_t raw = su32(smem_raw);
+  const uint32_t sbase = (raw + 1023u) & ~1023u;
+  uint8_t* smem = smem_raw + (sbase - raw);
+  float2* s_ml = (float2*)(smem + L::off_ml);
+  long long* tile_row = (long long*)(smem + L::off_rows);
+  float* kt_in = (float*)(smem + L::off_tree);      // tree rows: factors into fp16 (0: row of zeros)
+  float* vt_in = kt_in + kKeys;
+  float* kt_out = vt_in + kKeys;                    // factor of the scores (NaN: a row with a NaN or inf)
+  int* vt_u = (int*)(kt_out + kKeys);               // exponent of the value row
+  volatile int8_t* ek = (volatile int8_t*)(smem + L::off_ek);
+  volatile int8_t* ev = (volatile int8_t*)(smem + L::off_ev);
+  volatile uint32_t* flags = (volatile uint32_t*)(smem + L::off_flags);
+  int* s_top = (int*)(smem + L::off_top);           // largest exponent of a scratch value row, by warp
+  const uint32_t bar0 = sbase + L::off_bar;
+  auto bar = [&](int i) { return bar0 + 8u * i; };
+  auto wait_ready = [&](uint32_t at, uint32_t parity) {
+    return phase_ready<kPoll>(at, parity, a.wait_cycles);
+  };
+  auto wait_timed = [&](uint32_t at, uint32_t parity) {
+    return phase_timed<kPoll>(at, parity, a.wait_cycles);
+  };
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int hk = blockIdx.x / a.nrg, rg = blockIdx.x % a.nrg, sp = blockIdx.y;
+  int P;
+  const int b = request_at(a, blockIdx.z, P, (volatile int*)(smem + L::off_req));
+  const int nsb = q8_splits(a, P);
+  if (sp >= nsb) return;
+  const int k0 = min(sp * a.split_len, P), k1 = min(P, k0 + a.split_len);
+  const int n_pre = (k1 - k0 + kKeys - 1) / kKeys;
+  const bool with_tree = sp == nsb - 1;             // R <= 65 < 128: one tile
+  const int ntiles = n_pre + (with_tree ? 1 : 0);
+  const int row_base = rg * a.rb;
+  const int rows_here = min(a.rb, a.M - row_base);
+  const int live_warps = (rows_here + 31) / 32;     // softmax warps of a stream with rows
+  auto valid_of = [&](int t) { return min(kKeys, k1 - (k0 + t * kKeys)); };
+
+  // ---------------------------------------------------------------- set-up
+  const int wt = tid - kWide * 32;
+  using Share = Share4<D>;
+  const Share share(warp - kWide, lane);
+  uint64_t mask = 0ull;     // softmax threads: the scratch rows that the row sees,
+  float c2 = 0.f;           // and the factor of its scores
+  uint4 kreg[Share::kCount], vreg[Share::kCount];
+  // the tile at cache row `row` (a missing page: none)
+  auto load_codes = [&](uint4 (&w)[Share::kCount], const uint8_t* codes, long row, int nvalid) {
+    share.load(w, codes + (row < 0 ? 0 : row) * (D / 2), row < 0 ? 0 : nvalid);
+  };
+  Scales<D> ks, vs;
+  auto load_scales = [&](long row, int nvalid) {
+    const long at = (row < 0 ? 0 : row) * (NG * 2);
+    ks.load(a.ke + at, row < 0 ? 0 : nvalid, lane);
+    vs.load(a.ve + at, row < 0 ? 0 : nvalid, lane);
+  };
+
+  if (warp >= kWide) {
+    // the first tile, the rows of the split's tiles, the scratch rows
+    if (with_tree) tree_fetch<D, kWideThreads>(a, b, hk, wt, sbase + L::off_v, L::t_bytes);
+    const long r0 = n_pre > 0 ? a.map.row(b, hk, k0) : -1;
+    const long rt = wt < n_pre ? a.map.row(b, hk, k0 + wt * kKeys) : -1;
+    if (n_pre > 0) {
+      load_codes(kreg, a.kc, r0, valid_of(0));
+      load_codes(vreg, a.vc, r0, valid_of(0));
+    }
+#pragma unroll 1
+    for (int t = wt; t < n_pre; t += kWideThreads) {
+      const long r = t == wt ? rt : a.map.row(b, hk, k0 + t * kKeys);
+      tile_row[t] = r;
+      if (r < 0) report_error(a.err, TSD_DEV_ERR_BAD_PAGE, b);
+    }
+    int top = -1000;
+    if (with_tree)
+      top = tree_scan<D, kWideThreads>(a, b, wt, smem + L::off_v, L::t_bytes, kt_in, vt_in, kt_out, vt_u);
+    top = __reduce_max_sync(kFull, top);
+    if (lane == 0) s_top[warp - kWide] = top;
+  } else if (warp < 8) {
+    // Q into the tensor memory: a thread takes its packed row, whose largest element
+    // scales it, and converts the stream's half of it; and what the row sees
+    const int q = warp & 3, p = warp >> 2, row = q * 32 + lane;
+    if (q < live_warps) {
+      uint4 w[D / 8];
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i) w[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (row < rows_here) {
+        const int pr = row_base + row, tr = pr / a.g, qh = hk * a.g + pr % a.g;
+        const uint4* src =
+            (const uint4*)((const __nv_bfloat16*)a.q + (((long)b * a.R + tr) * a.Hq + qh) * D);
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) w[i] = __ldg(src + i);
+        mask = tr > 0 ? a.mask[(long)b * a.R + tr] : 0ull;
+      }
+      uint32_t qtop = 0;
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i) qtop = top_pairs(qtop, w[i]);
+      qtop = top_of(qtop);
+      const bool bad = qtop >= 0x7f800000u;
+      const int qe = row_exponent(qtop);
+      const float f = bad ? 0.f : q8_scale(268 - qe);
+      c2 = bad ? __int_as_float(0x7fffffff) : a.qscale * q8_scale(qe - 14);
+      __syncwarp();
+      asm volatile("bar.sync 2, %0;\n" ::"r"(64 * live_warps + 32) : "memory");   // (allocated)
+      const uint32_t tq = flags[0] + kColQ + p * (D / 4) + ((uint32_t)(q * 32) << 16);
+      uint4 x[D / 16];                             // the stream's half
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) {
+        x[i] = p ? w[D / 16 + i] : w[i];
+        if (bad) x[i] = make_uint4(0u, 0u, 0u, 0u);
+      }
+#pragma unroll 1
+      for (int c = 0; c < D / 16; ++c) {           // eight elements: four columns
+        const uint4 h = scale8(x[0], f);
+        tmem_st4(tq + 4 * c, __uint_as_float(h.x), __uint_as_float(h.y), __uint_as_float(h.z),
+                 __uint_as_float(h.w));
+#pragma unroll
+        for (int i = 0; i + 1 < D / 16; ++i) x[i] = x[i + 1];
+      }
+      tmem_wait_st();
+    }
+  } else if (warp == kScale) {
+    if (n_pre > 0) load_scales(a.map.row(b, hk, k0), valid_of(0));
+    if (lane == 0) {
+      for (int i = 0; i < kStages; ++i) {
+        mbar_init(bar(BAR_K_FULL + i), kWideWarps);
+        mbar_init(bar(BAR_K_EMPTY + i), 1);
+        mbar_init(bar(BAR_V_FULL + i), kWideWarps);
+        mbar_init(bar(BAR_V_EMPTY + i), 1);
+      }
+      for (int i = 0; i < kScaleRing; ++i) {
+        mbar_init(bar(BAR_F_FULL + i), 1);
+        mbar_init(bar(BAR_F_EMPTY + i), kWideWarps);
+      }
+      for (int i = 0; i < 2; ++i) {
+        mbar_init(bar(BAR_P_FULL + i), live_warps);
+        mbar_init(bar(BAR_PV_DONE + i), 1);
+        mbar_init(bar(BAR_FINAL + i), 1);
+        mbar_init(bar(BAR_S_FULL + i), 1);
+        mbar_init(bar(BAR_S_EMPTY + i), live_warps);
+      }
+      mbar_init(bar(BAR_O_DONE), 1);
+      flags[1] = 0;
+      asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
+    }
+    __syncwarp();
+  } else if (warp == kPv) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;\n" ::"r"(
+        sbase + L::off_flags));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n");
+    asm volatile("bar.arrive 2, %0;\n" ::"r"(64 * live_warps + 32) : "memory");
+  }
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem = flags[0];
+  auto tm_o = [&](int p) { return tmem + kColO + (uint32_t)(p * D); };
+  auto factors = [&](int t, int part) {
+    return smem + L::off_f + (uint32_t)((t % kScaleRing) * 2 + part) * L::f_bytes;
+  };
+
+  // --------------------------------------------------------------- scales
+  if (warp == kScale) {
+    for (int t = 0; t < n_pre; ++t) {
+      if (lane == 0) {                             // codes of the tiles to come
+        const int first = t == 0 ? 1 : t + kPrefetch - 1;
+        for (int i = first; i < t + kPrefetch && i < n_pre; ++i)
+          if (tile_row[i] >= 0) {
+            prefetch_l2(a.kc + tile_row[i] * (D / 2), (long)valid_of(i) * (D / 2));
+            prefetch_l2(a.vc + tile_row[i] * (D / 2), (long)valid_of(i) * (D / 2));
+            prefetch_l2(a.ke + tile_row[i] * (NG * 2), (long)valid_of(i) * (NG * 2));
+            prefetch_l2(a.ve + tile_row[i] * (NG * 2), (long)valid_of(i) * (NG * 2));
+          }
+      }
+      __syncwarp();
+      if (t >= kScaleRing &&
+          !__all_sync(kFull, wait_ready(bar(BAR_F_EMPTY + t % kScaleRing), (t / kScaleRing - 1) & 1))) {
+        flags[1] = 1;
+        break;
+      }
+      const int eK = ks.exponent(), eV = vs.exponent();
+      ks.store(factors(t, 0), eK, lane);
+      vs.store(factors(t, 1), eV, lane);
+      if (lane == 0) {
+        ek[t] = (int8_t)eK;
+        ev[t] = (int8_t)eV;
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(BAR_F_FULL + t % kScaleRing));
+      if (t + 1 < n_pre) load_scales(tile_row[t + 1], valid_of(t + 1));
+      if (__any_sync(kFull, flags[1] != 0)) break;
+    }
+  }
+
+  // -------------------------------------------------------------- widening
+  else if (warp >= kWide) {
+    for (int t = 0; t <= ntiles; ++t) {
+      if (t < ntiles) {                            // K of tile t
+        const int st = t % kStages;
+        uint8_t* const stage = smem + L::off_k + st * L::t_bytes;
+        bool ok = t < kStages || wait_ready(bar(BAR_K_EMPTY + st), (t / kStages - 1) & 1);
+        if (t < n_pre) ok = ok && wait_ready(bar(BAR_F_FULL + t % kScaleRing), (t / kScaleRing) & 1);
+        if (!__all_sync(kFull, ok)) {
+          flags[1] = 1;
+          break;
+        }
+        if (t < n_pre) share.widen(kreg, factors(t, 0), stage);
+        else tree_rows<D>(a, a.kt, b, hk, wt, kt_in, stage);
+        asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(BAR_K_FULL + st));
+        if (t + 1 < n_pre) load_codes(kreg, a.kc, tile_row[t + 1], valid_of(t + 1));
+      }
+      if (t > 0) {                                 // V of the tile before
+        const int u = t - 1, st = u % kStages;
+        uint8_t* const stage = smem + L::off_v + st * L::t_bytes;
+        if (u >= kStages &&
+            !__all_sync(kFull, wait_ready(bar(BAR_V_EMPTY + st), (u / kStages - 1) & 1))) {
+          flags[1] = 1;
+          break;
+        }
+        if (u < n_pre) share.widen(vreg, factors(u, 1), stage);
+        else tree_rows<D>(a, a.vt, b, hk, wt, vt_in, stage);
+        asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(bar(BAR_V_FULL + st));
+          if (u < n_pre) mbar_arrive(bar(BAR_F_EMPTY + u % kScaleRing));
+        }
+        if (u + 1 < n_pre) load_codes(vreg, a.vc, tile_row[u + 1], valid_of(u + 1));
+      }
+      if (__any_sync(kFull, flags[1] != 0)) break;
+    }
+  }
+
+  // ------------------------------------------------------------- scores
+  else if (warp == kQk) {
+    // fp16 operands are format 0, fp32 accumulator; B (K) is K-major
+    constexpr uint32_t idesc =
+        (1u << 4) | ((uint32_t)(kKeys / 2 >> 3) << 17) | ((uint32_t)(kRows >> 4) << 24);
+    const uint64_t kd0 = smem_desc(sbase + L::off_k, 16, 1024);
+    const uint32_t tq = tmem + kColQ;
+    const bool one = elect_one();
+    bool ok = true;
+    for (int t = 0; ok && t < ntiles; ++t) {
+      const int st = t % kStages;
+      ok = wait_ready(bar(BAR_K_FULL + st), (t / kStages) & 1);
+#pragma unroll
+      for (int p = 0; p < 2; ++p) {
+        ok = ok && (t == 0 || wait_ready(bar(BAR_S_EMPTY + p), (t - 1) & 1));
+        ok = __all_sync(kFull, ok);
+        if (!ok) break;
+        fence_after();
+        const uint64_t kd = kd0 + (uint64_t)(st * (L::t_bytes >> 4) + p * (kHalf / 2 >> 4));
+        if (one) {
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk)
+            mma_f16_ta(tmem + 64u * p, tq + 8 * kk, kd + (kk >> 2) * (kHalf >> 4) + 2 * (kk & 3), idesc,
+                       kk == 0 ? 0u : 1u);
+          mma_commit(bar(BAR_S_FULL + p));
+          if (p == 1) mma_commit(bar(BAR_K_EMPTY + st));
+        }
+        __syncwarp();
+      }
+    }
+    if (!ok) flags[1] = 1;
+  }
+
+  // ------------------------------------------------------------- outputs
+  else if (warp == kPv) {
+    // B (V) is N-major
+    constexpr uint32_t idesc =
+        (1u << 4) | (1u << 16) | ((uint32_t)(D >> 3) << 17) | ((uint32_t)(kRows >> 4) << 24);
+    const uint64_t vd0 = smem_desc(sbase + L::off_v, kHalf, 1024);
+    const bool one = elect_one();
+    bool ok = true;
+    for (int t = 0; ok && t < ntiles; ++t) {
+      const int st = t % kStages;
+      const uint64_t vd = vd0 + (uint64_t)(st * (L::t_bytes >> 4));
+      ok = wait_ready(bar(BAR_V_FULL + st), (t / kStages) & 1) && !flags[1];
+#pragma unroll
+      for (int p = 0; p < 2; ++p) {
+        ok = ok && wait_ready(bar(BAR_P_FULL + p), t & 1);
+        ok = __all_sync(kFull, ok);
+        if (!ok) break;
+        fence_after();
+        if (one) {
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            mma_f16_ta(tm_o(p), tmem + kColP + 32 * p + 8 * kk, vd + 128 * (4 * p + kk), idesc,
+                       t == 0 && kk == 0 ? 0u : 1u);
+          mma_commit(bar(BAR_PV_DONE + p));
+          if (p == 1) {
+            mma_commit(bar(BAR_V_EMPTY + st));
+            if (t == ntiles - 1) mma_commit(bar(BAR_O_DONE));
+          }
+        }
+        __syncwarp();
+      }
+    }
+    if (!ok) flags[1] = 1;
+  }
+
+  // -------------------------------------------------------------- softmax
+  else {
+    const int p = warp >> 2, q = warp & 3, row = q * 32 + lane;
+    const uint32_t lane_off = (uint32_t)(q * 32) << 16;
+    float m = -INFINITY, l = 0.f;
+    int top_e = kQ4MinExp;                         // the largest E of V met
+    bool failed = false;
+    if (q < live_warps) {
+      // The stream's product of the tile before: done before its P is written over
+      // or its accumulator is rescaled.
+      bool done = true;
+      auto product_done = [&](int t) -> bool {
+        return __all_sync(kFull, done || wait_ready(bar(BAR_PV_DONE + p), (t - 1) & 1));
+      };
+      // The bound is raised to X where X passes m by the headroom (or m is none), the sum
+      // and the accumulator are rescaled.
+      auto raise = [&](float X, int t) -> bool {
+        const bool need = !(X <= m + kOverflow);
+        if (__builtin_expect(!__any_sync(kFull, need), 1)) return true;
+        if (!product_done(t)) return false;
+        const float m_new = need ? fmaxf(m, X) : m;
+        const float al = m_new == m ? 1.f : m == -INFINITY ? 0.f : ex2(m - m_new);
+        m = m_new;
+        l *= al;
+        if (t == 0) return true;
+        fence_after();
+#pragma unroll 1
+        for (int c = 0; c < D; c += 16) {
+          float o[16];
+          uint32_t w[16];
+          tmem_ld8(tm_o(p) + lane_off + c, o);
+          tmem_ld8(tm_o(p) + lane_off + c + 8, o + 8);
+          tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(o[i] * al);
+          tmem_st16(tm_o(p) + lane_off + c, w);
+        }
+        tmem_wait_st();
+        return true;
+      };
+      // the scores have been read: their columns may take the next tile's
+      auto scores_read = [&] {
+        fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(BAR_S_EMPTY + p));
+      };
+
+      const int h = p;                           // a stream takes one half of every tile
+      const uint32_t ts = tmem + lane_off + 64u * h, tp = tmem + lane_off + kColP + 32u * p;
+      bool ready = false;                        // the next tile's scores
+      // (the scratch rows' tile has code of its own: the loop over the prefix stays small)
+      auto tile = [&](int t, auto tree) -> bool {
+        constexpr bool is_tree = decltype(tree)::value;
+        const int nvalid = is_tree ? a.R : valid_of(t);
+        if (t > 0) done = complete(bar(BAR_PV_DONE + p), (t - 1) & 1);
+        if (!__all_sync(kFull, ready || wait_ready(bar(BAR_S_FULL + p), t & 1))) return false;
+        fence_after();
+        const int nv = min(nvalid - 64 * h, 64);   // keys of this half
+        float v[64];
+        tmem_ld32(ts, *(float(*)[32])v);
+        tmem_ld32(ts + 32, *(float(*)[32])(v + 32));
+        int E, eK = 0;
+        if constexpr (is_tree) {
+          E = s_top[0];
+#pragma unroll
+          for (int i = 1; i < kWideWarps; ++i) E = max(E, s_top[i]);
+          E = min(max(E - 9, kQ4MinExp), kQ4MaxExp);
+        } else {
+          E = ev[t];
+          eK = ek[t];
+        }
+        top_e = max(top_e, E);
+        tmem_wait_ld();
+        scores_read();
+        // x + E = f v + E.  (f not 0, so that -inf stays -inf.)
+        float f = 1.f;
+        if constexpr (!is_tree) {
+          f = c2 * q8_scale(eK + 9 + 127);
+          f = f == 0.f ? 1.17549435e-38f : f;
+          if (__builtin_expect(nv < 64, 0)) {
+#pragma unroll
+            for (int i = 0; i < 64; ++i)
+              if (i >= nv) v[i] = -INFINITY;
+          }
+        } else {
+          // scratch rows: a factor per key, and what this row sees (key 0: the root)
+          const uint64_t vis = nv <= 0 ? 0ull
+                               : (h == 0 ? (mask << 1) | 1ull : mask >> 63) & (~0ull >> (64 - nv));
+          const uint32_t vlo = (uint32_t)vis, vhi = (uint32_t)(vis >> 32);
+#pragma unroll
+          for (int i = 0; i < 64; i += 4) {
+            const float4 k4 = *(const float4*)(kt_out + 64 * h + i);
+            const float kf[4] = {k4.x, k4.y, k4.z, k4.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const uint32_t word = i + j < 32 ? vlo : vhi;
+              const bool sees = (word >> ((i + j) & 31)) & 1u;
+              v[i + j] = sees ? v[i + j] * (c2 * kf[j]) : -INFINITY;
+            }
+          }
+        }
+        float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int i = 0; i < 64; i += 8)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) top[j] = max3f(top[j], v[i + 2 * j], v[i + 2 * j + 1]);
+        const float fE = (float)E;
+        if (!raise(fmaf(f, fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])), fE), t)) return false;
+        float off = fE + (float)kHeadroom - (m == -INFINITY ? 0.f : m);
+        if (__builtin_expect(__any_sync(kFull, fabsf(m) > 1048576.f && m != -INFINITY), 0)) {
+          // scores whose last bit is worth something: rounded as the bound was, not fused with it
+#pragma unroll
+          for (int i = 0; i < 64; ++i) v[i] = fmaf(v[i], f, fE);
+          f = 1.f;
+          off -= fE;
+        }
+        const float2 f2 = make_float2(f, f), o2 = make_float2(off, off);
+        float2 sa = make_float2(0.f, 0.f), sb = sa;
+        auto weights = [&](auto scaled) {          // scaled: a factor per value row
+#pragma unroll
+          for (int c = 0; c < 64; c += 32) {
+            uint32_t w[16];                        // (32 exponentials hide the product's wait)
+#pragma unroll
+            for (int i = 0; i < 32; i += 4) {
+              const float2 xa = __ffma2_rn(make_float2(v[c + i], v[c + i + 1]), f2, o2);
+              const float2 xb = __ffma2_rn(make_float2(v[c + i + 2], v[c + i + 3]), f2, o2);
+              float2 pa = make_float2(ex2(xa.x), ex2(xa.y));
+              float2 pb = make_float2(ex2(xb.x), ex2(xb.y));
+              sa = __fadd2_rn(sa, pa);
+              sb = __fadd2_rn(sb, pb);
+              if constexpr (decltype(scaled)::value) {
+                const int4 u = *(const int4*)(vt_u + 64 * h + c + i);
+                pa.x *= pow2i(u.x - 9 - E);
+                pa.y *= pow2i(u.y - 9 - E);
+                pb.x *= pow2i(u.z - 9 - E);
+                pb.y *= pow2i(u.w - 9 - E);
+              }
+              w[i / 2] = pack_half2(pa.x, pa.y);
+              w[i / 2 + 1] = pack_half2(pb.x, pb.y);
+            }
+            if (c == 0) {
+              if (!product_done(t)) return false;
+              fence_after();
+            }
+            tmem_st16(tp + c / 2, w);
+            if (c == 0) ready = complete(bar(BAR_S_FULL + p), (t + 1) & 1);
+          }
+          return true;
+        };
+        if (!weights(tree)) return false;
+        l = fmaf((sa.x + sa.y) + (sb.x + sb.y), pow2i(-E - kHeadroom), l);
+        tmem_wait_st();
+        fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(BAR_P_FULL + p));
+        return true;
+      };
+      for (int t = 0; t < n_pre && !failed; ++t) failed = !tile(t, std::false_type{});
+      if (with_tree && !failed) failed = !tile(n_pre, std::true_type{});
+    }
+
+    // ------------------------------------- epilogue: the two streams joined
+    const bool ok = !failed && __all_sync(kFull, wait_timed(bar(BAR_O_DONE), 0));
+    fence_after();
+    s_ml[p * kRows + row] = make_float2(m, l);
+    uint32_t stop;
+    asm volatile(
+        "{\n .reg .pred pi, po;\n setp.ne.u32 pi, %1, 0;\n"
+        " bar.red.or.pred po, 1, 256, pi;\n selp.u32 %0, 1, 0, po;\n}\n"
+        : "=r"(stop)
+        : "r"((uint32_t)(!ok || flags[1] != 0))
+        : "memory");
+    if (stop == 0 && q < live_warps) {
+      const float2 s0 = s_ml[row], s1 = s_ml[kRows + row];
+      const float top = fmaxf(s0.x, s1.x);
+      const float w0 = s0.x == -INFINITY ? (s0.y != s0.y ? s0.y : 0.f) : ex2(s0.x - top);
+      const float w1 = s1.x == -INFINITY ? (s1.y != s1.y ? s1.y : 0.f) : ex2(s1.x - top);
+      const float total = w0 * s0.y + w1 * s1.y;
+      // An output is below 2^(top_e + 3) (tree rows: 2^(top_e + 18)), or it is held over that
+      // where it goes to a split's fp16.  (top_e is the same for a warp's rows and both streams.)
+      const float unit = pow2i(top_e + 3), inv = pow2i(9 - kHeadroom) / total;
+      const float g0 = w0 * inv, g1 = w1 * inv, down = pow2i(-top_e - 3);
+      const float lse2 = top + log2f(total);
+      const int pr = row_base + min(row, rows_here - 1);
+      const int tr = pr / a.g, qh = hk * a.g + pr % a.g;
+      const long orow = ((long)b * a.R + tr) * a.Hq + qh;
+      const long prow = (((long)b * a.Hq + qh) * a.R + tr) * a.nsplit + sp;
+      const bool mine = row < rows_here;
+      if (mine && p == 0) {
+        if (nsb == 1) a.lse[orow] = lse2 * 0.69314718055994531f;
+        else a.part_meta[prow] = make_float2(lse2, unit);
+      }
+      // stream p writes the dims [p D/2, (p + 1) D/2)
+#pragma unroll 1
+      for (int c = p * (D / 2); c < (p + 1) * (D / 2); c += 32) {
+        float o0[32], o1[32];
+        tmem_ld32(tm_o(0) + lane_off + c, o0);
+        tmem_ld32(tm_o(1) + lane_off + c, o1);
+        tmem_wait_ld();
+        uint32_t w[16];
+#pragma unroll
+        for (int i = 0; i < 32; i += 2) {
+          const float x = o0[i] * g0 + o1[i] * g1, y = o0[i + 1] * g0 + o1[i + 1] * g1;
+          w[i / 2] = nsb == 1 ? pack_bf16x2(x, y) : pack_half2(x * down, y * down);
+        }
+        if (mine) {
+          uint4* dst = nsb == 1 ? (uint4*)((__nv_bfloat16*)a.out + orow * D + c)
+                                : (uint4*)((__half*)a.part_o + prow * D + c);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            dst[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+        }
+      }
+    }
+    if (!ok && lane == 0) flags[1] = 1;
+  }
+
+  // --------------------------------------------------------------- teardown
+  // Products in flight: the issuing warps wait for a commit of their own.
+  if (warp == kPv || warp == kQk) {
+    if (elect_one()) mma_commit(bar(BAR_FINAL + warp - kPv));
+    __syncwarp();
+    mbar_wait(bar(BAR_FINAL + warp - kPv), 0);
+  }
+  __syncwarp();
+  fence_before();
+  __syncthreads();
+  if (flags[1] && tid == 0) report_error(a.err, TSD_DEV_ERR_TIMEOUT, b);
+  fence_after();
+  if (warp == kPv) {
+    __syncwarp();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;\n" ::"r"(tmem));
+  }
+}
+
+template <int D>
+void launch_rows(const Q8AttnArgs& a, const Q8Plan& p, cudaStream_t st) {
+  const uint32_t smem = RowLayout<D>::total + 1024;
+  const auto kern = a.wait_cycles < kWaitCycles ? q4_rows_kernel<D, true> : q4_rows_kernel<D, false>;
+  cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  launch(kern, dim3(a.map.Hkv * p.nrg, p.nsplit, a.B), dim3(kThreads), smem, st, a);
+}
+
+}  // namespace
+
+void launch_q4_rows(const Q8AttnArgs& a, const Q8Plan& p, int D, cudaStream_t st) {
+  if (D == 128) launch_rows<128>(a, p, st);
+  else launch_rows<64>(a, p, st);
+}
+
+}  // namespace tsd

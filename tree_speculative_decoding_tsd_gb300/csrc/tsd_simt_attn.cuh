@@ -35,13 +35,7 @@ __device__ __forceinline__ void load4(const float* p, float (&x)[4]) {
   const float4 v = __ldg((const float4*)p);
   x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
 }
-__device__ __forceinline__ void load4(const __nv_bfloat16* p, float (&x)[4]) {
-  const uint2 v = __ldg((const uint2*)p);
-  x[0] = __uint_as_float(v.x << 16); x[1] = __uint_as_float(v.x & 0xffff0000u);
-  x[2] = __uint_as_float(v.y << 16); x[3] = __uint_as_float(v.y & 0xffff0000u);
-}
 __device__ __forceinline__ void store_out(float* p, float x) { *p = x; }
-__device__ __forceinline__ void store_out(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
 
 // Keys: how the prefix is read; its kDv <= kDk, kAlias: the value is the first kDv entries
 // of the key.
