@@ -22,11 +22,11 @@
 //          of the largest
 // A score's factor takes the tile's and the row's power of two in fp32.
 //
-// Roles (512 threads, 128 registers each): warps 0-3 and 4-7 softmax and epilogue; warp 8
-// issues the products with V and owns the tensor memory, warp 9 those with Q; warp 10 reads
-// the tiles' scales ahead, finds E and leaves fp16 factors in a ring; warps 11-15 widen, K a
-// tile ahead of V.  mbarriers order scales -> K -> S -> softmax -> O and V -> O; every wait
-// is bounded.
+// Roles (640 threads): warps 0-3 and 4-7 softmax and epilogue; warp 8 issues the products
+// with V and owns the tensor memory, warp 9 those with Q; warps 10 and 11 read the tiles'
+// scales of K and V ahead, find E and leave fp16 factors in a ring; warps 12-15 widen K,
+// 16-19 V.  Registers are dealt out anew at the start: the softmax needs 136.  mbarriers
+// order scales -> K -> S -> softmax -> O and V -> O; every wait is bounded.
 #include <type_traits>
 
 #include "tsd_common.cuh"
@@ -38,9 +38,18 @@
 namespace tsd {
 namespace {
 
-constexpr int kPv = 8, kQk = 9, kScale = 10, kWide = 11, kWideWarps = 5;
+constexpr int kPv = 8, kQk = 9, kScaleK = 10, kScaleV = 11, kWideK = 12, kWideV = 16;
+constexpr int kWideWarps = 4;                   // of K, and of V
 constexpr int kWideThreads = kWideWarps * 32;
-constexpr int kThreads = (kWide + kWideWarps) * 32;
+constexpr int kThreads = (kWideV + kWideWarps) * 32;
+// Registers of a thread: as launched, and then of the softmax, of warps 8-11, of those that
+// widen.
+constexpr int kLaunchRegs = 96, kSoftRegs = 136, kMidRegs = 64, kWideRegs = 72;
+static_assert(2 * kSoftRegs + kMidRegs + 2 * kWideRegs <= 5 * kLaunchRegs, "registers of the launch");
+template <int N, bool kMore> __device__ __forceinline__ void set_registers() {
+  if (kMore) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(N));
+  else asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(N));
+}
 constexpr int kStages = 3;                      // widened tiles of K, and of V
 constexpr int kScaleRing = 4;                   // tiles of factors
 constexpr int kRows = 128;
@@ -64,8 +73,8 @@ struct RowLayout {
   static constexpr uint32_t off_bar = off_ev + kMaxTiles;
   static constexpr int nbar = 32;
   static constexpr uint32_t off_flags = off_bar + 8 * nbar;            // tmem, abort
-  static constexpr uint32_t off_top = off_flags + 8;                   // int[kWideWarps]
-  static constexpr uint32_t off_req = off_top + 4 * kWideWarps;        // request, its length
+  static constexpr uint32_t off_top = off_flags + 8;                   // int[2 kWideWarps]
+  static constexpr uint32_t off_req = off_top + 8 * kWideWarps;        // request, its length
   static constexpr uint32_t total = off_req + 8;
   static_assert(total + 1024 <= 232448, "shared memory budget");
   static_assert(kTreeBytes<D> <= t_bytes && kStages > 1, "the scan's rows");
@@ -276,43 +285,42 @@ __global__ void __launch_bounds__(kThreads, 1) q4_rows_kernel(const __grid_const
   auto valid_of = [&](int t) { return min(kKeys, k1 - (k0 + t * kKeys)); };
 
   // ---------------------------------------------------------------- set-up
-  const int wt = tid - kWide * 32;
+  const int wt = tid - kWideK * 32;
+  static_assert(2 * kWideThreads >= kMaxTiles, "a thread per tile");
   using Share = Share4<D>;
-  const Share share(warp - kWide, lane);
+  const Share share(warp & 3, lane);
   uint64_t mask = 0ull;     // softmax threads: the scratch rows that the row sees,
   float c2 = 0.f;           // and the factor of its scores
-  uint4 kreg[Share::kCount], vreg[Share::kCount];
+  uint4 reg[2][Share::kCount];                     // widening: this tile and the next
   // the tile at cache row `row` (a missing page: none)
   auto load_codes = [&](uint4 (&w)[Share::kCount], const uint8_t* codes, long row, int nvalid) {
     share.load(w, codes + (row < 0 ? 0 : row) * (D / 2), row < 0 ? 0 : nvalid);
   };
-  Scales<D> ks, vs;
-  auto load_scales = [&](long row, int nvalid) {
-    const long at = (row < 0 ? 0 : row) * (NG * 2);
-    ks.load(a.ke + at, row < 0 ? 0 : nvalid, lane);
-    vs.load(a.ve + at, row < 0 ? 0 : nvalid, lane);
+  Scales<D> sc[2];          // of this tile and the next
+  const bool of_v = warp >= kWideV || warp == kScaleV;
+  const uint8_t* const my_codes = of_v ? a.vc : a.kc;
+  const uint8_t* const my_scales = of_v ? a.ve : a.ke;
+  auto load_scales = [&](Scales<D>& s, long row, int nvalid) {
+    s.load(my_scales + (row < 0 ? 0 : row) * (NG * 2), row < 0 ? 0 : nvalid, lane);
   };
 
-  if (warp >= kWide) {
-    // the first tile, the rows of the split's tiles, the scratch rows
-    if (with_tree) tree_fetch<D, kWideThreads>(a, b, hk, wt, sbase + L::off_v, L::t_bytes);
+  if (warp >= kWideK) {
+    // the first tiles, the rows of the split's tiles, the scratch rows
+    if (with_tree) tree_fetch<D, 2 * kWideThreads>(a, b, hk, wt, sbase + L::off_v, L::t_bytes);
     const long r0 = n_pre > 0 ? a.map.row(b, hk, k0) : -1;
+    const long r1 = n_pre > 1 ? a.map.row(b, hk, k0 + kKeys) : -1;
     const long rt = wt < n_pre ? a.map.row(b, hk, k0 + wt * kKeys) : -1;
-    if (n_pre > 0) {
-      load_codes(kreg, a.kc, r0, valid_of(0));
-      load_codes(vreg, a.vc, r0, valid_of(0));
-    }
-#pragma unroll 1
-    for (int t = wt; t < n_pre; t += kWideThreads) {
-      const long r = t == wt ? rt : a.map.row(b, hk, k0 + t * kKeys);
-      tile_row[t] = r;
-      if (r < 0) report_error(a.err, TSD_DEV_ERR_BAD_PAGE, b);
+    if (n_pre > 0) load_codes(reg[0], my_codes, r0, valid_of(0));
+    if (n_pre > 1) load_codes(reg[1], my_codes, r1, valid_of(1));
+    if (wt < n_pre) {
+      tile_row[wt] = rt;
+      if (rt < 0) report_error(a.err, TSD_DEV_ERR_BAD_PAGE, b);
     }
     int top = -1000;
     if (with_tree)
-      top = tree_scan<D, kWideThreads>(a, b, wt, smem + L::off_v, L::t_bytes, kt_in, vt_in, kt_out, vt_u);
+      top = tree_scan<D, 2 * kWideThreads>(a, b, wt, smem + L::off_v, L::t_bytes, kt_in, vt_in, kt_out, vt_u);
     top = __reduce_max_sync(kFull, top);
-    if (lane == 0) s_top[warp - kWide] = top;
+    if (lane == 0) s_top[warp - kWideK] = top;
   } else if (warp < 8) {
     // Q into the tensor memory: a thread takes its packed row, whose largest element
     // scales it, and converts the stream's half of it; and what the row sees
@@ -356,9 +364,12 @@ __global__ void __launch_bounds__(kThreads, 1) q4_rows_kernel(const __grid_const
       }
       tmem_wait_st();
     }
-  } else if (warp == kScale) {
-    if (n_pre > 0) load_scales(a.map.row(b, hk, k0), valid_of(0));
-    if (lane == 0) {
+  } else {
+    if (warp >= kScaleK) {
+      if (n_pre > 0) load_scales(sc[0], a.map.row(b, hk, k0), valid_of(0));
+      if (n_pre > 1) load_scales(sc[1], a.map.row(b, hk, k0 + kKeys), valid_of(1));
+    }
+    if (warp == kScaleK && lane == 0) {
       for (int i = 0; i < kStages; ++i) {
         mbar_init(bar(BAR_K_FULL + i), kWideWarps);
         mbar_init(bar(BAR_K_EMPTY + i), 1);
@@ -366,8 +377,8 @@ __global__ void __launch_bounds__(kThreads, 1) q4_rows_kernel(const __grid_const
         mbar_init(bar(BAR_V_EMPTY + i), 1);
       }
       for (int i = 0; i < kScaleRing; ++i) {
-        mbar_init(bar(BAR_F_FULL + i), 1);
-        mbar_init(bar(BAR_F_EMPTY + i), kWideWarps);
+        mbar_init(bar(BAR_F_FULL + i), 2);
+        mbar_init(bar(BAR_F_EMPTY + i), 2 * kWideWarps);
       }
       for (int i = 0; i < 2; ++i) {
         mbar_init(bar(BAR_P_FULL + i), live_warps);
@@ -381,11 +392,12 @@ __global__ void __launch_bounds__(kThreads, 1) q4_rows_kernel(const __grid_const
       asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
     }
     __syncwarp();
-  } else if (warp == kPv) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;\n" ::"r"(
-        sbase + L::off_flags));
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n");
-    asm volatile("bar.arrive 2, %0;\n" ::"r"(64 * live_warps + 32) : "memory");
+    if (warp == kPv) {
+      asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;\n" ::"r"(
+          sbase + L::off_flags));
+      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n");
+      asm volatile("bar.arrive 2, %0;\n" ::"r"(64 * live_warps + 32) : "memory");
+    }
   }
   fence_before();
   __syncthreads();
@@ -396,150 +408,143 @@ __global__ void __launch_bounds__(kThreads, 1) q4_rows_kernel(const __grid_const
     return smem + L::off_f + (uint32_t)((t % kScaleRing) * 2 + part) * L::f_bytes;
   };
 
-  // --------------------------------------------------------------- scales
-  if (warp == kScale) {
-    for (int t = 0; t < n_pre; ++t) {
-      if (lane == 0) {                             // codes of the tiles to come
-        const int first = t == 0 ? 1 : t + kPrefetch - 1;
-        for (int i = first; i < t + kPrefetch && i < n_pre; ++i)
-          if (tile_row[i] >= 0) {
-            prefetch_l2(a.kc + tile_row[i] * (D / 2), (long)valid_of(i) * (D / 2));
-            prefetch_l2(a.vc + tile_row[i] * (D / 2), (long)valid_of(i) * (D / 2));
-            prefetch_l2(a.ke + tile_row[i] * (NG * 2), (long)valid_of(i) * (NG * 2));
-            prefetch_l2(a.ve + tile_row[i] * (NG * 2), (long)valid_of(i) * (NG * 2));
-          }
-      }
-      __syncwarp();
-      if (t >= kScaleRing &&
-          !__all_sync(kFull, wait_ready(bar(BAR_F_EMPTY + t % kScaleRing), (t / kScaleRing - 1) & 1))) {
-        flags[1] = 1;
-        break;
-      }
-      const int eK = ks.exponent(), eV = vs.exponent();
-      ks.store(factors(t, 0), eK, lane);
-      vs.store(factors(t, 1), eV, lane);
-      if (lane == 0) {
-        ek[t] = (int8_t)eK;
-        ev[t] = (int8_t)eV;
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(BAR_F_FULL + t % kScaleRing));
-      if (t + 1 < n_pre) load_scales(tile_row[t + 1], valid_of(t + 1));
-      if (__any_sync(kFull, flags[1] != 0)) break;
-    }
-  }
-
   // -------------------------------------------------------------- widening
-  else if (warp >= kWide) {
-    for (int t = 0; t <= ntiles; ++t) {
-      if (t < ntiles) {                            // K of tile t
+  if (warp >= kWideK) {
+    set_registers<kWideRegs, false>();
+    const int full = of_v ? BAR_V_FULL : BAR_K_FULL, empty = of_v ? BAR_V_EMPTY : BAR_K_EMPTY;
+    uint8_t* const stages = smem + (of_v ? L::off_v : L::off_k);
+    auto one_tile = [&](int t, uint4 (&w)[Share::kCount]) -> bool {
+      const int st = t % kStages;
+      uint8_t* const stage = stages + st * L::t_bytes;
+      bool ok = t < kStages || wait_ready(bar(empty + st), (t / kStages - 1) & 1);
+      if (t < n_pre) ok = ok && wait_ready(bar(BAR_F_FULL + t % kScaleRing), (t / kScaleRing) & 1);
+      if (!__all_sync(kFull, ok)) return false;
+      if (t < n_pre) share.widen(w, factors(t, of_v), stage);
+      else tree_rows<D>(a, of_v ? a.vt : a.kt, b, hk, wt & (kWideThreads - 1), of_v ? vt_in : kt_in, stage);
+      asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(bar(full + st));
+        if (t < n_pre) mbar_arrive(bar(BAR_F_EMPTY + t % kScaleRing));
+      }
+      if (t + 2 < n_pre) load_codes(w, my_codes, tile_row[t + 2], valid_of(t + 2));
+      return !__any_sync(kFull, flags[1] != 0);
+    };
+    bool ok = true;
+#pragma unroll 1
+    for (int t = 0; ok && t < ntiles; t += 2) {
+      ok = one_tile(t, reg[0]);
+      if (ok && t + 1 < ntiles) ok = one_tile(t + 1, reg[1]);
+    }
+    if (!ok) flags[1] = 1;
+  }
+
+  else if (warp >= kPv) {
+    set_registers<kMidRegs, false>();   // (one instruction for the four warps)
+    // --------------------------------------------------------------- scales
+    if (warp == kScaleK || warp == kScaleV) {
+      volatile int8_t* const e_of = of_v ? ev : ek;
+      auto one_tile = [&](int t, Scales<D>& s) -> bool {
+        if (lane == 0) {                             // codes and scales of the tiles to come
+          for (int i = t == 0 ? 2 : t + kPrefetch - 1; i < t + kPrefetch && i < n_pre; ++i)
+            if (tile_row[i] >= 0) {
+              prefetch_l2(my_codes + tile_row[i] * (D / 2), (long)valid_of(i) * (D / 2));
+              prefetch_l2(my_scales + tile_row[i] * (NG * 2), (long)valid_of(i) * (NG * 2));
+            }
+        }
+        __syncwarp();
+        const int E = s.exponent();
+        if (t >= kScaleRing &&
+            !__all_sync(kFull, wait_ready(bar(BAR_F_EMPTY + t % kScaleRing), (t / kScaleRing - 1) & 1)))
+          return false;
+        s.store(factors(t, of_v), E, lane);
+        if (lane == 0) e_of[t] = (int8_t)E;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(BAR_F_FULL + t % kScaleRing));
+        if (t + 2 < n_pre) load_scales(s, tile_row[t + 2], valid_of(t + 2));
+        return !__any_sync(kFull, flags[1] != 0);
+      };
+      bool ok = true;
+  #pragma unroll 1
+      for (int t = 0; ok && t < n_pre; t += 2) {
+        ok = one_tile(t, sc[0]);
+        if (ok && t + 1 < n_pre) ok = one_tile(t + 1, sc[1]);
+      }
+      if (!ok) flags[1] = 1;
+    }
+
+    // ------------------------------------------------------------- scores
+    else if (warp == kQk) {
+      // fp16 operands are format 0, fp32 accumulator; B (K) is K-major
+      constexpr uint32_t idesc =
+          (1u << 4) | ((uint32_t)(kKeys / 2 >> 3) << 17) | ((uint32_t)(kRows >> 4) << 24);
+      const uint64_t kd0 = smem_desc(sbase + L::off_k, 16, 1024);
+      const uint32_t tq = tmem + kColQ;
+      const bool one = elect_one();
+      bool ok = true;
+      for (int t = 0; ok && t < ntiles; ++t) {
         const int st = t % kStages;
-        uint8_t* const stage = smem + L::off_k + st * L::t_bytes;
-        bool ok = t < kStages || wait_ready(bar(BAR_K_EMPTY + st), (t / kStages - 1) & 1);
-        if (t < n_pre) ok = ok && wait_ready(bar(BAR_F_FULL + t % kScaleRing), (t / kScaleRing) & 1);
-        if (!__all_sync(kFull, ok)) {
-          flags[1] = 1;
-          break;
-        }
-        if (t < n_pre) share.widen(kreg, factors(t, 0), stage);
-        else tree_rows<D>(a, a.kt, b, hk, wt, kt_in, stage);
-        asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(BAR_K_FULL + st));
-        if (t + 1 < n_pre) load_codes(kreg, a.kc, tile_row[t + 1], valid_of(t + 1));
-      }
-      if (t > 0) {                                 // V of the tile before
-        const int u = t - 1, st = u % kStages;
-        uint8_t* const stage = smem + L::off_v + st * L::t_bytes;
-        if (u >= kStages &&
-            !__all_sync(kFull, wait_ready(bar(BAR_V_EMPTY + st), (u / kStages - 1) & 1))) {
-          flags[1] = 1;
-          break;
-        }
-        if (u < n_pre) share.widen(vreg, factors(u, 1), stage);
-        else tree_rows<D>(a, a.vt, b, hk, wt, vt_in, stage);
-        asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(bar(BAR_V_FULL + st));
-          if (u < n_pre) mbar_arrive(bar(BAR_F_EMPTY + u % kScaleRing));
-        }
-        if (u + 1 < n_pre) load_codes(vreg, a.vc, tile_row[u + 1], valid_of(u + 1));
-      }
-      if (__any_sync(kFull, flags[1] != 0)) break;
-    }
-  }
-
-  // ------------------------------------------------------------- scores
-  else if (warp == kQk) {
-    // fp16 operands are format 0, fp32 accumulator; B (K) is K-major
-    constexpr uint32_t idesc =
-        (1u << 4) | ((uint32_t)(kKeys / 2 >> 3) << 17) | ((uint32_t)(kRows >> 4) << 24);
-    const uint64_t kd0 = smem_desc(sbase + L::off_k, 16, 1024);
-    const uint32_t tq = tmem + kColQ;
-    const bool one = elect_one();
-    bool ok = true;
-    for (int t = 0; ok && t < ntiles; ++t) {
-      const int st = t % kStages;
-      ok = wait_ready(bar(BAR_K_FULL + st), (t / kStages) & 1);
-#pragma unroll
-      for (int p = 0; p < 2; ++p) {
-        ok = ok && (t == 0 || wait_ready(bar(BAR_S_EMPTY + p), (t - 1) & 1));
-        ok = __all_sync(kFull, ok);
-        if (!ok) break;
-        fence_after();
-        const uint64_t kd = kd0 + (uint64_t)(st * (L::t_bytes >> 4) + p * (kHalf / 2 >> 4));
-        if (one) {
-#pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk)
-            mma_f16_ta(tmem + 64u * p, tq + 8 * kk, kd + (kk >> 2) * (kHalf >> 4) + 2 * (kk & 3), idesc,
-                       kk == 0 ? 0u : 1u);
-          mma_commit(bar(BAR_S_FULL + p));
-          if (p == 1) mma_commit(bar(BAR_K_EMPTY + st));
-        }
-        __syncwarp();
-      }
-    }
-    if (!ok) flags[1] = 1;
-  }
-
-  // ------------------------------------------------------------- outputs
-  else if (warp == kPv) {
-    // B (V) is N-major
-    constexpr uint32_t idesc =
-        (1u << 4) | (1u << 16) | ((uint32_t)(D >> 3) << 17) | ((uint32_t)(kRows >> 4) << 24);
-    const uint64_t vd0 = smem_desc(sbase + L::off_v, kHalf, 1024);
-    const bool one = elect_one();
-    bool ok = true;
-    for (int t = 0; ok && t < ntiles; ++t) {
-      const int st = t % kStages;
-      const uint64_t vd = vd0 + (uint64_t)(st * (L::t_bytes >> 4));
-      ok = wait_ready(bar(BAR_V_FULL + st), (t / kStages) & 1) && !flags[1];
-#pragma unroll
-      for (int p = 0; p < 2; ++p) {
-        ok = ok && wait_ready(bar(BAR_P_FULL + p), t & 1);
-        ok = __all_sync(kFull, ok);
-        if (!ok) break;
-        fence_after();
-        if (one) {
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            mma_f16_ta(tm_o(p), tmem + kColP + 32 * p + 8 * kk, vd + 128 * (4 * p + kk), idesc,
-                       t == 0 && kk == 0 ? 0u : 1u);
-          mma_commit(bar(BAR_PV_DONE + p));
-          if (p == 1) {
-            mma_commit(bar(BAR_V_EMPTY + st));
-            if (t == ntiles - 1) mma_commit(bar(BAR_O_DONE));
+        ok = wait_ready(bar(BAR_K_FULL + st), (t / kStages) & 1);
+  #pragma unroll
+        for (int p = 0; p < 2; ++p) {
+          ok = ok && (t == 0 || wait_ready(bar(BAR_S_EMPTY + p), (t - 1) & 1));
+          ok = __all_sync(kFull, ok);
+          if (!ok) break;
+          fence_after();
+          const uint64_t kd = kd0 + (uint64_t)(st * (L::t_bytes >> 4) + p * (kHalf / 2 >> 4));
+          if (one) {
+  #pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk)
+              mma_f16_ta(tmem + 64u * p, tq + 8 * kk, kd + (kk >> 2) * (kHalf >> 4) + 2 * (kk & 3), idesc,
+                         kk == 0 ? 0u : 1u);
+            mma_commit(bar(BAR_S_FULL + p));
+            if (p == 1) mma_commit(bar(BAR_K_EMPTY + st));
           }
+          __syncwarp();
         }
-        __syncwarp();
       }
+      if (!ok) flags[1] = 1;
     }
-    if (!ok) flags[1] = 1;
+
+    // ------------------------------------------------------------- outputs
+    else {
+      // B (V) is N-major
+      constexpr uint32_t idesc =
+          (1u << 4) | (1u << 16) | ((uint32_t)(D >> 3) << 17) | ((uint32_t)(kRows >> 4) << 24);
+      const uint64_t vd0 = smem_desc(sbase + L::off_v, kHalf, 1024);
+      const bool one = elect_one();
+      bool ok = true;
+      for (int t = 0; ok && t < ntiles; ++t) {
+        const int st = t % kStages;
+        const uint64_t vd = vd0 + (uint64_t)(st * (L::t_bytes >> 4));
+        ok = wait_ready(bar(BAR_V_FULL + st), (t / kStages) & 1) && !flags[1];
+  #pragma unroll
+        for (int p = 0; p < 2; ++p) {
+          ok = ok && wait_ready(bar(BAR_P_FULL + p), t & 1);
+          ok = __all_sync(kFull, ok);
+          if (!ok) break;
+          fence_after();
+          if (one) {
+  #pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              mma_f16_ta(tm_o(p), tmem + kColP + 32 * p + 8 * kk, vd + 128 * (4 * p + kk), idesc,
+                         t == 0 && kk == 0 ? 0u : 1u);
+            mma_commit(bar(BAR_PV_DONE + p));
+            if (p == 1) {
+              mma_commit(bar(BAR_V_EMPTY + st));
+              if (t == ntiles - 1) mma_commit(bar(BAR_O_DONE));
+            }
+          }
+          __syncwarp();
+        }
+      }
+      if (!ok) flags[1] = 1;
+    }
   }
 
   // -------------------------------------------------------------- softmax
   else {
+    set_registers<kSoftRegs, true>();
     const int p = warp >> 2, q = warp & 3, row = q * 32 + lane;
     const uint32_t lane_off = (uint32_t)(q * 32) << 16;
     float m = -INFINITY, l = 0.f;
@@ -603,7 +608,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_rows_kernel(const __grid_const
         if constexpr (is_tree) {
           E = s_top[0];
 #pragma unroll
-          for (int i = 1; i < kWideWarps; ++i) E = max(E, s_top[i]);
+          for (int i = 1; i < 2 * kWideWarps; ++i) E = max(E, s_top[i]);
           E = min(max(E - 9, kQ4MinExp), kQ4MaxExp);
         } else {
           E = ev[t];
