@@ -40,6 +40,7 @@ namespace {
 
 constexpr int kPv = 8, kQk = 9, kScaleK = 10, kScaleV = 11, kWideK = 12, kWideV = 16;
 constexpr int kWideWarps = 4;                   // of K, and of V
+constexpr int kPair = 2;                        // of them work on one tile, the others on the next
 constexpr int kWideThreads = kWideWarps * 32;
 constexpr int kThreads = (kWideV + kWideWarps) * 32;
 // Registers of a thread: as launched, and then of the softmax, of warps 8-11, of those that
@@ -129,14 +130,14 @@ __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
 }
 
 // A widening warp's share of a tile: 16-byte chunks (the 32 codes of a group) of eight (D =
-// 128) or sixteen rows at a time, every kWideWarps-th such block.  Eight lanes that store
+// 128) or sixteen rows at a time, every kPair-th such block.  Eight lanes that store
 // together hold two groups of a half row and four rows: their 16-byte units, permuted by
 // the swizzle, fall on eight different columns.
 template <int D>
 struct Share4 {
   static constexpr int NG = D / kQ4Group;
   static constexpr int kBlockRows = 32 / NG, kBlocks = kKeys / kBlockRows;
-  static constexpr int kCount = (kBlocks + kWideWarps - 1) / kWideWarps;
+  static constexpr int kCount = kBlocks / kPair;
   int row, grp, first;                             // within a block; the warp's first block
   uint32_t dst;                                    // the chunk's place in a stage, but for the units
   __device__ __forceinline__ Share4(int warp, int lane) {
@@ -150,7 +151,7 @@ struct Share4 {
   __device__ __forceinline__ void load(uint4 (&w)[kCount], const uint8_t* src, int nvalid) const {
 #pragma unroll
     for (int i = 0; i < kCount; ++i) {
-      const int r = (first + i * kWideWarps) * kBlockRows + row;
+      const int r = (first + i * kPair) * kBlockRows + row;
       w[i] = make_uint4(0u, 0u, 0u, 0u);
       if (r < nvalid) w[i] = ld_stream(src + (long)r * (D / 2) + grp * 16);
     }
@@ -160,8 +161,7 @@ struct Share4 {
                                         uint8_t* stage) const {
 #pragma unroll
     for (int i = 0; i < kCount; ++i) {
-      const int blk = first + i * kWideWarps;
-      if (blk >= kBlocks) break;                   // (a short last round)
+      const int blk = first + i * kPair;
       const int r = blk * kBlockRows + row;
       const uint32_t f = *(const uint16_t*)(factors + (r * NG + grp) * 2);
       const uint32_t f0 = f | f << 16, f1 = hmul2(f0, 0x2c002c00u), z = hmul2(f0, 0x80088008u);
@@ -288,10 +288,11 @@ __global__ void __launch_bounds__(kThreads, 1) q4_rows_kernel(const __grid_const
   const int wt = tid - kWideK * 32;
   static_assert(2 * kWideThreads >= kMaxTiles, "a thread per tile");
   using Share = Share4<D>;
-  const Share share(warp & 3, lane);
+  const Share share(warp & (kPair - 1), lane);
+  const int pair = (warp & 3) / kPair;             // widening: of the even tiles, or of the odd ones
   uint64_t mask = 0ull;     // softmax threads: the scratch rows that the row sees,
   float c2 = 0.f;           // and the factor of its scores
-  uint4 reg[2][Share::kCount];                     // widening: this tile and the next
+  uint4 reg[Share::kCount];                        // widening: the pair's next tile
   // the tile at cache row `row` (a missing page: none)
   auto load_codes = [&](uint4 (&w)[Share::kCount], const uint8_t* codes, long row, int nvalid) {
     share.load(w, codes + (row < 0 ? 0 : row) * (D / 2), row < 0 ? 0 : nvalid);
@@ -307,11 +308,9 @@ __global__ void __launch_bounds__(kThreads, 1) q4_rows_kernel(const __grid_const
   if (warp >= kWideK) {
     // the first tiles, the rows of the split's tiles, the scratch rows
     if (with_tree) tree_fetch<D, 2 * kWideThreads>(a, b, hk, wt, sbase + L::off_v, L::t_bytes);
-    const long r0 = n_pre > 0 ? a.map.row(b, hk, k0) : -1;
-    const long r1 = n_pre > 1 ? a.map.row(b, hk, k0 + kKeys) : -1;
+    const long r0 = pair < n_pre ? a.map.row(b, hk, k0 + pair * kKeys) : -1;
     const long rt = wt < n_pre ? a.map.row(b, hk, k0 + wt * kKeys) : -1;
-    if (n_pre > 0) load_codes(reg[0], my_codes, r0, valid_of(0));
-    if (n_pre > 1) load_codes(reg[1], my_codes, r1, valid_of(1));
+    if (pair < n_pre) load_codes(reg, my_codes, r0, valid_of(pair));
     if (wt < n_pre) {
       tile_row[wt] = rt;
       if (rt < 0) report_error(a.err, TSD_DEV_ERR_BAD_PAGE, b);
@@ -371,14 +370,14 @@ __global__ void __launch_bounds__(kThreads, 1) q4_rows_kernel(const __grid_const
     }
     if (warp == kScaleK && lane == 0) {
       for (int i = 0; i < kStages; ++i) {
-        mbar_init(bar(BAR_K_FULL + i), kWideWarps);
+        mbar_init(bar(BAR_K_FULL + i), kPair);
         mbar_init(bar(BAR_K_EMPTY + i), 1);
-        mbar_init(bar(BAR_V_FULL + i), kWideWarps);
+        mbar_init(bar(BAR_V_FULL + i), kPair);
         mbar_init(bar(BAR_V_EMPTY + i), 1);
       }
       for (int i = 0; i < kScaleRing; ++i) {
         mbar_init(bar(BAR_F_FULL + i), 2);
-        mbar_init(bar(BAR_F_EMPTY + i), 2 * kWideWarps);
+        mbar_init(bar(BAR_F_EMPTY + i), 2 * kPair);
       }
       for (int i = 0; i < 2; ++i) {
         mbar_init(bar(BAR_P_FULL + i), live_warps);
@@ -413,28 +412,36 @@ __global__ void __launch_bounds__(kThreads, 1) q4_rows_kernel(const __grid_const
     set_registers<kWideRegs, false>();
     const int full = of_v ? BAR_V_FULL : BAR_K_FULL, empty = of_v ? BAR_V_EMPTY : BAR_K_EMPTY;
     uint8_t* const stages = smem + (of_v ? L::off_v : L::off_k);
-    auto one_tile = [&](int t, uint4 (&w)[Share::kCount]) -> bool {
+    bool ok = true;
+#pragma unroll 1
+    for (int t = pair; ok && t < n_pre; t += kWideWarps / kPair) {
       const int st = t % kStages;
-      uint8_t* const stage = stages + st * L::t_bytes;
-      bool ok = t < kStages || wait_ready(bar(empty + st), (t / kStages - 1) & 1);
-      if (t < n_pre) ok = ok && wait_ready(bar(BAR_F_FULL + t % kScaleRing), (t / kScaleRing) & 1);
-      if (!__all_sync(kFull, ok)) return false;
-      if (t < n_pre) share.widen(w, factors(t, of_v), stage);
-      else tree_rows<D>(a, of_v ? a.vt : a.kt, b, hk, wt & (kWideThreads - 1), of_v ? vt_in : kt_in, stage);
+      ok = t < kStages || wait_ready(bar(empty + st), (t / kStages - 1) & 1);
+      ok = ok && wait_ready(bar(BAR_F_FULL + t % kScaleRing), (t / kScaleRing) & 1);
+      ok = __all_sync(kFull, ok);
+      if (!ok) break;
+      share.widen(reg, factors(t, of_v), stages + st * L::t_bytes);
       asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
       __syncwarp();
       if (lane == 0) {
         mbar_arrive(bar(full + st));
-        if (t < n_pre) mbar_arrive(bar(BAR_F_EMPTY + t % kScaleRing));
+        mbar_arrive(bar(BAR_F_EMPTY + t % kScaleRing));
       }
-      if (t + 2 < n_pre) load_codes(w, my_codes, tile_row[t + 2], valid_of(t + 2));
-      return !__any_sync(kFull, flags[1] != 0);
-    };
-    bool ok = true;
-#pragma unroll 1
-    for (int t = 0; ok && t < ntiles; t += 2) {
-      ok = one_tile(t, reg[0]);
-      if (ok && t + 1 < ntiles) ok = one_tile(t + 1, reg[1]);
+      const int next = t + kWideWarps / kPair;
+      if (next < n_pre) load_codes(reg, my_codes, tile_row[next], valid_of(next));
+      ok = !__any_sync(kFull, flags[1] != 0);
+    }
+    if (with_tree) {                               // by all four warps (which meet whatever failed)
+      const int st = n_pre % kStages;
+      ok = ok && (n_pre < kStages || wait_ready(bar(empty + st), (n_pre / kStages - 1) & 1));
+      ok = __all_sync(kFull, ok);
+      if (ok)
+        tree_rows<D>(a, of_v ? a.vt : a.kt, b, hk, wt & (kWideThreads - 1), of_v ? vt_in : kt_in,
+                     stages + st * L::t_bytes);
+      asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
+      if (of_v) asm volatile("bar.sync 3, %0;\n" ::"n"(kWideThreads) : "memory");
+      else asm volatile("bar.sync 4, %0;\n" ::"n"(kWideThreads) : "memory");
+      if (ok && pair == 0 && lane == 0) mbar_arrive(bar(full + st));
     }
     if (!ok) flags[1] = 1;
   }
