@@ -34,6 +34,7 @@ namespace tsd {
 namespace {
 
 constexpr int kChunk = 16;                         // keys of a chunk
+constexpr float kNone = -3.4e38f;                  // a bound before the first key
 
 template <int D, int NT, int W, int S>
 struct FewLayout {
@@ -127,39 +128,63 @@ __global__ void __launch_bounds__(W * 32, kCtas) q4_few_kernel(const __grid_cons
   const bool with_tree = sp == nsb - 1;
 
   // ------------------------------------------------------------- the ring
+  // A warp's chunks lie 128 keys apart, and a page is a multiple of that: within a page the
+  // next chunk is at a fixed distance.
+  static_assert(W * kChunk == 128, "chunks of a warp");
   const uint32_t ring = su32(smem) + warp * (S * L::stage);
   const int last = (k1 - k0 + kChunk - 1) / kChunk;   // chunks of the split
-  uint32_t missing = 0;                               // chunks of the ring without a page
-  long row_next = warp < last ? a.map.row(b, hk, k0 + warp * kChunk) : 0;
-  auto request = [&](int c, int slot) {
+  const uint8_t *kp, *vp, *sp_;                       // this lane's part of the next chunk
+  int left;                                           // steps within the page
+  auto point_at = [&](int c) {
+    long row = 0;
+    left = 0x7fffffff;
     if (c < last) {
-      const long row = row_next;
       const int pos = k0 + c * kChunk;
-      int nv = min(kChunk, k1 - pos);
-      missing &= ~(1u << slot);
-      if (row < 0) {
-        nv = 0;
-        missing |= 1u << slot;
+      row = a.map.row(b, hk, pos);
+      if (row < 0) {                                  // (the request's output is not valid)
         if (lane == 0) report_error(a.err, TSD_DEV_ERR_BAD_PAGE, b);
+        row = 0;
       }
-      if (c + W < last) row_next = a.map.row(b, hk, pos + W * kChunk);
-      const uint32_t st = ring + slot * L::stage;
-      const long r0 = row < 0 ? 0 : row;
+      if (a.map.page_size) left = (a.map.page_size - pos % a.map.page_size - 1) / (W * kChunk);
+    }
+    kp = a.kc + row * (D / 2) + lane * 16;
+    vp = a.vc + row * (D / 2) + lane * 16;
+    sp_ = (lane < 16 ? a.ke : a.ve) + (row + (lane & 15)) * (NG * 2);
+  };
+  const uint32_t to_k = unit_at<D, false>(lane / (D / 32), lane % (D / 32));
+  const uint32_t to_v = L::codes + unit_at<D, true>(lane / (D / 32), lane % (D / 32));
+  // chunk c into a slot; then on to the warp's next one
+  auto request = [&](int c, int slot) {
+    const uint32_t st = ring + slot * L::stage;
+    const int nv = k1 - (k0 + c * kChunk);
+    if (nv >= kChunk) {
+#pragma unroll
+      for (int i = 0; i < D / 64; ++i) {             // (32 units on: eight rows, the same permutation)
+        cp_async_z(st + to_k + 512 * i, kp + 512 * i, true);
+        cp_async_z(st + to_v + 512 * i, vp + 512 * i, true);
+      }
+      cp_async_small<NG * 2>(st + 2 * L::codes + lane * (NG * 2), sp_, true);
+    } else if (nv > 0) {                              // rows that are not there: zeros
 #pragma unroll
       for (int i = 0; i < D / 64; ++i) {
-        const int x = lane + 32 * i, r = x / (D / 32), u = x % (D / 32);
-        const bool there = r < nv;
-        const long at = (r0 + (there ? r : 0)) * (D / 2) + u * 16;
-        cp_async_z(st + unit_at<D, false>(r, u), a.kc + at, there);
-        cp_async_z(st + L::codes + unit_at<D, true>(r, u), a.vc + at, there);
+        const bool there = (lane + 32 * i) / (D / 32) < nv;
+        cp_async_z(st + to_k + 512 * i, there ? kp + 512 * i : a.kc, there);
+        cp_async_z(st + to_v + 512 * i, there ? vp + 512 * i : a.vc, there);
       }
-      const int r = lane & 15;
-      const bool there = r < nv;
-      const uint8_t* src = (lane < 16 ? a.ke : a.ve) + (r0 + (there ? r : 0)) * (NG * 2);
-      cp_async_small<NG * 2>(st + 2 * L::codes + lane * (NG * 2), src, there);
+      const bool there = (lane & 15) < nv;
+      cp_async_small<NG * 2>(st + 2 * L::codes + lane * (NG * 2), there ? sp_ : a.ke, there);
     }
     asm volatile("cp.async.commit_group;\n" ::: "memory");
+    if (left > 0) {
+      --left;
+      kp += W * kChunk * (D / 2);
+      vp += W * kChunk * (D / 2);
+      sp_ += W * kChunk * (NG * 2);
+    } else {
+      point_at(c + W);
+    }
   };
+  point_at(warp);
 #pragma unroll
   for (int i = 0; i < S - 1; ++i) request(warp + i * W, i);
 
@@ -291,7 +316,7 @@ __global__ void __launch_bounds__(W * 32, kCtas) q4_few_kernel(const __grid_cons
     for (int i = 0; i < NW * 4; ++i)
 #pragma unroll
       for (int x = 0; x < 4; ++x) acc[nt][i][x] = 0.f;
-    m[nt][0] = m[nt][1] = -INFINITY;
+    m[nt][0] = m[nt][1] = kNone;
     l[nt][0] = l[nt][1] = 0.f;
   }
   int slot = 0;
@@ -299,7 +324,7 @@ __global__ void __launch_bounds__(W * 32, kCtas) q4_few_kernel(const __grid_cons
   for (int c = warp; c < last; c += W) {
     asm volatile("cp.async.wait_group %0;\n" ::"n"(S - 2) : "memory");
     __syncwarp();
-    const int nv = (missing >> slot) & 1u ? 0 : min(kChunk, k1 - (k0 + c * kChunk));
+    const int nv = k1 - (k0 + c * kChunk);
     request(c + (S - 1) * W, slot == 0 ? S - 1 : slot - 1);
     const uint32_t st = ring + slot * L::stage;
     slot = slot == S - 1 ? 0 : slot + 1;
@@ -344,9 +369,12 @@ __global__ void __launch_bounds__(W * 32, kCtas) q4_few_kernel(const __grid_cons
     int E;
     {
       const uint32_t w = lds32(sv + (lane & (8 * NG - 1)) * 4);
-      const uint32_t lo = w & 0x7fffu, hi = w >> 16 & 0x7fffu;
-      const uint32_t top = max(lo < 0x7f80u ? lo : 0u, hi < 0x7f80u ? hi : 0u);
-      E = min(max((int)(__reduce_max_sync(kFull, top) >> 7) - 126, kQ4MinExp), kQ4MaxExp);
+      uint32_t top = __reduce_max_sync(kFull, max(w & 0x7fffu, w >> 16 & 0x7fffu));
+      if (top >= 0x7f80u) {                        // (not the scales that are not finite)
+        const uint32_t lo = w & 0x7fffu, hi = w >> 16 & 0x7fffu;
+        top = __reduce_max_sync(kFull, max(lo < 0x7f80u ? lo : 0u, hi < 0x7f80u ? hi : 0u));
+      }
+      E = min(max((int)(top >> 7) - 126, kQ4MinExp), kQ4MaxExp);
     }
     const float fE = (float)E;
 
@@ -373,7 +401,7 @@ __global__ void __launch_bounds__(W * 32, kCtas) q4_few_kernel(const __grid_cons
 #pragma unroll
           for (int o = 4; o < 32; o <<= 1) top[x] = fmaxf(top[x], __shfl_xor_sync(kFull, top[x], o));
           const float mn = fmaxf(m[nt][x], top[x]);
-          const float al = mn == m[nt][x] ? 1.f : ex2(m[nt][x] - mn);
+          const float al = ex2(m[nt][x] - mn);
           m[nt][x] = mn;
           l[nt][x] *= al;
 #pragma unroll
@@ -383,8 +411,8 @@ __global__ void __launch_bounds__(W * 32, kCtas) q4_few_kernel(const __grid_cons
           }
         }
       }
-      const float m0 = m[nt][0] == -INFINITY ? 0.f : m[nt][0], m1 = m[nt][1] == -INFINITY ? 0.f : m[nt][1];
-      const float p0 = ex2(y[0] - m0), p1 = ex2(y[1] - m1), p2 = ex2(y[2] - m0), p3 = ex2(y[3] - m1);
+      const float p0 = ex2(y[0] - m[nt][0]), p1 = ex2(y[1] - m[nt][1]);
+      const float p2 = ex2(y[2] - m[nt][0]), p3 = ex2(y[3] - m[nt][1]);
       const float down = q8_scale(127 - E);
       l[nt][0] = fmaf(p0 + p2, down, l[nt][0]);
       l[nt][1] = fmaf(p1 + p3, down, l[nt][1]);
@@ -448,7 +476,7 @@ __global__ void __launch_bounds__(W * 32, kCtas) q4_few_kernel(const __grid_cons
 #pragma unroll
       for (int o = 4; o < 32; o <<= 1) sum += __shfl_xor_sync(kFull, sum, o);
       const int n = nt * 8 + 2 * t + x;
-      if (g == 0) s_ml[warp * NT * 8 + n] = make_float2(m[nt][x], sum);
+      if (g == 0) s_ml[warp * NT * 8 + n] = make_float2(m[nt][x] == kNone ? -INFINITY : m[nt][x], sum);
       float* const dst = s_o + (warp * NT * 8 + n) * L::pitch + 8 * NW * g;
 #pragma unroll
       for (int i = 0; i < NW * 4; ++i)

@@ -560,7 +560,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_rows_kernel(const __grid_const
     if (q < live_warps) {
       // The stream's product of the tile before: done before its P is written over
       // or its accumulator is rescaled.
-      bool done = true;
+      bool done = true, far = false;             // far: a bound whose last bit is worth something
       auto product_done = [&](int t) -> bool {
         return __all_sync(kFull, done || wait_ready(bar(BAR_PV_DONE + p), (t - 1) & 1));
       };
@@ -574,6 +574,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_rows_kernel(const __grid_const
         const float al = m_new == m ? 1.f : m == -INFINITY ? 0.f : ex2(m - m_new);
         m = m_new;
         l *= al;
+        far = __any_sync(kFull, fabsf(m) > 1048576.f && m != -INFINITY);
         if (t == 0) return true;
         fence_after();
 #pragma unroll 1
@@ -604,7 +605,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_rows_kernel(const __grid_const
       auto tile = [&](int t, auto tree) -> bool {
         constexpr bool is_tree = decltype(tree)::value;
         const int nvalid = is_tree ? a.R : valid_of(t);
-        if (t > 0) done = complete(bar(BAR_PV_DONE + p), (t - 1) & 1);
+        done = t == 0;
         if (!__all_sync(kFull, ready || wait_ready(bar(BAR_S_FULL + p), t & 1))) return false;
         fence_after();
         const int nv = min(nvalid - 64 * h, 64);   // keys of this half
@@ -659,8 +660,8 @@ __global__ void __launch_bounds__(kThreads, 1) q4_rows_kernel(const __grid_const
         const float fE = (float)E;
         if (!raise(fmaf(f, fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])), fE), t)) return false;
         float off = fE + (float)kHeadroom - (m == -INFINITY ? 0.f : m);
-        if (__builtin_expect(__any_sync(kFull, fabsf(m) > 1048576.f && m != -INFINITY), 0)) {
-          // scores whose last bit is worth something: rounded as the bound was, not fused with it
+        if (t > 0) done = complete(bar(BAR_PV_DONE + p), (t - 1) & 1);   // (looked at a while before it is needed)
+        if (__builtin_expect(far, 0)) {            // rounded as the bound was, not fused with it
 #pragma unroll
           for (int i = 0; i < 64; ++i) v[i] = fmaf(v[i], f, fE);
           f = 1.f;
