@@ -33,22 +33,50 @@
 namespace tsd {
 namespace {
 
-constexpr int kChunk = 16;                         // keys of a chunk
+constexpr int kChunk = 32;                         // keys of a chunk: two halves, a product's rows each
 constexpr float kNone = -3.4e38f;                  // a bound before the first key
+constexpr int kWarps = 8;
+constexpr int kUnit = kWarps * kChunk;             // keys of a unit of work: a chunk for each warp
+constexpr int kShareBatch = kWarps * 32;           // requests whose work is dealt out evenly
+
+// Units of a request's head: at least one, for the scratch rows.
+__device__ __forceinline__ int units_of(int P) { return max(1, (P + kUnit - 1) / kUnit); }
+
+__device__ __noinline__ unsigned share_of(unsigned long long n, unsigned long long d) {
+  return (unsigned)(n / d);                        // (a 64-bit division is 100 instructions)
+}
+
+// Where the CTAs leave the outputs of requests that more than one has worked on: two
+// places per CTA (its first request, its last one).
+struct Shares {
+  float* out;               // [2 CTAs][M][D]
+  float2* meta;             // [2 CTAs][M] (log2-sum-exp, 1)
+  int2* place;              // [B][Hkv]: the first place, and how many: the others are the first
+                            // ones of the CTAs that follow
+  int least;                // units that a CTA gets at least, where all SMs have one
+};
 
 template <int D, int NT, int W, int S>
 struct FewLayout {
   static constexpr int NG = D / kQ4Group;
-  static constexpr uint32_t codes = kChunk * D / 2, scales = kChunk * NG * 2;
+  // A row's codes, padded so that neither way of reading (K: a unit of eight rows; V: a run
+  // of words of four even or four odd rows) meets a bank twice.
+  static constexpr uint32_t row = D / 2 + 16;
+  static constexpr uint32_t codes = kChunk * row, scales = kChunk * NG * 2;
   static constexpr uint32_t stage = 2 * codes + 2 * scales;
   static constexpr uint32_t ring = W * S * stage;
   static constexpr int pitch = D + 4;              // floats of a row in the joint
   static constexpr uint32_t joint = W * NT * 8 * pitch * 4;
   static constexpr uint32_t off_tree = ring > joint ? ring : joint;     // float [8 NT][D]
   static constexpr uint32_t off_ml = off_tree + NT * 8 * D * 4;         // float2 [W + 1][8 NT]
-  static constexpr uint32_t off_req = off_ml + (W + 1) * NT * 8 * 8;
-  static constexpr uint32_t total = off_req + 16;
-  static_assert(stage % 128 == 0, "whole lines");
+  static constexpr uint32_t off_q = off_ml + (W + 1) * NT * 8 * 8;      // uint4 [NT][NG][32]: B operands
+  static constexpr uint32_t off_qs = off_q + NT * NG * 32 * 16;         // float4 [NT][NG][4]: their start
+  static constexpr uint32_t off_c2 = off_qs + NT * NG * 4 * 16;         // float [8 NT]: factor of the scores
+  static constexpr uint32_t off_seg = off_c2 + NT * 8 * 4;              // int: request; a huge row
+  static constexpr uint32_t off_pre = off_seg + 16;                     // int [kShareBatch + 1]: units before
+  static constexpr uint32_t off_len = off_pre + (kShareBatch + 4) * 4;  // int [kShareBatch]: lengths
+  static constexpr uint32_t total = off_len + kShareBatch * 4;
+  static_assert(stage % 16 == 0, "whole units");
 };
 
 __device__ __forceinline__ void cp_async_z(uint32_t dst, const void* src, bool there) {
@@ -60,25 +88,9 @@ __device__ __forceinline__ void cp_async_small(uint32_t dst, const void* src, bo
   asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;\n" ::"r"(dst), "l"(src), "n"(N),
                "r"(there ? N : 0) : "memory");
 }
-__device__ __forceinline__ uint32_t lds32(uint32_t at) {
-  uint32_t v;
-  asm volatile("ld.shared.u32 %0, [%1];\n" : "=r"(v) : "r"(at));
-  return v;
-}
-__device__ __forceinline__ uint2 lds64(uint32_t at) {
-  uint2 v;
-  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];\n" : "=r"(v.x), "=r"(v.y) : "r"(at));
-  return v;
-}
-__device__ __forceinline__ uint32_t lds16(uint32_t at) {
-  uint16_t v;
-  asm volatile("ld.shared.u16 %0, [%1];\n" : "=h"(v) : "r"(at));
-  return v;
-}
 __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                           uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
       "{%0,%1,%2,%3};\n"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
@@ -100,40 +112,93 @@ __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
   return d;
 }
 
-// Where 16-byte unit u of row r of a chunk's codes lies: rows side by side, two (D = 128) or
-// four to a line of 128 bytes, the units of a line permuted so that neither way of
-// reading (K: a unit of eight rows; V: a run of units of four even or four odd rows) meets
-// a bank twice.
-template <int D, bool kV>
-__device__ __forceinline__ uint32_t unit_at(int r, int u) {
-  constexpr int U = D / 32;                        // units of a row
-  const int line = r * U >> 3, at = r * U + u & 7;
-  const int x = line & (U - 1);
-  return (uint32_t)(line * 128 + ((at ^ (kV ? 2 * x : x)) << 4));
-}
-
 template <int D, int NT, int W, int S, int kCtas>
-__global__ void __launch_bounds__(W * 32, kCtas) q4_few_kernel(const __grid_constant__ Q8AttnArgs a) {
+__global__ void __launch_bounds__(W * 32, kCtas)
+q4_few_kernel(const __grid_constant__ Q8AttnArgs a, const __grid_constant__ Shares sh) {
   using L = FewLayout<D, NT, W, S>;
   constexpr int NG = L::NG, NW = D / 64;           // groups; words of V per lane and key
   extern __shared__ __align__(128) uint8_t smem[];
   grid_dependency_sync();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
-  const int hk = blockIdx.x, sp = blockIdx.y;
-  int P;
-  const int b = request_at(a, blockIdx.z, P, (volatile int*)(smem + L::off_req));
-  const int nsb = q8_splits(a, P);
-  if (sp >= nsb) return;
-  const int k0 = min(sp * a.split_len, P), k1 = min(P, k0 + a.split_len);
-  const bool with_tree = sp == nsb - 1;
+  const int Hkv = a.map.Hkv;
+
+  // This CTA's share: units u .. u_end of all heads' units, in the order of requests and heads.
+  int* const s_pre = (int*)(smem + L::off_pre);
+  int* const s_len = (int*)(smem + L::off_len);
+  int* const s_seg = (int*)(smem + L::off_seg);
+  const bool shared = a.B <= kShareBatch;
+  unsigned u = blockIdx.x, u_end = u + 1, total = 0, ctas = 0;
+  if (shared) {
+    const int P = tid < a.B ? min(max(a.plen[tid], 0), a.map.cap) : 0;
+    int sum = tid < a.B ? units_of(P) : 0;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(kFull, sum, o);
+      if (lane >= o) sum += x;
+    }
+    if (lane == 31) s_len[warp] = sum;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < W - 1; ++w)
+      if (w < warp) sum += s_len[w];
+    __syncthreads();
+    s_len[tid] = P;
+    s_pre[tid + 1] = sum;
+    if (tid == 0) s_pre[0] = 0;
+    __syncthreads();
+    total = (unsigned)s_pre[a.B] * Hkv;
+    ctas = min(gridDim.x, max(total / sh.least, min(total, 152u)));
+    if (blockIdx.x >= ctas) return;
+    u = share_of((unsigned long long)blockIdx.x * total, ctas);
+    u_end = share_of((unsigned long long)(blockIdx.x + 1) * total, ctas);
+  }
+  const unsigned u0 = u;
+
+#pragma unroll 1
+  for (; u < u_end;) {
+  int b, hk, P, k0, k1, nparts = 1, place = 0;
+  bool with_tree = true;
+  if (tid == 0) s_seg[1] = 0;
+  if (shared) {
+    if (tid < a.B && (unsigned)s_pre[tid] * Hkv <= u && u < (unsigned)s_pre[tid + 1] * Hkv) s_seg[0] = tid;
+    __syncthreads();
+    b = s_seg[0];
+    P = s_len[b];
+    const unsigned tl = s_pre[b + 1] - s_pre[b], r = u - (unsigned)s_pre[b] * Hkv;
+    hk = r / tl;
+    const unsigned first = (unsigned)s_pre[b] * Hkv + hk * tl, end = first + tl;
+    const unsigned stop = min(u_end, end), tile = r - hk * tl;
+    k0 = min((int)tile * kUnit, P);
+    k1 = min(P, k0 + (int)(stop - u) * kUnit);
+    with_tree = stop == end;
+    if (u != first || stop != end) {               // others work on this head, too
+      const unsigned i0 = share_of((unsigned long long)(first + 1) * ctas - 1, total);
+      const unsigned i1 = share_of((unsigned long long)end * ctas - 1, total);
+      nparts = i1 - i0 + 1;
+      place = 2 * blockIdx.x + (u != u0);
+      if (tid == 0)
+        sh.place[b * Hkv + hk] =
+            make_int2(2 * i0 + (share_of((unsigned long long)i0 * total, ctas) != first), nparts);
+    } else if (tid == 0) {
+      sh.place[b * Hkv + hk] = make_int2(0, 1);
+    }
+    u = stop;
+  } else {
+    b = u / Hkv;
+    hk = u % Hkv;
+    P = min(max(a.plen[b], 0), a.map.cap);
+    k0 = 0;
+    k1 = P;
+    u = u_end;
+    __syncthreads();
+  }
 
   // ------------------------------------------------------------- the ring
-  // A warp's chunks lie 128 keys apart, and a page is a multiple of that: within a page the
-  // next chunk is at a fixed distance.
-  static_assert(W * kChunk == 128, "chunks of a warp");
+  // A warp's chunks lie W * kChunk keys apart: within a page the next one is at a fixed
+  // distance.
   const uint32_t ring = su32(smem) + warp * (S * L::stage);
   const int last = (k1 - k0 + kChunk - 1) / kChunk;   // chunks of the split
-  const uint8_t *kp, *vp, *sp_;                       // this lane's part of the next chunk
+  const uint8_t *kp, *vp, *ksp, *vsp;                 // this lane's part of the next chunk
   int left;                                           // steps within the page
   auto point_at = [&](int c) {
     long row = 0;
@@ -149,37 +214,40 @@ __global__ void __launch_bounds__(W * 32, kCtas) q4_few_kernel(const __grid_cons
     }
     kp = a.kc + row * (D / 2) + lane * 16;
     vp = a.vc + row * (D / 2) + lane * 16;
-    sp_ = (lane < 16 ? a.ke : a.ve) + (row + (lane & 15)) * (NG * 2);
+    ksp = a.ke + (row + lane) * (NG * 2);
+    vsp = a.ve + (row + lane) * (NG * 2);
   };
-  const uint32_t to_k = unit_at<D, false>(lane / (D / 32), lane % (D / 32));
-  const uint32_t to_v = L::codes + unit_at<D, true>(lane / (D / 32), lane % (D / 32));
+  constexpr int U = D / 32, kRowStep = 32 / U;        // units of a row, rows of a warp's copy
+  const uint32_t to = (uint32_t)(lane / U) * L::row + (lane % U) * 16;
   // chunk c into a slot; then on to the warp's next one
   auto request = [&](int c, int slot) {
     const uint32_t st = ring + slot * L::stage;
     const int nv = k1 - (k0 + c * kChunk);
     if (nv >= kChunk) {
 #pragma unroll
-      for (int i = 0; i < D / 64; ++i) {             // (32 units on: eight rows, the same permutation)
-        cp_async_z(st + to_k + 512 * i, kp + 512 * i, true);
-        cp_async_z(st + to_v + 512 * i, vp + 512 * i, true);
+      for (int i = 0; i < U; ++i) {
+        cp_async_z(st + to + i * kRowStep * L::row, kp + 512 * i, true);
+        cp_async_z(st + L::codes + to + i * kRowStep * L::row, vp + 512 * i, true);
       }
-      cp_async_small<NG * 2>(st + 2 * L::codes + lane * (NG * 2), sp_, true);
+      cp_async_small<NG * 2>(st + 2 * L::codes + lane * (NG * 2), ksp, true);
+      cp_async_small<NG * 2>(st + 2 * L::codes + L::scales + lane * (NG * 2), vsp, true);
     } else if (nv > 0) {                              // rows that are not there: zeros
-#pragma unroll
-      for (int i = 0; i < D / 64; ++i) {
-        const bool there = (lane + 32 * i) / (D / 32) < nv;
-        cp_async_z(st + to_k + 512 * i, there ? kp + 512 * i : a.kc, there);
-        cp_async_z(st + to_v + 512 * i, there ? vp + 512 * i : a.vc, there);
+#pragma unroll 1
+      for (int i = 0; i < U; ++i) {
+        const bool there = lane / U + i * kRowStep < nv;
+        cp_async_z(st + to + i * kRowStep * L::row, there ? kp + 512 * i : a.kc, there);
+        cp_async_z(st + L::codes + to + i * kRowStep * L::row, there ? vp + 512 * i : a.vc, there);
       }
-      const bool there = (lane & 15) < nv;
-      cp_async_small<NG * 2>(st + 2 * L::codes + lane * (NG * 2), there ? sp_ : a.ke, there);
+      cp_async_small<NG * 2>(st + 2 * L::codes + lane * (NG * 2), lane < nv ? ksp : a.ke, lane < nv);
+      cp_async_small<NG * 2>(st + 2 * L::codes + L::scales + lane * (NG * 2), lane < nv ? vsp : a.ve, lane < nv);
     }
     asm volatile("cp.async.commit_group;\n" ::: "memory");
     if (left > 0) {
       --left;
       kp += W * kChunk * (D / 2);
       vp += W * kChunk * (D / 2);
-      sp_ += W * kChunk * (NG * 2);
+      ksp += W * kChunk * (NG * 2);
+      vsp += W * kChunk * (NG * 2);
     } else {
       point_at(c + W);
     }
@@ -189,25 +257,24 @@ __global__ void __launch_bounds__(W * 32, kCtas) q4_few_kernel(const __grid_cons
   for (int i = 0; i < S - 1; ++i) request(warp + i * W, i);
 
   // ------------------------------------------------------ Q as the B operand
-  // lane (g, t): column g, and of each group j the dims of word 4 j + t
-  uint32_t qb[NT][NG][4];
-  float qs[NT][NG][2], c2[NT][2];
-  bool huge = false;                               // a row from 2^117 on (its factor in two steps)
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-    const int n = nt * 8 + g;
-    uint4 w[NG];
+  // lane (g, t): column g, and of each group j the dims of word 4 j + t.  In shared memory,
+  // for all warps, and with it what each group's product begins with: -8 * 2^-24 sum(q) of
+  // columns 2 t and 2 t + 1, for both halves of the rows.
+  uint4* const s_q = (uint4*)(smem + L::off_q);
+  float* const s_qs = (float*)(smem + L::off_qs);
+  float* const s_c2 = (float*)(smem + L::off_c2);
+  int* const s_huge = s_seg + 1;                     // a row from 2^117 on: its factor in two steps
+  static_assert(NT * NG <= W, "a warp per group");
+  if (warp < NT * NG) {
+    const int nt = warp / NG, j = warp % NG, n = nt * 8 + g;
+    uint4 w = make_uint4(0u, 0u, 0u, 0u);
     uint32_t top = 0;
-#pragma unroll
-    for (int j = 0; j < NG; ++j) w[j] = make_uint4(0u, 0u, 0u, 0u);
     if (n < a.M) {
       const int tr = n / a.g, qh = hk * a.g + n % a.g;
-      const uint4* src = (const uint4*)((const __nv_bfloat16*)a.q + (((long)b * a.R + tr) * a.Hq + qh) * D);
+      const uint4* src = (const uint4*)((const __nv_bfloat16*)a.q + (((long)b * a.R + tr) * a.Hq + qh) * D) + t;
+      w = __ldg(src + 4 * j);
 #pragma unroll
-      for (int j = 0; j < NG; ++j) {
-        w[j] = __ldg(src + 4 * j + t);
-        top = top_pairs(top, w[j]);
-      }
+      for (int i = 0; i < NG; ++i) top = top_pairs(top, __ldg(src + 4 * i));
     }
     top = top_of(top);
 #pragma unroll
@@ -216,36 +283,27 @@ __global__ void __launch_bounds__(W * 32, kCtas) q4_few_kernel(const __grid_cons
     const bool bad = top >= 0x7f800000u;
     const int e = row_exponent(top);
     const float f = bad ? 0.f : q8_scale(268 - e);
-    huge = huge || __any_sync(kFull, !bad && e >= 244);
-    // 2^(e - 127) of the row, over 2^14; 2^24 of the codes
-    const float c = bad ? __int_as_float(0x7fffffff) : a.qscale * q8_scale(e);
+    if (!bad && e >= 244) *s_huge = 1;
+    // 2^(e - 127) of the row, over 2^14; 2^24 of the codes: 2^10 to come
+    if (t == 0 && j == 0) s_c2[n] = bad ? __int_as_float(0x7fffffff) : a.qscale * q8_scale(e);
+    const uint32_t in[4] = {w.x, w.y, w.z, w.w};
+    uint32_t q[4];
+    float sum = 0.f;
 #pragma unroll
-    for (int j = 0; j < NG; ++j) {
-      const uint32_t in[4] = {w[j].x, w[j].y, w[j].z, w[j].w};
-      float sum = 0.f;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float h = i & 1 ? f * 0.0625f : f;
-        const uint32_t bits = bad ? 0u : in[i];
-        qb[nt][j][i] = pack_half2(__uint_as_float(bits << 16) * h, __uint_as_float(bits & 0xffff0000u) * h);
-        const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&qb[nt][j][i]));
-        sum = fmaf(i & 1 ? 16.f : 1.f, y.x + y.y, sum);
-      }
-#pragma unroll
-      for (int o = 1; o < 4; o <<= 1) sum += __shfl_xor_sync(kFull, sum, o);
-      sum *= -8.f * 5.9604644775390625e-08f;       // -8 * 2^-24
-      qs[nt][j][0] = __shfl_sync(kFull, sum, 8 * t);
-      qs[nt][j][1] = __shfl_sync(kFull, sum, 8 * t + 4);
+    for (int i = 0; i < 4; ++i) {
+      const float h = i & 1 ? f * 0.0625f : f;
+      const uint32_t bits = bad ? 0u : in[i];
+      q[i] = pack_half2(__uint_as_float(bits << 16) * h, __uint_as_float(bits & 0xffff0000u) * h);
+      const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&q[i]));
+      sum = fmaf(i & 1 ? 16.f : 1.f, y.x + y.y, sum);
     }
-    c2[nt][0] = __shfl_sync(kFull, c, 8 * t);
-    c2[nt][1] = __shfl_sync(kFull, c, 8 * t + 4);
+    s_q[warp * 32 + lane] = make_uint4(q[0], q[1], q[2], q[3]);
+#pragma unroll
+    for (int o = 1; o < 4; o <<= 1) sum += __shfl_xor_sync(kFull, sum, o);
+    sum *= -8.f * 5.9604644775390625e-08f;
+    // column g: of lanes t = g / 2, its place there g % 2, twice
+    if (t < 2) s_qs[(warp * 4 + (g >> 1)) * 4 + (g & 1) + 2 * t] = sum;
   }
-
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-    for (int x = 0; x < 2; ++x)
-      if (!huge) c2[nt][x] *= 1024.f;
 
   // --------------------------------------------------------- scratch rows
   float* const tree_o = (float*)(smem + L::off_tree);
@@ -253,7 +311,7 @@ __global__ void __launch_bounds__(W * 32, kCtas) q4_few_kernel(const __grid_cons
   if (with_tree) {
     constexpr int E = D / 32;                      // dims of a lane
 #pragma unroll 1
-    for (int n = warp; n < a.M; n += W) {
+    for (int n = W - 1 - warp; n < a.M; n += W) {   // (the warps that have no group of Q first)
       const int tr = n / a.g, qh = hk * a.g + n % a.g;
       const uint64_t vis = (tr > 0 ? a.mask[(long)b * a.R + tr] << 1 : 0ull) | 1ull;
       auto row4 = [&](const void* base, long row, float (&x)[E]) {
@@ -309,7 +367,9 @@ __global__ void __launch_bounds__(W * 32, kCtas) q4_few_kernel(const __grid_cons
   }
 
   // ------------------------------------------------------------ the chunks
-  float acc[NT][NW * 4][4], m[NT][2], l[NT][2];
+  __syncthreads();
+  const bool huge = *s_huge != 0;
+  float acc[NT][NW * 4][4], m[NT][2], l[NT][2], c2[NT][2];
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -318,7 +378,10 @@ __global__ void __launch_bounds__(W * 32, kCtas) q4_few_kernel(const __grid_cons
       for (int x = 0; x < 4; ++x) acc[nt][i][x] = 0.f;
     m[nt][0] = m[nt][1] = kNone;
     l[nt][0] = l[nt][1] = 0.f;
+#pragma unroll
+    for (int x = 0; x < 2; ++x) c2[nt][x] = s_c2[nt * 8 + 2 * t + x] * (huge ? 1.f : 1024.f);
   }
+  const uint8_t* const mine = smem + warp * (S * L::stage);
   int slot = 0;
 #pragma unroll 1
   for (int c = warp; c < last; c += W) {
@@ -326,76 +389,105 @@ __global__ void __launch_bounds__(W * 32, kCtas) q4_few_kernel(const __grid_cons
     __syncwarp();
     const int nv = k1 - (k0 + c * kChunk);
     request(c + (S - 1) * W, slot == 0 ? S - 1 : slot - 1);
-    const uint32_t st = ring + slot * L::stage;
+    const uint8_t* const st = mine + slot * L::stage;
     slot = slot == S - 1 ? 0 : slot + 1;
 
-    // scores of keys g and g + 8, columns 2 t and 2 t + 1
-    float s[NT][4];
+    // scores of keys g and g + 8 of each half, columns 2 t and 2 t + 1
+    float s[NT][2][4];
+    const uint8_t* const kl = st + g * L::row + 4 * t;
+    const uint8_t* const sl = st + 2 * L::codes + g * (NG * 2);
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+    for (int h = 0; h < 2; ++h) {
+      uint32_t ks[2][NG / 2];
 #pragma unroll
-      for (int x = 0; x < 4; ++x) s[nt][x] = 0.f;
-    uint32_t ks[2][NG / 2];
-    if constexpr (NG == 4) {
-      const uint2 x = lds64(st + 2 * L::codes + g * 8), y = lds64(st + 2 * L::codes + g * 8 + 64);
-      ks[0][0] = x.x; ks[0][1] = x.y; ks[1][0] = y.x; ks[1][1] = y.y;
-    } else {
-      ks[0][0] = lds32(st + 2 * L::codes + g * 4);
-      ks[1][0] = lds32(st + 2 * L::codes + g * 4 + 32);
-    }
+      for (int x = 0; x < 2; ++x) {
+        const uint8_t* const p = sl + (16 * h + 8 * x) * (NG * 2);
+        if constexpr (NG == 4) {
+          const uint2 y = *(const uint2*)p;
+          ks[x][0] = y.x;
+          ks[x][NG / 2 - 1] = y.y;
+        } else {
+          ks[x][0] = *(const uint32_t*)p;
+        }
+      }
 #pragma unroll
-    for (int j = 0; j < NG; ++j) {
-      const uint32_t w0 = lds32(st + unit_at<D, false>(g, j) + 4 * t);
-      const uint32_t w1 = lds32(st + unit_at<D, false>(g + 8, j) + 4 * t);
-      const uint32_t h0 = w0 >> 8, h1 = w1 >> 8;
-      const float s0 = j & 1 ? __uint_as_float(ks[0][j / 2] & 0xffff0000u) : __uint_as_float(ks[0][j / 2] << 16);
-      const float s1 = j & 1 ? __uint_as_float(ks[1][j / 2] & 0xffff0000u) : __uint_as_float(ks[1][j / 2] << 16);
+      for (int j = 0; j < NG; ++j) {
+        const uint32_t w0 = *(const uint32_t*)(kl + 16 * h * L::row + 16 * j);
+        const uint32_t w1 = *(const uint32_t*)(kl + (16 * h + 8) * L::row + 16 * j);
+        const uint32_t h0 = w0 >> 8, h1 = w1 >> 8;
+        const float s0 = __uint_as_float(j & 1 ? ks[0][j / 2] & 0xffff0000u : ks[0][j / 2] << 16);
+        const float s1 = __uint_as_float(j & 1 ? ks[1][j / 2] & 0xffff0000u : ks[1][j / 2] << 16);
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        float d[4] = {qs[nt][j][0], qs[nt][j][1], qs[nt][j][0], qs[nt][j][1]};
-        mma_16816(d, w0 & 0x000f000fu, w1 & 0x000f000fu, w0 & 0x00f000f0u, w1 & 0x00f000f0u,
-                  qb[nt][j][0], qb[nt][j][1]);
-        mma_16816(d, h0 & 0x000f000fu, h1 & 0x000f000fu, h0 & 0x00f000f0u, h1 & 0x00f000f0u,
-                  qb[nt][j][2], qb[nt][j][3]);
-        s[nt][0] = fmaf(d[0], s0, s[nt][0]);
-        s[nt][1] = fmaf(d[1], s0, s[nt][1]);
-        s[nt][2] = fmaf(d[2], s1, s[nt][2]);
-        s[nt][3] = fmaf(d[3], s1, s[nt][3]);
+        for (int nt = 0; nt < NT; ++nt) {
+          const uint4 q = s_q[(nt * NG + j) * 32 + lane];
+          const float4 x = *(const float4*)(s_qs + ((nt * NG + j) * 4 + t) * 4);
+          float d[4] = {x.x, x.y, x.z, x.w};
+          mma_16816(d, w0 & 0x000f000fu, w1 & 0x000f000fu, w0 & 0x00f000f0u, w1 & 0x00f000f0u, q.x, q.y);
+          mma_16816(d, h0 & 0x000f000fu, h1 & 0x000f000fu, h0 & 0x00f000f0u, h1 & 0x00f000f0u, q.z, q.w);
+          float* const r = s[nt][h];
+          r[0] = j == 0 ? d[0] * s0 : fmaf(d[0], s0, r[0]);
+          r[1] = j == 0 ? d[1] * s0 : fmaf(d[1], s0, r[1]);
+          r[2] = j == 0 ? d[2] * s1 : fmaf(d[2], s1, r[2]);
+          r[3] = j == 0 ? d[3] * s1 : fmaf(d[3], s1, r[3]);
+        }
       }
     }
 
     // the exponent above the chunk's largest value scale
-    const uint32_t sv = st + 2 * L::codes + L::scales;
+    const uint8_t* const sv = st + 2 * L::codes + L::scales;
     int E;
     {
-      const uint32_t w = lds32(sv + (lane & (8 * NG - 1)) * 4);
-      uint32_t top = __reduce_max_sync(kFull, max(w & 0x7fffu, w >> 16 & 0x7fffu));
+      uint32_t w[NG / 2], top = 0;
+      if constexpr (NG == 4) {
+        const uint2 y = *(const uint2*)(sv + lane * 8);
+        w[0] = y.x;
+        w[NG / 2 - 1] = y.y;
+      } else {
+        w[0] = *(const uint32_t*)(sv + lane * 4);
+      }
+#pragma unroll
+      for (int i = 0; i < NG / 2; ++i) top = __vmaxu2(top, w[i] & 0x7fff7fffu);
+      top = __reduce_max_sync(kFull, max(top & 0xffffu, top >> 16));
       if (top >= 0x7f80u) {                        // (not the scales that are not finite)
-        const uint32_t lo = w & 0x7fffu, hi = w >> 16 & 0x7fffu;
-        top = __reduce_max_sync(kFull, max(lo < 0x7f80u ? lo : 0u, hi < 0x7f80u ? hi : 0u));
+        top = 0;
+#pragma unroll
+        for (int i = 0; i < NG / 2; ++i) {
+          const uint32_t lo = w[i] & 0x7fffu, hi = w[i] >> 16 & 0x7fffu;
+          top = max(top, max(lo < 0x7f80u ? lo : 0u, hi < 0x7f80u ? hi : 0u));
+        }
+        top = __reduce_max_sync(kFull, top);
       }
       E = min(max((int)(top >> 7) - 126, kQ4MinExp), kQ4MaxExp);
     }
     const float fE = (float)E;
 
     // P, in the layout of the scores
-    uint32_t pb[NT][2];
+    uint32_t pb[NT][2][2];
+    const float down = q8_scale(127 - E);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      float y[4];
       if (huge) {
 #pragma unroll
-        for (int x = 0; x < 4; ++x) s[nt][x] *= 1024.f;
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int x = 0; x < 4; ++x) s[nt][h][x] *= 1024.f;
       }
 #pragma unroll
-      for (int x = 0; x < 4; ++x) y[x] = fmaf(s[nt][x], c2[nt][x & 1], fE);
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) s[nt][h][x] = fmaf(s[nt][h][x], c2[nt][x & 1], fE);
       if (nv < kChunk) {
-        if (g >= nv) y[0] = y[1] = -INFINITY;
-        if (g + 8 >= nv) y[2] = y[3] = -INFINITY;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int x = 0; x < 4; ++x)
+            if (16 * h + 8 * (x >> 1) + g >= nv) s[nt][h][x] = -INFINITY;
       }
-      const float y0 = fmaxf(y[0], y[2]), y1 = fmaxf(y[1], y[3]);
-      if (__any_sync(kFull, !(y0 <= m[nt][0] + kOverflow) || !(y1 <= m[nt][1] + kOverflow))) {
-        float top[2] = {y0, y1};
+      float top[2];
+#pragma unroll
+      for (int x = 0; x < 2; ++x)
+        top[x] = max3f(fmaxf(s[nt][0][x], s[nt][0][x + 2]), s[nt][1][x], s[nt][1][x + 2]);
+      if (__any_sync(kFull, !(top[0] <= m[nt][0] + kOverflow) || !(top[1] <= m[nt][1] + kOverflow))) {
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
 #pragma unroll
@@ -411,54 +503,66 @@ __global__ void __launch_bounds__(W * 32, kCtas) q4_few_kernel(const __grid_cons
           }
         }
       }
-      const float p0 = ex2(y[0] - m[nt][0]), p1 = ex2(y[1] - m[nt][1]);
-      const float p2 = ex2(y[2] - m[nt][0]), p3 = ex2(y[3] - m[nt][1]);
-      const float down = q8_scale(127 - E);
-      l[nt][0] = fmaf(p0 + p2, down, l[nt][0]);
-      l[nt][1] = fmaf(p1 + p3, down, l[nt][1]);
-      pb[nt][0] = transposed(pack_half2(p0, p1));
-      pb[nt][1] = transposed(pack_half2(p2, p3));
+      float sum[2] = {0.f, 0.f};
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const float p0 = ex2(s[nt][h][0] - m[nt][0]), p1 = ex2(s[nt][h][1] - m[nt][1]);
+        const float p2 = ex2(s[nt][h][2] - m[nt][0]), p3 = ex2(s[nt][h][3] - m[nt][1]);
+        sum[0] += p0 + p2;
+        sum[1] += p1 + p3;
+        pb[nt][h][0] = transposed(pack_half2(p0, p1));
+        pb[nt][h][1] = transposed(pack_half2(p2, p3));
+      }
+      l[nt][0] = fmaf(sum[0], down, l[nt][0]);
+      l[nt][1] = fmaf(sum[1], down, l[nt][1]);
     }
 
-    // V: lane (g, t) takes dims 8 NW g .. of keys 2 t, 2 t + 1 and 2 t + 8, 2 t + 9
-    uint32_t f0[2], f1[2], z[2], v[4][NW];
+    // V: lane (g, t) takes dims 8 NW g .. of keys 2 t, 2 t + 1 and 2 t + 8, 2 t + 9 of a half
     const float up = q8_scale(127 + 15 - E);
+    const uint8_t* const vl = st + L::codes + 2 * t * L::row + 4 * NW * g;
+    const uint8_t* const vs = sv + 2 * t * (NG * 2) + (NG == 4 ? g >> 1 : g >> 2) * 2;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int r = 2 * t + 8 * i;
-      const uint32_t at = sv + r * (NG * 2) + (NG == 4 ? g >> 1 : g >> 2) * 2;
-      f0[i] = pack_half2(bf16_value(lds16(at)) * up, bf16_value(lds16(at + NG * 2)) * up);
-      f1[i] = hmul2(f0[i], 0x2c002c00u);           // 2^-4
-      z[i] = hmul2(f0[i], 0x80088008u);            // -2^-21
+    for (int h = 0; h < 2; ++h) {
+      uint32_t f0[2], f1[2], z[2], v[4][NW];
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        if constexpr (NW == 2) {
-          const uint2 y = lds64(st + L::codes + unit_at<D, true>(r + x, g >> 1) + 8 * (g & 1));
-          v[2 * i + x][0] = y.x;
-          v[2 * i + x][NW - 1] = y.y;
-        } else {
-          v[2 * i + x][0] = lds32(st + L::codes + unit_at<D, true>(r + x, g >> 2) + 4 * (g & 3));
+      for (int i = 0; i < 2; ++i) {
+        const int r = 16 * h + 8 * i;
+        const uint32_t sa = *(const uint16_t*)(vs + r * (NG * 2)), sb = *(const uint16_t*)(vs + (r + 1) * (NG * 2));
+        f0[i] = pack_half2(bf16_value(sa) * up, bf16_value(sb) * up);
+        f1[i] = hmul2(f0[i], 0x2c002c00u);           // 2^-4
+        z[i] = hmul2(f0[i], 0x80088008u);            // -2^-21
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const uint8_t* const p = vl + (r + x) * L::row;
+          if constexpr (NW == 2) {
+            const uint2 y = *(const uint2*)p;
+            v[2 * i + x][0] = y.x;
+            v[2 * i + x][NW - 1] = y.y;
+          } else {
+            v[2 * i + x][0] = *(const uint32_t*)p;
+          }
         }
       }
-    }
 #pragma unroll
-    for (int w = 0; w < NW; ++w) {
-      // the halves of two keys: even dims, odd dims
-      uint32_t ea = __byte_perm(v[0][w], v[1][w], 0x5410), oa = __byte_perm(v[0][w], v[1][w], 0x7632);
-      uint32_t eb = __byte_perm(v[2][w], v[3][w], 0x5410), ob = __byte_perm(v[2][w], v[3][w], 0x7632);
+      for (int w = 0; w < NW; ++w) {
+        // the halves of two keys: even dims, odd dims
+        uint32_t ea = __byte_perm(v[0][w], v[1][w], 0x5410), oa = __byte_perm(v[0][w], v[1][w], 0x7632);
+        uint32_t eb = __byte_perm(v[2][w], v[3][w], 0x5410), ob = __byte_perm(v[2][w], v[3][w], 0x7632);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint32_t mask = i & 1 ? 0x00f000f0u : 0x000f000fu;
-        const uint32_t* const f = i & 1 ? f1 : f0;
-        const uint32_t a0 = hfma2(ea & mask, f[0], z[0]), a1 = hfma2(oa & mask, f[0], z[0]);
-        const uint32_t a2 = hfma2(eb & mask, f[1], z[1]), a3 = hfma2(ob & mask, f[1], z[1]);
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t mask = i & 1 ? 0x00f000f0u : 0x000f000fu;
+          const uint32_t* const f = i & 1 ? f1 : f0;
+          const uint32_t a0 = hfma2(ea & mask, f[0], z[0]), a1 = hfma2(oa & mask, f[0], z[0]);
+          const uint32_t a2 = hfma2(eb & mask, f[1], z[1]), a3 = hfma2(ob & mask, f[1], z[1]);
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) mma_16816(acc[nt][4 * w + i], a0, a1, a2, a3, pb[nt][0], pb[nt][1]);
-        if (i == 1) {
-          ea >>= 8;
-          oa >>= 8;
-          eb >>= 8;
-          ob >>= 8;
+          for (int nt = 0; nt < NT; ++nt)
+            mma_16816(acc[nt][4 * w + i], a0, a1, a2, a3, pb[nt][h][0], pb[nt][h][1]);
+          if (i == 1) {
+            ea >>= 8;
+            oa >>= 8;
+            eb >>= 8;
+            ob >>= 8;
+          }
         }
       }
     }
@@ -512,35 +616,122 @@ __global__ void __launch_bounds__(W * 32, kCtas) q4_few_kernel(const __grid_cons
     o.y *= inv;
     const float lse2 = top + log2f(total);
     const int tr = n / a.g, qh = hk * a.g + n % a.g;
-    if (nsb == 1) {
+    if (nparts == 1) {
       const long orow = ((long)b * a.R + tr) * a.Hq + qh;
       *(uint32_t*)((__nv_bfloat16*)a.out + orow * D + c) = pack_bf16x2(o.x, o.y);
       if (c == 0) a.lse[orow] = lse2 * 0.69314718055994531f;
     } else {
-      const long prow = (((long)b * a.Hq + qh) * a.R + tr) * a.nsplit + sp;
-      *(float2*)((float*)a.part_o + prow * D + c) = o;
-      if (c == 0) a.part_meta[prow] = make_float2(lse2, 1.f);
+      const long prow = (long)place * a.M + n;
+      *(float2*)(sh.out + prow * D + c) = o;
+      if (c == 0) sh.meta[prow] = make_float2(lse2, 1.f);
     }
+  }
+  __syncthreads();                                 // the joint has been read
   }
 }
 
-template <int D, int NT, int W, int S, int kCtas>
-void launch_few(const Q8AttnArgs& a, const Q8Plan& p, cudaStream_t st) {
-  const uint32_t smem = FewLayout<D, NT, W, S>::total;
-  const auto kern = q4_few_kernel<D, NT, W, S, kCtas>;
+// The joint of a head's CTAs: out = sum_s 2^(L_s - L) O_s, L = log2 sum_s 2^(L_s).  A warp per
+// output row; the first kBatch parts are requested together.
+template <int D>
+__global__ void __launch_bounds__(128)
+q4_join_kernel(const __grid_constant__ Q8AttnArgs a, const __grid_constant__ Shares sh) {
+  constexpr int kBatch = 16;
+  grid_dependency_sync();
+  const int lane = threadIdx.x & 31;
+  const long row = (long)blockIdx.x * 4 + (threadIdx.x >> 5);
+  if (row >= (long)a.B * a.R * a.Hq) return;
+  const int b = (int)(row / ((long)a.R * a.Hq)), r = (int)((row / a.Hq) % a.R), h = (int)(row % a.Hq);
+  const int2 pl = sh.place[b * a.map.Hkv + h / a.g];
+  if (pl.y == 1) return;                           // written by its only CTA
+  const int n = r * a.g + h % a.g;
+  auto part = [&](int s) { return (long)(s == 0 ? pl.x : 2 * ((pl.x >> 1) + s)) * a.M + n; };
+  float L = -INFINITY, sum = 0.f;
+  float2 acc = make_float2(0.f, 0.f), acc2 = acc;
+  for (int s0 = 0; s0 < pl.y; s0 += kBatch) {
+    float2 x[kBatch], y[kBatch];
+    const float mine = s0 + (lane & (kBatch - 1)) < pl.y ? sh.meta[part(s0 + (lane & (kBatch - 1)))].x : -INFINITY;
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      if (s0 + i >= pl.y) break;
+      const float2* p = (const float2*)(sh.out + part(s0 + i) * D);
+      x[i] = p[lane];
+      if (D == 128) y[i] = p[lane + 32];
+    }
+    float top = mine;
+#pragma unroll
+    for (int o = kBatch / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
+    const float now = fmaxf(L, top);
+    const float al = L == now ? 1.f : ex2(L - now);
+    // (a part whose pages are all missing saw nothing: weight 0; a NaN stays one)
+    const float w = mine == -INFINITY ? 0.f : ex2(mine - now);
+    L = now;
+    sum *= al;
+    acc.x *= al; acc.y *= al; acc2.x *= al; acc2.y *= al;
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      if (s0 + i >= pl.y) break;
+      const float f = __shfl_sync(kFull, w, i);
+      sum += f;
+      acc.x = fmaf(f, x[i].x, acc.x);
+      acc.y = fmaf(f, x[i].y, acc.y);
+      if (D == 128) {
+        acc2.x = fmaf(f, y[i].x, acc2.x);
+        acc2.y = fmaf(f, y[i].y, acc2.y);
+      }
+    }
+  }
+  const float inv = 1.f / sum;
+  uint32_t* const out = (uint32_t*)((__nv_bfloat16*)a.out + row * D);
+  out[lane] = pack_bf16x2(acc.x * inv, acc.y * inv);
+  if (D == 128) out[lane + 32] = pack_bf16x2(acc2.x * inv, acc2.y * inv);
+  if (lane == 0) a.lse[row] = (L + log2f(sum)) * 0.69314718055994531f;
+}
+
+template <int D, int NT, int S, int kCtas>
+void launch_few(const Q8AttnArgs& a, const Shares& sh, int grid, cudaStream_t st) {
+  const uint32_t smem = FewLayout<D, NT, kWarps, S>::total;
+  const auto kern = q4_few_kernel<D, NT, kWarps, S, kCtas>;
   cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  launch(kern, dim3(a.map.Hkv, p.nsplit, a.B), dim3(W * 32), smem, st, a);
+  launch(kern, dim3(grid), dim3(kWarps * 32), smem, st, a, sh);
 }
 
 }  // namespace
 
-void launch_q4_few(const Q8AttnArgs& a, const Q8Plan& p, int D, cudaStream_t st) {
-  if (D == 128) {
-    if (a.M <= 8) launch_few<128, 1, 8, 5, 2>(a, p, st);
-    else launch_few<128, 2, 8, 6, 1>(a, p, st);
+// CTAs: as many as run at once, or one per head of a large batch.
+int q4_few_grid(const tsd_attn_desc& d) {
+  const long heads = (long)d.B * d.Hkv, units = heads * ceil_div(d.cap, kUnit);
+  if (d.B > kShareBatch) return (int)heads;
+  const long most = 152L * (d.R * (d.Hq / d.Hkv) <= 8 ? 2 : 1);
+  return (int)(units < most ? units : most);
+}
+
+size_t q4_few_workspace(const tsd_attn_desc& d) {
+  if (d.B > kShareBatch) return 0;
+  const size_t rows = 2 * (size_t)q4_few_grid(d) * d.R * (d.Hq / d.Hkv);
+  return rows * (d.dk * sizeof(float) + sizeof(float2)) + (size_t)d.B * d.Hkv * sizeof(int2);
+}
+
+void launch_q4_few(const tsd_attn_desc& d, const Q8AttnArgs& a, void* ws, cudaStream_t st) {
+  const int grid = q4_few_grid(d);
+  Shares sh{};
+  if (d.B <= kShareBatch) {
+    const size_t rows = 2 * (size_t)grid * a.M;
+    sh.out = (float*)ws;
+    sh.meta = (float2*)(sh.out + rows * d.dk);
+    sh.place = (int2*)(sh.meta + rows);
+    sh.least = 4;
+  }
+  if (d.dk == 128) {
+    if (a.M <= 8) launch_few<128, 1, 2, 2>(a, sh, grid, st);
+    else launch_few<128, 2, 4, 1>(a, sh, grid, st);
   } else {
-    if (a.M <= 8) launch_few<64, 1, 8, 6, 2>(a, p, st);
-    else launch_few<64, 2, 8, 6, 1>(a, p, st);
+    if (a.M <= 8) launch_few<64, 1, 4, 2>(a, sh, grid, st);
+    else launch_few<64, 2, 4, 1>(a, sh, grid, st);
+  }
+  if (d.B <= kShareBatch && d.cap > kUnit) {       // (else no head is divided)
+    const dim3 rows((unsigned)ceil_div((long)d.B * d.R * d.Hq, 4));
+    if (d.dk == 128) launch_plain(q4_join_kernel<128>, rows, dim3(128), 0, st, a, sh);
+    else launch_plain(q4_join_kernel<64>, rows, dim3(128), 0, st, a, sh);
   }
 }
 
