@@ -51,33 +51,29 @@ Q8Plan plan_q4(const tsd_attn_desc& d) {
   Q8Plan p{};
   const int M = d.R * (d.Hq / d.Hkv);
   const long heads = (long)d.B * d.Hkv;
-  if (d.dtype == TSD_BF16 && M <= kQ4FewRows) {
-    p.path = kQ8Few;                               // (deals its work out on the device)
-    p.nrg = p.nsplit = 1;
-    p.ws_bytes = q4_few_workspace(d);
-    return p;
-  }
   if (d.dtype == TSD_BF16) {
-    p.path = kQ8Rows;
-    p.part_bytes = 2;
-    p.nrg = (int)ceil_div(M, 128);
+    const bool few = M <= kQ4FewRows;
+    p.path = few ? kQ8Few : kQ8Rows;
+    p.part_bytes = few ? 4 : 2;
+    p.nrg = few ? 1 : (int)ceil_div(M, 128);
     p.rb = (int)ceil_div(M, p.nrg);
     // The split count minimises the modelled time of requests that fill the cache: waves of
-    // CTAs times (tiles of 128 keys + 4 for a CTA's set-up and end), and 5 for the merge.
+    // CTAs times (tiles of 128 keys + a CTA's set-up and end), and the merge.
+    const long slots = 152L * (few && M <= 8 ? 2 : 1), ends = few ? 6 : 4, merge = few ? 6 : 5;
     const long units = heads * p.nrg, tiles = ceil_div(d.cap, 128);
     const long lo = ceil_div(tiles, 256), hi = lo > 64 ? lo : tiles < 64 ? tiles : 64;
     long best = -1, best_per = tiles;
     for (long n = lo; n <= hi; ++n) {
       const long per = ceil_div(tiles, n);
-      const long cost = ceil_div(units * ceil_div(tiles, per), 152L) * (per + 4) + (per < tiles ? 5 : 0);
+      const long cost = ceil_div(units * ceil_div(tiles, per), slots) * (per + ends) + (per < tiles ? merge : 0);
       if (best < 0 || cost < best) { best = cost; best_per = per; }
     }
     p.split_len = (int)best_per * 128;
     p.nsplit = (int)ceil_div(d.cap, p.split_len);
-    p.tree_split = p.nsplit > 1 && best_per <= 8 ? 1 : 0;
+    p.tree_split = !few && p.nsplit > 1 && best_per <= 8 ? 1 : 0;
     p.nsplit += p.tree_split;
     // More CTAs than run at once and a request's keys in one: the longest requests first.
-    p.by_length = p.nsplit == 1 && d.B > 1 && d.B <= 64 && units > 152;
+    p.by_length = p.nsplit == 1 && d.B > 1 && d.B <= 64 && units > slots;
   } else {
     p.path = kQ8Simt;
     p.part_bytes = 4;
@@ -163,7 +159,9 @@ extern "C" tsd_status tsd_tree_verify_attn_q4(const tsd_attn_desc* d, const void
   a.wait_cycles = wait_budget();
   const cudaStream_t st = (cudaStream_t)stream;
   if (p.path == kQ8Few) {
-    launch_q4_few(*d, a, ws, st);
+    launch_q4_few(a, p, d->dk, st);
+    if (d->dk == 128) launch_combine<__nv_bfloat16, 128, float>(a, p, st);
+    else launch_combine<__nv_bfloat16, 64, float>(a, p, st);
   } else if (p.path == kQ8Rows) {
     launch_q4_rows(a, p, d->dk, st);
     if (d->dk == 128) launch_combine<__nv_bfloat16, 128, __half>(a, p, st);

@@ -13,9 +13,7 @@ constexpr int kQ4FewRows = 16;      // packed rows of the path for few
 // scales that writes give: -92..125).
 constexpr int kQ4MinExp = -96, kQ4MaxExp = 118;
 
-int q4_few_grid(const tsd_attn_desc& d);
-size_t q4_few_workspace(const tsd_attn_desc& d);
-void launch_q4_few(const tsd_attn_desc& d, const Q8AttnArgs& a, void* ws, cudaStream_t st);
+void launch_q4_few(const Q8AttnArgs& a, const Q8Plan& p, int D, cudaStream_t st);
 void launch_q4_rows(const Q8AttnArgs& a, const Q8Plan& p, int D, cudaStream_t st);
 
 }  // namespace tsd

@@ -33,30 +33,11 @@
 namespace tsd {
 namespace {
 
-constexpr int kChunk = 32;                         // keys of a chunk: two halves, a product's rows each
 constexpr float kNone = -3.4e38f;                  // a bound before the first key
 constexpr int kWarps = 8;
-constexpr int kUnit = kWarps * kChunk;             // keys of a unit of work: a chunk for each warp
-constexpr int kShareBatch = kWarps * 32;           // requests whose work is dealt out evenly
+constexpr int H = 2, kChunk = 16 * H;              // keys of a chunk: two halves, a product's rows each
 
-// Units of a request's head: at least one, for the scratch rows.
-__device__ __forceinline__ int units_of(int P) { return max(1, (P + kUnit - 1) / kUnit); }
-
-__device__ __noinline__ unsigned share_of(unsigned long long n, unsigned long long d) {
-  return (unsigned)(n / d);                        // (a 64-bit division is 100 instructions)
-}
-
-// Where the CTAs leave the outputs of requests that more than one has worked on: two
-// places per CTA (its first request, its last one).
-struct Shares {
-  float* out;               // [2 CTAs][M][D]
-  float2* meta;             // [2 CTAs][M] (log2-sum-exp, 1)
-  int2* place;              // [B][Hkv]: the first place, and how many: the others are the first
-                            // ones of the CTAs that follow
-  int least;                // units that a CTA gets at least, where all SMs have one
-};
-
-template <int D, int NT, int W, int S>
+template <int D, int NT, int S>
 struct FewLayout {
   static constexpr int NG = D / kQ4Group;
   // A row's codes, padded so that neither way of reading (K: a unit of eight rows; V: a run
@@ -64,6 +45,7 @@ struct FewLayout {
   static constexpr uint32_t row = D / 2 + 16;
   static constexpr uint32_t codes = kChunk * row, scales = kChunk * NG * 2;
   static constexpr uint32_t stage = 2 * codes + 2 * scales;
+  static constexpr int W = kWarps;
   static constexpr uint32_t ring = W * S * stage;
   static constexpr int pitch = D + 4;              // floats of a row in the joint
   static constexpr uint32_t joint = W * NT * 8 * pitch * 4;
@@ -72,10 +54,8 @@ struct FewLayout {
   static constexpr uint32_t off_q = off_ml + (W + 1) * NT * 8 * 8;      // uint4 [NT][NG][32]: B operands
   static constexpr uint32_t off_qs = off_q + NT * NG * 32 * 16;         // float4 [NT][NG][4]: their start
   static constexpr uint32_t off_c2 = off_qs + NT * NG * 4 * 16;         // float [8 NT]: factor of the scores
-  static constexpr uint32_t off_seg = off_c2 + NT * 8 * 4;              // int: request; a huge row
-  static constexpr uint32_t off_pre = off_seg + 16;                     // int [kShareBatch + 1]: units before
-  static constexpr uint32_t off_len = off_pre + (kShareBatch + 4) * 4;  // int [kShareBatch]: lengths
-  static constexpr uint32_t total = off_len + kShareBatch * 4;
+  static constexpr uint32_t off_req = off_c2 + NT * 8 * 4;              // request, its length; a huge row
+  static constexpr uint32_t total = off_req + 16;
   static_assert(stage % 16 == 0, "whole units");
 };
 
@@ -112,86 +92,25 @@ __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
   return d;
 }
 
-template <int D, int NT, int W, int S, int kCtas>
-__global__ void __launch_bounds__(W * 32, kCtas)
-q4_few_kernel(const __grid_constant__ Q8AttnArgs a, const __grid_constant__ Shares sh) {
-  using L = FewLayout<D, NT, W, S>;
+template <int D, int NT, int S, int kCtas>
+__global__ void __launch_bounds__(kWarps * 32, kCtas)
+q4_few_kernel(const __grid_constant__ Q8AttnArgs a) {
+  using L = FewLayout<D, NT, S>;
+  constexpr int W = kWarps;
   constexpr int NG = L::NG, NW = D / 64;           // groups; words of V per lane and key
   extern __shared__ __align__(128) uint8_t smem[];
   grid_dependency_sync();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
-  const int Hkv = a.map.Hkv;
-
-  // This CTA's share: units u .. u_end of all heads' units, in the order of requests and heads.
-  int* const s_pre = (int*)(smem + L::off_pre);
-  int* const s_len = (int*)(smem + L::off_len);
-  int* const s_seg = (int*)(smem + L::off_seg);
-  const bool shared = a.B <= kShareBatch;
-  unsigned u = blockIdx.x, u_end = u + 1, total = 0, ctas = 0;
-  if (shared) {
-    const int P = tid < a.B ? min(max(a.plen[tid], 0), a.map.cap) : 0;
-    int sum = tid < a.B ? units_of(P) : 0;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int x = __shfl_up_sync(kFull, sum, o);
-      if (lane >= o) sum += x;
-    }
-    if (lane == 31) s_len[warp] = sum;
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < W - 1; ++w)
-      if (w < warp) sum += s_len[w];
-    __syncthreads();
-    s_len[tid] = P;
-    s_pre[tid + 1] = sum;
-    if (tid == 0) s_pre[0] = 0;
-    __syncthreads();
-    total = (unsigned)s_pre[a.B] * Hkv;
-    ctas = min(gridDim.x, max(total / sh.least, min(total, 152u)));
-    if (blockIdx.x >= ctas) return;
-    u = share_of((unsigned long long)blockIdx.x * total, ctas);
-    u_end = share_of((unsigned long long)(blockIdx.x + 1) * total, ctas);
-  }
-  const unsigned u0 = u;
-
-#pragma unroll 1
-  for (; u < u_end;) {
-  int b, hk, P, k0, k1, nparts = 1, place = 0;
-  bool with_tree = true;
-  if (tid == 0) s_seg[1] = 0;
-  if (shared) {
-    if (tid < a.B && (unsigned)s_pre[tid] * Hkv <= u && u < (unsigned)s_pre[tid + 1] * Hkv) s_seg[0] = tid;
-    __syncthreads();
-    b = s_seg[0];
-    P = s_len[b];
-    const unsigned tl = s_pre[b + 1] - s_pre[b], r = u - (unsigned)s_pre[b] * Hkv;
-    hk = r / tl;
-    const unsigned first = (unsigned)s_pre[b] * Hkv + hk * tl, end = first + tl;
-    const unsigned stop = min(u_end, end), tile = r - hk * tl;
-    k0 = min((int)tile * kUnit, P);
-    k1 = min(P, k0 + (int)(stop - u) * kUnit);
-    with_tree = stop == end;
-    if (u != first || stop != end) {               // others work on this head, too
-      const unsigned i0 = share_of((unsigned long long)(first + 1) * ctas - 1, total);
-      const unsigned i1 = share_of((unsigned long long)end * ctas - 1, total);
-      nparts = i1 - i0 + 1;
-      place = 2 * blockIdx.x + (u != u0);
-      if (tid == 0)
-        sh.place[b * Hkv + hk] =
-            make_int2(2 * i0 + (share_of((unsigned long long)i0 * total, ctas) != first), nparts);
-    } else if (tid == 0) {
-      sh.place[b * Hkv + hk] = make_int2(0, 1);
-    }
-    u = stop;
-  } else {
-    b = u / Hkv;
-    hk = u % Hkv;
-    P = min(max(a.plen[b], 0), a.map.cap);
-    k0 = 0;
-    k1 = P;
-    u = u_end;
-    __syncthreads();
-  }
+  const int hk = blockIdx.x, sp = blockIdx.y;
+  int* const s_huge = (int*)(smem + L::off_req) + 2;  // a row from 2^117 on: its factor in two steps
+  if (tid == 0) *s_huge = 0;
+  int P;
+  const int b = request_at(a, blockIdx.z, P, (volatile int*)(smem + L::off_req));
+  const int nsb = q8_splits(a, P);
+  if (sp >= nsb) return;
+  const int k0 = min(sp * a.split_len, P), k1 = min(P, k0 + a.split_len);
+  const bool with_tree = sp == nsb - 1;
+  __syncthreads();                                 // (s_huge)
 
   // ------------------------------------------------------------- the ring
   // A warp's chunks lie W * kChunk keys apart: within a page the next one is at a fixed
@@ -218,6 +137,7 @@ q4_few_kernel(const __grid_constant__ Q8AttnArgs a, const __grid_constant__ Shar
     vsp = a.ve + (row + lane) * (NG * 2);
   };
   constexpr int U = D / 32, kRowStep = 32 / U;        // units of a row, rows of a warp's copy
+  constexpr int kCopies = kChunk / kRowStep;
   const uint32_t to = (uint32_t)(lane / U) * L::row + (lane % U) * 16;
   // chunk c into a slot; then on to the warp's next one
   auto request = [&](int c, int slot) {
@@ -225,7 +145,7 @@ q4_few_kernel(const __grid_constant__ Q8AttnArgs a, const __grid_constant__ Shar
     const int nv = k1 - (k0 + c * kChunk);
     if (nv >= kChunk) {
 #pragma unroll
-      for (int i = 0; i < U; ++i) {
+      for (int i = 0; i < kCopies; ++i) {
         cp_async_z(st + to + i * kRowStep * L::row, kp + 512 * i, true);
         cp_async_z(st + L::codes + to + i * kRowStep * L::row, vp + 512 * i, true);
       }
@@ -233,13 +153,14 @@ q4_few_kernel(const __grid_constant__ Q8AttnArgs a, const __grid_constant__ Shar
       cp_async_small<NG * 2>(st + 2 * L::codes + L::scales + lane * (NG * 2), vsp, true);
     } else if (nv > 0) {                              // rows that are not there: zeros
 #pragma unroll 1
-      for (int i = 0; i < U; ++i) {
+      for (int i = 0; i < kCopies; ++i) {
         const bool there = lane / U + i * kRowStep < nv;
         cp_async_z(st + to + i * kRowStep * L::row, there ? kp + 512 * i : a.kc, there);
         cp_async_z(st + L::codes + to + i * kRowStep * L::row, there ? vp + 512 * i : a.vc, there);
       }
-      cp_async_small<NG * 2>(st + 2 * L::codes + lane * (NG * 2), lane < nv ? ksp : a.ke, lane < nv);
-      cp_async_small<NG * 2>(st + 2 * L::codes + L::scales + lane * (NG * 2), lane < nv ? vsp : a.ve, lane < nv);
+      const bool there = lane < nv;
+      cp_async_small<NG * 2>(st + 2 * L::codes + lane * (NG * 2), there ? ksp : a.ke, there);
+      cp_async_small<NG * 2>(st + 2 * L::codes + L::scales + lane * (NG * 2), there ? vsp : a.ve, there);
     }
     asm volatile("cp.async.commit_group;\n" ::: "memory");
     if (left > 0) {
@@ -263,7 +184,6 @@ q4_few_kernel(const __grid_constant__ Q8AttnArgs a, const __grid_constant__ Shar
   uint4* const s_q = (uint4*)(smem + L::off_q);
   float* const s_qs = (float*)(smem + L::off_qs);
   float* const s_c2 = (float*)(smem + L::off_c2);
-  int* const s_huge = s_seg + 1;                     // a row from 2^117 on: its factor in two steps
   static_assert(NT * NG <= W, "a warp per group");
   if (warp < NT * NG) {
     const int nt = warp / NG, j = warp % NG, n = nt * 8 + g;
@@ -393,37 +313,43 @@ q4_few_kernel(const __grid_constant__ Q8AttnArgs a, const __grid_constant__ Shar
     slot = slot == S - 1 ? 0 : slot + 1;
 
     // scores of keys g and g + 8 of each half, columns 2 t and 2 t + 1
-    float s[NT][2][4];
+    float s[NT][H][4];
     const uint8_t* const kl = st + g * L::row + 4 * t;
     const uint8_t* const sl = st + 2 * L::codes + g * (NG * 2);
+    uint32_t ks[2 * H][NG / 2];                    // rows g, g + 8, ..
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      uint32_t ks[2][NG / 2];
+    for (int x = 0; x < 2 * H; ++x) {
+      const uint8_t* const p = sl + 8 * x * (NG * 2);
+      if constexpr (NG == 4) {
+        const uint2 y = *(const uint2*)p;
+        ks[x][0] = y.x;
+        ks[x][NG / 2 - 1] = y.y;
+      } else {
+        ks[x][0] = *(const uint32_t*)p;
+      }
+    }
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const uint8_t* const p = sl + (16 * h + 8 * x) * (NG * 2);
-        if constexpr (NG == 4) {
-          const uint2 y = *(const uint2*)p;
-          ks[x][0] = y.x;
-          ks[x][NG / 2 - 1] = y.y;
-        } else {
-          ks[x][0] = *(const uint32_t*)p;
-        }
+    for (int j = 0; j < NG; ++j) {
+      uint4 q[NT];
+      float4 start[NT];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        q[nt] = s_q[(nt * NG + j) * 32 + lane];
+        start[nt] = *(const float4*)(s_qs + ((nt * NG + j) * 4 + t) * 4);
       }
 #pragma unroll
-      for (int j = 0; j < NG; ++j) {
+      for (int h = 0; h < H; ++h) {
         const uint32_t w0 = *(const uint32_t*)(kl + 16 * h * L::row + 16 * j);
         const uint32_t w1 = *(const uint32_t*)(kl + (16 * h + 8) * L::row + 16 * j);
         const uint32_t h0 = w0 >> 8, h1 = w1 >> 8;
-        const float s0 = __uint_as_float(j & 1 ? ks[0][j / 2] & 0xffff0000u : ks[0][j / 2] << 16);
-        const float s1 = __uint_as_float(j & 1 ? ks[1][j / 2] & 0xffff0000u : ks[1][j / 2] << 16);
+        const uint32_t k0w = ks[2 * h][j / 2], k1w = ks[2 * h + 1][j / 2];
+        const float s0 = __uint_as_float(j & 1 ? k0w & 0xffff0000u : k0w << 16);
+        const float s1 = __uint_as_float(j & 1 ? k1w & 0xffff0000u : k1w << 16);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          const uint4 q = s_q[(nt * NG + j) * 32 + lane];
-          const float4 x = *(const float4*)(s_qs + ((nt * NG + j) * 4 + t) * 4);
-          float d[4] = {x.x, x.y, x.z, x.w};
-          mma_16816(d, w0 & 0x000f000fu, w1 & 0x000f000fu, w0 & 0x00f000f0u, w1 & 0x00f000f0u, q.x, q.y);
-          mma_16816(d, h0 & 0x000f000fu, h1 & 0x000f000fu, h0 & 0x00f000f0u, h1 & 0x00f000f0u, q.z, q.w);
+          float d[4] = {start[nt].x, start[nt].y, start[nt].z, start[nt].w};
+          mma_16816(d, w0 & 0x000f000fu, w1 & 0x000f000fu, w0 & 0x00f000f0u, w1 & 0x00f000f0u, q[nt].x, q[nt].y);
+          mma_16816(d, h0 & 0x000f000fu, h1 & 0x000f000fu, h0 & 0x00f000f0u, h1 & 0x00f000f0u, q[nt].z, q[nt].w);
           float* const r = s[nt][h];
           r[0] = j == 0 ? d[0] * s0 : fmaf(d[0], s0, r[0]);
           r[1] = j == 0 ? d[1] * s0 : fmaf(d[1], s0, r[1]);
@@ -437,21 +363,22 @@ q4_few_kernel(const __grid_constant__ Q8AttnArgs a, const __grid_constant__ Shar
     const uint8_t* const sv = st + 2 * L::codes + L::scales;
     int E;
     {
-      uint32_t w[NG / 2], top = 0;
-      if constexpr (NG == 4) {
+      constexpr int kWords = NG / 2;
+      uint32_t w[kWords], top = 0;
+      if constexpr (kWords == 2) {
         const uint2 y = *(const uint2*)(sv + lane * 8);
         w[0] = y.x;
-        w[NG / 2 - 1] = y.y;
+        w[kWords - 1] = y.y;
       } else {
         w[0] = *(const uint32_t*)(sv + lane * 4);
       }
 #pragma unroll
-      for (int i = 0; i < NG / 2; ++i) top = __vmaxu2(top, w[i] & 0x7fff7fffu);
+      for (int i = 0; i < kWords; ++i) top = __vmaxu2(top, w[i] & 0x7fff7fffu);
       top = __reduce_max_sync(kFull, max(top & 0xffffu, top >> 16));
       if (top >= 0x7f80u) {                        // (not the scales that are not finite)
         top = 0;
 #pragma unroll
-        for (int i = 0; i < NG / 2; ++i) {
+        for (int i = 0; i < kWords; ++i) {
           const uint32_t lo = w[i] & 0x7fffu, hi = w[i] >> 16 & 0x7fffu;
           top = max(top, max(lo < 0x7f80u ? lo : 0u, hi < 0x7f80u ? hi : 0u));
         }
@@ -462,23 +389,23 @@ q4_few_kernel(const __grid_constant__ Q8AttnArgs a, const __grid_constant__ Shar
     const float fE = (float)E;
 
     // P, in the layout of the scores
-    uint32_t pb[NT][2][2];
+    uint32_t pb[NT][H][2];
     const float down = q8_scale(127 - E);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       if (huge) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
+        for (int h = 0; h < H; ++h)
 #pragma unroll
           for (int x = 0; x < 4; ++x) s[nt][h][x] *= 1024.f;
       }
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
+      for (int h = 0; h < H; ++h)
 #pragma unroll
         for (int x = 0; x < 4; ++x) s[nt][h][x] = fmaf(s[nt][h][x], c2[nt][x & 1], fE);
       if (nv < kChunk) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
+        for (int h = 0; h < H; ++h)
 #pragma unroll
           for (int x = 0; x < 4; ++x)
             if (16 * h + 8 * (x >> 1) + g >= nv) s[nt][h][x] = -INFINITY;
@@ -505,7 +432,7 @@ q4_few_kernel(const __grid_constant__ Q8AttnArgs a, const __grid_constant__ Shar
       }
       float sum[2] = {0.f, 0.f};
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
+      for (int h = 0; h < H; ++h) {
         const float p0 = ex2(s[nt][h][0] - m[nt][0]), p1 = ex2(s[nt][h][1] - m[nt][1]);
         const float p2 = ex2(s[nt][h][2] - m[nt][0]), p3 = ex2(s[nt][h][3] - m[nt][1]);
         sum[0] += p0 + p2;
@@ -522,7 +449,7 @@ q4_few_kernel(const __grid_constant__ Q8AttnArgs a, const __grid_constant__ Shar
     const uint8_t* const vl = st + L::codes + 2 * t * L::row + 4 * NW * g;
     const uint8_t* const vs = sv + 2 * t * (NG * 2) + (NG == 4 ? g >> 1 : g >> 2) * 2;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
+    for (int h = 0; h < H; ++h) {
       uint32_t f0[2], f1[2], z[2], v[4][NW];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
@@ -616,122 +543,35 @@ q4_few_kernel(const __grid_constant__ Q8AttnArgs a, const __grid_constant__ Shar
     o.y *= inv;
     const float lse2 = top + log2f(total);
     const int tr = n / a.g, qh = hk * a.g + n % a.g;
-    if (nparts == 1) {
+    if (nsb == 1) {
       const long orow = ((long)b * a.R + tr) * a.Hq + qh;
       *(uint32_t*)((__nv_bfloat16*)a.out + orow * D + c) = pack_bf16x2(o.x, o.y);
       if (c == 0) a.lse[orow] = lse2 * 0.69314718055994531f;
     } else {
-      const long prow = (long)place * a.M + n;
-      *(float2*)(sh.out + prow * D + c) = o;
-      if (c == 0) sh.meta[prow] = make_float2(lse2, 1.f);
+      const long prow = (((long)b * a.Hq + qh) * a.R + tr) * a.nsplit + sp;
+      *(float2*)((float*)a.part_o + prow * D + c) = o;
+      if (c == 0) a.part_meta[prow] = make_float2(lse2, 1.f);
     }
   }
-  __syncthreads();                                 // the joint has been read
-  }
-}
-
-// The joint of a head's CTAs: out = sum_s 2^(L_s - L) O_s, L = log2 sum_s 2^(L_s).  A warp per
-// output row; the first kBatch parts are requested together.
-template <int D>
-__global__ void __launch_bounds__(128)
-q4_join_kernel(const __grid_constant__ Q8AttnArgs a, const __grid_constant__ Shares sh) {
-  constexpr int kBatch = 16;
-  grid_dependency_sync();
-  const int lane = threadIdx.x & 31;
-  const long row = (long)blockIdx.x * 4 + (threadIdx.x >> 5);
-  if (row >= (long)a.B * a.R * a.Hq) return;
-  const int b = (int)(row / ((long)a.R * a.Hq)), r = (int)((row / a.Hq) % a.R), h = (int)(row % a.Hq);
-  const int2 pl = sh.place[b * a.map.Hkv + h / a.g];
-  if (pl.y == 1) return;                           // written by its only CTA
-  const int n = r * a.g + h % a.g;
-  auto part = [&](int s) { return (long)(s == 0 ? pl.x : 2 * ((pl.x >> 1) + s)) * a.M + n; };
-  float L = -INFINITY, sum = 0.f;
-  float2 acc = make_float2(0.f, 0.f), acc2 = acc;
-  for (int s0 = 0; s0 < pl.y; s0 += kBatch) {
-    float2 x[kBatch], y[kBatch];
-    const float mine = s0 + (lane & (kBatch - 1)) < pl.y ? sh.meta[part(s0 + (lane & (kBatch - 1)))].x : -INFINITY;
-#pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      if (s0 + i >= pl.y) break;
-      const float2* p = (const float2*)(sh.out + part(s0 + i) * D);
-      x[i] = p[lane];
-      if (D == 128) y[i] = p[lane + 32];
-    }
-    float top = mine;
-#pragma unroll
-    for (int o = kBatch / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
-    const float now = fmaxf(L, top);
-    const float al = L == now ? 1.f : ex2(L - now);
-    // (a part whose pages are all missing saw nothing: weight 0; a NaN stays one)
-    const float w = mine == -INFINITY ? 0.f : ex2(mine - now);
-    L = now;
-    sum *= al;
-    acc.x *= al; acc.y *= al; acc2.x *= al; acc2.y *= al;
-#pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      if (s0 + i >= pl.y) break;
-      const float f = __shfl_sync(kFull, w, i);
-      sum += f;
-      acc.x = fmaf(f, x[i].x, acc.x);
-      acc.y = fmaf(f, x[i].y, acc.y);
-      if (D == 128) {
-        acc2.x = fmaf(f, y[i].x, acc2.x);
-        acc2.y = fmaf(f, y[i].y, acc2.y);
-      }
-    }
-  }
-  const float inv = 1.f / sum;
-  uint32_t* const out = (uint32_t*)((__nv_bfloat16*)a.out + row * D);
-  out[lane] = pack_bf16x2(acc.x * inv, acc.y * inv);
-  if (D == 128) out[lane + 32] = pack_bf16x2(acc2.x * inv, acc2.y * inv);
-  if (lane == 0) a.lse[row] = (L + log2f(sum)) * 0.69314718055994531f;
 }
 
 template <int D, int NT, int S, int kCtas>
-void launch_few(const Q8AttnArgs& a, const Shares& sh, int grid, cudaStream_t st) {
-  const uint32_t smem = FewLayout<D, NT, kWarps, S>::total;
-  const auto kern = q4_few_kernel<D, NT, kWarps, S, kCtas>;
+void launch_few(const Q8AttnArgs& a, const Q8Plan& p, cudaStream_t st) {
+  const uint32_t smem = FewLayout<D, NT, S>::total;
+  const auto kern = q4_few_kernel<D, NT, S, kCtas>;
   cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  launch(kern, dim3(grid), dim3(kWarps * 32), smem, st, a, sh);
+  launch(kern, dim3(a.map.Hkv, p.nsplit, a.B), dim3(kWarps * 32), smem, st, a);
 }
 
 }  // namespace
 
-// CTAs: as many as run at once, or one per head of a large batch.
-int q4_few_grid(const tsd_attn_desc& d) {
-  const long heads = (long)d.B * d.Hkv, units = heads * ceil_div(d.cap, kUnit);
-  if (d.B > kShareBatch) return (int)heads;
-  const long most = 152L * (d.R * (d.Hq / d.Hkv) <= 8 ? 2 : 1);
-  return (int)(units < most ? units : most);
-}
-
-size_t q4_few_workspace(const tsd_attn_desc& d) {
-  if (d.B > kShareBatch) return 0;
-  const size_t rows = 2 * (size_t)q4_few_grid(d) * d.R * (d.Hq / d.Hkv);
-  return rows * (d.dk * sizeof(float) + sizeof(float2)) + (size_t)d.B * d.Hkv * sizeof(int2);
-}
-
-void launch_q4_few(const tsd_attn_desc& d, const Q8AttnArgs& a, void* ws, cudaStream_t st) {
-  const int grid = q4_few_grid(d);
-  Shares sh{};
-  if (d.B <= kShareBatch) {
-    const size_t rows = 2 * (size_t)grid * a.M;
-    sh.out = (float*)ws;
-    sh.meta = (float2*)(sh.out + rows * d.dk);
-    sh.place = (int2*)(sh.meta + rows);
-    sh.least = 4;
-  }
-  if (d.dk == 128) {
-    if (a.M <= 8) launch_few<128, 1, 2, 2>(a, sh, grid, st);
-    else launch_few<128, 2, 4, 1>(a, sh, grid, st);
+void launch_q4_few(const Q8AttnArgs& a, const Q8Plan& p, int D, cudaStream_t st) {
+  if (D == 128) {
+    if (a.M <= 8) launch_few<128, 1, 2, 2>(a, p, st);
+    else launch_few<128, 2, 3, 1>(a, p, st);
   } else {
-    if (a.M <= 8) launch_few<64, 1, 4, 2>(a, sh, grid, st);
-    else launch_few<64, 2, 4, 1>(a, sh, grid, st);
-  }
-  if (d.B <= kShareBatch && d.cap > kUnit) {       // (else no head is divided)
-    const dim3 rows((unsigned)ceil_div((long)d.B * d.R * d.Hq, 4));
-    if (d.dk == 128) launch_plain(q4_join_kernel<128>, rows, dim3(128), 0, st, a, sh);
-    else launch_plain(q4_join_kernel<64>, rows, dim3(128), 0, st, a, sh);
+    if (a.M <= 8) launch_few<64, 1, 3, 2>(a, p, st);
+    else launch_few<64, 2, 3, 1>(a, p, st);
   }
 }
 
