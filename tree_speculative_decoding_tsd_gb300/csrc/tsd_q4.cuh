@@ -48,15 +48,21 @@ __device__ __forceinline__ uint32_t q4_scale(float hi, float lo) {
 
 // Eight elements as a word of codes, given 1 / s (fp32, rounded to nearest): the nearest
 // whole number to x / s, ties to even, within -8..7, plus 8.  Adding 1.5 * 2^23 + 8 rounds
-// the exact product (a fused multiply-add) to a whole number in the sum's lowest bits.
+// the exact product (a fused multiply-add) to a whole number in the sum's lowest bits;
+// cvt.pack clamps two numbers to four bits and puts them behind those it is given.
 __device__ __forceinline__ uint32_t q4_word(const float (&x)[8], float inv) {
   constexpr float kZero = 12582912.f;
-  uint32_t w = 0;
+  int c[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float y = fminf(fmaxf(fmaf(x[i], inv, kZero + 8.f), kZero), kZero + 15.f);
-    w |= (__float_as_uint(y) & 15u) << ((i & 1) * 16 + (i >> 1) * 4);
-  }
+  for (int i = 0; i < 8; ++i) c[i] = __float_as_int(fmaf(x[i], inv, kZero + 8.f)) - 0x4b400000;
+  uint32_t w = 0;
+  auto pack = [&](int hi, int lo) {
+    asm("cvt.pack.sat.u4.s32.b32 %0, %1, %2, %0;\n" : "+r"(w) : "r"(hi), "r"(lo));
+  };
+  pack(c[7], c[5]);
+  pack(c[3], c[1]);
+  pack(c[6], c[4]);
+  pack(c[2], c[0]);
   return w;
 }
 // 1 / s; 0 for a group of zeros or one that holds a NaN, whose codes are 8.

@@ -8,9 +8,9 @@
 //   x* = the element of largest magnitude,  s = bf16(-x* / 8),
 //   c  = clamp(round(x / s), -8, 7) + 8;  read back: (c - 8) s
 //
-// Four lanes hold a group, eight elements (one word of codes) each: 16 bytes in, 4 out,
-// the group's largest and smallest by two shuffles.  Bounded by memory: a warp requests
-// four times 512 bytes before it uses any.
+// Writing, two lanes hold a group, sixteen elements (two words of codes) each: a scale and
+// its inverse cost as much as eight elements do, and a shuffle joins two ranges.  Reading, a
+// lane has eight elements.
 #include <cuda_bf16.h>
 #include <math.h>
 
@@ -35,95 +35,113 @@ struct Q4CacheArgs {
   int rows, S;             // rows per request of src or dst; path length bound
 };
 
-constexpr int kThreads = 128;
+constexpr int kThreads = 256;
 constexpr int kTokens = 32;                    // positions of a CTA (write, read)
-constexpr int kUnroll = 4;                     // rows of a lane requested together
+constexpr int kUnroll = 2;                     // rows of a lane requested together
 constexpr int kPathThreads = 512;
+// Appends of at most this many rows (those of a path) take one CTA per request and no second
+// launch.
+constexpr int kFewRows = 17;
 
-// Eight elements of a row as fp32, and their running largest and smallest (NaN if any is).
+// Sixteen elements of a row: half a group.  range: the group's largest element and minus its
+// smallest (NaN if any is), from two lanes.
 __device__ __forceinline__ float max_nan(float a, float b) {
   float r;
   asm("max.NaN.f32 %0, %1, %2;\n" : "=f"(r) : "f"(a), "f"(b));
   return r;
 }
-__device__ __forceinline__ float min_nan(float a, float b) {
-  float r;
-  asm("min.NaN.f32 %0, %1, %2;\n" : "=f"(r) : "f"(a), "f"(b));
-  return r;
-}
 struct RowF32 {
-  float4 a, b;
+  float4 a[4];
   __device__ __forceinline__ void load(const float* p) {
-    a = __ldg((const float4*)p);
-    b = __ldg((const float4*)p + 1);
-  }
-  __device__ __forceinline__ void values(float (&x)[8]) const {
-    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-    x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
-  }
-  __device__ __forceinline__ void range(float& hi, float& lo) const {
-    float x[8];
-    values(x);
-    hi = lo = x[0];
 #pragma unroll
-    for (int i = 1; i < 8; ++i) {
-      hi = max_nan(hi, x[i]);
-      lo = min_nan(lo, x[i]);
+    for (int i = 0; i < 4; ++i) a[i] = __ldg((const float4*)p + i);
+  }
+  template <int kHalf> __device__ __forceinline__ void values(float (&x)[8]) const {
+    const float4 u = a[2 * kHalf], v = a[2 * kHalf + 1];
+    x[0] = u.x; x[1] = u.y; x[2] = u.z; x[3] = u.w;
+    x[4] = v.x; x[5] = v.y; x[6] = v.z; x[7] = v.w;
+  }
+  __device__ __forceinline__ float2 range() const {
+    float x[8], y[8];
+    values<0>(x);
+    values<1>(y);
+    float hi = x[0], lo = -x[0];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      hi = max_nan(max_nan(hi, x[i]), y[i]);
+      lo = max_nan(max_nan(lo, -x[i]), -y[i]);
     }
+    hi = max_nan(hi, __shfl_xor_sync(kFull, hi, 1));
+    lo = max_nan(lo, __shfl_xor_sync(kFull, lo, 1));
+    return make_float2(hi, lo);
   }
 };
 struct RowBf16 {
-  uint4 a;
-  __device__ __forceinline__ void load(const __nv_bfloat16* p) { a = __ldg((const uint4*)p); }
-  __device__ __forceinline__ void values(float (&x)[8]) const {
-    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+  uint4 a[2];
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) {
+    a[0] = __ldg((const uint4*)p);
+    a[1] = __ldg((const uint4*)p + 1);
+  }
+  template <int kHalf> __device__ __forceinline__ void values(float (&x)[8]) const {
+    const uint32_t w[4] = {a[kHalf].x, a[kHalf].y, a[kHalf].z, a[kHalf].w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       x[2 * i] = __uint_as_float(w[i] << 16);
       x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
     }
   }
-  __device__ __forceinline__ void range(float& hi, float& lo) const {
-    auto pair = [](const uint32_t& w) { return *reinterpret_cast<const __nv_bfloat162*>(&w); };
-    const __nv_bfloat162 h =
-        __hmax2_nan(__hmax2_nan(pair(a.x), pair(a.y)), __hmax2_nan(pair(a.z), pair(a.w)));
-    const __nv_bfloat162 l =
-        __hmin2_nan(__hmin2_nan(pair(a.x), pair(a.y)), __hmin2_nan(pair(a.z), pair(a.w)));
-    hi = max_nan(__low2float(h), __high2float(h));
-    lo = min_nan(__low2float(l), __high2float(l));
+  __device__ __forceinline__ float2 range() const {
+    const uint32_t w[8] = {a[0].x, a[0].y, a[0].z, a[0].w, a[1].x, a[1].y, a[1].z, a[1].w};
+    auto pair = [](const uint32_t& v) { return *reinterpret_cast<const __nv_bfloat162*>(&v); };
+    __nv_bfloat162 h = pair(w[0]), l = h;
+#pragma unroll
+    for (int i = 1; i < 8; ++i) {
+      h = __hmax2_nan(h, pair(w[i]));
+      l = __hmin2_nan(l, pair(w[i]));
+    }
+    // (largest, minus the smallest) side by side, for one shuffle
+    l = __hneg2(l);
+    __nv_bfloat162 m = __hmax2_nan(__lows2bfloat162(h, l), __highs2bfloat162(h, l));
+    const uint32_t o = __shfl_xor_sync(kFull, *reinterpret_cast<const uint32_t*>(&m), 1);
+    m = __hmax2_nan(m, pair(o));
+    return __bfloat1622float2(m);
   }
 };
 template <typename T> struct RowOf { using type = RowF32; };
 template <> struct RowOf<__nv_bfloat16> { using type = RowBf16; };
 
-// Lane c (of D / 8) of a row: its eight elements to a word of codes and, from the first
+// Lane c (of D / 16) of a row: its sixteen elements to two words of codes and, from the first
 // lane of a group, the group's scale.  All lanes of a warp take part.
 template <typename Row>
 __device__ __forceinline__ void put_row(const Row& r, bool live, uint32_t* codes, uint16_t* scales,
                                         int c) {
-  float hi, lo;
-  r.range(hi, lo);
-#pragma unroll
-  for (int o = 1; o < 4; o <<= 1) {
-    hi = max_nan(hi, __shfl_xor_sync(kFull, hi, o));
-    lo = min_nan(lo, __shfl_xor_sync(kFull, lo, o));
-  }
-  const uint32_t s = q4_scale(hi, lo);
+  const float2 m = r.range();
+  const uint32_t s = q4_scale(m.x, -m.y);
   const float inv = q4_inverse(s);
-  float x[8];
-  r.values(x);
-  const uint32_t w = inv == 0.f ? 0x88888888u : q4_word(x, inv);
+  float x[8], y[8];
+  r.template values<0>(x);
+  r.template values<1>(y);
+  const uint32_t w0 = inv == 0.f ? 0x88888888u : q4_word(x, inv);
+  const uint32_t w1 = inv == 0.f ? 0x88888888u : q4_word(y, inv);
   if (!live) return;
-  codes[c] = w;
-  if ((c & 3) == 0) scales[c >> 2] = (uint16_t)s;
+  ((uint2*)codes)[c] = make_uint2(w0, w1);
+  if ((c & 1) == 0) scales[c >> 1] = (uint16_t)s;
+}
+
+// Rows of head 0 of positions pos .. pos + n - 1 (n <= kTokens), for the whole CTA; a head
+// further on they lie the returned distance further.
+__device__ __forceinline__ long head_rows(const CacheMap& m, int b, int pos, int n, long* rows) {
+  if ((int)threadIdx.x < n) rows[threadIdx.x] = m.row(b, 0, pos + threadIdx.x);
+  __syncthreads();
+  return m.page_size ? m.page_size : m.cap;
 }
 
 // Prefill: grid (tokens, K or V, request).  prefix_len changes only in
 // q4_advance_kernel, so every CTA reads the length of before.  A warp takes kUnroll times
-// 256 / D consecutive positions of a head, which it writes side by side.
+// 512 / D consecutive positions of a head, which it writes side by side.
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads) write_q4_kernel(const __grid_constant__ Q4CacheArgs a) {
-  constexpr int VR = D / 8, kRows = 32 / VR, kBatch = kRows * kUnroll;
+  constexpr int VR = D / 16, kRows = 32 / VR, kBatch = kRows * kUnroll;
   using Row = typename RowOf<T>::type;
   __shared__ AppendSmem s;
   grid_dependency_sync();
@@ -131,6 +149,8 @@ __global__ void __launch_bounds__(kThreads) write_q4_kernel(const __grid_constan
   const int n = append_rows<false>(a, b, P, n0, 0, s);
   const int t0 = blockIdx.x * kTokens;
   if (t0 >= n) return;                                 // (no rows, or an error)
+  __shared__ long rows[kTokens];
+  const long apart = head_rows(a.map, b, P + t0, min(kTokens, n - t0), rows);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int c = lane % VR, sub = lane / VR;
   const T* const src = (const T*)a.src[part] + (long)b * a.rows * a.map.Hkv * D;
@@ -142,8 +162,8 @@ __global__ void __launch_bounds__(kThreads) write_q4_kernel(const __grid_constan
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
       const int x = min(t + u * kRows, n - 1);
-      r[u].load(src + ((long)x * a.map.Hkv + h) * D + c * 8);
-      row[u] = a.map.row(b, h, P + x);
+      r[u].load(src + ((long)x * a.map.Hkv + h) * D + c * 16);
+      row[u] = rows[x - t0] + h * apart;
     }
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u)
@@ -166,7 +186,7 @@ __global__ void __launch_bounds__(128) q4_advance_kernel(const __grid_constant__
 template <typename T, int D, bool kPath>
 __global__ void __launch_bounds__(kPathThreads)
 append_q4_kernel(const __grid_constant__ Q4CacheArgs a) {
-  constexpr int VR = D / 8, kRows = 32 / VR;
+  constexpr int VR = D / 16, kRows = 32 / VR;
   using Row = typename RowOf<T>::type;
   __shared__ AppendSmem s;
   grid_dependency_sync();
@@ -178,6 +198,9 @@ append_q4_kernel(const __grid_constant__ Q4CacheArgs a) {
     else a.prefix_len[b] = P + n;
   }
   if (n <= 0) return;
+  static_assert(kFewRows <= kTokens, "a row per thread");
+  __shared__ long rows[kTokens];
+  const long apart = head_rows(a.map, b, P, n, rows);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int c = lane % VR, sub = lane / VR, Hkv = a.map.Hkv;
   const int work = 2 * Hkv * n;                        // (part, head, row)
@@ -185,8 +208,8 @@ append_q4_kernel(const __grid_constant__ Q4CacheArgs a) {
     const int i = i0 + sub, j = min(i, work - 1);
     const int t = j % n, h = j / n % Hkv, part = j / n / Hkv;
     Row r;
-    r.load((const T*)a.src[part] + (((long)b * a.rows + (kPath ? s.path[t] : t)) * Hkv + h) * D + c * 8);
-    const long row = a.map.row(b, h, P + t);
+    r.load((const T*)a.src[part] + (((long)b * a.rows + (kPath ? s.path[t] : t)) * Hkv + h) * D + c * 16);
+    const long row = rows[t] + h * apart;
     put_row(r, i < work, a.codes[part] + row * (D / 8), a.scales[part] + row * (D / kQ4Group), c);
   }
 }
@@ -233,6 +256,8 @@ __global__ void __launch_bounds__(kThreads) read_q4_kernel(const __grid_constant
   }
   const int t0 = blockIdx.x * kTokens;
   if (t0 >= n) return;
+  __shared__ long rows[kTokens];
+  const long apart = head_rows(a.map, b, p0 + t0, min(kTokens, n - t0), rows);
   const int lane = tid & 31, warp = tid >> 5;
   const int c = lane % VR, sub = lane / VR;
   T* const dst = (T*)a.dst[part] + (long)b * a.rows * a.map.Hkv * D;
@@ -243,7 +268,7 @@ __global__ void __launch_bounds__(kThreads) read_q4_kernel(const __grid_constant
     float f[kUnroll];
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
-      const long row = a.map.row(b, h, p0 + min(t + u * kRows, n - 1));
+      const long row = rows[min(t + u * kRows, n - 1) - t0] + h * apart;
       w[u] = __ldg(a.codes[part] + row * (D / 8) + c);
       f[u] = bf16_value(__ldg(a.scales[part] + row * (D / kQ4Group) + (c >> 2)));
     }
@@ -258,9 +283,6 @@ __global__ void __launch_bounds__(kThreads) read_q4_kernel(const __grid_constant
     }
   }
 }
-
-// Appends of at most this many rows take one CTA per request and no second launch.
-constexpr int kFewRows = 17;
 
 template <typename T, int D>
 void launch_append(const Q4CacheArgs& a, int B, bool commit, cudaStream_t st) {
