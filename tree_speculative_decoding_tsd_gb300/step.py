@@ -6,7 +6,9 @@ step (draft marginals, root tokens, queries, scratch-pad K/V, target logits)
 and the persistent state (KV cache, prefix lengths) are caller tensors.
 
 ``Q8TreeVerifyStep`` is the same step over an 8-bit cache, which it can hold at a
-budget of rows (``Q8Cache`` and ``RowWeights`` are its persistent state).
+budget of rows (``Q8Cache`` and ``RowWeights`` are its persistent state);
+``Q4TreeVerifyStep`` that over a 4-bit cache (``Q4Cache``).  Every step can make the
+attention's rows from a layer's projections (``Rope``, ``rotate``, ``rotate_tree``).
 """
 
 from __future__ import annotations
@@ -15,13 +17,14 @@ import dataclasses
 
 import torch
 
-from . import (make_desc, q8_blocks, tsd_accept_commit, tsd_accept_walk,
+from . import (TSD_Q4_GROUP, make_desc, make_rope_desc, q8_blocks, tsd_accept_commit, tsd_accept_walk,
                tsd_accept_walk_workspace_size, tsd_cache_evict_q8, tsd_cache_evict_workspace_size,
-               tsd_cache_weights_q8, tsd_cache_write_q8, tsd_commit_path, tsd_commit_path_q8,
+               tsd_cache_read_q4, tsd_cache_weights_q8, tsd_cache_write_q4, tsd_cache_write_q8,
+               tsd_commit_path, tsd_commit_path_q4, tsd_commit_path_q8, tsd_qk_norm_rope,
                tsd_target_argmax, tsd_walk_commit, tsd_tree_build, tsd_tree_build_adaptive,
                tsd_tree_build_conditioned, tsd_tree_build_workspace_size, tsd_tree_verify_attn,
-               tsd_tree_verify_attn_q8, tsd_verify_q8_workspace_size, tsd_verify_workspace_size,
-               workspace)
+               tsd_tree_verify_attn_q4, tsd_tree_verify_attn_q8, tsd_verify_q4_workspace_size,
+               tsd_verify_q8_workspace_size, tsd_verify_workspace_size, workspace)
 
 
 @dataclasses.dataclass
@@ -41,6 +44,20 @@ class WalkBuffers:
     accept_rows: torch.Tensor
     bonus: torch.Tensor
     chain_id: torch.Tensor
+
+
+@dataclasses.dataclass
+class Rope:
+    """What ``rotate`` and ``rotate_tree`` need of a layer: ``turns`` [axes][rot / 2] (``rope_turns``) and the
+    norm's weights [d] (None: 1; without ``norm`` there is none)."""
+
+    turns: torch.Tensor
+    q_weight: torch.Tensor | None = None
+    k_weight: torch.Tensor | None = None
+    norm: bool = True
+    eps: float = 1e-6
+    neighbours: bool = False
+    amplitude: float = 1.0
 
 
 class TreeVerifyStep:
@@ -81,6 +98,7 @@ class TreeVerifyStep:
         # prefixes 231.9 -> 231.3 us.  overlap_argmax=False keeps the round on
         # one stream (the fused tsd_accept_commit).
         self.overlap_argmax = True if overlap_argmax is None else bool(overlap_argmax)
+        self.depths = None             # the tree's depths once per position axis, for rotate_tree
         self.side = torch.cuda.Stream(device=dev)
         self.ev_fork = torch.cuda.Event()
         self.ev_join = torch.cuda.Event()
@@ -105,6 +123,36 @@ class TreeVerifyStep:
         tsd_tree_build_conditioned(cand_p, cand_tok, cand_parent, self.D, root_tok, t.token,
                                    t.parent, t.depth, t.score, t.mask, t.is_leaf, self.err,
                                    stream)
+
+    def rotate(self, rope, q, k, v, start, offset=None, count=None, out=None, stream=None):
+        """Norm and rotation of projected rows [B][T][H][d], which may be views of a fused
+        projection: to positions start[b] + offset[a][b][t] (by default 0..T-1 on every axis: a
+        prompt).  Rows count[b].. are left out.  Returns (q, k, v), dense: ``out``, or new
+        tensors (a captured step takes ``out``)."""
+        B, T = q.shape[:2]
+        axes, half = rope.turns.shape
+        main = stream if stream is not None else torch.cuda.current_stream(q.device)
+        if out is None:
+            with torch.cuda.stream(main):
+                out = tuple(torch.empty(t.shape, dtype=t.dtype, device=t.device) for t in (q, k, v))
+        desc = make_rope_desc(B, T, self.Hq, self.Hkv, self.dk, self.dtype, 2 * half, axes,
+                              rope.neighbours, rope.norm, rope.eps, rope.amplitude)
+        tsd_qk_norm_rope(desc, q, k, v, rope.turns, *out, rope.q_weight, rope.k_weight, start, offset,
+                         count, main)
+        return out
+
+    def rotate_tree(self, rope, q, k, v, start, out=None, stream=None):
+        """``rotate`` of the rows of the tree that was built last, to start + their depth.
+        ``start`` is [B]: the prefix lengths, or the tokens seen where the cache is held at a
+        budget."""
+        axes, depth = rope.turns.shape[0], self.tree.depth[None]
+        main = stream if stream is not None else torch.cuda.current_stream(q.device)
+        if axes > 1:
+            if self.depths is None or self.depths.shape[0] != axes:
+                self.depths = depth.new_empty((axes, self.B, self.R))
+            with torch.cuda.stream(main):
+                depth = self.depths.copy_(depth.expand_as(self.depths))
+        return self.rotate(rope, q, k, v, start, depth, None, out, main)
 
     def verify(self, q, kcache, vcache, prefix_len, ktree, vtree, stream=None):
         tsd_tree_verify_attn(self.desc, q, kcache, vcache, prefix_len, ktree, vtree,
@@ -322,3 +370,98 @@ class Q8TreeVerifyStep(TreeVerifyStep):
     def for_workload(cls, w, device="cuda", **held):
         return cls(w.B, w.S, w.V, w.k, w.D, w.Hq, w.Hkv, w.dk, w.dv, w.cap, w.torch_dtype,
                    w.v_aliases_k, w.scale, device, **held)
+
+
+@dataclasses.dataclass
+class Q4Cache:
+    """Codes [B][Hkv][cap][d / 2] (uint8) and scales [B][Hkv][cap][d / 32] (bf16).  With a page
+    table: pools of pages [num_pages][Hkv][page_size][..]."""
+
+    kq: torch.Tensor
+    vq: torch.Tensor
+    kscale: torch.Tensor
+    vscale: torch.Tensor
+    page_table: torch.Tensor | None = None
+    page_size: int = 0
+
+    def paging(self):
+        return dict(page_table=self.page_table, page_size=self.page_size)
+
+    def arrays(self):
+        return self.kq, self.vq, self.kscale, self.vscale
+
+
+class Q4TreeVerifyStep(TreeVerifyStep):
+    """The step over a 4-bit cache: build -> verify -> walk -> commit, for heads of 64 or 128
+    dims (not latent ones).  With a ``Rope``, run() and capture() take the layer's projections of
+    the tree's rows and rotate them first: ``q``, ``ktree``, ``vtree`` of the step are then its
+    own buffers.  All of a round is on one stream (no ``overlap_argmax``), and its tree is
+    build()'s."""
+
+    def __init__(self, B, S, V, k, D, Hq, Hkv, dk, dv, cap, dtype, v_aliases_k, scale,
+                 device="cuda", rope=None):
+        if v_aliases_k or dk != dv or dk not in (64, 128):
+            raise ValueError(f"a 4-bit cache takes heads of 64 or 128 dims, K and V apart (dk {dk}, dv {dv})")
+        super().__init__(B, S, V, k, D, Hq, Hkv, dk, dv, cap, dtype, v_aliases_k, scale, device)
+        dev, R = self.out.device, self.R
+        self.ws_verify = workspace(tsd_verify_q4_workspace_size(self.desc), dev)
+        self.rope = rope
+        if rope is not None:
+            self.q, self.ktree, self.vtree = (torch.empty((B, R, h, dk), dtype=dtype, device=dev)
+                                              for h in (Hq, Hkv, Hkv))
+
+    def new_cache(self):
+        """An empty contiguous cache."""
+        dev, lead = self.out.device, (self.B, self.Hkv, self.cap)
+        codes, scales = (*lead, self.dk // 2), (*lead, self.dk // TSD_Q4_GROUP)
+        return Q4Cache(*(torch.zeros(codes, dtype=torch.uint8, device=dev) for _ in range(2)),
+                       *(torch.zeros(scales, dtype=torch.bfloat16, device=dev) for _ in range(2)))
+
+    def append(self, knew, vnew, new_len, cache, prefix_len, stream=None):
+        """Rows [B][T][Hkv][d], ``new_len[b]`` of them, behind the prefix (a prompt)."""
+        tsd_cache_write_q4(self.desc, knew, vnew, new_len, *cache.arrays(), prefix_len, self.err, stream,
+                           **cache.paging())
+
+    def read(self, cache, prefix_len, first, count, kout, vout, stream=None):
+        """Rows first[b] .. first[b] + count[b] - 1 of the cache to kout/vout [B][T][Hkv][d]."""
+        tsd_cache_read_q4(self.desc, *cache.arrays(), prefix_len, first, count, kout, vout, self.err,
+                          stream, **cache.paging())
+
+    def verify(self, q, cache, prefix_len, ktree, vtree, stream=None):
+        tsd_tree_verify_attn_q4(self.desc, q, *cache.arrays(), prefix_len, ktree, vtree, self.tree.mask,
+                                self.out, self.lse, self.ws_verify, self.err, stream, **cache.paging())
+
+    def commit(self, ktree, vtree, cache, prefix_len, stream=None):
+        w = self.walk
+        tsd_commit_path_q4(self.desc, self.S, ktree, vtree, w.accept_rows, w.accept_len, *cache.arrays(),
+                           prefix_len, self.err, stream, **cache.paging())
+
+    def run(self, probs, root_tok, q, cache, prefix_len, ktree, vtree, logits, start=None, stream=None):
+        """The whole step (asynchronous): build -> (rotate ->) verify -> walk -> commit.  With a
+        ``Rope``, q, ktree and vtree are projections ([B][R][H][d], also as views), turned to the
+        positions start (by default prefix_len) + depth."""
+        main = stream if stream is not None else torch.cuda.current_stream(probs.device)
+        self.build(probs, root_tok, main)
+        if self.rope is not None:
+            self.rotate_tree(self.rope, q, ktree, vtree, prefix_len if start is None else start,
+                             (self.q, self.ktree, self.vtree), main)
+            q, ktree, vtree = self.q, self.ktree, self.vtree
+        elif start is not None:
+            raise ValueError("start: needed with a Rope only")
+        self.verify(q, cache, prefix_len, ktree, vtree, main)
+        self.accept(logits, main)
+        self.commit(ktree, vtree, cache, prefix_len, main)
+
+    def accept_commit(self, *args, **kw):
+        raise NotImplementedError("the 4-bit cache takes accept() and commit()")
+
+    def capture(self, probs, root_tok, q, cache, prefix_len, ktree, vtree, logits, start=None, stream=None):
+        """Record ``run`` on the given tensors as one CUDA graph, as TreeVerifyStep.capture
+        (one round runs before the recording, behind the caller's queued work)."""
+        return self._record(probs.device, stream, lambda main: self.run(
+            probs, root_tok, q, cache, prefix_len, ktree, vtree, logits, start, main))
+
+    @classmethod
+    def for_workload(cls, w, device="cuda", rope=None):
+        return cls(w.B, w.S, w.V, w.k, w.D, w.Hq, w.Hkv, w.dk, w.dv, w.cap, w.torch_dtype,
+                   w.v_aliases_k, w.scale, device, rope)
