@@ -696,7 +696,7 @@ tsd_status tsd_tree_verify_attn_q4(const tsd_attn_desc* desc, const void* q, con
  *   pair i of the first rot dims, (y_i, y_(i + rot/2)), or with desc->neighbours
  *   (y_2i, y_(2i+1)), is turned by the angle
  *     t_i = sum over axes a of position_a * turns[a][i],
- *     position_a = start[b] + offset[a][b][t],
+ *     position_a = start[b] + offset[a][b][t]   (offset[0][b][t] where offset_axes = 1),
  *   (u, w) -> amplitude * (u cos t_i - w sin t_i, u sin t_i + w cos t_i)
  * computed in fp32 and rounded once.  Rows of v are copied.  Rows t >= count[b] are
  * neither read nor written.
@@ -710,7 +710,9 @@ tsd_status tsd_tree_verify_attn_q4(const tsd_attn_desc* desc, const void* q, con
  *            turn is 0), so that far positions keep their angle to 2^-32 turns.  A pair
  *            that does not turn with an axis has 0 there: the sections, in any order, of
  *            a model's position axes (time, height, width).
- * start      [B] int32, NULL: 0.      offset [axes][B][T] int32, NULL: 0..T-1 on each axis
+ * start      [B] int32, NULL: 0
+ * offset     [offset_axes][B][T] int32, offset_axes = axes, or 1: the same on each axis; NULL
+ *            (offset_axes unused): 0..T-1 on each axis
  * count      [B] int32, NULL: T
  * q_out, k_out, v_out  dense [B][T][H][d].  They may be q, k, v themselves where those are
  *            dense; otherwise they do not overlap the inputs.
@@ -732,8 +734,8 @@ typedef struct {
 tsd_status tsd_qk_norm_rope(const tsd_rope_desc* desc, const void* q, int64_t q_stride,
                             const void* k, int64_t k_stride, const void* v, int64_t v_stride,
                             const void* q_weight, const void* k_weight, const uint64_t* turns,
-                            const int32_t* start, const int32_t* offset, const int32_t* count,
-                            void* q_out, void* k_out, void* v_out, tsd_stream_t stream);
+                            const int32_t* start, const int32_t* offset, int offset_axes,
+                            const int32_t* count, void* q_out, void* k_out, void* v_out, tsd_stream_t stream);
 
 #ifdef __cplusplus
 }

@@ -117,13 +117,13 @@ class Setup:
 A, U, N = ctypes.c_void_p(0x10000), ctypes.c_void_p(0x10008), None
 
 
-def _call(q=A, qs=512, k=A, ks=256, v=A, vs=256, qw=A, kw=A, turns=A, start=A, offset=A, count=A, qo=A,
-          ko=A, vo=A, **kw_desc):
+def _call(q=A, qs=512, k=A, ks=256, v=A, vs=256, qw=A, kw=A, turns=A, start=A, offset=A, oa=1, count=A,
+          qo=A, ko=A, vo=A, **kw_desc):
     base = dict(B=2, T=3, Hq=4, Hkv=2, d=128, dtype=T.TSD_BF16, rot=128, neighbours=0, axes=1, norm=1,
                 eps=1e-6, amplitude=1.0)
     base.update(kw_desc)
     return T.lib.tsd_qk_norm_rope(ctypes.byref(T.tsd_rope_desc(**base)), q, qs, k, ks, v, vs, qw, kw, turns,
-                                  start, offset, count, qo, ko, vo, N)
+                                  start, offset, oa, count, qo, ko, vo, N)
 
 
 @pytest.mark.parametrize("kw", [
@@ -132,13 +132,14 @@ def _call(q=A, qs=512, k=A, ks=256, v=A, vs=256, qw=A, kw=A, turns=A, start=A, o
     dict(amplitude=NAN), dict(amplitude=INF), dict(q=N), dict(k=N), dict(q=U), dict(k=U), dict(v=U), dict(vo=N),
     dict(v=N), dict(qo=N), dict(ko=U), dict(qw=U), dict(kw=U), dict(turns=N), dict(turns=U), dict(start=U),
     dict(offset=U), dict(count=U), dict(norm=0), dict(norm=0, qw=N), dict(qs=504), dict(qs=516), dict(ks=128),
-    dict(ks=-256), dict(vs=0), dict(vs=257), dict(B=2 ** 31 - 1, T=2 ** 31 - 1)])
+    dict(ks=-256), dict(vs=0), dict(vs=257), dict(oa=0), dict(oa=2), dict(oa=2, axes=3),
+    dict(B=2 ** 31 - 1, T=2 ** 31 - 1)])
 def test_call_rejects_bad_arguments(kw):
     assert _call(**kw) == T.TSD_ERR_INVALID_ARG
 
 
 def test_call_rejects_no_descriptor():
-    assert T.lib.tsd_qk_norm_rope(N, *[A, 512] * 3, *[A] * 9, N) == T.TSD_ERR_INVALID_ARG
+    assert T.lib.tsd_qk_norm_rope(N, *[A, 512] * 3, *[A] * 5, 1, *[A] * 4, N) == T.TSD_ERR_INVALID_ARG
 
 
 def test_turns_are_fractions_of_a_turn():
@@ -202,6 +203,15 @@ def test_far_positions_keep_their_angle(far):
                 tol = 2.0 ** -20 + abs(pos) * 2.0 ** -62
                 assert abs(float(s.out[0][b, t, 1, i]) - math.cos(2 * math.pi * turn)) < tol
                 assert abs(float(s.out[0][b, t, 1, 32 + i]) - math.sin(2 * math.pi * turn)) < tol
+
+
+@gpu
+def test_one_offset_serves_all_axes():
+    s = Setup(2, 33, 8, 2, 128, axes=3)
+    s.offset = s.offset[:1].contiguous()
+    s.call()
+    s.offset = s.offset.expand(3, -1, -1).contiguous()
+    s.check()
 
 
 @gpu

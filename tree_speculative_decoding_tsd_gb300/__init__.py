@@ -164,7 +164,7 @@ def _load():
     lib.tsd_tree_verify_attn_q4.restype = I
     L = ctypes.c_int64
     lib.tsd_qk_norm_rope.argtypes = [ctypes.POINTER(tsd_rope_desc), P, L, P, L, P, L, P, P, P, P, P,
-                                     P, P, P, P, P]
+                                     I, P, P, P, P, P]
     lib.tsd_qk_norm_rope.restype = I
     lib.tsd_set_verify_path.argtypes = [I]
     lib.tsd_set_verify_path.restype = I
@@ -843,15 +843,17 @@ def _strided_rows(t, name, dt, shape, dev):
 def tsd_qk_norm_rope(desc, q, k, v, turns, q_out, k_out, v_out, q_weight=None, k_weight=None,
                      start=None, offset=None, count=None, stream=None):
     """RMS norm of every head's query and key and the position rotation; v is copied (v and
-    v_out may be None).  q, k, v [B][T][H][d] may be views of a fused projection."""
+    v_out may be None).  q, k, v [B][T][H][d] may be views of a fused projection; offset is
+    [axes][B][T], or [1][B][T] for all axes."""
     B, T, Hq, Hkv, d, axes = desc.B, desc.T, desc.Hq, desc.Hkv, desc.d, desc.axes
     dt, dev = (_attn_dtype(desc),), torch.cuda.current_device()
     rows_q, rows_k, one = (B, T, Hq, d), (B, T, Hkv, d), (B,)
+    own_axes = axes if offset is None or offset.shape[0] != 1 else 1
     _check("tsd_qk_norm_rope", _L().tsd_qk_norm_rope(
         ctypes.byref(desc), *_strided_rows(q, "q", dt, rows_q, dev),
         *_strided_rows(k, "k", dt, rows_k, dev), *_strided_rows(v, "v", dt, rows_k, dev),
         _p(q_weight, "q_weight", dt, (d,), dev), _p(k_weight, "k_weight", dt, (d,), dev),
         _p(turns, "turns", _TURNS, (axes, desc.rot // 2), dev), _p(start, "start", _I32T, one, dev),
-        _p(offset, "offset", _I32T, (axes, B, T), dev), _p(count, "count", _I32T, one, dev),
+        _p(offset, "offset", _I32T, (own_axes, B, T), dev), own_axes, _p(count, "count", _I32T, one, dev),
         _p(q_out, "q_out", dt, rows_q, dev), _p(k_out, "k_out", dt, rows_k, dev),
         _p(v_out, "v_out", dt, rows_k, dev), _raw_stream(stream, dev)))

@@ -36,7 +36,8 @@ struct RopeArgs {
   const void* weight[2];    // of Q, K; null: 1
   const uint64_t* turns;    // [axes][rot / 2]
   const int32_t* start;     // [B] or null
-  const int32_t* offset;    // [axes][B][T] or null: 0..T-1
+  const int32_t* offset;    // [axes][B][T], or [B][T] for all axes (offset_step 0), or null: 0..T-1
+  long offset_step;         // elements between two axes' offsets
   const int32_t* count;     // [B] or null: T
   int B, T, Hq, Hkv, rot, axes, norm, parts;
   float eps, amplitude;
@@ -108,7 +109,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
     const long long first = a.start != nullptr ? a.start[b] : 0;
     for (int x = 0; x < a.axes; ++x) {
       const long long pos =
-          first + (a.offset != nullptr ? a.offset[((long)x * a.B + b) * a.T + t] : t);
+          first + (a.offset != nullptr ? a.offset[x * a.offset_step + tok] : t);
       const ulonglong2* f = (const ulonglong2*)(a.turns + (long)x * half + p0);
       const ulonglong2 f0 = __ldg(f), f1 = __ldg(f + 1);
       angle[0] += (uint64_t)pos * f0.x;
@@ -204,7 +205,7 @@ extern "C" tsd_status tsd_qk_norm_rope(const tsd_rope_desc* d, const void* q, in
                                        int64_t v_stride, const void* q_weight,
                                        const void* k_weight, const uint64_t* turns,
                                        const int32_t* start, const int32_t* offset,
-                                       const int32_t* count, void* q_out, void* k_out, void* v_out,
+                                       int offset_axes, const int32_t* count, void* q_out, void* k_out, void* v_out,
                                        tsd_stream_t stream) {
   if (d == nullptr || d->B < 1 || d->T < 1 || d->Hq < 1 || d->Hkv < 1 || d->Hq > 65535 ||
       d->Hkv > 65535)
@@ -219,6 +220,7 @@ extern "C" tsd_status tsd_qk_norm_rope(const tsd_rope_desc* d, const void* q, in
       !ok_opt_ptr(k_weight) || !ok_opt_ptr(start) || !ok_opt_ptr(offset) || !ok_opt_ptr(count))
     return TSD_ERR_INVALID_ARG;
   if (d->rot > 0 && !ok_ptr(turns)) return TSD_ERR_INVALID_ARG;
+  if (offset != nullptr && offset_axes != 1 && offset_axes != d->axes) return TSD_ERR_INVALID_ARG;
   if (!d->norm && (q_weight != nullptr || k_weight != nullptr)) return TSD_ERR_INVALID_ARG;
   const int vec = d->dtype == TSD_BF16 ? 8 : 4;        // elements of 16 bytes
   const int64_t s[3] = {q_stride, k_stride, v == nullptr ? (int64_t)d->Hkv * d->d : v_stride};
@@ -232,6 +234,7 @@ extern "C" tsd_status tsd_qk_norm_rope(const tsd_rope_desc* d, const void* q, in
   a.turns = turns;
   a.start = start;
   a.offset = offset;
+  a.offset_step = offset_axes == 1 ? 0 : (long)d->B * d->T;
   a.count = count;
   a.B = d->B; a.T = d->T; a.Hq = d->Hq; a.Hkv = d->Hkv;
   a.rot = d->rot; a.axes = d->axes; a.norm = d->norm != 0;

@@ -98,7 +98,6 @@ class TreeVerifyStep:
         # prefixes 231.9 -> 231.3 us.  overlap_argmax=False keeps the round on
         # one stream (the fused tsd_accept_commit).
         self.overlap_argmax = True if overlap_argmax is None else bool(overlap_argmax)
-        self.depths = None             # the tree's depths once per position axis, for rotate_tree
         self.side = torch.cuda.Stream(device=dev)
         self.ev_fork = torch.cuda.Event()
         self.ev_join = torch.cuda.Event()
@@ -126,8 +125,8 @@ class TreeVerifyStep:
 
     def rotate(self, rope, q, k, v, start, offset=None, count=None, out=None, stream=None):
         """Norm and rotation of projected rows [B][T][H][d], which may be views of a fused
-        projection: to positions start[b] + offset[a][b][t] (by default 0..T-1 on every axis: a
-        prompt).  Rows count[b].. are left out.  Returns (q, k, v), dense: ``out``, or new
+        projection: to positions start[b] + offset[a][b][t] (one offset for all axes: [1][B][T];
+        by default 0..T-1, a prompt).  Rows count[b].. are left out.  Returns (q, k, v), dense: ``out``, or new
         tensors (a captured step takes ``out``)."""
         B, T = q.shape[:2]
         axes, half = rope.turns.shape
@@ -145,14 +144,7 @@ class TreeVerifyStep:
         """``rotate`` of the rows of the tree that was built last, to start + their depth.
         ``start`` is [B]: the prefix lengths, or the tokens seen where the cache is held at a
         budget."""
-        axes, depth = rope.turns.shape[0], self.tree.depth[None]
-        main = stream if stream is not None else torch.cuda.current_stream(q.device)
-        if axes > 1:
-            if self.depths is None or self.depths.shape[0] != axes:
-                self.depths = depth.new_empty((axes, self.B, self.R))
-            with torch.cuda.stream(main):
-                depth = self.depths.copy_(depth.expand_as(self.depths))
-        return self.rotate(rope, q, k, v, start, depth, None, out, main)
+        return self.rotate(rope, q, k, v, start, self.tree.depth[None], None, out, stream)
 
     def verify(self, q, kcache, vcache, prefix_len, ktree, vtree, stream=None):
         tsd_tree_verify_attn(self.desc, q, kcache, vcache, prefix_len, ktree, vtree,
