@@ -25,7 +25,7 @@
 // Roles (640 threads): warps 0-3 and 4-7 softmax and epilogue; warp 8 issues the products
 // with V and owns the tensor memory, warp 9 those with Q; warps 10 and 11 read the tiles'
 // scales of K and V ahead, find E and leave fp16 factors in a ring; warps 12-15 widen K,
-// 16-19 V.  Registers are dealt out anew at the start: the softmax needs 136.  mbarriers
+// 16-19 V.  Registers are dealt out anew at the start: the softmax needs 120 (with 136 for it: 399 us instead of 390 for the 65-row trees below).  mbarriers
 // order scales -> K -> S -> softmax -> O and V -> O; every wait is bounded.
 #include <type_traits>
 
@@ -45,7 +45,7 @@ constexpr int kWideThreads = kWideWarps * 32;
 constexpr int kThreads = (kWideV + kWideWarps) * 32;
 // Registers of a thread: as launched, and then of the softmax, of warps 8-11, of those that
 // widen.
-constexpr int kLaunchRegs = 96, kSoftRegs = 136, kMidRegs = 64, kWideRegs = 72;
+constexpr int kLaunchRegs = 96, kSoftRegs = 120, kMidRegs = 80, kWideRegs = 80;
 static_assert(2 * kSoftRegs + kMidRegs + 2 * kWideRegs <= 5 * kLaunchRegs, "registers of the launch");
 template <int N, bool kMore> __device__ __forceinline__ void set_registers() {
   if (kMore) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(N));
@@ -149,23 +149,29 @@ struct Share4 {
   }
   // chunks of the rows below nvalid of the tile whose codes start at `src`
   __device__ __forceinline__ void load(uint4 (&w)[kCount], const uint8_t* src, int nvalid) const {
+    const uint8_t* const p = src + (first * kBlockRows + row) * (D / 2) + grp * 16;
+    if (nvalid >= kKeys) {
+#pragma unroll
+      for (int i = 0; i < kCount; ++i) w[i] = ld_stream(p + i * (kPair * kBlockRows * (D / 2)));
+      return;
+    }
 #pragma unroll
     for (int i = 0; i < kCount; ++i) {
       const int r = (first + i * kPair) * kBlockRows + row;
       w[i] = make_uint4(0u, 0u, 0u, 0u);
-      if (r < nvalid) w[i] = ld_stream(src + (long)r * (D / 2) + grp * 16);
+      if (r < nvalid) w[i] = ld_stream(p + i * (kPair * kBlockRows * (D / 2)));
     }
   }
   // factors: fp16 s 2^(15 - E) [128][NG], 0 for rows that are not there
   __device__ __forceinline__ void widen(const uint4 (&w)[kCount], const uint8_t* factors,
                                         uint8_t* stage) const {
+    const uint8_t* const fp = factors + ((first * kBlockRows + row) * NG + grp) * 2;
+    uint8_t* const base = stage + first * (kBlockRows * 128) + dst;
 #pragma unroll
     for (int i = 0; i < kCount; ++i) {
-      const int blk = first + i * kPair;
-      const int r = blk * kBlockRows + row;
-      const uint32_t f = *(const uint16_t*)(factors + (r * NG + grp) * 2);
+      const uint32_t f = *(const uint16_t*)(fp + i * (kPair * kBlockRows * NG * 2));
       const uint32_t f0 = f | f << 16, f1 = hmul2(f0, 0x2c002c00u), z = hmul2(f0, 0x80088008u);
-      uint8_t* const d = stage + blk * (kBlockRows * 128) + dst;
+      uint8_t* const d = base + i * (kPair * kBlockRows * 128);
       const uint32_t in[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
@@ -201,6 +207,19 @@ struct Scales {
   static constexpr int NW = D / 64;                // words of a row
   uint32_t w[4][NW];
   __device__ __forceinline__ void load(const uint8_t* src, int nvalid, int lane) {
+    if (nvalid >= kKeys) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if constexpr (NW == 2) {
+          const uint2 v = __ldg((const uint2*)src + lane + 32 * i);
+          w[i][0] = v.x;
+          w[i][NW - 1] = v.y;
+        } else {
+          w[i][0] = __ldg((const uint32_t*)src + lane + 32 * i);
+        }
+      }
+      return;
+    }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int r = lane + 32 * i;
@@ -223,11 +242,20 @@ struct Scales {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int x = 0; x < NW; ++x) {
-        const uint32_t lo = w[i][x] & 0x7fffu, hi = w[i][x] >> 16 & 0x7fffu;
-        top = max(top, max(lo < 0x7f80u ? lo : 0u, hi < 0x7f80u ? hi : 0u));
-      }
-    return min(max((int)(__reduce_max_sync(kFull, top) >> 7) - 126, kQ4MinExp), kQ4MaxExp);
+      for (int x = 0; x < NW; ++x) top = __vmaxu2(top, w[i][x] & 0x7fff7fffu);
+    top = __reduce_max_sync(kFull, max(top & 0xffffu, top >> 16));
+    if (top >= 0x7f80u) {                          // (not the scales that are not finite)
+      top = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int x = 0; x < NW; ++x) {
+          const uint32_t lo = w[i][x] & 0x7fffu, hi = w[i][x] >> 16 & 0x7fffu;
+          top = max(top, max(lo < 0x7f80u ? lo : 0u, hi < 0x7f80u ? hi : 0u));
+        }
+      top = __reduce_max_sync(kFull, top);
+    }
+    return min(max((int)(top >> 7) - 126, kQ4MinExp), kQ4MaxExp);
   }
   // s 2^(15 - E) in fp16: exact down to 2^-29 2^E
   __device__ __forceinline__ void store(uint8_t* dst, int E, int lane) const {
