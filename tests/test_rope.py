@@ -152,9 +152,13 @@ def test_turns_are_fractions_of_a_turn():
         off = (Fraction(bits) - want) % 2 ** 64
         assert min(off, 2 ** 64 - off) < 2
     assert T.rope_turns([0.5, 0.25]).shape == (1, 2)
-    for bad in (NAN, INF):
+    for bad in (NAN, INF, 2.0 ** 20, -1e30):
         with pytest.raises(ValueError):
             T.rope_turns([0.5, bad])
+    for f in (2.0 ** 20 - 1, -5e-324, 2.0 ** -300, 1e5 / 3):
+        want, bits = Fraction(f) / (2 * pi) * 2 ** 64, int(T.rope_turns([f])[0, 0])
+        off = (Fraction(bits) - want) % 2 ** 64
+        assert min(off, 2 ** 64 - off) < 2
 
 
 # ---------------------------------------------------------------- results --

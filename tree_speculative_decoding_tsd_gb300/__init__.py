@@ -25,8 +25,8 @@ the path it finds).
 from __future__ import annotations
 
 import ctypes
+import math
 import os
-from fractions import Fraction
 
 import torch
 
@@ -801,18 +801,24 @@ def make_rope_desc(B, T, Hq, Hkv, d, dtype, rot=None, axes=1, neighbours=False, 
                          d if rot is None else rot, int(neighbours), axes, int(norm), eps, amplitude)
 
 
+# 2^192 / (2 pi), to the nearest whole number
+_PER_RADIAN = 999031769477504631556283515717616693813654938713089696784
+
+
 def rope_turns(freq, device=None):
     """``turns`` of tsd_qk_norm_rope from radians per position, [rot / 2] or [axes][rot / 2]
-    (float64): int64 with the bits of the fraction of a turn times 2^64.  A host computation;
-    ``device`` is that of freq by default."""
+    (float64, below 2^20 in magnitude): int64 with the bits of the fraction of a turn times 2^64.
+    A host computation in whole numbers; ``device`` is that of freq by default."""
     freq = torch.as_tensor(freq, dtype=torch.float64)
     device = freq.device if device is None else device
-    two_pi = Fraction("6.28318530717958647692528676655900576839433879875021164194989")
-    whole = 1 << 64
-    if not bool(freq.isfinite().all()):
-        raise ValueError("freq: a frequency is not finite")
-    bits = [round(Fraction(x) / two_pi * whole) % whole for x in freq.flatten().tolist()]
-    bits = [b - whole if b >> 63 else b for b in bits]
+    bits = []
+    for x in freq.flatten().tolist():
+        if not abs(x) < 1 << 20:
+            raise ValueError(f"freq: {x} radians per position, expected less than 2^20")
+        m, e = math.frexp(x)                       # x = m 2^53 2^(e - 53)
+        shift = 128 + 53 - e
+        b = ((int(m * (1 << 53)) * _PER_RADIAN >> shift - 1) + 1 >> 1) & (1 << 64) - 1
+        bits.append(b - (1 << 64) if b >> 63 else b)
     return torch.tensor(bits, dtype=torch.int64).view(-1, freq.shape[-1]).to(device)
 
 
