@@ -126,50 +126,52 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
     }
   }
 
-  const int heads = a.Hq + a.Hkv, all = heads + (a.in[2] != nullptr ? a.Hkv : 0);
-  const int steps = (all + kRows - 1) / kRows, per = (steps + a.parts - 1) / a.parts;
+  // Steps of kRows heads: those of the queries, of the keys, of the values; this warp's run of
+  // them.  The weights stay in registers through a kind's heads.
+  const int steps_q = (a.Hq + kRows - 1) / kRows, steps_k = (a.Hkv + kRows - 1) / kRows;
+  const int steps = steps_q + steps_k + (a.in[2] != nullptr ? steps_k : 0);
+  const int per = (steps + a.parts - 1) / a.parts;
   const int s0 = part * per, s1 = min(steps, s0 + per);
-  for (int s = s0; s < s1; s += kRopeUnroll) {
-    Four x0[kRopeUnroll], x1[kRopeUnroll];
-    T* dst[kRopeUnroll];
-    int kind[kRopeUnroll];
+
+  auto turn_heads = [&](int kind, int H, int first, int last) {
+    if (first >= last) return;
+    const T* const src = (const T*)a.in[kind] + tok * a.stride[kind];
+    T* const dst = (T*)a.out[kind] + tok * H * D;
+    float w[8];
 #pragma unroll
-    for (int u = 0; u < kRopeUnroll; ++u) {
-      const int head = min((s + u) * kRows + sub, all - 1);
-      const int k = head < a.Hq ? 0 : head < heads ? 1 : 2;
-      const int h = head - (k == 0 ? 0 : k == 1 ? a.Hq : heads), H = k == 0 ? a.Hq : a.Hkv;
-      const T* src = (const T*)a.in[k] + tok * a.stride[k] + (long)h * D;
-      dst[u] = (T*)a.out[k] + (tok * H + h) * D;
-      kind[u] = (s + u) * kRows + sub < all && s + u < s1 ? k : 3;
-      x0[u].load(src + o0);
-      x1[u].load(src + o1);
+    for (int i = 0; i < 8; ++i) w[i] = 1.f;
+    if (a.weight[kind] != nullptr) {
+      Four w0, w1;
+      w0.load((const T*)a.weight[kind] + o0);
+      w1.load((const T*)a.weight[kind] + o1);
+      w0.get(w);
+      w1.get(w + 4);
     }
+    for (int s = first; s < last; s += kRopeUnroll) {
+      Four x0[kRopeUnroll], x1[kRopeUnroll];
 #pragma unroll
-    for (int u = 0; u < kRopeUnroll; ++u) {
-      float x[8], sum = 0.f;
-      x0[u].get(x);
-      x1[u].get(x + 4);
-      if (a.norm) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) sum = fmaf(x[i], x[i], sum);
-#pragma unroll
-        for (int o = VR / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
-        const float f = rsqrtf(sum * (1.f / D) + a.eps);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] *= f;
+      for (int u = 0; u < kRopeUnroll; ++u) {
+        const int h = min((s + u) * kRows + sub, H - 1);
+        x0[u].load(src + h * D + o0);
+        x1[u].load(src + h * D + o1);
       }
-      if (kind[u] == 3) continue;
-      if (kind[u] < 2) {
-        if (a.weight[kind[u]] != nullptr) {
-          Four w0, w1;
-          float w[8];
-          w0.load((const T*)a.weight[kind[u]] + o0);
-          w1.load((const T*)a.weight[kind[u]] + o1);
-          w0.get(w);
-          w1.get(w + 4);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) x[i] *= w[i];
+      for (int u = 0; u < kRopeUnroll; ++u) {
+        const int h = (s + u) * kRows + sub;
+        float x[8], f = 1.f;
+        x0[u].get(x);
+        x1[u].get(x + 4);
+        if (a.norm) {
+          float sum = 0.f;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) sum = fmaf(x[i], x[i], sum);
+#pragma unroll
+          for (int o = VR / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
+          f = rsqrtf(sum * (1.f / D) + a.eps);
         }
+        if (s + u >= last || h >= H) continue;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] *= f * w[i];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           float& p = kNear ? x[2 * i] : x[i];
@@ -180,9 +182,32 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
         }
         x0[u].set(x);
         x1[u].set(x + 4);
+        x0[u].store(dst + h * D + o0);
+        x1[u].store(dst + h * D + o1);
       }
-      x0[u].store(dst[u] + o0);
-      x1[u].store(dst[u] + o1);
+    }
+  };
+  turn_heads(0, a.Hq, s0, min(s1, steps_q));
+  turn_heads(1, a.Hkv, max(s0 - steps_q, 0), min(s1 - steps_q, steps_k));
+  if (a.in[2] != nullptr) {
+    const T* const src = (const T*)a.in[2] + tok * a.stride[2];
+    T* const dst = (T*)a.out[2] + tok * a.Hkv * D;
+    const int first = max(s0 - steps_q - steps_k, 0), last = s1 - steps_q - steps_k;
+    for (int s = first; s < last; s += kRopeUnroll) {
+      Four x0[kRopeUnroll], x1[kRopeUnroll];
+#pragma unroll
+      for (int u = 0; u < kRopeUnroll; ++u) {
+        const int h = min((s + u) * kRows + sub, a.Hkv - 1);
+        x0[u].load(src + h * D + 8 * c);
+        x1[u].load(src + h * D + 8 * c + 4);
+      }
+#pragma unroll
+      for (int u = 0; u < kRopeUnroll; ++u) {
+        const int h = (s + u) * kRows + sub;
+        if (s + u >= last || h >= a.Hkv) continue;
+        x0[u].store(dst + h * D + 8 * c);
+        x1[u].store(dst + h * D + 8 * c + 4);
+      }
     }
   }
 }
@@ -242,8 +267,9 @@ extern "C" tsd_status tsd_qk_norm_rope(const tsd_rope_desc* d, const void* q, in
   a.amplitude = d->amplitude;
   for (int i = 0; i < 3; ++i) a.stride[i] = s[i];
   // runs of a token's heads: as many warps as the GPU holds, or one per batch of loads
-  const int rows = 32 / (d->d / 8), heads = d->Hq + d->Hkv + (v != nullptr ? d->Hkv : 0);
-  const long most = ceil_div(ceil_div(heads, rows), kRopeUnroll), tokens = (long)d->B * d->T;
+  const int rows = 32 / (d->d / 8);
+  const long steps = ceil_div(d->Hq, rows) + ceil_div(d->Hkv, rows) * (v != nullptr ? 2 : 1);
+  const long most = ceil_div(steps, kRopeUnroll), tokens = (long)d->B * d->T;
   const long want = ceil_div(152L * 48, tokens);
   a.parts = (int)(want < 1 ? 1 : want > most ? most : want);
   if (ceil_div(tokens * a.parts, kRopeThreads / 32) > 0x7fffffffl) return TSD_ERR_INVALID_ARG;
