@@ -214,18 +214,28 @@ append_q4_kernel(const __grid_constant__ Q4CacheArgs a) {
   }
 }
 
-__device__ __forceinline__ void store8(float* p, const float (&x)[8]) {
-  ((float4*)p)[0] = make_float4(x[0], x[1], x[2], x[3]);
-  ((float4*)p)[1] = make_float4(x[4], x[5], x[6], x[7]);
+// The eight values of a word, times the scale, to p.
+__device__ __forceinline__ void store_word(float* p, uint32_t w, uint32_t scale) {
+  float x[8];
+  q4_values(w, x);
+  const float f = bf16_value(scale);
+  ((float4*)p)[0] = make_float4(x[0] * f, x[1] * f, x[2] * f, x[3] * f);
+  ((float4*)p)[1] = make_float4(x[4] * f, x[5] * f, x[6] * f, x[7] * f);
 }
-__device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&x)[8]) {
-  uint32_t w[4];
+// bf16: a code in the lowest bits of 128 is 128 + c, less 136 exactly c - 8; the product with the
+// scale is rounded once, as that in fp32 (which is exact) would be.
+__device__ __forceinline__ void store_word(__nv_bfloat16* p, uint32_t w, uint32_t scale) {
+  const uint32_t f = scale | scale << 16;
+  uint32_t out[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const __nv_bfloat162 v = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
-    w[i] = *reinterpret_cast<const uint32_t*>(&v);
+    const uint32_t c = ((w >> (4 * i)) & 0x000f000fu) | 0x43004300u;
+    const __nv_bfloat162 x = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&c),
+                                     __bfloat162bfloat162(__ushort_as_bfloat16(0x4308)));
+    const __nv_bfloat162 y = __hmul2(x, *reinterpret_cast<const __nv_bfloat162*>(&f));
+    out[i] = *reinterpret_cast<const uint32_t*>(&y);
   }
-  *(uint4*)p = make_uint4(w[0], w[1], w[2], w[3]);
+  *(uint4*)p = make_uint4(out[0], out[1], out[2], out[3]);
 }
 
 // Positions first..first+count-1 to rows 0.. of [B][rows][Hkv][d]: as the write, the
@@ -264,22 +274,17 @@ __global__ void __launch_bounds__(kThreads) read_q4_kernel(const __grid_constant
   constexpr int kPerHead = kTokens / kBatch;
   for (int i = warp; i < a.map.Hkv * kPerHead; i += kThreads / 32) {
     const int h = i / kPerHead, t = t0 + (i % kPerHead) * kBatch + sub;
-    uint32_t w[kUnroll];
-    float f[kUnroll];
+    uint32_t w[kUnroll], f[kUnroll];
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
       const long row = rows[min(t + u * kRows, n - 1) - t0] + h * apart;
       w[u] = __ldg(a.codes[part] + row * (D / 8) + c);
-      f[u] = bf16_value(__ldg(a.scales[part] + row * (D / kQ4Group) + (c >> 2)));
+      f[u] = __ldg(a.scales[part] + row * (D / kQ4Group) + (c >> 2));
     }
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
       if (t + u * kRows >= n) break;
-      float x[8];
-      q4_values(w[u], x);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] *= f[u];
-      store8(dst + ((long)(t + u * kRows) * a.map.Hkv + h) * D + c * 8, x);
+      store_word(dst + ((long)(t + u * kRows) * a.map.Hkv + h) * D + c * 8, w[u], f[u]);
     }
   }
 }
