@@ -9,8 +9,11 @@
 //   c  = clamp(round(x / s), -8, 7) + 8;  read back: (c - 8) s
 //
 // Writing, two lanes hold a group, sixteen elements (two words of codes) each: a scale and
-// its inverse cost as much as eight elements do, and a shuffle joins two ranges.  Reading, a
-// lane has eight elements.
+// its inverse cost as much as eight elements do, and a shuffle joins two ranges (eight elements
+// a lane: 40 instead of 28 us for the prompt below).  Reading, a lane has eight elements.
+//
+// 4 x up to 8192 rows of 8 heads: written in 28 us (22 by the bytes; issue slots 62%, memory 59%),
+// read back in 25; 32 requests of 1k to 4k rows read from pages in 56 us (47 by the bytes).
 #include <cuda_bf16.h>
 #include <math.h>
 
@@ -35,9 +38,12 @@ struct Q4CacheArgs {
   int rows, S;             // rows per request of src or dst; path length bound
 };
 
+// Threads, positions of a CTA and rows of a lane requested together (write, read).  Prompt and its
+// read-back / read of 32 requests in a graph: 60 / 63 us; four rows 73 / 87, one 60 / 67; 128
+// threads 62 / 66, 512 threads 69 / 79; 64 positions 65 / 69.
 constexpr int kThreads = 256;
-constexpr int kTokens = 32;                    // positions of a CTA (write, read)
-constexpr int kUnroll = 2;                     // rows of a lane requested together
+constexpr int kTokens = 32;
+constexpr int kUnroll = 2;
 constexpr int kPathThreads = 512;
 // Appends of at most this many rows (those of a path) take one CTA per request and no second
 // launch.

@@ -7,9 +7,9 @@
 // Widening is what this path has to do cheaply: codes go from shared memory straight into
 // the operand registers of mma.sync (tcgen05 takes operands from shared or tensor memory,
 // so that every widened element would be written and read once more; the products of
-// few columns are far from binding here).  A warp works alone on chunks of 16 keys, which it
-// copies itself, several ahead, into a ring of its own: no barrier between the first
-// chunk and the last.
+// few columns are far from binding here: 23% of the tensor pipe).  A warp works alone on
+// chunks of 32 keys, which it copies itself, a chunk ahead, into a ring of its own: no barrier
+// between the first chunk and the last.
 //
 // Numbers.
 //   K   a word's masked halves are fp16 numbers as they stand, c * 2^-24 or c * 2^-20
@@ -19,12 +19,24 @@
 //   Q   fp16 times a power of two of its row: exact for elements down to 2^-29 of the
 //       row's largest, off by 2^-35 of it at most below.
 //   V   fp16, one fused multiply-add: (c - 8) s 2^(-E - 9), E the exponent above the chunk's
-//       largest scale: 2^-12, or 2^-25 (2^-18 of the chunk's largest value) where that is more.
+//       largest scale: 2^-12, or 2^-25 (2^-15 of the chunk's largest scale) where that is more.
 //   P   fp16: 2^(x + E - m), m a running bound of x + E over the warp's keys (raised
-//       where a chunk passes it by 8): 2^-12, and steps of 2^-24, 2^-32 of the largest at most.
+//       where a chunk passes it by 8): 2^-12, and steps of 2^-24.
 //   scratch rows: fp32 on the CUDA cores, a warp per packed row, while the first chunks are
 //       under way.
 // Each warp's sum, bound and output are joined at the end, in fp32.
+//
+// What bounds it.  One token of 16 requests of 32 heads over 20k to 32k keys: 118 us, 4.1 TB/s
+// (72 us by the bytes).  The copies alone, the arithmetic left out, take 93 us in the same
+// graph that takes 121 with it: 17 us of that are launch, set-up, joint and merge.  Two
+// CTAs per SM, so that one's start and end lie beside the other's chunks (one of 16 warps: 142
+// us); the scheduler serves the older of the two first.  Within the loop the issue slots are
+// three quarters full (585 instructions for 32 keys, 258 of them on the ALU, which takes one in
+// two cycles).  Tried and dropped: chunks of 16 keys with rings of two to five (131 us, 45
+// instead of 42 for 32 requests over 1k to 4k), three CTAs of 80 registers (144 us), the work
+// dealt out evenly over one CTA per slot by the requests' lengths (120 us, but 80 instead of 56
+// us for 200 requests below 900 keys and 77 instead of 56 for 32 of 4 rows: a CTA then starts
+// and ends once per request).
 #include "tsd_host.h"
 #include "tsd_q4.cuh"
 #include "tsd_q4_attn.cuh"
@@ -565,6 +577,8 @@ void launch_few(const Q8AttnArgs& a, const Q8Plan& p, cudaStream_t st) {
 
 }  // namespace
 
+// Up to eight packed rows, two CTAs per SM; more need the registers of one (two of 128: 69 instead
+// of 56 us for 16 rows of 32 requests over 1k to 4k keys).
 void launch_q4_few(const Q8AttnArgs& a, const Q8Plan& p, int D, cudaStream_t st) {
   if (D == 128) {
     if (a.M <= 8) launch_few<128, 1, 2, 2>(a, p, st);

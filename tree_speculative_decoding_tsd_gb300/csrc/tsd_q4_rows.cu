@@ -25,8 +25,22 @@
 // Roles (640 threads): warps 0-3 and 4-7 softmax and epilogue; warp 8 issues the products
 // with V and owns the tensor memory, warp 9 those with Q; warps 10 and 11 read the tiles'
 // scales of K and V ahead, find E and leave fp16 factors in a ring; warps 12-15 widen K,
-// 16-19 V.  Registers are dealt out anew at the start: the softmax needs 120 (with 136 for it: 399 us instead of 390 for the 65-row trees below).  mbarriers
-// order scales -> K -> S -> softmax -> O and V -> O; every wait is bounded.
+// 16-19 V.  Registers are dealt out anew at the start: the softmax needs 120.  mbarriers
+// order scales -> K -> S -> softmax -> O and V -> O; every wait is bounded.  Of four widening
+// warps two take the even tiles and two the odd ones: a tile's way through them is mostly
+// latency (all four on each tile: 421 instead of 390 us for the trees below; one group of five
+// warps for K and V in turn: 589).
+//
+// What bounds it: the way of a tile through a softmax warp, about 2000 cycles; K and V lie
+// widened 2500 cycles before they are used.  Left out one at a time, 392 us become 331 without
+// the widening, 380 without the scales, 373 without the maxima, 374 without the exponentials, 300
+// without all of it: instructions and shared memory (64 KB stored and 64 KB read by products per
+// tile, half of its rate) are shared by all roles.  The tensor core needs 1280 cycles a tile.
+// 8 x 65 rows of 32 heads over 32k keys: 386 us, 723 TFLOP/s; 32 x 33 rows over 1k to 4k: 112 us
+// (q8's kernel, whose K needs no widening: 330 and 101); 8 x 32 rows over 32k: 149 us.
+// Tried and dropped: more of the widening on the scheduler that has no softmax warp (three of
+// four have rows: 472 us), the last few rows behind a group of 128 in a launch of tsd_q4_few.cu
+// (384 and 121 us, but 46 instead of 36 us for a 65-row tree of one request over 2k keys).
 #include <type_traits>
 
 #include "tsd_common.cuh"
@@ -44,7 +58,7 @@ constexpr int kPair = 2;                        // of them work on one tile, the
 constexpr int kWideThreads = kWideWarps * 32;
 constexpr int kThreads = (kWideV + kWideWarps) * 32;
 // Registers of a thread: as launched, and then of the softmax, of warps 8-11, of those that
-// widen.
+// widen.  (136, 64, 72: 399 us instead of 390 for the 65-row trees.)
 constexpr int kLaunchRegs = 96, kSoftRegs = 120, kMidRegs = 80, kWideRegs = 80;
 static_assert(2 * kSoftRegs + kMidRegs + 2 * kWideRegs <= 5 * kLaunchRegs, "registers of the launch");
 template <int N, bool kMore> __device__ __forceinline__ void set_registers() {
