@@ -14,8 +14,8 @@
 // Numbers.
 //   K   a word's masked halves are fp16 numbers as they stand, c * 2^-24 or c * 2^-20
 //       (tsd_q4.cuh), exact; columns of Q carry the factor between the two.  Each group
-//       of 32 dims has its own product, begun at -8 sum(q): (c - 8) . q in fp32, then times
-//       the group's scale: no rounding.
+//       of 32 dims has its own product c . q in fp32, then times the group's scale; -8 sum(q)
+//       times the scales comes from a small product (sums in three bf16 terms): fp32 all the way.
 //   Q   fp16 times a power of two of its row: exact for elements down to 2^-29 of the
 //       row's largest, off by 2^-35 of it at most below.
 //   V   fp16, one fused multiply-add: (c - 8) s 2^(-E - 9), E the exponent above the chunk's
@@ -64,8 +64,8 @@ struct FewLayout {
   static constexpr uint32_t off_tree = ring > joint ? ring : joint;     // float [8 NT][D]
   static constexpr uint32_t off_ml = off_tree + NT * 8 * D * 4;         // float2 [W + 1][8 NT]
   static constexpr uint32_t off_q = off_ml + (W + 1) * NT * 8 * 8;      // uint4 [NT][NG][32]: B operands
-  static constexpr uint32_t off_qs = off_q + NT * NG * 32 * 16;         // float4 [NT][NG][4]: their start
-  static constexpr uint32_t off_c2 = off_qs + NT * NG * 4 * 16;         // float [8 NT]: factor of the scores
+  static constexpr uint32_t off_qs = off_q + NT * NG * 32 * 16;         // float [NT][NG][8]: -8 times their sums
+  static constexpr uint32_t off_c2 = off_qs + NT * NG * 8 * 4;          // float [8 NT]: factor of the scores
   static constexpr uint32_t off_req = off_c2 + NT * 8 * 4;              // request, its length; a huge row
   static constexpr uint32_t total = off_req + 16;
   static_assert(stage % 16 == 0, "whole units");
@@ -86,6 +86,14 @@ __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a
       "{%0,%1,%2,%3};\n"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// D = A.B, bf16.
+__device__ __forceinline__ void mma_16816_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                               uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%10,%10,%10,%10};\n"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 // An 8 x 8 matrix of 16-bit elements, a row on four lanes, transposed.
 __device__ __forceinline__ uint32_t transposed(uint32_t x) {
@@ -191,8 +199,7 @@ q4_few_kernel(const __grid_constant__ Q8AttnArgs a) {
 
   // ------------------------------------------------------ Q as the B operand
   // lane (g, t): column g, and of each group j the dims of word 4 j + t.  In shared memory,
-  // for all warps, and with it what each group's product begins with: -8 * 2^-24 sum(q) of
-  // columns 2 t and 2 t + 1, for both halves of the rows.
+  // for all warps, and with it -8 * 2^-24 sum(q) of each group.
   uint4* const s_q = (uint4*)(smem + L::off_q);
   float* const s_qs = (float*)(smem + L::off_qs);
   float* const s_c2 = (float*)(smem + L::off_c2);
@@ -233,8 +240,7 @@ q4_few_kernel(const __grid_constant__ Q8AttnArgs a) {
 #pragma unroll
     for (int o = 1; o < 4; o <<= 1) sum += __shfl_xor_sync(kFull, sum, o);
     sum *= -8.f * 5.9604644775390625e-08f;
-    // column g: of lanes t = g / 2, its place there g % 2, twice
-    if (t < 2) s_qs[(warp * 4 + (g >> 1)) * 4 + (g & 1) + 2 * t] = sum;
+    if (t == 0) s_qs[warp * 8 + g] = sum;
   }
 
   // --------------------------------------------------------- scratch rows
@@ -313,6 +319,22 @@ q4_few_kernel(const __grid_constant__ Q8AttnArgs a) {
 #pragma unroll
     for (int x = 0; x < 2; ++x) c2[nt][x] = s_c2[nt * 8 + 2 * t + x] * (huge ? 1.f : 1024.f);
   }
+  // The codes' offset as a product of its own: scales of a key (NG of them, bf16, as they are)
+  // times the sums, each in three bf16 terms (24 bits): its rows are (term, group).
+  uint32_t ob[NT][2];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int k = 2 * t + 8 * i, term = k / NG;  // (a pair is of one term)
+      float x[2];
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        x[y] = term < 3 ? s_qs[(nt * NG + k % NG + y) * 8 + g] : 0.f;
+        for (int z = 0; z < term && z < 2; ++z) x[y] -= __bfloat162float(__float2bfloat16_rn(x[y]));
+      }
+      ob[nt][i] = pack_bf16x2(x[0], x[1]);
+    }
   const uint8_t* const mine = smem + warp * (S * L::stage);
   int slot = 0;
 #pragma unroll 1
@@ -341,14 +363,17 @@ q4_few_kernel(const __grid_constant__ Q8AttnArgs a) {
       }
     }
 #pragma unroll
+    for (int h = 0; h < H; ++h) {
+      const uint32_t a0 = NG == 4 && (t & 1) ? ks[2 * h][NG / 2 - 1] : ks[2 * h][0];
+      const uint32_t a1 = NG == 4 && (t & 1) ? ks[2 * h + 1][NG / 2 - 1] : ks[2 * h + 1][0];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) mma_16816_bf16(s[nt][h], a0, a1, a0, a1, ob[nt][0], ob[nt][1]);
+    }
+#pragma unroll
     for (int j = 0; j < NG; ++j) {
       uint4 q[NT];
-      float4 start[NT];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        q[nt] = s_q[(nt * NG + j) * 32 + lane];
-        start[nt] = *(const float4*)(s_qs + ((nt * NG + j) * 4 + t) * 4);
-      }
+      for (int nt = 0; nt < NT; ++nt) q[nt] = s_q[(nt * NG + j) * 32 + lane];
 #pragma unroll
       for (int h = 0; h < H; ++h) {
         const uint32_t w0 = *(const uint32_t*)(kl + 16 * h * L::row + 16 * j);
@@ -359,14 +384,14 @@ q4_few_kernel(const __grid_constant__ Q8AttnArgs a) {
         const float s1 = __uint_as_float(j & 1 ? k1w & 0xffff0000u : k1w << 16);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          float d[4] = {start[nt].x, start[nt].y, start[nt].z, start[nt].w};
+          float d[4] = {0.f, 0.f, 0.f, 0.f};
           mma_16816(d, w0 & 0x000f000fu, w1 & 0x000f000fu, w0 & 0x00f000f0u, w1 & 0x00f000f0u, q[nt].x, q[nt].y);
           mma_16816(d, h0 & 0x000f000fu, h1 & 0x000f000fu, h0 & 0x00f000f0u, h1 & 0x00f000f0u, q[nt].z, q[nt].w);
           float* const r = s[nt][h];
-          r[0] = j == 0 ? d[0] * s0 : fmaf(d[0], s0, r[0]);
-          r[1] = j == 0 ? d[1] * s0 : fmaf(d[1], s0, r[1]);
-          r[2] = j == 0 ? d[2] * s1 : fmaf(d[2], s1, r[2]);
-          r[3] = j == 0 ? d[3] * s1 : fmaf(d[3], s1, r[3]);
+          r[0] = fmaf(d[0], s0, r[0]);
+          r[1] = fmaf(d[1], s0, r[1]);
+          r[2] = fmaf(d[2], s1, r[2]);
+          r[3] = fmaf(d[3], s1, r[3]);
         }
       }
     }
