@@ -47,6 +47,32 @@ struct Q4Keys {
   }
 };
 
+// Modelled time of a call with nine to sixteen packed rows, splits of `per` tiles (128 keys), one
+// CTA of twelve warps per SM or three of four; the unit is an SM's time for a tile.  A CTA's
+// set-up and end cost six tiles, or three (twice that of 64 dims); one of four warps alone on its
+// SM takes 1.4 times as long.  It is the sum for caches that are full and for caches three quarters full on average,
+// whose CTAs fill one another's gaps.
+// (Measured with one of 12 / three of 4, us: 4 rows of 1 request over 32k keys 27 / 30, of 32 over
+// 1k to 4k 49 / 61, of 8 over 32k 107 / 91, of 200 below 900 125 / 87.)
+double few_cost(long units, long tiles, long per, bool small, int D) {
+  constexpr double kSms = 152, kAlone = 1.4, kFill = 0.75;
+  const double ends = (small ? 3 : 6) * (128 / D), room = small ? 3 : 1;
+  const long n = ceil_div(tiles, per), full = units * n, slots = small ? 456 : 152;
+  auto round = [&](double deep) {                  // of CTAs that start together, so many per SM
+    return small ? (deep > kAlone ? deep : kAlone) * (per + ends) + 4 : deep * (per + ends);
+  };
+  double cost = full / slots * room * (per + ends);
+  if (full % slots) cost += round((double)ceil_div(full % slots, 152));
+  const double some = n == 1 ? units : units * (kFill * n + 1 - kFill);
+  if (full <= slots || some * 1.1 <= slots) {
+    const double deep = n == 1 ? (double)ceil_div(full, 152) : 1.15 * some / kSms;
+    cost += round(deep < 1 ? 1 : deep > room ? room : deep);
+  } else {
+    cost += (units * tiles * kFill + some * ends) / kSms + (n == 1 ? 0.1 : 0.5) * (per + ends);
+  }
+  return cost + (n > 1 ? 12 : 0);                  // (the merge, in both)
+}
+
 Q8Plan plan_q4(const tsd_attn_desc& d) {
   Q8Plan p{};
   const int M = d.R * (d.Hq / d.Hkv);
@@ -57,14 +83,23 @@ Q8Plan plan_q4(const tsd_attn_desc& d) {
     p.part_bytes = few ? 4 : 2;
     p.nrg = few ? 1 : (int)ceil_div(M, 128);
     p.rb = (int)ceil_div(M, p.nrg);
-    // The split count minimises the modelled time of requests that fill the cache: waves of
-    // CTAs times (tiles of 128 keys + a CTA's set-up and end), and the merge.
-    const long slots = 152L * (few && M <= 8 ? 2 : 1), ends = few ? 6 : 4, merge = few ? 6 : 5;
+    // The split count minimises a modelled time: that above, or that of requests that fill the
+    // cache: waves of CTAs times (tiles of 128 keys + a CTA's set-up and end), and the merge.
+    const bool eight = few && M <= 8;
+    const long slots = 152L * (eight ? 2 : 1), ends = few ? 6 : 4, merge = few ? 6 : 5;
     const long units = heads * p.nrg, tiles = ceil_div(d.cap, 128);
     const long lo = ceil_div(tiles, 256), hi = lo > 64 ? lo : tiles < 64 ? tiles : 64;
-    long best = -1, best_per = tiles;
+    double best = -1;
+    long best_per = tiles;
     for (long n = lo; n <= hi; ++n) {
       const long per = ceil_div(tiles, n);
+      if (few && !eight) {
+        for (int small = 0; small < 2; ++small) {
+          const double cost = few_cost(units, tiles, per, small, d.dk);
+          if (best < 0 || cost < best) { best = cost; best_per = per; p.small_ctas = small; }
+        }
+        continue;
+      }
       const long cost = ceil_div(units * ceil_div(tiles, per), slots) * (per + ends) + (per < tiles ? merge : 0);
       if (best < 0 || cost < best) { best = cost; best_per = per; }
     }
@@ -73,7 +108,7 @@ Q8Plan plan_q4(const tsd_attn_desc& d) {
     p.tree_split = !few && p.nsplit > 1 && best_per <= 8 ? 1 : 0;
     p.nsplit += p.tree_split;
     // More CTAs than run at once and a request's keys in one: the longest requests first.
-    p.by_length = p.nsplit == 1 && d.B > 1 && d.B <= 64 && units > slots;
+    p.by_length = p.nsplit == 1 && d.B > 1 && d.B <= 64 && units > slots * (p.small_ctas ? 3 : 1);
   } else {
     p.path = kQ8Simt;
     p.part_bytes = 4;

@@ -46,10 +46,9 @@ namespace tsd {
 namespace {
 
 constexpr float kNone = -3.4e38f;                  // a bound before the first key
-constexpr int kWarps = 8;
 constexpr int H = 2, kChunk = 16 * H;              // keys of a chunk: two halves, a product's rows each
 
-template <int D, int NT, int S>
+template <int D, int NT, int S, int W>
 struct FewLayout {
   static constexpr int NG = D / kQ4Group;
   // A row's codes, padded so that neither way of reading (K: a unit of eight rows; V: a run
@@ -57,7 +56,6 @@ struct FewLayout {
   static constexpr uint32_t row = D / 2 + 16;
   static constexpr uint32_t codes = kChunk * row, scales = kChunk * NG * 2;
   static constexpr uint32_t stage = 2 * codes + 2 * scales;
-  static constexpr int W = kWarps;
   static constexpr uint32_t ring = W * S * stage;
   static constexpr int pitch = D + 4;              // floats of a row in the joint
   static constexpr uint32_t joint = W * NT * 8 * pitch * 4;
@@ -112,11 +110,10 @@ __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
   return d;
 }
 
-template <int D, int NT, int S, int kCtas>
-__global__ void __launch_bounds__(kWarps * 32, kCtas)
+template <int D, int NT, int S, int W, int kCtas>
+__global__ void __launch_bounds__(W * 32, kCtas)
 q4_few_kernel(const __grid_constant__ Q8AttnArgs a) {
-  using L = FewLayout<D, NT, S>;
-  constexpr int W = kWarps;
+  using L = FewLayout<D, NT, S, W>;
   constexpr int NG = L::NG, NW = D / 64;           // groups; words of V per lane and key
   extern __shared__ __align__(128) uint8_t smem[];
   grid_dependency_sync();
@@ -203,9 +200,9 @@ q4_few_kernel(const __grid_constant__ Q8AttnArgs a) {
   uint4* const s_q = (uint4*)(smem + L::off_q);
   float* const s_qs = (float*)(smem + L::off_qs);
   float* const s_c2 = (float*)(smem + L::off_c2);
-  static_assert(NT * NG <= W, "a warp per group");
-  if (warp < NT * NG) {
-    const int nt = warp / NG, j = warp % NG, n = nt * 8 + g;
+#pragma unroll 1
+  for (int i0 = warp; i0 < NT * NG; i0 += W) {     // a warp per group
+    const int nt = i0 / NG, j = i0 % NG, n = nt * 8 + g;
     uint4 w = make_uint4(0u, 0u, 0u, 0u);
     uint32_t top = 0;
     if (n < a.M) {
@@ -236,11 +233,11 @@ q4_few_kernel(const __grid_constant__ Q8AttnArgs a) {
       const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&q[i]));
       sum = fmaf(i & 1 ? 16.f : 1.f, y.x + y.y, sum);
     }
-    s_q[warp * 32 + lane] = make_uint4(q[0], q[1], q[2], q[3]);
+    s_q[i0 * 32 + lane] = make_uint4(q[0], q[1], q[2], q[3]);
 #pragma unroll
     for (int o = 1; o < 4; o <<= 1) sum += __shfl_xor_sync(kFull, sum, o);
     sum *= -8.f * 5.9604644775390625e-08f;
-    if (t == 0) s_qs[warp * 8 + g] = sum;
+    if (t == 0) s_qs[i0 * 8 + g] = sum;
   }
 
   // --------------------------------------------------------- scratch rows
@@ -592,12 +589,12 @@ q4_few_kernel(const __grid_constant__ Q8AttnArgs a) {
   }
 }
 
-template <int D, int NT, int S, int kCtas>
+template <int D, int NT, int S, int W, int kCtas>
 void launch_few(const Q8AttnArgs& a, const Q8Plan& p, cudaStream_t st) {
-  const uint32_t smem = FewLayout<D, NT, S>::total;
-  const auto kern = q4_few_kernel<D, NT, S, kCtas>;
+  const uint32_t smem = FewLayout<D, NT, S, W>::total;
+  const auto kern = q4_few_kernel<D, NT, S, W, kCtas>;
   cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  launch(kern, dim3(a.map.Hkv, p.nsplit, a.B), dim3(kWarps * 32), smem, st, a);
+  launch(kern, dim3(a.map.Hkv, p.nsplit, a.B), dim3(W * 32), smem, st, a);
 }
 
 }  // namespace
@@ -606,11 +603,13 @@ void launch_few(const Q8AttnArgs& a, const Q8Plan& p, cudaStream_t st) {
 // of 56 us for 16 rows of 32 requests over 1k to 4k keys).
 void launch_q4_few(const Q8AttnArgs& a, const Q8Plan& p, int D, cudaStream_t st) {
   if (D == 128) {
-    if (a.M <= 8) launch_few<128, 1, 2, 2>(a, p, st);
-    else launch_few<128, 2, 3, 1>(a, p, st);
+    if (a.M <= 8) launch_few<128, 1, 2, 8, 2>(a, p, st);
+    else if (p.small_ctas) launch_few<128, 2, 2, 4, 3>(a, p, st);
+    else launch_few<128, 2, 2, 12, 1>(a, p, st);
   } else {
-    if (a.M <= 8) launch_few<64, 1, 3, 2>(a, p, st);
-    else launch_few<64, 2, 3, 1>(a, p, st);
+    if (a.M <= 8) launch_few<64, 1, 3, 8, 2>(a, p, st);
+    else if (p.small_ctas) launch_few<64, 2, 3, 4, 3>(a, p, st);
+    else launch_few<64, 2, 3, 12, 1>(a, p, st);
   }
 }
 

@@ -43,6 +43,7 @@ struct Q8Plan {
   int by_length;              // requests are taken longest first
   int tree_split;             // the tree rows are a split of their own, behind the prefix splits
   int part_bytes;             // element size of a split's output: 4 (fp32) or 2 (fp16)
+  int small_ctas;             // (4-bit cache, few rows) several small CTAs per SM
   size_t ws_bytes;
 };
 
