@@ -47,28 +47,35 @@ struct Q4Keys {
   }
 };
 
-// Modelled time of a call with nine to sixteen packed rows, splits of `per` tiles (128 keys), one
-// CTA of twelve warps per SM or three of four; the unit is an SM's time for a tile.  A CTA's
-// set-up and end cost six tiles, or three (twice that of 64 dims); one of four warps alone on its
-// SM takes 1.4 times as long.  It is the sum for caches that are full and for caches three quarters full on average,
-// whose CTAs fill one another's gaps.
-// (Measured with one of 12 / three of 4, us: 4 rows of 1 request over 32k keys 27 / 30, of 32 over
-// 1k to 4k 49 / 61, of 8 over 32k 107 / 91, of 200 below 900 125 / 87.)
-double few_cost(long units, long tiles, long per, bool small, int D) {
-  constexpr double kSms = 152, kAlone = 1.4, kFill = 0.75;
-  const double ends = (small ? 3 : 6) * (128 / D), room = small ? 3 : 1;
-  const long n = ceil_div(tiles, per), full = units * n, slots = small ? 456 : 152;
-  auto round = [&](double deep) {                  // of CTAs that start together, so many per SM
-    return small ? (deep > kAlone ? deep : kAlone) * (per + ends) + 4 : deep * (per + ends);
-  };
-  double cost = full / slots * room * (per + ends);
+// Modelled time of the few path with splits of `per` tiles (128 keys); the unit is an SM's time
+// for a tile.  An SM holds `room` CTAs: one of twelve warps or three of four for nine to sixteen
+// packed rows, two of eight or four of four for fewer.  A CTA's set-up and end cost `ends` tiles
+// (twice that of 64 dims); CTAs of four warps start later, and one that is alone on its SM takes
+// `alone` times as long.  It is the sum for caches that are full and for caches three quarters
+// full on average, whose CTAs fill one another's gaps.
+// (Measured with larger / smaller CTAs, us.  Four rows of 4 heads each: 1 request over 32k keys 27
+// and 30, 32 over 1k to 4k 49 and 61, 8 over 32k 107 and 91, 200 below 900 125 and 87.  One row:
+// 1 over 2k 13 and 14, 64 over 1k to 8k 83 and 89, 200 below 900 54 and 44.)
+struct FewShape {
+  int room;
+  double ends, alone, start;
+};
+constexpr FewShape kFewShapes[2][2] = {{{2, 5, 1.1, 0}, {4, 3, 1.35, 4}}, {{1, 6, 1, 0}, {3, 3, 1.4, 4}}};
+
+double few_cost(long units, long tiles, long per, int D, const FewShape& s) {
+  constexpr double kSms = 152, kFill = 0.75;
+  const long n = ceil_div(tiles, per), full = units * n, slots = 152L * s.room;
+  const double ends = s.ends * (128 / D), whole = per + ends;
+  // CTAs that start together, so many per SM
+  auto round = [&](double deep) { return (deep > s.alone ? deep : s.alone) * whole + s.start; };
+  double cost = full / slots * s.room * whole;
   if (full % slots) cost += round((double)ceil_div(full % slots, 152));
   const double some = n == 1 ? units : units * (kFill * n + 1 - kFill);
   if (full <= slots || some * 1.1 <= slots) {
     const double deep = n == 1 ? (double)ceil_div(full, 152) : 1.15 * some / kSms;
-    cost += round(deep < 1 ? 1 : deep > room ? room : deep);
+    cost += round(deep > s.room ? s.room : deep);
   } else {
-    cost += (units * tiles * kFill + some * ends) / kSms + (n == 1 ? 0.1 : 0.5) * (per + ends);
+    cost += (units * tiles * kFill + some * ends) / kSms + (n == 1 ? 0.1 : 0.5) * whole;
   }
   return cost + (n > 1 ? 12 : 0);                  // (the merge, in both)
 }
@@ -83,32 +90,37 @@ Q8Plan plan_q4(const tsd_attn_desc& d) {
     p.part_bytes = few ? 4 : 2;
     p.nrg = few ? 1 : (int)ceil_div(M, 128);
     p.rb = (int)ceil_div(M, p.nrg);
-    // The split count minimises a modelled time: that above, or that of requests that fill the
-    // cache: waves of CTAs times (tiles of 128 keys + a CTA's set-up and end), and the merge.
+    // The split count minimises a modelled time.  Nine to sixteen rows: that above.  Others: that
+    // of requests that fill the cache, waves of CTAs times (tiles of 128 keys + a CTA's set-up
+    // and end), and the merge.
     const bool eight = few && M <= 8;
     const long slots = 152L * (eight ? 2 : 1), ends = few ? 6 : 4, merge = few ? 6 : 5;
     const long units = heads * p.nrg, tiles = ceil_div(d.cap, 128);
     const long lo = ceil_div(tiles, 256), hi = lo > 64 ? lo : tiles < 64 ? tiles : 64;
+    const FewShape* const shapes = kFewShapes[eight ? 0 : 1];
     double best = -1;
     long best_per = tiles;
     for (long n = lo; n <= hi; ++n) {
       const long per = ceil_div(tiles, n);
       if (few && !eight) {
         for (int small = 0; small < 2; ++small) {
-          const double cost = few_cost(units, tiles, per, small, d.dk);
+          const double cost = few_cost(units, tiles, per, d.dk, shapes[small]);
           if (best < 0 || cost < best) { best = cost; best_per = per; p.small_ctas = small; }
         }
-        continue;
+      } else {
+        const double cost = ceil_div(units * ceil_div(tiles, per), slots) * (per + ends) + (per < tiles ? merge : 0);
+        if (best < 0 || cost < best) { best = cost; best_per = per; }
       }
-      const long cost = ceil_div(units * ceil_div(tiles, per), slots) * (per + ends) + (per < tiles ? merge : 0);
-      if (best < 0 || cost < best) { best = cost; best_per = per; }
     }
+    // Up to eight rows: the smaller CTAs for many short caches.
+    if (eight && best_per == tiles)
+      p.small_ctas = few_cost(units, tiles, tiles, d.dk, shapes[1]) < few_cost(units, tiles, tiles, d.dk, shapes[0]);
     p.split_len = (int)best_per * 128;
     p.nsplit = (int)ceil_div(d.cap, p.split_len);
     p.tree_split = !few && p.nsplit > 1 && best_per <= 8 ? 1 : 0;
     p.nsplit += p.tree_split;
     // More CTAs than run at once and a request's keys in one: the longest requests first.
-    p.by_length = p.nsplit == 1 && d.B > 1 && d.B <= 64 && units > slots * (p.small_ctas ? 3 : 1);
+    p.by_length = p.nsplit == 1 && d.B > 1 && d.B <= 64 && units > (few ? 152L * shapes[p.small_ctas].room : slots);
   } else {
     p.path = kQ8Simt;
     p.part_bytes = 4;

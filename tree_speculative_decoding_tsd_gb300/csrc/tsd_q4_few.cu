@@ -599,17 +599,16 @@ void launch_few(const Q8AttnArgs& a, const Q8Plan& p, cudaStream_t st) {
 
 }  // namespace
 
-// Up to eight packed rows, two CTAs per SM; more need the registers of one (two of 128: 69 instead
-// of 56 us for 16 rows of 32 requests over 1k to 4k keys).
+// Up to eight packed rows, 16 warps of 128 registers per SM; more need 168 (two CTAs of eight warps
+// with 128: 69 instead of 50 us for 16 rows of 32 requests over 1k to 4k keys).
 void launch_q4_few(const Q8AttnArgs& a, const Q8Plan& p, int D, cudaStream_t st) {
+  const bool small = p.small_ctas;
   if (D == 128) {
-    if (a.M <= 8) launch_few<128, 1, 2, 8, 2>(a, p, st);
-    else if (p.small_ctas) launch_few<128, 2, 2, 4, 3>(a, p, st);
-    else launch_few<128, 2, 2, 12, 1>(a, p, st);
+    if (a.M <= 8) small ? launch_few<128, 1, 2, 4, 4>(a, p, st) : launch_few<128, 1, 2, 8, 2>(a, p, st);
+    else small ? launch_few<128, 2, 2, 4, 3>(a, p, st) : launch_few<128, 2, 2, 12, 1>(a, p, st);
   } else {
-    if (a.M <= 8) launch_few<64, 1, 3, 8, 2>(a, p, st);
-    else if (p.small_ctas) launch_few<64, 2, 3, 4, 3>(a, p, st);
-    else launch_few<64, 2, 3, 12, 1>(a, p, st);
+    if (a.M <= 8) small ? launch_few<64, 1, 3, 4, 4>(a, p, st) : launch_few<64, 1, 3, 8, 2>(a, p, st);
+    else small ? launch_few<64, 2, 3, 4, 3>(a, p, st) : launch_few<64, 2, 3, 12, 1>(a, p, st);
   }
 }
 
