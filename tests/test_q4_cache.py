@@ -516,6 +516,53 @@ def test_rows_written_are_read_back(kind):
             assert ((g - w).square().mean().sqrt() < 0.12 * w.square().mean().sqrt())
 
 
+@gpu
+def test_writes_and_reads_on_streams_and_in_graphs():
+    """A write and the read of its rows, on two streams at once, then captured and replayed."""
+    sets = [Setup("gqa", 3, 1, [5, 0, 260], extra=400, page=128, seed=50),
+            Setup("narrow", 2, 1, [129, 70], extra=400, dtype=torch.float32, seed=51)]
+    Tn = 37
+    streams = [torch.cuda.Stream() for _ in sets]
+    work = []
+    for s in sets:
+        n = torch.tensor([Tn, 9, 20][:s.B], dtype=torch.int32, device=DEV)
+        work.append((s.normal(s.B, Tn, s.Hkv, s.d), s.normal(s.B, Tn, s.Hkv, s.d), n, torch.empty_like(n),
+                     [torch.zeros(s.B, Tn, s.Hkv, s.d, dtype=s.dt, device=DEV) for _ in range(2)]))
+
+    def turn(s, x, y, n, first, out, stream=None):
+        with torch.cuda.stream(stream or torch.cuda.current_stream()):
+            first.copy_(s.plen)
+            T.tsd_cache_write_q4(s.desc, x, y, n, *s.arrays(), s.plen, s.err, stream, **s.paging)
+            T.tsd_cache_read_q4(s.desc, *s.arrays(), s.plen, first, n, *out, s.err, stream, **s.paging)
+
+    def check(s, x, y, n, first, out):
+        assert int(s.err) == 0
+        for b in range(s.B):
+            for got, new in zip(out, (x, y)):
+                c, f = quantise(new[b, :int(n[b])].double())
+                want = ((c - 8).double() * f.repeat_interleave(G, -1)).to(s.dt)
+                assert torch.equal(got[b, :int(n[b])], want.view(-1, s.Hkv, s.d))
+
+    torch.cuda.synchronize()
+    for _ in range(4):
+        for s, w, st in zip(sets, work, streams):
+            turn(s, *w, st)
+    torch.cuda.synchronize()
+    for s, w in zip(sets, work):
+        check(s, *w)
+        assert s.plen.tolist() == [p + 4 * int(k) for p, k in zip(s.lens, w[2])]
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            turn(s, *w)
+        for _ in range(3):
+            w[0].copy_(s.normal(*w[0].shape))
+            w[1].copy_(s.normal(*w[1].shape))
+            graph.replay()
+            torch.cuda.synchronize()
+            check(s, *w)
+        assert s.plen.tolist() == [p + 7 * int(k) for p, k in zip(s.lens, w[2])]
+
+
 # -------------------------------------------------------------- attention --
 
 ATTN = [("gqa", 3, 1, [2048, 700, 5], {}), ("gqa", 2, 1, [4100], {}), ("gqa", 2, 4, [1300, 129], {}),
@@ -536,6 +583,17 @@ ATTN = [("gqa", 3, 1, [2048, 700, 5], {}), ("gqa", 2, 1, [4100], {}), ("gqa", 2,
 def test_attention_matches_plain(kind, B, R, lens, kw):
     s = Setup(kind, B, R, lens, seed=len(lens) + R, **kw)
     s.check_attn(*s.attn())
+    assert int(s.err) == 0
+
+
+@gpu
+@pytest.mark.parametrize("kind,B,R,page", [("gqa", 200, 1, 0), ("gqa", 150, 4, 128), ("gqa", 64, 4, 0),
+                                           ("gqa", 64, 1, 128), ("narrow", 400, 1, 128), ("narrow", 400, 2, 0),
+                                           ("gqa", 150, 33, 128)])
+def test_attention_of_many_short_requests(kind, B, R, page):
+    s = Setup(kind, B, R, [300, 0, 127, 1, 260, 33, 64, 129, 17], page=page, seed=40)
+    some = [0, 1, 2, 3, 4, 5, 6, 7, 8, B // 2, B - 2, B - 1]
+    s.check_attn(*s.attn(), requests=some, heads=[0, s.Hkv - 1])
     assert int(s.err) == 0
 
 
