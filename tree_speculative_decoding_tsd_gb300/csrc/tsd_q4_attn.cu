@@ -47,22 +47,24 @@ struct Q4Keys {
   }
 };
 
-// Modelled time of the few path with splits of `per` tiles (128 keys); the unit is an SM's time
-// for a tile.  An SM holds `room` CTAs: one of twelve warps or three of four for nine to sixteen
-// packed rows, two of eight or four of four for fewer.  A CTA's set-up and end cost `ends` tiles
-// (twice that of 64 dims); CTAs of four warps start later, and one that is alone on its SM takes
-// `alone` times as long.  It is the sum for caches that are full and for caches three quarters
-// full on average, whose CTAs fill one another's gaps.
+// Modelled time of a tensor-core path with splits of `per` tiles (128 keys); the unit is an SM's
+// time for a tile.  An SM holds `room` CTAs: one of the rows path; one of twelve warps or three of
+// four for nine to sixteen packed rows; two of eight or four of four for fewer.  A CTA's set-up
+// and end cost `ends` tiles (twice that of 64 dims); CTAs of four warps start later, and one that
+// is alone on its SM takes `alone` times as long.  It is the sum for caches that are full and for
+// caches three quarters full on average, whose CTAs fill one another's gaps, the longest requests
+// first where each has one split.
 // (Measured with larger / smaller CTAs, us.  Four rows of 4 heads each: 1 request over 32k keys 27
 // and 30, 32 over 1k to 4k 49 and 61, 8 over 32k 107 and 91, 200 below 900 125 and 87.  One row:
 // 1 over 2k 13 and 14, 64 over 1k to 8k 83 and 89, 200 below 900 54 and 44.)
-struct FewShape {
+struct CtaShape {
   int room;
   double ends, alone, start;
 };
-constexpr FewShape kFewShapes[2][2] = {{{2, 5, 1.1, 0}, {4, 3, 1.35, 4}}, {{1, 6, 1, 0}, {3, 3, 1.4, 4}}};
+constexpr CtaShape kFewShapes[2][2] = {{{2, 5, 1.1, 0}, {4, 3, 1.35, 4}}, {{1, 6, 1, 0}, {3, 3, 1.4, 4}}};
+constexpr CtaShape kRowsShape{1, 5, 1, 0};
 
-double few_cost(long units, long tiles, long per, int D, const FewShape& s) {
+double split_cost(long units, long tiles, long per, int D, const CtaShape& s) {
   constexpr double kSms = 152, kFill = 0.75;
   const long n = ceil_div(tiles, per), full = units * n, slots = 152L * s.room;
   const double ends = s.ends * (128 / D), whole = per + ends;
@@ -90,37 +92,31 @@ Q8Plan plan_q4(const tsd_attn_desc& d) {
     p.part_bytes = few ? 4 : 2;
     p.nrg = few ? 1 : (int)ceil_div(M, 128);
     p.rb = (int)ceil_div(M, p.nrg);
-    // The split count minimises a modelled time.  Nine to sixteen rows: that above.  Others: that
-    // of requests that fill the cache, waves of CTAs times (tiles of 128 keys + a CTA's set-up
-    // and end), and the merge.
+    // The split count minimises a modelled time: that above, and for up to eight rows that of
+    // requests that fill the cache, waves of CTAs times (tiles + 6), and the merge.
     const bool eight = few && M <= 8;
-    const long slots = 152L * (eight ? 2 : 1), ends = few ? 6 : 4, merge = few ? 6 : 5;
     const long units = heads * p.nrg, tiles = ceil_div(d.cap, 128);
     const long lo = ceil_div(tiles, 256), hi = lo > 64 ? lo : tiles < 64 ? tiles : 64;
-    const FewShape* const shapes = kFewShapes[eight ? 0 : 1];
+    const CtaShape* const shapes = few ? kFewShapes[eight ? 0 : 1] : &kRowsShape;
     double best = -1;
     long best_per = tiles;
     for (long n = lo; n <= hi; ++n) {
       const long per = ceil_div(tiles, n);
-      if (few && !eight) {
-        for (int small = 0; small < 2; ++small) {
-          const double cost = few_cost(units, tiles, per, d.dk, shapes[small]);
-          if (best < 0 || cost < best) { best = cost; best_per = per; p.small_ctas = small; }
-        }
-      } else {
-        const double cost = ceil_div(units * ceil_div(tiles, per), slots) * (per + ends) + (per < tiles ? merge : 0);
-        if (best < 0 || cost < best) { best = cost; best_per = per; }
+      for (int small = 0; small < (few && !eight ? 2 : 1); ++small) {
+        const double cost = eight ? ceil_div(units * ceil_div(tiles, per), 304) * (per + 6) + (per < tiles ? 6 : 0)
+                                  : split_cost(units, tiles, per, d.dk, shapes[small]);
+        if (best < 0 || cost < best) { best = cost; best_per = per; p.small_ctas = small; }
       }
     }
     // Up to eight rows: the smaller CTAs for many short caches.
     if (eight && best_per == tiles)
-      p.small_ctas = few_cost(units, tiles, tiles, d.dk, shapes[1]) < few_cost(units, tiles, tiles, d.dk, shapes[0]);
+      p.small_ctas = split_cost(units, tiles, tiles, d.dk, shapes[1]) < split_cost(units, tiles, tiles, d.dk, shapes[0]);
     p.split_len = (int)best_per * 128;
     p.nsplit = (int)ceil_div(d.cap, p.split_len);
     p.tree_split = !few && p.nsplit > 1 && best_per <= 8 ? 1 : 0;
     p.nsplit += p.tree_split;
     // More CTAs than run at once and a request's keys in one: the longest requests first.
-    p.by_length = p.nsplit == 1 && d.B > 1 && d.B <= 64 && units > (few ? 152L * shapes[p.small_ctas].room : slots);
+    p.by_length = p.nsplit == 1 && d.B > 1 && d.B <= 64 && units > 152L * shapes[p.small_ctas].room;
   } else {
     p.path = kQ8Simt;
     p.part_bytes = 4;
