@@ -587,6 +587,95 @@ def test_attention_matches_plain(kind, B, R, lens, kw):
 
 
 @gpu
+@pytest.mark.parametrize("kind,B,R,lens,page", [
+    ("gqa", 3, 33, [700, 129, 64], 128), ("gqa", 1, 65, [1000], 0), ("narrow", 2, 65, [333, 1], 0),
+    ("narrow", 2, 9, [2000, 65], 256), ("wide", 1, 65, [500], 128), ("wide", 2, 2, [63, 900], 0),
+    ("one", 2, 65, [300, 0], 0), ("one", 2, 17, [130, 64], 128), ("one", 3, 1, [5000, 1, 64], 0),
+    ("odd", 2, 6, [333, 20], 0), ("wide64", 2, 4, [640, 15], 0), ("gqa", 60, 1, [65, 200, 511, 1, 90], 128)])
+def test_attention_of_fp32_matches_plain(kind, B, R, lens, page):
+    """In the bounds of check_attn, q and scratch keys off by 2^-22 each are four of the 16 spare
+    steps of 2^-23 of a score; the exponential's 2^-22, a weight's 2^-23 and a scratch value's
+    2^-22 lie within 2^-20."""
+    s = Setup(kind, B, R, lens, page=page, dtype=torch.float32, seed=60 + R)
+    s.check_attn(*s.attn())
+    assert int(s.err) == 0
+
+
+@gpu
+@pytest.mark.parametrize("kind,R", [("gqa", 1), ("gqa", 5), ("gqa", 17), ("narrow", 4), ("one", 65)])
+@pytest.mark.parametrize("power", [-112, -70, -40, 40, 80])
+def test_attention_of_very_small_and_large_fp32_values(kind, R, power):
+    s = Setup(kind, 2, R, [700, 40], dtype=torch.float32, seed=61)
+    f = 2.0 ** power
+    if power > -100:
+        s.vs *= f
+        s.vt *= f
+        s.check_attn(*s.attn())
+    s = Setup(kind, 2, R, [700, 40], dtype=torch.float32, seed=62)
+    s.ks /= f
+    s.kt /= f
+    s.q *= f
+    s.check_attn(*s.attn())
+    s = Setup(kind, 2, R, [700, 40], dtype=torch.float32, seed=63, spread=40)
+    s.check_attn(*s.attn())
+
+
+@gpu
+@pytest.mark.parametrize("kind,R", [("gqa", 1), ("gqa", 4), ("gqa", 20), ("narrow", 2), ("narrow", 12)])
+def test_attention_of_fp32_with_late_large_scores(kind, R):
+    s = Setup(kind, 2, R, [1500, 333], dtype=torch.float32, seed=64)
+    ramp = torch.exp2(torch.linspace(-3, 5, s.rows, device=DEV)).bfloat16()
+    s.ks *= ramp[:, None]
+    s.vs *= ramp.flip(0)[:, None]
+    s.check_attn(*s.attn())
+
+
+@gpu
+@pytest.mark.parametrize("kind,R,page", [("gqa", 1, 0), ("gqa", 4, 128), ("narrow", 9, 0), ("gqa", 20, 128),
+                                         ("one", 65, 0)])
+def test_attention_of_fp32_leaves_out_what_no_row_sees(kind, R, page):
+    s = Setup(kind, 4, R, [0, 100, 129, 240], page=page, dtype=torch.float32, seed=65)
+    for b in range(4):
+        for p in range(s.lens[b], s.cap):
+            pg, at = (b, p) if s.table is None else (int(s.table[b, p // page]), p % page)
+            s.ks[pg, :, at], s.vs[pg, :, at] = NAN, INF
+    if R > 2:
+        s.set_masks([[m & ~1 for m in row] for row in s.masks])
+        s.kt[:, 1], s.vt[:, 1] = NAN, INF
+    out, lse = s.attn()
+    assert out.isfinite().all() and lse.isfinite().all()
+    s.check_attn(out, lse)
+
+
+@gpu
+@pytest.mark.parametrize("R", [1, 5, 20])
+def test_attention_of_fp32_reports_pages_and_replays(R):
+    s = Setup("gqa", 3, R, [300, 500, 200], page=128, dtype=torch.float32, seed=66)
+    want, _ = s.attn()
+    good = s.table.clone()
+    s.table[1, 2] = s.k.shape[0]
+    s.table[0, 3] = -1                              # not needed
+    out, lse = s.attn()
+    assert int(s.err) == T.TSD_DEV_ERR_BAD_PAGE | 1
+    s.check_attn(out, lse, requests=[0, 2])
+    s.table.copy_(good)
+    s.err.zero_()
+    ws = T.workspace(T.tsd_verify_q4_workspace_size(s.desc))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        s.attn_into(out, lse, ws)
+    out.fill_(7)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want) and int(s.err) == 0
+    s.plen.copy_(torch.tensor([128, 0, 1], dtype=torch.int32))
+    s.lens = [128, 0, 1]
+    graph.replay()
+    torch.cuda.synchronize()
+    s.check_attn(out, lse)
+
+
+@gpu
 @pytest.mark.parametrize("kind,B,R,page", [("gqa", 200, 1, 0), ("gqa", 150, 4, 128), ("gqa", 64, 4, 0),
                                            ("gqa", 64, 1, 128), ("narrow", 400, 1, 128), ("narrow", 400, 2, 0),
                                            ("gqa", 150, 33, 128)])

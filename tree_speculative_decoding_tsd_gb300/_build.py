@@ -26,7 +26,7 @@ SOURCES = ["tsd_api.cu", "tsd_tree_build.cu", "tsd_verify.cu", "tsd_verify_mma.c
            "tsd_commit.cu", "tsd_q8_write.cu", "tsd_q8_attn.cu", "tsd_q8_tc.cu", "tsd_q8_few.cu", "tsd_q8_latent.cu",
            "tsd_weights.cu",
            "tsd_weights_tc.cu", "tsd_weights_latent.cu", "tsd_evict.cu", "tsd_q4_cache.cu",
-           "tsd_q4_attn.cu", "tsd_q4_few.cu", "tsd_q4_rows.cu", "tsd_rope.cu"]
+           "tsd_q4_attn.cu", "tsd_q4_few.cu", "tsd_q4_f32.cu", "tsd_q4_rows.cu", "tsd_rope.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
               "--expt-relaxed-constexpr", "-I", INCLUDE, "-I", CSRC]

@@ -12,41 +12,6 @@
 namespace tsd {
 namespace {
 
-// Four keys of the 4-bit cache, for tsd_simt_attn.cuh: a lane's four dims are half of the
-// codes of a word.
-template <int D>
-struct Q4Keys {
-  static constexpr int kDk = D, kDv = D;
-  static constexpr bool kAlias = false;
-  static __device__ __forceinline__ void values(uint32_t w, float f, int lane, float (&x)[4]) {
-    w >>= 8 * (lane & 1);
-    x[0] = ((int)(w & 15u) - 8) * f;
-    x[1] = ((int)(w >> 16 & 15u) - 8) * f;
-    x[2] = ((int)(w >> 4 & 15u) - 8) * f;
-    x[3] = ((int)(w >> 20 & 15u) - 8) * f;
-  }
-  static __device__ __forceinline__ void read(const Q8AttnArgs& a, int, int, int, long row0, int live,
-                                              int lane, float (&k)[kSimtKeys][1][4],
-                                              float (&v)[kSimtKeys][1][4]) {
-    uint32_t kw[kSimtKeys], vw[kSimtKeys];
-    uint16_t ks[kSimtKeys], vs[kSimtKeys];
-#pragma unroll
-    for (int u = 0; u < kSimtKeys; ++u) {
-      const bool there = u < live && lane < D / 4;
-      const long w = (row0 + u) * (D / 8) + (lane >> 1), s = (row0 + u) * (D / kQ4Group) + (lane >> 3);
-      kw[u] = there ? __ldg((const uint32_t*)a.kc + w) : 0u;
-      vw[u] = there ? __ldg((const uint32_t*)a.vc + w) : 0u;
-      ks[u] = there ? __ldg((const uint16_t*)a.ke + s) : (uint16_t)0;
-      vs[u] = there ? __ldg((const uint16_t*)a.ve + s) : (uint16_t)0;
-    }
-#pragma unroll
-    for (int u = 0; u < kSimtKeys; ++u) {
-      values(kw[u], bf16_value(ks[u]), lane, k[u][0]);
-      values(vw[u], bf16_value(vs[u]), lane, v[u][0]);
-    }
-  }
-};
-
 // Modelled time of a tensor-core path with splits of `per` tiles (128 keys); the unit is an SM's
 // time for a tile.  An SM holds `room` CTAs: one of the rows path; one of twelve warps or three of
 // four for nine to sixteen packed rows; two of eight or four of four for fewer.  A CTA's set-up
@@ -118,27 +83,25 @@ Q8Plan plan_q4(const tsd_attn_desc& d) {
     // More CTAs than run at once and a request's keys in one: the longest requests first.
     p.by_length = p.nsplit == 1 && d.B > 1 && d.B <= 64 && units > 152L * shapes[p.small_ctas].room;
   } else {
-    p.path = kQ8Simt;
+    p.path = kQ4F32;
     p.part_bytes = 4;
-    p.rb = M <= 4 ? 4 : 8;
-    p.nrg = (int)ceil_div(M, p.rb);
-    // about four CTAs per SM over the whole batch, splits of at least 64 keys
-    long ns = ceil_div(152L * 4, heads * p.nrg);
-    const long most = ceil_div(d.cap, 64);
-    if (ns > most) ns = most;
-    p.split_len = (int)ceil_div(ceil_div(d.cap, ns), 64) * 64;
+    p.nrg = (int)ceil_div(M, 64);
+    p.rb = (int)ceil_div(M, p.nrg);
+    // As many splits of whole tiles (64 keys), up to 64, as give an SM two CTAs; the scratch rows
+    // are a split of their own where they are much of one.  (4 rows of 4 requests over 1k to 4k
+    // keys, 3, 6, 12, 24 splits: 69, 48, 34, 40 us; 17 rows of one over 2k: 63, 42, 39, 40, and
+    // with the scratch rows in the last split 81, 48, 46, 49.)
+    const long tiles = ceil_div(d.cap, 64), most = 304 / (heads * p.nrg);
+    const long n = most < 1 ? 1 : most > 64 ? 64 : most, per = ceil_div(tiles, n);
+    p.split_len = (int)per * 64;
     p.nsplit = (int)ceil_div(d.cap, p.split_len);
+    p.tree_split = p.nsplit > 1 && per <= 12 ? 1 : 0;
+    p.nsplit += p.tree_split;
   }
   p.ws_bytes = p.nsplit > 1 ? (size_t)d.B * d.Hq * d.R * p.nsplit *
                                   (d.dv * (size_t)p.part_bytes + sizeof(float2))
                             : 0;
   return p;
-}
-
-template <int D>
-void launch_simt_q4(const Q8AttnArgs& a, const Q8Plan& p, cudaStream_t st) {
-  if (p.rb == 8) launch_simt<float, 8, Q4Keys<D>>(a, p, st);
-  else launch_simt<float, 4, Q4Keys<D>>(a, p, st);
 }
 
 }  // namespace
@@ -209,10 +172,10 @@ extern "C" tsd_status tsd_tree_verify_attn_q4(const tsd_attn_desc* d, const void
     launch_q4_rows(a, p, d->dk, st);
     if (d->dk == 128) launch_combine<__nv_bfloat16, 128, __half>(a, p, st);
     else launch_combine<__nv_bfloat16, 64, __half>(a, p, st);
-  } else if (d->dk == 128) {
-    launch_simt_q4<128>(a, p, st);
   } else {
-    launch_simt_q4<64>(a, p, st);
+    launch_q4_f32(a, p, d->dk, st);
+    if (d->dk == 128) launch_combine<float, 128, float>(a, p, st);
+    else launch_combine<float, 64, float>(a, p, st);
   }
   return cuda_status();
 }

@@ -12,11 +12,14 @@ namespace tsd {
 // over 32k keys 118 and 144 us.)
 constexpr int kQ4FewRows = 16;
 
+constexpr int kQ4F32 = kQ8Simt;                      // the path of fp32 heads
+
 // Exponents above a tile's scales, within which its keys or values are held in fp16 (the
 // scales that writes give: -92..125).
 constexpr int kQ4MinExp = -96, kQ4MaxExp = 118;
 
 void launch_q4_few(const Q8AttnArgs& a, const Q8Plan& p, int D, cudaStream_t st);
+void launch_q4_f32(const Q8AttnArgs& a, const Q8Plan& p, int D, cudaStream_t st);
 void launch_q4_rows(const Q8AttnArgs& a, const Q8Plan& p, int D, cudaStream_t st);
 
 }  // namespace tsd
