@@ -8,8 +8,8 @@
 namespace tsd {
 
 // Up to this many packed rows take the path with keys on the product's rows.  (12 rows of 32
-// requests over 1k to 4k keys: 51 us so and 69 us on tcgen05; 16 rows: 52 and 69, of 8 requests
-// over 32k keys 118 and 144 us.)
+// requests over 1k to 4k keys: 48 us so and 67 us on tcgen05; 16 rows: 50 and 67, of 8 requests
+// over 32k keys 93 and 138 us.)
 constexpr int kQ4FewRows = 16;
 
 constexpr int kQ4F32 = kQ8Simt;                      // the path of fp32 heads

@@ -7,7 +7,7 @@
 // Widening is what this path has to do cheaply: codes go from shared memory straight into
 // the operand registers of mma.sync (tcgen05 takes operands from shared or tensor memory,
 // so that every widened element would be written and read once more; the products of
-// few columns are far from binding here: 23% of the tensor pipe).  A warp works alone on
+// few columns are far from binding here: 26% of the tensor pipe).  A warp works alone on
 // chunks of 32 keys, which it copies itself, a chunk ahead, into a ring of its own: no barrier
 // between the first chunk and the last.
 //
@@ -26,17 +26,19 @@
 //       under way.
 // Each warp's sum, bound and output are joined at the end, in fp32.
 //
-// What bounds it.  One token of 16 requests of 32 heads over 20k to 32k keys: 118 us, 4.1 TB/s
-// (72 us by the bytes).  The copies alone, the arithmetic left out, take 93 us in the same
-// graph that takes 121 with it: 17 us of that are launch, set-up, joint and merge.  Two
-// CTAs per SM, so that one's start and end lie beside the other's chunks (one of 16 warps: 142
-// us); the scheduler serves the older of the two first.  Within the loop the issue slots are
-// three quarters full (585 instructions for 32 keys, 258 of them on the ALU, which takes one in
-// two cycles).  Tried and dropped: chunks of 16 keys with rings of two to five (131 us, 45
-// instead of 42 for 32 requests over 1k to 4k), three CTAs of 80 registers (144 us), the work
-// dealt out evenly over one CTA per slot by the requests' lengths (120 us, but 80 instead of 56
-// us for 200 requests below 900 keys and 77 instead of 56 for 32 of 4 rows: a CTA then starts
-// and ends once per request).
+// What bounds it.  One token of 16 requests of 32 heads over 20k to 32k keys: 111 us, 4.4 TB/s
+// (72 us by the bytes; 105 in the kernel, where no warp waits for its copies to speak of).  The
+// copies alone, the arithmetic left out, take 93 us in the same graph: 17 us of that are launch,
+// set-up, joint and merge.  It is issue slots (58% full over the kernel's whole time, three
+// quarters within the loop), the ALU (49%; it takes an instruction in two cycles) and the
+// products' latency, at four warps a scheduler.  Up to eight packed rows need 128 registers:
+// sixteen warps an SM, in CTAs of eight, or of four for many short requests, so that one's start
+// and end lie beside the others' chunks (one CTA of sixteen: 142 us); nine to sixteen rows 168
+// registers: twelve warps, in one CTA or in three.  Tried and dropped: chunks of 16 keys with
+// rings of two to five (131 us, 45 instead of 42 for 32 requests over 1k to 4k), three CTAs of
+// eight warps and 80 registers (144 us), the work dealt out evenly over one CTA per slot by the
+// requests' lengths (120 us, but 80 instead of 56 us for 200 requests below 900 keys and 77
+// instead of 56 for 32 of 4 rows: a CTA then starts and ends once per request).
 #include "tsd_host.h"
 #include "tsd_q4.cuh"
 #include "tsd_q4_attn.cuh"

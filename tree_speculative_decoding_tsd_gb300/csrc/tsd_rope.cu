@@ -16,8 +16,8 @@
 // a division).
 //
 // A row's 8-element pieces lie on d / 8 lanes, both elements of a pair on one lane: the
-// rotation needs no other lane, the mean four (three) shuffles.  A warp takes a token and a run of its
-// heads, whose sines it computes once; a grid of few tokens cuts the heads into more
+// rotation needs no other lane, the mean four (three) shuffles.  A warp takes a token and a run
+// of its heads, whose sines it computes once; a grid of few tokens cuts the heads into more
 // runs.  Bounded by memory: each element is read and written once (prompts of 4 x up to 8192
 // rows of 32 + 16 heads: 91 us on the device, 89 by the bytes; with a head's weights loaded for
 // each row instead of kept for all queries or keys 108).  Small trees: the host's side of the
