@@ -13,7 +13,7 @@
 // a lane: 40 instead of 28 us for the prompt below).  Reading, a lane has eight elements.
 //
 // 4 x up to 8192 rows of 8 heads: written in 28 us (22 by the bytes; issue slots 62%, memory 59%),
-// read back in 25; 32 requests of 1k to 4k rows read from pages in 56 us (47 by the bytes).
+// read back in 23; 32 requests of 1k to 4k rows read from pages in 50 us (47 by the bytes).
 #include <cuda_bf16.h>
 #include <math.h>
 
@@ -284,8 +284,11 @@ __global__ void __launch_bounds__(kThreads) read_q4_kernel(const __grid_constant
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
       const long row = rows[min(t + u * kRows, n - 1) - t0] + h * apart;
-      w[u] = __ldg(a.codes[part] + row * (D / 8) + c);
-      f[u] = __ldg(a.scales[part] + row * (D / kQ4Group) + (c >> 2));
+      // (Read once, past L1: 32 requests 54 us in a graph, 63 with __ldg.  Scales of fp32 rows,
+      // whose stores leave more time between loads: 73 so, 87 past L1.)
+      w[u] = __ldcs(a.codes[part] + row * (D / 8) + c);
+      const uint16_t* const scale = a.scales[part] + row * (D / kQ4Group) + (c >> 2);
+      f[u] = sizeof(T) == 2 ? __ldcg(scale) : __ldg(scale);
     }
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
