@@ -649,7 +649,8 @@ tsd_status tsd_cache_evict_q8(const tsd_attn_desc* desc, int keep, int sink, int
  * behind prefix_len are not used, whatever they hold; nor are scratch rows that no row
  * sees.  A NaN or an infinity in a scratch row reaches the outputs of the rows that see it
  * and no others.  fp32 inputs: q, probabilities and scratch rows enter their products to
- * 2^-22, cached values as they are, sums in fp32.  bf16 inputs: probabilities and values
+ * 2^-22 (scratch elements below 2^-104: to 2^-126), cached values as they are, sums in
+ * fp32.  bf16 inputs: probabilities and values
  * enter their products in fp16, each to 2^-12, and so do keys where a call has more than 16
  * packed rows (R * Hq / Hkv); values (and those keys) of a run of up to 128 cached rows share a
  * power of two, so that they are off by at most 2^-15 of the run's largest scale as well, and

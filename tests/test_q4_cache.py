@@ -839,6 +839,30 @@ def test_attention_on_streams_and_in_graphs(R):
 
 
 @gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("R", [1, 4, 20])
+def test_attention_over_a_table_of_many_pages(R, dtype):
+    """A capacity of 2^27 positions, of which a request holds 300."""
+    s = Setup("gqa", 1, R, [300], page=128, dtype=dtype, seed=67)
+    table = torch.full((1, 1 << 20), -1, dtype=torch.int32, device=DEV)
+    table[:, :s.table.shape[1]] = s.table
+    s.paging["page_table"] = table
+    s.desc = T.make_desc(1, R, s.Hq, s.Hkv, s.d, s.d, 1 << 27, dtype, False, s.scale)
+    s.check_attn(*s.attn())
+    assert int(s.err) == 0
+
+
+def test_workspaces_of_the_largest_caches():
+    for dtype in (torch.bfloat16, torch.float32):
+        for R in (1, 4, 65):
+            d = T.make_desc(40, R, 32, 8, 128, 128, 2 ** 31 - 128, dtype, False, 0.1)
+            size = T.tsd_verify_q4_workspace_size(d)
+            parts, rest = divmod(size, 40 * 32 * R)
+            assert rest == 0 and size > 0
+            assert parts // (128 * 4 + 8) >= 2 ** 31 // (1 << 21) - 1
+
+
+@gpu
 def test_attention_past_32_bit_offsets():
     """A pool whose codes pass 2^32 bytes, the request's pages at its end."""
     pages = (1 << 32) // (8 * 128 * 64) + 40

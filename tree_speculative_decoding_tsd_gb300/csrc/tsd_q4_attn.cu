@@ -92,7 +92,8 @@ Q8Plan plan_q4(const tsd_attn_desc& d) {
     // keys, 3, 6, 12, 24 splits: 69, 48, 34, 40 us; 17 rows of one over 2k: 63, 42, 39, 40, and
     // with the scratch rows in the last split 81, 48, 46, 49.)
     const long tiles = ceil_div(d.cap, 64), most = 304 / (heads * p.nrg);
-    const long n = most < 1 ? 1 : most > 64 ? 64 : most, per = ceil_div(tiles, n);
+    const long n = most < 1 ? 1 : most > 64 ? 64 : most, even = ceil_div(tiles, n);
+    const long per = even < 32768 ? even : 32768;  // (sums of a length and a split's stay within 32 bits)
     p.split_len = (int)per * 64;
     p.nsplit = (int)ceil_div(d.cap, p.split_len);
     p.tree_split = p.nsplit > 1 && per <= 12 ? 1 : 0;
