@@ -553,8 +553,14 @@ def _scratch(ws, err, dev):
             None if err is None else _p(err, "err", _I32T, err.shape, dev))
 
 
+# The current stream's handle, without a stream object made for it (1.1 us a call).
+_current_handle = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _raw_stream(stream, dev):
     if stream is None:
+        if _current_handle is not None:
+            return _current_handle(dev)
         stream = torch.cuda.current_stream(dev)
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
