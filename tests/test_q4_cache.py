@@ -602,6 +602,29 @@ def test_attention_of_fp32_matches_plain(kind, B, R, lens, page):
 
 
 @gpu
+@pytest.mark.parametrize("kind,R,lens", [("gqa", 5, [700, 333]), ("gqa", 1, [8000, 5000]), ("gqa", 20, [900]),
+                                         ("narrow", 30, [4000, 333]), ("one", 9, [6000])])
+def test_attention_of_fp32_is_as_good_as_plain_fp32(kind, R, lens):
+    """The root mean square of the error, against that of the same sums in PyTorch's fp32, whose
+    roundings are as many: no more than twice it."""
+    s = Setup(kind, len(lens), R, lens, dtype=torch.float32, seed=68)
+    out, _ = s.attn()
+    got = plain = 0.0
+    for b, P in enumerate(s.lens):
+        for h in range(s.Hkv):
+            k = torch.cat([s.cache("k").values(b, h)[:P], s.kt[b, :, h].double()])
+            v = torch.cat([s.cache("v").values(b, h)[:P], s.vt[b, :, h].double()])
+            g = s.Hq // s.Hkv
+            sees = torch.cat([torch.ones(R, P, dtype=torch.bool, device=DEV), s.sees(b)], 1).repeat_interleave(g, 0)
+            q = s.q[b, :, h * g:(h + 1) * g].reshape(-1, s.d)
+            o = plain_attn(q.double(), k, v, sees, s.scale)[0]
+            p = torch.softmax((q @ k.float().T * s.scale).masked_fill(~sees, -INF), -1) @ v.float()
+            got += float((out[b, :, h * g:(h + 1) * g].double().reshape(-1, s.d) - o).square().sum())
+            plain += float((p.double() - o).square().sum())
+    assert got <= 4 * plain
+
+
+@gpu
 @pytest.mark.parametrize("kind,R", [("gqa", 1), ("gqa", 5), ("gqa", 17), ("narrow", 4), ("one", 65)])
 @pytest.mark.parametrize("power", [-112, -70, -40, 40, 80])
 def test_attention_of_very_small_and_large_fp32_values(kind, R, power):

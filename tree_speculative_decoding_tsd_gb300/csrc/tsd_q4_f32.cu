@@ -16,12 +16,15 @@
 // shared memory (16-byte units permuted by key: no reader and no writer meets a bank twice).
 // The keys' order within a product is that of its accumulators, so that P stays in registers.
 //
-// What bounds it: with 64 rows the products (two of 1024 multiply-adds for each; 58% of the tensor
-// pipe) and their waits, two CTAs per SM (three of 168 registers spill: 304 instead of 262 us).
-// 65 rows of 64 heads over 8000 keys: 236 us, 72 TFLOP/s; 4 x 33 rows of 32 heads over 1k to 4k
-// keys: 166 us.  On the CUDA cores, with a thread's 8 x 4 scores from shared memory, whose loads
-// bound that, 484 and 267 us; a warp per eight rows with keys in registers, as over the 8-bit
-// cache, 1531 and 558.
+// The tensor core cuts its sums: over thousands of keys an accumulator loses a few 2^-20, always
+// towards zero.  So 32 dims of a score, and 64 keys of an output, are summed there and then added
+// in fp32 (6% of the time; the outputs' error is then that of plain fp32 code, before four times).
+//
+// What bounds it: with 64 rows the products (two of 1024 multiply-adds for each; 60% of the tensor
+// pipe) and their waits, at 255 registers and two CTAs per SM.  65 rows of 64 heads over 8000
+// keys: 250 us, 68 TFLOP/s; 4 x 33 rows of 32 heads over 1k to 4k keys: 177 us.  On the CUDA
+// cores, with a thread's 8 x 4 scores from shared memory, whose loads bound that, 484 and 267 us;
+// a warp per eight rows with keys in registers, as over the 8-bit cache, 1531 and 558.
 #include <type_traits>
 
 #include "tsd_common.cuh"
@@ -170,40 +173,52 @@ __global__ void __launch_bounds__(kF32Threads, 2) q4_f32_kernel(const __grid_con
     const float4* const q4 = (const float4*)sq + wr * (D / 8) * 32 + lane;
     const float* const kb = sk + (key_base + g) * D;
     const int turn = k_turn(g);
-#pragma unroll 2
-    for (int j = 0; j < D / 16; ++j) {             // 16 dims: two products
-      uint32_t hi[2][4], lo[2][4];
+#pragma unroll 1
+    for (int j = 0; j < D / 16; j += 2) {
+      float d[NT][4];
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const float4 q = q4[(2 * j + i) * 32];
-        cut_terms(q.x, hi[i][0], lo[i][0]);
-        cut_terms(q.y, hi[i][1], lo[i][1]);
-        cut_terms(q.z, hi[i][2], lo[i][2]);
-        cut_terms(q.w, hi[i][3], lo[i][3]);
-      }
-      const int unit = ((4 * j + t) ^ turn) * 4;
+      for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        const float4 k = *(const float4*)(kb + 8 * n * D + unit);
-        uint32_t kx = __float_as_uint(k.x), ky = __float_as_uint(k.y), kz = __float_as_uint(k.z),
-                 kw = __float_as_uint(k.w);
-        if constexpr (is_tree) {
-          uint32_t hx, hy, hz, hw, lx, ly, lz, lw;
-          cut_terms(k.x, hx, lx);
-          cut_terms(k.y, hy, ly);
-          cut_terms(k.z, hz, lz);
-          cut_terms(k.w, hw, lw);
-          mma_tf32(s[n], lo[0], lx, ly);
-          mma_tf32(s[n], lo[1], lz, lw);
-          mma_tf32(s[n], hi[0], lx, ly);
-          mma_tf32(s[n], hi[1], lz, lw);
-          kx = hx; ky = hy; kz = hz; kw = hw;
+        for (int x = 0; x < 4; ++x) d[n][x] = 0.f;
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {                // 16 dims: two products
+        uint32_t hi[2][4], lo[2][4];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const float4 q = q4[(2 * (j + y) + i) * 32];
+          cut_terms(q.x, hi[i][0], lo[i][0]);
+          cut_terms(q.y, hi[i][1], lo[i][1]);
+          cut_terms(q.z, hi[i][2], lo[i][2]);
+          cut_terms(q.w, hi[i][3], lo[i][3]);
         }
-        mma_tf32(s[n], lo[0], kx, ky);
-        mma_tf32(s[n], hi[0], kx, ky);
-        mma_tf32(s[n], lo[1], kz, kw);
-        mma_tf32(s[n], hi[1], kz, kw);
+        const int unit = ((4 * (j + y) + t) ^ turn) * 4;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          const float4 k = *(const float4*)(kb + 8 * n * D + unit);
+          uint32_t kx = __float_as_uint(k.x), ky = __float_as_uint(k.y), kz = __float_as_uint(k.z),
+                   kw = __float_as_uint(k.w);
+          if constexpr (is_tree) {
+            uint32_t hx, hy, hz, hw, lx, ly, lz, lw;
+            cut_terms(k.x, hx, lx);
+            cut_terms(k.y, hy, ly);
+            cut_terms(k.z, hz, lz);
+            cut_terms(k.w, hw, lw);
+            mma_tf32(d[n], lo[0], lx, ly);
+            mma_tf32(d[n], lo[1], lz, lw);
+            mma_tf32(d[n], hi[0], lx, ly);
+            mma_tf32(d[n], hi[1], lz, lw);
+            kx = hx; ky = hy; kz = hz; kw = hw;
+          }
+          mma_tf32(d[n], lo[0], kx, ky);
+          mma_tf32(d[n], lo[1], kz, kw);
+          mma_tf32(d[n], hi[0], kx, ky);
+          mma_tf32(d[n], hi[1], kz, kw);
+        }
       }
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) s[n][x] += d[n][x];
     }
     bool raised = false;
     float al[2];
@@ -249,34 +264,48 @@ __global__ void __launch_bounds__(kF32Threads, 2) q4_f32_kernel(const __grid_con
         for (int x = 0; x < 4; ++x) o[i][x] *= al[x >> 1];
     }
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {                 // eight keys: lane t has 2 t and 2 t + 1
-      uint32_t hi[4], lo[4];
-      near_terms(s[n][0], hi[0], lo[0]);
-      near_terms(s[n][2], hi[1], lo[1]);
-      near_terms(s[n][1], hi[2], lo[2]);
-      near_terms(s[n][3], hi[3], lo[3]);
-      const float* const vb = sv + (key_base + 8 * n + 2 * t) * D;
+    for (int c = 0; c < D / 64; ++c) {             // 64 dims
+      float d[8][4];
 #pragma unroll
-      for (int u = 0; u < D / 32; ++u) {           // lane g has dims 4 g .. of 32
-        const float4 va = *(const float4*)(vb + ((8 * u + g) ^ v_turn(2 * t)) * 4);
-        const float4 vc = *(const float4*)(vb + D + ((8 * u + g) ^ v_turn(2 * t + 1)) * 4);
-        const float x0[4] = {va.x, va.y, va.z, va.w}, x1[4] = {vc.x, vc.y, vc.z, vc.w};
+      for (int i = 0; i < 8; ++i)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          uint32_t b0 = __float_as_uint(x0[i]), b1 = __float_as_uint(x1[i]);
-          if constexpr (is_tree) {
-            uint32_t h0, h1, l0, l1;
-            cut_terms(x0[i], h0, l0);
-            cut_terms(x1[i], h1, l1);
-            mma_tf32(o[4 * u + i], lo, l0, l1);
-            mma_tf32(o[4 * u + i], hi, l0, l1);
-            b0 = h0;
-            b1 = h1;
+        for (int x = 0; x < 4; ++x) d[i][x] = 0.f;
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {               // eight keys: lane t has 2 t and 2 t + 1
+        uint32_t hi[4], lo[4];
+        near_terms(s[n][0], hi[0], lo[0]);
+        near_terms(s[n][2], hi[1], lo[1]);
+        near_terms(s[n][1], hi[2], lo[2]);
+        near_terms(s[n][3], hi[3], lo[3]);
+        const float* const vb = sv + (key_base + 8 * n + 2 * t) * D;
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {              // lane g has dims 4 g .. of 32
+          const int unit = 16 * c + 8 * u + g;
+          const float4 va = *(const float4*)(vb + (unit ^ v_turn(2 * t)) * 4);
+          const float4 vc = *(const float4*)(vb + D + (unit ^ v_turn(2 * t + 1)) * 4);
+          const float x0[4] = {va.x, va.y, va.z, va.w}, x1[4] = {vc.x, vc.y, vc.z, vc.w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint32_t b0 = __float_as_uint(x0[i]), b1 = __float_as_uint(x1[i]);
+            float (&to)[4] = d[4 * u + i];
+            if constexpr (is_tree) {
+              uint32_t h0, h1, l0, l1;
+              cut_terms(x0[i], h0, l0);
+              cut_terms(x1[i], h1, l1);
+              mma_tf32(to, lo, l0, l1);
+              mma_tf32(to, hi, l0, l1);
+              b0 = h0;
+              b1 = h1;
+            }
+            mma_tf32(to, lo, b0, b1);
+            mma_tf32(to, hi, b0, b1);
           }
-          mma_tf32(o[4 * u + i], lo, b0, b1);
-          mma_tf32(o[4 * u + i], hi, b0, b1);
         }
       }
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) o[8 * c + i][x] += d[i][x];
     }
   };
 
