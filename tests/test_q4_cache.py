@@ -698,6 +698,72 @@ def test_attention_of_fp32_reports_pages_and_replays(R):
     s.check_attn(out, lse)
 
 
+BESIDE = [("gqa", 32, 33, [300, 0, 1000, 129, 1, 64, 127, 700, 2000], 2100, 0),
+          ("gqa", 16, 65, [1000, 129, 0, 300], 3200, 128), ("gqa", 2, 33, [32700, 400], 60, 128),
+          ("gqa", 4, 65, [20000, 0, 129, 5], 100, 0), ("wide", 128, 17, [400, 64, 0, 129], 3800, 128)]
+
+
+@gpu
+@pytest.mark.parametrize("kind,B,R,lens,extra,page", BESIDE)
+def test_attention_with_the_last_row_on_its_own(kind, B, R, lens, extra, page):
+    """Large batches and long caches, of trees that leave 4 or 8 packed rows behind groups of 128."""
+    s = Setup(kind, B, R, lens, extra=extra, page=page, seed=70)
+    out, lse = s.attn()
+    assert int(s.err) == 0
+    s.check_attn(out, lse, requests=sorted({0, 1, min(3, B - 1), B // 2, B - 1}), heads=[0, s.Hkv - 1])
+    assert not (out == 7).all(-1).any() and not (lse == 7).any()
+    s.kt[0, R - 1], s.mask[0, 5] = NAN, 0           # seen by the last row alone, and no longer by row 5
+    s.masks[0] = [m & ~(1 << (R - 2)) for m in s.masks[0][:-1]] + s.masks[0][-1:]
+    s.masks[0][5] = 0
+    s.set_masks(s.masks)
+    again, _ = s.attn()
+    assert again[0, R - 1].isnan().all() and again[0, :R - 1].isfinite().all()
+    assert torch.equal(again[1:], out[1:])
+
+
+@gpu
+@pytest.mark.parametrize("kind,B,R,lens,extra,page", BESIDE[:2])
+def test_attention_with_the_last_row_on_its_own_in_a_round(kind, B, R, lens, extra, page):
+    """Between an append that it waits for and one that waits for it, in a graph."""
+    s = Setup(kind, B, R, lens, extra=extra, page=page, seed=71)
+    x, y = s.normal(B, 20, s.Hkv, s.d), s.normal(B, 20, s.Hkv, s.d)
+    n = torch.tensor([(3 * b) % 21 for b in range(B)], dtype=torch.int32, device=DEV)
+    out, lse = torch.empty_like(s.q), torch.empty(B, R, s.Hq, device=DEV)
+    ws = T.workspace(T.tsd_verify_q4_workspace_size(s.desc))
+    kept = [t.clone() for t in s.arrays()] + [s.plen.clone()]
+
+    def turn():
+        T.tsd_cache_write_q4(s.desc, x, y, n, *s.arrays(), s.plen, s.err, **s.paging)
+        s.attn_into(out, lse, ws)
+        T.tsd_cache_write_q4(s.desc, y, x, n, *s.arrays(), s.plen, s.err, **s.paging)
+
+    def restore():
+        for t, old in zip((*s.arrays(), s.plen), kept):
+            t.copy_(old)
+        out.fill_(7)
+        torch.cuda.synchronize()
+
+    T.tsd_cache_write_q4(s.desc, x, y, n, *s.arrays(), s.plen, s.err, **s.paging)
+    torch.cuda.synchronize()
+    s.attn_into(out, lse, ws)
+    torch.cuda.synchronize()
+    want = out.clone()
+    restore()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        turn()
+    for _ in range(10):
+        restore()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
+        restore()
+        turn()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
+    assert int(s.err) == 0
+
+
 @gpu
 @pytest.mark.parametrize("kind,B,R,page", [("gqa", 200, 1, 0), ("gqa", 150, 4, 128), ("gqa", 64, 4, 0),
                                            ("gqa", 64, 1, 128), ("narrow", 400, 1, 128), ("narrow", 400, 2, 0),

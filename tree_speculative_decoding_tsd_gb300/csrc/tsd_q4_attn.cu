@@ -47,9 +47,10 @@ double split_cost(long units, long tiles, long per, int D, const CtaShape& s) {
   return cost + (n > 1 ? 12 : 0);                  // (the merge, in both)
 }
 
-Q8Plan plan_q4(const tsd_attn_desc& d) {
+// Plan of a launch for R of the tree's rows.
+Q8Plan plan_rows(const tsd_attn_desc& d, int R) {
   Q8Plan p{};
-  const int M = d.R * (d.Hq / d.Hkv);
+  const int M = R * (d.Hq / d.Hkv);
   const long heads = (long)d.B * d.Hkv;
   if (d.dtype == TSD_BF16) {
     const bool few = M <= kQ4FewRows;
@@ -99,10 +100,76 @@ Q8Plan plan_q4(const tsd_attn_desc& d) {
     p.tree_split = p.nsplit > 1 && per <= 12 ? 1 : 0;
     p.nsplit += p.tree_split;
   }
-  p.ws_bytes = p.nsplit > 1 ? (size_t)d.B * d.Hq * d.R * p.nsplit *
+  p.ws_bytes = p.nsplit > 1 ? (size_t)d.B * d.Hq * R * p.nsplit *
                                   (d.dv * (size_t)p.part_bytes + sizeof(float2))
                             : 0;
   return p;
+}
+
+// Trees of 1 + 32 n rows (the root and 32 n nodes) times 4 or 8 heads leave 4 or 8 packed rows behind
+// groups of 128.  With much to do the last tree row then has a launch of its own, on the path for few
+// rows, instead of one more group: beside the groups', whose last CTAs leave room, where a cache is
+// one split; behind their merge where it is several, and long.  (Rows of 32 heads, us, so and in
+// equal groups.  Beside: 16, 32, 64 x 33 rows over 1k to 4k keys 66, 116, 196 and 75, 124, 225.
+// Behind: 8 x 33 over 32k 228 and 280, 8 x 65 375 and 391, 2 x 33 over 20k to 32k 77 and 87; 4 x 33
+// over 4k to 8k, which therefore stay together, 62 and 52.)
+constexpr long kQ4RestWork = 4096, kQ4RestTiles = 128;   // heads times tiles; tiles, if several splits
+
+struct Q4Plan {
+  Q8Plan main, rest;
+  int rest_rows;                                   // tree rows of `rest`; 0: none
+  size_t rest_at, ws_bytes;
+};
+Q4Plan plan_q4(const tsd_attn_desc& d) {
+  Q4Plan p{};
+  const int g = d.Hq / d.Hkv, M = d.R * g, behind = M % 128;
+  const long tiles = ceil_div(d.cap, 128);
+  if (d.dtype == TSD_BF16 && M > 128 && behind > 0 && behind <= 8 && behind % g == 0 &&
+      (long)d.B * d.Hkv * tiles >= kQ4RestWork) {
+    p.rest_rows = behind / g;
+    p.main = plan_rows(d, d.R - p.rest_rows);
+    if (p.main.nsplit > 1 && tiles < kQ4RestTiles) p.rest_rows = 0;
+  }
+  if (p.rest_rows == 0) p.main = plan_rows(d, d.R);
+  p.ws_bytes = p.main.ws_bytes;
+  if (p.rest_rows > 0) {
+    p.rest = plan_rows(d, p.rest_rows);
+    p.rest_at = (p.ws_bytes + 255) / 256 * 256;
+    p.ws_bytes = p.rest_at + p.rest.ws_bytes;
+  }
+  return p;
+}
+
+// A launch for tree rows r0 .. r0 + nr - 1, and the merge of its splits.
+void run_q4(Q8AttnArgs a, const Q8Plan& p, int r0, int nr, bool beside, int D, void* ws, cudaStream_t st) {
+  a.beside = beside;
+  a.r0 = r0;
+  a.nr = nr;
+  a.M = nr * a.g;
+  if (p.nsplit > 1) {
+    const size_t parts = (size_t)a.B * a.Hq * nr * p.nsplit;
+    a.part_o = ws;
+    a.part_meta = (float2*)((char*)ws + parts * D * p.part_bytes);
+  }
+  a.nsplit = p.nsplit;
+  a.split_len = p.split_len;
+  a.nrg = p.nrg;
+  a.rb = p.rb;
+  a.tree_split = p.tree_split;
+  a.by_length = p.by_length;
+  if (p.path == kQ8Few) {
+    launch_q4_few(a, p, D, st);
+    if (D == 128) launch_combine<__nv_bfloat16, 128, float>(a, p, st);
+    else launch_combine<__nv_bfloat16, 64, float>(a, p, st);
+  } else if (p.path == kQ8Rows) {
+    launch_q4_rows(a, p, D, st);
+    if (D == 128) launch_combine<__nv_bfloat16, 128, __half>(a, p, st);
+    else launch_combine<__nv_bfloat16, 64, __half>(a, p, st);
+  } else {
+    launch_q4_f32(a, p, D, st);
+    if (D == 128) launch_combine<float, 128, float>(a, p, st);
+    else launch_combine<float, 64, float>(a, p, st);
+  }
 }
 
 }  // namespace
@@ -129,8 +196,9 @@ extern "C" tsd_status tsd_tree_verify_attn_q4(const tsd_attn_desc* d, const void
       !ok_ptr(vscale) || !ok_ptr(prefix_len) || !ok_ptr(ktree) || !ok_ptr(vtree) || !ok_ptr(mask) ||
       !ok_ptr(out) || !ok_ptr(lse) || !paging_ok(d, page_table, max_pages, page_size, num_pages))
     return TSD_ERR_INVALID_ARG;
-  const Q8Plan p = plan_q4(*d);
-  if ((long)d->Hkv * p.nrg > 65535 || p.nsplit > 65535) return TSD_ERR_INVALID_ARG;
+  const Q4Plan p = plan_q4(*d);
+  if ((long)d->Hkv * p.main.nrg > 65535 || p.main.nsplit > 65535 || p.rest.nsplit > 65535)
+    return TSD_ERR_INVALID_ARG;
   if (ws_bytes < p.ws_bytes || (p.ws_bytes > 0 && !ok_ptr(ws))) return TSD_ERR_INVALID_ARG;
   Q8AttnArgs a{};
   a.q = q;
@@ -144,39 +212,18 @@ extern "C" tsd_status tsd_tree_verify_attn_q4(const tsd_attn_desc* d, const void
   a.mask = mask;
   a.out = out;
   a.lse = lse;
-  if (p.nsplit > 1) {
-    const size_t parts = (size_t)d->B * d->Hq * d->R * p.nsplit;
-    a.part_o = ws;
-    a.part_meta = (float2*)((char*)ws + parts * d->dv * p.part_bytes);
-  }
   a.err = err;
   a.map = cache_map(d, page_table, max_pages, page_size, num_pages);
   a.B = d->B;
   a.R = d->R;
   a.Hq = d->Hq;
   a.g = d->Hq / d->Hkv;
-  a.M = d->R * a.g;
-  a.nsplit = p.nsplit;
-  a.split_len = p.split_len;
-  a.nrg = p.nrg;
-  a.rb = p.rb;
-  a.tree_split = p.tree_split;
-  a.by_length = p.by_length;
   a.qscale = d->scale * 1.4426950408889634f;
   a.wait_cycles = wait_budget();
   const cudaStream_t st = (cudaStream_t)stream;
-  if (p.path == kQ8Few) {
-    launch_q4_few(a, p, d->dk, st);
-    if (d->dk == 128) launch_combine<__nv_bfloat16, 128, float>(a, p, st);
-    else launch_combine<__nv_bfloat16, 64, float>(a, p, st);
-  } else if (p.path == kQ8Rows) {
-    launch_q4_rows(a, p, d->dk, st);
-    if (d->dk == 128) launch_combine<__nv_bfloat16, 128, __half>(a, p, st);
-    else launch_combine<__nv_bfloat16, 64, __half>(a, p, st);
-  } else {
-    launch_q4_f32(a, p, d->dk, st);
-    if (d->dk == 128) launch_combine<float, 128, float>(a, p, st);
-    else launch_combine<float, 64, float>(a, p, st);
-  }
+  const int together = d->R - p.rest_rows;
+  run_q4(a, p.main, 0, together, false, d->dk, ws, st);
+  if (p.rest_rows > 0)
+    run_q4(a, p.rest, together, p.rest_rows, p.main.nsplit == 1, d->dk, (char*)ws + p.rest_at, st);
   return cuda_status();
 }

@@ -417,7 +417,7 @@ __global__ void __launch_bounds__(kF32Threads, 2) q4_f32_kernel(const __grid_con
     if (row >= rows_here) continue;
     const int pr = row_base + row, tr = pr / a.g, qh = hk * a.g + pr % a.g;
     const long orow = ((long)b * a.R + tr) * a.Hq + qh;
-    const long prow = (((long)b * a.Hq + qh) * a.R + tr) * a.nsplit + sp;
+    const long prow = (((long)b * a.Hq + qh) * a.nr + tr) * a.nsplit + sp;
     // (a split whose pages are all missing saw nothing: weight 0)
     const float inv = m[i] == -INFINITY && l[i] == 0.f ? 0.f : 1.f / l[i];
     const float lse2 = m[i] + log2f(l[i]);

@@ -118,7 +118,13 @@ q4_few_kernel(const __grid_constant__ Q8AttnArgs a) {
   using L = FewLayout<D, NT, S, W>;
   constexpr int NG = L::NG, NW = D / 64;           // groups; words of V per lane and key
   extern __shared__ __align__(128) uint8_t smem[];
-  grid_dependency_sync();
+  // Beside another launch of the same call: all of that one's CTAs have waited for what came
+  // before the call, or this one would not run yet.  It ends behind the other: what follows
+  // waits for this launch alone.
+  if (!a.beside) grid_dependency_sync();
+  auto finish = [&] {
+    if (a.beside && blockIdx.x + blockIdx.y + blockIdx.z == 0) grid_dependency_sync();
+  };
   // (The last splits first: those that are cut short or hold the scratch rows do not end up behind
   // the others.  One token of 16 requests over 20k to 32k keys 113 -> 110 us, of 16 over 8k to 32k
   // 95 -> 90.)
@@ -129,7 +135,10 @@ q4_few_kernel(const __grid_constant__ Q8AttnArgs a) {
   int P;
   const int b = request_at(a, blockIdx.y, P, (volatile int*)(smem + L::off_req));
   const int nsb = q8_splits(a, P);
-  if (sp >= nsb) return;
+  if (sp >= nsb) {
+    finish();
+    return;
+  }
   const int k0 = min(sp * a.split_len, P), k1 = min(P, k0 + a.split_len);
   const bool with_tree = sp == nsb - 1;
   __syncthreads();                                 // (s_huge)
@@ -211,7 +220,7 @@ q4_few_kernel(const __grid_constant__ Q8AttnArgs a) {
     uint4 w = make_uint4(0u, 0u, 0u, 0u);
     uint32_t top = 0;
     if (n < a.M) {
-      const int tr = n / a.g, qh = hk * a.g + n % a.g;
+      const int tr = a.r0 + n / a.g, qh = hk * a.g + n % a.g;
       const uint4* src = (const uint4*)((const __nv_bfloat16*)a.q + (((long)b * a.R + tr) * a.Hq + qh) * D) + t;
       w = __ldg(src + 4 * j);
 #pragma unroll
@@ -252,8 +261,8 @@ q4_few_kernel(const __grid_constant__ Q8AttnArgs a) {
     constexpr int E = D / 32;                      // dims of a lane
 #pragma unroll 1
     for (int n = W - 1 - warp; n < a.M; n += W) {   // (the warps that have no group of Q first)
-      const int tr = n / a.g, qh = hk * a.g + n % a.g;
-      const uint64_t vis = (tr > 0 ? a.mask[(long)b * a.R + tr] << 1 : 0ull) | 1ull;
+      const int tr = a.r0 + n / a.g, qh = hk * a.g + n % a.g;
+      const uint64_t mask = tr > 0 ? a.mask[(long)b * a.R + tr] : 0ull;   // (row 0: the root; bit j - 1: row j)
       auto row4 = [&](const void* base, long row, float (&x)[E]) {
         const uint32_t* p = (const uint32_t*)((const __nv_bfloat16*)base + row * D) + lane * (E / 2);
 #pragma unroll
@@ -269,6 +278,8 @@ q4_few_kernel(const __grid_constant__ Q8AttnArgs a) {
       for (int i = 0; i < E; ++i) o[i] = 0.f;
 #pragma unroll 1
       for (int j0 = 0; j0 < a.R; j0 += 4) {
+        const uint32_t four = j0 == 0 ? (uint32_t)(mask << 1) | 1u : (uint32_t)(mask >> (j0 - 1));
+        if ((four & 15u) == 0u) continue;          // (the same for the whole warp)
         float k[4][E], v[4][E], s[4];
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
@@ -289,7 +300,7 @@ q4_few_kernel(const __grid_constant__ Q8AttnArgs a) {
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
           const int j = j0 + u;
-          if (j >= a.R || !((vis >> j) & 1ull)) continue;      // (the same for the whole warp)
+          if (j >= a.R || !(four >> u & 1u)) continue;
           const float x = s[u] * a.qscale;
           if (x == -INFINITY) continue;
           const float mn = fmaxf(m, x);
@@ -581,17 +592,18 @@ q4_few_kernel(const __grid_constant__ Q8AttnArgs a) {
     o.x *= inv;
     o.y *= inv;
     const float lse2 = top + log2f(total);
-    const int tr = n / a.g, qh = hk * a.g + n % a.g;
+    const int tr = a.r0 + n / a.g, qh = hk * a.g + n % a.g;
     if (nsb == 1) {
       const long orow = ((long)b * a.R + tr) * a.Hq + qh;
       *(uint32_t*)((__nv_bfloat16*)a.out + orow * D + c) = pack_bf16x2(o.x, o.y);
       if (c == 0) a.lse[orow] = lse2 * 0.69314718055994531f;
     } else {
-      const long prow = (((long)b * a.Hq + qh) * a.R + tr) * a.nsplit + sp;
+      const long prow = (((long)b * a.Hq + qh) * a.nr + tr - a.r0) * a.nsplit + sp;
       *(float2*)((float*)a.part_o + prow * D + c) = o;
       if (c == 0) a.part_meta[prow] = make_float2(lse2, 1.f);
     }
   }
+  finish();
 }
 
 template <int D, int NT, int S, int W, int kCtas>

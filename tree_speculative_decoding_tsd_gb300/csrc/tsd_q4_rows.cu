@@ -779,7 +779,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_rows_kernel(const __grid_const
       const int pr = row_base + min(row, rows_here - 1);
       const int tr = pr / a.g, qh = hk * a.g + pr % a.g;
       const long orow = ((long)b * a.R + tr) * a.Hq + qh;
-      const long prow = (((long)b * a.Hq + qh) * a.R + tr) * a.nsplit + sp;
+      const long prow = (((long)b * a.Hq + qh) * a.nr + tr) * a.nsplit + sp;
       const bool mine = row < rows_here;
       if (mine && p == 0) {
         if (nsb == 1) a.lse[orow] = lse2 * 0.69314718055994531f;

@@ -176,6 +176,7 @@ extern "C" tsd_status tsd_tree_verify_attn_q8(const tsd_attn_desc* d, const void
   a.map = cache_map(d, page_table, max_pages, page_size, num_pages);
   a.B = d->B;
   a.R = d->R;
+  a.nr = d->R;
   a.Hq = d->Hq;
   a.g = d->Hq / d->Hkv;
   a.M = d->R * a.g;

@@ -17,11 +17,13 @@ struct Q8AttnArgs {
   const uint64_t* mask;
   void* out;
   float* lse;
-  void* part_o;               // [B][Hq][R][nsplit][dv] normalised outputs of the splits, over scale
-  float2* part_meta;          // [B][Hq][R][nsplit] (log2-sum-exp, scale)
+  void* part_o;               // [B][Hq][nr][nsplit][dv] normalised outputs of the splits, over scale
+  float2* part_meta;          // [B][Hq][nr][nsplit] (log2-sum-exp, scale)
   int32_t* err;
   CacheMap map;
   int B, R, Hq, g, M;
+  int r0, nr;                 // the launch's tree rows: r0 .. r0 + nr - 1 (M = nr g packed rows)
+  int beside;                 // (4-bit cache) does not wait for the launch before it
   int nsplit, split_len, nrg, rb, tree_split;
   int by_length;              // grid z is a rank in (prefix length desc, index asc) order
   float qscale;               // softmax scale * log2(e)

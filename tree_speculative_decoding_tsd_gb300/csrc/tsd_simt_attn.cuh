@@ -253,9 +253,10 @@ __global__ void __launch_bounds__(128) combine_kernel(const __grid_constant__ Q8
   grid_dependency_sync();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const long row = (long)blockIdx.x * 4 + warp;
-  if (row >= (long)a.B * a.R * a.Hq) return;
-  const int b = (int)(row / ((long)a.R * a.Hq)), r = (int)((row / a.Hq) % a.R), h = (int)(row % a.Hq);
-  const long base = (((long)b * a.Hq + h) * a.R + r) * a.nsplit;
+  if (row >= (long)a.B * a.nr * a.Hq) return;
+  const int b = (int)(row / ((long)a.nr * a.Hq)), r = (int)((row / a.Hq) % a.nr), h = (int)(row % a.Hq);
+  const long base = (((long)b * a.Hq + h) * a.nr + r) * a.nsplit;
+  const long orow = ((long)b * a.R + a.r0 + r) * a.Hq + h;
   const PT* const parts = (const PT*)a.part_o + base * DV;
   const bool active = DV >= 128 || lane < DV / 4;
   // (the workspace holds nsplit entries per row; those of splits without work are
@@ -315,15 +316,15 @@ __global__ void __launch_bounds__(128) combine_kernel(const __grid_constant__ Q8
   }
   if (active) {
 #pragma unroll
-    for (int i = 0; i < kStep; ++i) store4((T*)a.out + row * DV + 128 * i + 4 * lane, acc[i]);
+    for (int i = 0; i < kStep; ++i) store4((T*)a.out + orow * DV + 128 * i + 4 * lane, acc[i]);
   }
-  if (lane == 0) a.lse[row] = (mx + log2f(sum)) * 0.69314718055994531f;
+  if (lane == 0) a.lse[orow] = (mx + log2f(sum)) * 0.69314718055994531f;
 }
 
 template <typename T, int DV, typename PT>
 void launch_combine(const Q8AttnArgs& a, const Q8Plan& p, cudaStream_t st) {
   if (p.nsplit <= 1) return;
-  const long rows = (long)a.B * a.R * a.Hq;
+  const long rows = (long)a.B * a.nr * a.Hq;
   launch_plain(combine_kernel<T, DV, PT>, dim3((unsigned)ceil_div(rows, 4)), dim3(128), 0, st, a);
 }
 
