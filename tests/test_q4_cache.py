@@ -945,10 +945,8 @@ def test_workspaces_of_the_largest_caches():
     for dtype in (torch.bfloat16, torch.float32):
         for R in (1, 4, 65):
             d = T.make_desc(40, R, 32, 8, 128, 128, 2 ** 31 - 128, dtype, False, 0.1)
-            size = T.tsd_verify_q4_workspace_size(d)
-            parts, rest = divmod(size, 40 * 32 * R)
-            assert rest == 0 and size > 0
-            assert parts // (128 * 4 + 8) >= 2 ** 31 // (1 << 21) - 1
+            size = T.tsd_verify_q4_workspace_size(d)      # (a split has at most 2^21 positions)
+            assert size >= (2 ** 31 // (1 << 21) - 1) * 40 * 32 * R * (128 * 2 + 8)
 
 
 @gpu
