@@ -79,7 +79,7 @@ def plain_attn(q, k, v, sees, scale):
 # ----------------------------------------------------------------- inputs --
 
 KINDS = {"gqa": (32, 8, 128), "narrow": (14, 2, 64), "one": (2, 2, 128), "wide": (16, 1, 128),
-         "wide64": (24, 2, 64), "odd": (3, 1, 64)}
+         "wide64": (24, 2, 64), "odd": (3, 1, 64), "eight": (64, 8, 128)}
 
 
 class Setup:
@@ -986,4 +986,92 @@ def test_attention_waits_give_up_at_the_budget(kind, R, page):
         assert int(s.err) & T.TSD_DEV_ERR_MASK == T.TSD_DEV_ERR_TIMEOUT
     s.err.zero_()
     s.check_attn(*s.attn())
+    assert int(s.err) == 0
+
+
+# 64 heads over 8 leave 8 packed rows behind groups of 128 for one tree row, 32 over 8 for two
+LAST = [("eight", 32, 17, [300, 0, 1000, 129], 1100, 0), ("eight", 32, 33, [700, 64, 2000, 1], 100, 128),
+        ("eight", 3, 17, [22000, 129, 0], 100, 128), ("gqa", 32, 34, [1000, 129, 0, 300], 1100, 0),
+        ("gqa", 2, 34, [32700, 400], 60, 128), ("gqa", 40, 65, [64, 1800, 127], 300, 0)]
+
+
+@gpu
+@pytest.mark.parametrize("kind,B,R,lens,extra,page", LAST)
+def test_attention_with_the_last_rows_on_their_own(kind, B, R, lens, extra, page):
+    """One row of eight heads, two rows of four, over one split and over several."""
+    s = Setup(kind, B, R, lens, extra=extra, page=page, seed=80)
+    out, lse = s.attn()
+    assert int(s.err) == 0
+    s.check_attn(out, lse, requests=sorted({0, 1, min(2, B - 1), B // 2, B - 1}), heads=[0, s.Hkv - 1])
+    assert not (out == 7).all(-1).any() and not (lse == 7).any()
+    s.kt[1, R - 1] = NAN                            # seen by the last row alone
+    again, _ = s.attn()
+    assert again[1, R - 1].isnan().all() and again[1, :R - 1].isfinite().all()
+    assert torch.equal(again[0], out[0]) and torch.equal(again[2:], out[2:])
+
+
+@gpu
+@pytest.mark.parametrize("kind,B,R,lens,extra,page", [
+    ("gqa", 16, 33, [4000, 300, 0, 129], 96, 0), ("gqa", 32, 33, [2000, 300, 0, 129], 96, 0),
+    ("gqa", 34, 34, [2000, 1, 700], 96, 128), ("eight", 16, 17, [4000, 64, 2000], 96, 0),
+    ("eight", 32, 17, [2000, 64], 96, 0), ("gqa", 2, 33, [32700, 20000], 68, 128)])
+def test_attention_of_rows_rewritten_right_before(kind, B, R, lens, extra, page):
+    """Queries, scratch rows and masks that change right before every call: each launch of a call
+    has to see what was written before it, on SMs that an earlier launch of the call left empty, too
+    (16 requests: fewer CTAs than SMs)."""
+    s = Setup(kind, B, R, lens, extra=extra, page=page, seed=81)
+    masks = [s.mask.clone()]
+    for _ in range(2):
+        m = [[0] for _ in range(B)]
+        for row in m:
+            for r in range(1, R):
+                row.append(row[s.rnd.randrange(max(0, r - 4), r)] | (1 << (r - 1)))
+        s.set_masks(m)
+        masks.append(s.mask)
+    last = s.masks
+    s.mask = masks[0].clone()
+    rows = [[s.normal(B, R, h, s.d) for h in (s.Hq, s.Hkv, s.Hkv)] for _ in range(3)]
+    starts = [torch.full((B,), n, dtype=torch.int32, device=DEV) for n in (5, 300, 7000)]
+    start = starts[0].clone()
+    freq = 1e4 ** (-torch.arange(s.d // 2, dtype=torch.float64) / (s.d // 2))
+    rope, turns = T.make_rope_desc(B, R, s.Hq, s.Hkv, s.d, s.dt), T.rope_turns(freq, DEV)
+    out, lse = torch.empty_like(s.q), torch.empty(B, R, s.Hq, device=DEV)
+    ws = T.workspace(T.tsd_verify_q4_workspace_size(s.desc))
+
+    def turn(i, wait=lambda: None):
+        start.copy_(starts[i])
+        s.mask.copy_(masks[i])
+        wait()
+        T.tsd_qk_norm_rope(rope, *rows[i], turns, s.q, s.kt, s.vt, start=start)
+        wait()
+        s.attn_into(out, lse, ws)
+        wait()
+
+    want = []
+    for i in range(3):
+        turn(i, torch.cuda.synchronize)
+        want.append((out.clone(), lse.clone()))
+    s.masks = last
+    s.check_attn(out, lse, requests=[0, B - 1], heads=[0, s.Hkv - 1])
+    kept = [(torch.empty_like(out), torch.empty_like(lse)) for _ in range(24)]
+    for n, (o, l) in enumerate(kept):
+        turn(n % 3)
+        o.copy_(out)
+        l.copy_(lse)
+    torch.cuda.synchronize()
+    for n, (o, l) in enumerate(kept):
+        assert torch.equal(o, want[n % 3][0]) and torch.equal(l, want[n % 3][1]), n
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for n in range(6):
+            turn(n % 3)
+            kept[n][0].copy_(out)
+            kept[n][1].copy_(lse)
+    for _ in range(5):
+        for o, _ in kept:
+            o.fill_(7)
+        graph.replay()
+        torch.cuda.synchronize()
+        for n in range(6):
+            assert torch.equal(kept[n][0], want[n % 3][0]) and torch.equal(kept[n][1], want[n % 3][1]), n
     assert int(s.err) == 0

@@ -107,13 +107,15 @@ Q8Plan plan_rows(const tsd_attn_desc& d, int R) {
 }
 
 // Trees of 1 + 32 n rows (the root and 32 n nodes) times 4 or 8 heads leave 4 or 8 packed rows behind
-// groups of 128.  With much to do the last tree row then has a launch of its own, on the path for few
-// rows, instead of one more group: beside the groups', whose last CTAs leave room, where a cache is
-// one split; behind their merge where it is several, and long.  (Rows of 32 heads, us, so and in
-// equal groups.  Beside: 16, 32, 64 x 33 rows over 1k to 4k keys 66, 116, 196 and 75, 124, 225.
-// Behind: 8 x 33 over 32k 228 and 280, 8 x 65 375 and 391, 2 x 33 over 20k to 32k 77 and 87; 4 x 33
-// over 4k to 8k, which therefore stay together, 62 and 52.)
-constexpr long kQ4RestWork = 4096, kQ4RestTiles = 128;   // heads times tiles; tiles, if several splits
+// groups of 128.  With much to do the last tree rows then have a launch of their own, on the path for
+// few rows and behind the groups', instead of being one more group: where a cache is one split and the
+// groups' CTAs are several waves, or where it is several splits and long.  (Rows of 32 heads, us, so
+// and in equal groups.  One split: 16, 24, 32, 40, 64 x 33 rows over 1k to 4k keys 81, 108, 122, 148,
+// 204 and 75, 97, 122, 153, 225; 32 x 34 119 and 121; 24 x 65 157 and 138; 128 x 33 below 1k 184 and
+// 224.  Several: 8 x 33 over 32k 227 and 280, 8 x 34 229 and 281, 8 x 65 374 and 392, 2 x 33 over 20k
+// to 32k 77 and 87; 4 x 33 over 4k to 8k, which therefore stay together, 61 and 54.)
+constexpr long kQ4RestWork = 4096;                 // heads times tiles
+constexpr long kQ4RestHeads = 256, kQ4RestTiles = 128;   // of one split; of several
 
 struct Q4Plan {
   Q8Plan main, rest;
@@ -123,12 +125,12 @@ struct Q4Plan {
 Q4Plan plan_q4(const tsd_attn_desc& d) {
   Q4Plan p{};
   const int g = d.Hq / d.Hkv, M = d.R * g, behind = M % 128;
-  const long tiles = ceil_div(d.cap, 128);
+  const long tiles = ceil_div(d.cap, 128), heads = (long)d.B * d.Hkv;
   if (d.dtype == TSD_BF16 && M > 128 && behind > 0 && behind <= 8 && behind % g == 0 &&
-      (long)d.B * d.Hkv * tiles >= kQ4RestWork) {
+      heads * tiles >= kQ4RestWork) {
     p.rest_rows = behind / g;
     p.main = plan_rows(d, d.R - p.rest_rows);
-    if (p.main.nsplit > 1 && tiles < kQ4RestTiles) p.rest_rows = 0;
+    if (p.main.nsplit > 1 ? tiles < kQ4RestTiles : heads < kQ4RestHeads) p.rest_rows = 0;
   }
   if (p.rest_rows == 0) p.main = plan_rows(d, d.R);
   p.ws_bytes = p.main.ws_bytes;
@@ -141,8 +143,7 @@ Q4Plan plan_q4(const tsd_attn_desc& d) {
 }
 
 // A launch for tree rows r0 .. r0 + nr - 1, and the merge of its splits.
-void run_q4(Q8AttnArgs a, const Q8Plan& p, int r0, int nr, bool beside, int D, void* ws, cudaStream_t st) {
-  a.beside = beside;
+void run_q4(Q8AttnArgs a, const Q8Plan& p, int r0, int nr, int D, void* ws, cudaStream_t st) {
   a.r0 = r0;
   a.nr = nr;
   a.M = nr * a.g;
@@ -222,8 +223,8 @@ extern "C" tsd_status tsd_tree_verify_attn_q4(const tsd_attn_desc* d, const void
   a.wait_cycles = wait_budget();
   const cudaStream_t st = (cudaStream_t)stream;
   const int together = d->R - p.rest_rows;
-  run_q4(a, p.main, 0, together, false, d->dk, ws, st);
+  run_q4(a, p.main, 0, together, d->dk, ws, st);
   if (p.rest_rows > 0)
-    run_q4(a, p.rest, together, p.rest_rows, p.main.nsplit == 1, d->dk, (char*)ws + p.rest_at, st);
+    run_q4(a, p.rest, together, p.rest_rows, d->dk, (char*)ws + p.rest_at, st);
   return cuda_status();
 }

@@ -118,13 +118,7 @@ q4_few_kernel(const __grid_constant__ Q8AttnArgs a) {
   using L = FewLayout<D, NT, S, W>;
   constexpr int NG = L::NG, NW = D / 64;           // groups; words of V per lane and key
   extern __shared__ __align__(128) uint8_t smem[];
-  // Beside another launch of the same call: all of that one's CTAs have waited for what came
-  // before the call, or this one would not run yet.  It ends behind the other: what follows
-  // waits for this launch alone.
-  if (!a.beside) grid_dependency_sync();
-  auto finish = [&] {
-    if (a.beside && blockIdx.x + blockIdx.y + blockIdx.z == 0) grid_dependency_sync();
-  };
+  grid_dependency_sync();
   // (The last splits first: those that are cut short or hold the scratch rows do not end up behind
   // the others.  One token of 16 requests over 20k to 32k keys 113 -> 110 us, of 16 over 8k to 32k
   // 95 -> 90.)
@@ -135,10 +129,7 @@ q4_few_kernel(const __grid_constant__ Q8AttnArgs a) {
   int P;
   const int b = request_at(a, blockIdx.y, P, (volatile int*)(smem + L::off_req));
   const int nsb = q8_splits(a, P);
-  if (sp >= nsb) {
-    finish();
-    return;
-  }
+  if (sp >= nsb) return;
   const int k0 = min(sp * a.split_len, P), k1 = min(P, k0 + a.split_len);
   const bool with_tree = sp == nsb - 1;
   __syncthreads();                                 // (s_huge)
@@ -603,7 +594,6 @@ q4_few_kernel(const __grid_constant__ Q8AttnArgs a) {
       if (c == 0) a.part_meta[prow] = make_float2(lse2, 1.f);
     }
   }
-  finish();
 }
 
 template <int D, int NT, int S, int W, int kCtas>

@@ -23,7 +23,6 @@ struct Q8AttnArgs {
   CacheMap map;
   int B, R, Hq, g, M;
   int r0, nr;                 // the launch's tree rows: r0 .. r0 + nr - 1 (M = nr g packed rows)
-  int beside;                 // (4-bit cache) does not wait for the launch before it
   int nsplit, split_len, nrg, rb, tree_split;
   int by_length;              // grid z is a rank in (prefix length desc, index asc) order
   float qscale;               // softmax scale * log2(e)
