@@ -1075,3 +1075,95 @@ def test_attention_of_rows_rewritten_right_before(kind, B, R, lens, extra, page)
         for n in range(6):
             assert torch.equal(kept[n][0], want[n % 3][0]) and torch.equal(kept[n][1], want[n % 3][1]), n
     assert int(s.err) == 0
+
+
+def check_tight(s, out, lse, requests=None, heads=None):
+    """The bounds of check_attn for bf16 inputs, with each error at its own weight.  A run is 128 cached
+    rows from a multiple of 128 (a scratch row is one of its own), S_k the largest |scale| of the run of
+    key k (the largest element of the scratch row), p_k the key's probability.  A value is held to
+    2^-12 and 2^-15 S_k, which costs sum_k p_k 2^-15 S_k.  A probability is held to 2^-12 and half a
+    step 2^-24 where the largest p_k 2^E_k (2^E_k <= 2 S_k) is 1 or more: with |v| < 8 2^E_k, a cached key
+    adds 8 2^-25 2 max_k p_k S_k at most.  A scratch row's value is held over 2^-18 of its largest element
+    or less, relative to 2^E: its weight's half step is worth 2^-14 2 max_k p_k S_k."""
+    g = s.Hq // s.Hkv
+    for b in requests if requests is not None else range(s.B):
+        P = min(s.lens[b], s.cap)
+        sees = torch.cat([torch.ones(s.R, P, dtype=torch.bool, device=DEV), s.sees(b)], 1).repeat_interleave(g, 0)
+        for h in heads if heads is not None else range(s.Hkv):
+            ck, cv = s.cache("k"), s.cache("v")
+            kt, vt = s.kt[b, :, h].double(), s.vt[b, :, h].double()
+            k, v = torch.cat([ck.values(b, h)[:P], kt]), torch.cat([cv.values(b, h)[:P], vt])
+
+            def by_run(x):
+                x = x[:P].abs().amax(-1)
+                x = torch.cat([x, x.new_zeros(-P % 128)]).view(-1, 128).amax(-1)
+                return x.repeat_interleave(128)[:P]
+
+            Sk = torch.cat([by_run(ck.scales(b, h)), kt.abs().amax(-1)])
+            Sv = torch.cat([by_run(cv.scales(b, h)), vt.abs().amax(-1)])
+            wide = torch.cat([16 * ck.scales(b, h)[:P].abs().repeat_interleave(G, 1), kt.abs()])
+            q = s.q[b, :, h * g:(h + 1) * g].double().reshape(-1, s.d)
+            x = (q @ k.T * s.scale).masked_fill(~sees, -INF)
+            l = torch.logsumexp(x, -1)
+            p = torch.exp(x - l[:, None])
+            n = k.shape[0]
+            # scores, each weighted by its key: off by ds_k, so a mean of v by at most twice sum_k p_k ds_k |v_k|
+            qa = q.abs()
+            ds = (s.d + 16) * 2.0 ** -23 * s.scale * (qa @ wide.T) + s.scale * (
+                2.0 ** -12 * (qa @ k.abs().T) + 2.0 ** -15 * qa.sum(-1, keepdim=True) * Sk)
+            mean = (p * ds).sum(-1, keepdim=True)
+            o, A = p @ v, p @ v.abs()
+            top = (p * Sv).amax(-1, keepdim=True)
+            tol = 2.0 ** -8 * o.abs() + 1.1 * ((p * ds) @ v.abs() + mean * A) + \
+                (3 * 2.0 ** -12 + 2.0 ** -19 + n * 2.0 ** -23) * A + 2.0 ** -15 * (p @ Sv)[:, None] + \
+                (n * 2.0 ** -21 + s.R * 2.0 ** -13) * top + 1e-37
+            got = out[b, :, h * g:(h + 1) * g].double().reshape(-1, s.d)
+            far = (got - o).abs() / tol
+            assert not got.isnan().any() and (far <= 1).all(), (b, h, float(far.max()))
+            gl = lse[b, :, h * g:(h + 1) * g].double().reshape(-1)
+            tl = 1.1 * mean[:, 0] + 2.0 ** -19 + n * 2.0 ** -23 + 2.0 ** -22 * l.abs()
+            far = (gl - l).abs() / tl
+            assert (far <= 1).all(), (b, h, float(far.max()))
+
+
+def _blocks(s, powers, run):
+    """Runs of value scales times 2^power, in turn along the cache (None: zeros)."""
+    f = torch.tensor([0.0 if p is None else 2.0 ** p for p in powers], dtype=torch.float64, device=DEV)
+    at = torch.arange(s.cap, device=DEV) // run % len(powers)
+    for b in range(s.B):
+        for pos in range(0, s.cap, run):
+            pg, row = (b, pos) if s.table is None else (int(s.table[b, pos // s.page]), pos % s.page)
+            part = s.vs[pg, :, row:row + run]
+            part.copy_((part.double() * f[at[pos]]).bfloat16())
+
+
+SPREAD = {"zeros beside 2^30": ([None, 30], 32), "zeros beside 2^100": ([None, 100], 128),
+          "2^100 and zeros": ([100, None, None], 32), "80 apart": ([-40, 40, 0], 32),
+          "160 apart": ([-80, 80], 128), "rising": ([-90, -30, 30, 90], 128), "falling": ([90, 20, -50, -90], 128)}
+
+
+@gpu
+@pytest.mark.parametrize("kind,R,page", [("gqa", 1, 0), ("gqa", 4, 128), ("narrow", 2, 0), ("gqa", 20, 128),
+                                         ("one", 65, 0), ("narrow", 12, 256)])
+@pytest.mark.parametrize("name", SPREAD)
+def test_attention_counts_keys_whatever_their_values_size(kind, R, page, name):
+    """Runs of values that are zero or 2^80 and more apart: every key counts in the sum of weights."""
+    for tree in (1.0, 0.0, 2.0 ** 100):
+        s = Setup(kind, 3, R, [700, 130, 33], page=page, seed=82)
+        _blocks(s, *SPREAD[name])
+        s.vt *= tree
+        s.check_attn(*s.attn())
+        check_tight(s, *s.attn())
+    assert int(s.err) == 0
+
+
+@gpu
+@pytest.mark.parametrize("kind,R", [("gqa", 1), ("gqa", 4), ("narrow", 2)])
+def test_attention_counts_keys_of_large_scores_beside_large_values(kind, R):
+    """Scores that rise and fall by a hundred while the values' size does the opposite, over several splits."""
+    s = Setup(kind, 2, R, [6000, 900], seed=83)
+    ramp = torch.exp2(3 * torch.sin(torch.arange(s.rows, device=DEV) / 150.0)).bfloat16()
+    s.ks *= ramp[:, None]
+    _blocks(s, [100, 60, 20, -20, -60, -90, None, 0], 64)
+    s.check_attn(*s.attn())
+    check_tight(s, *s.attn())

@@ -21,7 +21,8 @@
 //   V   fp16, one fused multiply-add: (c - 8) s 2^(-E - 9), E the exponent above the chunk's
 //       largest scale: 2^-12, or 2^-25 (2^-15 of the chunk's largest scale) where that is more.
 //   P   fp16: 2^(x + E - m), m a running bound of x + E over the warp's keys (raised
-//       where a chunk passes it by 8): 2^-12, and steps of 2^-24.
+//       where a chunk passes it by 8): 2^-12, and steps of 2^-24.  Its sum has a bound of its
+//       own (kQ4Near).
 //   scratch rows: fp32 on the CUDA cores, a warp per packed row, while the first chunks are
 //       under way.
 // Each warp's sum, bound and output are joined at the end, in fp32.
@@ -62,8 +63,8 @@ struct FewLayout {
   static constexpr int pitch = D + 4;              // floats of a row in the joint
   static constexpr uint32_t joint = W * NT * 8 * pitch * 4;
   static constexpr uint32_t off_tree = ring > joint ? ring : joint;     // float [8 NT][D]
-  static constexpr uint32_t off_ml = off_tree + NT * 8 * D * 4;         // float2 [W + 1][8 NT]
-  static constexpr uint32_t off_q = off_ml + (W + 1) * NT * 8 * 8;      // uint4 [NT][NG][32]: B operands
+  static constexpr uint32_t off_ml = off_tree + NT * 8 * D * 4;         // float4 [W + 1][8 NT]: m, l, u
+  static constexpr uint32_t off_q = off_ml + (W + 1) * NT * 8 * 16;     // uint4 [NT][NG][32]: B operands
   static constexpr uint32_t off_qs = off_q + NT * NG * 32 * 16;         // float [NT][NG][8]: -8 times their sums
   static constexpr uint32_t off_c2 = off_qs + NT * NG * 8 * 4;          // float [8 NT]: factor of the scores
   static constexpr uint32_t off_req = off_c2 + NT * 8 * 4;              // request, its length; a huge row
@@ -247,7 +248,7 @@ q4_few_kernel(const __grid_constant__ Q8AttnArgs a) {
 
   // --------------------------------------------------------- scratch rows
   float* const tree_o = (float*)(smem + L::off_tree);
-  float2* const s_ml = (float2*)(smem + L::off_ml);
+  float4* const s_ml = (float4*)(smem + L::off_ml);
   if (with_tree) {
     constexpr int E = D / 32;                      // dims of a lane
 #pragma unroll 1
@@ -304,7 +305,7 @@ q4_few_kernel(const __grid_constant__ Q8AttnArgs a) {
       }
 #pragma unroll
       for (int i = 0; i < E; ++i) tree_o[n * D + lane * E + i] = o[i] * 0.001953125f;   // 2^-9
-      if (lane == 0) s_ml[W * NT * 8 + n] = make_float2(m, l);
+      if (lane == 0) s_ml[W * NT * 8 + n] = make_float4(m, l, m, 0.f);
     }
   }
 
@@ -340,6 +341,10 @@ q4_few_kernel(const __grid_constant__ Q8AttnArgs a) {
       ob[nt][i] = pack_bf16x2(x[0], x[1]);
     }
   const uint8_t* const mine = smem + warp * (S * L::stage);
+  // The exponents of the sums' bounds, a byte for each of the lane's columns, from the first chunk on
+  // whose E is far from 0 (kQ4Near).
+  uint32_t eus = 0;
+  float head = kOverflow;                          // (then -inf: every chunk raises the bounds)
   int slot = 0;
 #pragma unroll 1
   for (int c = warp; c < last; c += W) {
@@ -403,6 +408,7 @@ q4_few_kernel(const __grid_constant__ Q8AttnArgs a) {
     // the exponent above the chunk's largest value scale
     const uint8_t* const sv = st + 2 * L::codes + L::scales;
     int E;
+    float down;                                    // weights as terms of the sum
     {
       constexpr int kWords = NG / 2;
       uint32_t w[kWords], top = 0;
@@ -416,22 +422,27 @@ q4_few_kernel(const __grid_constant__ Q8AttnArgs a) {
 #pragma unroll
       for (int i = 0; i < kWords; ++i) top = __vmaxu2(top, w[i] & 0x7fff7fffu);
       top = __reduce_max_sync(kFull, max(top & 0xffffu, top >> 16));
-      if (top >= 0x7f80u) {                        // (not the scales that are not finite)
-        top = 0;
+      E = (int)(top >> 7) - 126;
+      // (far from 0, or scales that are not finite)
+      if (__builtin_expect(top - ((126u - kQ4Near) << 7) >= (2u * kQ4Near + 1u) << 7, 0)) {
+        if (top >= 0x7f80u) {
+          top = 0;
 #pragma unroll
-        for (int i = 0; i < kWords; ++i) {
-          const uint32_t lo = w[i] & 0x7fffu, hi = w[i] >> 16 & 0x7fffu;
-          top = max(top, max(lo < 0x7f80u ? lo : 0u, hi < 0x7f80u ? hi : 0u));
+          for (int i = 0; i < kWords; ++i) {
+            const uint32_t lo = w[i] & 0x7fffu, hi = w[i] >> 16 & 0x7fffu;
+            top = max(top, max(lo < 0x7f80u ? lo : 0u, hi < 0x7f80u ? hi : 0u));
+          }
+          top = __reduce_max_sync(kFull, top);
         }
-        top = __reduce_max_sync(kFull, top);
+        E = top == 0u ? 0 : min(max((int)(top >> 7) - 126, kQ4MinExp), kQ4MaxExp);   // (zeros: at any)
+        if (abs(E) > kQ4Near) head = -INFINITY;
       }
-      E = min(max((int)(top >> 7) - 126, kQ4MinExp), kQ4MaxExp);
+      down = q8_scale(127 - E);
     }
     const float fE = (float)E;
 
     // P, in the layout of the scores
     uint32_t pb[NT][H][2];
-    const float down = q8_scale(127 - E);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       if (huge) {
@@ -455,15 +466,26 @@ q4_few_kernel(const __grid_constant__ Q8AttnArgs a) {
 #pragma unroll
       for (int x = 0; x < 2; ++x)
         top[x] = max3f(fmaxf(s[nt][0][x], s[nt][0][x + 2]), s[nt][1][x], s[nt][1][x + 2]);
-      if (__any_sync(kFull, !(top[0] <= m[nt][0] + kOverflow) || !(top[1] <= m[nt][1] + kOverflow))) {
+      if (__any_sync(kFull, !(top[0] <= m[nt][0] + head) || !(top[1] <= m[nt][1] + head))) {
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
 #pragma unroll
           for (int o = 4; o < 32; o <<= 1) top[x] = fmaxf(top[x], __shfl_xor_sync(kFull, top[x], o));
           const float mn = fmaxf(m[nt][x], top[x]);
           const float al = ex2(m[nt][x] - mn);
+          if (head < 0.f) {                          // the sum of the chunk on its own
+            down = 0.f;
+            const int at = 8 * (2 * nt + x);
+            const float e0 = (float)(int8_t)(eus >> at), e = q4_near(m[nt][x], e0, mn, top[x] - fE);
+            eus = (eus & ~(255u << at)) | ((uint32_t)(int)e & 255u) << at;
+            l[nt][x] *= ex2((m[nt][x] - mn) + (e - e0));
+#pragma unroll
+            for (int h = 0; h < H; ++h)
+              l[nt][x] += ex2((s[nt][h][x] - mn) + (e - fE)) + ex2((s[nt][h][x + 2] - mn) + (e - fE));
+          } else {
+            l[nt][x] *= al;
+          }
           m[nt][x] = mn;
-          l[nt][x] *= al;
 #pragma unroll
           for (int i = 0; i < NW * 4; ++i) {
             acc[nt][i][x] *= al;
@@ -538,8 +560,6 @@ q4_few_kernel(const __grid_constant__ Q8AttnArgs a) {
 
   // ------------------------------------------------------------- the joint
   asm volatile("cp.async.wait_group 0;\n" ::: "memory");
-  __syncthreads();                                 // the ring has been read
-  float* const s_o = (float*)smem;
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -547,42 +567,57 @@ q4_few_kernel(const __grid_constant__ Q8AttnArgs a) {
       float sum = l[nt][x];
 #pragma unroll
       for (int o = 4; o < 32; o <<= 1) sum += __shfl_xor_sync(kFull, sum, o);
-      const int n = nt * 8 + 2 * t + x;
-      if (g == 0) s_ml[warp * NT * 8 + n] = make_float2(m[nt][x] == kNone ? -INFINITY : m[nt][x], sum);
-      float* const dst = s_o + (warp * NT * 8 + n) * L::pitch + 8 * NW * g;
+      const float top = m[nt][x] == kNone ? -INFINITY : m[nt][x];
+      const float e = (float)(int8_t)(eus >> 8 * (2 * nt + x));
+      if (g == 0) s_ml[warp * NT * 8 + nt * 8 + 2 * t + x] = make_float4(top, sum, top - e, 0.f);
+    }
+  __syncthreads();                                 // the ring has been read
+  float* const s_o = (float*)smem;
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      float* const dst = s_o + (warp * NT * 8 + nt * 8 + 2 * t + x) * L::pitch + 8 * NW * g;
 #pragma unroll
       for (int i = 0; i < NW * 4; ++i)
         *(float2*)(dst + 2 * i) = make_float2(acc[nt][i][x], acc[nt][i][x + 2]);
     }
+  // A row's W + 1 parts, on sixteen lanes: the factor of each one's output.
+  static_assert(W < 16, "a lane per part");
+  for (int i = tid; i < NT * 8 * 16; i += W * 32) {   // (whole warps)
+    const int n = i / 16, w = i % 16;
+    const bool there = w < W || (w == W && with_tree);
+    const float4 ml = there ? s_ml[w * NT * 8 + n] : make_float4(-INFINITY, 0.f, -INFINITY, 0.f);
+    float top = ml.x, near = ml.z;                 // bounds of the products, and of the sums
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) {
+      top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
+      near = fmaxf(near, __shfl_xor_sync(kFull, near, o));
+    }
+    // (no bound: nothing seen, or scores that are all NaN)
+    const bool none = ml.x == -INFINITY;
+    const float f = none ? (ml.y != ml.y ? ml.y : 0.f) : ex2(ml.x - top);
+    float total = none ? f : ex2(ml.z - near) * ml.y;
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) total += __shfl_xor_sync(kFull, total, o);
+    if (there) s_ml[w * NT * 8 + n] = make_float4(f * q4_over(9.f + (top - near), total), 0.f, near, total);
+  }
   __syncthreads();
   for (int i = tid; i < a.M * (D / 2); i += W * 32) {
     const int n = i / (D / 2), c = i % (D / 2) * 2;
-    float2 ml[W + 1];
-    float top = -INFINITY;
-#pragma unroll
-    for (int w = 0; w <= W; ++w) {
-      ml[w] = w < W || with_tree ? s_ml[w * NT * 8 + n] : make_float2(-INFINITY, 0.f);
-      top = fmaxf(top, ml[w].x);
-    }
-    float total = 0.f;
     float2 o = make_float2(0.f, 0.f);
 #pragma unroll
     for (int w = 0; w <= W; ++w) {
       if (w == W && !with_tree) break;
-      // (no bound: nothing seen, or scores that are all NaN)
-      const float f = ml[w].x == -INFINITY ? (ml[w].y != ml[w].y ? ml[w].y : 0.f) : ex2(ml[w].x - top);
+      const float f = s_ml[w * NT * 8 + n].x;
       const float2 x = w < W ? *(const float2*)(s_o + (w * NT * 8 + n) * L::pitch + c)
                              : *(const float2*)(tree_o + n * D + c);
-      total = fmaf(f, ml[w].y, total);
       if (f != 0.f) {
         o.x = fmaf(f, x.x, o.x);
         o.y = fmaf(f, x.y, o.y);
       }
     }
-    const float inv = total == 0.f ? 0.f : 512.f / total;
-    o.x *= inv;
-    o.y *= inv;
-    const float lse2 = top + log2f(total);
+    const float lse2 = s_ml[n].z + log2f(s_ml[n].w);
     const int tr = a.r0 + n / a.g, qh = hk * a.g + n % a.g;
     if (nsb == 1) {
       const long orow = ((long)b * a.R + tr) * a.Hq + qh;

@@ -19,7 +19,7 @@
 //          down to 2^-29 of it
 //   tree   scratch rows of K and V in fp16, each times a power of two of its own
 //   P      fp16: 2^(x + E - m + 7), m a running bound of x + E: 2^-12, and steps of 2^-24, 2^-39
-//          of the largest
+//          of the largest.  Its sum has a bound of its own (kQ4Near).
 // A score's factor takes the tile's and the row's power of two in fp32.
 //
 // Roles (640 threads): warps 0-3 and 4-7 softmax and epilogue; warp 8 issues the products
@@ -79,12 +79,14 @@ struct RowLayout {
   static constexpr uint32_t off_k = 0;
   static constexpr uint32_t off_v = kStages * t_bytes;
   static constexpr uint32_t off_f = off_v + kStages * t_bytes;         // fp16 [ring][K, V][128][NG]
-  static constexpr uint32_t off_ml = off_f + kScaleRing * 2 * f_bytes; // float2[2][128] (m, l)
-  static constexpr uint32_t off_rows = off_ml + 16 * kRows;            // i64[kMaxTiles]
+  static constexpr uint32_t off_ml = off_f + kScaleRing * 2 * f_bytes; // float4[2][128] (m, l, u)
+  static constexpr uint32_t off_eu = off_ml + 32 * kRows;              // float[2][128] (kQ4Near)
+  static constexpr uint32_t off_rows = off_eu + 8 * kRows;             // i64[kMaxTiles]
   static constexpr uint32_t off_tree = off_rows + 8 * kMaxTiles;       // 4 x 32 bits [128]
   static constexpr uint32_t off_ek = off_tree + 16 * kKeys;            // i8[kMaxTiles]: E of K
   static constexpr uint32_t off_ev = off_ek + kMaxTiles;               // and of V
-  static constexpr uint32_t off_bar = off_ev + kMaxTiles;
+  static constexpr uint32_t off_near = off_ev + kMaxTiles;             // float[kMaxTiles]: E of V, or NaN
+  static constexpr uint32_t off_bar = off_near + 4 * kMaxTiles;
   static constexpr int nbar = 32;
   static constexpr uint32_t off_flags = off_bar + 8 * nbar;            // tmem, abort
   static constexpr uint32_t off_top = off_flags + 8;                   // int[2 kWideWarps]
@@ -268,7 +270,7 @@ struct Scales {
         }
       top = __reduce_max_sync(kFull, top);
     }
-    return min(max((int)(top >> 7) - 126, kQ4MinExp), kQ4MaxExp);
+    return top == 0u ? 0 : min(max((int)(top >> 7) - 126, kQ4MinExp), kQ4MaxExp);   // (zeros: at any)
   }
   // s 2^(15 - E) in fp16: exact down to 2^-29 2^E
   __device__ __forceinline__ void store(uint8_t* dst, int E, int lane) const {
@@ -291,7 +293,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_rows_kernel(const __grid_const
   const uint32_t raw = su32(smem_raw);
   const uint32_t sbase = (raw + 1023u) & ~1023u;
   uint8_t* smem = smem_raw + (sbase - raw);
-  float2* s_ml = (float2*)(smem + L::off_ml);
+  float4* s_ml = (float4*)(smem + L::off_ml);
   long long* tile_row = (long long*)(smem + L::off_rows);
   float* kt_in = (float*)(smem + L::off_tree);      // tree rows: factors into fp16 (0: row of zeros)
   float* vt_in = kt_in + kKeys;
@@ -299,6 +301,9 @@ __global__ void __launch_bounds__(kThreads, 1) q4_rows_kernel(const __grid_const
   int* vt_u = (int*)(kt_out + kKeys);               // exponent of the value row
   volatile int8_t* ek = (volatile int8_t*)(smem + L::off_ek);
   volatile int8_t* ev = (volatile int8_t*)(smem + L::off_ev);
+  // E of V; NaN from the first tile on whose E is far from 0 (kQ4Near), so that the softmax meets those
+  // tiles where it raises its bounds
+  volatile float* e_near = (volatile float*)(smem + L::off_near);
   volatile uint32_t* flags = (volatile uint32_t*)(smem + L::off_flags);
   int* s_top = (int*)(smem + L::off_top);           // largest exponent of a scratch value row, by warp
   const uint32_t bar0 = sbase + L::off_bar;
@@ -492,6 +497,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_rows_kernel(const __grid_const
     // --------------------------------------------------------------- scales
     if (warp == kScaleK || warp == kScaleV) {
       volatile int8_t* const e_of = of_v ? ev : ek;
+      bool far_off = false;
       auto one_tile = [&](int t, Scales<D>& s) -> bool {
         if (lane == 0) {                             // codes and scales of the tiles to come
           for (int i = t == 0 ? 2 : t + kPrefetch - 1; i < t + kPrefetch && i < n_pre; ++i)
@@ -506,7 +512,11 @@ __global__ void __launch_bounds__(kThreads, 1) q4_rows_kernel(const __grid_const
             !__all_sync(kFull, wait_ready(bar(BAR_F_EMPTY + t % kScaleRing), (t / kScaleRing - 1) & 1)))
           return false;
         s.store(factors(t, of_v), E, lane);
-        if (lane == 0) e_of[t] = (int8_t)E;
+        far_off |= abs(E) > kQ4Near;
+        if (lane == 0) {
+          e_of[t] = (int8_t)E;
+          if (of_v) e_near[t] = far_off ? __int_as_float(0x7fffffff) : (float)E;
+        }
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(BAR_F_FULL + t % kScaleRing));
         if (t + 2 < n_pre) load_scales(s, tile_row[t + 2], valid_of(t + 2));
@@ -595,26 +605,43 @@ __global__ void __launch_bounds__(kThreads, 1) q4_rows_kernel(const __grid_const
     set_registers<kSoftRegs, true>();
     const int p = warp >> 2, q = warp & 3, row = q * 32 + lane;
     const uint32_t lane_off = (uint32_t)(q * 32) << 16;
-    float m = -INFINITY, l = 0.f;
-    int top_e = kQ4MinExp;                         // the largest E of V met
+    float m = -INFINITY, l = 0.f;                  // l: over 2^(m - eu)
+    float* const eu = (float*)(smem + L::off_eu) + p * kRows + row;
+    *eu = 0.f;
+    float top_e = kQ4MinExp;                       // the largest E of V met
     bool failed = false;
     if (q < live_warps) {
       // The stream's product of the tile before: done before its P is written over
       // or its accumulator is rescaled.
       bool done = true, far = false;             // far: a bound whose last bit is worth something
+      float own = -(float)kHeadroom;             // -inf: tiles' sums are computed on their own (kQ4Near)
       auto product_done = [&](int t) -> bool {
         return __all_sync(kFull, done || wait_ready(bar(BAR_PV_DONE + p), (t - 1) & 1));
       };
-      // The bound is raised to X where X passes m by the headroom (or m is none), the sum
-      // and the accumulator are rescaled.
-      auto raise = [&](float X, int t) -> bool {
-        const bool need = !(X <= m + kOverflow);
-        if (__builtin_expect(!__any_sync(kFull, need), 1)) return true;
+      // The bound is raised to X = f top + E, top the largest of v, where X passes m by the headroom (or
+      // m is none), the sum and the accumulator are rescaled.  E is NaN where it is far from 0, and
+      // becomes far_E.
+      auto raise = [&](const float (&v)[64], float f, float top, float& fE, int t, auto far_E) -> bool {
+        if (__builtin_expect(!__any_sync(kFull, !(fmaf(f, top, fE) <= m + kOverflow)), 1)) return true;
         if (!product_done(t)) return false;
+        if (fE != fE) {
+          own = -INFINITY;
+          fE = far_E();
+        }
+        const float X = fmaf(f, top, fE);
+        const bool need = !(X <= m + kOverflow);
         const float m_new = need ? fmaxf(m, X) : m;
         const float al = m_new == m ? 1.f : m == -INFINITY ? 0.f : ex2(m - m_new);
+        if (own == -INFINITY) {
+          const float e0 = *eu, e = q4_near(m, e0, m_new, X - fE), base = m_new == -INFINITY ? 0.f : m_new;
+          l *= m == -INFINITY ? 0.f : ex2((m - m_new) + (e - e0));
+#pragma unroll
+          for (int i = 0; i < 64; ++i) l += ex2((fmaf(v[i], f, fE) - base) + (e - fE));
+          *eu = e;
+        } else {
+          l *= al;
+        }
         m = m_new;
-        l *= al;
         far = __any_sync(kFull, fabsf(m) > 1048576.f && m != -INFINITY);
         if (t == 0) return true;
         fence_after();
@@ -653,17 +680,18 @@ __global__ void __launch_bounds__(kThreads, 1) q4_rows_kernel(const __grid_const
         float v[64];
         tmem_ld32(ts, *(float(*)[32])v);
         tmem_ld32(ts + 32, *(float(*)[32])(v + 32));
-        int E, eK = 0;
+        int tree_E = 0, eK = 0;
+        float fE;
         if constexpr (is_tree) {
-          E = s_top[0];
+          tree_E = s_top[0];
 #pragma unroll
-          for (int i = 1; i < 2 * kWideWarps; ++i) E = max(E, s_top[i]);
-          E = min(max(E - 9, kQ4MinExp), kQ4MaxExp);
+          for (int i = 1; i < 2 * kWideWarps; ++i) tree_E = max(tree_E, s_top[i]);
+          tree_E = min(max(tree_E - 9, kQ4MinExp), kQ4MaxExp);
+          fE = own == -INFINITY || abs(tree_E) > kQ4Near ? __int_as_float(0x7fffffff) : (float)tree_E;
         } else {
-          E = ev[t];
+          fE = e_near[t];
           eK = ek[t];
         }
-        top_e = max(top_e, E);
         tmem_wait_ld();
         scores_read();
         // x + E = f v + E.  (f not 0, so that -inf stays -inf.)
@@ -698,8 +726,10 @@ __global__ void __launch_bounds__(kThreads, 1) q4_rows_kernel(const __grid_const
         for (int i = 0; i < 64; i += 8)
 #pragma unroll
           for (int j = 0; j < 4; ++j) top[j] = max3f(top[j], v[i + 2 * j], v[i + 2 * j + 1]);
-        const float fE = (float)E;
-        if (!raise(fmaf(f, fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])), fE), t)) return false;
+        if (!raise(v, f, fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])), fE, t,
+                   [&] { return (float)(is_tree ? tree_E : ev[t]); }))
+          return false;
+        top_e = fmaxf(top_e, fE);
         float off = fE + (float)kHeadroom - (m == -INFINITY ? 0.f : m);
         if (t > 0) done = complete(bar(BAR_PV_DONE + p), (t - 1) & 1);   // (looked at a while before it is needed)
         if (__builtin_expect(far, 0)) {            // rounded as the bound was, not fused with it
@@ -724,10 +754,10 @@ __global__ void __launch_bounds__(kThreads, 1) q4_rows_kernel(const __grid_const
               sb = __fadd2_rn(sb, pb);
               if constexpr (decltype(scaled)::value) {
                 const int4 u = *(const int4*)(vt_u + 64 * h + c + i);
-                pa.x *= pow2i(u.x - 9 - E);
-                pa.y *= pow2i(u.y - 9 - E);
-                pb.x *= pow2i(u.z - 9 - E);
-                pb.y *= pow2i(u.w - 9 - E);
+                pa.x *= pow2i(u.x - 9 - tree_E);
+                pa.y *= pow2i(u.y - 9 - tree_E);
+                pb.x *= pow2i(u.z - 9 - tree_E);
+                pb.y *= pow2i(u.w - 9 - tree_E);
               }
               w[i / 2] = pack_half2(pa.x, pa.y);
               w[i / 2 + 1] = pack_half2(pb.x, pb.y);
@@ -742,7 +772,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_rows_kernel(const __grid_const
           return true;
         };
         if (!weights(tree)) return false;
-        l = fmaf((sa.x + sa.y) + (sb.x + sb.y), pow2i(-E - kHeadroom), l);
+        l = fmaf((sa.x + sa.y) + (sb.x + sb.y), ex2(own - fE), l);
         tmem_wait_st();
         fence_before();
         __syncwarp();
@@ -756,7 +786,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_rows_kernel(const __grid_const
     // ------------------------------------- epilogue: the two streams joined
     const bool ok = !failed && __all_sync(kFull, wait_timed(bar(BAR_O_DONE), 0));
     fence_after();
-    s_ml[p * kRows + row] = make_float2(m, l);
+    s_ml[p * kRows + row] = make_float4(m, l, m - *eu, 0.f);
     uint32_t stop;
     asm volatile(
         "{\n .reg .pred pi, po;\n setp.ne.u32 pi, %1, 0;\n"
@@ -765,16 +795,17 @@ __global__ void __launch_bounds__(kThreads, 1) q4_rows_kernel(const __grid_const
         : "r"((uint32_t)(!ok || flags[1] != 0))
         : "memory");
     if (stop == 0 && q < live_warps) {
-      const float2 s0 = s_ml[row], s1 = s_ml[kRows + row];
-      const float top = fmaxf(s0.x, s1.x);
-      const float w0 = s0.x == -INFINITY ? (s0.y != s0.y ? s0.y : 0.f) : ex2(s0.x - top);
-      const float w1 = s1.x == -INFINITY ? (s1.y != s1.y ? s1.y : 0.f) : ex2(s1.x - top);
-      const float total = w0 * s0.y + w1 * s1.y;
+      const float4 s0 = s_ml[row], s1 = s_ml[kRows + row];
+      const float top = fmaxf(s0.x, s1.x), near = fmaxf(s0.z, s1.z);   // of the products, of the sums
+      const bool none0 = s0.x == -INFINITY, none1 = s1.x == -INFINITY;
+      const float w0 = none0 ? (s0.y != s0.y ? s0.y : 0.f) : ex2(s0.x - top);
+      const float w1 = none1 ? (s1.y != s1.y ? s1.y : 0.f) : ex2(s1.x - top);
+      const float total = (none0 ? w0 : ex2(s0.z - near)) * s0.y + (none1 ? w1 : ex2(s1.z - near)) * s1.y;
       // An output is below 2^(top_e + 3) (tree rows: 2^(top_e + 18)), or it is held over that
       // where it goes to a split's fp16.  (top_e is the same for a warp's rows and both streams.)
-      const float unit = pow2i(top_e + 3), inv = pow2i(9 - kHeadroom) / total;
-      const float g0 = w0 * inv, g1 = w1 * inv, down = pow2i(-top_e - 3);
-      const float lse2 = top + log2f(total);
+      const float unit = pow2i((int)top_e + 3), inv = q4_over((float)(9 - kHeadroom) + (top - near), total);
+      const float g0 = w0 * inv, g1 = w1 * inv, down = pow2i(-(int)top_e - 3);
+      const float lse2 = near + log2f(total);
       const int pr = row_base + min(row, rows_here - 1);
       const int tr = pr / a.g, qh = hk * a.g + pr % a.g;
       const long orow = ((long)b * a.R + tr) * a.Hq + qh;
