@@ -1158,7 +1158,7 @@ def test_attention_counts_keys_whatever_their_values_size(kind, R, page, name):
 
 
 @gpu
-@pytest.mark.parametrize("kind,R", [("gqa", 1), ("gqa", 4), ("narrow", 2)])
+@pytest.mark.parametrize("kind,R", [("gqa", 1), ("gqa", 4), ("narrow", 2), ("narrow", 12), ("gqa", 20)])
 def test_attention_counts_keys_of_large_scores_beside_large_values(kind, R):
     """Scores that rise and fall by a hundred while the values' size does the opposite, over several splits."""
     s = Setup(kind, 2, R, [6000, 900], seed=83)
@@ -1167,3 +1167,29 @@ def test_attention_counts_keys_of_large_scores_beside_large_values(kind, R):
     _blocks(s, [100, 60, 20, -20, -60, -90, None, 0], 64)
     s.check_attn(*s.attn())
     check_tight(s, *s.attn())
+
+
+def _shunned(s, pos, power):
+    """A run of 128 cached rows whose weight is nothing (scores below -150) and whose values are 2^power."""
+    s.q[..., 0] = 8.0
+    for b in range(s.B):
+        if s.lens[b] < pos + 128:
+            continue
+        pg, row = (b, pos) if s.table is None else (int(s.table[b, pos // s.page]), pos % s.page)
+        s.ks[pg, :, row:row + 128, 0] = 64.0
+        s.k[pg, :, row:row + 128, 1:16] = 0x88
+        s.k[pg, :, row:row + 128, 0] = 0x80     # dim 0: code 0, -8 s; the other dims of the group: 0
+        s.vs[pg, :, row:row + 128] = 2.0 ** power
+
+
+@gpu
+@pytest.mark.parametrize("kind,R,page,lens", [("gqa", 20, 128, [5000, 700]), ("one", 30, 0, [4000]),
+                                              ("narrow", 12, 0, [6000, 400]), ("gqa", 65, 128, [20000, 300]),
+                                              ("gqa", 4, 0, [5000]), ("narrow", 1, 128, [6000])])
+@pytest.mark.parametrize("power", [16, 22, 30, 100])
+def test_attention_keeps_small_values_beside_large_ones_of_no_weight(kind, R, page, lens, power):
+    """Also where the large ones are in the same split."""
+    s = Setup(kind, len(lens), R, lens, page=page, seed=84)
+    _shunned(s, 256, power)
+    check_tight(s, *s.attn())
+    assert int(s.err) == 0

@@ -608,7 +608,6 @@ __global__ void __launch_bounds__(kThreads, 1) q4_rows_kernel(const __grid_const
     float m = -INFINITY, l = 0.f;                  // l: over 2^(m - eu)
     float* const eu = (float*)(smem + L::off_eu) + p * kRows + row;
     *eu = 0.f;
-    float top_e = kQ4MinExp;                       // the largest E of V met
     bool failed = false;
     if (q < live_warps) {
       // The stream's product of the tile before: done before its P is written over
@@ -729,7 +728,6 @@ __global__ void __launch_bounds__(kThreads, 1) q4_rows_kernel(const __grid_const
         if (!raise(v, f, fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])), fE, t,
                    [&] { return (float)(is_tree ? tree_E : ev[t]); }))
           return false;
-        top_e = fmaxf(top_e, fE);
         float off = fE + (float)kHeadroom - (m == -INFINITY ? 0.f : m);
         if (t > 0) done = complete(bar(BAR_PV_DONE + p), (t - 1) & 1);   // (looked at a while before it is needed)
         if (__builtin_expect(far, 0)) {            // rounded as the bound was, not fused with it
@@ -801,39 +799,66 @@ __global__ void __launch_bounds__(kThreads, 1) q4_rows_kernel(const __grid_const
       const float w0 = none0 ? (s0.y != s0.y ? s0.y : 0.f) : ex2(s0.x - top);
       const float w1 = none1 ? (s1.y != s1.y ? s1.y : 0.f) : ex2(s1.x - top);
       const float total = (none0 ? w0 : ex2(s0.z - near)) * s0.y + (none1 ? w1 : ex2(s1.z - near)) * s1.y;
-      // An output is below 2^(top_e + 3) (tree rows: 2^(top_e + 18)), or it is held over that
-      // where it goes to a split's fp16.  (top_e is the same for a warp's rows and both streams.)
-      const float unit = pow2i((int)top_e + 3), inv = q4_over((float)(9 - kHeadroom) + (top - near), total);
-      const float g0 = w0 * inv, g1 = w1 * inv, down = pow2i(-(int)top_e - 3);
+      const float inv = q4_over((float)(9 - kHeadroom) + (top - near), total);
+      const float g0 = w0 * inv, g1 = w1 * inv;
       const float lse2 = near + log2f(total);
       const int pr = row_base + min(row, rows_here - 1);
       const int tr = pr / a.g, qh = hk * a.g + pr % a.g;
       const long orow = ((long)b * a.R + tr) * a.Hq + qh;
       const long prow = (((long)b * a.Hq + qh) * a.nr + tr) * a.nsplit + sp;
       const bool mine = row < rows_here;
+      // stream p writes the dims [p D/2, (p + 1) D/2)
+      float x[D / 2];
+#pragma unroll
+      for (int c = 0; c < D / 2; c += 32) {
+        float o0[32], o1[32];
+        tmem_ld32(tm_o(0) + lane_off + p * (D / 2) + c, o0);
+        tmem_ld32(tm_o(1) + lane_off + p * (D / 2) + c, o1);
+        tmem_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 32; ++i) x[c + i] = o0[i] * g0 + o1[i] * g1;
+      }
+      // A split's outputs go to fp16 over a power of two of their row, whose largest then lies in
+      // [2^14, 2^15): off by 2^-12 of each, and 2^-39 of the largest.  (In fp32: 8 x 64 rows over 32k keys
+      // 319 instead of 305 us.  One power of two for all rows, from the values' scales, loses rows that
+      // give the largest values no weight.)
+      float unit = 1.f, down = 1.f;
+      if (nsb > 1) {
+        float top2[2] = {0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < D / 2; i += 4)
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+            top2[j] = max3f(top2[j], fabsf(x[i + 2 * j]), fabsf(x[i + 2 * j + 1]));
+        float big = fmaxf(top2[0], top2[1]);
+        if (!(big < INFINITY)) {                   // (of the finite ones)
+          big = 0.f;
+#pragma unroll
+          for (int i = 0; i < D / 2; ++i) big = fmaxf(big, fabsf(x[i]) < INFINITY ? fabsf(x[i]) : 0.f);
+        }
+        s_ml[p * kRows + row].w = big;
+        asm volatile("bar.sync 5, %0;\n" ::"r"(64 * live_warps) : "memory");
+        big = fmaxf(big, s_ml[(1 - p) * kRows + row].w);
+        const int e = big == 0.f ? 0 : max((int)(__float_as_uint(big) >> 23) - 127, -100) - 14;
+        unit = pow2i(e);
+        down = pow2i(-e);
+      }
       if (mine && p == 0) {
         if (nsb == 1) a.lse[orow] = lse2 * 0.69314718055994531f;
         else a.part_meta[prow] = make_float2(lse2, unit);
       }
-      // stream p writes the dims [p D/2, (p + 1) D/2)
-#pragma unroll 1
-      for (int c = p * (D / 2); c < (p + 1) * (D / 2); c += 32) {
-        float o0[32], o1[32];
-        tmem_ld32(tm_o(0) + lane_off + c, o0);
-        tmem_ld32(tm_o(1) + lane_off + c, o1);
-        tmem_wait_ld();
-        uint32_t w[16];
+      if (mine) {
+        uint4* const dst = nsb == 1 ? (uint4*)((__nv_bfloat16*)a.out + orow * D + p * (D / 2))
+                                    : (uint4*)((__half*)a.part_o + prow * D + p * (D / 2));
 #pragma unroll
-        for (int i = 0; i < 32; i += 2) {
-          const float x = o0[i] * g0 + o1[i] * g1, y = o0[i + 1] * g0 + o1[i + 1] * g1;
-          w[i / 2] = nsb == 1 ? pack_bf16x2(x, y) : pack_half2(x * down, y * down);
-        }
-        if (mine) {
-          uint4* dst = nsb == 1 ? (uint4*)((__nv_bfloat16*)a.out + orow * D + c)
-                                : (uint4*)((__half*)a.part_o + prow * D + c);
+        for (int i = 0; i < D / 16; ++i) {
+          uint32_t w[4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            dst[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+          for (int j = 0; j < 4; ++j) {
+            const float y = x[8 * i + 2 * j], z = x[8 * i + 2 * j + 1];
+            w[j] = nsb == 1 ? pack_bf16x2(y, z) : pack_half2(y * down, z * down);
+          }
+          dst[i] = make_uint4(w[0], w[1], w[2], w[3]);
         }
       }
     }
