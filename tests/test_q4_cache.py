@@ -1193,3 +1193,29 @@ def test_attention_keeps_small_values_beside_large_ones_of_no_weight(kind, R, pa
     _shunned(s, 256, power)
     check_tight(s, *s.attn())
     assert int(s.err) == 0
+
+
+@gpu
+@pytest.mark.parametrize("kind,R,dtype", [("gqa", 2, torch.bfloat16), ("gqa", 4, torch.bfloat16),
+                                          ("narrow", 2, torch.bfloat16), ("gqa", 20, torch.bfloat16),
+                                          ("gqa", 3, torch.float32), ("gqa", 20, torch.float32)])
+@pytest.mark.parametrize("lens", [[200, 40, 0, 90], [6000, 5000, 4000, 3000]])
+def test_attention_passes_infinite_scratch_rows_on(kind, R, dtype, lens):
+    """To the rows that see them, and to no others, whatever their scores: of both signs, and in a value
+    whose weight is nothing."""
+    s = Setup(kind, 4, R, lens, dtype=dtype, seed=85)
+    masks = [list(m) for m in s.masks]
+    for m in masks:
+        m[R - 1] = 1 << (R - 2)                     # the last row is seen by itself alone
+    s.set_masks(masks)
+    s.q[..., 0] = s.q[..., 0].abs() + 1
+    s.kt[0, R - 1, :, 0] = -INF
+    s.kt[1, R - 1, :, 0] = INF
+    s.kt[2, R - 1, :, 0] = -20000.0
+    s.vt[2, R - 1, :, 5] = -INF
+    s.kt[3, R - 1, :, 0] = -INF
+    s.vt[3, R - 1, :, 3] = INF
+    out, lse = s.attn()
+    assert out[:, :R - 1].isfinite().all() and lse[:, :R - 1].isfinite().all()
+    assert not out[:, R - 1].isfinite().all(-1).any()
+    assert out[[0, 1, 3], R - 1].isnan().all()

@@ -293,8 +293,14 @@ q4_few_kernel(const __grid_constant__ Q8AttnArgs a) {
         for (int u = 0; u < 4; ++u) {
           const int j = j0 + u;
           if (j >= a.R || !(four >> u & 1u)) continue;
-          const float x = s[u] * a.qscale;
-          if (x == -INFINITY) continue;
+          float x = s[u] * a.qscale;
+          if (x == -INFINITY) {                    // no weight, unless an element is not finite
+            float zero = 0.f;
+#pragma unroll
+            for (int i = 0; i < E; ++i) zero += k[u][i] * 0.f + v[u][i] * 0.f;
+            if (!__any_sync(kFull, zero != 0.f)) continue;
+            x = __int_as_float(0x7fffffff);
+          }
           const float mn = fmaxf(m, x);
           const float al = mn == m ? 1.f : ex2(m - mn), p = ex2(x - mn);
           m = mn;
@@ -612,10 +618,8 @@ q4_few_kernel(const __grid_constant__ Q8AttnArgs a) {
       const float f = s_ml[w * NT * 8 + n].x;
       const float2 x = w < W ? *(const float2*)(s_o + (w * NT * 8 + n) * L::pitch + c)
                              : *(const float2*)(tree_o + n * D + c);
-      if (f != 0.f) {
-        o.x = fmaf(f, x.x, o.x);
-        o.y = fmaf(f, x.y, o.y);
-      }
+      o.x = fmaf(f, x.x, o.x);                     // (0 times an infinity of a scratch value is seen, too)
+      o.y = fmaf(f, x.y, o.y);
     }
     const float lse2 = s_ml[n].z + log2f(s_ml[n].w);
     const int tr = a.r0 + n / a.g, qh = hk * a.g + n % a.g;
