@@ -145,3 +145,17 @@ def test_rotate_tree_serves_the_16_bit_step():
     y, size = plain(proj[:, :, : s.Hq].double(), rope.q_weight, a, s.d, False, True, float(torch.tensor(1e-6)), 1.0)
     assert ((q.double() - y).abs() <= 2.0 ** -8 * y.abs() + (s.d / 2 + 16) * 2.0 ** -24 * size).all()
     assert torch.equal(v, proj[:, :, s.Hq + s.Hkv:])
+
+
+@gpu
+def test_rotate_takes_a_raw_stream_handle():
+    """As the calls around it do, also without buffers for the result; they belong to that stream."""
+    s, step, cache, rope, freq, probs, root, logits, proj = _prepare("gqa", 0, 1)
+    parts = proj.split([s.Hq, s.Hkv, s.Hkv], 2)
+    want = [t.clone() for t in step.rotate_tree(rope, *parts, s.plen)]
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for stream in (side.cuda_stream, side, torch.cuda.current_stream().cuda_stream):
+        got = step.rotate_tree(rope, *parts, s.plen, stream=stream)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))

@@ -132,7 +132,10 @@ class TreeVerifyStep:
         axes, half = rope.turns.shape
         main = stream if stream is not None else torch.cuda.current_stream(q.device)
         if out is None:
-            with torch.cuda.stream(main):
+            own = main
+            if not hasattr(main, "cuda_stream"):      # a raw handle
+                own = torch.cuda.ExternalStream(main, q.device) if main else torch.cuda.default_stream(q.device)
+            with torch.cuda.stream(own):
                 out = tuple(torch.empty(t.shape, dtype=t.dtype, device=t.device) for t in (q, k, v))
         desc = make_rope_desc(B, T, self.Hq, self.Hkv, self.dk, self.dtype, 2 * half, axes,
                               rope.neighbours, rope.norm, rope.eps, rope.amplitude)
