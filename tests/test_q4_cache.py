@@ -1219,3 +1219,65 @@ def test_attention_passes_infinite_scratch_rows_on(kind, R, dtype, lens):
     assert out[:, :R - 1].isfinite().all() and lse[:, :R - 1].isfinite().all()
     assert not out[:, R - 1].isfinite().all(-1).any()
     assert out[[0, 1, 3], R - 1].isnan().all()
+
+
+@gpu
+@pytest.mark.parametrize("R,dtype", [(1, torch.float32), (20, torch.float32)])
+def test_attention_over_prefixes_near_two_to_the_31(R, dtype):
+    """A request of 2^31 - 228 positions: one page again and again, and another as the last one, whose
+    scores are large enough for it to count.  The sums have up to 2^15 + 2^11 terms one after the other,
+    each rounded to 2^-24: off by 2^-8, relatively.  Probabilities in the last split (2^15 keys) are held
+    to half a step 2^-24 of the largest product: 2^15 2^-25 16 max_k p_k S_k."""
+    s = Setup("odd", 1, R, [156], page=128, dtype=dtype, seed=86)
+    pages = (1 << 24) - 1
+    first, end = s.table[0, :2].tolist()
+    s.ks[end] *= 16
+    s.plen.fill_(pages * 128 - 100)
+    table = torch.full((1, pages), first, dtype=torch.int32, device=DEV)
+    table[0, -1] = end
+    s.paging["page_table"] = table
+    s.desc = T.make_desc(1, R, s.Hq, s.Hkv, s.d, s.d, pages * 128, dtype, False, s.scale)
+    out, lse = s.attn()
+    assert int(s.err) == 0
+    ck, cv = s.cache("k"), s.cache("v")                   # (its positions 0..155 are the two pages' rows)
+    k = torch.cat([ck.values(0, 0)[:156], s.kt[0, :, 0].double()])
+    v = torch.cat([cv.values(0, 0)[:156], s.vt[0, :, 0].double()])
+    times = torch.ones(156 + R, dtype=torch.float64, device=DEV)
+    times[:128] = pages - 1
+    sees = torch.cat([torch.ones(R, 156, dtype=torch.bool, device=DEV), s.sees(0)], 1).repeat_interleave(s.Hq, 0)
+    q = s.q[0].double().reshape(-1, s.d)
+    x = (q @ k.T * s.scale + times.log()).masked_fill(~sees, -INF)
+    l = torch.logsumexp(x, -1)
+    p = torch.exp(x - l[:, None])
+    o, A = p @ v, p @ v.abs()
+    wide = torch.cat([16 * ck.scales(0, 0)[:156].abs().repeat_interleave(G, 1), s.kt[0, :, 0].double().abs()])
+    ds = s.scale * (s.d + 16) * 2.0 ** -23 * (q.abs() @ wide.T).masked_fill(~sees, 0).amax(-1, keepdim=True)
+    low, p16, top = 2.0 ** -24, 0.0, torch.zeros_like(ds)
+    if dtype == torch.bfloat16:
+        low, p16 = 2.0 ** -8, 3 * 2.0 ** -12
+        S = torch.cat([cv.scales(0, 0)[:156].abs().amax(-1), s.vt[0, :, 0].double().abs().amax(-1)])
+        Sk = torch.cat([ck.scales(0, 0)[:156].abs().amax(-1), s.kt[0, :, 0].double().abs().amax(-1)])
+        ds = ds + s.scale * (2.0 ** -12 * q.abs() @ k.abs().T + 2.0 ** -15 * q.abs().sum(-1, keepdim=True) * Sk.max()
+                             ).masked_fill(~sees, 0).amax(-1, keepdim=True)
+        top = 2.0 ** -15 * S.max() + 2.0 ** (15 - 25 + 4) * (p / times * S).amax(-1, keepdim=True)
+    tol = low * o.abs() + (2.2 * ds + 2 * 2.0 ** -8 + p16) * A + top
+    far = (out[0].double().reshape(-1, s.d) - o).abs() / tol
+    assert (far <= 1).all(), float(far.max())
+    far = (lse[0].double().reshape(-1) - l).abs() / (1.1 * ds[:, 0] + 2.0 ** -8 + 2.0 ** -22 * l.abs())
+    assert (far <= 1).all(), float(far.max())
+    # an append ends at the last position
+    x, y = s.normal(1, 100, 1, s.d), s.normal(1, 100, 1, s.d)
+    n = torch.tensor([100], dtype=torch.int32, device=DEV)
+    T.tsd_cache_write_q4(s.desc, x, y, n, *s.arrays(), s.plen, s.err, **s.paging)
+    back = _read(s, [pages * 128 - 1], [1], 1)
+    c, f = quantise(x[0, 99].double())
+    assert torch.equal(back[0][0, 0], ((c - 8).double() * f.repeat_interleave(G, 1)).to(dtype))
+    assert int(s.plen) == pages * 128 and int(s.err) == 0
+
+
+def test_workspaces_of_the_largest_caches_by_type():
+    """At most 2^15 positions a split of bf16 inputs, 2^21 of fp32 ones."""
+    for dtype, most, size in ((torch.bfloat16, 1 << 15, 2), (torch.float32, 1 << 21, 4)):
+        for R in (1, 4, 65):
+            d = T.make_desc(40, R, 32, 8, 128, 128, 2 ** 31 - 128, dtype, False, 0.1)
+            assert T.tsd_verify_q4_workspace_size(d) >= 2 ** 31 // most * 40 * 32 * R * (128 * size + 8)

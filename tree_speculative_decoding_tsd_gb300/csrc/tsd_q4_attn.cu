@@ -94,7 +94,7 @@ Q8Plan plan_rows(const tsd_attn_desc& d, int R) {
     // with the scratch rows in the last split 81, 48, 46, 49.)
     const long tiles = ceil_div(d.cap, 64), most = 304 / (heads * p.nrg);
     const long n = most < 1 ? 1 : most > 64 ? 64 : most, even = ceil_div(tiles, n);
-    const long per = even < 32768 ? even : 32768;  // (sums of a length and a split's stay within 32 bits)
+    const long per = even < 32768 ? even : 32768;  // (positions of a split: 2^21)
     p.split_len = (int)per * 64;
     p.nsplit = (int)ceil_div(d.cap, p.split_len);
     p.tree_split = p.nsplit > 1 && per <= 12 ? 1 : 0;

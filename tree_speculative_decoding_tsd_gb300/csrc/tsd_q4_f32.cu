@@ -94,7 +94,7 @@ __global__ void __launch_bounds__(kF32Threads, 2) q4_f32_kernel(const __grid_con
   const int P = min(max(a.plen[b], 0), a.map.cap);
   const int nsb = q8_splits(a, P);
   if (sp >= nsb) return;
-  const int k0 = min(sp * a.split_len, P), k1 = min(P, k0 + a.split_len);
+  const int k0 = q8_first(a, P, sp), k1 = q8_end(a, P, k0);
   const int n_pre = (k1 - k0 + kF32Keys - 1) / kF32Keys;
   const int row_base = rg * a.rb, rows_here = min(a.rb, a.M - row_base);
 

@@ -131,7 +131,7 @@ q4_few_kernel(const __grid_constant__ Q8AttnArgs a) {
   const int b = request_at(a, blockIdx.y, P, (volatile int*)(smem + L::off_req));
   const int nsb = q8_splits(a, P);
   if (sp >= nsb) return;
-  const int k0 = min(sp * a.split_len, P), k1 = min(P, k0 + a.split_len);
+  const int k0 = q8_first(a, P, sp), k1 = q8_end(a, P, k0);
   const bool with_tree = sp == nsb - 1;
   __syncthreads();                                 // (s_huge)
 
@@ -165,7 +165,7 @@ q4_few_kernel(const __grid_constant__ Q8AttnArgs a) {
   // chunk c into a slot; then on to the warp's next one
   auto request = [&](int c, int slot) {
     const uint32_t st = ring + slot * L::stage;
-    const int nv = k1 - (k0 + c * kChunk);
+    const int nv = k1 - k0 - c * kChunk;
     if (nv >= kChunk) {
 #pragma unroll
       for (int i = 0; i < kCopies; ++i) {
@@ -356,7 +356,7 @@ q4_few_kernel(const __grid_constant__ Q8AttnArgs a) {
   for (int c = warp; c < last; c += W) {
     asm volatile("cp.async.wait_group %0;\n" ::"n"(S - 2) : "memory");
     __syncwarp();
-    const int nv = k1 - (k0 + c * kChunk);
+    const int nv = k1 - k0 - c * kChunk;
     request(c + (S - 1) * W, slot == 0 ? S - 1 : slot - 1);
     const uint8_t* const st = mine + slot * L::stage;
     slot = slot == S - 1 ? 0 : slot + 1;

@@ -321,14 +321,14 @@ __global__ void __launch_bounds__(kThreads, 1) q4_rows_kernel(const __grid_const
   const int b = request_at(a, blockIdx.z, P, (volatile int*)(smem + L::off_req));
   const int nsb = q8_splits(a, P);
   if (sp >= nsb) return;
-  const int k0 = min(sp * a.split_len, P), k1 = min(P, k0 + a.split_len);
+  const int k0 = q8_first(a, P, sp), k1 = q8_end(a, P, k0);
   const int n_pre = (k1 - k0 + kKeys - 1) / kKeys;
   const bool with_tree = sp == nsb - 1;             // R <= 65 < 128: one tile
   const int ntiles = n_pre + (with_tree ? 1 : 0);
   const int row_base = rg * a.rb;
   const int rows_here = min(a.rb, a.M - row_base);
   const int live_warps = (rows_here + 31) / 32;     // softmax warps of a stream with rows
-  auto valid_of = [&](int t) { return min(kKeys, k1 - (k0 + t * kKeys)); };
+  auto valid_of = [&](int t) { return min(kKeys, k1 - k0 - t * kKeys); };
 
   // ---------------------------------------------------------------- set-up
   const int wt = tid - kWideK * 32;

@@ -48,10 +48,17 @@ struct Q8Plan {
   size_t ws_bytes;
 };
 
-// Splits that hold work for a request of prefix length P.
+// Splits that hold work for a request of prefix length P, and the positions k0 .. k1 - 1 of one of them.
+// (Unsigned: P and the end of its last split may lie on either side of 2^31.)
 __device__ __forceinline__ int q8_splits(const Q8AttnArgs& a, int P) {
-  const int npre = P > 0 ? (P + a.split_len - 1) / a.split_len : 0;
+  const int npre = P > 0 ? (int)(((uint32_t)P + a.split_len - 1u) / (uint32_t)a.split_len) : 0;
   return a.tree_split ? npre + 1 : max(npre, 1);
+}
+__device__ __forceinline__ int q8_first(const Q8AttnArgs& a, int P, int sp) {
+  return (int)min((uint32_t)sp * a.split_len, (uint32_t)P);
+}
+__device__ __forceinline__ int q8_end(const Q8AttnArgs& a, int P, int k0) {
+  return (int)min((uint32_t)k0 + a.split_len, (uint32_t)P);
 }
 
 bool launch_q8_few(const tsd_attn_desc& d, const Q8AttnArgs& a, const Q8Plan& p, cudaStream_t st);

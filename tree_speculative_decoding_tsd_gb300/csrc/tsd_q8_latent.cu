@@ -128,7 +128,7 @@ q8_latent_kernel(const __grid_constant__ LatentMaps maps, const __grid_constant_
   const int b = request_at(a, blockIdx.z, P, (volatile int*)(smem + kOffReq));
   const int nsb = q8_splits(a, P);
   if (sp >= nsb) return;
-  const int k0 = min(sp * a.split_len, P), k1 = min(P, k0 + a.split_len);
+  const int k0 = q8_first(a, P, sp), k1 = q8_end(a, P, k0);
   const int n_pre = (k1 - k0 + kKeys - 1) / kKeys;
   const bool with_tree = sp == nsb - 1;
   const int ntiles = n_pre + (with_tree ? 1 : 0);

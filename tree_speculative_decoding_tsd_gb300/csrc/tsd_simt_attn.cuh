@@ -53,7 +53,7 @@ simt_attn_kernel(const __grid_constant__ Q8AttnArgs a) {
   const int P = min(max(a.plen[b], 0), a.map.cap);
   const int nsb = q8_splits(a, P);
   if (sp >= nsb) return;
-  const int k0 = min(sp * a.split_len, P), k1 = min(P, k0 + a.split_len);
+  const int k0 = q8_first(a, P, sp), k1 = q8_end(a, P, k0);
 
   // the (row, key of four) that this lane's score is of; the row's maximum, the sum of
   // its keys' weights, and what the row sees
