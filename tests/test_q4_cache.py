@@ -1222,7 +1222,8 @@ def test_attention_passes_infinite_scratch_rows_on(kind, R, dtype, lens):
 
 
 @gpu
-@pytest.mark.parametrize("R,dtype", [(1, torch.float32), (20, torch.float32)])
+@pytest.mark.parametrize("R,dtype", [(1, torch.bfloat16), (5, torch.bfloat16), (20, torch.bfloat16),
+                                     (1, torch.float32), (20, torch.float32)])
 def test_attention_over_prefixes_near_two_to_the_31(R, dtype):
     """A request of 2^31 - 228 positions: one page again and again, and another as the last one, whose
     scores are large enough for it to count.  The sums have up to 2^15 + 2^11 terms one after the other,
@@ -1281,3 +1282,11 @@ def test_workspaces_of_the_largest_caches_by_type():
         for R in (1, 4, 65):
             d = T.make_desc(40, R, 32, 8, 128, 128, 2 ** 31 - 128, dtype, False, 0.1)
             assert T.tsd_verify_q4_workspace_size(d) >= 2 ** 31 // most * 40 * 32 * R * (128 * size + 8)
+
+
+@pytest.mark.parametrize("R,dtype", [(1, T.TSD_BF16), (20, T.TSD_BF16), (20, T.TSD_F32)])
+def test_attention_checks_the_largest_caches_as_others(R, dtype):
+    """A capacity of 2^31 - 128 positions is refused for its workspace alone."""
+    d = _desc(B=1, R=R, cap=2 ** 31 - 128, dtype=dtype)
+    need = T.tsd_verify_q4_workspace_size(d)
+    assert need > 0 and _calls(d, ws=need - 1)["attn"]() == T.TSD_ERR_INVALID_ARG

@@ -198,8 +198,7 @@ extern "C" tsd_status tsd_tree_verify_attn_q4(const tsd_attn_desc* d, const void
       !ok_ptr(out) || !ok_ptr(lse) || !paging_ok(d, page_table, max_pages, page_size, num_pages))
     return TSD_ERR_INVALID_ARG;
   const Q4Plan p = plan_q4(*d);
-  if ((long)d->Hkv * p.main.nrg > 65535 || p.main.nsplit > 65535 || p.rest.nsplit > 65535)
-    return TSD_ERR_INVALID_ARG;
+  if ((long)d->Hkv * p.main.nrg > kMaxGrid) return TSD_ERR_INVALID_ARG;
   if (ws_bytes < p.ws_bytes || (p.ws_bytes > 0 && !ok_ptr(ws))) return TSD_ERR_INVALID_ARG;
   Q8AttnArgs a{};
   a.q = q;

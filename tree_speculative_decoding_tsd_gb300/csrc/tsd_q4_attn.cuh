@@ -13,6 +13,9 @@ namespace tsd {
 // over 32k keys 93 and 138 us.)
 constexpr int kQ4FewRows = 16;
 
+// Splits of a launch at most (a grid's y and z); caches near 2^31 positions have one more.
+constexpr int kMaxGrid = 65535;
+
 constexpr int kQ4F32 = kQ8Simt;                      // the path of fp32 heads
 
 // Exponents above a tile's scales, within which its keys or values are held in fp16 (the

@@ -40,6 +40,8 @@
 // eight warps and 80 registers (144 us), the work dealt out evenly over one CTA per slot by the
 // requests' lengths (120 us, but 80 instead of 56 us for 200 requests below 900 keys and 77
 // instead of 56 for 32 of 4 rows: a CTA then starts and ends once per request).
+#include <algorithm>
+
 #include "tsd_host.h"
 #include "tsd_q4.cuh"
 #include "tsd_q4_attn.cuh"
@@ -124,7 +126,7 @@ q4_few_kernel(const __grid_constant__ Q8AttnArgs a) {
   // the others.  One token of 16 requests over 20k to 32k keys 113 -> 110 us, of 16 over 8k to 32k
   // 95 -> 90.)
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
-  const int hk = blockIdx.x, sp = a.nsplit - 1 - blockIdx.z;
+  const int hk = blockIdx.x, sp = a.nsplit - 1 - a.split0 - blockIdx.z;
   int* const s_huge = (int*)(smem + L::off_req) + 2;  // a row from 2^117 on: its factor in two steps
   if (tid == 0) *s_huge = 0;
   int P;
@@ -640,7 +642,8 @@ void launch_few(const Q8AttnArgs& a, const Q8Plan& p, cudaStream_t st) {
   const uint32_t smem = FewLayout<D, NT, S, W>::total;
   const auto kern = q4_few_kernel<D, NT, S, W, kCtas>;
   cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  launch(kern, dim3(a.map.Hkv, a.B, p.nsplit), dim3(W * 32), smem, st, a);
+  for (Q8AttnArgs part = a; part.split0 < p.nsplit; part.split0 += kMaxGrid)
+    launch(kern, dim3(a.map.Hkv, a.B, std::min(p.nsplit - part.split0, kMaxGrid)), dim3(W * 32), smem, st, part);
 }
 
 }  // namespace

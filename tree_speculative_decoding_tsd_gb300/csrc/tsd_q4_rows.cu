@@ -40,6 +40,7 @@
 // 8 x 32 rows over 32k: 149 us.  (The figures above: 8 x 65 rows in three groups of 87.)
 // Tried and dropped: more of the widening on the scheduler that has no softmax warp (three of
 // four have rows: 472 us), the next tile's scores asked for during a tile's exponentials (403).
+#include <algorithm>
 #include <type_traits>
 
 #include "tsd_common.cuh"
@@ -316,7 +317,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_rows_kernel(const __grid_const
   };
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int hk = blockIdx.x / a.nrg, rg = blockIdx.x % a.nrg, sp = blockIdx.y;
+  const int hk = blockIdx.x / a.nrg, rg = blockIdx.x % a.nrg, sp = a.split0 + blockIdx.y;
   int P;
   const int b = request_at(a, blockIdx.z, P, (volatile int*)(smem + L::off_req));
   const int nsb = q8_splits(a, P);
@@ -888,7 +889,9 @@ void launch_rows(const Q8AttnArgs& a, const Q8Plan& p, cudaStream_t st) {
   const uint32_t smem = RowLayout<D>::total + 1024;
   const auto kern = a.wait_cycles < kWaitCycles ? q4_rows_kernel<D, true> : q4_rows_kernel<D, false>;
   cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  launch(kern, dim3(a.map.Hkv * p.nrg, p.nsplit, a.B), dim3(kThreads), smem, st, a);
+  for (Q8AttnArgs part = a; part.split0 < p.nsplit; part.split0 += kMaxGrid)
+    launch(kern, dim3(a.map.Hkv * p.nrg, std::min(p.nsplit - part.split0, kMaxGrid), a.B), dim3(kThreads), smem, st,
+           part);
 }
 
 }  // namespace

@@ -24,6 +24,7 @@ struct Q8AttnArgs {
   int B, R, Hq, g, M;
   int r0, nr;                 // the launch's tree rows: r0 .. r0 + nr - 1 (M = nr g packed rows)
   int nsplit, split_len, nrg, rb, tree_split;
+  int split0;                 // (4-bit cache) the launch's first split
   int by_length;              // grid z is a rank in (prefix length desc, index asc) order
   float qscale;               // softmax scale * log2(e)
   long long wait_cycles;      // of a pipeline wait (kernels that poll)
