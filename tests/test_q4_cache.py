@@ -1290,3 +1290,28 @@ def test_attention_checks_the_largest_caches_as_others(R, dtype):
     d = _desc(B=1, R=R, cap=2 ** 31 - 128, dtype=dtype)
     need = T.tsd_verify_q4_workspace_size(d)
     assert need > 0 and _calls(d, ws=need - 1)["attn"]() == T.TSD_ERR_INVALID_ARG
+
+
+@gpu
+@pytest.mark.parametrize("kind,R,dtype", [("gqa", 1, torch.bfloat16), ("gqa", 20, torch.bfloat16),
+                                          ("gqa", 1, torch.float32), ("gqa", 3, torch.float32),
+                                          ("gqa", 20, torch.float32), ("narrow", 4, torch.float32)])
+@pytest.mark.parametrize("lens", [[200, 0], [5000, 300]])
+def test_attention_of_rows_of_q_that_are_not_finite_is_nan(kind, R, dtype, lens):
+    """Also where every score is -inf, and whatever the NaN's bits."""
+    s = Setup(kind, 2, R, lens, dtype=dtype, seed=87)
+    s.k[..., 0] = (s.k[..., 0] & 0xf0) | 0xc            # dim 0 of every cached key: 4 s, s > 0
+    s.ks[..., 0] = s.ks[..., 0].abs()
+    s.kt[..., 0] = s.kt[..., 0].abs() + 1
+    s.q[0, 0, 0, 0] = -INF
+    s.q[0, R - 1, 3, 0] = INF
+    s.q[1, R - 1, 1, 0] = NAN
+    if dtype == torch.float32:
+        s.q.view(torch.int32)[1, 0, 2, 9] = 0x7f800001
+    else:
+        s.q.view(torch.int16)[1, 0, 2, 9] = 0x7f81
+    bad = torch.zeros(2, R, s.Hq, dtype=torch.bool, device=DEV)
+    bad[0, 0, 0] = bad[0, R - 1, 3] = bad[1, R - 1, 1] = bad[1, 0, 2] = True
+    out, lse = s.attn()
+    assert out[bad].isnan().all() and lse[bad].isnan().all()
+    assert out[~bad].isfinite().all() and lse[~bad].isfinite().all()

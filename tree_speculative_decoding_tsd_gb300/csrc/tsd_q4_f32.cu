@@ -128,7 +128,7 @@ __global__ void __launch_bounds__(kF32Threads, 2) q4_f32_kernel(const __grid_con
   for (int i = 0; i < 2; ++i) {
     const int row = 16 * wr + g + 8 * i;
     float4 w[D / 16];
-    float top = 0.f;
+    float top = 0.f, zero = 0.f;                   // (zero: NaN if an element is not finite)
 #pragma unroll
     for (int j = 0; j < D / 16; ++j) {
       w[j] = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -137,12 +137,17 @@ __global__ void __launch_bounds__(kF32Threads, 2) q4_f32_kernel(const __grid_con
         w[j] = __ldg((const float4*)((const float*)a.q + (((long)b * a.R + tr) * a.Hq + qh) * D) + 4 * j + t);
       }
       top = fmaxf(top, fmaxf(fmaxf(fabsf(w[j].x), fabsf(w[j].y)), fmaxf(fabsf(w[j].z), fabsf(w[j].w))));
+      zero += (w[j].x * 0.f + w[j].y * 0.f) + (w[j].z * 0.f + w[j].w * 0.f);
     }
 #pragma unroll
-    for (int x = 1; x < 4; x <<= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, x));
+    for (int x = 1; x < 4; x <<= 1) {
+      top = fmaxf(top, __shfl_xor_sync(kFull, top, x));
+      zero += __shfl_xor_sync(kFull, zero, x);
+    }
     const bool low = top < 8.67361738e-19f;        // 2^-60
     const float f = low ? 18446744073709551616.f : 1.f;
-    c2[i] = a.qscale * (low ? 5.42101086e-20f : 1.f);
+    // (NaN for such a row: its terms would lose that)
+    c2[i] = a.qscale * (low ? 5.42101086e-20f : 1.f) + zero;
     if (warp < WR) {
 #pragma unroll
       for (int j = 0; j < D / 16; ++j) {           // operands: (g, 2 dims), (g + 8, 2 dims)
