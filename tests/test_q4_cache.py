@@ -1315,3 +1315,15 @@ def test_attention_of_rows_of_q_that_are_not_finite_is_nan(kind, R, dtype, lens)
     out, lse = s.attn()
     assert out[bad].isnan().all() and lse[bad].isnan().all()
     assert out[~bad].isfinite().all() and lse[~bad].isfinite().all()
+
+
+@gpu
+@pytest.mark.parametrize("kind,R", [("gqa", 1), ("gqa", 4), ("narrow", 2), ("gqa", 20)])
+@pytest.mark.parametrize("lens", [[0, 5], [300, 5000]])
+def test_attention_of_the_largest_scratch_values(kind, R, lens):
+    """A mean of values next to bf16's largest is finite, though their sum is not in fp32."""
+    s = Setup(kind, 2, R, lens, seed=88)
+    s.vt = torch.where(s.vt > 0, 1.0, -1.0).to(s.dt) * (s.normal(*s.vt.shape).abs().clamp(max=1) * 0.5 + 0.5) * 3.3e38
+    out, lse = s.attn()
+    assert out.isfinite().all() and lse.isfinite().all()
+    check_tight(s, out, lse)

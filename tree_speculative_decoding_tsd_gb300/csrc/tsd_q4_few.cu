@@ -305,14 +305,15 @@ q4_few_kernel(const __grid_constant__ Q8AttnArgs a) {
           }
           const float mn = fmaxf(m, x);
           const float al = mn == m ? 1.f : ex2(m - mn), p = ex2(x - mn);
+          const float p9 = p * 0.001953125f;       // 2^-9: sums of the largest values stay finite
           m = mn;
           l = fmaf(l, al, p);
 #pragma unroll
-          for (int i = 0; i < E; ++i) o[i] = fmaf(o[i], al, p * v[u][i]);
+          for (int i = 0; i < E; ++i) o[i] = fmaf(o[i], al, p9 * v[u][i]);
         }
       }
 #pragma unroll
-      for (int i = 0; i < E; ++i) tree_o[n * D + lane * E + i] = o[i] * 0.001953125f;   // 2^-9
+      for (int i = 0; i < E; ++i) tree_o[n * D + lane * E + i] = o[i];
       if (lane == 0) s_ml[W * NT * 8 + n] = make_float4(m, l, m, 0.f);
     }
   }
