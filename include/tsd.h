@@ -648,14 +648,16 @@ tsd_status tsd_cache_evict_q8(const tsd_attn_desc* desc, int keep, int sink, int
  * and values are the codes' values, the scratch rows ktree, vtree are in dtype.  Rows
  * behind prefix_len are not used, whatever they hold; nor are scratch rows that no row
  * sees.  A NaN or an infinity in a scratch row reaches the outputs of the rows that see it
- * and no others.  fp32 inputs: q, probabilities and scratch rows enter their products to
+ * and no others; a row of q with one gives NaN.  fp32 inputs: q, probabilities and scratch rows enter their products to
  * 2^-22 (scratch elements below 2^-104: to 2^-126), cached values as they are, sums in
  * fp32.  bf16 inputs: probabilities and values
  * enter their products in fp16, each to 2^-12, and so do keys where a call has more than 16
- * packed rows (R * Hq / Hkv); values (and those keys) of a run of up to 128 cached rows share a
- * power of two, so that they are off by at most 2^-15 of the run's largest scale as well, and
- * a probability times its value by 2^-17 of the largest such product.  Scales from 2^-97 (a
- * write's smallest is 2^-93) to 2^118 are held; values of larger ones become infinite.
+ * packed rows (R * Hq / Hkv), whose outputs over parts of the prefix are joined from fp16, too;
+ * values (and those keys) of a run of up to 128 cached rows share a power of two, so that they are
+ * off by at most 2^-15 of the run's largest scale as well, and a probability times its value by
+ * 2^-17 (a scratch row's: 2^-16) of the largest such product.  Scales from 2^-97 (a write's
+ * smallest is 2^-93) to 2^118 are held, whatever lies beside them; values of larger ones become
+ * infinite.
  * ws: tsd_verify_q4_workspace_size(desc) bytes
  * (0 is a valid size); calls that may overlap, captured ones among them, each need their
  * own.

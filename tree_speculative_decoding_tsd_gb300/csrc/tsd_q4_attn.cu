@@ -110,10 +110,10 @@ Q8Plan plan_rows(const tsd_attn_desc& d, int R) {
 // groups of 128.  With much to do the last tree rows then have a launch of their own, on the path for
 // few rows and behind the groups', instead of being one more group: where a cache is one split and the
 // groups' CTAs are several waves, or where it is several splits and long.  (Rows of 32 heads, us, so
-// and in equal groups.  One split: 16, 24, 32, 40, 64 x 33 rows over 1k to 4k keys 81, 108, 122, 148,
-// 204 and 75, 97, 122, 153, 225; 32 x 34 119 and 121; 24 x 65 157 and 138; 128 x 33 below 1k 184 and
-// 224.  Several: 8 x 33 over 32k 227 and 280, 8 x 34 229 and 281, 8 x 65 374 and 392, 2 x 33 over 20k
-// to 32k 77 and 87; 4 x 33 over 4k to 8k, which therefore stay together, 61 and 54.)
+// and in equal groups.  One split: 16, 24, 32, 40, 64 x 33 rows over 1k to 4k keys 83, 114, 120, 151,
+// 208 and 78, 100, 124, 157, 231; 32 x 34 122 and 125; 24 x 65 163 and 142; 128 x 33 below 1k 188 and
+// 231.  Several: 8 x 33 over 32k 230 and 288, 8 x 34 232 and 288, 8 x 65 384 and 400, 2 x 33 over 20k
+// to 32k 79 and 89; 4 x 33 over 4k to 8k, which therefore stay together, 61 and 54.)
 constexpr long kQ4RestWork = 4096;                 // heads times tiles
 constexpr long kQ4RestHeads = 256, kQ4RestTiles = 128;   // of one split; of several
 

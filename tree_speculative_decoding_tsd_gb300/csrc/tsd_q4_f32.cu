@@ -22,7 +22,7 @@
 //
 // What bounds it: with 64 rows the products (two of 1024 multiply-adds for each; 60% of the tensor
 // pipe) and their waits, at 255 registers and two CTAs per SM.  65 rows of 64 heads over 8000
-// keys: 250 us, 68 TFLOP/s; 4 x 33 rows of 32 heads over 1k to 4k keys: 177 us.  On the CUDA
+// keys: 255 us, 67 TFLOP/s; 4 x 33 rows of 32 heads over 1k to 4k keys: 181 us.  On the CUDA
 // cores, with a thread's 8 x 4 scores from shared memory, whose loads bound that, 484 and 267 us;
 // a warp per eight rows with keys in registers, as over the 8-bit cache, 1531 and 558.
 #include <type_traits>

@@ -16,8 +16,8 @@
 //       (tsd_q4.cuh), exact; columns of Q carry the factor between the two.  Each group
 //       of 32 dims has its own product c . q in fp32, then times the group's scale; -8 sum(q)
 //       times the scales comes from a small product (sums in three bf16 terms): fp32 all the way.
-//   Q   fp16 times a power of two of its row: exact for elements down to 2^-29 of the
-//       row's largest, off by 2^-35 of it at most below.
+//   Q   fp16 times a power of two of its row, every other pair over 16: exact for elements
+//       down to 2^-27 of the row's largest, off by 2^-35 of it at most below.
 //   V   fp16, one fused multiply-add: (c - 8) s 2^(-E - 9), E the exponent above the chunk's
 //       largest scale: 2^-12, or 2^-25 (2^-15 of the chunk's largest scale) where that is more.
 //   P   fp16: 2^(x + E - m), m a running bound of x + E over the warp's keys (raised
@@ -27,11 +27,11 @@
 //       under way.
 // Each warp's sum, bound and output are joined at the end, in fp32.
 //
-// What bounds it.  One token of 16 requests of 32 heads over 20k to 32k keys: 111 us, 4.4 TB/s
-// (72 us by the bytes; 105 in the kernel, where no warp waits for its copies to speak of).  The
+// What bounds it.  One token of 16 requests of 32 heads over 20k to 32k keys: 112 us, 4.4 TB/s
+// (72 us by the bytes; 106 in the kernel, where no warp waits for its copies to speak of).  The
 // copies alone, the arithmetic left out, take 93 us in the same graph: 17 us of that are launch,
-// set-up, joint and merge.  It is issue slots (58% full over the kernel's whole time, three
-// quarters within the loop), the ALU (49%; it takes an instruction in two cycles) and the
+// set-up, joint and merge.  It is issue slots (56% full over the kernel's whole time, three
+// quarters within the loop), the ALU (48%; it takes an instruction in two cycles) and the
 // products' latency, at four warps a scheduler.  Up to eight packed rows need 128 registers:
 // sixteen warps an SM, in CTAs of eight, or of four for many short requests, so that one's start
 // and end lie beside the others' chunks (one CTA of sixteen: 142 us); nine to sixteen rows 168

@@ -36,8 +36,9 @@
 // the widening, 380 without the scales, 373 without the maxima, 374 without the exponentials, 300
 // without all of it: instructions and shared memory (64 KB stored and 64 KB read by products per
 // tile, half of its rate) are shared by all roles.  The tensor core needs 1280 cycles a tile.
-// 8 x 64 rows of 32 heads over 32k keys: 292 us, 942 TFLOP/s; 32 x 32 rows over 1k to 4k: 68 us;
-// 8 x 32 rows over 32k: 149 us.  (The figures above: 8 x 65 rows in three groups of 87.)
+// 8 x 64 rows of 32 heads over 32k keys: 299 us, 920 TFLOP/s; 32 x 32 rows over 1k to 4k: 71 us;
+// 8 x 32 rows over 32k: 153 us.  (292, 68, 149 with one bound for both sums and one power of two for
+// all rows of a split.  The figures above: 8 x 65 rows in three groups of 87.)
 // Tried and dropped: more of the widening on the scheduler that has no softmax warp (three of
 // four have rows: 472 us), the next tile's scores asked for during a tile's exponentials (403).
 #include <algorithm>
