@@ -1327,3 +1327,13 @@ def test_attention_of_the_largest_scratch_values(kind, R, lens):
     out, lse = s.attn()
     assert out.isfinite().all() and lse.isfinite().all()
     check_tight(s, out, lse)
+
+
+@pytest.mark.parametrize("dtype", [T.TSD_BF16, T.TSD_F32])
+def test_workspace_of_a_call_that_is_refused_is_none(dtype):
+    """More KV heads than a grid has rows."""
+    for R, Hkv in ((1, 65536), (65, 65536), (1, 65535)):
+        d = _desc(B=1, R=R, Hq=Hkv, Hkv=Hkv, cap=1 << 24, dtype=dtype)
+        refused = Hkv > 65535
+        assert (T.tsd_verify_q4_workspace_size(d) == 0) == refused
+        assert not refused or _calls(d)["attn"]() == T.TSD_ERR_INVALID_ARG

@@ -142,6 +142,8 @@ Q4Plan plan_q4(const tsd_attn_desc& d) {
   return p;
 }
 
+bool grid_ok(const tsd_attn_desc& d, const Q4Plan& p) { return (long)d.Hkv * p.main.nrg <= kMaxGrid; }
+
 // A launch for tree rows r0 .. r0 + nr - 1, and the merge of its splits.
 void run_q4(Q8AttnArgs a, const Q8Plan& p, int r0, int nr, int D, void* ws, cudaStream_t st) {
   a.r0 = r0;
@@ -180,7 +182,8 @@ using namespace tsd;
 
 extern "C" size_t tsd_verify_q4_workspace_size(const tsd_attn_desc* d) {
   if (q4_desc_status(d, true) != TSD_OK) return 0;
-  return plan_q4(*d).ws_bytes;
+  const Q4Plan p = plan_q4(*d);
+  return grid_ok(*d, p) ? p.ws_bytes : 0;
 }
 
 extern "C" tsd_status tsd_tree_verify_attn_q4(const tsd_attn_desc* d, const void* q,
@@ -198,7 +201,7 @@ extern "C" tsd_status tsd_tree_verify_attn_q4(const tsd_attn_desc* d, const void
       !ok_ptr(out) || !ok_ptr(lse) || !paging_ok(d, page_table, max_pages, page_size, num_pages))
     return TSD_ERR_INVALID_ARG;
   const Q4Plan p = plan_q4(*d);
-  if ((long)d->Hkv * p.main.nrg > kMaxGrid) return TSD_ERR_INVALID_ARG;
+  if (!grid_ok(*d, p)) return TSD_ERR_INVALID_ARG;
   if (ws_bytes < p.ws_bytes || (p.ws_bytes > 0 && !ok_ptr(ws))) return TSD_ERR_INVALID_ARG;
   Q8AttnArgs a{};
   a.q = q;
